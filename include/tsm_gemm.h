@@ -330,6 +330,120 @@ gemm_status_t rowsum_f32acc(const void *X, int32_t elem_type, float *out, int64_
 gemm_status_t gemv_f16_f32acc(const uint16_t *A, const uint16_t *x, float *y, int64_t M, int64_t K,
                               int64_t lda, int64_t incx, gemm_stream_t stream);
 
+/* ---------------------------------------------------------------- experts' tokens
+ *
+ * Moving token rows to the experts of a Mixture-of-Experts layer and back,
+ * around the grouped calls above: the experts' side is `groups` matrices of
+ * `capacity` rows each, row r of expert e being row e * capacity + r, and
+ * counts[e] of them in use -- the layout and the counts the grouped calls
+ * take.  Strides are in elements, rows have a unit last stride, row pitches
+ * may exceed the width, and bases need only their elements' alignment (rows
+ * whose bases, pitches and widths are multiples of 16 bytes move fastest).
+ * All the calls are asynchronous on `stream`, use no atomics on
+ * floating-point data and are bitwise reproducible.  A written buffer may not
+ * overlap another buffer of the call (GEMM_ERR_ALIAS). */
+
+/* Give every choice of an expert a row.  For token t and its choice j, in the
+ * order (0,0), (0,1), ..., (1,0), ...: the choice of expert e = expert_ids[t * topk + j]
+ * gets the rank r = the number of earlier choices of e, and
+ *     slots[t * topk + j] = e * capacity + r   when r < capacity, else -1 (dropped);
+ * an id outside [0, groups) names no expert and gets -1 (a padded token).
+ *     counts[e] = min(capacity, the choices of e).
+ *   expert_ids  device, tokens x topk int32 or int64 values (id_bytes 4 or 8)
+ *   slots       device, tokens x topk int32, written
+ *   counts      device, groups int32, written
+ * groups <= 1024; tokens x topk and groups x capacity below 2^31. */
+gemm_status_t moe_route_slots(const void *expert_ids, int32_t id_bytes, int32_t *slots, int32_t *counts,
+                        int64_t tokens, int64_t topk, int64_t groups, int64_t capacity,
+                        gemm_stream_t stream);
+
+/* rows[slots[t * topk + j]] = x[t] for every slot in [0, rows); the other
+ * rows stay untouched.  Rows are copied as bytes: elem_bytes 1 (8-bit
+ * integers), 2 (f16, bf16) or 4 (f32; the per-row scales of 8-bit rows with
+ * width 1).  Slots must differ from one another, as moe_route_slots's do. */
+gemm_status_t moe_dispatch_rows(const void *x, int32_t elem_bytes, const int32_t *slots, void *rows_out,
+                           int64_t tokens, int64_t topk, int64_t rows, int64_t width,
+                           int64_t ldx, int64_t ld_rows, gemm_stream_t stream);
+
+/* The gradient of moe_dispatch_rows: dx[t] = sum over j of drows[slots[t * topk + j]],
+ * summed in f32 in ascending j and rounded once to elem_type (GEMM_OUT_F32,
+ * GEMM_OUT_F16 or GEMM_OUT_BF16, both sides alike); a token with no row gets zeros. */
+gemm_status_t moe_dispatch_rows_grad(const void *drows, int32_t elem_type, const int32_t *slots, void *dx,
+                                int64_t tokens, int64_t topk, int64_t rows, int64_t width,
+                                int64_t ld_rows, int64_t ldx, gemm_stream_t stream);
+
+/* out[t] = sum over j of weights[t * topk + j] * rows[slots[t * topk + j]],
+ * summed in f32 in ascending j and rounded once to elem_type; a choice
+ * without a row adds nothing (whatever its weight).  weights NULL: all ones. */
+gemm_status_t moe_combine_rows(const void *rows_in, int32_t elem_type, const int32_t *slots,
+                          const float *weights, void *out, int64_t tokens, int64_t topk, int64_t rows,
+                          int64_t width, int64_t ld_rows, int64_t ld_out, gemm_stream_t stream);
+
+/* The gradients of moe_combine_rows, in one pass over the rows:
+ *     drows[slots[t * topk + j]] = weights[t * topk + j] * dout[t]   (the other rows untouched)
+ *     dweights[t * topk + j] = sum over k of dout[t][k] * rows[slots[t * topk + j]][k]
+ * the sums in f32 in a fixed order; 0 for a choice without a row.  dweights
+ * NULL: not wanted.  weights NULL: all ones.  drows may not be `rows` itself. */
+gemm_status_t moe_combine_rows_grad(const void *dout, const void *rows_in, int32_t elem_type,
+                               const int32_t *slots, const float *weights, void *drows, float *dweights,
+                               int64_t tokens, int64_t topk, int64_t rows, int64_t width,
+                               int64_t ld_dout, int64_t ld_rows, int64_t ld_drows,
+                               gemm_stream_t stream);
+
+/* ---------------------------------------------------------------- 8-bit integers */
+
+/* Quantise rows to 8-bit integers, symmetrically:
+ *     scales[i] = max over k of |X[i][k]| / 127        (f32 division)
+ *     q[i][k]   = X[i][k] / scales[i], rounded to the nearest integer (ties to even)
+ * so q is in [-127, 127] and X[i][k] is within scales[i] / 2 of q[i][k] * scales[i].
+ * A row of zeros (or one whose scale underflows) gets the scale 0 and zeros;
+ * a row holding an infinity or a NaN gets a NaN scale and zeros, so that its
+ * products come out NaN.
+ *   X           device, batch matrices of M rows of K values of elem_type, ldx / strideX apart
+ *   q           device, written, ldq / strideQ apart (ldq a multiple of 16 suits gemm_s8_scaled)
+ *   scales      device, batch x M f32, scale_stride apart, written
+ *   group_rows  NULL, or device, batch int32: only the first group_rows[b] rows of matrix b are
+ *               read and written (the grouped calls' counts) */
+gemm_status_t quantize_rows_s8(const void *X, int32_t elem_type, int8_t *q, float *scales,
+                               const int32_t *group_rows, int64_t M, int64_t K, int64_t ldx, int64_t ldq,
+                               int64_t strideX, int64_t strideQ, int64_t scale_stride, int64_t batch,
+                               gemm_stream_t stream);
+
+/* C[i][j] = act(alpha * scale_a[i] * scale_b[j] * S[i][j] + bias[j]),
+ * S[i][j] = sum over k of A[i][k] * B[k][j], for 8-bit integers A and B.
+ * The sum is the exact integer (32 bits: K below 131072), so a call is
+ * bitwise reproducible whatever the launch shape; it is converted to f32,
+ * scaled, and rounded once to the output type.
+ *   A        device, M rows of K int8 values (-128 included), row stride lda
+ *   B        device, K rows of N int8 values, row stride ldb
+ *   C        device, M rows of N values of epi->out_type (f32 without epi), row stride ldc;
+ *            written, never read; elements of a row past N are left untouched
+ *   scale_a  device, M f32 values per matrix, scale_a_stride apart (NULL: ones)
+ *   scale_b  device, N f32 values per matrix, scale_b_stride apart (NULL: ones)
+ *   epi      as for gemm_f16_fused; NULL: f32, no bias, no activation
+ * Any pitch and base is accepted; A and B with 16-byte aligned bases and
+ * pitches (and batch strides) are read in place, others are first copied to
+ * such a layout.  K == 0 gives act(bias[j]) in every cell.  Other errors as
+ * for gemm_f16_f32acc_batched. */
+gemm_status_t gemm_s8_scaled(const int8_t *A, const int8_t *B, void *C, const float *scale_a,
+                             const float *scale_b, int64_t M, int64_t N, int64_t K,
+                             int64_t lda, int64_t ldb, int64_t ldc,
+                             int64_t strideA, int64_t strideB, int64_t strideC,
+                             int64_t scale_a_stride, int64_t scale_b_stride, int64_t batch,
+                             const gemm_epilogue_t *epi, gemm_stream_t stream);
+
+/* The grouped (Mixture-of-Experts) form: group g computes the first
+ * group_rows[g] of its M rows (device memory, clamped to [0, M]; a count
+ * outside that range is reported by the next gemm_get_device_status); the
+ * other rows of C stay untouched. */
+gemm_status_t gemm_s8_grouped_scaled(const int8_t *A, const int8_t *B, void *C, const float *scale_a,
+                                     const float *scale_b, const int32_t *group_rows, int64_t groups,
+                                     int64_t M, int64_t N, int64_t K,
+                                     int64_t lda, int64_t ldb, int64_t ldc,
+                                     int64_t strideA, int64_t strideB, int64_t strideC,
+                                     int64_t scale_a_stride, int64_t scale_b_stride,
+                                     const gemm_epilogue_t *epi, gemm_stream_t stream);
+
 /* The plan the library would use, computed on the host only (no GPU is
  * touched).  num_sms is the SM count to plan for (0 = the current device's).
  * It is the plan of an ungrouped call; a grouped call plans with split_k 1

@@ -122,6 +122,24 @@ def _load() -> ctypes.CDLL:
     lib.rowsum_f32acc.argtypes = [vp, i32, vp, i64, i64, i64, i64, vp]
     lib.gemv_f16_f32acc.restype = ctypes.c_int
     lib.gemv_f16_f32acc.argtypes = [vp, vp, vp, i64, i64, i64, i64, vp]
+    lib.moe_route_slots.restype = ctypes.c_int
+    lib.moe_route_slots.argtypes = [vp, i32, vp, vp, i64, i64, i64, i64, vp]
+    lib.moe_dispatch_rows.restype = ctypes.c_int
+    lib.moe_dispatch_rows.argtypes = [vp, i32, vp, vp, i64, i64, i64, i64, i64, i64, vp]
+    lib.moe_dispatch_rows_grad.restype = ctypes.c_int
+    lib.moe_dispatch_rows_grad.argtypes = [vp, i32, vp, vp, i64, i64, i64, i64, i64, i64, vp]
+    lib.moe_combine_rows.restype = ctypes.c_int
+    lib.moe_combine_rows.argtypes = [vp, i32, vp, vp, vp, i64, i64, i64, i64, i64, i64, vp]
+    lib.moe_combine_rows_grad.restype = ctypes.c_int
+    lib.moe_combine_rows_grad.argtypes = [vp, vp, i32, vp, vp, vp, vp, i64, i64, i64, i64, i64, i64, i64, vp]
+    lib.quantize_rows_s8.restype = ctypes.c_int
+    lib.quantize_rows_s8.argtypes = [vp, i32, vp, vp, vp, i64, i64, i64, i64, i64, i64, i64, i64, vp]
+    lib.gemm_s8_scaled.restype = ctypes.c_int
+    lib.gemm_s8_scaled.argtypes = [vp, vp, vp, vp, vp, i64, i64, i64, i64, i64, i64, i64, i64, i64, i64,
+                                   i64, i64, ctypes.POINTER(GemmEpilogue), vp]
+    lib.gemm_s8_grouped_scaled.restype = ctypes.c_int
+    lib.gemm_s8_grouped_scaled.argtypes = [vp, vp, vp, vp, vp, vp, i64, i64, i64, i64, i64, i64, i64, i64,
+                                           i64, i64, i64, i64, ctypes.POINTER(GemmEpilogue), vp]
     lib.gemm_f16_f32acc_splitk_noalloc.restype = ctypes.c_int
     lib.gemm_f16_f32acc_splitk_noalloc.argtypes = [vp, vp, vp, i64, i64, i64, i64, i64, i64,
                                                    i32, vp]
@@ -200,6 +218,52 @@ def gemm_f16_f32acc_splitk_noalloc(A, B, C, M, N, K, lda, ldb, ldc, split_k=0, s
     """The entry point that allocates nothing (split-K partials in a fixed
     16 MiB device array inside the library); see include/tsm_gemm.h."""
     return _lib.gemm_f16_f32acc_splitk_noalloc(A, B, C, M, N, K, lda, ldb, ldc, split_k, stream)
+
+
+def moe_route_slots(expert_ids, id_bytes, slots, counts, tokens, topk, groups, capacity, stream=0) -> int:
+    return _lib.moe_route_slots(expert_ids, id_bytes, slots, counts, tokens, topk, groups, capacity, stream)
+
+
+def moe_dispatch_rows(x, elem_bytes, slots, rows_out, tokens, topk, rows, width, ldx, ld_rows, stream=0) -> int:
+    return _lib.moe_dispatch_rows(x, elem_bytes, slots, rows_out, tokens, topk, rows, width, ldx, ld_rows, stream)
+
+
+def moe_dispatch_rows_grad(drows, elem_type, slots, dx, tokens, topk, rows, width, ld_rows, ldx, stream=0) -> int:
+    return _lib.moe_dispatch_rows_grad(drows, elem_type, slots, dx, tokens, topk, rows, width, ld_rows, ldx, stream)
+
+
+def moe_combine_rows(rows_in, elem_type, slots, weights, out, tokens, topk, rows, width, ld_rows, ld_out,
+                    stream=0) -> int:
+    return _lib.moe_combine_rows(rows_in, elem_type, slots, weights, out, tokens, topk, rows, width, ld_rows, ld_out,
+                            stream)
+
+
+def moe_combine_rows_grad(dout, rows_in, elem_type, slots, weights, drows, dweights, tokens, topk, rows, width,
+                         ld_dout, ld_rows, ld_drows, stream=0) -> int:
+    return _lib.moe_combine_rows_grad(dout, rows_in, elem_type, slots, weights, drows, dweights, tokens, topk, rows,
+                                 width, ld_dout, ld_rows, ld_drows, stream)
+
+
+def quantize_rows_s8(X, elem_type, q, scales, group_rows, M, K, ldx, ldq, strideX=0, strideQ=0, scale_stride=0,
+                     batch=1, stream=0) -> int:
+    return _lib.quantize_rows_s8(X, OUT_TYPES.get(elem_type, elem_type), q, scales, group_rows, M, K, ldx, ldq,
+                                 strideX, strideQ, scale_stride, batch, stream)
+
+
+def gemm_s8_scaled(A, B, C, scale_a, scale_b, M, N, K, lda, ldb, ldc, strideA=0, strideB=0, strideC=0,
+                   scale_a_stride=0, scale_b_stride=0, batch=1, epi: GemmEpilogue | None = None,
+                   stream=0) -> int:
+    e = ctypes.byref(epi) if epi is not None else None
+    return _lib.gemm_s8_scaled(A, B, C, scale_a, scale_b, M, N, K, lda, ldb, ldc, strideA, strideB, strideC,
+                               scale_a_stride, scale_b_stride, batch, e, stream)
+
+
+def gemm_s8_grouped_scaled(A, B, C, scale_a, scale_b, group_rows, groups, M, N, K, lda, ldb, ldc, strideA,
+                           strideB, strideC, scale_a_stride, scale_b_stride, epi: GemmEpilogue | None = None,
+                           stream=0) -> int:
+    e = ctypes.byref(epi) if epi is not None else None
+    return _lib.gemm_s8_grouped_scaled(A, B, C, scale_a, scale_b, group_rows, groups, M, N, K, lda, ldb, ldc,
+                                       strideA, strideB, strideC, scale_a_stride, scale_b_stride, e, stream)
 
 
 def gemm_plan(M, N, K, batch=1, opts: GemmOptions | None = None, num_sms=0) -> dict:
@@ -392,6 +456,267 @@ def gemv(A, x, out=None, *, stream=None):
                           A.stride(0) if M > 1 else max(K, 1), x.stride(0) if K > 1 else 1,
                           _stream_handle(stream)))
     return out
+
+
+# Mixture-of-Experts: token rows to their experts and back.  The experts' side
+# is a groups x capacity x width tensor, the layout grouped_gemm takes.
+
+def _elem_type(dtype):
+    import torch
+    code = {torch.float32: 0, torch.float16: 1, torch.bfloat16: 2}.get(dtype)
+    if code is None:
+        raise TypeError(f"rows must be torch.float32, torch.float16 or torch.bfloat16, not {dtype}")
+    return code
+
+
+def _check_slots(slots, tokens):
+    import torch
+    if slots.dtype != torch.int32 or not slots.is_cuda or slots.dim() != 2 or not slots.is_contiguous():
+        raise ValueError("slots must be a contiguous CUDA int32 tensor of tokens x topk values")
+    if slots.shape[0] != tokens:
+        raise ValueError(f"slots are of {slots.shape[0]} tokens, not {tokens}")
+
+
+def _check_token_rows(x, name):
+    if x.dim() != 2 or not x.is_cuda or (x.shape[1] > 1 and x.numel() and x.stride(1) != 1):
+        raise ValueError(f"{name} must be a 2-D CUDA tensor with a unit last stride")
+
+
+def _check_expert_rows(rows, width, dtype, name):
+    """The pitch of a groups x capacity x width tensor whose rows are evenly spaced."""
+    if rows.dim() != 3 or not rows.is_cuda or rows.shape[2] != width or rows.dtype != dtype:
+        raise ValueError(f"{name} must be a groups x capacity x {width} CUDA tensor of {dtype}")
+    G, cap, _ = rows.shape
+    ld = rows.stride(1) if cap > 1 else rows.stride(0) if G > 1 else width
+    if rows.numel() and ((width > 1 and rows.stride(2) != 1) or (G > 1 and rows.stride(0) != cap * ld)
+                         or (G * cap > 1 and ld < width)):
+        raise ValueError(f"{name} must have a unit last stride and evenly spaced rows "
+                         "(stride(0) == capacity * stride(1))")
+    return max(ld, width)
+
+
+def _check_weights(weights, slots):
+    import torch
+    if weights.dtype != torch.float32 or not weights.is_cuda or weights.shape != slots.shape \
+            or not weights.is_contiguous():
+        raise ValueError("weights must be a contiguous CUDA float32 tensor of tokens x topk values")
+
+
+def moe_route(expert_ids, groups, capacity, *, stream=None):
+    """Rows for the experts' choices: ``(slots, counts)`` for a tokens x topk
+    CUDA tensor of expert numbers (int32 or int64).
+
+    ``slots[t, j] = e * capacity + rank`` with ranks in token order, -1 for a
+    choice past the capacity or an id outside [0, groups); ``counts`` is what
+    ``grouped_gemm`` takes as ``group_rows``.  Both are int32."""
+    import torch
+    if expert_ids.dtype not in (torch.int32, torch.int64) or not expert_ids.is_cuda or expert_ids.dim() != 2:
+        raise ValueError("expert_ids must be a 2-D CUDA tensor of int32 or int64")
+    ids = expert_ids.contiguous()
+    T, k = ids.shape
+    slots = torch.empty((T, k), dtype=torch.int32, device=ids.device)
+    counts = torch.empty((groups,), dtype=torch.int32, device=ids.device)
+    check(moe_route_slots(ids.data_ptr(), ids.element_size(), slots.data_ptr(), counts.data_ptr(), T, k, groups,
+                        capacity, _stream_handle(stream)))
+    return slots, counts
+
+
+def moe_dispatch(x, slots, groups, capacity, out=None, *, stream=None):
+    """Copy token rows to their experts: ``out[e, r] = x[t]`` where
+    ``slots[t, j] == e * capacity + r``.
+
+    ``x`` is tokens x width (f32, f16, bf16 or int8).  Returns ``out`` (groups
+    x capacity x width); rows no slot names keep their contents (zeros when
+    ``out`` is not given)."""
+    import torch
+    _check_token_rows(x, "x")
+    T, H = x.shape
+    _check_slots(slots, T)
+    if out is None:
+        out = torch.zeros((groups, capacity, H), dtype=x.dtype, device=x.device)
+    if tuple(out.shape) != (groups, capacity, H):
+        raise ValueError(f"out must be a {groups} x {capacity} x {H} tensor")
+    ld = _check_expert_rows(out, H, x.dtype, "out")
+    check(moe_dispatch_rows(x.data_ptr(), x.element_size(), slots.data_ptr(), out.data_ptr(), T, slots.shape[1],
+                           groups * capacity, H, x.stride(0) if T > 1 else H, ld, _stream_handle(stream)))
+    return out
+
+
+def moe_dispatch_grad(drows, slots, out=None, *, stream=None):
+    """The gradient of ``moe_dispatch``: ``dx[t] = sum_j drows[slots[t, j]]``
+    for groups x capacity x width ``drows`` (f32, f16 or bf16); summed in f32,
+    returned in the rows' type."""
+    import torch
+    G, cap, H = drows.shape
+    ld = _check_expert_rows(drows, H, drows.dtype, "drows")
+    T, k = slots.shape
+    _check_slots(slots, T)
+    if out is None:
+        out = torch.empty((T, H), dtype=drows.dtype, device=drows.device)
+    _check_token_rows(out, "out")
+    if tuple(out.shape) != (T, H) or out.dtype != drows.dtype:
+        raise ValueError(f"out must be a {T} x {H} tensor of {drows.dtype}")
+    check(moe_dispatch_rows_grad(drows.data_ptr(), _elem_type(drows.dtype), slots.data_ptr(), out.data_ptr(), T, k,
+                                G * cap, H, ld, out.stride(0) if T > 1 else H, _stream_handle(stream)))
+    return out
+
+
+def moe_combine(rows, slots, weights=None, out=None, *, stream=None):
+    """Bring the experts' rows back to their tokens:
+    ``out[t] = sum_j weights[t, j] * rows[slots[t, j]]`` for groups x capacity
+    x width ``rows`` (f32, f16 or bf16), f32 ``weights`` (tokens x topk; none:
+    ones); summed in f32, returned in the rows' type."""
+    import torch
+    G, cap, H = rows.shape
+    ld = _check_expert_rows(rows, H, rows.dtype, "rows")
+    T, k = slots.shape
+    _check_slots(slots, T)
+    if weights is not None:
+        _check_weights(weights, slots)
+    if out is None:
+        out = torch.empty((T, H), dtype=rows.dtype, device=rows.device)
+    _check_token_rows(out, "out")
+    if tuple(out.shape) != (T, H) or out.dtype != rows.dtype:
+        raise ValueError(f"out must be a {T} x {H} tensor of {rows.dtype}")
+    check(moe_combine_rows(rows.data_ptr(), _elem_type(rows.dtype), slots.data_ptr(),
+                          weights.data_ptr() if weights is not None else 0, out.data_ptr(), T, k, G * cap, H, ld,
+                          out.stride(0) if T > 1 else H, _stream_handle(stream)))
+    return out
+
+
+def moe_combine_grad(dout, rows, slots, weights=None, drows=None, *, stream=None):
+    """The gradients of ``moe_combine``: ``(drows, dweights)`` with
+    ``drows[slots[t, j]] = weights[t, j] * dout[t]`` (rows no slot names keep
+    their contents, zeros when ``drows`` is not given) and ``dweights[t, j] =
+    <dout[t], rows[slots[t, j]]>`` (f32, 0 for a dropped choice)."""
+    import torch
+    _check_token_rows(dout, "dout")
+    T, H = dout.shape
+    _check_slots(slots, T)
+    ld = _check_expert_rows(rows, H, dout.dtype, "rows")
+    if weights is not None:
+        _check_weights(weights, slots)
+    if drows is None:
+        drows = torch.zeros(rows.shape, dtype=rows.dtype, device=rows.device)
+    if drows.shape != rows.shape:
+        raise ValueError("drows must have the rows' shape")
+    ldd = _check_expert_rows(drows, H, dout.dtype, "drows")
+    dweights = torch.empty(slots.shape, dtype=torch.float32, device=dout.device)
+    check(moe_combine_rows_grad(dout.data_ptr(), rows.data_ptr(), _elem_type(dout.dtype), slots.data_ptr(),
+                               weights.data_ptr() if weights is not None else 0, drows.data_ptr(),
+                               dweights.data_ptr(), T, slots.shape[1], rows.shape[0] * rows.shape[1], H,
+                               dout.stride(0) if T > 1 else H, ld, ldd, _stream_handle(stream)))
+    return drows, dweights
+
+
+# 8-bit integers.
+
+def quantize_rows(X, group_rows=None, q=None, scales=None, *, stream=None):
+    """Quantise the rows of an M x K (or batch x M x K) CUDA tensor (f32, f16
+    or bf16) to int8: ``(q, scales)`` with ``scales = max|row| / 127`` and
+    ``q = round(X / scales)``.
+
+    ``q``'s rows are allocated with a pitch of a multiple of 16 bytes, as the
+    products want.  ``group_rows`` (int32, one count per matrix) limits the
+    rows that are read and written."""
+    import torch
+    code = _elem_type(X.dtype)
+    if X.dim() not in (2, 3) or not X.is_cuda or (X.shape[-1] > 1 and X.numel() and X.stride(-1) != 1):
+        raise ValueError("X must be a 2-D or 3-D CUDA tensor with a unit last stride")
+    batch = X.shape[0] if X.dim() == 3 else 1
+    M, K = X.shape[-2], X.shape[-1]
+    if q is None:
+        q = torch.empty((*X.shape[:-1], -(-K // 16) * 16), dtype=torch.int8, device=X.device)[..., :K]
+    if scales is None:
+        scales = torch.empty(X.shape[:-1], dtype=torch.float32, device=X.device)
+    if q.shape != X.shape or q.dtype != torch.int8 or (K > 1 and q.numel() and q.stride(-1) != 1):
+        raise ValueError("q must be an int8 tensor of X's shape with a unit last stride")
+    if scales.shape != X.shape[:-1] or scales.dtype != torch.float32 or (M > 1 and scales.stride(-1) != 1):
+        raise ValueError("scales must be a float32 tensor of one value per row")
+    if group_rows is not None and (group_rows.dtype != torch.int32 or not group_rows.is_cuda
+                                   or group_rows.numel() != batch or not group_rows.is_contiguous()):
+        raise ValueError("group_rows must be a contiguous CUDA int32 tensor of one count per matrix")
+    three = X.dim() == 3
+    check(quantize_rows_s8(X.data_ptr(), code, q.data_ptr(), scales.data_ptr(),
+                           group_rows.data_ptr() if group_rows is not None else 0, M, K,
+                           X.stride(-2) if M > 1 else K, q.stride(-2) if M > 1 else K,
+                           X.stride(0) if three else 0, q.stride(0) if three else 0,
+                           scales.stride(0) if three else 0, batch, _stream_handle(stream)))
+    return q, scales
+
+
+def _s8_call(A, B, scale_a, scale_b, group_rows, out, alpha, bias, activation, slope, out_dtype, stream):
+    import torch
+    if A.dtype != torch.int8 or B.dtype != torch.int8:
+        raise TypeError("A and B must be torch.int8")
+    if A.dim() != B.dim() or A.dim() not in (2, 3):
+        raise ValueError("A and B must both be 2-D or both 3-D")
+    three = A.dim() == 3
+    M, K = A.shape[-2], A.shape[-1]
+    N = B.shape[-1]
+    if B.shape[-2] != K:
+        raise ValueError(f"inner sizes differ: {K} vs {B.shape[-2]}")
+    batch = A.shape[0] if three else 1
+    if three and B.shape[0] != batch:
+        raise ValueError("batch sizes differ")
+    dtype = out.dtype if out is not None else (out_dtype or torch.float32)
+    shape = (batch, M, N) if three else (M, N)
+    if out is None:
+        make = torch.empty if group_rows is None else torch.zeros
+        out = make(shape, dtype=dtype, device=A.device)
+    if tuple(out.shape) != shape:
+        raise ValueError(f"out must be a {' x '.join(map(str, shape))} tensor")
+    for t, name in ((A, "A"), (B, "B"), (out, "out")):
+        if not t.is_cuda or (t.shape[-1] > 1 and t.numel() and t.stride(-1) != 1):
+            raise ValueError(f"{name} must be a CUDA tensor with a unit last stride")
+
+    def vector(t, n, name):
+        if t is None:
+            return 0, 0
+        if t.dtype != torch.float32 or not t.is_cuda or t.shape[-1] != n or (n > 1 and t.stride(-1) != 1) \
+                or t.dim() > (2 if three else 1) or (t.dim() == 2 and t.shape[0] != batch):
+            raise ValueError(f"{name} must be a CUDA float32 tensor of {n} values"
+                             + (f" (or {batch} x {n})" if three else ""))
+        return t.data_ptr(), t.stride(0) if t.dim() == 2 and batch > 1 else 0
+
+    pa, sa = vector(scale_a, M, "scale_a")
+    pb, sb = vector(scale_b, N, "scale_b")
+    pbias, sbias = vector(bias, N, "bias")
+    epi = epilogue(alpha, pbias, sbias, activation, slope, _elem_type(dtype))
+    args = (M, N, K, A.stride(-2) if M > 1 else max(K, 1), B.stride(-2) if K > 1 else max(N, 1),
+            out.stride(-2) if M > 1 else max(N, 1), A.stride(0) if three else 0, B.stride(0) if three else 0,
+            out.stride(0) if three else 0, sa, sb)
+    if group_rows is None:
+        check(gemm_s8_scaled(A.data_ptr(), B.data_ptr(), out.data_ptr(), pa, pb, *args, batch, epi,
+                             _stream_handle(stream)))
+    else:
+        check(gemm_s8_grouped_scaled(A.data_ptr(), B.data_ptr(), out.data_ptr(), pa, pb, group_rows.data_ptr(),
+                                     batch, *args, epi, _stream_handle(stream)))
+    return out
+
+
+def gemm_s8(A, B, scale_a=None, scale_b=None, out=None, *, alpha=1.0, bias=None, activation="none", slope=0.01,
+            out_dtype=None, stream=None):
+    """``out = activation(alpha * scale_a[:, None] * scale_b[None, :] * (A @ B) + bias)``
+    for int8 CUDA tensors A (M x K) and B (K x N), or a batch of them; the sums
+    are exact integers.  ``scale_a`` holds M and ``scale_b`` N f32 values (per
+    matrix, or one vector for the batch; none: ones); ``out`` is f32 unless
+    ``out_dtype`` (or the given ``out``) says torch.float16 / torch.bfloat16.
+    Pitches that are multiples of 16 bytes are read in place; others cost a
+    copy.  Returns ``out``."""
+    return _s8_call(A, B, scale_a, scale_b, None, out, alpha, bias, activation, slope, out_dtype, stream)
+
+
+def grouped_gemm_s8(A, B, scale_a, scale_b, group_rows, out=None, *, alpha=1.0, bias=None, activation="none",
+                    slope=0.01, out_dtype=None, stream=None):
+    """The grouped (Mixture-of-Experts) form of ``gemm_s8``: A is groups x M x
+    K, B groups x K x N; of group g the first ``group_rows[g]`` rows are
+    computed, the others keep the contents of ``out`` (zeros when not given)."""
+    import torch
+    if A.dim() != 3 or group_rows.dtype != torch.int32 or not group_rows.is_cuda \
+            or group_rows.numel() != A.shape[0] or not group_rows.is_contiguous():
+        raise ValueError("A must be 3-D and group_rows a contiguous CUDA int32 tensor of one count per group")
+    return _s8_call(A, B, scale_a, scale_b, group_rows, out, alpha, bias, activation, slope, out_dtype, stream)
 
 
 def gemm_host(A_host, B_host, C_host, dA, dB, dC, stream=None):

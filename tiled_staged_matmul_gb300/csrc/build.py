@@ -2,8 +2,8 @@
 
 The translation units compile in parallel: the plain GEMM kernels and the
 cluster split-K sums, the fused-epilogue GEMM kernels once per activation
-(``gemm_epi.cu`` with ``-DTSM_EPI_ACT``), the row-reduction kernels and the
-host API.  The kernel units are compiled with ``-Xptxas -v`` and the build
+(``gemm_epi.cu`` with ``-DTSM_EPI_ACT``), the row-reduction kernels, the
+expert token movement, the 8-bit integer products and the host API.  The kernel units are compiled with ``-Xptxas -v`` and the build
 fails if ptxas reports any spill stores or loads (only ptxas's printed
 summary is read).
 """
@@ -28,9 +28,12 @@ PTXAS_LOG = os.path.join(BUILD_DIR, "ptxas.log")
 ACTIVATIONS = ["none", "relu", "leaky_relu", "gelu", "gelu_tanh", "silu"]
 UNITS = ([("gemm_kernels.cu", "gemm_kernels", [])] +
          [("gemm_epi.cu", f"gemm_epi_{a}", [f"-DTSM_EPI_ACT={i}"]) for i, a in enumerate(ACTIVATIONS)] +
-         [("rowsum_kernels.cu", "rowsum_kernels", []), ("gemm_api.cu", "gemm_api", [])])
+         [("rowsum_kernels.cu", "rowsum_kernels", []), ("moe_kernels.cu", "moe_kernels", []),
+          ("s8_kernels.cu", "s8_kernels", []), ("gemm_api.cu", "gemm_api", []),
+          ("ops_api.cu", "ops_api", [])])
+HOST_SOURCES = ("gemm_api.cu", "ops_api.cu")
 SOURCES = sorted({u[0] for u in UNITS})
-HEADERS = ["gemm_internal.h", "gemm_kernel.cuh", "ptx.cuh"]
+HEADERS = ["api_internal.h", "gemm_internal.h", "gemm_kernel.cuh", "ops_internal.h", "ptx.cuh"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 
 
@@ -79,7 +82,7 @@ def build(force: bool = False, quiet: bool = True) -> str:
         return LIB_PATH
     os.makedirs(BUILD_DIR, exist_ok=True)
     objs = [os.path.join(BUILD_DIR, name + ".o") for _, name, _ in UNITS]
-    kernel_unit = [src != "gemm_api.cu" for src, _, _ in UNITS]
+    kernel_unit = [src not in HOST_SOURCES for src, _, _ in UNITS]
     with ThreadPoolExecutor(len(UNITS)) as ex:
         logs = list(ex.map(lambda a: _compile(*a),
                            [(src, o, k, fl) for (src, _, fl), o, k in zip(UNITS, objs, kernel_unit)]))

@@ -11,8 +11,7 @@
 // chosen so that the persistent grid fills the SMs.  Unlike the pages' pass
 // there is no "decline" outcome: ragged K is handled by zero fill rather
 // than by a divisibility gate.
-#include "../../include/tsm_gemm.h"
-#include "gemm_internal.h"
+#include "api_internal.h"
 
 #include <cudaTypedefs.h>
 
@@ -26,7 +25,6 @@
 #include <string>
 
 namespace tsm {
-namespace {
 
 thread_local std::string g_last_error;
 
@@ -63,6 +61,8 @@ gemm_status_t fail_cuda(cudaError_t e, const char *what)
 {
     return fail(GEMM_ERR_CUDA, "%s: %s (%s)", what, cudaGetErrorName(e), cudaGetErrorString(e));
 }
+
+namespace {
 
 constexpr int kMaxDevices = 64;
 // Dynamic shared memory of a GEMM CTA outside its operand ring and epilogue
@@ -108,20 +108,10 @@ Driver &driver()
 
 // ------------------------------------------------------------- per-device state
 
-struct DeviceState {
-    bool ready = false;
-    int sms = 0;
-    int cc_major = 0, cc_minor = 0;
-    int smem_optin = 0;
-    bool attrs_set[46] = {};  // see attr_index
-    cudaMemPool_t pool = nullptr;
-    uint32_t *status = nullptr;
-    // Clusters of 2 and of 4 CTAs of the cluster-sum kernel that fit at once.
-    int caps2 = 0, caps4 = 0;
-};
-
 DeviceState g_devices[kMaxDevices];
 std::mutex g_device_mutex;
+
+}  // namespace
 
 gemm_status_t device_state(int dev, DeviceState **out)
 {
@@ -162,6 +152,8 @@ gemm_status_t device_state(int dev, DeviceState **out)
     *out = &s;
     return GEMM_OK;
 }
+
+namespace {
 
 // One slot per kernel instantiation: single-CTA tile_n 64 / 128 / 256, CTA-pair 128 / 256.
 int config_index(int tile_m, int tile_n)
@@ -207,6 +199,8 @@ struct Problem {
     Epilogue epi;
 };
 
+}  // namespace
+
 // Bytes spanned by `batch` matrices of `rows` x `cols` elements of `elem`
 // bytes, row stride `ld`, batch stride `stride` (all in elements).
 int64_t span_bytes(int64_t batch, int64_t stride, int64_t rows, int64_t ld, int64_t cols, int64_t elem)
@@ -224,6 +218,8 @@ bool overlaps(const void *p, int64_t pn, const void *q, int64_t qn)
     const uintptr_t b0 = reinterpret_cast<uintptr_t>(q), b1 = b0 + uint64_t(qn);
     return a0 < b1 && b0 < a1;
 }
+
+namespace {
 
 // Checks that need no GPU.  Sets *trivial when there is nothing to compute.
 gemm_status_t check_host(const Problem &pr, bool *trivial)
@@ -302,6 +298,8 @@ TmaLayout tma_layout(const Problem &pr)
     return t;
 }
 
+}  // namespace
+
 // The pointer is device memory of `dev` and its allocation covers `bytes`:
 // one driver query for the memory type, the managed flag, the device and the
 // allocation's range (a pointer the driver does not know comes back as type 0).
@@ -336,6 +334,8 @@ gemm_status_t check_device_pointer(const void *p, int64_t bytes, int dev, const 
 }
 
 // ------------------------------------------------------------- planner
+
+namespace {
 
 int ceil_div(int64_t a, int64_t b) { return int((a + b - 1) / b); }
 
@@ -661,11 +661,12 @@ constexpr int kMapCacheEntries = 16;
 thread_local MapCacheEntry t_map_cache[kMapCacheEntries];
 thread_local int t_map_cache_used = 0, t_map_cache_next = 0;
 
+}  // namespace
+
 gemm_status_t encode_3d(CUtensorMap *map, CUtensorMapDataType dt, int elem, const void *base,
                         int64_t cols, int64_t rows, int64_t mats, int64_t ld, int64_t stride,
                         uint32_t box_cols, uint32_t box_rows, CUtensorMapL2promotion promo,
-                        const char *name, uint32_t box_mats = 1,
-                        CUtensorMapSwizzle swizzle = CU_TENSOR_MAP_SWIZZLE_128B)
+                        const char *name, uint32_t box_mats, CUtensorMapSwizzle swizzle)
 {
     const MapKey key{uint64_t(reinterpret_cast<uintptr_t>(base)), cols, rows, mats, ld, stride,
                      box_cols, box_rows, box_mats, int32_t(dt), elem, int32_t(promo), int32_t(swizzle)};
@@ -698,6 +699,8 @@ gemm_status_t encode_3d(CUtensorMap *map, CUtensorMapDataType dt, int elem, cons
 
 // ------------------------------------------------------------- the call
 
+namespace {
+
 int64_t timeout_ns_for(const gemm_options_t *o, const gemm_plan_info_t &pl)
 {
     const int64_t base_ms = (o && o->timeout_ms > 0) ? o->timeout_ms : 2000;
@@ -706,8 +709,6 @@ int64_t timeout_ns_for(const gemm_options_t *o, const gemm_plan_info_t &pl)
 }
 
 gemm_status_t run(const Problem &pr, const gemm_options_t *o, cudaStream_t stream);
-
-int64_t round_up(int64_t x, int64_t m) { return (x + m - 1) / m * m; }
 
 // An operand the TMA cannot address (TmaLayout) goes through a packed,
 // aligned copy in the pool: A and B are copied in before the GEMM, C is
@@ -1205,7 +1206,6 @@ gemm_status_t gemv_f16_f32acc(const uint16_t *A, const uint16_t *x, float *y, in
 }  // extern "C"
 
 namespace tsm {
-namespace {
 
 // The public epilogue description, checked, as the kernels' Epilogue.
 gemm_status_t epilogue_of(const gemm_epilogue_t *e, Epilogue *out)
@@ -1225,6 +1225,8 @@ gemm_status_t epilogue_of(const gemm_epilogue_t *e, Epilogue *out)
     out->out_type = e->out_type;
     return GEMM_OK;
 }
+
+namespace {
 
 // Grouped calls: launches of at most kMaxGroupsPerLaunch groups, in stream order.
 gemm_status_t grouped(const uint16_t *A, const uint16_t *B, void *C, const int32_t *group_rows,

@@ -1,0 +1,558 @@
+// moe_kernels.cu -- moving token rows to their experts and back.
+//
+//   route         slots[t][j] = e * capacity + rank, e = ids[t][j], rank = the
+//                 number of earlier (t', j') < (t, j) with the same expert; -1
+//                 when rank >= capacity or e is no expert.
+//                 counts[e] = min(capacity, choices of e).
+//   dispatch      rows[slots[t][j]] = x[t]
+//   dispatch_grad dx[t] = sum_j drows[slots[t][j]]           (combine without weights)
+//   combine       out[t] = sum_j w[t][j] rows[slots[t][j]]
+//   combine_grad  drows[slots[t][j]] = w[t][j] dout[t],  dw[t][j] = <dout[t], rows[slots[t][j]]>
+//
+// All of it is bound by memory (one multiply-add for two to four bytes), or,
+// for a decode step's few tokens, by launch and load latency.  Every kernel
+// is built around the token: its row is read once for all its choices
+// (dispatch, combine_grad) or written once (combine), so each byte crosses
+// HBM once and no inverse map of the slots is needed.  Sums run in f32 over j
+// in ascending order, rounded once to the rows' type; there are no atomics on
+// floating-point data, so a call is bitwise reproducible.
+#include "ops_internal.h"
+
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+
+namespace tsm {
+
+namespace {
+
+// ------------------------------------------------------------- route
+
+// The expert of assignment i, or -1.
+template <bool WIDE>
+__device__ __forceinline__ int32_t expert_of(const RouteParams &p, int64_t i)
+{
+    if (i >= p.n)
+        return -1;
+    const int64_t e = WIDE ? static_cast<const long long *>(p.ids)[i]
+                           : int64_t(static_cast<const int32_t *>(p.ids)[i]);
+    return e >= 0 && e < p.groups ? int32_t(e) : -1;
+}
+
+// Counts per expert of one chunk (several chunks only).
+template <bool WIDE, int ROUNDS>
+__global__ void __launch_bounds__(32 * kRouteWarps) tsm_moe_count_kernel(RouteParams p)
+{
+    extern __shared__ uint32_t count[];
+    for (int e = int(threadIdx.x); e < p.groups; e += int(blockDim.x))
+        count[e] = 0;
+    __syncthreads();
+    const int64_t first = int64_t(blockIdx.x) * route_chunk(ROUNDS);
+#pragma unroll
+    for (int r = 0; r < ROUNDS; ++r) {
+        const int32_t e = expert_of<WIDE>(p, first + int64_t(r) * blockDim.x + threadIdx.x);
+        if (e >= 0)
+            atomicAdd(count + e, 1u);
+    }
+    __syncthreads();
+    for (int e = int(threadIdx.x); e < p.groups; e += int(blockDim.x))
+        p.hist[int64_t(blockIdx.x) * p.groups + e] = int32_t(count[e]);
+}
+
+// Ranks of one chunk.  Warp w holds ROUNDS x 32 consecutive assignments; a
+// lane's rank is what the warp counted in earlier rounds, plus the lower lanes
+// of the same expert (a warp match), plus the earlier warps' counts, plus the
+// earlier chunks' (summed here from the count kernel's table).
+template <bool WIDE, int ROUNDS>
+__global__ void __launch_bounds__(32 * kRouteWarps) tsm_moe_rank_kernel(RouteParams p)
+{
+    extern __shared__ uint32_t smem[];
+    uint32_t *const base = smem;                                        // [groups]
+    uint16_t *const seen = reinterpret_cast<uint16_t *>(smem + p.groups);  // [warps][groups]
+    const int warp = int(threadIdx.x >> 5), lane = int(threadIdx.x & 31);
+    const int G = p.groups;
+    const int64_t first = int64_t(blockIdx.x) * route_chunk(ROUNDS) + int64_t(warp) * 32 * ROUNDS;
+    int32_t id[ROUNDS];
+#pragma unroll
+    for (int r = 0; r < ROUNDS; ++r)
+        id[r] = expert_of<WIDE>(p, first + 32 * r + lane);
+    for (int i = lane; i < G; i += 32)
+        seen[warp * G + i] = 0;
+    // The earlier chunks' counts, while the ids are on their way.
+    for (int e = int(threadIdx.x); e < G; e += int(blockDim.x)) {
+        uint32_t before = 0;
+        for (int64_t c = 0; c < int64_t(blockIdx.x); ++c)
+            before += uint32_t(p.hist[c * G + e]);
+        base[e] = before;
+    }
+    __syncwarp();
+    uint32_t at[ROUNDS];
+#pragma unroll
+    for (int r = 0; r < ROUNDS; ++r) {
+        const uint32_t same = __match_any_sync(0xffffffffu, id[r]);
+        const uint32_t lower = __popc(same & ((1u << lane) - 1u));
+        uint32_t earlier = 0;
+        if (id[r] >= 0)
+            earlier = seen[warp * G + id[r]];
+        __syncwarp();
+        if (id[r] >= 0 && lower == 0)
+            seen[warp * G + id[r]] = uint16_t(earlier + __popc(same));
+        __syncwarp();
+        at[r] = earlier + lower;
+    }
+    __syncthreads();
+    // Exclusive sums over the warps, in place; the chunk's total on top of base.
+    const bool last = blockIdx.x == gridDim.x - 1;
+    for (int e = int(threadIdx.x); e < G; e += int(blockDim.x)) {
+        uint32_t sum = 0;
+        for (int w = 0; w < kRouteWarps; ++w) {
+            const uint32_t c = seen[w * G + e];
+            seen[w * G + e] = uint16_t(sum);
+            sum += c;
+        }
+        if (last)
+            p.counts[e] = int32_t(min(base[e] + sum, uint32_t(p.capacity)));
+    }
+    __syncthreads();
+#pragma unroll
+    for (int r = 0; r < ROUNDS; ++r) {
+        const int64_t i = first + 32 * r + lane;
+        if (i < p.n) {
+            int32_t slot = -1;
+            if (id[r] >= 0) {
+                const uint32_t rank = base[id[r]] + seen[warp * G + id[r]] + at[r];
+                if (rank < uint32_t(p.capacity))
+                    slot = id[r] * p.capacity + int32_t(rank);
+            }
+            p.slots[i] = slot;
+        }
+    }
+}
+
+// ------------------------------------------------------------- row types
+
+// One access of V elements of type ET (V x element size = 16 bytes, or V = 1).
+template <int ET, bool VEC>
+struct Piece {
+    static constexpr int EB = ET == kOutF32 ? 4 : 2;
+    static constexpr int V = VEC ? 16 / EB : 1;
+
+    static __device__ __forceinline__ void load(const void *row, int64_t i, float (&v)[V])
+    {
+        if constexpr (!VEC) {
+            v[0] = one(static_cast<const char *>(row) + i * EB);
+        } else {
+            const uint4 u = __ldg(static_cast<const uint4 *>(row) + i);
+            const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+                if constexpr (ET == kOutF32) {
+                    v[k] = __uint_as_float(w[k]);
+                } else if constexpr (ET == kOutF16) {
+                    const float2 f = __half22float2(*reinterpret_cast<const __half2 *>(&w[k]));
+                    v[2 * k] = f.x;
+                    v[2 * k + 1] = f.y;
+                } else {
+                    v[2 * k] = __uint_as_float(w[k] << 16);
+                    v[2 * k + 1] = __uint_as_float(w[k] & 0xffff0000u);
+                }
+            }
+        }
+    }
+    static __device__ __forceinline__ void store(void *row, int64_t i, const float (&v)[V])
+    {
+        if constexpr (!VEC) {
+            if constexpr (ET == kOutF32)
+                static_cast<float *>(row)[i] = v[0];
+            else if constexpr (ET == kOutF16)
+                static_cast<__half *>(row)[i] = __float2half_rn(v[0]);
+            else
+                static_cast<__nv_bfloat16 *>(row)[i] = __float2bfloat16_rn(v[0]);
+        } else {
+            uint32_t w[4];
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+                if constexpr (ET == kOutF32) {
+                    w[k] = __float_as_uint(v[k]);
+                } else if constexpr (ET == kOutF16) {
+                    const __half2 h = __floats2half2_rn(v[2 * k], v[2 * k + 1]);
+                    w[k] = *reinterpret_cast<const uint32_t *>(&h);
+                } else {
+                    const __nv_bfloat162 h = __floats2bfloat162_rn(v[2 * k], v[2 * k + 1]);
+                    w[k] = *reinterpret_cast<const uint32_t *>(&h);
+                }
+            }
+            static_cast<uint4 *>(row)[i] = make_uint4(w[0], w[1], w[2], w[3]);
+        }
+    }
+
+private:
+    static __device__ __forceinline__ float one(const char *p)
+    {
+        if constexpr (ET == kOutF32)
+            return __ldg(reinterpret_cast<const float *>(p));
+        else if constexpr (ET == kOutF16)
+            return __half2float(__ushort_as_half(__ldg(reinterpret_cast<const unsigned short *>(p))));
+        else
+            return __uint_as_float(uint32_t(__ldg(reinterpret_cast<const unsigned short *>(p))) << 16);
+    }
+};
+
+// Row `slot` of the experts' side exists.
+__device__ __forceinline__ bool has_row(const MoveParams &p, int32_t slot)
+{
+    return slot >= 0 && int64_t(slot) < p.rows;
+}
+
+// ------------------------------------------------------------- dispatch
+
+// A warp copies kCopyUnroll x 32 units of one token's row to all its slots.
+constexpr int kCopyUnroll = 4;
+
+template <typename U>
+__global__ void __launch_bounds__(256) tsm_moe_dispatch_kernel(MoveParams p)
+{
+    const int lane = int(threadIdx.x & 31);
+    const int64_t per = 32 * kCopyUnroll;
+    const int64_t segs = (p.width + per - 1) / per;
+    const int64_t warps = int64_t(gridDim.x) * (blockDim.x / 32);
+    for (int64_t i = int64_t(blockIdx.x) * (blockDim.x / 32) + (threadIdx.x >> 5); i < p.tokens * segs;
+         i += warps) {
+        const int64_t t = i / segs;
+        const int64_t c0 = (i - t * segs) * per + lane;
+        const U *src = static_cast<const U *>(p.src) + t * p.ld_src;
+        U v[kCopyUnroll];
+#pragma unroll
+        for (int k = 0; k < kCopyUnroll; ++k)
+            if (c0 + 32 * k < p.width)
+                v[k] = __ldg(src + c0 + 32 * k);
+        for (int64_t j = 0; j < p.topk; ++j) {
+            const int32_t slot = __ldg(p.slots + t * p.topk + j);
+            if (!has_row(p, slot))
+                continue;
+            U *dst = static_cast<U *>(p.dst) + int64_t(slot) * p.ld_dst;
+#pragma unroll
+            for (int k = 0; k < kCopyUnroll; ++k)
+                if (c0 + 32 * k < p.width)
+                    dst[c0 + 32 * k] = v[k];
+        }
+    }
+}
+
+// ------------------------------------------------------------- combine
+
+// A thread sums one piece of a token's row over its choices, kSumUnroll rows
+// loaded at a time.
+constexpr int kSumUnroll = 4;
+
+template <int ET, bool VEC>
+__global__ void __launch_bounds__(256) tsm_moe_combine_kernel(MoveParams p)
+{
+    using P = Piece<ET, VEC>;
+    const int64_t pieces = (p.width + P::V - 1) / P::V;
+    const int64_t total = p.tokens * pieces;
+    for (int64_t i = int64_t(blockIdx.x) * blockDim.x + threadIdx.x; i < total;
+         i += int64_t(gridDim.x) * blockDim.x) {
+        const int64_t t = i / pieces;
+        const int64_t c = i - t * pieces;
+        float acc[P::V];
+#pragma unroll
+        for (int k = 0; k < P::V; ++k)
+            acc[k] = 0.f;
+        for (int64_t j0 = 0; j0 < p.topk; j0 += kSumUnroll) {
+            float v[kSumUnroll][P::V];
+            float w[kSumUnroll];
+            bool on[kSumUnroll];
+#pragma unroll
+            for (int u = 0; u < kSumUnroll; ++u) {
+                on[u] = false;
+                if (j0 + u < p.topk) {
+                    const int32_t slot = __ldg(p.slots + t * p.topk + j0 + u);
+                    on[u] = has_row(p, slot);
+                    if (on[u]) {
+                        w[u] = p.weights ? __ldg(p.weights + t * p.topk + j0 + u) : 1.f;
+                        P::load(static_cast<const char *>(p.src) + int64_t(slot) * p.ld_src * P::EB, c, v[u]);
+                    }
+                }
+            }
+#pragma unroll
+            for (int u = 0; u < kSumUnroll; ++u)
+                if (on[u]) {
+#pragma unroll
+                    for (int k = 0; k < P::V; ++k)
+                        acc[k] = fmaf(w[u], v[u][k], acc[k]);
+                }
+        }
+        P::store(static_cast<char *>(p.dst) + t * p.ld_dst * P::EB, c, acc);
+    }
+}
+
+// ------------------------------------------------------------- combine's gradient
+
+// One CTA per token.  Choices are taken kGradUnroll at a time: each thread
+// walks its pieces of dout once for them, writes w dout and keeps one partial
+// dot product per choice; the partials meet in a fixed order (a butterfly in
+// the warp, then the warps in turn).
+constexpr int kGradUnroll = 6;
+constexpr int kGradThreads = 256;
+
+template <int ET, bool VEC>
+__global__ void __launch_bounds__(kGradThreads) tsm_moe_combine_grad_kernel(MoveParams p)
+{
+    using P = Piece<ET, VEC>;
+    __shared__ float part[kGradThreads / 32][kGradUnroll];
+    const int64_t t = blockIdx.x;
+    const int64_t pieces = (p.width + P::V - 1) / P::V;
+    const char *dout = static_cast<const char *>(p.dout) + t * p.ld_dout * P::EB;
+    const int warp = int(threadIdx.x >> 5), lane = int(threadIdx.x & 31);
+    for (int64_t j0 = 0; j0 < p.topk; j0 += kGradUnroll) {
+        float dot[kGradUnroll], w[kGradUnroll];
+        int32_t slot[kGradUnroll];
+#pragma unroll
+        for (int u = 0; u < kGradUnroll; ++u) {
+            dot[u] = 0.f;
+            w[u] = 0.f;
+            slot[u] = -1;
+            if (j0 + u < p.topk) {
+                slot[u] = __ldg(p.slots + t * p.topk + j0 + u);
+                w[u] = p.weights ? __ldg(p.weights + t * p.topk + j0 + u) : 1.f;
+                if (!has_row(p, slot[u]))
+                    slot[u] = -1;
+            }
+        }
+        for (int64_t c = threadIdx.x; c < pieces; c += kGradThreads) {
+            float d[P::V];
+            P::load(dout, c, d);
+#pragma unroll
+            for (int u = 0; u < kGradUnroll; ++u) {
+                if (slot[u] < 0)
+                    continue;
+                float y[P::V], g[P::V];
+                P::load(static_cast<const char *>(p.src) + int64_t(slot[u]) * p.ld_src * P::EB, c, y);
+                float s = 0.f;
+#pragma unroll
+                for (int k = 0; k < P::V; ++k) {
+                    s = fmaf(d[k], y[k], s);
+                    g[k] = w[u] * d[k];
+                }
+                dot[u] += s;
+                P::store(static_cast<char *>(p.dst) + int64_t(slot[u]) * p.ld_dst * P::EB, c, g);
+            }
+        }
+#pragma unroll
+        for (int u = 0; u < kGradUnroll; ++u) {
+#pragma unroll
+            for (int m = 16; m; m >>= 1)
+                dot[u] += __shfl_xor_sync(0xffffffffu, dot[u], m);
+            if (lane == 0)
+                part[warp][u] = dot[u];
+        }
+        __syncthreads();
+        if (threadIdx.x < kGradUnroll && j0 + threadIdx.x < p.topk && p.dweights) {
+            float s = 0.f;
+            for (int k = 0; k < kGradThreads / 32; ++k)
+                s += part[k][threadIdx.x];
+            p.dweights[t * p.topk + j0 + threadIdx.x] = s;
+        }
+        __syncthreads();
+    }
+}
+
+// ------------------------------------------------------------- row quantisation
+
+//   scale = max_k |x_k| / 127,  q_k = rint(x_k / scale)   (a row of zeros: scale 0, q 0;
+//   a row with an infinity or a NaN: scale NaN, q 0, so that its products are NaN)
+//
+// One CTA per row; a row of up to kQuantKeep pieces per thread stays in
+// registers between the maximum and the rounding, so it is read once.  The
+// quotient is the IEEE division, so the codes are those of the formula in f32
+// whatever the launch shape.
+constexpr int kQuantThreads = 256;
+constexpr int kQuantKeep = 4;
+
+template <int ET, bool VEC>
+__global__ void __launch_bounds__(kQuantThreads) tsm_quantize_rows_kernel(QuantParams p)
+{
+    using P = Piece<ET, VEC>;
+    __shared__ uint32_t part[kQuantThreads / 32];
+    const int64_t g = blockIdx.x / p.M;
+    const int64_t r = blockIdx.x - g * p.M;
+    if (p.group_rows && r >= int64_t(__ldg(p.group_rows + g)))
+        return;
+    const char *x = static_cast<const char *>(p.X) + (g * p.sX + r * p.ldx) * P::EB;
+    int8_t *q = p.q + g * p.sQ + r * p.ldq;
+    const int64_t pieces = p.K / P::V;  // whole pieces; the host takes VEC only then
+    float keep[kQuantKeep][P::V];
+    uint32_t top = 0;
+#pragma unroll
+    for (int i = 0; i < kQuantKeep; ++i) {
+        const int64_t c = threadIdx.x + int64_t(i) * kQuantThreads;
+        if (c < pieces) {
+            P::load(x, c, keep[i]);
+#pragma unroll
+            for (int k = 0; k < P::V; ++k)
+                top = max(top, __float_as_uint(keep[i][k]) & 0x7fffffffu);
+        }
+    }
+    for (int64_t c = threadIdx.x + int64_t(kQuantKeep) * kQuantThreads; c < pieces; c += kQuantThreads) {
+        float v[P::V];
+        P::load(x, c, v);
+#pragma unroll
+        for (int k = 0; k < P::V; ++k)
+            top = max(top, __float_as_uint(v[k]) & 0x7fffffffu);
+    }
+    top = __reduce_max_sync(0xffffffffu, top);
+    if ((threadIdx.x & 31) == 0)
+        part[threadIdx.x >> 5] = top;
+    __syncthreads();
+#pragma unroll
+    for (int k = 0; k < kQuantThreads / 32; ++k)
+        top = max(top, part[k]);
+    // As bits of non-negative floats the maximum orders infinities and NaNs last.
+    const bool finite = top < 0x7f800000u;
+    const float scale = finite ? __fdiv_rn(__uint_as_float(top), 127.f) : __uint_as_float(0x7fffffffu);
+    const bool zero = !finite || scale == 0.f;
+    if (threadIdx.x == 0)
+        p.scales[g * p.sS + r] = scale;
+    auto code = [&](float v) -> uint32_t {
+        if (zero)
+            return 0u;
+        // |v / scale| can pass 127 by a rounding (or, where the scale is subnormal, by more).
+        const float c = fminf(fmaxf(rintf(__fdiv_rn(v, scale)), -127.f), 127.f);
+        return uint32_t(int32_t(c)) & 0xffu;
+    };
+    auto put = [&](int64_t c, const float (&v)[P::V]) {
+        if constexpr (!VEC) {
+            q[c] = int8_t(code(v[0]));
+        } else {
+            uint32_t w[P::V / 4];
+#pragma unroll
+            for (int k = 0; k < P::V / 4; ++k)
+                w[k] = code(v[4 * k]) | code(v[4 * k + 1]) << 8 | code(v[4 * k + 2]) << 16 |
+                       code(v[4 * k + 3]) << 24;
+            if constexpr (P::V == 8)
+                reinterpret_cast<uint2 *>(q)[c] = make_uint2(w[0], w[1]);
+            else
+                reinterpret_cast<uint32_t *>(q)[c] = w[0];
+        }
+    };
+#pragma unroll
+    for (int i = 0; i < kQuantKeep; ++i) {
+        const int64_t c = threadIdx.x + int64_t(i) * kQuantThreads;
+        if (c < pieces)
+            put(c, keep[i]);
+    }
+    for (int64_t c = threadIdx.x + int64_t(kQuantKeep) * kQuantThreads; c < pieces; c += kQuantThreads) {
+        float v[P::V];
+        P::load(x, c, v);
+        put(c, v);
+    }
+}
+
+template <bool WIDE, int ROUNDS>
+cudaError_t route_as(const RouteParams &p, int64_t chunks, cudaStream_t stream)
+{
+    constexpr int threads = 32 * kRouteWarps;
+    if (chunks > 1)
+        tsm_moe_count_kernel<WIDE, ROUNDS><<<unsigned(chunks), threads, size_t(p.groups) * 4, stream>>>(p);
+    tsm_moe_rank_kernel<WIDE, ROUNDS><<<unsigned(chunks), threads,
+                                        size_t(p.groups) * (4 + 2 * kRouteWarps), stream>>>(p);
+    return cudaGetLastError();
+}
+
+template <typename U>
+void dispatch_as(const MoveParams &p, int sms, cudaStream_t stream)
+{
+    const int64_t segs = (p.width + 32 * kCopyUnroll - 1) / (32 * kCopyUnroll);
+    const int64_t blocks = (p.tokens * segs + 7) / 8;
+    tsm_moe_dispatch_kernel<U><<<unsigned(min(blocks, int64_t(sms) * 64)), 256, 0, stream>>>(p);
+}
+
+}  // namespace
+
+cudaError_t launch_route(const RouteParams &p, bool wide_ids, int rounds, int64_t chunks, cudaStream_t stream)
+{
+    if (rounds == kRouteRoundsSmall)
+        return wide_ids ? route_as<true, kRouteRoundsSmall>(p, chunks, stream)
+                        : route_as<false, kRouteRoundsSmall>(p, chunks, stream);
+    return wide_ids ? route_as<true, kRouteRoundsLarge>(p, chunks, stream)
+                    : route_as<false, kRouteRoundsLarge>(p, chunks, stream);
+}
+
+cudaError_t launch_dispatch(const MoveParams &p, int vec, int sms, cudaStream_t stream)
+{
+    switch (vec) {
+    case 16: dispatch_as<uint4>(p, sms, stream); break;
+    case 8: dispatch_as<uint2>(p, sms, stream); break;
+    case 4: dispatch_as<uint32_t>(p, sms, stream); break;
+    case 2: dispatch_as<unsigned short>(p, sms, stream); break;
+    default: dispatch_as<unsigned char>(p, sms, stream); break;
+    }
+    return cudaGetLastError();
+}
+
+cudaError_t launch_combine(const MoveParams &p, int elem, bool vec, int sms, cudaStream_t stream)
+{
+    const int64_t v = vec ? (elem == kOutF32 ? 4 : 8) : 1;
+    const int64_t blocks = (p.tokens * ((p.width + v - 1) / v) + 255) / 256;
+    const unsigned grid = unsigned(min(blocks, int64_t(sms) * 64));
+    if (vec) {
+        if (elem == kOutF32)
+            tsm_moe_combine_kernel<kOutF32, true><<<grid, 256, 0, stream>>>(p);
+        else if (elem == kOutF16)
+            tsm_moe_combine_kernel<kOutF16, true><<<grid, 256, 0, stream>>>(p);
+        else
+            tsm_moe_combine_kernel<kOutBF16, true><<<grid, 256, 0, stream>>>(p);
+    } else {
+        if (elem == kOutF32)
+            tsm_moe_combine_kernel<kOutF32, false><<<grid, 256, 0, stream>>>(p);
+        else if (elem == kOutF16)
+            tsm_moe_combine_kernel<kOutF16, false><<<grid, 256, 0, stream>>>(p);
+        else
+            tsm_moe_combine_kernel<kOutBF16, false><<<grid, 256, 0, stream>>>(p);
+    }
+    return cudaGetLastError();
+}
+
+cudaError_t launch_combine_grad(const MoveParams &p, int elem, bool vec, cudaStream_t stream)
+{
+    const unsigned grid = unsigned(p.tokens);
+    if (vec) {
+        if (elem == kOutF32)
+            tsm_moe_combine_grad_kernel<kOutF32, true><<<grid, kGradThreads, 0, stream>>>(p);
+        else if (elem == kOutF16)
+            tsm_moe_combine_grad_kernel<kOutF16, true><<<grid, kGradThreads, 0, stream>>>(p);
+        else
+            tsm_moe_combine_grad_kernel<kOutBF16, true><<<grid, kGradThreads, 0, stream>>>(p);
+    } else {
+        if (elem == kOutF32)
+            tsm_moe_combine_grad_kernel<kOutF32, false><<<grid, kGradThreads, 0, stream>>>(p);
+        else if (elem == kOutF16)
+            tsm_moe_combine_grad_kernel<kOutF16, false><<<grid, kGradThreads, 0, stream>>>(p);
+        else
+            tsm_moe_combine_grad_kernel<kOutBF16, false><<<grid, kGradThreads, 0, stream>>>(p);
+    }
+    return cudaGetLastError();
+}
+
+cudaError_t launch_quantize_rows(const QuantParams &p, int elem, bool vec, cudaStream_t stream)
+{
+    const unsigned grid = unsigned(p.M * p.batch);
+    if (vec) {
+        if (elem == kOutF32)
+            tsm_quantize_rows_kernel<kOutF32, true><<<grid, kQuantThreads, 0, stream>>>(p);
+        else if (elem == kOutF16)
+            tsm_quantize_rows_kernel<kOutF16, true><<<grid, kQuantThreads, 0, stream>>>(p);
+        else
+            tsm_quantize_rows_kernel<kOutBF16, true><<<grid, kQuantThreads, 0, stream>>>(p);
+    } else {
+        if (elem == kOutF32)
+            tsm_quantize_rows_kernel<kOutF32, false><<<grid, kQuantThreads, 0, stream>>>(p);
+        else if (elem == kOutF16)
+            tsm_quantize_rows_kernel<kOutF16, false><<<grid, kQuantThreads, 0, stream>>>(p);
+        else
+            tsm_quantize_rows_kernel<kOutBF16, false><<<grid, kQuantThreads, 0, stream>>>(p);
+    }
+    return cudaGetLastError();
+}
+
+}  // namespace tsm
