@@ -5,6 +5,7 @@
 #include "ops_internal.h"
 
 #include <algorithm>
+#include <mutex>
 
 namespace tsm {
 namespace {
@@ -375,6 +376,119 @@ gemm_status_t check_s8(const S8Params &p, bool *trivial)
     return GEMM_OK;
 }
 
+// An operand the tensor-memory accelerator can address (no copy needed).
+bool addressable(const int8_t *x, int64_t ld, int64_t stride, int64_t rows, int64_t batch)
+{
+    return !misaligned(x, 16) && (rows == 1 || ld % 16 == 0) && (batch == 1 || stride % 16 == 0);
+}
+
+std::once_flag g_s8_attr_once[64];
+cudaError_t g_s8_attr[64];
+
+// All checks are done and every size is positive (K may be 0).
+gemm_status_t launch_s8(S8Params p, DeviceState *ds, cudaStream_t stream)
+{
+    cudaError_t e;
+    if (p.K == 0) {
+        const int64_t total = int64_t(p.M) * p.N * p.batch;
+        const int grid = int(std::min<int64_t>((total + 255) / 256, int64_t(ds->sms) * 8));
+        e = launch_zero_fill(p.C, p.M, p.N, p.batch, p.ldc, p.sC, p.group_rows, p.epi, grid, stream);
+        return e == cudaSuccess ? GEMM_OK : fail_cuda(e, "int8 product of the empty sum");
+    }
+    int dev = 0;
+    if ((e = cudaGetDevice(&dev)) != cudaSuccess)
+        return fail_cuda(e, "cudaGetDevice");
+    std::call_once(g_s8_attr_once[dev], [dev] { g_s8_attr[dev] = set_s8_attributes(); });
+    if (g_s8_attr[dev] != cudaSuccess)
+        return fail_cuda(g_s8_attr[dev], "cudaFuncSetAttribute(int8 product)");
+
+    const bool pair = p.M > 128;
+    const S8Shape shape = s8_shape(pair);
+    p.tiles_m = int32_t((int64_t(p.M) + shape.tile_m - 1) / shape.tile_m);
+    p.tiles_n = int32_t((int64_t(p.N) + shape.tile_n - 1) / shape.tile_n);
+    p.kb = int32_t((int64_t(p.K) + shape.block_k - 1) / shape.block_k);
+    p.group_m = 8;
+    p.workers = pair ? ds->sms / 2 : ds->sms;
+    p.timeout_ns = 2000000000ull + uint64_t(p.kb) * 20000ull;
+    p.tag = next_launch_epoch() >> 16;
+    const int64_t per4 = p.epi.out_type == kOutF32 ? 16 : 8;
+    p.vec_c = !misaligned(p.C, per4) && p.ldc % 4 == 0 && (p.batch == 1 || p.sC % 4 == 0);
+
+    // Workspace: packed copies of operands that cannot be addressed, then the
+    // pieces' sums and arrival words.
+    const bool pack_a = !addressable(p.A, p.lda, p.sA, p.M, p.batch);
+    const bool pack_b = !addressable(p.B, p.ldb, p.sB, p.K, p.batch);
+    const int64_t lda2 = round_up(p.K, 16), ldb2 = round_up(p.N, 16);
+    const int64_t bytes_a = pack_a ? round_up(p.batch * p.M * lda2, 256) : 0;
+    const int64_t bytes_b = pack_b ? round_up(p.batch * int64_t(p.K) * ldb2, 256) : 0;
+    const int64_t tiles = int64_t(p.tiles_m) * p.tiles_n * p.batch;
+    if (tiles > S8Schedule::kMaxTiles)
+        return fail(GEMM_ERR_INVALID_VALUE, "more than 2^30 output tiles in one call");
+    S8Schedule sched;
+    sched.plan(int32_t(tiles), p.kb, p.workers);
+    // (A grouped launch's tiles are counted on the device: any number up to these.)
+    const int64_t cut = p.group_rows ? 2 * int64_t(p.workers) : sched.shared;
+    const int64_t bytes_p = cut ? 2 * int64_t(p.workers) * shape.slot_bytes : 0;
+    const int64_t bytes_w = cut * shape.parts * 8;
+    char *ws = nullptr;
+    if (bytes_a + bytes_b + bytes_p + bytes_w > 0 &&
+        (e = cudaMallocFromPoolAsync(reinterpret_cast<void **>(&ws), size_t(bytes_a + bytes_b + bytes_p + bytes_w),
+                                     ds->pool, stream)) != cudaSuccess)
+        return fail_cuda(e, "int8 product workspace");
+    gemm_status_t st = GEMM_OK;
+    if (pack_a) {
+        int8_t *to = reinterpret_cast<int8_t *>(ws);
+        if ((e = launch_pack_s8(p.A, p.lda, p.sA, to, lda2, p.M * lda2, p.M, p.K, p.batch, ds->sms, stream)) !=
+            cudaSuccess)
+            st = fail_cuda(e, "repacking A");
+        p.A = to;
+        p.lda = lda2;
+        p.sA = p.M * lda2;
+    }
+    if (pack_b && st == GEMM_OK) {
+        int8_t *to = reinterpret_cast<int8_t *>(ws + bytes_a);
+        if ((e = launch_pack_s8(p.B, p.ldb, p.sB, to, ldb2, p.K * ldb2, p.K, p.N, p.batch, ds->sms, stream)) !=
+            cudaSuccess)
+            st = fail_cuda(e, "repacking B");
+        p.B = to;
+        p.ldb = ldb2;
+        p.sB = p.K * ldb2;
+    }
+    if (bytes_w && st == GEMM_OK) {
+        // A captured launch is replayed with the tag it was captured with, so
+        // its graph clears the words that the replay before it counted up.
+        cudaStreamCaptureStatus capturing = cudaStreamCaptureStatusNone;
+        if ((e = cudaStreamIsCapturing(stream, &capturing)) != cudaSuccess)
+            st = fail_cuda(e, "cudaStreamIsCapturing");
+        else if (capturing != cudaStreamCaptureStatusNone &&
+                 (e = cudaMemsetAsync(ws + bytes_a + bytes_b + bytes_p, 0, size_t(bytes_w), stream)) != cudaSuccess)
+            st = fail_cuda(e, "clearing the arrival words");
+    }
+    p.partial = reinterpret_cast<int32_t *>(ws + bytes_a + bytes_b);
+    p.arrivals = reinterpret_cast<unsigned long long *>(ws + bytes_a + bytes_b + bytes_p);
+    alignas(64) CUtensorMap map_a, map_b;
+    // (A single row or matrix may have any pitch: the map wants a multiple of 16.)
+    const int64_t lda = p.M > 1 ? p.lda : round_up(p.lda, 16), ldb = p.K > 1 ? p.ldb : round_up(p.ldb, 16);
+    const int64_t sA = p.batch > 1 ? p.sA : p.M * lda, sB = p.batch > 1 ? p.sB : p.K * ldb;
+    if (st == GEMM_OK)
+        st = encode_3d(&map_a, CU_TENSOR_MAP_DATA_TYPE_UINT8, 1, p.A, p.K, p.M, p.batch, lda, sA, 128, 128,
+                       CU_TENSOR_MAP_L2_PROMOTION_L2_256B, "A");
+    if (st == GEMM_OK)
+        st = encode_3d(&map_b, CU_TENSOR_MAP_DATA_TYPE_UINT8, 1, p.B, p.N, p.K, p.batch, ldb, sB, 64, 128,
+                       CU_TENSOR_MAP_L2_PROMOTION_L2_256B, "B", 1, CU_TENSOR_MAP_SWIZZLE_NONE);
+    if (st == GEMM_OK) {
+        const int64_t most = p.group_rows ? p.workers
+                                          : std::max<int64_t>(sched.shared ? sched.cutters : 0,
+                                                              std::min<int64_t>(sched.tiles, p.workers));
+        e = launch_s8_tiled(map_a, map_b, p, pair, int(most) * (pair ? 2 : 1), stream);
+        if (e != cudaSuccess)
+            st = fail_cuda(e, "int8 product launch");
+    }
+    if (ws)
+        cudaFreeAsync(ws, stream);
+    return st;
+}
+
 gemm_status_t run_s8(S8Params p, cudaStream_t stream)
 {
     bool trivial = false;
@@ -396,8 +510,7 @@ gemm_status_t run_s8(S8Params p, cudaStream_t stream)
     if ((st = current(&dev, &ds)) != GEMM_OK || (st = check_on_device(buf, 7, dev)) != GEMM_OK)
         return st;
     p.status = ds->status;
-    const cudaError_t e = launch_s8_simple(p, stream);
-    return e == cudaSuccess ? GEMM_OK : fail_cuda(e, "int8 product launch");
+    return launch_s8(p, ds, stream);
 }
 
 gemm_status_t s8_call(const int8_t *A, const int8_t *B, void *C, const float *scale_a, const float *scale_b,
@@ -409,8 +522,9 @@ gemm_status_t s8_call(const int8_t *A, const int8_t *B, void *C, const float *sc
     if (M < 0 || N < 0 || K < 0 || batch < 0)
         return fail(GEMM_ERR_INVALID_VALUE, "negative size: M=%lld N=%lld K=%lld batch=%lld", (long long)M,
                     (long long)N, (long long)K, (long long)batch);
-    if (M > kInt32Max || N > kInt32Max || batch > kInt32Max)
-        return fail(GEMM_ERR_INVALID_VALUE, "M, N and batch must be below 2^31");
+    // (Tile coordinates past the edges stay below 2^31.)
+    if (M > kInt32Max - 512 || N > kInt32Max - 512 || batch > kInt32Max)
+        return fail(GEMM_ERR_INVALID_VALUE, "M and N must be below 2^31 - 512, batch below 2^31");
     // |S| <= 128 * 128 * K has to fit 32 bits.
     if (K > 131071)
         return fail(GEMM_ERR_INVALID_VALUE, "K must be below 131072: longer sums can pass 32 bits");
@@ -438,9 +552,24 @@ gemm_status_t s8_call(const int8_t *A, const int8_t *B, void *C, const float *sc
     p.sA = batch > 1 ? strideA : 0;
     p.sB = batch > 1 ? strideB : 0;
     p.sC = batch > 1 ? strideC : 0;
-    p.group_rows = group_rows;
     p.epi = e;
-    return run_s8(p, stream);
+    if (!grouped)
+        return run_s8(p, stream);
+    // Launches of at most kMaxGroupsPerLaunch groups, in stream order.
+    for (int64_t g0 = 0; g0 < batch; g0 += kMaxGroupsPerLaunch) {
+        S8Params q = p;
+        q.batch = int32_t(std::min<int64_t>(kMaxGroupsPerLaunch, batch - g0));
+        q.A = A ? A + g0 * p.sA : A;
+        q.B = B ? B + g0 * p.sB : B;
+        q.C = C ? static_cast<char *>(C) + g0 * p.sC * e.out_bytes() : C;
+        q.scale_a = scale_a ? scale_a + g0 * scale_a_stride : scale_a;
+        q.scale_b = scale_b ? scale_b + g0 * scale_b_stride : scale_b;
+        q.epi.bias = e.bias ? e.bias + g0 * e.bias_stride : e.bias;
+        q.group_rows = group_rows + g0;
+        if ((st = run_s8(q, stream)) != GEMM_OK)
+            return st;
+    }
+    return GEMM_OK;
 }
 
 }  // namespace

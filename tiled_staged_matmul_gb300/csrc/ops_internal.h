@@ -60,6 +60,40 @@ cudaError_t launch_quantize_rows(const QuantParams &p, int elem, bool vec, cudaS
 
 // ------------------------------------------------------------- int8 products
 
+// The work of one launch: `tiles` output tiles of `kb` k-blocks each, spread
+// over `workers` CTAs (or CTA pairs).  As many whole waves of tiles as leave
+// between one and two waves over run tile by tile; the tiles left over (the
+// first `shared` ones) are cut as one long row of shared * kb blocks into
+// equal pieces, one per worker, which starts with its piece.  A tile that
+// several workers hold pieces of is summed by the one that arrives last, in
+// integers, so the order does not matter.
+struct S8Schedule {
+    int32_t tiles;
+    int32_t shared;         // tiles cut into pieces: 0 .. shared - 1 (fewer than two per worker)
+    int32_t kb;
+    int32_t workers;        // of the whole tiles
+    int32_t cutters;        // workers that get a piece
+    static constexpr int kMinPiece = 2;
+    static constexpr int32_t kMaxTiles = 1 << 30;
+
+    __host__ __device__ void plan(int32_t tiles_, int32_t kb_, int32_t workers_)
+    {
+        tiles = tiles_;
+        kb = kb_;
+        workers = workers_;
+        const int32_t over = tiles % workers;
+        shared = over == 0 ? 0 : tiles < workers ? tiles : over + workers;
+        // At least one piece per tile, however few blocks that is.
+        const int32_t pieces = kb < kMinPiece ? shared : shared * kb / kMinPiece;
+        cutters = pieces < 1 ? 1 : pieces < workers ? pieces : workers;
+    }
+    // First block of worker w's piece (w <= cutters).
+    __host__ __device__ int32_t piece_begin(int32_t w) const { return shared * kb * w / cutters; }
+    // The worker whose piece holds block x.
+    __host__ __device__ int32_t owner(int32_t x) const { return ((x + 1) * cutters - 1) / (shared * kb); }
+};
+
+// Arguments of a product (device pointers; strides in elements).
 struct S8Params {
     const int8_t *A, *B;
     void *C;                  // epi.out_type elements
@@ -70,8 +104,31 @@ struct S8Params {
     int64_t lda, ldb, ldc, sA, sB, sC;
     const int32_t *group_rows;  // grouped: the rows of each matrix, clamped to [0, M]; else null
     Epilogue epi;
+    // What the launch adds.
     uint32_t *status;
+    uint64_t timeout_ns;
+    int32_t tiles_m, tiles_n, kb;
+    int32_t group_m;            // raster: tiles of M walked together
+    int32_t workers;
+    int32_t vec_c;              // C's rows take stores of four elements
+    int32_t *partial;           // sums of pieces: two slots per worker
+    unsigned long long *arrivals;  // one word per part of a shared tile: launch tag, count
+    unsigned long long tag;     // 48 bits, unique to the launch
 };
-cudaError_t launch_s8_simple(const S8Params &p, cudaStream_t stream);
+
+// The tiled kernel: a CTA pair per 256 x 256 tile, or one CTA per 128 x 128.
+struct S8Shape {
+    int tile_m, tile_n, block_k;
+    int64_t slot_bytes;         // of one worker's partial sums of one tile
+    int parts;                  // arrival words per tile
+};
+S8Shape s8_shape(bool pair);
+cudaError_t set_s8_attributes();
+cudaError_t launch_s8_tiled(const CUtensorMap &map_a, const CUtensorMap &map_b, const S8Params &p, bool pair,
+                            int grid, cudaStream_t stream);
+// Rows of `cols` bytes into rows 16-byte aligned and `d_ld` apart.
+cudaError_t launch_pack_s8(const int8_t *src, int64_t s_ld, int64_t s_stride, int8_t *dst, int64_t d_ld,
+                           int64_t d_stride, int64_t rows, int64_t cols, int64_t batch, int sms,
+                           cudaStream_t stream);
 
 }  // namespace tsm

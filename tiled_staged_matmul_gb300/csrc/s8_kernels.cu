@@ -2,93 +2,805 @@
 // column:
 //
 //   C[i][j] = act(alpha * scale_a[i] * scale_b[j] * S[i][j] + bias[j]),
-//   S[i][j] = sum_k A[i][k] B[k][j]   (a 32-bit integer sum, exact)
+//   S[i][j] = sum_k A[i][k] B[k][j]   (the exact 32-bit integer)
 //
-// One 64 x 64 tile per block, K in steps of 32: both operands are staged in
-// shared memory as words of four consecutive k (B's bytes transposed on the
-// way in), each thread adds four-way byte products into a 4 x 4 block.
+// The tensor cores' rate for 8-bit integers on this part is a small fraction
+// of their f16 rate, but f16 holds every integer up to 2048 exactly, so the
+// f16 pipe can do the work: a product of two codes is at most 2^14, exact in
+// the f32 accumulator, and so is the sum of 1024 of them (2^24).  The kernels
+// therefore feed the codes as f16 and take the accumulator out into 32-bit
+// integers every 1024 of K: S is exact, whatever the order of the pieces.
+//
+// A code becomes f16 without a conversion instruction: byte c of a word, sign
+// bit flipped (c + 128), placed below the byte 0x64 is the f16 number
+// 1024 + (c + 128); subtracting 1152 leaves c, exactly.  Five instructions
+// turn four codes into two f16 pairs.
 #include "gemm_kernel.cuh"
 #include "ops_internal.h"
+#include "s8_ptx.cuh"
 
 namespace tsm {
 
 namespace {
 
-constexpr int kSimpleTile = 64, kSimpleK = 32;
+constexpr int kChunkBlocks = 8;  // k-blocks of 128 whose sums the f32 accumulator holds exactly
 
-__global__ void __launch_bounds__(256) tsm_s8_simple_kernel(S8Params p)
+// Four codes (k, k+1, k+2, k+3 of a word) as two f16 pairs.
+__device__ __forceinline__ void codes_to_f16(uint32_t w, uint32_t &lo, uint32_t &hi)
 {
-    __shared__ int32_t as[kSimpleK / 4][kSimpleTile + 1];
-    __shared__ int32_t bs[kSimpleK / 4][kSimpleTile + 1];
-    const int64_t z = blockIdx.z;
-    const int rows = p.group_rows ? min(max(p.group_rows[z], 0), p.M) : p.M;
-    if (p.group_rows && blockIdx.x == 0 && blockIdx.y == 0 && threadIdx.x == 0 &&
-        (p.group_rows[z] < 0 || p.group_rows[z] > p.M))
-        atomicOr(p.status, kStatusGroupRows);
-    const int64_t m0 = int64_t(blockIdx.y) * kSimpleTile;
-    const int64_t n0 = int64_t(blockIdx.x) * kSimpleTile;
-    if (m0 >= rows)
-        return;
-    const int8_t *A = p.A + z * p.sA, *B = p.B + z * p.sB;
-    const int tx = int(threadIdx.x & 15), ty = int(threadIdx.x >> 4);
-    int32_t acc[4][4] = {};
-    for (int32_t k0 = 0; k0 < p.K; k0 += kSimpleK) {
-        for (int i = int(threadIdx.x); i < kSimpleTile * (kSimpleK / 4); i += 256) {
-            const int64_t m = m0 + i / (kSimpleK / 4);
-            const int kq = i % (kSimpleK / 4);
-            uint32_t w = 0;
-            for (int b = 0; b < 4; ++b) {
-                const int64_t k = int64_t(k0) + 4 * kq + b;
-                if (m < rows && k < p.K)
-                    w |= uint32_t(uint8_t(A[m * p.lda + k])) << (8 * b);
-            }
-            as[kq][i / (kSimpleK / 4)] = int32_t(w);
-        }
-        for (int i = int(threadIdx.x); i < kSimpleTile * (kSimpleK / 4); i += 256) {
-            const int64_t n = n0 + i % kSimpleTile;
-            const int kq = i / kSimpleTile;
-            uint32_t w = 0;
-            for (int b = 0; b < 4; ++b) {
-                const int64_t k = int64_t(k0) + 4 * kq + b;
-                if (n < p.N && k < p.K)
-                    w |= uint32_t(uint8_t(B[k * p.ldb + n])) << (8 * b);
-            }
-            bs[kq][i % kSimpleTile] = int32_t(w);
-        }
-        __syncthreads();
-#pragma unroll
-        for (int kq = 0; kq < kSimpleK / 4; ++kq)
-#pragma unroll
-            for (int i = 0; i < 4; ++i)
-#pragma unroll
-                for (int j = 0; j < 4; ++j)
-                    acc[i][j] = __dp4a(as[kq][ty * 4 + i], bs[kq][tx + 16 * j], acc[i][j]);
-        __syncthreads();
+    const uint32_t u = w ^ 0x80808080u;
+    const uint32_t l = __byte_perm(u, 0x64646464u, 0x4140);
+    const uint32_t h = __byte_perm(u, 0x64646464u, 0x4342);
+    const __half2 off = __half2half2(__ushort_as_half(0x6480));  // 1152
+    const __half2 a = __hsub2(*reinterpret_cast<const __half2 *>(&l), off);
+    const __half2 b = __hsub2(*reinterpret_cast<const __half2 *>(&h), off);
+    lo = *reinterpret_cast<const uint32_t *>(&a);
+    hi = *reinterpret_cast<const uint32_t *>(&b);
+}
+
+// ------------------------------------------------------------- tiled kernel
+//
+// One persistent CTA (or CTA pair) per SM (pair of SMs), warp-specialised:
+//   warp 0       TMA producer: codes of A (128 rows x 128 k) and B (128 k x 128
+//                columns) into the code ring
+//   warp 1       MMA issuer (the pair's leader): A from TMEM, B from shared memory
+//   warps 4-7    A's codes -> f16 -> TMEM, one row per lane (they never pass
+//                through shared memory as f16)
+//   warps 8-11   B's codes -> f16 -> the 128-byte swizzled layout of the MMA
+//   warps 12-19  two per TMEM lane quarter, one per column half of the tile:
+//                accumulator -> 32-bit sums in registers, then the epilogue
+// The bound is shared-memory bandwidth: a 256 x 256 x 128 block costs an SM
+// 32 KB of codes in, 32 KB out to the converters, 32 KB of f16 B written and
+// 32 KB read by the MMAs = 1024 cycles at 128 bytes, just the time its MMAs
+// take; with A's f16 in shared memory too it would be 1.5 times that.
+//
+// The tile's two column halves have an accumulator each, and every k-block
+// does all of half 0 and then all of half 1.  So when a chunk of 1024 k ends,
+// half 0 is read out while half 1 still computes its last block, and half 1
+// while half 0 starts the next chunk.
+template <bool PAIR>
+struct S8Cfg {
+    static constexpr int ROWS = 128;
+    static constexpr int CTAS = PAIR ? 2 : 1;
+    static constexpr int TILE_M = ROWS * CTAS;
+    static constexpr int HC = 64 * CTAS;        // columns of one half: the MMA's width
+    static constexpr int TILE_N = 2 * HC;
+    static constexpr int BK = 128;
+    static constexpr int A_CODES = ROWS * BK;   // bytes
+    static constexpr int B_BOX = 64 * BK;       // 64 columns of codes
+    static constexpr int CODE_STAGE = A_CODES + 2 * B_BOX;
+    static constexpr int F_BOX = 64 * BK * 2;   // 64 columns of f16
+    static constexpr int F_STAGE = 2 * F_BOX;
+    static constexpr int S1 = 3, S2 = 3;        // ring depths
+    static constexpr int STAGING = 8 * 32 * 32 * 4;
+    static constexpr int CTRL = 2048, GROUP_TABLE_OFF = 1024;
+    static constexpr int SMEM_BYTES = 1024 + S1 * CODE_STAGE + S2 * F_STAGE + STAGING + CTRL;
+    static_assert(SMEM_BYTES <= 232448, "227 KiB per block");
+    static constexpr uint32_t ACC_COL = 0;      // two accumulators of HC columns
+    static constexpr uint32_t A_COL = 256;      // the f16 A ring: BK / 2 columns per stage
+    static_assert(A_COL + S2 * (BK / 2) <= 512 && 2 * HC <= 256, "TMEM columns");
+    static constexpr int PARTS = 2 * CTAS;      // (CTA, half) parts of a tile
+    static constexpr int64_t SLOT_INTS = int64_t(PARTS) * ROWS * HC;
+};
+
+constexpr int kS8Threads = 640;
+// Registers per thread by warpgroup (five of 128 threads): together exactly
+// what the block was launched with (640 x 96).
+constexpr int kS8RegsIssue = 48, kS8RegsConvert = 56, kS8RegsDrain = 160;
+static_assert(128 * kS8RegsIssue + 256 * kS8RegsConvert + 256 * kS8RegsDrain <= kS8Threads * 96,
+              "register split");
+
+// The schedule in shared memory, read field by field: the registers are for
+// the sums.
+struct SharedSchedule {
+    uint32_t at;
+    __device__ __forceinline__ void put(const S8Schedule &s) const
+    {
+        ptx::st_shared_u32(at, uint32_t(s.tiles));
+        ptx::st_shared_u32(at + 4, uint32_t(s.shared));
+        ptx::st_shared_u32(at + 8, uint32_t(s.kb));
+        ptx::st_shared_u32(at + 12, uint32_t(s.workers));
+        ptx::st_shared_u32(at + 16, uint32_t(s.cutters));
     }
-    for (int i = 0; i < 4; ++i) {
-        const int64_t m = m0 + ty * 4 + i;
-        for (int j = 0; j < 4; ++j) {
-            const int64_t n = n0 + tx + 16 * j;
-            if (m >= rows || n >= p.N)
-                continue;
-            float v = float(acc[i][j]);
-            if (p.scale_a)
-                v *= p.scale_a[z * p.sa_stride + m];
-            if (p.scale_b)
-                v *= p.scale_b[z * p.sb_stride + n];
-            const float bias = p.epi.bias ? p.epi.bias[z * p.epi.bias_stride + n] : 0.f;
-            epi_store(p.C, z * p.sC + m * p.ldc + n, epi_value(v, bias, p.epi), p.epi.out_type);
+    __device__ __forceinline__ int32_t tiles() const { return int32_t(ptx::ld_shared_u32(at)); }
+    __device__ __forceinline__ int32_t kb() const { return int32_t(ptx::ld_shared_u32(at + 8)); }
+    __device__ __forceinline__ int32_t workers() const { return int32_t(ptx::ld_shared_u32(at + 12)); }
+    __device__ __forceinline__ S8Schedule all() const
+    {
+        S8Schedule s;
+        s.tiles = tiles();
+        s.shared = int32_t(ptx::ld_shared_u32(at + 4));
+        s.kb = kb();
+        s.workers = workers();
+        s.cutters = int32_t(ptx::ld_shared_u32(at + 16));
+        return s;
+    }
+};
+
+// One worker's pieces in order: its share of the cut tiles, then whole tiles.
+struct PieceWalk {
+    int32_t cur, end, next;  // blocks of the cut tiles; next whole tile
+    int32_t tile, kb0, kb1;
+    __device__ __forceinline__ PieceWalk(const SharedSchedule &shared, int32_t w)
+    {
+        const S8Schedule s = shared.all();
+        const bool cuts = s.shared > 0 && w < s.cutters;
+        cur = cuts ? s.piece_begin(w) : 0;
+        end = cuts ? s.piece_begin(w + 1) : 0;
+        next = s.shared + w;
+        tile = kb0 = kb1 = 0;
+    }
+    __device__ __forceinline__ bool advance(const SharedSchedule &s)
+    {
+        kb0 = 0;
+        kb1 = s.kb();
+        if (cur < end) {
+            tile = cur / kb1;
+            kb0 = cur - tile * kb1;
+            kb1 = min(kb1, kb0 + (end - cur));
+            cur += kb1 - kb0;
+            return true;
+        }
+        tile = next;
+        next += s.workers();
+        return tile < s.tiles();
+    }
+};
+
+// Where a tile lies.
+struct S8Tile {
+    int32_t m0, n0, z, rows;
+};
+
+__device__ __forceinline__ S8Tile tile_at(int32_t t, const S8Params &p, uint32_t gtab, int tile_m, int tile_n)
+{
+    S8Tile w;
+    int32_t tiles_m = p.tiles_m;
+    if (p.group_rows) {
+        int32_t lo = 0, hi = p.batch - 1;
+        while (lo < hi) {
+            const int32_t mid = (lo + hi) >> 1;
+            if (int32_t(ptx::ld_shared_u32(gtab + 4u * mid)) > t)
+                hi = mid;
+            else
+                lo = mid + 1;
+        }
+        const int32_t first = lo ? int32_t(ptx::ld_shared_u32(gtab + 4u * (lo - 1))) : 0;
+        tiles_m = (int32_t(ptx::ld_shared_u32(gtab + 4u * lo)) - first) / p.tiles_n;
+        t -= first;
+        w.z = lo;
+        w.rows = min(max(p.group_rows[lo], 0), p.M);
+    } else {
+        const int32_t per = p.tiles_m * p.tiles_n;
+        w.z = t / per;
+        t -= w.z * per;
+        w.rows = p.M;
+    }
+    const int32_t group = p.group_m * p.tiles_n;
+    const int32_t g = t / group;
+    const int32_t first_m = g * p.group_m;
+    const int32_t in_group = min(tiles_m - first_m, p.group_m);
+    const int32_t r = t - g * group;
+    w.m0 = (first_m + r % in_group) * tile_m;
+    w.n0 = r / in_group * tile_n;
+    return w;
+}
+
+// Count one arrival on `word` (a whole warp calls it): true for the last of
+// `total`.  The word holds the launch's tag and the count; under another tag
+// (whatever the workspace's last user left there) the count is none.  A failed
+// exchange means that another of the at most `total` contributors has arrived,
+// so the loop ends.  The loop is the warp's, not one lane's, so that the
+// compiler need not plan for a warp that has come apart.
+__device__ __forceinline__ bool arrive_last(unsigned long long *word, unsigned long long tag, uint32_t total, int lane)
+{
+    unsigned long long old = __shfl_sync(0xffffffffu, ptx::ld_relaxed_gpu(word), 0);
+    for (;;) {
+        const uint32_t seen = (old >> 16) == tag ? uint32_t(old & 0xffffu) : 0u;
+        unsigned long long prev = 0;
+        if (lane == 0)
+            prev = atomicCAS(word, old, (tag << 16) | (seen + 1u));
+        prev = __shfl_sync(0xffffffffu, prev, 0);
+        if (prev == old)
+            return seen + 1u == total;
+        old = prev;
+    }
+}
+
+// Bounded mbarrier wait, as wait_bounded, with nothing kept in registers
+// between waits: the CTA's abort flag is the word at `flag` in shared memory
+// (in a pair, at the same place in the peer), the limit and the status word
+// are the launch's.
+template <bool PAIR>
+__device__ __forceinline__ bool s8_wait(uint32_t bar, uint32_t parity, uint32_t flag, const S8Params &p, uint32_t who,
+                                        bool honor_abort = true)
+{
+    auto try_wait = [&]() {
+        return PAIR ? ptx::mbar_try_wait_cluster(bar, parity) : ptx::mbar_try_wait(bar, parity);
+    };
+    if (try_wait())
+        return true;
+    const uint64_t t0 = ptx::globaltimer_ns();
+    for (uint32_t it = 1;; ++it) {
+        if (try_wait())
+            return true;
+        if ((it & 31u) == 0) {
+            if (honor_abort && ptx::ld_shared_u32(flag))
+                return false;
+            if (ptx::globaltimer_ns() - t0 > p.timeout_ns) {
+                ptx::st_shared_u32(flag, 1u);
+                if (PAIR)
+                    ptx::st_cluster_u32(ptx::mapa_shared(flag, ptx::cluster_ctarank() ^ 1u), 1u);
+                atomicOr(p.status, who);
+                return false;
+            }
         }
     }
 }
 
+// Four values of a row through the epilogue into C.
+__device__ __forceinline__ void put4(const S8Params &p, int64_t at, int32_t col, float4 v, const float (&sb)[4],
+                                     const float (&bias)[4])
+{
+    float o[4] = {v.x, v.y, v.z, v.w};
+    with_activation<kActRuntime>(p.epi.act, [&](auto act) {
+#pragma unroll
+        for (int k = 0; k < 4; ++k)
+            o[k] = epi_act(fmaf(sb[k], o[k], bias[k]), decltype(act)::value, p.epi.slope);
+    });
+    if (p.vec_c && col + 3 < p.N) {
+        if (p.epi.out_type == kOutF32)
+            *reinterpret_cast<float4 *>(static_cast<float *>(p.C) + at) = make_float4(o[0], o[1], o[2], o[3]);
+        else
+            *reinterpret_cast<uint2 *>(static_cast<uint16_t *>(p.C) + at) =
+                make_uint2(epi_out16(o[0], p.epi.out_type) | (epi_out16(o[1], p.epi.out_type) << 16),
+                           epi_out16(o[2], p.epi.out_type) | (epi_out16(o[3], p.epi.out_type) << 16));
+        return;
+    }
+#pragma unroll
+    for (int k = 0; k < 4; ++k)
+        if (col + k < p.N)
+            epi_store(p.C, at + k, o[k], p.epi.out_type);
+}
+
+// Column scales (times alpha) and biases of four columns.
+__device__ __forceinline__ void column_terms(const S8Params &p, int32_t z, int32_t col, float (&sb)[4],
+                                             float (&bias)[4])
+{
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+        const bool in = col + k < p.N;
+        sb[k] = p.epi.alpha;
+        if (p.scale_b && in)
+            sb[k] *= __ldg(p.scale_b + z * p.sb_stride + col + k);
+        bias[k] = p.epi.bias && in ? __ldg(p.epi.bias + z * p.epi.bias_stride + col + k) : 0.f;
+    }
+}
+
+template <bool PAIR>
+__global__ void __launch_bounds__(kS8Threads, 1)
+    tsm_s8_tiled_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ CUtensorMap map_b,
+                        const S8Params p)
+{
+    using Cfg = S8Cfg<PAIR>;
+    constexpr int S1 = Cfg::S1, S2 = Cfg::S2;
+    extern __shared__ uint8_t smem_raw[];
+    const uint32_t raw = ptx::smem_addr(smem_raw);
+    const uint32_t base = (raw + 1023u) & ~1023u;
+    uint8_t *const base_ptr = smem_raw + (base - raw);
+    const uint32_t codes0 = base;
+    const uint32_t f16_0 = codes0 + S1 * Cfg::CODE_STAGE;
+    const uint32_t staging = f16_0 + S2 * Cfg::F_STAGE;
+    const uint32_t ctrl = staging + Cfg::STAGING;
+    uint8_t *const ctrl_ptr = base_ptr + (ctrl - base);
+
+    // Barriers.  `ready` and `tempty` are used in the pair's leader only.
+    const uint32_t full0 = ctrl;               // [S1] codes landed
+    const uint32_t empty0 = ctrl + 32u;        // [S1] codes read by the converters
+    const uint32_t ready0 = ctrl + 64u;        // [S2] f16 written (both CTAs)
+    const uint32_t free0 = ctrl + 96u;         // [S2] MMAs that read the f16 are done
+    const uint32_t tfull0 = ctrl + 128u;       // [2] accumulator complete
+    const uint32_t tempty0 = ctrl + 144u;      // [2] accumulator read out
+    const uint32_t done_bar = ctrl + 160u;     // all MMAs completed
+    uint32_t *const tmem_slot = reinterpret_cast<uint32_t *>(ctrl_ptr + 176);
+    const uint32_t flag = ctrl + 180u;         // this CTA gives up
+    const SharedSchedule sched{ctrl + 256u};
+    const uint32_t last_flag = ctrl + 184u;    // [2] one per column half
+    const uint32_t gtab = ctrl + Cfg::GROUP_TABLE_OFF;
+
+    const int warp = __shfl_sync(0xffffffffu, int(threadIdx.x >> 5), 0);  // (uniform to the compiler)
+    const int lane = int(threadIdx.x & 31);
+    const uint32_t rank = PAIR ? ptx::cluster_ctarank() : 0u;
+    const int32_t worker = int32_t(PAIR ? (blockIdx.x >> 1) : blockIdx.x);
+
+    if (threadIdx.x == 0) {
+        for (int s = 0; s < S1; ++s) {
+            ptx::mbar_init(full0 + 8u * s, 1);
+            ptx::mbar_init(empty0 + 8u * s, 8);
+        }
+        for (int s = 0; s < S2; ++s) {
+            ptx::mbar_init(ready0 + 8u * s, 8 * Cfg::CTAS);
+            ptx::mbar_init(free0 + 8u * s, 1);
+        }
+        for (int h = 0; h < 2; ++h) {
+            ptx::mbar_init(tfull0 + 8u * h, 1);
+            ptx::mbar_init(tempty0 + 8u * h, 4 * Cfg::CTAS);
+        }
+        ptx::mbar_init(done_bar, 1);
+        ptx::st_shared_u32(flag, 0u);
+        ptx::fence_mbar_init();
+        ptx::prefetch_tensormap(&map_a);
+        ptx::prefetch_tensormap(&map_b);
+    }
+    __syncwarp();
+    if constexpr (PAIR)
+        ptx::cluster_sync();
+    if (warp == 1) {
+        ptx::tmem_alloc<PAIR>(ptx::smem_addr(tmem_slot), 512);
+        ptx::tmem_relinquish<PAIR>();
+    } else if (warp == 2 && p.group_rows) {
+        build_group_table(p.group_rows, p.batch, p.M, Cfg::TILE_M, p.tiles_n,
+                          reinterpret_cast<uint32_t *>(ctrl_ptr + Cfg::GROUP_TABLE_OFF), p.status);
+        __syncwarp();
+    }
+    if (warp == 2 && lane == 0) {
+        S8Schedule s;
+        s.plan(p.group_rows ? int32_t(ptx::ld_shared_u32(gtab + 4u * (p.batch - 1))) : p.tiles_m * p.tiles_n * p.batch, p.kb, p.workers);
+        sched.put(s);
+    }
+    ptx::tc_fence_before_sync();
+    ptx::cta_sync();
+    ptx::tc_fence_after_sync();
+    const uint32_t tmem = *tmem_slot;
+
+    const uint32_t ready_lead0 = PAIR ? ptx::mapa_shared(ready0, 0) : ready0;
+    const uint32_t tempty_lead0 = PAIR ? ptx::mapa_shared(tempty0, 0) : tempty0;
+    const int32_t row_off = int32_t(rank) * Cfg::ROWS;
+
+    if (warp < 4) {
+        ptx::regs_dec<kS8RegsIssue>();
+        if (warp == 0 && lane == 0) {
+            // ---------------- TMA producer
+            uint32_t stage = 0, phase = 0;
+            uint32_t issued = 0;
+            bool ok = true;
+            for (PieceWalk w(sched, worker); ok && w.advance(sched);) {
+                const S8Tile t = tile_at(w.tile, p, gtab, Cfg::TILE_M, Cfg::TILE_N);
+                const int32_t col = t.n0 + int32_t(rank) * 64;
+                for (int32_t kb = w.kb0; kb < w.kb1; ++kb) {
+                    if (!s8_wait<false>(empty0 + 8u * stage, phase ^ 1u, flag, p, kStatusProducer)) {
+                        ok = false;
+                        break;
+                    }
+                    const uint32_t sa = codes0 + stage * Cfg::CODE_STAGE;
+                    const uint32_t fb = full0 + 8u * stage;
+                    ptx::mbar_arrive_expect_tx(fb, Cfg::CODE_STAGE);
+                    ptx::tma_load_3d(sa, &map_a, fb, kb * Cfg::BK, t.m0 + row_off, t.z);
+                    ptx::tma_load_3d(sa + Cfg::A_CODES, &map_b, fb, col, kb * Cfg::BK, t.z);
+                    ptx::tma_load_3d(sa + Cfg::A_CODES + Cfg::B_BOX, &map_b, fb, col + Cfg::HC, kb * Cfg::BK, t.z);
+                    ++issued;
+                    if (++stage == S1) {
+                        stage = 0;
+                        phase ^= 1u;
+                    }
+                }
+            }
+            // No TMA write into shared memory outlives the CTA.
+            // (The last S1 loads: the slots from `stage` on, oldest first.)
+            for (int i = 0; i < S1; ++i) {
+                if (issued + i >= uint32_t(S1))
+                    s8_wait<false>(full0 + 8u * stage, phase ^ 1u, flag, p, kStatusDrain, false);
+                if (++stage == S1) {
+                    stage = 0;
+                    phase ^= 1u;
+                }
+            }
+        } else if (warp == 1 && lane == 0 && rank == 0) {
+            // ---------------- MMA issuer
+            constexpr uint32_t idesc = mma_idesc<Cfg::HC, PAIR>();
+            constexpr uint16_t both = PAIR ? 3 : 1;
+            uint32_t stage = 0, phase = 0, aphase = 0;
+            bool ok = true;
+            for (PieceWalk w(sched, worker); ok && w.advance(sched);) {
+                int c = 0;  // blocks in the accumulator
+                for (int32_t kb = w.kb0; ok && kb < w.kb1; ++kb) {
+                    if (!s8_wait<PAIR>(ready0 + 8u * stage, phase, flag, p, kStatusMma)) {
+                        ok = false;
+                        break;
+                    }
+                    ptx::tc_fence_after_sync();
+                    const bool last = c == kChunkBlocks - 1 || kb == w.kb1 - 1;
+                    const uint32_t a = tmem + Cfg::A_COL + stage * uint32_t(Cfg::BK / 2);
+#pragma unroll 1
+                    for (int h = 0; h < 2; ++h) {
+                        if (c == 0) {
+                            if (!s8_wait<PAIR>(tempty0 + 8u * h, aphase ^ 1u, flag, p, kStatusMma)) {
+                                ok = false;
+                                break;
+                            }
+                            ptx::tc_fence_after_sync();
+                        }
+                        const uint32_t d = tmem + Cfg::ACC_COL + uint32_t(h * Cfg::HC);
+                        const uint32_t sb = f16_0 + stage * Cfg::F_STAGE + uint32_t(h * Cfg::F_BOX);
+#pragma unroll
+                        for (int kk = 0; kk < Cfg::BK / 16; ++kk)
+                            ptx::mma_f16_ts<PAIR>(d, a + 8u * kk, desc_b(sb + 2048u * kk), idesc,
+                                                  (c > 0 || kk > 0) ? 1u : 0u);
+                        if (last)
+                            ptx::mma_commit<PAIR>(tfull0 + 8u * h, both);
+                    }
+                    if (!ok)
+                        break;
+                    ptx::mma_commit<PAIR>(free0 + 8u * stage, both);
+                    if (++stage == S2) {
+                        stage = 0;
+                        phase ^= 1u;
+                    }
+                    c = last ? 0 : c + 1;
+                    if (last)
+                        aphase ^= 1u;
+                }
+            }
+            // Every MMA must finish before TMEM is freed.
+            ptx::mma_commit<PAIR>(done_bar, 1);
+            s8_wait<false>(done_bar, 0, flag, p, kStatusDrain, false);
+        }
+        __syncwarp();
+    } else if (warp < 12) {
+        // ---------------- converters
+        ptx::regs_dec<kS8RegsConvert>();
+        const bool is_a = warp < 8;
+        const int q = warp & 3;
+        uint32_t s1 = 0, p1 = 0, s2 = 0, p2 = 0;
+        bool ok = true;
+        for (PieceWalk w(sched, worker); ok && w.advance(sched);) {
+            for (int32_t kb = w.kb0; kb < w.kb1; ++kb) {
+                ok = s8_wait<false>(full0 + 8u * s1, p1, flag, p, kStatusProducer) &&
+                     s8_wait<false>(free0 + 8u * s2, p2 ^ 1u, flag, p, kStatusProducer);
+                ok = __all_sync(0xffffffffu, ok);
+                if (!ok)
+                    break;
+                const uint32_t codes = codes0 + s1 * Cfg::CODE_STAGE;
+                if (is_a) {
+                    // Row 32q + lane: eight 16-byte chunks, swizzled by the row.
+                    ptx::tc_fence_after_sync();
+                    const uint32_t row = codes + uint32_t(32 * q + lane) * 128u;
+                    const uint32_t to = tmem + (uint32_t(32 * q) << 16) + Cfg::A_COL + s2 * uint32_t(Cfg::BK / 2);
+#pragma unroll
+                    for (int g = 0; g < 4; ++g) {
+                        const uint4 u = ptx::ld_shared_v4(row + (uint32_t((2 * g) ^ (lane & 7)) << 4));
+                        const uint4 v = ptx::ld_shared_v4(row + (uint32_t((2 * g + 1) ^ (lane & 7)) << 4));
+                        uint32_t r[16];
+                        codes_to_f16(u.x, r[0], r[1]);
+                        codes_to_f16(u.y, r[2], r[3]);
+                        codes_to_f16(u.z, r[4], r[5]);
+                        codes_to_f16(u.w, r[6], r[7]);
+                        codes_to_f16(v.x, r[8], r[9]);
+                        codes_to_f16(v.y, r[10], r[11]);
+                        codes_to_f16(v.z, r[12], r[13]);
+                        codes_to_f16(v.w, r[14], r[15]);
+                        ptx::tmem_st_32x32b_x16(to + 16u * g, r);
+                    }
+                    __syncwarp();
+                    if (lane == 0)
+                        ptx::mbar_arrive(empty0 + 8u * s1);
+                    ptx::tmem_wait_st();
+                    ptx::tc_fence_before_sync();
+                } else {
+                    // Box h: 128 rows of 64 codes; a lane takes 16 codes of
+                    // one row and writes two 16-byte chunks of f16 (eight
+                    // lanes cover all eight chunk positions of the banks).
+                    const int i = 32 * q + lane;
+#pragma unroll
+                    for (int j = 0; j < 8; ++j) {
+                        const int h = j >> 2;
+                        const int at = i + 128 * (j & 3);  // 16-byte chunk of the box
+                        const int k = at >> 2, c = at & 3;
+                        const uint4 u = ptx::ld_shared_v4(codes + uint32_t(Cfg::A_CODES + h * Cfg::B_BOX) + uint32_t(at) * 16u);
+                        uint32_t r[8];
+                        codes_to_f16(u.x, r[0], r[1]);
+                        codes_to_f16(u.y, r[2], r[3]);
+                        codes_to_f16(u.z, r[4], r[5]);
+                        codes_to_f16(u.w, r[6], r[7]);
+                        const uint32_t to = f16_0 + s2 * Cfg::F_STAGE + uint32_t(h * Cfg::F_BOX) + uint32_t(k) * 128u;
+                        ptx::st_shared_v4(to + (uint32_t((2 * c) ^ (k & 7)) << 4), r[0], r[1], r[2], r[3]);
+                        ptx::st_shared_v4(to + (uint32_t((2 * c + 1) ^ (k & 7)) << 4), r[4], r[5], r[6], r[7]);
+                    }
+                    ptx::fence_proxy_async_smem();
+                    __syncwarp();
+                    if (lane == 0)
+                        ptx::mbar_arrive(empty0 + 8u * s1);
+                }
+                __syncwarp();
+                if (lane == 0) {
+                    if constexpr (PAIR)
+                        ptx::mbar_arrive_cluster(ready_lead0 + 8u * s2);
+                    else
+                        ptx::mbar_arrive(ready0 + 8u * s2);
+                }
+                if (++s1 == S1) {
+                    s1 = 0;
+                    p1 ^= 1u;
+                }
+                if (++s2 == S2) {
+                    s2 = 0;
+                    p2 ^= 1u;
+                }
+            }
+        }
+    } else {
+        // ---------------- accumulator -> integers -> C
+        ptx::regs_inc<kS8RegsDrain>();
+        const int e = warp - 12;
+        const int h = e >> 2;
+        const int q = warp & 3;
+        const int tid = 32 * q + lane;  // row of the CTA's 128
+        const uint32_t acc = tmem + (uint32_t(32 * q) << 16) + Cfg::ACC_COL + uint32_t(h * Cfg::HC);
+        const uint32_t buf = staging + uint32_t(e) * 4096u;
+        constexpr int KEEP = Cfg::HC < 96 ? Cfg::HC : 96;
+        static_assert(Cfg::HC - KEEP <= 32, "one staging box");
+        const uint32_t mine_at = buf + 4u * uint32_t(lane);
+        uint32_t aphase = 0;
+        bool ok = true;
+        for (PieceWalk w(sched, worker); ok && w.advance(sched);) {
+            // The row's sums: the first KEEP columns in registers, the others
+            // (one box, in a pair) in the lane's column of the idle staging
+            // box, which keeps the warp within its registers.
+            int32_t sum[KEEP];
+#pragma unroll
+            for (int j = 0; j < KEEP; ++j)
+                sum[j] = 0;
+#pragma unroll
+            for (int j = KEEP; j < Cfg::HC; ++j)
+                ptx::st_shared_u32(mine_at + 128u * (j - KEEP), 0u);
+            for (int32_t kb = w.kb0; kb < w.kb1; kb += kChunkBlocks) {
+                ok = s8_wait<PAIR>(tfull0 + 8u * h, aphase, flag, p, kStatusEpilogue);
+                ok = __all_sync(0xffffffffu, ok);
+                if (!ok)
+                    break;
+                ptx::tc_fence_after_sync();
+                // Eight columns on their way while eight are added.
+                uint32_t r[2][8];
+                ptx::tmem_ld_32x32b_x8(acc, r[0]);
+#pragma unroll
+                for (int c = 0; c < Cfg::HC / 8; ++c) {
+                    ptx::tmem_wait_ld(r[c & 1]);
+                    if (c + 1 < Cfg::HC / 8)
+                        ptx::tmem_ld_32x32b_x8(acc + 8u * (c + 1), r[(c + 1) & 1]);
+#pragma unroll
+                    for (int j = 0; j < 8; ++j) {
+                        const int32_t v = __float2int_rn(__uint_as_float(r[c & 1][j]));
+                        if (8 * c < KEEP) {
+                            sum[(8 * c + j) % KEEP] += v;
+                        } else {
+                            const uint32_t to = mine_at + 128u * (8 * c + j - KEEP);
+                            ptx::st_shared_u32(to, ptx::ld_shared_u32(to) + uint32_t(v));
+                        }
+                    }
+                }
+                ptx::tc_fence_before_sync();
+                __syncwarp();
+                if (lane == 0) {
+                    if constexpr (PAIR)
+                        ptx::mbar_arrive_cluster(tempty_lead0 + 8u * h);
+                    else
+                        ptx::mbar_arrive(tempty0 + 8u * h);
+                }
+                aphase ^= 1u;
+            }
+            // The four warps go on or give up together (they meet below).
+            ok = ptx::named_bar_and(1 + h, 128, ok);
+            if (!ok)
+                break;
+            const S8Tile t = tile_at(w.tile, p, gtab, Cfg::TILE_M, Cfg::TILE_N);
+            if (w.kb1 - w.kb0 < sched.kb()) {
+                // A piece: its sums go to this worker's slot, and whoever
+                // arrives last adds up the others'.  [4-column group][row].
+                const int part = int(rank) * 2 + h;
+                const int64_t part_at = int64_t(part) * Cfg::ROWS * Cfg::HC;
+                int4 *mine = reinterpret_cast<int4 *>(p.partial + (2 * worker + (w.kb0 == 0 ? 1 : 0)) * Cfg::SLOT_INTS + part_at);
+#pragma unroll
+                for (int j = 0; j < Cfg::HC / 4; ++j) {
+                    int4 x;
+                    if (4 * j < KEEP) {
+                        x = make_int4(sum[4 * j % KEEP], sum[(4 * j + 1) % KEEP], sum[(4 * j + 2) % KEEP],
+                                      sum[(4 * j + 3) % KEEP]);
+                    } else {
+                        const uint32_t at = mine_at + 128u * (4 * j - KEEP);
+                        x = make_int4(int32_t(ptx::ld_shared_u32(at)), int32_t(ptx::ld_shared_u32(at + 128u)),
+                                      int32_t(ptx::ld_shared_u32(at + 256u)), int32_t(ptx::ld_shared_u32(at + 384u)));
+                    }
+                    __stcg(mine + j * Cfg::ROWS + tid, x);
+                }
+                __threadfence();
+                ptx::named_bar_sync(1 + h, 128);
+                const S8Schedule cut = sched.all();
+                const int32_t first = cut.owner(w.tile * cut.kb);
+                const int32_t last = cut.owner((w.tile + 1) * cut.kb - 1);
+                if (q == 0)
+                    ptx::st_shared_u32(last_flag + 4u * h, arrive_last(p.arrivals + w.tile * Cfg::PARTS + part, p.tag,
+                                                                      uint32_t(last - first + 1), lane));
+                ptx::named_bar_sync(1 + h, 128);
+                const bool mine_to_sum = __any_sync(0xffffffffu, ptx::ld_shared_u32(last_flag + 4u * h) != 0);
+                __threadfence();
+                if (!mine_to_sum)
+                    continue;
+                for (int32_t v = first; v <= last; ++v) {
+                    if (v == worker)
+                        continue;
+                    const int32_t slot = 2 * v + (cut.piece_begin(v) > w.tile * cut.kb ? 0 : 1);
+                    const int4 *theirs = reinterpret_cast<const int4 *>(p.partial + slot * Cfg::SLOT_INTS + part_at);
+#pragma unroll
+                    for (int j = 0; j < Cfg::HC / 4; ++j) {
+                        const int4 x = ptx::ld_cg_v4(theirs + j * Cfg::ROWS + tid);
+                        if (4 * j < KEEP) {
+                            sum[4 * j % KEEP] += x.x;
+                            sum[(4 * j + 1) % KEEP] += x.y;
+                            sum[(4 * j + 2) % KEEP] += x.z;
+                            sum[(4 * j + 3) % KEEP] += x.w;
+                        } else {
+                            const uint32_t at = mine_at + 128u * (4 * j - KEEP);
+                            ptx::st_shared_u32(at, ptx::ld_shared_u32(at) + uint32_t(x.x));
+                            ptx::st_shared_u32(at + 128u, ptx::ld_shared_u32(at + 128u) + uint32_t(x.y));
+                            ptx::st_shared_u32(at + 256u, ptx::ld_shared_u32(at + 256u) + uint32_t(x.z));
+                            ptx::st_shared_u32(at + 384u, ptx::ld_shared_u32(at + 384u) + uint32_t(x.w));
+                        }
+                    }
+                }
+            }
+            // Through the warp's staging box: lane = row in, lane = column group out.
+            const int32_t my_row = t.m0 + row_off + tid;
+            const float sa = p.scale_a && my_row < t.rows ? __ldg(p.scale_a + t.z * p.sa_stride + my_row) : 1.f;
+            const int32_t row0 = t.m0 + row_off + 32 * q + (lane >> 3);
+#pragma unroll
+            for (int i = 0; i < Cfg::HC / 32; ++i) {
+                // The box whose sums wait in the staging space goes first.
+                const int b = (i + Cfg::HC / 32 - (KEEP < Cfg::HC ? 1 : 0)) % (Cfg::HC / 32);
+                uint32_t v[32];
+#pragma unroll
+                for (int j = 0; j < 32; ++j)
+                    v[j] = 32 * b < KEEP ? uint32_t(sum[(32 * b + j) % KEEP]) : ptx::ld_shared_u32(mine_at + 128u * j);
+                __syncwarp();  // every lane has its sums before the box is overwritten
+#pragma unroll
+                for (int j = 0; j < 8; ++j)
+                    ptx::st_shared_v4(buf + uint32_t(lane) * 128u + (uint32_t(j ^ (lane & 7)) << 4),
+                                      __float_as_uint(float(int32_t(v[4 * j])) * sa),
+                                      __float_as_uint(float(int32_t(v[4 * j + 1])) * sa),
+                                      __float_as_uint(float(int32_t(v[4 * j + 2])) * sa),
+                                      __float_as_uint(float(int32_t(v[4 * j + 3])) * sa));
+                __syncwarp();
+                const int32_t col = t.n0 + h * Cfg::HC + 32 * b + 4 * (lane & 7);
+                if (col < p.N) {
+                    float sb[4], bias[4];
+                    column_terms(p, t.z, col, sb, bias);
+#pragma unroll 1
+                    for (int k = 0; k < 8; ++k) {
+                        const int32_t row = row0 + 4 * k;
+                        if (row >= t.rows)
+                            break;
+                        const int r = 4 * k + (lane >> 3);
+                        const uint4 u = ptx::ld_shared_v4(buf + uint32_t(r) * 128u + (uint32_t((lane & 7) ^ (r & 7)) << 4));
+                        put4(p, t.z * p.sC + row * p.ldc + col, col,
+                             make_float4(__uint_as_float(u.x), __uint_as_float(u.y), __uint_as_float(u.z),
+                                         __uint_as_float(u.w)),
+                             sb, bias);
+                    }
+                }
+                __syncwarp();
+            }
+        }
+    }
+
+    ptx::tc_fence_before_sync();
+    ptx::cta_sync();
+    if constexpr (PAIR)
+        ptx::cluster_sync();
+    if (warp == 1) {
+        __syncwarp();
+        ptx::tc_fence_after_sync();
+        ptx::tmem_dealloc<PAIR>(ptx::ld_shared_u32(ctrl + 176u), 512);
+    }
+}
+
+// ------------------------------------------------------------- repacking
+
+// One thread per 16 bytes of the packed rows (zeros past a row's end).
+__global__ void __launch_bounds__(256)
+    tsm_pack_s8_kernel(const int8_t *src, int64_t s_ld, int64_t s_stride, int8_t *dst, int64_t d_ld, int64_t d_stride,
+                       int64_t rows, int64_t cols, int64_t batch)
+{
+    const int64_t chunks = d_ld / 16;
+    const int64_t total = batch * rows * chunks;
+    for (int64_t i = int64_t(blockIdx.x) * blockDim.x + threadIdx.x; i < total; i += int64_t(gridDim.x) * blockDim.x) {
+        const int64_t row = i / chunks;
+        const int64_t c = (i - row * chunks) * 16;
+        const int64_t z = row / rows, r = row - z * rows;
+        const uint8_t *s = reinterpret_cast<const uint8_t *>(src) + z * s_stride + r * s_ld + c;
+        uint32_t w[4] = {0, 0, 0, 0};
+        if (c + 20 <= cols) {
+            // Five aligned words cover the 16 bytes: the first starts at most
+            // three bytes early, so it is taken byte by byte.
+            const int off = int(reinterpret_cast<uintptr_t>(s) & 3u);
+            if (off == 0) {
+#pragma unroll
+                for (int k = 0; k < 4; ++k)
+                    w[k] = __ldg(reinterpret_cast<const uint32_t *>(s) + k);
+            } else {
+                const uint32_t *a = reinterpret_cast<const uint32_t *>(s - off) + 1;
+                uint32_t prev = 0;
+                for (int b = off; b < 4; ++b)
+                    prev |= uint32_t(__ldg(s - off + b)) << (8 * b);
+#pragma unroll
+                for (int k = 0; k < 4; ++k) {
+                    const uint32_t next = __ldg(a + k);
+                    w[k] = __funnelshift_r(prev, next, 8 * off);
+                    prev = next;
+                }
+            }
+        } else {
+            for (int k = 0; k < 16 && c + k < cols; ++k)
+                w[k >> 2] |= uint32_t(__ldg(s + k)) << (8 * (k & 3));
+        }
+        *reinterpret_cast<uint4 *>(dst + z * d_stride + r * d_ld + c) = make_uint4(w[0], w[1], w[2], w[3]);
+    }
+}
+
+template <bool PAIR>
+cudaError_t set_tiled()
+{
+    return cudaFuncSetAttribute(tsm_s8_tiled_kernel<PAIR>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                S8Cfg<PAIR>::SMEM_BYTES);
+}
+
+template <bool PAIR>
+cudaError_t launch_tiled(const CUtensorMap &map_a, const CUtensorMap &map_b, const S8Params &p, int grid,
+                         cudaStream_t stream)
+{
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(unsigned(grid), 1, 1);
+    cfg.blockDim = dim3(kS8Threads, 1, 1);
+    cfg.dynamicSmemBytes = S8Cfg<PAIR>::SMEM_BYTES;
+    cfg.stream = stream;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = 2;
+    attr[0].val.clusterDim.y = 1;
+    attr[0].val.clusterDim.z = 1;
+    cfg.attrs = PAIR ? attr : nullptr;
+    cfg.numAttrs = PAIR ? 1 : 0;
+    return cudaLaunchKernelEx(&cfg, tsm_s8_tiled_kernel<PAIR>, map_a, map_b, p);
+}
+
+template <bool PAIR>
+S8Shape shape_of()
+{
+    using Cfg = S8Cfg<PAIR>;
+    return S8Shape{Cfg::TILE_M, Cfg::TILE_N, Cfg::BK, Cfg::SLOT_INTS * 4, Cfg::PARTS};
+}
+
 }  // namespace
 
-cudaError_t launch_s8_simple(const S8Params &p, cudaStream_t stream)
+S8Shape s8_shape(bool pair) { return pair ? shape_of<true>() : shape_of<false>(); }
+
+cudaError_t set_s8_attributes()
 {
-    const dim3 grid(unsigned((p.N + kSimpleTile - 1) / kSimpleTile),
-                    unsigned((p.M + kSimpleTile - 1) / kSimpleTile), unsigned(p.batch));
-    tsm_s8_simple_kernel<<<grid, 256, 0, stream>>>(p);
+    const cudaError_t e = set_tiled<true>();
+    return e == cudaSuccess ? set_tiled<false>() : e;
+}
+
+cudaError_t launch_s8_tiled(const CUtensorMap &map_a, const CUtensorMap &map_b, const S8Params &p, bool pair,
+                            int grid, cudaStream_t stream)
+{
+    return pair ? launch_tiled<true>(map_a, map_b, p, grid, stream) : launch_tiled<false>(map_a, map_b, p, grid, stream);
+}
+
+cudaError_t launch_pack_s8(const int8_t *src, int64_t s_ld, int64_t s_stride, int8_t *dst, int64_t d_ld,
+                           int64_t d_stride, int64_t rows, int64_t cols, int64_t batch, int sms,
+                           cudaStream_t stream)
+{
+    const int64_t blocks = (batch * rows * (d_ld / 16) + 255) / 256;
+    tsm_pack_s8_kernel<<<unsigned(min(blocks, int64_t(sms) * 32)), 256, 0, stream>>>(src, s_ld, s_stride, dst, d_ld,
+                                                                                     d_stride, rows, cols, batch);
     return cudaGetLastError();
 }
 
