@@ -474,8 +474,8 @@ gemm_status_t launch_s8(S8Params p, DeviceState *ds, cudaStream_t stream)
         st = encode_3d(&map_a, CU_TENSOR_MAP_DATA_TYPE_UINT8, 1, p.A, p.K, p.M, p.batch, lda, sA, 128, 128,
                        CU_TENSOR_MAP_L2_PROMOTION_L2_256B, "A");
     if (st == GEMM_OK)
-        st = encode_3d(&map_b, CU_TENSOR_MAP_DATA_TYPE_UINT8, 1, p.B, p.N, p.K, p.batch, ldb, sB, 64, 128,
-                       CU_TENSOR_MAP_L2_PROMOTION_L2_256B, "B", 1, CU_TENSOR_MAP_SWIZZLE_NONE);
+        st = encode_3d(&map_b, CU_TENSOR_MAP_DATA_TYPE_UINT8, 1, p.B, p.N, p.K, p.batch, ldb, sB, 128, 128,
+                       CU_TENSOR_MAP_L2_PROMOTION_L2_256B, "B");
     if (st == GEMM_OK) {
         const int64_t most = p.group_rows ? p.workers
                                           : std::max<int64_t>(sched.shared ? sched.cutters : 0,

@@ -46,29 +46,29 @@ __device__ __forceinline__ void codes_to_f16(uint32_t w, uint32_t &lo, uint32_t 
 //   warp 1       MMA issuer (the pair's leader): A from TMEM, B from shared memory
 //   warps 4-7    A's codes -> f16 -> TMEM, one row per lane (they never pass
 //                through shared memory as f16)
-//   warps 8-11   B's codes -> f16 -> the 128-byte swizzled layout of the MMA
-//   warps 12-19  two per TMEM lane quarter, one per column half of the tile:
-//                accumulator -> 32-bit sums in registers, then the epilogue
+//   warps 8-15   B's codes -> f16 -> the 128-byte swizzled layout of the MMA
+//   warps 16-23  two per TMEM lane quarter, one per column half of the tile:
+//                accumulator -> 32-bit sums, then the epilogue
 // The bound is shared-memory bandwidth: a 256 x 256 x 128 block costs an SM
 // 32 KB of codes in, 32 KB out to the converters, 32 KB of f16 B written and
 // 32 KB read by the MMAs = 1024 cycles at 128 bytes, just the time its MMAs
-// take; with A's f16 in shared memory too it would be 1.5 times that.
-//
-// The tile's two column halves have an accumulator each, and every k-block
-// does all of half 0 and then all of half 1.  So when a chunk of 1024 k ends,
-// half 0 is read out while half 1 still computes its last block, and half 1
-// while half 0 starts the next chunk.
+// take; with A's f16 in shared memory too it would be 1.5 times that.  A's f16
+// ring takes the TMEM columns a second accumulator would need, so the MMAs
+// pause while a chunk of 1024 k is read out.  (Two accumulators of half the
+// width would not: but the MMA runs at full rate only at its full width, 256
+// columns for a pair.)
 template <bool PAIR>
 struct S8Cfg {
     static constexpr int ROWS = 128;
     static constexpr int CTAS = PAIR ? 2 : 1;
     static constexpr int TILE_M = ROWS * CTAS;
-    static constexpr int HC = 64 * CTAS;        // columns of one half: the MMA's width
-    static constexpr int TILE_N = 2 * HC;
+    static constexpr int B_COLS = 128;          // columns of B staged by one CTA
+    static constexpr int TILE_N = B_COLS * CTAS;  // the MMA's width
+    static constexpr int HC = TILE_N / 2;       // columns of one epilogue half
     static constexpr int BK = 128;
     static constexpr int A_CODES = ROWS * BK;   // bytes
-    static constexpr int B_BOX = 64 * BK;       // 64 columns of codes
-    static constexpr int CODE_STAGE = A_CODES + 2 * B_BOX;
+    static constexpr int B_CODES = B_COLS * BK;
+    static constexpr int CODE_STAGE = A_CODES + B_CODES;
     static constexpr int F_BOX = 64 * BK * 2;   // 64 columns of f16
     static constexpr int F_STAGE = 2 * F_BOX;
     static constexpr int S1 = 3, S2 = 3;        // ring depths
@@ -76,24 +76,38 @@ struct S8Cfg {
     static constexpr int CTRL = 2048, GROUP_TABLE_OFF = 1024;
     static constexpr int SMEM_BYTES = 1024 + S1 * CODE_STAGE + S2 * F_STAGE + STAGING + CTRL;
     static_assert(SMEM_BYTES <= 232448, "227 KiB per block");
-    static constexpr uint32_t ACC_COL = 0;      // two accumulators of HC columns
-    static constexpr uint32_t A_COL = 256;      // the f16 A ring: BK / 2 columns per stage
-    static_assert(A_COL + S2 * (BK / 2) <= 512 && 2 * HC <= 256, "TMEM columns");
+    static constexpr uint32_t A_COL = 256;      // TMEM: the accumulator, then the f16 A ring
+    static_assert(A_COL + S2 * (BK / 2) <= 512 && TILE_N <= 256, "TMEM columns");
     static constexpr int PARTS = 2 * CTAS;      // (CTA, half) parts of a tile
     static constexpr int64_t SLOT_INTS = int64_t(PARTS) * ROWS * HC;
 };
 
-constexpr int kS8Threads = 640;
-// Registers per thread by warpgroup (five of 128 threads): together exactly
-// what the block was launched with (640 x 96).
-constexpr int kS8RegsIssue = 48, kS8RegsConvert = 56, kS8RegsDrain = 160;
-static_assert(128 * kS8RegsIssue + 256 * kS8RegsConvert + 256 * kS8RegsDrain <= kS8Threads * 96,
+constexpr int kWarpA = 4, kWarpB = 8, kWarpDrain = 16, kS8Warps = 24;  // first warps of the roles
+constexpr int kS8Threads = 32 * kS8Warps;
+// Registers per thread by warpgroup (six of 128 threads): together no more
+// than what the block was launched with (768 x 80).
+constexpr int kS8RegsIssue = 64, kS8RegsConvert = 48, kS8RegsDrain = 136;
+static_assert(128 * kS8RegsIssue + 3 * 128 * kS8RegsConvert + 2 * 128 * kS8RegsDrain <= kS8Threads * 80,
               "register split");
 
+// B's shared-memory descriptor: MN-major, 64-column boxes of BK rows of 128 bytes.
+template <bool PAIR>
+__device__ __forceinline__ uint64_t desc_b_s8(uint32_t saddr)
+{
+    return desc_common() | (uint64_t(S8Cfg<PAIR>::F_BOX >> 4) << 16) | uint64_t((saddr & 0x3FFFFu) >> 4);
+}
+
 // The schedule in shared memory, read field by field: the registers are for
-// the sums.
+// the sums.  WARP: a whole warp reads it together, and the compiler is told
+// that the values are the warp's (they then need no register per lane).
+template <bool WARP>
 struct SharedSchedule {
     uint32_t at;
+    __device__ __forceinline__ int32_t field(int i) const
+    {
+        const int32_t v = int32_t(ptx::ld_shared_u32(at + 4u * i));
+        return WARP ? __shfl_sync(0xffffffffu, v, 0) : v;
+    }
     __device__ __forceinline__ void put(const S8Schedule &s) const
     {
         ptx::st_shared_u32(at, uint32_t(s.tiles));
@@ -102,26 +116,27 @@ struct SharedSchedule {
         ptx::st_shared_u32(at + 12, uint32_t(s.workers));
         ptx::st_shared_u32(at + 16, uint32_t(s.cutters));
     }
-    __device__ __forceinline__ int32_t tiles() const { return int32_t(ptx::ld_shared_u32(at)); }
-    __device__ __forceinline__ int32_t kb() const { return int32_t(ptx::ld_shared_u32(at + 8)); }
-    __device__ __forceinline__ int32_t workers() const { return int32_t(ptx::ld_shared_u32(at + 12)); }
+    __device__ __forceinline__ int32_t tiles() const { return field(0); }
+    __device__ __forceinline__ int32_t kb() const { return field(2); }
+    __device__ __forceinline__ int32_t workers() const { return field(3); }
     __device__ __forceinline__ S8Schedule all() const
     {
         S8Schedule s;
         s.tiles = tiles();
-        s.shared = int32_t(ptx::ld_shared_u32(at + 4));
+        s.shared = field(1);
         s.kb = kb();
         s.workers = workers();
-        s.cutters = int32_t(ptx::ld_shared_u32(at + 16));
+        s.cutters = field(4);
         return s;
     }
 };
 
 // One worker's pieces in order: its share of the cut tiles, then whole tiles.
+template <bool WARP>
 struct PieceWalk {
     int32_t cur, end, next;  // blocks of the cut tiles; next whole tile
     int32_t tile, kb0, kb1;
-    __device__ __forceinline__ PieceWalk(const SharedSchedule &shared, int32_t w)
+    __device__ __forceinline__ PieceWalk(const SharedSchedule<WARP> &shared, int32_t w)
     {
         const S8Schedule s = shared.all();
         const bool cuts = s.shared > 0 && w < s.cutters;
@@ -130,7 +145,7 @@ struct PieceWalk {
         next = s.shared + w;
         tile = kb0 = kb1 = 0;
     }
-    __device__ __forceinline__ bool advance(const SharedSchedule &s)
+    __device__ __forceinline__ bool advance(const SharedSchedule<WARP> &s)
     {
         kb0 = 0;
         kb1 = s.kb();
@@ -210,13 +225,13 @@ __device__ __forceinline__ bool arrive_last(unsigned long long *word, unsigned l
 // Bounded mbarrier wait, as wait_bounded, with nothing kept in registers
 // between waits: the CTA's abort flag is the word at `flag` in shared memory
 // (in a pair, at the same place in the peer), the limit and the status word
-// are the launch's.
-template <bool PAIR>
+// are the launch's.  ACQ_CLUSTER: the phase counts another CTA's arrivals.
+template <bool PAIR, bool ACQ_CLUSTER = false>
 __device__ __forceinline__ bool s8_wait(uint32_t bar, uint32_t parity, uint32_t flag, const S8Params &p, uint32_t who,
                                         bool honor_abort = true)
 {
     auto try_wait = [&]() {
-        return PAIR ? ptx::mbar_try_wait_cluster(bar, parity) : ptx::mbar_try_wait(bar, parity);
+        return ACQ_CLUSTER ? ptx::mbar_try_wait_cluster(bar, parity) : ptx::mbar_try_wait(bar, parity);
     };
     if (try_wait())
         return true;
@@ -238,43 +253,66 @@ __device__ __forceinline__ bool s8_wait(uint32_t bar, uint32_t parity, uint32_t 
     }
 }
 
-// Four values of a row through the epilogue into C.
-__device__ __forceinline__ void put4(const S8Params &p, int64_t at, int32_t col, float4 v, const float (&sb)[4],
-                                     const float (&bias)[4])
+// Arrive on a barrier of the pair's leader.  Released to the CTA only: what the
+// arrival stands for is complete in this SM before it is sent -- f16 in its own
+// shared memory (the proxy fence) or TMEM (the store wait), or TMEM read out
+// (the load wait) -- and is next touched by this SM's own tensor core.
+// Released to the cluster, every arrival would first wait for the warp's other
+// stores, global ones included: measured 1.34 times the whole kernel's time at
+// 8192^3 (1028 against 770 us).
+template <bool PAIR>
+__device__ __forceinline__ void arrive_leader(uint32_t bar)
 {
-    float o[4] = {v.x, v.y, v.z, v.w};
-    with_activation<kActRuntime>(p.epi.act, [&](auto act) {
-#pragma unroll
-        for (int k = 0; k < 4; ++k)
-            o[k] = epi_act(fmaf(sb[k], o[k], bias[k]), decltype(act)::value, p.epi.slope);
-    });
-    if (p.vec_c && col + 3 < p.N) {
-        if (p.epi.out_type == kOutF32)
-            *reinterpret_cast<float4 *>(static_cast<float *>(p.C) + at) = make_float4(o[0], o[1], o[2], o[3]);
-        else
-            *reinterpret_cast<uint2 *>(static_cast<uint16_t *>(p.C) + at) =
-                make_uint2(epi_out16(o[0], p.epi.out_type) | (epi_out16(o[1], p.epi.out_type) << 16),
-                           epi_out16(o[2], p.epi.out_type) | (epi_out16(o[3], p.epi.out_type) << 16));
-        return;
-    }
-#pragma unroll
-    for (int k = 0; k < 4; ++k)
-        if (col + k < p.N)
-            epi_store(p.C, at + k, o[k], p.epi.out_type);
+    if constexpr (PAIR)
+        ptx::mbar_arrive_remote(bar);
+    else
+        ptx::mbar_arrive(bar);
 }
 
-// Column scales (times alpha) and biases of four columns.
-__device__ __forceinline__ void column_terms(const S8Params &p, int32_t z, int32_t col, float (&sb)[4],
-                                             float (&bias)[4])
+// A staged box (32 rows of 32 f32 values, 16-byte chunks swizzled by the row)
+// through the epilogue into C: eight lanes take a row's chunks, four rows at a
+// time, four loads and stores in flight.
+__device__ __forceinline__ void store_box(const S8Params &p, const S8Tile &t, uint32_t buf, int32_t row0, int32_t col0,
+                                          int lane)
 {
+    const int32_t col = col0 + 4 * (lane & 7);
+    if (col >= p.N)
+        return;
+    float sb[4], bias[4];
+    const bool four = p.vec_c && col + 3 < p.N;
 #pragma unroll
     for (int k = 0; k < 4; ++k) {
         const bool in = col + k < p.N;
         sb[k] = p.epi.alpha;
         if (p.scale_b && in)
-            sb[k] *= __ldg(p.scale_b + z * p.sb_stride + col + k);
-        bias[k] = p.epi.bias && in ? __ldg(p.epi.bias + z * p.epi.bias_stride + col + k) : 0.f;
+            sb[k] *= __ldg(p.scale_b + t.z * p.sb_stride + col + k);
+        bias[k] = p.epi.bias && in ? __ldg(p.epi.bias + t.z * p.epi.bias_stride + col + k) : 0.f;
     }
+    const int32_t first = lane >> 3;
+    const int32_t rows = min(32, t.rows - row0);
+    with_activation<kActRuntime>(p.epi.act, [&](auto act) {
+#pragma unroll 4
+        for (int r = first; r < rows; r += 4) {
+            const int64_t at = t.z * p.sC + int64_t(row0 + r) * p.ldc + col;
+            const uint4 u = ptx::ld_shared_v4(buf + uint32_t(r) * 128u + (uint32_t((lane & 7) ^ (r & 7)) << 4));
+            float o[4] = {__uint_as_float(u.x), __uint_as_float(u.y), __uint_as_float(u.z), __uint_as_float(u.w)};
+#pragma unroll
+            for (int k = 0; k < 4; ++k)
+                o[k] = epi_act(fmaf(sb[k], o[k], bias[k]), decltype(act)::value, p.epi.slope);
+            if (four && p.epi.out_type == kOutF32) {
+                *reinterpret_cast<float4 *>(static_cast<float *>(p.C) + at) = make_float4(o[0], o[1], o[2], o[3]);
+            } else if (four) {
+                *reinterpret_cast<uint2 *>(static_cast<uint16_t *>(p.C) + at) =
+                    make_uint2(epi_out16(o[0], p.epi.out_type) | (epi_out16(o[1], p.epi.out_type) << 16),
+                               epi_out16(o[2], p.epi.out_type) | (epi_out16(o[3], p.epi.out_type) << 16));
+            } else {
+#pragma unroll
+                for (int k = 0; k < 4; ++k)
+                    if (col + k < p.N)
+                        epi_store(p.C, at + k, o[k], p.epi.out_type);
+            }
+        }
+    });
 }
 
 template <bool PAIR>
@@ -299,12 +337,13 @@ __global__ void __launch_bounds__(kS8Threads, 1)
     const uint32_t empty0 = ctrl + 32u;        // [S1] codes read by the converters
     const uint32_t ready0 = ctrl + 64u;        // [S2] f16 written (both CTAs)
     const uint32_t free0 = ctrl + 96u;         // [S2] MMAs that read the f16 are done
-    const uint32_t tfull0 = ctrl + 128u;       // [2] accumulator complete
-    const uint32_t tempty0 = ctrl + 144u;      // [2] accumulator read out
+    const uint32_t tfull = ctrl + 128u;        // accumulator complete
+    const uint32_t tempty = ctrl + 136u;       // accumulator read out (the leader's: by both CTAs)
     const uint32_t done_bar = ctrl + 160u;     // all MMAs completed
     uint32_t *const tmem_slot = reinterpret_cast<uint32_t *>(ctrl_ptr + 176);
     const uint32_t flag = ctrl + 180u;         // this CTA gives up
-    const SharedSchedule sched{ctrl + 256u};
+    const SharedSchedule<false> sched{ctrl + 256u};
+    const SharedSchedule<true> wsched{ctrl + 256u};
     const uint32_t last_flag = ctrl + 184u;    // [2] one per column half
     const uint32_t gtab = ctrl + Cfg::GROUP_TABLE_OFF;
 
@@ -316,16 +355,14 @@ __global__ void __launch_bounds__(kS8Threads, 1)
     if (threadIdx.x == 0) {
         for (int s = 0; s < S1; ++s) {
             ptx::mbar_init(full0 + 8u * s, 1);
-            ptx::mbar_init(empty0 + 8u * s, 8);
+            ptx::mbar_init(empty0 + 8u * s, 12);
         }
         for (int s = 0; s < S2; ++s) {
-            ptx::mbar_init(ready0 + 8u * s, 8 * Cfg::CTAS);
+            ptx::mbar_init(ready0 + 8u * s, 12 * Cfg::CTAS);
             ptx::mbar_init(free0 + 8u * s, 1);
         }
-        for (int h = 0; h < 2; ++h) {
-            ptx::mbar_init(tfull0 + 8u * h, 1);
-            ptx::mbar_init(tempty0 + 8u * h, 4 * Cfg::CTAS);
-        }
+        ptx::mbar_init(tfull, 1);
+        ptx::mbar_init(tempty, 8 * Cfg::CTAS);
         ptx::mbar_init(done_bar, 1);
         ptx::st_shared_u32(flag, 0u);
         ptx::fence_mbar_init();
@@ -354,7 +391,7 @@ __global__ void __launch_bounds__(kS8Threads, 1)
     const uint32_t tmem = *tmem_slot;
 
     const uint32_t ready_lead0 = PAIR ? ptx::mapa_shared(ready0, 0) : ready0;
-    const uint32_t tempty_lead0 = PAIR ? ptx::mapa_shared(tempty0, 0) : tempty0;
+    const uint32_t tempty_lead = PAIR ? ptx::mapa_shared(tempty, 0) : tempty;
     const int32_t row_off = int32_t(rank) * Cfg::ROWS;
 
     if (warp < 4) {
@@ -364,11 +401,11 @@ __global__ void __launch_bounds__(kS8Threads, 1)
             uint32_t stage = 0, phase = 0;
             uint32_t issued = 0;
             bool ok = true;
-            for (PieceWalk w(sched, worker); ok && w.advance(sched);) {
+            for (PieceWalk<false> w(sched, worker); ok && w.advance(sched);) {
                 const S8Tile t = tile_at(w.tile, p, gtab, Cfg::TILE_M, Cfg::TILE_N);
-                const int32_t col = t.n0 + int32_t(rank) * 64;
+                const int32_t col = t.n0 + int32_t(rank) * 128;
                 for (int32_t kb = w.kb0; kb < w.kb1; ++kb) {
-                    if (!s8_wait<false>(empty0 + 8u * stage, phase ^ 1u, flag, p, kStatusProducer)) {
+                    if (!s8_wait<PAIR>(empty0 + 8u * stage, phase ^ 1u, flag, p, kStatusProducer)) {
                         ok = false;
                         break;
                     }
@@ -377,7 +414,6 @@ __global__ void __launch_bounds__(kS8Threads, 1)
                     ptx::mbar_arrive_expect_tx(fb, Cfg::CODE_STAGE);
                     ptx::tma_load_3d(sa, &map_a, fb, kb * Cfg::BK, t.m0 + row_off, t.z);
                     ptx::tma_load_3d(sa + Cfg::A_CODES, &map_b, fb, col, kb * Cfg::BK, t.z);
-                    ptx::tma_load_3d(sa + Cfg::A_CODES + Cfg::B_BOX, &map_b, fb, col + Cfg::HC, kb * Cfg::BK, t.z);
                     ++issued;
                     if (++stage == S1) {
                         stage = 0;
@@ -389,7 +425,7 @@ __global__ void __launch_bounds__(kS8Threads, 1)
             // (The last S1 loads: the slots from `stage` on, oldest first.)
             for (int i = 0; i < S1; ++i) {
                 if (issued + i >= uint32_t(S1))
-                    s8_wait<false>(full0 + 8u * stage, phase ^ 1u, flag, p, kStatusDrain, false);
+                    s8_wait<PAIR>(full0 + 8u * stage, phase ^ 1u, flag, p, kStatusDrain, false);
                 if (++stage == S1) {
                     stage = 0;
                     phase ^= 1u;
@@ -397,40 +433,34 @@ __global__ void __launch_bounds__(kS8Threads, 1)
             }
         } else if (warp == 1 && lane == 0 && rank == 0) {
             // ---------------- MMA issuer
-            constexpr uint32_t idesc = mma_idesc<Cfg::HC, PAIR>();
+            constexpr uint32_t idesc = mma_idesc<Cfg::TILE_N, PAIR>();
             constexpr uint16_t both = PAIR ? 3 : 1;
             uint32_t stage = 0, phase = 0, aphase = 0;
             bool ok = true;
-            for (PieceWalk w(sched, worker); ok && w.advance(sched);) {
+            for (PieceWalk<false> w(sched, worker); ok && w.advance(sched);) {
                 int c = 0;  // blocks in the accumulator
                 for (int32_t kb = w.kb0; ok && kb < w.kb1; ++kb) {
-                    if (!s8_wait<PAIR>(ready0 + 8u * stage, phase, flag, p, kStatusMma)) {
+                    if (!s8_wait<PAIR, PAIR>(ready0 + 8u * stage, phase, flag, p, kStatusMma)) {
                         ok = false;
                         break;
                     }
                     ptx::tc_fence_after_sync();
                     const bool last = c == kChunkBlocks - 1 || kb == w.kb1 - 1;
                     const uint32_t a = tmem + Cfg::A_COL + stage * uint32_t(Cfg::BK / 2);
-#pragma unroll 1
-                    for (int h = 0; h < 2; ++h) {
-                        if (c == 0) {
-                            if (!s8_wait<PAIR>(tempty0 + 8u * h, aphase ^ 1u, flag, p, kStatusMma)) {
-                                ok = false;
-                                break;
-                            }
-                            ptx::tc_fence_after_sync();
+                    if (c == 0) {
+                        if (!s8_wait<PAIR, PAIR>(tempty, aphase ^ 1u, flag, p, kStatusMma)) {
+                            ok = false;
+                            break;
                         }
-                        const uint32_t d = tmem + Cfg::ACC_COL + uint32_t(h * Cfg::HC);
-                        const uint32_t sb = f16_0 + stage * Cfg::F_STAGE + uint32_t(h * Cfg::F_BOX);
-#pragma unroll
-                        for (int kk = 0; kk < Cfg::BK / 16; ++kk)
-                            ptx::mma_f16_ts<PAIR>(d, a + 8u * kk, desc_b(sb + 2048u * kk), idesc,
-                                                  (c > 0 || kk > 0) ? 1u : 0u);
-                        if (last)
-                            ptx::mma_commit<PAIR>(tfull0 + 8u * h, both);
+                        ptx::tc_fence_after_sync();
                     }
-                    if (!ok)
-                        break;
+                    const uint32_t sb = f16_0 + stage * Cfg::F_STAGE;
+#pragma unroll
+                    for (int kk = 0; kk < Cfg::BK / 16; ++kk)
+                        ptx::mma_f16_ts<PAIR>(tmem, a + 8u * kk, desc_b_s8<PAIR>(sb + 2048u * kk), idesc,
+                                              (c > 0 || kk > 0) ? 1u : 0u);
+                    if (last)
+                        ptx::mma_commit<PAIR>(tfull, both);
                     ptx::mma_commit<PAIR>(free0 + 8u * stage, both);
                     if (++stage == S2) {
                         stage = 0;
@@ -443,20 +473,20 @@ __global__ void __launch_bounds__(kS8Threads, 1)
             }
             // Every MMA must finish before TMEM is freed.
             ptx::mma_commit<PAIR>(done_bar, 1);
-            s8_wait<false>(done_bar, 0, flag, p, kStatusDrain, false);
+            s8_wait<PAIR>(done_bar, 0, flag, p, kStatusDrain, false);
         }
         __syncwarp();
-    } else if (warp < 12) {
+    } else if (warp < kWarpDrain) {
         // ---------------- converters
         ptx::regs_dec<kS8RegsConvert>();
-        const bool is_a = warp < 8;
-        const int q = warp & 3;
+        const bool is_a = warp < kWarpB;
+        const int q = is_a ? warp - kWarpA : warp - kWarpB;
         uint32_t s1 = 0, p1 = 0, s2 = 0, p2 = 0;
         bool ok = true;
-        for (PieceWalk w(sched, worker); ok && w.advance(sched);) {
+        for (PieceWalk<true> w(wsched, worker); ok && w.advance(wsched);) {
             for (int32_t kb = w.kb0; kb < w.kb1; ++kb) {
-                ok = s8_wait<false>(full0 + 8u * s1, p1, flag, p, kStatusProducer) &&
-                     s8_wait<false>(free0 + 8u * s2, p2 ^ 1u, flag, p, kStatusProducer);
+                ok = s8_wait<PAIR>(full0 + 8u * s1, p1, flag, p, kStatusProducer) &&
+                     s8_wait<PAIR>(free0 + 8u * s2, p2 ^ 1u, flag, p, kStatusProducer);
                 ok = __all_sync(0xffffffffu, ok);
                 if (!ok)
                     break;
@@ -487,24 +517,28 @@ __global__ void __launch_bounds__(kS8Threads, 1)
                     ptx::tmem_wait_st();
                     ptx::tc_fence_before_sync();
                 } else {
-                    // Box h: 128 rows of 64 codes; a lane takes 16 codes of
-                    // one row and writes two 16-byte chunks of f16 (eight
-                    // lanes cover all eight chunk positions of the banks).
-                    const int i = 32 * q + lane;
+                    // 128 rows (k) of 128 codes, swizzled by the row.  A warp
+                    // takes eight rows of one 64-column half at a time: a lane
+                    // 16 codes of a row, written as two 16-byte chunks of f16.
+                    // Rows k and k ^ 5 share eight lanes: bit 2 keeps their
+                    // loads, bit 0 their stores in different banks.
+                    const int c = lane & 3, i = lane >> 2;
+                    const uint32_t r0 = uint32_t((i >> 1) ^ ((i & 1) * 5));  // row of the eight
 #pragma unroll
-                    for (int j = 0; j < 8; ++j) {
-                        const int h = j >> 2;
-                        const int at = i + 128 * (j & 3);  // 16-byte chunk of the box
-                        const int k = at >> 2, c = at & 3;
-                        const uint4 u = ptx::ld_shared_v4(codes + uint32_t(Cfg::A_CODES + h * Cfg::B_BOX) + uint32_t(at) * 16u);
+                    for (int j = 0; j < 4; ++j) {
+                        const int h = j & 1;
+                        const uint32_t k = uint32_t(8 * (2 * q + (j >> 1))) + r0;
+                        const uint4 u = ptx::ld_shared_v4(codes + uint32_t(Cfg::A_CODES) + k * 128u +
+                                                          (uint32_t(4 * h + c) ^ r0) * 16u);
                         uint32_t r[8];
                         codes_to_f16(u.x, r[0], r[1]);
                         codes_to_f16(u.y, r[2], r[3]);
                         codes_to_f16(u.z, r[4], r[5]);
                         codes_to_f16(u.w, r[6], r[7]);
-                        const uint32_t to = f16_0 + s2 * Cfg::F_STAGE + uint32_t(h * Cfg::F_BOX) + uint32_t(k) * 128u;
-                        ptx::st_shared_v4(to + (uint32_t((2 * c) ^ (k & 7)) << 4), r[0], r[1], r[2], r[3]);
-                        ptx::st_shared_v4(to + (uint32_t((2 * c + 1) ^ (k & 7)) << 4), r[4], r[5], r[6], r[7]);
+                        const uint32_t to = f16_0 + s2 * Cfg::F_STAGE + uint32_t(h * Cfg::F_BOX) + k * 128u;
+                        const uint32_t first = (uint32_t(2 * c) ^ r0) << 4;
+                        ptx::st_shared_v4(to + first, r[0], r[1], r[2], r[3]);
+                        ptx::st_shared_v4(to + (first ^ 16u), r[4], r[5], r[6], r[7]);
                     }
                     ptx::fence_proxy_async_smem();
                     __syncwarp();
@@ -512,12 +546,8 @@ __global__ void __launch_bounds__(kS8Threads, 1)
                         ptx::mbar_arrive(empty0 + 8u * s1);
                 }
                 __syncwarp();
-                if (lane == 0) {
-                    if constexpr (PAIR)
-                        ptx::mbar_arrive_cluster(ready_lead0 + 8u * s2);
-                    else
-                        ptx::mbar_arrive(ready0 + 8u * s2);
-                }
+                if (lane == 0)
+                    arrive_leader<PAIR>(ready_lead0 + 8u * s2);
                 if (++s1 == S1) {
                     s1 = 0;
                     p1 ^= 1u;
@@ -531,30 +561,31 @@ __global__ void __launch_bounds__(kS8Threads, 1)
     } else {
         // ---------------- accumulator -> integers -> C
         ptx::regs_inc<kS8RegsDrain>();
-        const int e = warp - 12;
+        const int e = warp - kWarpDrain;
         const int h = e >> 2;
         const int q = warp & 3;
         const int tid = 32 * q + lane;  // row of the CTA's 128
-        const uint32_t acc = tmem + (uint32_t(32 * q) << 16) + Cfg::ACC_COL + uint32_t(h * Cfg::HC);
+        const uint32_t acc = tmem + (uint32_t(32 * q) << 16) + uint32_t(h * Cfg::HC);
         const uint32_t buf = staging + uint32_t(e) * 4096u;
         constexpr int KEEP = Cfg::HC < 96 ? Cfg::HC : 96;
         static_assert(Cfg::HC - KEEP <= 32, "one staging box");
-        const uint32_t mine_at = buf + 4u * uint32_t(lane);
+        // Columns j .. j + 3 of the lane's row of the staging box.
+        auto stash = [&](int j) { return buf + uint32_t(lane) * 128u + (uint32_t((j >> 2) ^ (lane & 7)) << 4); };
         uint32_t aphase = 0;
         bool ok = true;
-        for (PieceWalk w(sched, worker); ok && w.advance(sched);) {
+        for (PieceWalk<true> w(wsched, worker); ok && w.advance(wsched);) {
             // The row's sums: the first KEEP columns in registers, the others
-            // (one box, in a pair) in the lane's column of the idle staging
-            // box, which keeps the warp within its registers.
+            // (one box, in a pair) in the lane's row of the idle staging box,
+            // which keeps the warp within its registers.
             int32_t sum[KEEP];
 #pragma unroll
             for (int j = 0; j < KEEP; ++j)
                 sum[j] = 0;
 #pragma unroll
-            for (int j = KEEP; j < Cfg::HC; ++j)
-                ptx::st_shared_u32(mine_at + 128u * (j - KEEP), 0u);
+            for (int j = KEEP; j < Cfg::HC; j += 4)
+                ptx::st_shared_v4(stash(j - KEEP), 0u, 0u, 0u, 0u);
             for (int32_t kb = w.kb0; kb < w.kb1; kb += kChunkBlocks) {
-                ok = s8_wait<PAIR>(tfull0 + 8u * h, aphase, flag, p, kStatusEpilogue);
+                ok = s8_wait<PAIR>(tfull, aphase, flag, p, kStatusEpilogue);
                 ok = __all_sync(0xffffffffu, ok);
                 if (!ok)
                     break;
@@ -568,32 +599,38 @@ __global__ void __launch_bounds__(kS8Threads, 1)
                     if (c + 1 < Cfg::HC / 8)
                         ptx::tmem_ld_32x32b_x8(acc + 8u * (c + 1), r[(c + 1) & 1]);
 #pragma unroll
-                    for (int j = 0; j < 8; ++j) {
-                        const int32_t v = __float2int_rn(__uint_as_float(r[c & 1][j]));
+                    for (int j = 0; j < 8; j += 4) {
+                        int32_t v[4];
+#pragma unroll
+                        for (int i = 0; i < 4; ++i)
+                            v[i] = __float2int_rn(__uint_as_float(r[c & 1][j + i]));
                         if (8 * c < KEEP) {
-                            sum[(8 * c + j) % KEEP] += v;
+#pragma unroll
+                            for (int i = 0; i < 4; ++i)
+                                sum[(8 * c + j + i) % KEEP] += v[i];
                         } else {
-                            const uint32_t to = mine_at + 128u * (8 * c + j - KEEP);
-                            ptx::st_shared_u32(to, ptx::ld_shared_u32(to) + uint32_t(v));
+                            const uint32_t at = stash(8 * c + j - KEEP);
+                            const uint4 o = ptx::ld_shared_v4(at);
+                            ptx::st_shared_v4(at, o.x + v[0], o.y + v[1], o.z + v[2], o.w + v[3]);
                         }
                     }
                 }
                 ptx::tc_fence_before_sync();
                 __syncwarp();
-                if (lane == 0) {
-                    if constexpr (PAIR)
-                        ptx::mbar_arrive_cluster(tempty_lead0 + 8u * h);
-                    else
-                        ptx::mbar_arrive(tempty0 + 8u * h);
-                }
+                if (lane == 0)
+                    arrive_leader<PAIR>(tempty_lead);
                 aphase ^= 1u;
             }
             // The four warps go on or give up together (they meet below).
-            ok = ptx::named_bar_and(1 + h, 128, ok);
+            ok = __all_sync(0xffffffffu, ptx::named_bar_and(1 + h, 128, ok));
             if (!ok)
                 break;
-            const S8Tile t = tile_at(w.tile, p, gtab, Cfg::TILE_M, Cfg::TILE_N);
-            if (w.kb1 - w.kb0 < sched.kb()) {
+            S8Tile t = tile_at(w.tile, p, gtab, Cfg::TILE_M, Cfg::TILE_N);
+            t.m0 = __shfl_sync(0xffffffffu, t.m0, 0);  // (uniform to the compiler)
+            t.n0 = __shfl_sync(0xffffffffu, t.n0, 0);
+            t.z = __shfl_sync(0xffffffffu, t.z, 0);
+            t.rows = __shfl_sync(0xffffffffu, t.rows, 0);
+            if (w.kb1 - w.kb0 < wsched.kb()) {
                 // A piece: its sums go to this worker's slot, and whoever
                 // arrives last adds up the others'.  [4-column group][row].
                 const int part = int(rank) * 2 + h;
@@ -606,15 +643,14 @@ __global__ void __launch_bounds__(kS8Threads, 1)
                         x = make_int4(sum[4 * j % KEEP], sum[(4 * j + 1) % KEEP], sum[(4 * j + 2) % KEEP],
                                       sum[(4 * j + 3) % KEEP]);
                     } else {
-                        const uint32_t at = mine_at + 128u * (4 * j - KEEP);
-                        x = make_int4(int32_t(ptx::ld_shared_u32(at)), int32_t(ptx::ld_shared_u32(at + 128u)),
-                                      int32_t(ptx::ld_shared_u32(at + 256u)), int32_t(ptx::ld_shared_u32(at + 384u)));
+                        const uint4 o = ptx::ld_shared_v4(stash(4 * j - KEEP));
+                        x = make_int4(int32_t(o.x), int32_t(o.y), int32_t(o.z), int32_t(o.w));
                     }
                     __stcg(mine + j * Cfg::ROWS + tid, x);
                 }
                 __threadfence();
                 ptx::named_bar_sync(1 + h, 128);
-                const S8Schedule cut = sched.all();
+                const S8Schedule cut = wsched.all();
                 const int32_t first = cut.owner(w.tile * cut.kb);
                 const int32_t last = cut.owner((w.tile + 1) * cut.kb - 1);
                 if (q == 0)
@@ -639,11 +675,9 @@ __global__ void __launch_bounds__(kS8Threads, 1)
                             sum[(4 * j + 2) % KEEP] += x.z;
                             sum[(4 * j + 3) % KEEP] += x.w;
                         } else {
-                            const uint32_t at = mine_at + 128u * (4 * j - KEEP);
-                            ptx::st_shared_u32(at, ptx::ld_shared_u32(at) + uint32_t(x.x));
-                            ptx::st_shared_u32(at + 128u, ptx::ld_shared_u32(at + 128u) + uint32_t(x.y));
-                            ptx::st_shared_u32(at + 256u, ptx::ld_shared_u32(at + 256u) + uint32_t(x.z));
-                            ptx::st_shared_u32(at + 384u, ptx::ld_shared_u32(at + 384u) + uint32_t(x.w));
+                            const uint32_t at = stash(4 * j - KEEP);
+                            const uint4 o = ptx::ld_shared_v4(at);
+                            ptx::st_shared_v4(at, o.x + x.x, o.y + x.y, o.z + x.z, o.w + x.w);
                         }
                     }
                 }
@@ -651,41 +685,34 @@ __global__ void __launch_bounds__(kS8Threads, 1)
             // Through the warp's staging box: lane = row in, lane = column group out.
             const int32_t my_row = t.m0 + row_off + tid;
             const float sa = p.scale_a && my_row < t.rows ? __ldg(p.scale_a + t.z * p.sa_stride + my_row) : 1.f;
-            const int32_t row0 = t.m0 + row_off + 32 * q + (lane >> 3);
-#pragma unroll
-            for (int i = 0; i < Cfg::HC / 32; ++i) {
-                // The box whose sums wait in the staging space goes first.
-                const int b = (i + Cfg::HC / 32 - (KEEP < Cfg::HC ? 1 : 0)) % (Cfg::HC / 32);
-                uint32_t v[32];
-#pragma unroll
-                for (int j = 0; j < 32; ++j)
-                    v[j] = 32 * b < KEEP ? uint32_t(sum[(32 * b + j) % KEEP]) : ptx::ld_shared_u32(mine_at + 128u * j);
-                __syncwarp();  // every lane has its sums before the box is overwritten
-#pragma unroll
-                for (int j = 0; j < 8; ++j)
-                    ptx::st_shared_v4(buf + uint32_t(lane) * 128u + (uint32_t(j ^ (lane & 7)) << 4),
-                                      __float_as_uint(float(int32_t(v[4 * j])) * sa),
-                                      __float_as_uint(float(int32_t(v[4 * j + 1])) * sa),
-                                      __float_as_uint(float(int32_t(v[4 * j + 2])) * sa),
-                                      __float_as_uint(float(int32_t(v[4 * j + 3])) * sa));
-                __syncwarp();
-                const int32_t col = t.n0 + h * Cfg::HC + 32 * b + 4 * (lane & 7);
-                if (col < p.N) {
-                    float sb[4], bias[4];
-                    column_terms(p, t.z, col, sb, bias);
+            const int32_t row0 = t.m0 + row_off + 32 * q;
+            constexpr int BOXES = Cfg::HC / 32;
 #pragma unroll 1
-                    for (int k = 0; k < 8; ++k) {
-                        const int32_t row = row0 + 4 * k;
-                        if (row >= t.rows)
-                            break;
-                        const int r = 4 * k + (lane >> 3);
-                        const uint4 u = ptx::ld_shared_v4(buf + uint32_t(r) * 128u + (uint32_t((lane & 7) ^ (r & 7)) << 4));
-                        put4(p, t.z * p.sC + row * p.ldc + col, col,
-                             make_float4(__uint_as_float(u.x), __uint_as_float(u.y), __uint_as_float(u.z),
-                                         __uint_as_float(u.w)),
-                             sb, bias);
+            for (int i = 0; i < BOXES; ++i) {
+                // The box whose sums wait in the staging space goes first.
+                const int b = KEEP < Cfg::HC ? (i + BOXES - 1) % BOXES : i;
+                const int32_t col = t.n0 + h * Cfg::HC + 32 * b;
+                if (__any_sync(0xffffffffu, col >= p.N))
+                    continue;  // (the whole warp)
+#pragma unroll
+                for (int bb = 0; bb < BOXES; ++bb)
+                    if (b == bb) {
+#pragma unroll
+                        for (int j = 0; j < 32; j += 4) {
+                            uint4 v;
+                            if (32 * bb < KEEP)
+                                v = make_uint4(sum[(32 * bb + j) % KEEP], sum[(32 * bb + j + 1) % KEEP],
+                                               sum[(32 * bb + j + 2) % KEEP], sum[(32 * bb + j + 3) % KEEP]);
+                            else
+                                v = ptx::ld_shared_v4(stash(j));
+                            ptx::st_shared_v4(stash(j), __float_as_uint(float(int32_t(v.x)) * sa),
+                                              __float_as_uint(float(int32_t(v.y)) * sa),
+                                              __float_as_uint(float(int32_t(v.z)) * sa),
+                                              __float_as_uint(float(int32_t(v.w)) * sa));
+                        }
                     }
-                }
+                __syncwarp();
+                store_box(p, t, buf, row0, col, lane);
                 __syncwarp();
             }
         }

@@ -21,6 +21,13 @@ __device__ __forceinline__ void regs_inc()
     asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(REGS));
 }
 
+// Arrive on an mbarrier of any CTA of the cluster (a shared::cluster address),
+// releasing this thread's earlier accesses to its own CTA.
+__device__ __forceinline__ void mbar_arrive_remote(uint32_t cluster_addr)
+{
+    asm volatile("mbarrier.arrive.release.cta.shared::cluster.b64 _, [%0];" ::"r"(cluster_addr) : "memory");
+}
+
 // Warp-wide: lane l writes 16 consecutive 32-bit columns of TMEM lane
 // (taddr.lane + l).
 __device__ __forceinline__ void tmem_st_32x32b_x16(uint32_t taddr, const uint32_t (&r)[16])
