@@ -46,8 +46,8 @@ __device__ __forceinline__ void codes_to_f16(uint32_t w, uint32_t &lo, uint32_t 
 //   warp 1       MMA issuer (the pair's leader): A from TMEM, B from shared memory
 //   warps 4-7    A's codes -> f16 -> TMEM, one row per lane (they never pass
 //                through shared memory as f16)
-//   warps 8-15   B's codes -> f16 -> the 128-byte swizzled layout of the MMA
-//   warps 16-23  two per TMEM lane quarter, one per column half of the tile:
+//   warps 8-11   B's codes -> f16 -> the 128-byte swizzled layout of the MMA
+//   warps 12-19  two per TMEM lane quarter, one per column half of the tile:
 //                accumulator -> 32-bit sums, then the epilogue
 // The bound is shared-memory bandwidth: a 256 x 256 x 128 block costs an SM
 // 32 KB of codes in, 32 KB out to the converters, 32 KB of f16 B written and
@@ -79,15 +79,15 @@ struct S8Cfg {
     static constexpr uint32_t A_COL = 256;      // TMEM: the accumulator, then the f16 A ring
     static_assert(A_COL + S2 * (BK / 2) <= 512 && TILE_N <= 256, "TMEM columns");
     static constexpr int PARTS = 2 * CTAS;      // (CTA, half) parts of a tile
-    static constexpr int64_t SLOT_INTS = int64_t(PARTS) * ROWS * HC;
+    static constexpr int32_t SLOT_INTS = PARTS * ROWS * HC;
 };
 
-constexpr int kWarpA = 4, kWarpB = 8, kWarpDrain = 16, kS8Warps = 24;  // first warps of the roles
+constexpr int kWarpA = 4, kWarpB = 8, kWarpDrain = 12, kS8Warps = 20;  // first warps of the roles
 constexpr int kS8Threads = 32 * kS8Warps;
-// Registers per thread by warpgroup (six of 128 threads): together no more
-// than what the block was launched with (768 x 80).
-constexpr int kS8RegsIssue = 64, kS8RegsConvert = 48, kS8RegsDrain = 136;
-static_assert(128 * kS8RegsIssue + 3 * 128 * kS8RegsConvert + 2 * 128 * kS8RegsDrain <= kS8Threads * 80,
+// Registers per thread by warpgroup (five of 128 threads): together exactly
+// what the block was launched with (640 x 96).
+constexpr int kS8RegsIssue = 48, kS8RegsConvert = 56, kS8RegsDrain = 160;
+static_assert(128 * kS8RegsIssue + 2 * 128 * kS8RegsConvert + 2 * 128 * kS8RegsDrain <= kS8Threads * 96,
               "register split");
 
 // B's shared-memory descriptor: MN-major, 64-column boxes of BK rows of 128 bytes.
@@ -253,6 +253,44 @@ __device__ __forceinline__ bool s8_wait(uint32_t bar, uint32_t parity, uint32_t 
     }
 }
 
+// Add a chunk's f32 sums (HC columns of a TMEM lane) to the lane's integers.
+// 1.5 * 2^23 + f has f + kMagicBits as its bits while |f| < 2^22, so an
+// addition and an integer addition do what a conversion does at an eighth of
+// their rate (8192^3: 744 -> 7xx us).  A sum can reach 2^24, though it takes
+// codes near the limits with one sign to do so: where one of a warp's passes
+// 2^22, the warp converts those eight columns.  Eight columns are on their way
+// while eight are added.
+constexpr uint32_t kMagicBits = 0x4b400000u;  // of 1.5 * 2^23
+
+template <int HC>
+__device__ __forceinline__ void add_chunk(uint32_t acc, int32_t (&sum)[HC])
+{
+    const float magic = __uint_as_float(kMagicBits);
+    uint32_t r[2][8];
+    ptx::tmem_ld_32x32b_x8(acc, r[0]);
+#pragma unroll
+    for (int c = 0; c < HC / 8; ++c) {
+        ptx::tmem_wait_ld(r[c & 1]);
+        if (c + 1 < HC / 8)
+            ptx::tmem_ld_32x32b_x8(acc + 8u * (c + 1), r[(c + 1) & 1]);
+        float f[8];
+#pragma unroll
+        for (int j = 0; j < 8; ++j)
+            f[j] = __uint_as_float(r[c & 1][j]);
+        const float top = ptx::max_abs3(ptx::max_abs3(ptx::max_abs3(f[0], f[1], f[2]), f[3], f[4]), f[5],
+                                        ptx::max_abs3(f[6], f[7], 0.f));
+        if (__any_sync(0xffffffffu, top >= 4194304.f)) {
+#pragma unroll
+            for (int j = 0; j < 8; ++j)
+                sum[8 * c + j] += __float2int_rn(f[j]) + int32_t(kMagicBits);
+        } else {
+#pragma unroll
+            for (int j = 0; j < 8; ++j)
+                sum[8 * c + j] += __float_as_int(f[j] + magic);
+        }
+    }
+}
+
 // Arrive on a barrier of the pair's leader.  Released to the CTA only: what the
 // arrival stands for is complete in this SM before it is sent -- f16 in its own
 // shared memory (the proxy fence) or TMEM (the store wait), or TMEM read out
@@ -271,7 +309,7 @@ __device__ __forceinline__ void arrive_leader(uint32_t bar)
 
 // A staged box (32 rows of 32 f32 values, 16-byte chunks swizzled by the row)
 // through the epilogue into C: eight lanes take a row's chunks, four rows at a
-// time, four loads and stores in flight.
+// time.
 __device__ __forceinline__ void store_box(const S8Params &p, const S8Tile &t, uint32_t buf, int32_t row0, int32_t col0,
                                           int lane)
 {
@@ -291,7 +329,7 @@ __device__ __forceinline__ void store_box(const S8Params &p, const S8Tile &t, ui
     const int32_t first = lane >> 3;
     const int32_t rows = min(32, t.rows - row0);
     with_activation<kActRuntime>(p.epi.act, [&](auto act) {
-#pragma unroll 4
+#pragma unroll 1
         for (int r = first; r < rows; r += 4) {
             const int64_t at = t.z * p.sC + int64_t(row0 + r) * p.ldc + col;
             const uint4 u = ptx::ld_shared_v4(buf + uint32_t(r) * 128u + (uint32_t((lane & 7) ^ (r & 7)) << 4));
@@ -355,10 +393,10 @@ __global__ void __launch_bounds__(kS8Threads, 1)
     if (threadIdx.x == 0) {
         for (int s = 0; s < S1; ++s) {
             ptx::mbar_init(full0 + 8u * s, 1);
-            ptx::mbar_init(empty0 + 8u * s, 12);
+            ptx::mbar_init(empty0 + 8u * s, 8);
         }
         for (int s = 0; s < S2; ++s) {
-            ptx::mbar_init(ready0 + 8u * s, 12 * Cfg::CTAS);
+            ptx::mbar_init(ready0 + 8u * s, 8 * Cfg::CTAS);
             ptx::mbar_init(free0 + 8u * s, 1);
         }
         ptx::mbar_init(tfull, 1);
@@ -525,9 +563,9 @@ __global__ void __launch_bounds__(kS8Threads, 1)
                     const int c = lane & 3, i = lane >> 2;
                     const uint32_t r0 = uint32_t((i >> 1) ^ ((i & 1) * 5));  // row of the eight
 #pragma unroll
-                    for (int j = 0; j < 4; ++j) {
+                    for (int j = 0; j < 8; ++j) {
                         const int h = j & 1;
-                        const uint32_t k = uint32_t(8 * (2 * q + (j >> 1))) + r0;
+                        const uint32_t k = uint32_t(8 * (4 * q + (j >> 1))) + r0;
                         const uint4 u = ptx::ld_shared_v4(codes + uint32_t(Cfg::A_CODES) + k * 128u +
                                                           (uint32_t(4 * h + c) ^ r0) * 16u);
                         uint32_t r[8];
@@ -564,57 +602,25 @@ __global__ void __launch_bounds__(kS8Threads, 1)
         const int e = warp - kWarpDrain;
         const int h = e >> 2;
         const int q = warp & 3;
-        const int tid = 32 * q + lane;  // row of the CTA's 128
         const uint32_t acc = tmem + (uint32_t(32 * q) << 16) + uint32_t(h * Cfg::HC);
         const uint32_t buf = staging + uint32_t(e) * 4096u;
-        constexpr int KEEP = Cfg::HC < 96 ? Cfg::HC : 96;
-        static_assert(Cfg::HC - KEEP <= 32, "one staging box");
-        // Columns j .. j + 3 of the lane's row of the staging box.
-        auto stash = [&](int j) { return buf + uint32_t(lane) * 128u + (uint32_t((j >> 2) ^ (lane & 7)) << 4); };
         uint32_t aphase = 0;
         bool ok = true;
         for (PieceWalk<true> w(wsched, worker); ok && w.advance(wsched);) {
-            // The row's sums: the first KEEP columns in registers, the others
-            // (one box, in a pair) in the lane's row of the idle staging box,
-            // which keeps the warp within its registers.
-            int32_t sum[KEEP];
+            // The row's sums.  A chunk adds integer + kMagicBits to each (see
+            // add_chunk), so they start that much lower for every chunk.
+            int32_t sum[Cfg::HC];
+            const uint32_t chunks = uint32_t(w.kb1 - w.kb0 + kChunkBlocks - 1) / kChunkBlocks;
 #pragma unroll
-            for (int j = 0; j < KEEP; ++j)
-                sum[j] = 0;
-#pragma unroll
-            for (int j = KEEP; j < Cfg::HC; j += 4)
-                ptx::st_shared_v4(stash(j - KEEP), 0u, 0u, 0u, 0u);
+            for (int j = 0; j < Cfg::HC; ++j)
+                sum[j] = int32_t(0u - chunks * kMagicBits);
             for (int32_t kb = w.kb0; kb < w.kb1; kb += kChunkBlocks) {
                 ok = s8_wait<PAIR>(tfull, aphase, flag, p, kStatusEpilogue);
                 ok = __all_sync(0xffffffffu, ok);
                 if (!ok)
                     break;
                 ptx::tc_fence_after_sync();
-                // Eight columns on their way while eight are added.
-                uint32_t r[2][8];
-                ptx::tmem_ld_32x32b_x8(acc, r[0]);
-#pragma unroll
-                for (int c = 0; c < Cfg::HC / 8; ++c) {
-                    ptx::tmem_wait_ld(r[c & 1]);
-                    if (c + 1 < Cfg::HC / 8)
-                        ptx::tmem_ld_32x32b_x8(acc + 8u * (c + 1), r[(c + 1) & 1]);
-#pragma unroll
-                    for (int j = 0; j < 8; j += 4) {
-                        int32_t v[4];
-#pragma unroll
-                        for (int i = 0; i < 4; ++i)
-                            v[i] = __float2int_rn(__uint_as_float(r[c & 1][j + i]));
-                        if (8 * c < KEEP) {
-#pragma unroll
-                            for (int i = 0; i < 4; ++i)
-                                sum[(8 * c + j + i) % KEEP] += v[i];
-                        } else {
-                            const uint32_t at = stash(8 * c + j - KEEP);
-                            const uint4 o = ptx::ld_shared_v4(at);
-                            ptx::st_shared_v4(at, o.x + v[0], o.y + v[1], o.z + v[2], o.w + v[3]);
-                        }
-                    }
-                }
+                add_chunk<Cfg::HC>(acc, sum);
                 ptx::tc_fence_before_sync();
                 __syncwarp();
                 if (lane == 0)
@@ -625,34 +631,29 @@ __global__ void __launch_bounds__(kS8Threads, 1)
             ok = __all_sync(0xffffffffu, ptx::named_bar_and(1 + h, 128, ok));
             if (!ok)
                 break;
-            S8Tile t = tile_at(w.tile, p, gtab, Cfg::TILE_M, Cfg::TILE_N);
-            t.m0 = __shfl_sync(0xffffffffu, t.m0, 0);  // (uniform to the compiler)
-            t.n0 = __shfl_sync(0xffffffffu, t.n0, 0);
-            t.z = __shfl_sync(0xffffffffu, t.z, 0);
-            t.rows = __shfl_sync(0xffffffffu, t.rows, 0);
+            // (Read again rather than kept through the loop above, where
+            // registers are short.)
+            const uint32_t rank_now = PAIR ? ptx::cluster_ctarank() : 0u;
+            const int32_t tid = 32 * q + lane;
+            const int32_t me = int32_t(PAIR ? ptx::cta_id() >> 1 : ptx::cta_id());
+            int32_t cut_first = 0, cut_last = -1;  // contributors of a cut tile
             if (w.kb1 - w.kb0 < wsched.kb()) {
                 // A piece: its sums go to this worker's slot, and whoever
                 // arrives last adds up the others'.  [4-column group][row].
-                const int part = int(rank) * 2 + h;
-                const int64_t part_at = int64_t(part) * Cfg::ROWS * Cfg::HC;
-                int4 *mine = reinterpret_cast<int4 *>(p.partial + (2 * worker + (w.kb0 == 0 ? 1 : 0)) * Cfg::SLOT_INTS + part_at);
-#pragma unroll
-                for (int j = 0; j < Cfg::HC / 4; ++j) {
-                    int4 x;
-                    if (4 * j < KEEP) {
-                        x = make_int4(sum[4 * j % KEEP], sum[(4 * j + 1) % KEEP], sum[(4 * j + 2) % KEEP],
-                                      sum[(4 * j + 3) % KEEP]);
-                    } else {
-                        const uint4 o = ptx::ld_shared_v4(stash(4 * j - KEEP));
-                        x = make_int4(int32_t(o.x), int32_t(o.y), int32_t(o.z), int32_t(o.w));
-                    }
-                    __stcg(mine + j * Cfg::ROWS + tid, x);
-                }
-                __threadfence();
-                ptx::named_bar_sync(1 + h, 128);
+                // A tile's first contributor holds its first block and uses
+                // its second slot; the others start in the tile: their first.
                 const S8Schedule cut = wsched.all();
                 const int32_t first = cut.owner(w.tile * cut.kb);
                 const int32_t last = cut.owner((w.tile + 1) * cut.kb - 1);
+                const int32_t part = int32_t(rank_now) * 2 + h;
+                const int32_t lane_at = part * (Cfg::ROWS * Cfg::HC) + 4 * tid;
+                int32_t *const mine = p.partial + (2 * me + (me == first)) * Cfg::SLOT_INTS + lane_at;
+#pragma unroll
+                for (int j = 0; j < Cfg::HC; j += 4)
+                    __stcg(reinterpret_cast<int4 *>(mine + j * Cfg::ROWS),
+                           make_int4(sum[j], sum[j + 1], sum[j + 2], sum[j + 3]));
+                __threadfence();
+                ptx::named_bar_sync(1 + h, 128);
                 if (q == 0)
                     ptx::st_shared_u32(last_flag + 4u * h, arrive_last(p.arrivals + w.tile * Cfg::PARTS + part, p.tag,
                                                                       uint32_t(last - first + 1), lane));
@@ -661,58 +662,66 @@ __global__ void __launch_bounds__(kS8Threads, 1)
                 __threadfence();
                 if (!mine_to_sum)
                     continue;
-                for (int32_t v = first; v <= last; ++v) {
-                    if (v == worker)
-                        continue;
-                    const int32_t slot = 2 * v + (cut.piece_begin(v) > w.tile * cut.kb ? 0 : 1);
-                    const int4 *theirs = reinterpret_cast<const int4 *>(p.partial + slot * Cfg::SLOT_INTS + part_at);
-#pragma unroll
-                    for (int j = 0; j < Cfg::HC / 4; ++j) {
-                        const int4 x = ptx::ld_cg_v4(theirs + j * Cfg::ROWS + tid);
-                        if (4 * j < KEEP) {
-                            sum[4 * j % KEEP] += x.x;
-                            sum[(4 * j + 1) % KEEP] += x.y;
-                            sum[(4 * j + 2) % KEEP] += x.z;
-                            sum[(4 * j + 3) % KEEP] += x.w;
-                        } else {
-                            const uint32_t at = stash(4 * j - KEEP);
-                            const uint4 o = ptx::ld_shared_v4(at);
-                            ptx::st_shared_v4(at, o.x + x.x, o.y + x.y, o.z + x.z, o.w + x.w);
-                        }
-                    }
-                }
+                cut_first = first;
+                cut_last = last;
             }
+            S8Tile t = tile_at(w.tile, p, gtab, Cfg::TILE_M, Cfg::TILE_N);
+            t.m0 = __shfl_sync(0xffffffffu, t.m0, 0);  // (uniform to the compiler)
+            t.n0 = __shfl_sync(0xffffffffu, t.n0, 0);
+            t.z = __shfl_sync(0xffffffffu, t.z, 0);
+            t.rows = __shfl_sync(0xffffffffu, t.rows, 0);
+            const int32_t first_row = int32_t(rank_now) * Cfg::ROWS;
             // Through the warp's staging box: lane = row in, lane = column group out.
-            const int32_t my_row = t.m0 + row_off + tid;
+            const int32_t my_row = t.m0 + first_row + tid;
             const float sa = p.scale_a && my_row < t.rows ? __ldg(p.scale_a + t.z * p.sa_stride + my_row) : 1.f;
-            const int32_t row0 = t.m0 + row_off + 32 * q;
-            constexpr int BOXES = Cfg::HC / 32;
+            const int32_t row0 = t.m0 + first_row + 32 * q;
+            auto stage = [&](int j, int32_t a, int32_t b, int32_t c, int32_t d) {
+                ptx::st_shared_v4(buf + uint32_t(lane) * 128u + (uint32_t((j >> 2) ^ (lane & 7)) << 4),
+                                  __float_as_uint(float(a) * sa), __float_as_uint(float(b) * sa),
+                                  __float_as_uint(float(c) * sa), __float_as_uint(float(d) * sa));
+            };
+            const int32_t boxes = min(Cfg::HC / 32, (p.N - t.n0 - h * Cfg::HC + 31) / 32);
+            if (cut_first <= cut_last) {
+                // All contributors' sums, this one's too, a box at a time.
+                const int32_t *from = p.partial + (int32_t(rank_now) * 2 + h) * (Cfg::ROWS * Cfg::HC) + 4 * tid;
 #pragma unroll 1
-            for (int i = 0; i < BOXES; ++i) {
-                // The box whose sums wait in the staging space goes first.
-                const int b = KEEP < Cfg::HC ? (i + BOXES - 1) % BOXES : i;
-                const int32_t col = t.n0 + h * Cfg::HC + 32 * b;
-                if (__any_sync(0xffffffffu, col >= p.N))
-                    continue;  // (the whole warp)
+                for (int b = 0; b < boxes; ++b, from += 32 * Cfg::ROWS) {
+#pragma unroll 1
+                    for (int j = 0; j < 32; j += 16) {
+                        int4 x[4] = {};
+#pragma unroll 1
+                        for (int32_t v = cut_first; v <= cut_last; ++v) {
+                            const int32_t *theirs = from + (2 * v + (v == cut_first)) * Cfg::SLOT_INTS + j * Cfg::ROWS;
 #pragma unroll
-                for (int bb = 0; bb < BOXES; ++bb)
+                            for (int i = 0; i < 4; ++i) {
+                                const int4 y = __ldcg(reinterpret_cast<const int4 *>(theirs + 4 * i * Cfg::ROWS));
+                                x[i].x += y.x;
+                                x[i].y += y.y;
+                                x[i].z += y.z;
+                                x[i].w += y.w;
+                            }
+                        }
+#pragma unroll
+                        for (int i = 0; i < 4; ++i)
+                            stage(j + 4 * i, x[i].x, x[i].y, x[i].z, x[i].w);
+                    }
+                    __syncwarp();
+                    store_box(p, t, buf, row0, t.n0 + h * Cfg::HC + 32 * b, lane);
+                    __syncwarp();
+                }
+                continue;
+            }
+#pragma unroll 1
+            for (int b = 0; b < boxes; ++b) {
+#pragma unroll
+                for (int bb = 0; bb < Cfg::HC / 32; ++bb)
                     if (b == bb) {
 #pragma unroll
-                        for (int j = 0; j < 32; j += 4) {
-                            uint4 v;
-                            if (32 * bb < KEEP)
-                                v = make_uint4(sum[(32 * bb + j) % KEEP], sum[(32 * bb + j + 1) % KEEP],
-                                               sum[(32 * bb + j + 2) % KEEP], sum[(32 * bb + j + 3) % KEEP]);
-                            else
-                                v = ptx::ld_shared_v4(stash(j));
-                            ptx::st_shared_v4(stash(j), __float_as_uint(float(int32_t(v.x)) * sa),
-                                              __float_as_uint(float(int32_t(v.y)) * sa),
-                                              __float_as_uint(float(int32_t(v.z)) * sa),
-                                              __float_as_uint(float(int32_t(v.w)) * sa));
-                        }
+                        for (int j = 0; j < 32; j += 4)
+                            stage(j, sum[32 * bb + j], sum[32 * bb + j + 1], sum[32 * bb + j + 2], sum[32 * bb + j + 3]);
                     }
                 __syncwarp();
-                store_box(p, t, buf, row0, col, lane);
+                store_box(p, t, buf, row0, t.n0 + h * Cfg::HC + 32 * b, lane);
                 __syncwarp();
             }
         }
@@ -802,7 +811,7 @@ template <bool PAIR>
 S8Shape shape_of()
 {
     using Cfg = S8Cfg<PAIR>;
-    return S8Shape{Cfg::TILE_M, Cfg::TILE_N, Cfg::BK, Cfg::SLOT_INTS * 4, Cfg::PARTS};
+    return S8Shape{Cfg::TILE_M, Cfg::TILE_N, Cfg::BK, int64_t(Cfg::SLOT_INTS) * 4, Cfg::PARTS};
 }
 
 }  // namespace

@@ -116,6 +116,22 @@ __device__ __forceinline__ bool named_bar_and(uint32_t id, uint32_t count, bool 
     return all != 0;
 }
 
+// blockIdx.x, read where it is written.
+__device__ __forceinline__ uint32_t cta_id()
+{
+    uint32_t r;
+    asm volatile("mov.u32 %0, %%ctaid.x;" : "=r"(r));
+    return r;
+}
+
+// The largest of |a|, |b| and |c|.
+__device__ __forceinline__ float max_abs3(float a, float b, float c)
+{
+    float d;
+    asm("max.abs.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
+    return d;
+}
+
 // 16 bytes through L2 (not L1), in program order with the other accesses.
 __device__ __forceinline__ int4 ld_cg_v4(const int4 *p)
 {
