@@ -73,7 +73,6 @@ struct S8Schedule {
     int32_t kb;
     int32_t workers;        // of the whole tiles
     int32_t cutters;        // workers that get a piece
-    static constexpr int kMinPiece = 2;
     static constexpr int32_t kMaxTiles = 1 << 30;
 
     __host__ __device__ void plan(int32_t tiles_, int32_t kb_, int32_t workers_)
@@ -83,8 +82,12 @@ struct S8Schedule {
         workers = workers_;
         const int32_t over = tiles % workers;
         shared = over == 0 ? 0 : tiles < workers ? tiles : over + workers;
-        // At least one piece per tile, however few blocks that is.
-        const int32_t pieces = kb < kMinPiece ? shared : shared * kb / kMinPiece;
+        // A tile's contributors: as many as balance the blocks each multiplies
+        // with the sums the last one adds up, about two blocks' time apiece.
+        int32_t each = 1;
+        while (2 * each * each < kb)
+            ++each;
+        const int32_t pieces = shared * each;
         cutters = pieces < 1 ? 1 : pieces < workers ? pieces : workers;
     }
     // First block of worker w's piece (w <= cutters).

@@ -636,6 +636,12 @@ __global__ void __launch_bounds__(kS8Threads, 1)
             const uint32_t rank_now = PAIR ? ptx::cluster_ctarank() : 0u;
             const int32_t tid = 32 * q + lane;
             const int32_t me = int32_t(PAIR ? ptx::cta_id() >> 1 : ptx::cta_id());
+            S8Tile t = tile_at(w.tile, p, gtab, Cfg::TILE_M, Cfg::TILE_N);
+            t.m0 = __shfl_sync(0xffffffffu, t.m0, 0);  // (uniform to the compiler)
+            t.n0 = __shfl_sync(0xffffffffu, t.n0, 0);
+            t.z = __shfl_sync(0xffffffffu, t.z, 0);
+            t.rows = __shfl_sync(0xffffffffu, t.rows, 0);
+            const int32_t row0 = t.m0 + int32_t(rank_now) * Cfg::ROWS + 32 * q;  // the warp's first row
             int32_t cut_first = 0, cut_last = -1;  // contributors of a cut tile
             if (w.kb1 - w.kb0 < wsched.kb()) {
                 // A piece: its sums go to this worker's slot, and whoever
@@ -648,10 +654,12 @@ __global__ void __launch_bounds__(kS8Threads, 1)
                 const int32_t part = int32_t(rank_now) * 2 + h;
                 const int32_t lane_at = part * (Cfg::ROWS * Cfg::HC) + 4 * tid;
                 int32_t *const mine = p.partial + (2 * me + (me == first)) * Cfg::SLOT_INTS + lane_at;
+                if (row0 < t.rows) {
 #pragma unroll
-                for (int j = 0; j < Cfg::HC; j += 4)
-                    __stcg(reinterpret_cast<int4 *>(mine + j * Cfg::ROWS),
-                           make_int4(sum[j], sum[j + 1], sum[j + 2], sum[j + 3]));
+                    for (int j = 0; j < Cfg::HC; j += 4)
+                        __stcg(reinterpret_cast<int4 *>(mine + j * Cfg::ROWS),
+                               make_int4(sum[j], sum[j + 1], sum[j + 2], sum[j + 3]));
+                }
                 __threadfence();
                 ptx::named_bar_sync(1 + h, 128);
                 if (q == 0)
@@ -665,46 +673,36 @@ __global__ void __launch_bounds__(kS8Threads, 1)
                 cut_first = first;
                 cut_last = last;
             }
-            S8Tile t = tile_at(w.tile, p, gtab, Cfg::TILE_M, Cfg::TILE_N);
-            t.m0 = __shfl_sync(0xffffffffu, t.m0, 0);  // (uniform to the compiler)
-            t.n0 = __shfl_sync(0xffffffffu, t.n0, 0);
-            t.z = __shfl_sync(0xffffffffu, t.z, 0);
-            t.rows = __shfl_sync(0xffffffffu, t.rows, 0);
-            const int32_t first_row = int32_t(rank_now) * Cfg::ROWS;
             // Through the warp's staging box: lane = row in, lane = column group out.
-            const int32_t my_row = t.m0 + first_row + tid;
-            const float sa = p.scale_a && my_row < t.rows ? __ldg(p.scale_a + t.z * p.sa_stride + my_row) : 1.f;
-            const int32_t row0 = t.m0 + first_row + 32 * q;
+            const float sa = p.scale_a && row0 + lane < t.rows ? __ldg(p.scale_a + t.z * p.sa_stride + row0 + lane) : 1.f;
             auto stage = [&](int j, int32_t a, int32_t b, int32_t c, int32_t d) {
                 ptx::st_shared_v4(buf + uint32_t(lane) * 128u + (uint32_t((j >> 2) ^ (lane & 7)) << 4),
                                   __float_as_uint(float(a) * sa), __float_as_uint(float(b) * sa),
                                   __float_as_uint(float(c) * sa), __float_as_uint(float(d) * sa));
             };
-            const int32_t boxes = min(Cfg::HC / 32, (p.N - t.n0 - h * Cfg::HC + 31) / 32);
+            const int32_t boxes = row0 < t.rows ? min(Cfg::HC / 32, (p.N - t.n0 - h * Cfg::HC + 31) / 32) : 0;
             if (cut_first <= cut_last) {
                 // All contributors' sums, this one's too, a box at a time.
                 const int32_t *from = p.partial + (int32_t(rank_now) * 2 + h) * (Cfg::ROWS * Cfg::HC) + 4 * tid;
 #pragma unroll 1
                 for (int b = 0; b < boxes; ++b, from += 32 * Cfg::ROWS) {
-#pragma unroll 1
-                    for (int j = 0; j < 32; j += 16) {
-                        int4 x[4] = {};
-#pragma unroll 1
-                        for (int32_t v = cut_first; v <= cut_last; ++v) {
-                            const int32_t *theirs = from + (2 * v + (v == cut_first)) * Cfg::SLOT_INTS + j * Cfg::ROWS;
+                    int4 x[8] = {};
+                    // Two contributors' loads in flight together.
+#pragma unroll 2
+                    for (int32_t v = cut_first; v <= cut_last; ++v) {
+                        const int32_t *theirs = from + (2 * v + (v == cut_first)) * Cfg::SLOT_INTS;
 #pragma unroll
-                            for (int i = 0; i < 4; ++i) {
-                                const int4 y = __ldcg(reinterpret_cast<const int4 *>(theirs + 4 * i * Cfg::ROWS));
-                                x[i].x += y.x;
-                                x[i].y += y.y;
-                                x[i].z += y.z;
-                                x[i].w += y.w;
-                            }
+                        for (int i = 0; i < 8; ++i) {
+                            const int4 y = __ldcg(reinterpret_cast<const int4 *>(theirs + 4 * i * Cfg::ROWS));
+                            x[i].x += y.x;
+                            x[i].y += y.y;
+                            x[i].z += y.z;
+                            x[i].w += y.w;
                         }
-#pragma unroll
-                        for (int i = 0; i < 4; ++i)
-                            stage(j + 4 * i, x[i].x, x[i].y, x[i].z, x[i].w);
                     }
+#pragma unroll
+                    for (int i = 0; i < 8; ++i)
+                        stage(4 * i, x[i].x, x[i].y, x[i].z, x[i].w);
                     __syncwarp();
                     store_box(p, t, buf, row0, t.n0 + h * Cfg::HC + 32 * b, lane);
                     __syncwarp();
