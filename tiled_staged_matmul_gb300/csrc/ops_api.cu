@@ -386,7 +386,7 @@ std::once_flag g_s8_attr_once[64];
 cudaError_t g_s8_attr[64];
 
 // All checks are done and every size is positive (K may be 0).
-gemm_status_t launch_s8(S8Params p, DeviceState *ds, cudaStream_t stream)
+gemm_status_t launch_product(S8Params p, DeviceState *ds, cudaStream_t stream)
 {
     cudaError_t e;
     if (p.K == 0) {
@@ -402,13 +402,15 @@ gemm_status_t launch_s8(S8Params p, DeviceState *ds, cudaStream_t stream)
     if (g_s8_attr[dev] != cudaSuccess)
         return fail_cuda(g_s8_attr[dev], "cudaFuncSetAttribute(int8 product)");
 
-    const bool pair = p.M > 128;
-    const S8Shape shape = s8_shape(pair);
+    const S8Kind kind = p.M <= 16 ? S8Kind::kFew16 : p.M <= 32 ? S8Kind::kFew32
+                        : p.M <= 128 ? S8Kind::kOne : S8Kind::kPair;
+    const bool few = p.M <= 32;
+    const S8Shape shape = s8_shape(kind);
     p.tiles_m = int32_t((int64_t(p.M) + shape.tile_m - 1) / shape.tile_m);
     p.tiles_n = int32_t((int64_t(p.N) + shape.tile_n - 1) / shape.tile_n);
     p.kb = int32_t((int64_t(p.K) + shape.block_k - 1) / shape.block_k);
     p.group_m = 8;
-    p.workers = pair ? ds->sms / 2 : ds->sms;
+    p.workers = kind == S8Kind::kPair ? ds->sms / 2 : ds->sms;
     p.timeout_ns = 2000000000ull + uint64_t(p.kb) * 20000ull;
     p.tag = next_launch_epoch() >> 16;
     const int64_t per4 = p.epi.out_type == kOutF32 ? 16 : 8;
@@ -425,7 +427,7 @@ gemm_status_t launch_s8(S8Params p, DeviceState *ds, cudaStream_t stream)
     if (tiles > S8Schedule::kMaxTiles)
         return fail(GEMM_ERR_INVALID_VALUE, "more than 2^30 output tiles in one call");
     S8Schedule sched;
-    sched.plan(int32_t(tiles), p.kb, p.workers);
+    sched.plan(int32_t(tiles), p.kb, p.workers, few ? S8Schedule::kFewRows : S8Schedule::kTiled);
     // (A grouped launch's tiles are counted on the device: any number up to these.)
     const int64_t cut = p.group_rows ? 2 * int64_t(p.workers) : sched.shared;
     const int64_t bytes_p = cut ? 2 * int64_t(p.workers) * shape.slot_bytes : 0;
@@ -471,16 +473,18 @@ gemm_status_t launch_s8(S8Params p, DeviceState *ds, cudaStream_t stream)
     const int64_t lda = p.M > 1 ? p.lda : round_up(p.lda, 16), ldb = p.K > 1 ? p.ldb : round_up(p.ldb, 16);
     const int64_t sA = p.batch > 1 ? p.sA : p.M * lda, sB = p.batch > 1 ? p.sB : p.K * ldb;
     if (st == GEMM_OK)
-        st = encode_3d(&map_a, CU_TENSOR_MAP_DATA_TYPE_UINT8, 1, p.A, p.K, p.M, p.batch, lda, sA, 128, 128,
-                       CU_TENSOR_MAP_L2_PROMOTION_L2_256B, "A");
+        st = encode_3d(&map_a, CU_TENSOR_MAP_DATA_TYPE_UINT8, 1, p.A, p.K, p.M, p.batch, lda, sA,
+                       uint32_t(shape.block_k), few ? uint32_t(shape.tile_m) : 128u,
+                       CU_TENSOR_MAP_L2_PROMOTION_L2_256B, "A", 1,
+                       few ? CU_TENSOR_MAP_SWIZZLE_NONE : CU_TENSOR_MAP_SWIZZLE_128B);
     if (st == GEMM_OK)
-        st = encode_3d(&map_b, CU_TENSOR_MAP_DATA_TYPE_UINT8, 1, p.B, p.N, p.K, p.batch, ldb, sB, 128, 128,
+        st = encode_3d(&map_b, CU_TENSOR_MAP_DATA_TYPE_UINT8, 1, p.B, p.N, p.K, p.batch, ldb, sB, 128, uint32_t(shape.block_k),
                        CU_TENSOR_MAP_L2_PROMOTION_L2_256B, "B");
     if (st == GEMM_OK) {
         const int64_t most = p.group_rows ? p.workers
                                           : std::max<int64_t>(sched.shared ? sched.cutters : 0,
                                                               std::min<int64_t>(sched.tiles, p.workers));
-        e = launch_s8_tiled(map_a, map_b, p, pair, int(most) * (pair ? 2 : 1), stream);
+        e = launch_s8(map_a, map_b, p, kind, int(most), stream);
         if (e != cudaSuccess)
             st = fail_cuda(e, "int8 product launch");
     }
@@ -510,7 +514,7 @@ gemm_status_t run_s8(S8Params p, cudaStream_t stream)
     if ((st = current(&dev, &ds)) != GEMM_OK || (st = check_on_device(buf, 7, dev)) != GEMM_OK)
         return st;
     p.status = ds->status;
-    return launch_s8(p, ds, stream);
+    return launch_product(p, ds, stream);
 }
 
 gemm_status_t s8_call(const int8_t *A, const int8_t *B, void *C, const float *scale_a, const float *scale_b,

@@ -74,20 +74,28 @@ struct S8Schedule {
     int32_t workers;        // of the whole tiles
     int32_t cutters;        // workers that get a piece
     static constexpr int32_t kMaxTiles = 1 << 30;
+    enum { kTiled, kFewRows };
 
-    __host__ __device__ void plan(int32_t tiles_, int32_t kb_, int32_t workers_)
+    __host__ __device__ void plan(int32_t tiles_, int32_t kb_, int32_t workers_, int kind)
     {
         tiles = tiles_;
         kb = kb_;
         workers = workers_;
         const int32_t over = tiles % workers;
         shared = over == 0 ? 0 : tiles < workers ? tiles : over + workers;
-        // A tile's contributors: as many as balance the blocks each multiplies
-        // with the sums the last one adds up, about two blocks' time apiece.
-        int32_t each = 1;
-        while (2 * each * each < kb)
-            ++each;
-        const int32_t pieces = shared * each;
+        int32_t pieces;
+        if (kind == kTiled) {
+            // A tile's contributors: as many as balance the blocks each
+            // multiplies with the sums the last one adds up, about two blocks'
+            // time apiece.
+            int32_t each = 1;
+            while (2 * each * each < kb)
+                ++each;
+            pieces = shared * each;
+        } else {
+            // The sums are small: at least a block per warp.
+            pieces = (shared * kb + 7) / 8;
+        }
         cutters = pieces < 1 ? 1 : pieces < workers ? pieces : workers;
     }
     // First block of worker w's piece (w <= cutters).
@@ -119,16 +127,18 @@ struct S8Params {
     unsigned long long tag;     // 48 bits, unique to the launch
 };
 
-// The tiled kernel: a CTA pair per 256 x 256 tile, or one CTA per 128 x 128.
+// The kernels: few rows (up to 16 or 32, 128 columns a tile); tiled, one CTA per
+// 128 x 128 tile or a CTA pair per 256 x 256.
+enum class S8Kind { kFew16, kFew32, kOne, kPair };
 struct S8Shape {
     int tile_m, tile_n, block_k;
     int64_t slot_bytes;         // of one worker's partial sums of one tile
     int parts;                  // arrival words per tile
 };
-S8Shape s8_shape(bool pair);
+S8Shape s8_shape(S8Kind kind);
 cudaError_t set_s8_attributes();
-cudaError_t launch_s8_tiled(const CUtensorMap &map_a, const CUtensorMap &map_b, const S8Params &p, bool pair,
-                            int grid, cudaStream_t stream);
+cudaError_t launch_s8(const CUtensorMap &map_a, const CUtensorMap &map_b, const S8Params &p, S8Kind kind, int grid,
+                      cudaStream_t stream);
 // Rows of `cols` bytes into rows 16-byte aligned and `d_ld` apart.
 cudaError_t launch_pack_s8(const int8_t *src, int64_t s_ld, int64_t s_stride, int8_t *dst, int64_t d_ld,
                            int64_t d_stride, int64_t rows, int64_t cols, int64_t batch, int sms,

@@ -307,6 +307,49 @@ __device__ __forceinline__ void arrive_leader(uint32_t bar)
         ptx::mbar_arrive(bar);
 }
 
+// Column scales (times alpha) and biases of four columns.
+__device__ __forceinline__ void column_terms(const S8Params &p, int32_t z, int32_t col, float (&sb)[4],
+                                             float (&bias)[4])
+{
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+        const bool in = col + k < p.N;
+        sb[k] = p.epi.alpha;
+        if (p.scale_b && in)
+            sb[k] *= __ldg(p.scale_b + z * p.sb_stride + col + k);
+        bias[k] = p.epi.bias && in ? __ldg(p.epi.bias + z * p.epi.bias_stride + col + k) : 0.f;
+    }
+}
+
+// Four values of a row (scaled by the row) through the epilogue into C.
+template <int ACT>
+__device__ __forceinline__ void put4_as(const S8Params &p, int64_t at, int32_t col, float (&o)[4],
+                                        const float (&sb)[4], const float (&bias)[4])
+{
+#pragma unroll
+    for (int k = 0; k < 4; ++k)
+        o[k] = epi_act(fmaf(sb[k], o[k], bias[k]), ACT, p.epi.slope);
+    if (p.vec_c && col + 3 < p.N) {
+        if (p.epi.out_type == kOutF32)
+            *reinterpret_cast<float4 *>(static_cast<float *>(p.C) + at) = make_float4(o[0], o[1], o[2], o[3]);
+        else
+            *reinterpret_cast<uint2 *>(static_cast<uint16_t *>(p.C) + at) =
+                make_uint2(epi_out16(o[0], p.epi.out_type) | (epi_out16(o[1], p.epi.out_type) << 16),
+                           epi_out16(o[2], p.epi.out_type) | (epi_out16(o[3], p.epi.out_type) << 16));
+        return;
+    }
+#pragma unroll
+    for (int k = 0; k < 4; ++k)
+        if (col + k < p.N)
+            epi_store(p.C, at + k, o[k], p.epi.out_type);
+}
+__device__ __forceinline__ void put4(const S8Params &p, int64_t at, int32_t col, float (&o)[4], const float (&sb)[4],
+                                     const float (&bias)[4])
+{
+    with_activation<kActRuntime>(p.epi.act,
+                                 [&](auto act) { put4_as<decltype(act)::value>(p, at, col, o, sb, bias); });
+}
+
 // A staged box (32 rows of 32 f32 values, 16-byte chunks swizzled by the row)
 // through the epilogue into C: eight lanes take a row's chunks, four rows at a
 // time.
@@ -317,38 +360,14 @@ __device__ __forceinline__ void store_box(const S8Params &p, const S8Tile &t, ui
     if (col >= p.N)
         return;
     float sb[4], bias[4];
-    const bool four = p.vec_c && col + 3 < p.N;
-#pragma unroll
-    for (int k = 0; k < 4; ++k) {
-        const bool in = col + k < p.N;
-        sb[k] = p.epi.alpha;
-        if (p.scale_b && in)
-            sb[k] *= __ldg(p.scale_b + t.z * p.sb_stride + col + k);
-        bias[k] = p.epi.bias && in ? __ldg(p.epi.bias + t.z * p.epi.bias_stride + col + k) : 0.f;
-    }
-    const int32_t first = lane >> 3;
+    column_terms(p, t.z, col, sb, bias);
     const int32_t rows = min(32, t.rows - row0);
     with_activation<kActRuntime>(p.epi.act, [&](auto act) {
 #pragma unroll 1
-        for (int r = first; r < rows; r += 4) {
-            const int64_t at = t.z * p.sC + int64_t(row0 + r) * p.ldc + col;
+        for (int r = lane >> 3; r < rows; r += 4) {
             const uint4 u = ptx::ld_shared_v4(buf + uint32_t(r) * 128u + (uint32_t((lane & 7) ^ (r & 7)) << 4));
             float o[4] = {__uint_as_float(u.x), __uint_as_float(u.y), __uint_as_float(u.z), __uint_as_float(u.w)};
-#pragma unroll
-            for (int k = 0; k < 4; ++k)
-                o[k] = epi_act(fmaf(sb[k], o[k], bias[k]), decltype(act)::value, p.epi.slope);
-            if (four && p.epi.out_type == kOutF32) {
-                *reinterpret_cast<float4 *>(static_cast<float *>(p.C) + at) = make_float4(o[0], o[1], o[2], o[3]);
-            } else if (four) {
-                *reinterpret_cast<uint2 *>(static_cast<uint16_t *>(p.C) + at) =
-                    make_uint2(epi_out16(o[0], p.epi.out_type) | (epi_out16(o[1], p.epi.out_type) << 16),
-                               epi_out16(o[2], p.epi.out_type) | (epi_out16(o[3], p.epi.out_type) << 16));
-            } else {
-#pragma unroll
-                for (int k = 0; k < 4; ++k)
-                    if (col + k < p.N)
-                        epi_store(p.C, at + k, o[k], p.epi.out_type);
-            }
+            put4_as<decltype(act)::value>(p, t.z * p.sC + int64_t(row0 + r) * p.ldc + col, col, o, sb, bias);
         }
     });
 }
@@ -420,7 +439,8 @@ __global__ void __launch_bounds__(kS8Threads, 1)
     }
     if (warp == 2 && lane == 0) {
         S8Schedule s;
-        s.plan(p.group_rows ? int32_t(ptx::ld_shared_u32(gtab + 4u * (p.batch - 1))) : p.tiles_m * p.tiles_n * p.batch, p.kb, p.workers);
+        s.plan(p.group_rows ? int32_t(ptx::ld_shared_u32(gtab + 4u * (p.batch - 1))) : p.tiles_m * p.tiles_n * p.batch, p.kb, p.workers,
+               S8Schedule::kTiled);
         sched.put(s);
     }
     ptx::tc_fence_before_sync();
@@ -736,6 +756,290 @@ __global__ void __launch_bounds__(kS8Threads, 1)
     }
 }
 
+// ------------------------------------------------------------- few rows
+//
+// Up to 32 rows of A (a decode step): the product reads every code of B once
+// and is bound by that.  Eight independent warps per CTA, each with a ring of
+// its own that TMA fills with 32 k x 128 columns of B (4 KiB) and the rows' 32
+// k of A, 160 KiB in flight per SM; no warp waits for another until a piece
+// ends.  Warp-wide f16 MMAs (16 rows x 8 columns x 16 k) run far below the
+// tcgen05 rate, but 16 or 32 rows need no more: one SM's share of the memory
+// rate is 23 codes a cycle, 16 x 23 multiply-adds.
+//
+// B's codes go from shared memory to the MMA's operand layout in registers:
+// lane 4g + t takes 16 columns (chunk g) of rows 4t ... 4t + 3, and a byte of
+// two rows each makes the f16 pair that it has to hold for one column.  Which
+// columns and which k a lane's registers stand for is free as long as A's
+// lanes agree, so no transpose is needed: MMA j of 16 gets column 16 g + j, and
+// k index 2t, 2t + 1, 2t + 8, 2t + 9 is row 4t, 4t + 1, 4t + 2, 4t + 3.
+//
+// A warp's f32 sums go into the CTA's 32-bit ones in shared memory (integer
+// atomics: any order gives the same sum) after at most 1024 k.
+template <int MT>
+struct S8FewCfg {
+    static constexpr int ROWS = 16 * MT, COLS = 128, BK = 32;
+    static constexpr int WARPS = 8, STAGES = 5;
+    static constexpr int B_BYTES = BK * COLS, A_BYTES = ROWS * BK;
+    static constexpr int SUMS = ROWS * COLS;  // [value of a lane][lane]
+    static constexpr int CTRL = 2048, GROUP_TABLE_OFF = 1024;
+    static constexpr int SMEM_BYTES = 1024 + WARPS * STAGES * (B_BYTES + A_BYTES) + SUMS * 4 + CTRL;
+    static_assert(SMEM_BYTES <= 232448, "227 KiB per block");
+    static constexpr int FLUSH = 1024 / BK;   // blocks whose sums f32 holds exactly
+};
+
+// Column pair of a byte column: f16(lo.byte b), f16(hi.byte b).
+template <int B>
+__device__ __forceinline__ uint32_t code_pair(uint32_t lo, uint32_t hi)
+{
+    const uint32_t v = (__byte_perm(lo, hi, 0x0400 + 0x0101 * B) & 0x00ff00ffu) ^ 0x64806480u;
+    const __half2 x = __hsub2(*reinterpret_cast<const __half2 *>(&v), __half2half2(__ushort_as_half(0x6480)));
+    return *reinterpret_cast<const uint32_t *>(&x);
+}
+
+template <int MT>
+__global__ void __launch_bounds__(256, 1)
+    tsm_s8_few_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ CUtensorMap map_b,
+                      const S8Params p)
+{
+    using Cfg = S8FewCfg<MT>;
+    constexpr int S = Cfg::STAGES;
+    extern __shared__ uint8_t smem_raw[];
+    const uint32_t raw = ptx::smem_addr(smem_raw);
+    const uint32_t base = (raw + 1023u) & ~1023u;
+    uint8_t *const base_ptr = smem_raw + (base - raw);
+    constexpr uint32_t A0 = Cfg::WARPS * S * Cfg::B_BYTES;
+    constexpr uint32_t SUMS0 = A0 + Cfg::WARPS * S * Cfg::A_BYTES;
+    constexpr uint32_t CTRL0 = SUMS0 + Cfg::SUMS * 4;
+    const uint32_t ctrl = base + CTRL0;
+    const uint32_t flag = ctrl + 384u, last_flag = ctrl + 388u;  // (barriers: 8 warps x S x 8 bytes)
+    static_assert(Cfg::WARPS * S * 8 <= 384, "control block");
+    const SharedSchedule<true> sched{ctrl + 400u};
+    const uint32_t gtab = ctrl + Cfg::GROUP_TABLE_OFF;
+    int32_t *const sums = reinterpret_cast<int32_t *>(base_ptr + SUMS0);
+
+    const int warp = __shfl_sync(0xffffffffu, int(threadIdx.x >> 5), 0);
+    const int lane = int(threadIdx.x & 31);
+    const int g = lane >> 2, t4 = lane & 3;
+    const int32_t worker = int32_t(blockIdx.x);
+    const uint32_t full0 = ctrl + uint32_t(warp * S) * 8u;
+    const uint32_t ring_b = base + uint32_t(warp * S) * Cfg::B_BYTES;
+    const uint32_t ring_a = base + A0 + uint32_t(warp * S) * Cfg::A_BYTES;
+
+    if (lane == 0) {
+        for (int s = 0; s < S; ++s)
+            ptx::mbar_init(full0 + 8u * s, 1);
+        ptx::fence_mbar_init();
+    }
+    if (warp == 0) {
+        if (p.group_rows) {
+            build_group_table(p.group_rows, p.batch, p.M, Cfg::ROWS, p.tiles_n,
+                              reinterpret_cast<uint32_t *>(base_ptr + CTRL0 + Cfg::GROUP_TABLE_OFF), p.status);
+            __syncwarp();
+        }
+        if (lane == 0) {
+            ptx::st_shared_u32(flag, 0u);
+            S8Schedule s;
+            s.plan(p.group_rows ? int32_t(ptx::ld_shared_u32(gtab + 4u * (p.batch - 1))) : p.tiles_n * p.batch, p.kb,
+                   p.workers, S8Schedule::kFewRows);
+            sched.put(s);
+        }
+    }
+    for (int i = int(threadIdx.x); i < Cfg::SUMS; i += 256)
+        sums[i] = 0;
+    __syncthreads();
+
+    // The warp's loads run S blocks ahead of its MMAs, with a walk of their own.
+    PieceWalk<true> wp(sched, worker);
+    int32_t pk = 0;
+    bool more = wp.advance(sched);
+    S8Tile pt = {};
+    if (more) {
+        pt = tile_at(wp.tile, p, gtab, Cfg::ROWS, Cfg::COLS);
+        pk = wp.kb0 + warp;
+    }
+    uint32_t issued = 0;  // stages that hold or await a block
+    auto issue = [&](uint32_t stage) {
+        while (more && pk >= wp.kb1) {
+            more = wp.advance(sched);
+            if (more) {
+                pt = tile_at(wp.tile, p, gtab, Cfg::ROWS, Cfg::COLS);
+                pk = wp.kb0 + warp;
+            }
+        }
+        if (!more)
+            return;
+        if (lane == 0) {
+            const uint32_t fb = full0 + 8u * stage;
+            ptx::mbar_arrive_expect_tx(fb, Cfg::B_BYTES + Cfg::A_BYTES);
+            ptx::tma_load_3d(ring_b + stage * Cfg::B_BYTES, &map_b, fb, pt.n0, pk * Cfg::BK, pt.z);
+            ptx::tma_load_3d(ring_a + stage * Cfg::A_BYTES, &map_a, fb, pk * Cfg::BK, 0, pt.z);
+        }
+        __syncwarp();
+        pk += Cfg::WARPS;
+        ++issued;
+    };
+#pragma unroll 1
+    for (uint32_t s = 0; s < uint32_t(S); ++s)
+        issue(s);
+
+    uint32_t stage = 0, phase = 0;
+    bool ok = true;
+    for (PieceWalk<true> w(sched, worker); ok && w.advance(sched);) {
+        float acc[MT][16][4];
+#pragma unroll
+        for (int m = 0; m < MT; ++m)
+#pragma unroll
+            for (int j = 0; j < 16; ++j)
+#pragma unroll
+                for (int d = 0; d < 4; ++d)
+                    acc[m][j][d] = 0.f;
+        auto flush = [&]() {
+#pragma unroll
+            for (int m = 0; m < MT; ++m)
+#pragma unroll
+                for (int j = 0; j < 16; ++j)
+#pragma unroll
+                    for (int d = 0; d < 4; ++d) {
+                        atomicAdd(sums + ((m * 16 + j) * 4 + d) * 32 + lane, __float2int_rn(acc[m][j][d]));
+                        acc[m][j][d] = 0.f;
+                    }
+        };
+        int held = 0;
+        for (int32_t kb = w.kb0 + warp; kb < w.kb1; kb += Cfg::WARPS) {
+            ok = __all_sync(0xffffffffu, s8_wait<false>(full0 + 8u * stage, phase, flag, p, kStatusProducer));
+            if (!ok)
+                break;
+            --issued;
+            const uint32_t sb = ring_b + stage * Cfg::B_BYTES, sa = ring_a + stage * Cfg::A_BYTES;
+#pragma unroll
+            for (int kk = 0; kk < 2; ++kk) {
+                uint32_t a[MT][4];
+#pragma unroll
+                for (int m = 0; m < MT; ++m) {
+                    codes_to_f16(ptx::ld_shared_u32(sa + uint32_t((16 * m + g) * Cfg::BK + 16 * kk + 4 * t4)),
+                                 a[m][0], a[m][2]);
+                    codes_to_f16(ptx::ld_shared_u32(sa + uint32_t((16 * m + g + 8) * Cfg::BK + 16 * kk + 4 * t4)),
+                                 a[m][1], a[m][3]);
+                }
+                uint32_t r[4][4];
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    const uint32_t k = uint32_t(16 * kk + 4 * t4 + i);
+                    const uint4 u = ptx::ld_shared_v4(sb + k * 128u + ((uint32_t(g) ^ (k & 7u)) << 4));
+                    r[i][0] = u.x;
+                    r[i][1] = u.y;
+                    r[i][2] = u.z;
+                    r[i][3] = u.w;
+                }
+#pragma unroll
+                for (int x = 0; x < 4; ++x) {
+                    auto column = [&](auto b) {
+                        constexpr int B = decltype(b)::value;
+                        const uint32_t b0 = code_pair<B>(r[0][x], r[1][x]);
+                        const uint32_t b1 = code_pair<B>(r[2][x], r[3][x]);
+#pragma unroll
+                        for (int m = 0; m < MT; ++m)
+                            ptx::mma_16816(acc[m][4 * x + B], a[m], b0, b1);
+                    };
+                    column(ActTag<0>{});
+                    column(ActTag<1>{});
+                    column(ActTag<2>{});
+                    column(ActTag<3>{});
+                }
+            }
+            __syncwarp();  // every lane has read the stage
+            issue(stage);
+            if (++stage == uint32_t(S)) {
+                stage = 0;
+                phase ^= 1u;
+            }
+            if (++held == Cfg::FLUSH) {
+                flush();
+                held = 0;
+            }
+        }
+        if (held)
+            flush();
+        ok = __syncthreads_and(ok);  // the CTA's sums are complete, or all its warps give up
+        if (!ok)
+            break;
+        const S8Tile t = tile_at(w.tile, p, gtab, Cfg::ROWS, Cfg::COLS);
+        bool mine = true;
+        if (w.kb1 - w.kb0 < sched.kb()) {
+            // A piece of a tile: as in the tiled kernel, with one part per tile.
+            const S8Schedule cut = sched.all();
+            const int32_t first = cut.owner(w.tile * cut.kb);
+            const int32_t last = cut.owner((w.tile + 1) * cut.kb - 1);
+            int32_t *const slot = p.partial + (2 * worker + (worker == first)) * Cfg::SUMS;
+            int4 own[2 * MT];
+#pragma unroll
+            for (int i = 0; i < 2 * MT; ++i) {
+                own[i] = reinterpret_cast<const int4 *>(sums)[i * 256 + threadIdx.x];
+                __stcg(reinterpret_cast<int4 *>(slot) + i * 256 + threadIdx.x, own[i]);
+            }
+            __threadfence();
+            __syncthreads();
+            if (warp == 0) {
+                const bool l = arrive_last(p.arrivals + w.tile, p.tag, uint32_t(last - first + 1), lane);
+                if (lane == 0)
+                    ptx::st_shared_u32(last_flag, l ? 1u : 0u);
+            }
+            __syncthreads();
+            mine = ptx::ld_shared_u32(last_flag) != 0;
+            __threadfence();
+            if (mine) {
+#pragma unroll 4
+                for (int32_t v = first; v <= last; ++v) {
+                    if (v == worker)
+                        continue;
+                    const int4 *theirs = reinterpret_cast<const int4 *>(p.partial + (2 * v + (v == first)) * Cfg::SUMS);
+#pragma unroll
+                    for (int i = 0; i < 2 * MT; ++i) {
+                        const int4 y = __ldcg(theirs + i * 256 + threadIdx.x);
+                        own[i].x += y.x;
+                        own[i].y += y.y;
+                        own[i].z += y.z;
+                        own[i].w += y.w;
+                    }
+                }
+#pragma unroll
+                for (int i = 0; i < 2 * MT; ++i)
+                    reinterpret_cast<int4 *>(sums)[i * 256 + threadIdx.x] = own[i];
+                __syncthreads();
+            }
+        }
+        if (mine) {
+            // Four columns of a row per thread.
+            const int32_t col = t.n0 + 4 * lane;
+            float sb[4], bias[4];
+            column_terms(p, t.z, col, sb, bias);
+            for (int row = warp; row < t.rows; row += Cfg::WARPS) {
+                float o[4];
+                const float sa = p.scale_a ? __ldg(p.scale_a + t.z * p.sa_stride + row) : 1.f;
+                const int c = 4 * lane;  // column 32 t + 16 d + j of value (j, d) of lane 4 (row % 8) + t
+#pragma unroll
+                for (int k = 0; k < 4; ++k) {
+                    const int j = (c + k) & 15, d = ((c >> 4) & 1) + 2 * ((row >> 3) & 1);
+                    o[k] = float(sums[(((row >> 4) * 16 + j) * 4 + d) * 32 + 4 * (row & 7) + (c >> 5)]) * sa;
+                }
+                put4(p, t.z * p.sC + row * p.ldc + col, col, o, sb, bias);
+            }
+        }
+        __syncthreads();
+        for (int i = int(threadIdx.x); i < Cfg::SUMS; i += 256)
+            sums[i] = 0;
+        __syncthreads();
+    }
+    // No TMA write into shared memory outlives the CTA.
+    for (; issued > 0; --issued) {
+        s8_wait<false>(full0 + 8u * stage, phase, flag, p, kStatusDrain, false);
+        if (++stage == uint32_t(S)) {
+            stage = 0;
+            phase ^= 1u;
+        }
+    }
+}
+
 // ------------------------------------------------------------- repacking
 
 // One thread per 16 bytes of the packed rows (zeros past a row's end).
@@ -814,18 +1118,43 @@ S8Shape shape_of()
 
 }  // namespace
 
-S8Shape s8_shape(bool pair) { return pair ? shape_of<true>() : shape_of<false>(); }
+S8Shape s8_shape(S8Kind kind)
+{
+    switch (kind) {
+    case S8Kind::kFew16: return S8Shape{16, 128, 32, S8FewCfg<1>::SUMS * 4, 1};
+    case S8Kind::kFew32: return S8Shape{32, 128, 32, S8FewCfg<2>::SUMS * 4, 1};
+    case S8Kind::kOne: return shape_of<false>();
+    default: return shape_of<true>();
+    }
+}
 
 cudaError_t set_s8_attributes()
 {
-    const cudaError_t e = set_tiled<true>();
-    return e == cudaSuccess ? set_tiled<false>() : e;
+    cudaError_t e = set_tiled<true>();
+    if (e == cudaSuccess)
+        e = set_tiled<false>();
+    if (e == cudaSuccess)
+        e = cudaFuncSetAttribute(tsm_s8_few_kernel<1>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                 S8FewCfg<1>::SMEM_BYTES);
+    if (e == cudaSuccess)
+        e = cudaFuncSetAttribute(tsm_s8_few_kernel<2>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                 S8FewCfg<2>::SMEM_BYTES);
+    return e;
 }
 
-cudaError_t launch_s8_tiled(const CUtensorMap &map_a, const CUtensorMap &map_b, const S8Params &p, bool pair,
-                            int grid, cudaStream_t stream)
+cudaError_t launch_s8(const CUtensorMap &map_a, const CUtensorMap &map_b, const S8Params &p, S8Kind kind, int grid,
+                      cudaStream_t stream)
 {
-    return pair ? launch_tiled<true>(map_a, map_b, p, grid, stream) : launch_tiled<false>(map_a, map_b, p, grid, stream);
+    switch (kind) {
+    case S8Kind::kFew16:
+        tsm_s8_few_kernel<1><<<unsigned(grid), 256, S8FewCfg<1>::SMEM_BYTES, stream>>>(map_a, map_b, p);
+        return cudaGetLastError();
+    case S8Kind::kFew32:
+        tsm_s8_few_kernel<2><<<unsigned(grid), 256, S8FewCfg<2>::SMEM_BYTES, stream>>>(map_a, map_b, p);
+        return cudaGetLastError();
+    case S8Kind::kOne: return launch_tiled<false>(map_a, map_b, p, grid, stream);
+    default: return launch_tiled<true>(map_a, map_b, p, 2 * grid, stream);
+    }
 }
 
 cudaError_t launch_pack_s8(const int8_t *src, int64_t s_ld, int64_t s_stride, int8_t *dst, int64_t d_ld,
