@@ -203,13 +203,15 @@ __device__ __forceinline__ S8Tile tile_at(int32_t t, const S8Params &p, uint32_t
 
 // Count one arrival on `word` (a whole warp calls it): true for the last of
 // `total`.  The word holds the launch's tag and the count; under another tag
-// (whatever the workspace's last user left there) the count is none.  A failed
+// (whatever the workspace's last user left there) the count is none.  The
+// first exchange expects everyone else to have arrived, so that the last one,
+// whom the result waits for, is done after one trip to L2.  Any other failed
 // exchange means that another of the at most `total` contributors has arrived,
 // so the loop ends.  The loop is the warp's, not one lane's, so that the
 // compiler need not plan for a warp that has come apart.
 __device__ __forceinline__ bool arrive_last(unsigned long long *word, unsigned long long tag, uint32_t total, int lane)
 {
-    unsigned long long old = __shfl_sync(0xffffffffu, ptx::ld_relaxed_gpu(word), 0);
+    unsigned long long old = (tag << 16) | (total - 1u);
     for (;;) {
         const uint32_t seen = (old >> 16) == tag ? uint32_t(old & 0xffffu) : 0u;
         unsigned long long prev = 0;
@@ -781,7 +783,7 @@ struct S8FewCfg {
     static constexpr int WARPS = 8, STAGES = 5;
     static constexpr int B_BYTES = BK * COLS, A_BYTES = ROWS * BK;
     static constexpr int SUMS = ROWS * COLS;  // [value of a lane][lane]
-    static constexpr int CTRL = 2048, GROUP_TABLE_OFF = 1024;
+    static constexpr int CTRL = 4096, GROUP_TABLE_OFF = 1024, TERMS_OFF = 2048;
     static constexpr int SMEM_BYTES = 1024 + WARPS * STAGES * (B_BYTES + A_BYTES) + SUMS * 4 + CTRL;
     static_assert(SMEM_BYTES <= 232448, "227 KiB per block");
     static constexpr int FLUSH = 1024 / BK;   // blocks whose sums f32 holds exactly
@@ -816,6 +818,8 @@ __global__ void __launch_bounds__(256, 1)
     const SharedSchedule<true> sched{ctrl + 400u};
     const uint32_t gtab = ctrl + Cfg::GROUP_TABLE_OFF;
     int32_t *const sums = reinterpret_cast<int32_t *>(base_ptr + SUMS0);
+    // The tile's column scales, biases and row scales.
+    float *const terms = reinterpret_cast<float *>(base_ptr + CTRL0 + Cfg::TERMS_OFF);
 
     const int warp = __shfl_sync(0xffffffffu, int(threadIdx.x >> 5), 0);
     const int lane = int(threadIdx.x & 31);
@@ -826,6 +830,10 @@ __global__ void __launch_bounds__(256, 1)
     const uint32_t ring_a = base + A0 + uint32_t(warp * S) * Cfg::A_BYTES;
 
     if (lane == 0) {
+        if (warp == 0) {
+            ptx::prefetch_tensormap(&map_a);
+            ptx::prefetch_tensormap(&map_b);
+        }
         for (int s = 0; s < S; ++s)
             ptx::mbar_init(full0 + 8u * s, 1);
         ptx::fence_mbar_init();
@@ -885,6 +893,19 @@ __global__ void __launch_bounds__(256, 1)
     uint32_t stage = 0, phase = 0;
     bool ok = true;
     for (PieceWalk<true> w(sched, worker); ok && w.advance(sched);) {
+        // The terms of the epilogue start on their way now: thread i < 128 for
+        // column i, the others for row i - 128 (and the columns' biases).
+        const S8Tile t = tile_at(w.tile, p, gtab, Cfg::ROWS, Cfg::COLS);
+        float term0 = p.epi.alpha, term1 = 0.f;
+        const int ti = int(threadIdx.x);
+        if (ti < 128) {
+            if (p.scale_b && t.n0 + ti < p.N)
+                term0 *= __ldg(p.scale_b + t.z * p.sb_stride + t.n0 + ti);
+            if (p.epi.bias && t.n0 + ti < p.N)
+                term1 = __ldg(p.epi.bias + t.z * p.epi.bias_stride + t.n0 + ti);
+        } else {
+            term0 = p.scale_a && ti - 128 < t.rows ? __ldg(p.scale_a + t.z * p.sa_stride + ti - 128) : 1.f;
+        }
         float acc[MT][16][4];
 #pragma unroll
         for (int m = 0; m < MT; ++m)
@@ -960,10 +981,12 @@ __global__ void __launch_bounds__(256, 1)
         }
         if (held)
             flush();
+        terms[ti] = term0;  // [columns' scales, rows' scales, columns' biases]
+        if (ti < 128)
+            terms[256 + ti] = term1;
         ok = __syncthreads_and(ok);  // the CTA's sums are complete, or all its warps give up
         if (!ok)
             break;
-        const S8Tile t = tile_at(w.tile, p, gtab, Cfg::ROWS, Cfg::COLS);
         bool mine = true;
         if (w.kb1 - w.kb0 < sched.kb()) {
             // A piece of a tile: as in the tiled kernel, with one part per tile.
@@ -1010,19 +1033,19 @@ __global__ void __launch_bounds__(256, 1)
         }
         if (mine) {
             // Four columns of a row per thread.
-            const int32_t col = t.n0 + 4 * lane;
-            float sb[4], bias[4];
-            column_terms(p, t.z, col, sb, bias);
+            const int c = 4 * lane;  // column 32 t + 16 d + j is value (j, d) of lane 4 (row % 8) + t
+            const float4 sb4 = *reinterpret_cast<const float4 *>(terms + c);
+            const float4 bias4 = *reinterpret_cast<const float4 *>(terms + 256 + c);
+            const float sb[4] = {sb4.x, sb4.y, sb4.z, sb4.w}, bias[4] = {bias4.x, bias4.y, bias4.z, bias4.w};
             for (int row = warp; row < t.rows; row += Cfg::WARPS) {
                 float o[4];
-                const float sa = p.scale_a ? __ldg(p.scale_a + t.z * p.sa_stride + row) : 1.f;
-                const int c = 4 * lane;  // column 32 t + 16 d + j of value (j, d) of lane 4 (row % 8) + t
+                const float sa = terms[128 + row];
 #pragma unroll
                 for (int k = 0; k < 4; ++k) {
                     const int j = (c + k) & 15, d = ((c >> 4) & 1) + 2 * ((row >> 3) & 1);
                     o[k] = float(sums[(((row >> 4) * 16 + j) * 4 + d) * 32 + 4 * (row & 7) + (c >> 5)]) * sa;
                 }
-                put4(p, t.z * p.sC + row * p.ldc + col, col, o, sb, bias);
+                put4(p, t.z * p.sC + row * p.ldc + t.n0 + c, t.n0 + c, o, sb, bias);
             }
         }
         __syncthreads();
