@@ -776,15 +776,19 @@ __global__ void __launch_bounds__(kS8Threads, 1)
 // k index 2t, 2t + 1, 2t + 8, 2t + 9 is row 4t, 4t + 1, 4t + 2, 4t + 3.
 //
 // A warp's f32 sums go into the CTA's 32-bit ones in shared memory (integer
-// atomics: any order gives the same sum) after at most 1024 k.
+// atomics: any order gives the same sum) after at most 1024 k.  There are two
+// sets of those: four more warps take a finished piece to C, or to the
+// workspace and the tile's other contributors, while the eight go on with the
+// next (done by the eight themselves, each piece's end stopped the reading of B
+// for three to five microseconds).
 template <int MT>
 struct S8FewCfg {
     static constexpr int ROWS = 16 * MT, COLS = 128, BK = 32;
-    static constexpr int WARPS = 8, STAGES = 5;
+    static constexpr int WARPS = 8, FINISHERS = 4, STAGES = MT == 1 ? 5 : 4;
     static constexpr int B_BYTES = BK * COLS, A_BYTES = ROWS * BK;
     static constexpr int SUMS = ROWS * COLS;  // [value of a lane][lane]
     static constexpr int CTRL = 4096, GROUP_TABLE_OFF = 1024, TERMS_OFF = 2048;
-    static constexpr int SMEM_BYTES = 1024 + WARPS * STAGES * (B_BYTES + A_BYTES) + SUMS * 4 + CTRL;
+    static constexpr int SMEM_BYTES = 1024 + WARPS * STAGES * (B_BYTES + A_BYTES) + 2 * SUMS * 4 + CTRL;
     static_assert(SMEM_BYTES <= 232448, "227 KiB per block");
     static constexpr int FLUSH = 1024 / BK;   // blocks whose sums f32 holds exactly
 };
@@ -798,8 +802,118 @@ __device__ __forceinline__ uint32_t code_pair(uint32_t lo, uint32_t hi)
     return *reinterpret_cast<const uint32_t *>(&x);
 }
 
+// The finishing warps: piece by piece, the CTA's sums through the epilogue into
+// C, or to the tile's other contributors.
 template <int MT>
-__global__ void __launch_bounds__(256, 1)
+__device__ __forceinline__ void few_rows_finish(const S8Params &p, const SharedSchedule<true> &sched, uint32_t gtab,
+                                                int32_t *sums0, float *terms, uint32_t sums_full0,
+                                                uint32_t sums_free0, uint32_t flag, uint32_t last_flag,
+                                                int32_t worker, int lane)
+{
+    using Cfg = S8FewCfg<MT>;
+    constexpr int FT = 32 * Cfg::FINISHERS;   // threads
+    constexpr int EACH = Cfg::SUMS / 4 / FT;  // 16-byte pieces of the sums per thread
+    const int ft = int(threadIdx.x) - 32 * Cfg::WARPS, fw = ft >> 5;
+    uint32_t set = 0, phase = 0;
+    for (PieceWalk<true> w(sched, worker); w.advance(sched);) {
+        const S8Tile t = tile_at(w.tile, p, gtab, Cfg::ROWS, Cfg::COLS);
+        int4 *const sums = reinterpret_cast<int4 *>(sums0 + set * Cfg::SUMS);
+        // The terms of the epilogue while the sums are on their way: thread i
+        // for column i and row i.
+        {
+            const bool in = t.n0 + ft < p.N;
+            float sb = p.epi.alpha, bias = 0.f, sa = 1.f;
+            if (p.scale_b && in)
+                sb *= __ldg(p.scale_b + t.z * p.sb_stride + t.n0 + ft);
+            if (p.epi.bias && in)
+                bias = __ldg(p.epi.bias + t.z * p.epi.bias_stride + t.n0 + ft);
+            if (p.scale_a && ft < t.rows)
+                sa = __ldg(p.scale_a + t.z * p.sa_stride + ft);
+            terms[ft] = sb;
+            terms[FT + ft] = bias;
+            terms[2 * FT + ft] = sa;
+        }
+        bool ok = s8_wait<false>(sums_full0 + 8u * set, phase, flag, p, kStatusEpilogue);
+        ok = __all_sync(0xffffffffu, ptx::named_bar_and(1, FT, ok));
+        if (!ok)
+            return;
+        bool finish = true;
+        if (w.kb1 - w.kb0 < sched.kb()) {
+            // A piece of a tile: as in the tiled kernel, with one part per tile.
+            const S8Schedule cut = sched.all();
+            const int32_t first = cut.owner(w.tile * cut.kb);
+            const int32_t last = cut.owner((w.tile + 1) * cut.kb - 1);
+            int4 *const slot = reinterpret_cast<int4 *>(p.partial + (2 * worker + (worker == first)) * Cfg::SUMS);
+            int4 own[EACH];
+#pragma unroll
+            for (int i = 0; i < EACH; ++i) {
+                own[i] = sums[i * FT + ft];
+                __stcg(slot + i * FT + ft, own[i]);
+            }
+            __threadfence();
+            ptx::named_bar_sync(1, FT);
+            if (fw == 0) {
+                const bool l = arrive_last(p.arrivals + w.tile, p.tag, uint32_t(last - first + 1), lane);
+                if (lane == 0)
+                    ptx::st_shared_u32(last_flag, l ? 1u : 0u);
+            }
+            ptx::named_bar_sync(1, FT);
+            finish = __any_sync(0xffffffffu, ptx::ld_shared_u32(last_flag) != 0);
+            __threadfence();
+            if (finish) {
+#pragma unroll 2
+                for (int32_t v = first; v <= last; ++v) {
+                    if (v == worker)
+                        continue;
+                    const int4 *theirs = reinterpret_cast<const int4 *>(p.partial + (2 * v + (v == first)) * Cfg::SUMS);
+#pragma unroll
+                    for (int i = 0; i < EACH; ++i) {
+                        const int4 y = __ldcg(theirs + i * FT + ft);
+                        own[i].x += y.x;
+                        own[i].y += y.y;
+                        own[i].z += y.z;
+                        own[i].w += y.w;
+                    }
+                }
+#pragma unroll
+                for (int i = 0; i < EACH; ++i)
+                    sums[i * FT + ft] = own[i];
+                ptx::named_bar_sync(1, FT);
+            }
+        }
+        if (finish) {
+            // Four columns of a row per thread.
+            const int c = 4 * lane;  // column 32 t + 16 d + j is value (j, d) of lane 4 (row % 8) + t
+            const float4 sb4 = *reinterpret_cast<const float4 *>(terms + c);
+            const float4 bias4 = *reinterpret_cast<const float4 *>(terms + FT + c);
+            const float sb[4] = {sb4.x, sb4.y, sb4.z, sb4.w}, bias[4] = {bias4.x, bias4.y, bias4.z, bias4.w};
+            const int32_t *const v = sums0 + set * Cfg::SUMS;
+            for (int row = fw; row < t.rows; row += Cfg::FINISHERS) {
+                float o[4];
+                const float sa = terms[2 * FT + row];
+#pragma unroll
+                for (int k = 0; k < 4; ++k) {
+                    const int j = (c + k) & 15, d = ((c >> 4) & 1) + 2 * ((row >> 3) & 1);
+                    o[k] = float(v[(((row >> 4) * 16 + j) * 4 + d) * 32 + 4 * (row & 7) + (c >> 5)]) * sa;
+                }
+                put4(p, t.z * p.sC + row * p.ldc + t.n0 + c, t.n0 + c, o, sb, bias);
+            }
+        }
+        ptx::named_bar_sync(1, FT);  // the sums and the terms have been read
+#pragma unroll
+        for (int i = 0; i < EACH; ++i)
+            sums[i * FT + ft] = make_int4(0, 0, 0, 0);
+        ptx::named_bar_sync(1, FT);
+        if (ft == 0)
+            ptx::mbar_arrive(sums_free0 + 8u * set);
+        set ^= 1u;
+        if (set == 0)
+            phase ^= 1u;
+    }
+}
+
+template <int MT>
+__global__ void __launch_bounds__(32 * (S8FewCfg<MT>::WARPS + S8FewCfg<MT>::FINISHERS), 1)
     tsm_s8_few_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ CUtensorMap map_b,
                       const S8Params p)
 {
@@ -811,13 +925,14 @@ __global__ void __launch_bounds__(256, 1)
     uint8_t *const base_ptr = smem_raw + (base - raw);
     constexpr uint32_t A0 = Cfg::WARPS * S * Cfg::B_BYTES;
     constexpr uint32_t SUMS0 = A0 + Cfg::WARPS * S * Cfg::A_BYTES;
-    constexpr uint32_t CTRL0 = SUMS0 + Cfg::SUMS * 4;
+    constexpr uint32_t CTRL0 = SUMS0 + 2 * Cfg::SUMS * 4;
     const uint32_t ctrl = base + CTRL0;
     const uint32_t flag = ctrl + 384u, last_flag = ctrl + 388u;  // (barriers: 8 warps x S x 8 bytes)
     static_assert(Cfg::WARPS * S * 8 <= 384, "control block");
     const SharedSchedule<true> sched{ctrl + 400u};
+    const uint32_t sums_full0 = ctrl + 432u, sums_free0 = ctrl + 448u;  // [2] each
     const uint32_t gtab = ctrl + Cfg::GROUP_TABLE_OFF;
-    int32_t *const sums = reinterpret_cast<int32_t *>(base_ptr + SUMS0);
+    int32_t *const sums0 = reinterpret_cast<int32_t *>(base_ptr + SUMS0);  // [2][SUMS]
     // The tile's column scales, biases and row scales.
     float *const terms = reinterpret_cast<float *>(base_ptr + CTRL0 + Cfg::TERMS_OFF);
 
@@ -829,10 +944,14 @@ __global__ void __launch_bounds__(256, 1)
     const uint32_t ring_b = base + uint32_t(warp * S) * Cfg::B_BYTES;
     const uint32_t ring_a = base + A0 + uint32_t(warp * S) * Cfg::A_BYTES;
 
-    if (lane == 0) {
+    if (lane == 0 && warp < Cfg::WARPS) {
         if (warp == 0) {
             ptx::prefetch_tensormap(&map_a);
             ptx::prefetch_tensormap(&map_b);
+            for (int i = 0; i < 2; ++i) {
+                ptx::mbar_init(sums_full0 + 8u * i, Cfg::WARPS);
+                ptx::mbar_init(sums_free0 + 8u * i, 1);
+            }
         }
         for (int s = 0; s < S; ++s)
             ptx::mbar_init(full0 + 8u * s, 1);
@@ -852,9 +971,19 @@ __global__ void __launch_bounds__(256, 1)
             sched.put(s);
         }
     }
-    for (int i = int(threadIdx.x); i < Cfg::SUMS; i += 256)
-        sums[i] = 0;
+    for (int i = int(threadIdx.x); i < 2 * Cfg::SUMS; i += int(blockDim.x))
+        sums0[i] = 0;
     __syncthreads();
+    // (The two-tile form needs more registers than an even share.)
+    if (warp >= Cfg::WARPS) {
+        if constexpr (MT == 2)
+            ptx::regs_dec<88>();
+        few_rows_finish<MT>(p, sched, gtab, sums0, terms, sums_full0, sums_free0, flag, last_flag, worker, lane);
+        return;
+    }
+
+    if constexpr (MT == 2)
+        ptx::regs_inc<208>();
 
     // The warp's loads run S blocks ahead of its MMAs, with a walk of their own.
     PieceWalk<true> wp(sched, worker);
@@ -890,22 +1019,11 @@ __global__ void __launch_bounds__(256, 1)
     for (uint32_t s = 0; s < uint32_t(S); ++s)
         issue(s);
 
-    uint32_t stage = 0, phase = 0;
+    uint32_t stage = 0, phase = 0, set = 0, set_phase = 0;
     bool ok = true;
     for (PieceWalk<true> w(sched, worker); ok && w.advance(sched);) {
-        // The terms of the epilogue start on their way now: thread i < 128 for
-        // column i, the others for row i - 128 (and the columns' biases).
-        const S8Tile t = tile_at(w.tile, p, gtab, Cfg::ROWS, Cfg::COLS);
-        float term0 = p.epi.alpha, term1 = 0.f;
-        const int ti = int(threadIdx.x);
-        if (ti < 128) {
-            if (p.scale_b && t.n0 + ti < p.N)
-                term0 *= __ldg(p.scale_b + t.z * p.sb_stride + t.n0 + ti);
-            if (p.epi.bias && t.n0 + ti < p.N)
-                term1 = __ldg(p.epi.bias + t.z * p.epi.bias_stride + t.n0 + ti);
-        } else {
-            term0 = p.scale_a && ti - 128 < t.rows ? __ldg(p.scale_a + t.z * p.sa_stride + ti - 128) : 1.f;
-        }
+        int32_t *const sums = sums0 + set * Cfg::SUMS;
+        bool mine = false;  // the set is this piece's
         float acc[MT][16][4];
 #pragma unroll
         for (int m = 0; m < MT; ++m)
@@ -914,7 +1032,15 @@ __global__ void __launch_bounds__(256, 1)
 #pragma unroll
                 for (int d = 0; d < 4; ++d)
                     acc[m][j][d] = 0.f;
+        auto take = [&]() {  // the set's last piece has left it
+            if (!mine)
+                ok = __all_sync(0xffffffffu, s8_wait<false>(sums_free0 + 8u * set, set_phase ^ 1u, flag, p, kStatusReduce));
+            mine = true;
+            return ok;
+        };
         auto flush = [&]() {
+            if (!take())
+                return;
 #pragma unroll
             for (int m = 0; m < MT; ++m)
 #pragma unroll
@@ -977,81 +1103,22 @@ __global__ void __launch_bounds__(256, 1)
             if (++held == Cfg::FLUSH) {
                 flush();
                 held = 0;
+                if (!ok)
+                    break;
             }
         }
-        if (held)
+        if (ok && held)
             flush();
-        terms[ti] = term0;  // [columns' scales, rows' scales, columns' biases]
-        if (ti < 128)
-            terms[256 + ti] = term1;
-        ok = __syncthreads_and(ok);  // the CTA's sums are complete, or all its warps give up
-        if (!ok)
+        // (A warp without a block in the piece waits for the set, too, before
+        // it arrives: it could otherwise arrive twice in one phase.)
+        if (!ok || !take())
             break;
-        bool mine = true;
-        if (w.kb1 - w.kb0 < sched.kb()) {
-            // A piece of a tile: as in the tiled kernel, with one part per tile.
-            const S8Schedule cut = sched.all();
-            const int32_t first = cut.owner(w.tile * cut.kb);
-            const int32_t last = cut.owner((w.tile + 1) * cut.kb - 1);
-            int32_t *const slot = p.partial + (2 * worker + (worker == first)) * Cfg::SUMS;
-            int4 own[2 * MT];
-#pragma unroll
-            for (int i = 0; i < 2 * MT; ++i) {
-                own[i] = reinterpret_cast<const int4 *>(sums)[i * 256 + threadIdx.x];
-                __stcg(reinterpret_cast<int4 *>(slot) + i * 256 + threadIdx.x, own[i]);
-            }
-            __threadfence();
-            __syncthreads();
-            if (warp == 0) {
-                const bool l = arrive_last(p.arrivals + w.tile, p.tag, uint32_t(last - first + 1), lane);
-                if (lane == 0)
-                    ptx::st_shared_u32(last_flag, l ? 1u : 0u);
-            }
-            __syncthreads();
-            mine = ptx::ld_shared_u32(last_flag) != 0;
-            __threadfence();
-            if (mine) {
-#pragma unroll 4
-                for (int32_t v = first; v <= last; ++v) {
-                    if (v == worker)
-                        continue;
-                    const int4 *theirs = reinterpret_cast<const int4 *>(p.partial + (2 * v + (v == first)) * Cfg::SUMS);
-#pragma unroll
-                    for (int i = 0; i < 2 * MT; ++i) {
-                        const int4 y = __ldcg(theirs + i * 256 + threadIdx.x);
-                        own[i].x += y.x;
-                        own[i].y += y.y;
-                        own[i].z += y.z;
-                        own[i].w += y.w;
-                    }
-                }
-#pragma unroll
-                for (int i = 0; i < 2 * MT; ++i)
-                    reinterpret_cast<int4 *>(sums)[i * 256 + threadIdx.x] = own[i];
-                __syncthreads();
-            }
-        }
-        if (mine) {
-            // Four columns of a row per thread.
-            const int c = 4 * lane;  // column 32 t + 16 d + j is value (j, d) of lane 4 (row % 8) + t
-            const float4 sb4 = *reinterpret_cast<const float4 *>(terms + c);
-            const float4 bias4 = *reinterpret_cast<const float4 *>(terms + 256 + c);
-            const float sb[4] = {sb4.x, sb4.y, sb4.z, sb4.w}, bias[4] = {bias4.x, bias4.y, bias4.z, bias4.w};
-            for (int row = warp; row < t.rows; row += Cfg::WARPS) {
-                float o[4];
-                const float sa = terms[128 + row];
-#pragma unroll
-                for (int k = 0; k < 4; ++k) {
-                    const int j = (c + k) & 15, d = ((c >> 4) & 1) + 2 * ((row >> 3) & 1);
-                    o[k] = float(sums[(((row >> 4) * 16 + j) * 4 + d) * 32 + 4 * (row & 7) + (c >> 5)]) * sa;
-                }
-                put4(p, t.z * p.sC + row * p.ldc + t.n0 + c, t.n0 + c, o, sb, bias);
-            }
-        }
-        __syncthreads();
-        for (int i = int(threadIdx.x); i < Cfg::SUMS; i += 256)
-            sums[i] = 0;
-        __syncthreads();
+        __syncwarp();
+        if (lane == 0)
+            ptx::mbar_arrive(sums_full0 + 8u * set);
+        set ^= 1u;
+        if (set == 0)
+            set_phase ^= 1u;
     }
     // No TMA write into shared memory outlives the CTA.
     for (; issued > 0; --issued) {
@@ -1170,10 +1237,10 @@ cudaError_t launch_s8(const CUtensorMap &map_a, const CUtensorMap &map_b, const 
 {
     switch (kind) {
     case S8Kind::kFew16:
-        tsm_s8_few_kernel<1><<<unsigned(grid), 256, S8FewCfg<1>::SMEM_BYTES, stream>>>(map_a, map_b, p);
+        tsm_s8_few_kernel<1><<<unsigned(grid), 384, S8FewCfg<1>::SMEM_BYTES, stream>>>(map_a, map_b, p);
         return cudaGetLastError();
     case S8Kind::kFew32:
-        tsm_s8_few_kernel<2><<<unsigned(grid), 256, S8FewCfg<2>::SMEM_BYTES, stream>>>(map_a, map_b, p);
+        tsm_s8_few_kernel<2><<<unsigned(grid), 384, S8FewCfg<2>::SMEM_BYTES, stream>>>(map_a, map_b, p);
         return cudaGetLastError();
     case S8Kind::kOne: return launch_tiled<false>(map_a, map_b, p, grid, stream);
     default: return launch_tiled<true>(map_a, map_b, p, 2 * grid, stream);
