@@ -382,8 +382,37 @@ bool addressable(const int8_t *x, int64_t ld, int64_t stride, int64_t rows, int6
     return !misaligned(x, 16) && (rows == 1 || ld % 16 == 0) && (batch == 1 || stride % 16 == 0);
 }
 
-std::once_flag g_s8_attr_once[64];
-cudaError_t g_s8_attr[64];
+std::once_flag g_s8_once[64];
+cudaError_t g_s8_error[64];
+S8Capacity g_s8_capacity[64];
+
+// CTAs per cluster of a few-rows launch: the least estimated time over 1, 2, 4
+// and 8.  A CTA's rate is its share of the memory's, or what its warps can
+// multiply if that is less; a cluster waits for its slowest CTA, the launch
+// for the fullest cluster; passing the sums between CTAs costs about 1 us.
+int few_rows_ranks(int64_t tiles, int32_t kb, const S8Capacity &cap, bool two, int *clusters)
+{
+    const double block = 8192.0;                   // bytes of 32 k x 256 columns
+    const double memory = 6.0e6;                   // bytes per us, all CTAs
+    const double most = two ? 38.0e3 : 52.0e3;     // bytes per us, one CTA
+    int best = 1;
+    double best_us = 0.0;
+    for (int i = 0; i < S8Capacity::KINDS; ++i) {
+        const int ranks = 1 << i;
+        if (cap.clusters[i] <= 0 || (i > 0 && ranks > kb))
+            continue;
+        const int64_t n = std::min<int64_t>(tiles, cap.clusters[i]);
+        const double rate = std::min(most, memory / double(n * ranks));
+        const double blocks = double((tiles + n - 1) / n) * double((kb + ranks - 1) / ranks);
+        const double us = blocks * block / rate + (ranks > 1 ? 1.0 : 0.0);
+        if (i == 0 || us < best_us) {
+            best = ranks;
+            best_us = us;
+            *clusters = int(n);
+        }
+    }
+    return best;
+}
 
 // All checks are done and every size is positive (K may be 0).
 gemm_status_t launch_product(S8Params p, DeviceState *ds, cudaStream_t stream)
@@ -398,9 +427,9 @@ gemm_status_t launch_product(S8Params p, DeviceState *ds, cudaStream_t stream)
     int dev = 0;
     if ((e = cudaGetDevice(&dev)) != cudaSuccess)
         return fail_cuda(e, "cudaGetDevice");
-    std::call_once(g_s8_attr_once[dev], [dev] { g_s8_attr[dev] = set_s8_attributes(); });
-    if (g_s8_attr[dev] != cudaSuccess)
-        return fail_cuda(g_s8_attr[dev], "cudaFuncSetAttribute(int8 product)");
+    std::call_once(g_s8_once[dev], [dev] { g_s8_error[dev] = set_s8_attributes(&g_s8_capacity[dev]); });
+    if (g_s8_error[dev] != cudaSuccess)
+        return fail_cuda(g_s8_error[dev], "setting up the int8 product kernels");
 
     const S8Kind kind = p.M <= 16 ? S8Kind::kFew16 : p.M <= 32 ? S8Kind::kFew32
                         : p.M <= 128 ? S8Kind::kOne : S8Kind::kPair;
@@ -426,10 +455,19 @@ gemm_status_t launch_product(S8Params p, DeviceState *ds, cudaStream_t stream)
     const int64_t tiles = int64_t(p.tiles_m) * p.tiles_n * p.batch;
     if (tiles > S8Schedule::kMaxTiles)
         return fail(GEMM_ERR_INVALID_VALUE, "more than 2^30 output tiles in one call");
-    S8Schedule sched;
-    sched.plan(int32_t(tiles), p.kb, p.workers, few ? S8Schedule::kFewRows : S8Schedule::kTiled);
+    S8Schedule sched = {};
+    int grid = 0;
+    if (few) {
+        // (A grouped launch's tiles are counted on the device: at most these.)
+        p.ranks = few_rows_ranks(tiles, p.kb, g_s8_capacity[dev], kind == S8Kind::kFew32, &grid);
+    } else {
+        sched.plan(int32_t(tiles), p.kb, p.workers);
+        grid = p.group_rows ? p.workers
+                            : int(std::max<int64_t>(sched.shared ? sched.cutters : 0,
+                                                    std::min<int64_t>(sched.tiles, p.workers)));
+    }
     // (A grouped launch's tiles are counted on the device: any number up to these.)
-    const int64_t cut = p.group_rows ? 2 * int64_t(p.workers) : sched.shared;
+    const int64_t cut = few ? 0 : p.group_rows ? 2 * int64_t(p.workers) : sched.shared;
     const int64_t bytes_p = cut ? 2 * int64_t(p.workers) * shape.slot_bytes : 0;
     const int64_t bytes_w = cut * shape.parts * 8;
     char *ws = nullptr;
@@ -481,10 +519,7 @@ gemm_status_t launch_product(S8Params p, DeviceState *ds, cudaStream_t stream)
         st = encode_3d(&map_b, CU_TENSOR_MAP_DATA_TYPE_UINT8, 1, p.B, p.N, p.K, p.batch, ldb, sB, 128, uint32_t(shape.block_k),
                        CU_TENSOR_MAP_L2_PROMOTION_L2_256B, "B");
     if (st == GEMM_OK) {
-        const int64_t most = p.group_rows ? p.workers
-                                          : std::max<int64_t>(sched.shared ? sched.cutters : 0,
-                                                              std::min<int64_t>(sched.tiles, p.workers));
-        e = launch_s8(map_a, map_b, p, kind, int(most), stream);
+        e = launch_s8(map_a, map_b, p, kind, grid, stream);
         if (e != cudaSuccess)
             st = fail_cuda(e, "int8 product launch");
     }

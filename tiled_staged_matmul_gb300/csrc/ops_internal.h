@@ -60,7 +60,7 @@ cudaError_t launch_quantize_rows(const QuantParams &p, int elem, bool vec, cudaS
 
 // ------------------------------------------------------------- int8 products
 
-// The work of one launch: `tiles` output tiles of `kb` k-blocks each, spread
+// The work of one tiled launch: `tiles` output tiles of `kb` k-blocks each, spread
 // over `workers` CTAs (or CTA pairs).  As many whole waves of tiles as leave
 // between one and two waves over run tile by tile; the tiles left over (the
 // first `shared` ones) are cut as one long row of shared * kb blocks into
@@ -74,28 +74,20 @@ struct S8Schedule {
     int32_t workers;        // of the whole tiles
     int32_t cutters;        // workers that get a piece
     static constexpr int32_t kMaxTiles = 1 << 30;
-    enum { kTiled, kFewRows };
 
-    __host__ __device__ void plan(int32_t tiles_, int32_t kb_, int32_t workers_, int kind)
+    __host__ __device__ void plan(int32_t tiles_, int32_t kb_, int32_t workers_)
     {
         tiles = tiles_;
         kb = kb_;
         workers = workers_;
         const int32_t over = tiles % workers;
         shared = over == 0 ? 0 : tiles < workers ? tiles : over + workers;
-        int32_t pieces;
-        if (kind == kTiled) {
-            // A tile's contributors: as many as balance the blocks each
-            // multiplies with the sums the last one adds up, about two blocks'
-            // time apiece.
-            int32_t each = 1;
-            while (2 * each * each < kb)
-                ++each;
-            pieces = shared * each;
-        } else {
-            // The sums are small: at least a block per warp.
-            pieces = (shared * kb + 7) / 8;
-        }
+        // A tile's contributors: as many as balance the blocks each multiplies
+        // with the sums the last one adds up, about two blocks' time apiece.
+        int32_t each = 1;
+        while (2 * each * each < kb)
+            ++each;
+        const int32_t pieces = shared * each;
         cutters = pieces < 1 ? 1 : pieces < workers ? pieces : workers;
     }
     // First block of worker w's piece (w <= cutters).
@@ -121,13 +113,14 @@ struct S8Params {
     int32_t tiles_m, tiles_n, kb;
     int32_t group_m;            // raster: tiles of M walked together
     int32_t workers;
+    int32_t ranks;              // few rows: CTAs (a cluster) that cut a tile's K
     int32_t vec_c;              // C's rows take stores of four elements
     int32_t *partial;           // sums of pieces: two slots per worker
     unsigned long long *arrivals;  // one word per part of a shared tile: launch tag, count
     unsigned long long tag;     // 48 bits, unique to the launch
 };
 
-// The kernels: few rows (up to 16 or 32, 128 columns a tile); tiled, one CTA per
+// The kernels: few rows (up to 16 or 32, 256 columns a tile); tiled, one CTA per
 // 128 x 128 tile or a CTA pair per 256 x 256.
 enum class S8Kind { kFew16, kFew32, kOne, kPair };
 struct S8Shape {
@@ -136,7 +129,12 @@ struct S8Shape {
     int parts;                  // arrival words per tile
 };
 S8Shape s8_shape(S8Kind kind);
-cudaError_t set_s8_attributes();
+// Clusters of 1, 2, 4 and 8 CTAs of the few-rows kernels that fit on the device at once.
+struct S8Capacity {
+    static constexpr int KINDS = 4;
+    int clusters[KINDS];
+};
+cudaError_t set_s8_attributes(S8Capacity *cap);
 cudaError_t launch_s8(const CUtensorMap &map_a, const CUtensorMap &map_b, const S8Params &p, S8Kind kind, int grid,
                       cudaStream_t stream);
 // Rows of `cols` bytes into rows 16-byte aligned and `d_ld` apart.

@@ -441,8 +441,7 @@ __global__ void __launch_bounds__(kS8Threads, 1)
     }
     if (warp == 2 && lane == 0) {
         S8Schedule s;
-        s.plan(p.group_rows ? int32_t(ptx::ld_shared_u32(gtab + 4u * (p.batch - 1))) : p.tiles_m * p.tiles_n * p.batch, p.kb, p.workers,
-               S8Schedule::kTiled);
+        s.plan(p.group_rows ? int32_t(ptx::ld_shared_u32(gtab + 4u * (p.batch - 1))) : p.tiles_m * p.tiles_n * p.batch, p.kb, p.workers);
         sched.put(s);
     }
     ptx::tc_fence_before_sync();
@@ -761,36 +760,47 @@ __global__ void __launch_bounds__(kS8Threads, 1)
 // ------------------------------------------------------------- few rows
 //
 // Up to 32 rows of A (a decode step): the product reads every code of B once
-// and is bound by that.  Eight independent warps per CTA, each with a ring of
-// its own that TMA fills with 32 k x 128 columns of B (4 KiB) and the rows' 32
-// k of A, 160 KiB in flight per SM; no warp waits for another until a piece
-// ends.  Warp-wide f16 MMAs (16 rows x 8 columns x 16 k) run far below the
-// tcgen05 rate, but 16 or 32 rows need no more: one SM's share of the memory
-// rate is 23 codes a cycle, 16 x 23 multiply-adds.
+// and is bound by that.  A tile is 256 columns; its K is cut over the CTAs of a
+// cluster (1, 2, 4 or 8 of them, by a time model on the host).  In a CTA,
+// independent warps in pairs take 32 k of the tile at a time, one warp for each
+// 128 columns, so that a row of B is read 256 bytes at a time (reading 128
+// bytes of it ran at 4.6 TB/s, 256 at 6.0, 512 no faster).  Each warp has a TMA
+// ring of its own and never waits for another.
 //
-// B's codes go from shared memory to the MMA's operand layout in registers:
-// lane 4g + t takes 16 columns (chunk g) of rows 4t ... 4t + 3, and a byte of
-// two rows each makes the f16 pair that it has to hold for one column.  Which
-// columns and which k a lane's registers stand for is free as long as A's
-// lanes agree, so no transpose is needed: MMA j of 16 gets column 16 g + j, and
-// k index 2t, 2t + 1, 2t + 8, 2t + 9 is row 4t, 4t + 1, 4t + 2, 4t + 3.
+// Warp-wide f16 MMAs (16 rows x 8 columns x 16 k) run far below the tcgen05
+// rate, but 16 or 32 rows need no more: one SM's share of the memory rate is 23
+// codes a cycle, 16 x 23 multiply-adds.  B's codes go from shared memory to the
+// MMA's operand layout in registers: lane 4g + t takes 16 columns (chunk g) of
+// rows 4t ... 4t + 3, and a byte of two rows each makes the f16 pair that it
+// has to hold for one column.  Which columns and which k a lane's registers
+// stand for is free as long as A's lanes agree, so no transpose is needed: MMA
+// j of 16 gets column 16 g + j, and k index 2t, 2t + 1, 2t + 8, 2t + 9 is row
+// 4t, 4t + 1, 4t + 2, 4t + 3.
 //
 // A warp's f32 sums go into the CTA's 32-bit ones in shared memory (integer
 // atomics: any order gives the same sum) after at most 1024 k.  There are two
-// sets of those: four more warps take a finished piece to C, or to the
-// workspace and the tile's other contributors, while the eight go on with the
-// next (done by the eight themselves, each piece's end stopped the reading of B
-// for three to five microseconds).
+// sets of those: four more warps take a finished tile on while the others go on
+// with the next.  Each CTA of the cluster finishes its share of the columns: it
+// adds up that share of every CTA's sums through distributed shared memory, so
+// nothing passes through the workspace (which, with its fences and arrivals,
+// cost a tile's end three to five microseconds, this about one).
 template <int MT>
 struct S8FewCfg {
-    static constexpr int ROWS = 16 * MT, COLS = 128, BK = 32;
-    static constexpr int WARPS = 8, FINISHERS = 4, STAGES = MT == 1 ? 5 : 4;
-    static constexpr int B_BYTES = BK * COLS, A_BYTES = ROWS * BK;
-    static constexpr int SUMS = ROWS * COLS;  // [value of a lane][lane]
-    static constexpr int CTRL = 4096, GROUP_TABLE_OFF = 1024, TERMS_OFF = 2048;
+    static constexpr int ROWS = 16 * MT, COLS = 256, BK = 32;
+    static constexpr int WARPS = MT == 1 ? 16 : 8, FINISHERS = 4, STAGES = MT == 1 ? 2 : 3;
+    static constexpr int THREADS = 32 * (WARPS + FINISHERS);
+    static constexpr int KWARPS = WARPS / 2;  // warps along k
+    static constexpr int B_BYTES = BK * 128, A_BYTES = ROWS * BK;
+    static constexpr int HALF_SUMS = ROWS * 128;  // of 128 columns: [value of a lane][lane]
+    static constexpr int SUMS = 2 * HALF_SUMS;
+    static constexpr int CTRL = 6144, GROUP_TABLE_OFF = 1024, TERMS_OFF = 2048;
     static constexpr int SMEM_BYTES = 1024 + WARPS * STAGES * (B_BYTES + A_BYTES) + 2 * SUMS * 4 + CTRL;
-    static_assert(SMEM_BYTES <= 232448, "227 KiB per block");
+    static_assert(SMEM_BYTES <= 232448 && SMEM_BYTES > 232448 / 2, "227 KiB per block, one block per SM");
     static constexpr int FLUSH = 1024 / BK;   // blocks whose sums f32 holds exactly
+    // Registers by role: the MMA warps' accumulators need more than an even share.
+    static constexpr int LAUNCH_REGS = MT == 1 ? 96 : 168;
+    static constexpr int MMA_REGS = MT == 1 ? 104 : 208, FINISH_REGS = MT == 1 ? 64 : 88;
+    static_assert(32 * (WARPS * MMA_REGS + FINISHERS * FINISH_REGS) <= THREADS * LAUNCH_REGS, "register split");
 };
 
 // Column pair of a byte column: f16(lo.byte b), f16(hi.byte b).
@@ -802,228 +812,171 @@ __device__ __forceinline__ uint32_t code_pair(uint32_t lo, uint32_t hi)
     return *reinterpret_cast<const uint32_t *>(&x);
 }
 
-// The finishing warps: piece by piece, the CTA's sums through the epilogue into
-// C, or to the tile's other contributors.
+// Where value (j, d) of row block m of a lane's accumulator is kept among a
+// half's sums: 32 lanes together, in an order that lets the lanes that finish
+// 128 columns of one row read different banks.
+__device__ __forceinline__ int few_rows_sum(int m, int j, int d, int lane)
+{
+    return ((m * 16 + j) * 4 + d) * 32 + (lane ^ (4 * (2 * (j >> 2) + (d & 1))));
+}
+
+// A CTA's addresses and place in the launch.
+struct FewPlace {
+    uint32_t sums0, terms0;                       // shared memory: [2][SUMS] ints; scales and biases
+    uint32_t sums_full0, sums_free0, ready0, taken0;  // barriers, [2] each
+    uint32_t flag, gtab;
+    int32_t tiles, cluster, clusters, rank, ranks;
+};
+
+// The finishing warps: tile by tile, the cluster's sums of this CTA's share of
+// the columns through the epilogue into C.
 template <int MT>
-__device__ __forceinline__ void few_rows_finish(const S8Params &p, const SharedSchedule<true> &sched, uint32_t gtab,
-                                                int32_t *sums0, float *terms, uint32_t sums_full0,
-                                                uint32_t sums_free0, uint32_t flag, uint32_t last_flag,
-                                                int32_t worker, int lane)
+__device__ __forceinline__ void few_rows_finish(const S8Params &p, const FewPlace &f, int lane)
 {
     using Cfg = S8FewCfg<MT>;
-    constexpr int FT = 32 * Cfg::FINISHERS;   // threads
-    constexpr int EACH = Cfg::SUMS / 4 / FT;  // 16-byte pieces of the sums per thread
+    constexpr int FT = 32 * Cfg::FINISHERS;
     const int ft = int(threadIdx.x) - 32 * Cfg::WARPS, fw = ft >> 5;
+    const uint32_t sb0 = f.terms0, bias0 = f.terms0 + 4u * Cfg::COLS, sa0 = f.terms0 + 8u * Cfg::COLS;
+    const int share = Cfg::COLS / f.ranks, c0 = f.rank * share;  // this CTA's columns of a tile
     uint32_t set = 0, phase = 0;
-    for (PieceWalk<true> w(sched, worker); w.advance(sched);) {
-        const S8Tile t = tile_at(w.tile, p, gtab, Cfg::ROWS, Cfg::COLS);
-        int4 *const sums = reinterpret_cast<int4 *>(sums0 + set * Cfg::SUMS);
-        // The terms of the epilogue while the sums are on their way: thread i
-        // for column i and row i.
-        {
-            const bool in = t.n0 + ft < p.N;
-            float sb = p.epi.alpha, bias = 0.f, sa = 1.f;
-            if (p.scale_b && in)
-                sb *= __ldg(p.scale_b + t.z * p.sb_stride + t.n0 + ft);
-            if (p.epi.bias && in)
-                bias = __ldg(p.epi.bias + t.z * p.epi.bias_stride + t.n0 + ft);
-            if (p.scale_a && ft < t.rows)
-                sa = __ldg(p.scale_a + t.z * p.sa_stride + ft);
-            terms[ft] = sb;
-            terms[FT + ft] = bias;
-            terms[2 * FT + ft] = sa;
+    for (int32_t tile = f.cluster; tile < f.tiles; tile += f.clusters) {
+        const S8Tile t = tile_at(tile, p, f.gtab, Cfg::ROWS, Cfg::COLS);
+        // The terms of the epilogue while the sums are on their way.
+        for (int c = ft; c < share; c += FT) {
+            const int32_t col = t.n0 + c0 + c;
+            float sb = p.epi.alpha, bias = 0.f;
+            if (p.scale_b && col < p.N)
+                sb *= __ldg(p.scale_b + t.z * p.sb_stride + col);
+            if (p.epi.bias && col < p.N)
+                bias = __ldg(p.epi.bias + t.z * p.epi.bias_stride + col);
+            ptx::st_shared_u32(sb0 + 4u * c, __float_as_uint(sb));
+            ptx::st_shared_u32(bias0 + 4u * c, __float_as_uint(bias));
         }
-        bool ok = s8_wait<false>(sums_full0 + 8u * set, phase, flag, p, kStatusEpilogue);
+        if (ft < Cfg::ROWS)
+            ptx::st_shared_u32(sa0 + 4u * ft, __float_as_uint(p.scale_a && ft < t.rows
+                                                                  ? __ldg(p.scale_a + t.z * p.sa_stride + ft) : 1.f));
+        const uint32_t sums = f.sums0 + set * uint32_t(Cfg::SUMS * 4);
+        bool ok = s8_wait<false>(f.sums_full0 + 8u * set, phase, f.flag, p, kStatusEpilogue);
         ok = __all_sync(0xffffffffu, ptx::named_bar_and(1, FT, ok));
         if (!ok)
             return;
-        bool finish = true;
-        if (w.kb1 - w.kb0 < sched.kb()) {
-            // A piece of a tile: as in the tiled kernel, with one part per tile.
-            const S8Schedule cut = sched.all();
-            const int32_t first = cut.owner(w.tile * cut.kb);
-            const int32_t last = cut.owner((w.tile + 1) * cut.kb - 1);
-            int4 *const slot = reinterpret_cast<int4 *>(p.partial + (2 * worker + (worker == first)) * Cfg::SUMS);
-            int4 own[EACH];
+        if (f.ranks > 1) {
+            // This CTA's sums are complete: so says one thread to every CTA.
+            if (ft < f.ranks)
+                ptx::mbar_arrive_cluster(ptx::mapa_shared(f.ready0 + 8u * set, uint32_t(ft)));
+            ok = s8_wait<false, true>(f.ready0 + 8u * set, phase, f.flag, p, kStatusReduce);
+            ok = __all_sync(0xffffffffu, ptx::named_bar_and(1, FT, ok));
+            if (!ok)
+                return;
+        }
+        // Four columns of a row per thread.  Column 128 h + 32 t + 16 d + j is
+        // value (j, d) of lane 4 (row % 8) + t of half h.
+        const int quads = share / 4;
+        for (int i = ft; i < t.rows * quads; i += FT) {
+            const int row = i / quads, c = 4 * (i - row * quads);
+            const int32_t col = t.n0 + c0 + c;
+            if (col >= p.N)
+                continue;
+            const int in = c0 + c, h = in >> 7, d = ((in >> 4) & 1) + 2 * ((row >> 3) & 1);
+            const uint32_t at = sums + 4u * uint32_t(h * Cfg::HALF_SUMS + few_rows_sum(row >> 4, in & 15, d,
+                                                                                       4 * (row & 7) + ((in >> 5) & 3)));
+            int32_t v[4] = {};
+            if (f.ranks == 1) {
 #pragma unroll
-            for (int i = 0; i < EACH; ++i) {
-                own[i] = sums[i * FT + ft];
-                __stcg(slot + i * FT + ft, own[i]);
-            }
-            __threadfence();
-            ptx::named_bar_sync(1, FT);
-            if (fw == 0) {
-                const bool l = arrive_last(p.arrivals + w.tile, p.tag, uint32_t(last - first + 1), lane);
-                if (lane == 0)
-                    ptx::st_shared_u32(last_flag, l ? 1u : 0u);
-            }
-            ptx::named_bar_sync(1, FT);
-            finish = __any_sync(0xffffffffu, ptx::ld_shared_u32(last_flag) != 0);
-            __threadfence();
-            if (finish) {
+                for (int k = 0; k < 4; ++k)
+                    v[k] = int32_t(ptx::ld_shared_u32(at + 512u * k));
+            } else {
 #pragma unroll 2
-                for (int32_t v = first; v <= last; ++v) {
-                    if (v == worker)
-                        continue;
-                    const int4 *theirs = reinterpret_cast<const int4 *>(p.partial + (2 * v + (v == first)) * Cfg::SUMS);
+                for (int r = 0; r < f.ranks; ++r) {
+                    const uint32_t there = ptx::mapa_shared(at, uint32_t(r));
 #pragma unroll
-                    for (int i = 0; i < EACH; ++i) {
-                        const int4 y = __ldcg(theirs + i * FT + ft);
-                        own[i].x += y.x;
-                        own[i].y += y.y;
-                        own[i].z += y.z;
-                        own[i].w += y.w;
-                    }
+                    for (int k = 0; k < 4; ++k)
+                        v[k] += int32_t(ptx::ld_cluster_u32(there + 512u * k));
                 }
-#pragma unroll
-                for (int i = 0; i < EACH; ++i)
-                    sums[i * FT + ft] = own[i];
-                ptx::named_bar_sync(1, FT);
             }
-        }
-        if (finish) {
-            // Four columns of a row per thread.
-            const int c = 4 * lane;  // column 32 t + 16 d + j is value (j, d) of lane 4 (row % 8) + t
-            const float4 sb4 = *reinterpret_cast<const float4 *>(terms + c);
-            const float4 bias4 = *reinterpret_cast<const float4 *>(terms + FT + c);
-            const float sb[4] = {sb4.x, sb4.y, sb4.z, sb4.w}, bias[4] = {bias4.x, bias4.y, bias4.z, bias4.w};
-            const int32_t *const v = sums0 + set * Cfg::SUMS;
-            for (int row = fw; row < t.rows; row += Cfg::FINISHERS) {
-                float o[4];
-                const float sa = terms[2 * FT + row];
+            const float sa = __uint_as_float(ptx::ld_shared_u32(sa0 + 4u * row));
+            const uint4 s4 = ptx::ld_shared_v4(sb0 + 4u * c), b4 = ptx::ld_shared_v4(bias0 + 4u * c);
+            const float sb[4] = {__uint_as_float(s4.x), __uint_as_float(s4.y), __uint_as_float(s4.z), __uint_as_float(s4.w)};
+            const float bias[4] = {__uint_as_float(b4.x), __uint_as_float(b4.y), __uint_as_float(b4.z), __uint_as_float(b4.w)};
+            float o[4];
 #pragma unroll
-                for (int k = 0; k < 4; ++k) {
-                    const int j = (c + k) & 15, d = ((c >> 4) & 1) + 2 * ((row >> 3) & 1);
-                    o[k] = float(v[(((row >> 4) * 16 + j) * 4 + d) * 32 + 4 * (row & 7) + (c >> 5)]) * sa;
-                }
-                put4(p, t.z * p.sC + row * p.ldc + t.n0 + c, t.n0 + c, o, sb, bias);
-            }
+            for (int k = 0; k < 4; ++k)
+                o[k] = float(v[k]) * sa;
+            put4(p, t.z * p.sC + row * p.ldc + col, col, o, sb, bias);
         }
-        ptx::named_bar_sync(1, FT);  // the sums and the terms have been read
-#pragma unroll
-        for (int i = 0; i < EACH; ++i)
-            sums[i * FT + ft] = make_int4(0, 0, 0, 0);
+        ptx::named_bar_sync(1, FT);  // the sums and the terms have been read here
+        if (f.ranks > 1) {
+            // ... and in every CTA of the cluster, before they are cleared.
+            if (ft < f.ranks)
+                ptx::mbar_arrive_cluster(ptx::mapa_shared(f.taken0 + 8u * set, uint32_t(ft)));
+            ok = s8_wait<false, true>(f.taken0 + 8u * set, phase, f.flag, p, kStatusReduce);
+            ok = __all_sync(0xffffffffu, ptx::named_bar_and(1, FT, ok));
+            if (!ok)
+                return;
+        }
+        for (int i = ft; i < Cfg::SUMS / 4; i += FT)
+            ptx::st_shared_v4(sums + 16u * i, 0u, 0u, 0u, 0u);
         ptx::named_bar_sync(1, FT);
         if (ft == 0)
-            ptx::mbar_arrive(sums_free0 + 8u * set);
+            ptx::mbar_arrive(f.sums_free0 + 8u * set);
         set ^= 1u;
         if (set == 0)
             phase ^= 1u;
     }
 }
 
+// The multiplying warps.
 template <int MT>
-__global__ void __launch_bounds__(32 * (S8FewCfg<MT>::WARPS + S8FewCfg<MT>::FINISHERS), 1)
-    tsm_s8_few_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ CUtensorMap map_b,
-                      const S8Params p)
+__device__ __forceinline__ void few_rows_multiply(const CUtensorMap &map_a, const CUtensorMap &map_b,
+                                                  const S8Params &p, const FewPlace &f, uint32_t full0,
+                                                  uint32_t ring_b, uint32_t ring_a, int32_t *sums0, int warp, int lane)
 {
     using Cfg = S8FewCfg<MT>;
-    constexpr int S = Cfg::STAGES;
-    extern __shared__ uint8_t smem_raw[];
-    const uint32_t raw = ptx::smem_addr(smem_raw);
-    const uint32_t base = (raw + 1023u) & ~1023u;
-    uint8_t *const base_ptr = smem_raw + (base - raw);
-    constexpr uint32_t A0 = Cfg::WARPS * S * Cfg::B_BYTES;
-    constexpr uint32_t SUMS0 = A0 + Cfg::WARPS * S * Cfg::A_BYTES;
-    constexpr uint32_t CTRL0 = SUMS0 + 2 * Cfg::SUMS * 4;
-    const uint32_t ctrl = base + CTRL0;
-    const uint32_t flag = ctrl + 384u, last_flag = ctrl + 388u;  // (barriers: 8 warps x S x 8 bytes)
-    static_assert(Cfg::WARPS * S * 8 <= 384, "control block");
-    const SharedSchedule<true> sched{ctrl + 400u};
-    const uint32_t sums_full0 = ctrl + 432u, sums_free0 = ctrl + 448u;  // [2] each
-    const uint32_t gtab = ctrl + Cfg::GROUP_TABLE_OFF;
-    int32_t *const sums0 = reinterpret_cast<int32_t *>(base_ptr + SUMS0);  // [2][SUMS]
-    // The tile's column scales, biases and row scales.
-    float *const terms = reinterpret_cast<float *>(base_ptr + CTRL0 + Cfg::TERMS_OFF);
-
-    const int warp = __shfl_sync(0xffffffffu, int(threadIdx.x >> 5), 0);
-    const int lane = int(threadIdx.x & 31);
+    constexpr uint32_t S = Cfg::STAGES;
     const int g = lane >> 2, t4 = lane & 3;
-    const int32_t worker = int32_t(blockIdx.x);
-    const uint32_t full0 = ctrl + uint32_t(warp * S) * 8u;
-    const uint32_t ring_b = base + uint32_t(warp * S) * Cfg::B_BYTES;
-    const uint32_t ring_a = base + A0 + uint32_t(warp * S) * Cfg::A_BYTES;
+    const int half = warp & 1;
+    // This CTA's k-blocks, and the warp's first of them.
+    const int32_t end = int32_t(int64_t(f.rank + 1) * p.kb / f.ranks);
+    const int32_t begin = int32_t(int64_t(f.rank) * p.kb / f.ranks) + (warp >> 1);
 
-    if (lane == 0 && warp < Cfg::WARPS) {
-        if (warp == 0) {
-            ptx::prefetch_tensormap(&map_a);
-            ptx::prefetch_tensormap(&map_b);
-            for (int i = 0; i < 2; ++i) {
-                ptx::mbar_init(sums_full0 + 8u * i, Cfg::WARPS);
-                ptx::mbar_init(sums_free0 + 8u * i, 1);
-            }
-        }
-        for (int s = 0; s < S; ++s)
-            ptx::mbar_init(full0 + 8u * s, 1);
-        ptx::fence_mbar_init();
-    }
-    if (warp == 0) {
-        if (p.group_rows) {
-            build_group_table(p.group_rows, p.batch, p.M, Cfg::ROWS, p.tiles_n,
-                              reinterpret_cast<uint32_t *>(base_ptr + CTRL0 + Cfg::GROUP_TABLE_OFF), p.status);
-            __syncwarp();
-        }
-        if (lane == 0) {
-            ptx::st_shared_u32(flag, 0u);
-            S8Schedule s;
-            s.plan(p.group_rows ? int32_t(ptx::ld_shared_u32(gtab + 4u * (p.batch - 1))) : p.tiles_n * p.batch, p.kb,
-                   p.workers, S8Schedule::kFewRows);
-            sched.put(s);
-        }
-    }
-    for (int i = int(threadIdx.x); i < 2 * Cfg::SUMS; i += int(blockDim.x))
-        sums0[i] = 0;
-    __syncthreads();
-    // (The two-tile form needs more registers than an even share.)
-    if (warp >= Cfg::WARPS) {
-        if constexpr (MT == 2)
-            ptx::regs_dec<88>();
-        few_rows_finish<MT>(p, sched, gtab, sums0, terms, sums_full0, sums_free0, flag, last_flag, worker, lane);
-        return;
-    }
-
-    if constexpr (MT == 2)
-        ptx::regs_inc<208>();
-
-    // The warp's loads run S blocks ahead of its MMAs, with a walk of their own.
-    PieceWalk<true> wp(sched, worker);
-    int32_t pk = 0;
-    bool more = wp.advance(sched);
+    // The warp's loads run S blocks ahead of its MMAs.
+    int32_t next_tile = f.cluster, next_k = begin;
     S8Tile pt = {};
-    if (more) {
-        pt = tile_at(wp.tile, p, gtab, Cfg::ROWS, Cfg::COLS);
-        pk = wp.kb0 + warp;
-    }
+    if (next_tile < f.tiles)
+        pt = tile_at(next_tile, p, f.gtab, Cfg::ROWS, Cfg::COLS);
     uint32_t issued = 0;  // stages that hold or await a block
     auto issue = [&](uint32_t stage) {
-        while (more && pk >= wp.kb1) {
-            more = wp.advance(sched);
-            if (more) {
-                pt = tile_at(wp.tile, p, gtab, Cfg::ROWS, Cfg::COLS);
-                pk = wp.kb0 + warp;
-            }
+        if (next_k >= end) {
+            if (begin >= end)
+                return;  // (no block of any tile is this warp's)
+            next_k = begin;
+            next_tile += f.clusters;
+            if (next_tile < f.tiles)
+                pt = tile_at(next_tile, p, f.gtab, Cfg::ROWS, Cfg::COLS);
         }
-        if (!more)
+        if (next_tile >= f.tiles) {
+            next_k = end;  // (comes back here; the tile only grows)
             return;
+        }
         if (lane == 0) {
             const uint32_t fb = full0 + 8u * stage;
             ptx::mbar_arrive_expect_tx(fb, Cfg::B_BYTES + Cfg::A_BYTES);
-            ptx::tma_load_3d(ring_b + stage * Cfg::B_BYTES, &map_b, fb, pt.n0, pk * Cfg::BK, pt.z);
-            ptx::tma_load_3d(ring_a + stage * Cfg::A_BYTES, &map_a, fb, pk * Cfg::BK, 0, pt.z);
+            ptx::tma_load_3d(ring_b + stage * Cfg::B_BYTES, &map_b, fb, pt.n0 + 128 * half, next_k * Cfg::BK, pt.z);
+            ptx::tma_load_3d(ring_a + stage * Cfg::A_BYTES, &map_a, fb, next_k * Cfg::BK, 0, pt.z);
         }
         __syncwarp();
-        pk += Cfg::WARPS;
+        next_k += Cfg::KWARPS;
         ++issued;
     };
 #pragma unroll 1
-    for (uint32_t s = 0; s < uint32_t(S); ++s)
+    for (uint32_t s = 0; s < S; ++s)
         issue(s);
 
     uint32_t stage = 0, phase = 0, set = 0, set_phase = 0;
     bool ok = true;
-    for (PieceWalk<true> w(sched, worker); ok && w.advance(sched);) {
-        int32_t *const sums = sums0 + set * Cfg::SUMS;
-        bool mine = false;  // the set is this piece's
+    for (int32_t tile = f.cluster; ok && tile < f.tiles; tile += f.clusters) {
+        int32_t *const sums = sums0 + set * Cfg::SUMS + half * Cfg::HALF_SUMS;
+        bool mine = false;  // the set is this tile's
         float acc[MT][16][4];
 #pragma unroll
         for (int m = 0; m < MT; ++m)
@@ -1032,9 +985,9 @@ __global__ void __launch_bounds__(32 * (S8FewCfg<MT>::WARPS + S8FewCfg<MT>::FINI
 #pragma unroll
                 for (int d = 0; d < 4; ++d)
                     acc[m][j][d] = 0.f;
-        auto take = [&]() {  // the set's last piece has left it
+        auto take = [&]() {  // the set's last tile has left it
             if (!mine)
-                ok = __all_sync(0xffffffffu, s8_wait<false>(sums_free0 + 8u * set, set_phase ^ 1u, flag, p, kStatusReduce));
+                ok = __all_sync(0xffffffffu, s8_wait<false>(f.sums_free0 + 8u * set, set_phase ^ 1u, f.flag, p, kStatusReduce));
             mine = true;
             return ok;
         };
@@ -1047,18 +1000,18 @@ __global__ void __launch_bounds__(32 * (S8FewCfg<MT>::WARPS + S8FewCfg<MT>::FINI
                 for (int j = 0; j < 16; ++j)
 #pragma unroll
                     for (int d = 0; d < 4; ++d) {
-                        atomicAdd(sums + ((m * 16 + j) * 4 + d) * 32 + lane, __float2int_rn(acc[m][j][d]));
+                        atomicAdd(sums + few_rows_sum(m, j, d, lane), __float2int_rn(acc[m][j][d]));
                         acc[m][j][d] = 0.f;
                     }
         };
         int held = 0;
-        for (int32_t kb = w.kb0 + warp; kb < w.kb1; kb += Cfg::WARPS) {
-            ok = __all_sync(0xffffffffu, s8_wait<false>(full0 + 8u * stage, phase, flag, p, kStatusProducer));
+        for (int32_t kb = begin; kb < end; kb += Cfg::KWARPS) {
+            ok = __all_sync(0xffffffffu, s8_wait<false>(full0 + 8u * stage, phase, f.flag, p, kStatusProducer));
             if (!ok)
                 break;
             --issued;
             const uint32_t sb = ring_b + stage * Cfg::B_BYTES, sa = ring_a + stage * Cfg::A_BYTES;
-#pragma unroll
+#pragma unroll 1
             for (int kk = 0; kk < 2; ++kk) {
                 uint32_t a[MT][4];
 #pragma unroll
@@ -1096,7 +1049,7 @@ __global__ void __launch_bounds__(32 * (S8FewCfg<MT>::WARPS + S8FewCfg<MT>::FINI
             }
             __syncwarp();  // every lane has read the stage
             issue(stage);
-            if (++stage == uint32_t(S)) {
+            if (++stage == S) {
                 stage = 0;
                 phase ^= 1u;
             }
@@ -1109,25 +1062,95 @@ __global__ void __launch_bounds__(32 * (S8FewCfg<MT>::WARPS + S8FewCfg<MT>::FINI
         }
         if (ok && held)
             flush();
-        // (A warp without a block in the piece waits for the set, too, before
+        // (A warp without a block in the tile waits for the set, too, before
         // it arrives: it could otherwise arrive twice in one phase.)
         if (!ok || !take())
             break;
         __syncwarp();
         if (lane == 0)
-            ptx::mbar_arrive(sums_full0 + 8u * set);
+            ptx::mbar_arrive(f.sums_full0 + 8u * set);
         set ^= 1u;
         if (set == 0)
             set_phase ^= 1u;
     }
     // No TMA write into shared memory outlives the CTA.
     for (; issued > 0; --issued) {
-        s8_wait<false>(full0 + 8u * stage, phase, flag, p, kStatusDrain, false);
-        if (++stage == uint32_t(S)) {
+        s8_wait<false>(full0 + 8u * stage, phase, f.flag, p, kStatusDrain, false);
+        if (++stage == S) {
             stage = 0;
             phase ^= 1u;
         }
     }
+}
+
+template <int MT>
+__global__ void __launch_bounds__(S8FewCfg<MT>::THREADS, 1)
+    tsm_s8_few_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ CUtensorMap map_b,
+                      const S8Params p)
+{
+    using Cfg = S8FewCfg<MT>;
+    constexpr int S = Cfg::STAGES;
+    extern __shared__ uint8_t smem_raw[];
+    const uint32_t raw = ptx::smem_addr(smem_raw);
+    const uint32_t base = (raw + 1023u) & ~1023u;
+    uint8_t *const base_ptr = smem_raw + (base - raw);
+    constexpr uint32_t A0 = Cfg::WARPS * S * Cfg::B_BYTES;
+    constexpr uint32_t SUMS0 = A0 + Cfg::WARPS * S * Cfg::A_BYTES;
+    constexpr uint32_t CTRL0 = SUMS0 + 2 * Cfg::SUMS * 4;
+    static_assert(Cfg::WARPS * S * 8 <= 384, "control block");
+    const uint32_t ctrl = base + CTRL0;
+    const int warp = __shfl_sync(0xffffffffu, int(threadIdx.x >> 5), 0);
+    const int lane = int(threadIdx.x & 31);
+
+    FewPlace f;
+    f.sums0 = base + SUMS0;
+    f.terms0 = ctrl + Cfg::TERMS_OFF;
+    f.sums_full0 = ctrl + 384u;
+    f.sums_free0 = ctrl + 400u;
+    f.ready0 = ctrl + 416u;
+    f.taken0 = ctrl + 432u;
+    f.flag = ctrl + 448u;
+    f.gtab = ctrl + Cfg::GROUP_TABLE_OFF;
+    f.ranks = p.ranks;
+    f.rank = int32_t(ptx::cluster_ctarank());
+    f.cluster = int32_t(blockIdx.x) / p.ranks;
+    f.clusters = int32_t(gridDim.x) / p.ranks;
+
+    if (threadIdx.x == 0) {
+        ptx::prefetch_tensormap(&map_a);
+        ptx::prefetch_tensormap(&map_b);
+        for (int i = 0; i < Cfg::WARPS * S; ++i)
+            ptx::mbar_init(ctrl + 8u * i, 1);
+        for (uint32_t i = 0; i < 2; ++i) {
+            ptx::mbar_init(f.sums_full0 + 8u * i, Cfg::WARPS);
+            ptx::mbar_init(f.sums_free0 + 8u * i, 1);
+            ptx::mbar_init(f.ready0 + 8u * i, uint32_t(p.ranks));
+            ptx::mbar_init(f.taken0 + 8u * i, uint32_t(p.ranks));
+        }
+        ptx::st_shared_u32(f.flag, 0u);
+        ptx::fence_mbar_init();
+    } else if (warp == 1 && p.group_rows) {
+        build_group_table(p.group_rows, p.batch, p.M, Cfg::ROWS, p.tiles_n,
+                          reinterpret_cast<uint32_t *>(base_ptr + CTRL0 + Cfg::GROUP_TABLE_OFF), p.status);
+    }
+    for (int i = int(threadIdx.x); i < 2 * Cfg::SUMS / 4; i += Cfg::THREADS)
+        ptx::st_shared_v4(f.sums0 + 16u * i, 0u, 0u, 0u, 0u);
+    __syncthreads();
+    if (p.ranks > 1)
+        ptx::cluster_sync();  // the other CTAs' barriers exist
+    f.tiles = p.group_rows ? int32_t(ptx::ld_shared_u32(f.gtab + 4u * (p.batch - 1))) : p.tiles_n * p.batch;
+    if (warp < Cfg::WARPS) {
+        ptx::regs_inc<Cfg::MMA_REGS>();
+        few_rows_multiply<MT>(map_a, map_b, p, f, ctrl + uint32_t(warp * S) * 8u,
+                              base + uint32_t(warp * S) * Cfg::B_BYTES, base + A0 + uint32_t(warp * S) * Cfg::A_BYTES,
+                              reinterpret_cast<int32_t *>(base_ptr + SUMS0), warp, lane);
+    } else {
+        ptx::regs_dec<Cfg::FINISH_REGS>();
+        few_rows_finish<MT>(p, f, lane);
+    }
+    __syncwarp();
+    if (p.ranks > 1)
+        ptx::cluster_sync();  // no CTA leaves while another may still reach into it
 }
 
 // ------------------------------------------------------------- repacking
@@ -1211,24 +1234,65 @@ S8Shape shape_of()
 S8Shape s8_shape(S8Kind kind)
 {
     switch (kind) {
-    case S8Kind::kFew16: return S8Shape{16, 128, 32, S8FewCfg<1>::SUMS * 4, 1};
-    case S8Kind::kFew32: return S8Shape{32, 128, 32, S8FewCfg<2>::SUMS * 4, 1};
+    case S8Kind::kFew16: return S8Shape{16, 256, 32, 0, 0};
+    case S8Kind::kFew32: return S8Shape{32, 256, 32, 0, 0};
     case S8Kind::kOne: return shape_of<false>();
     default: return shape_of<true>();
     }
 }
 
-cudaError_t set_s8_attributes()
+namespace {
+
+template <int MT>
+cudaLaunchConfig_t few_config(int grid, int ranks, cudaLaunchAttribute *attr, cudaStream_t stream)
+{
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(unsigned(grid), 1, 1);
+    cfg.blockDim = dim3(S8FewCfg<MT>::THREADS, 1, 1);
+    cfg.dynamicSmemBytes = S8FewCfg<MT>::SMEM_BYTES;
+    cfg.stream = stream;
+    attr->id = cudaLaunchAttributeClusterDimension;
+    attr->val.clusterDim.x = unsigned(ranks);
+    attr->val.clusterDim.y = 1;
+    attr->val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    return cfg;
+}
+
+template <int MT>
+cudaError_t set_few(S8Capacity *cap)
+{
+    cudaError_t e = cudaFuncSetAttribute(tsm_s8_few_kernel<MT>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                         S8FewCfg<MT>::SMEM_BYTES);
+    for (int i = 0; e == cudaSuccess && i < S8Capacity::KINDS; ++i) {
+        cudaLaunchAttribute attr;
+        const cudaLaunchConfig_t cfg = few_config<MT>(1 << i, 1 << i, &attr, nullptr);
+        e = cudaOccupancyMaxActiveClusters(&cap->clusters[i], tsm_s8_few_kernel<MT>, &cfg);
+    }
+    return e;
+}
+
+template <int MT>
+cudaError_t launch_few(const CUtensorMap &map_a, const CUtensorMap &map_b, const S8Params &p, int grid,
+                       cudaStream_t stream)
+{
+    cudaLaunchAttribute attr;
+    const cudaLaunchConfig_t cfg = few_config<MT>(grid * p.ranks, p.ranks, &attr, stream);
+    return cudaLaunchKernelEx(&cfg, tsm_s8_few_kernel<MT>, map_a, map_b, p);
+}
+
+}  // namespace
+
+cudaError_t set_s8_attributes(S8Capacity *cap)
 {
     cudaError_t e = set_tiled<true>();
     if (e == cudaSuccess)
         e = set_tiled<false>();
     if (e == cudaSuccess)
-        e = cudaFuncSetAttribute(tsm_s8_few_kernel<1>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                 S8FewCfg<1>::SMEM_BYTES);
+        e = set_few<1>(cap);
     if (e == cudaSuccess)
-        e = cudaFuncSetAttribute(tsm_s8_few_kernel<2>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                 S8FewCfg<2>::SMEM_BYTES);
+        e = set_few<2>(cap);
     return e;
 }
 
@@ -1236,12 +1300,8 @@ cudaError_t launch_s8(const CUtensorMap &map_a, const CUtensorMap &map_b, const 
                       cudaStream_t stream)
 {
     switch (kind) {
-    case S8Kind::kFew16:
-        tsm_s8_few_kernel<1><<<unsigned(grid), 384, S8FewCfg<1>::SMEM_BYTES, stream>>>(map_a, map_b, p);
-        return cudaGetLastError();
-    case S8Kind::kFew32:
-        tsm_s8_few_kernel<2><<<unsigned(grid), 384, S8FewCfg<2>::SMEM_BYTES, stream>>>(map_a, map_b, p);
-        return cudaGetLastError();
+    case S8Kind::kFew16: return launch_few<1>(map_a, map_b, p, grid, stream);
+    case S8Kind::kFew32: return launch_few<2>(map_a, map_b, p, grid, stream);
     case S8Kind::kOne: return launch_tiled<false>(map_a, map_b, p, grid, stream);
     default: return launch_tiled<true>(map_a, map_b, p, 2 * grid, stream);
     }
