@@ -386,25 +386,30 @@ std::once_flag g_s8_once[64];
 cudaError_t g_s8_error[64];
 S8Capacity g_s8_capacity[64];
 
-// CTAs per cluster of a few-rows launch: the least estimated time over 1, 2, 4
-// and 8.  A CTA's rate is its share of the memory's, or what its warps can
-// multiply if that is less; a cluster waits for its slowest CTA, the launch
-// for the fullest cluster; passing the sums between CTAs costs about 1 us.
+// CTAs per cluster of a few-rows launch: the least estimated time over 1 to 8.
+// A CTA's rate is its share of the memory's, or what its warps can multiply if
+// that is less; its pairs of warps (8, or 4 for two blocks of rows) take whole
+// blocks; adding up their sums takes 1 us.  The launch waits for the cluster
+// with the most tiles.  Finishing a tile takes 2 us, 3 where its sums pass
+// between CTAs; it hides behind the next tile if that takes longer.
 int few_rows_ranks(int64_t tiles, int32_t kb, const S8Capacity &cap, bool two, int *clusters)
 {
     const double block = 8192.0;                   // bytes of 32 k x 256 columns
     const double memory = 6.0e6;                   // bytes per us, all CTAs
-    const double most = two ? 38.0e3 : 52.0e3;     // bytes per us, one CTA
+    const double most = two ? 38.0e3 : 45.0e3;     // bytes per us, one CTA
+    const int pairs = two ? 4 : 8;
     int best = 1;
     double best_us = 0.0;
     for (int i = 0; i < S8Capacity::KINDS; ++i) {
-        const int ranks = 1 << i;
+        const int ranks = i + 1;
         if (cap.clusters[i] <= 0 || (i > 0 && ranks > kb))
             continue;
         const int64_t n = std::min<int64_t>(tiles, cap.clusters[i]);
         const double rate = std::min(most, memory / double(n * ranks));
-        const double blocks = double((tiles + n - 1) / n) * double((kb + ranks - 1) / ranks);
-        const double us = blocks * block / rate + (ranks > 1 ? 1.0 : 0.0);
+        const double finish = ranks > 1 ? 3.0 : 2.0;
+        const int64_t steps = ((kb + ranks - 1) / ranks + pairs - 1) / pairs;
+        const double each = std::max(finish, double(steps * pairs) * block / rate + 1.0);
+        const double us = double((tiles + n - 1) / n) * each + finish;
         if (i == 0 || us < best_us) {
             best = ranks;
             best_us = us;

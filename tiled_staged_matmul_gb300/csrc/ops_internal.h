@@ -129,9 +129,9 @@ struct S8Shape {
     int parts;                  // arrival words per tile
 };
 S8Shape s8_shape(S8Kind kind);
-// Clusters of 1, 2, 4 and 8 CTAs of the few-rows kernels that fit on the device at once.
+// Clusters of 1 to 8 CTAs of the few-rows kernels that fit on the device at once.
 struct S8Capacity {
-    static constexpr int KINDS = 4;
+    static constexpr int KINDS = 8;
     int clusters[KINDS];
 };
 cudaError_t set_s8_attributes(S8Capacity *cap);

@@ -345,13 +345,6 @@ __device__ __forceinline__ void put4_as(const S8Params &p, int64_t at, int32_t c
         if (col + k < p.N)
             epi_store(p.C, at + k, o[k], p.epi.out_type);
 }
-__device__ __forceinline__ void put4(const S8Params &p, int64_t at, int32_t col, float (&o)[4], const float (&sb)[4],
-                                     const float (&bias)[4])
-{
-    with_activation<kActRuntime>(p.epi.act,
-                                 [&](auto act) { put4_as<decltype(act)::value>(p, at, col, o, sb, bias); });
-}
-
 // A staged box (32 rows of 32 f32 values, 16-byte chunks swizzled by the row)
 // through the epilogue into C: eight lanes take a row's chunks, four rows at a
 // time.
@@ -761,7 +754,7 @@ __global__ void __launch_bounds__(kS8Threads, 1)
 //
 // Up to 32 rows of A (a decode step): the product reads every code of B once
 // and is bound by that.  A tile is 256 columns; its K is cut over the CTAs of a
-// cluster (1, 2, 4 or 8 of them, by a time model on the host).  In a CTA,
+// cluster (up to 8 of them, by a time model on the host).  In a CTA,
 // independent warps in pairs take 32 k of the tile at a time, one warp for each
 // 128 columns, so that a row of B is read 256 bytes at a time (reading 128
 // bytes of it ran at 4.6 TB/s, 256 at 6.0, 512 no faster).  Each warp has a TMA
@@ -780,7 +773,7 @@ __global__ void __launch_bounds__(kS8Threads, 1)
 // A warp's f32 sums go into the CTA's 32-bit ones in shared memory (integer
 // atomics: any order gives the same sum) after at most 1024 k.  There are two
 // sets of those: four more warps take a finished tile on while the others go on
-// with the next.  Each CTA of the cluster finishes its share of the columns: it
+// with the next.  Each CTA of the cluster finishes its share of the tile: it
 // adds up that share of every CTA's sums through distributed shared memory, so
 // nothing passes through the workspace (which, with its fences and arrivals,
 // cost a tile's end three to five microseconds, this about one).
@@ -791,7 +784,7 @@ struct S8FewCfg {
     static constexpr int THREADS = 32 * (WARPS + FINISHERS);
     static constexpr int KWARPS = WARPS / 2;  // warps along k
     static constexpr int B_BYTES = BK * 128, A_BYTES = ROWS * BK;
-    static constexpr int HALF_SUMS = ROWS * 128;  // of 128 columns: [value of a lane][lane]
+    static constexpr int HALF_SUMS = ROWS * 128;  // of 128 columns (few_rows_sum)
     static constexpr int SUMS = 2 * HALF_SUMS;
     static constexpr int CTRL = 6144, GROUP_TABLE_OFF = 1024, TERMS_OFF = 2048;
     static constexpr int SMEM_BYTES = 1024 + WARPS * STAGES * (B_BYTES + A_BYTES) + 2 * SUMS * 4 + CTRL;
@@ -812,12 +805,14 @@ __device__ __forceinline__ uint32_t code_pair(uint32_t lo, uint32_t hi)
     return *reinterpret_cast<const uint32_t *>(&x);
 }
 
-// Where value (j, d) of row block m of a lane's accumulator is kept among a
-// half's sums: 32 lanes together, in an order that lets the lanes that finish
-// 128 columns of one row read different banks.
-__device__ __forceinline__ int few_rows_sum(int m, int j, int d, int lane)
+// Where a half's sums are kept: rows in groups of eight, then column bit 4, the
+// row, and chunks of the four columns 32 apart, column j's chunk at j ^ row --
+// so that the lanes of an accumulator value (eight rows of four columns 32
+// apart) add to different banks, and sixteen threads read sixteen neighbouring
+// columns' chunks.
+__device__ __forceinline__ constexpr int few_rows_sum(int octet, int d1, int row, int j, int t)
 {
-    return ((m * 16 + j) * 4 + d) * 32 + (lane ^ (4 * (2 * (j >> 2) + (d & 1))));
+    return ((octet * 2 + d1) * 8 + row) * 64 + 4 * (j ^ row) + t;
 }
 
 // A CTA's addresses and place in the launch.
@@ -829,21 +824,20 @@ struct FewPlace {
 };
 
 // The finishing warps: tile by tile, the cluster's sums of this CTA's share of
-// the columns through the epilogue into C.
+// the tile through the epilogue into C.
 template <int MT>
 __device__ __forceinline__ void few_rows_finish(const S8Params &p, const FewPlace &f, int lane)
 {
     using Cfg = S8FewCfg<MT>;
     constexpr int FT = 32 * Cfg::FINISHERS;
-    const int ft = int(threadIdx.x) - 32 * Cfg::WARPS, fw = ft >> 5;
+    const int ft = int(threadIdx.x) - 32 * Cfg::WARPS;
     const uint32_t sb0 = f.terms0, bias0 = f.terms0 + 4u * Cfg::COLS, sa0 = f.terms0 + 8u * Cfg::COLS;
-    const int share = Cfg::COLS / f.ranks, c0 = f.rank * share;  // this CTA's columns of a tile
     uint32_t set = 0, phase = 0;
     for (int32_t tile = f.cluster; tile < f.tiles; tile += f.clusters) {
         const S8Tile t = tile_at(tile, p, f.gtab, Cfg::ROWS, Cfg::COLS);
         // The terms of the epilogue while the sums are on their way.
-        for (int c = ft; c < share; c += FT) {
-            const int32_t col = t.n0 + c0 + c;
+        for (int c = ft; c < Cfg::COLS; c += FT) {
+            const int32_t col = t.n0 + c;
             float sb = p.epi.alpha, bias = 0.f;
             if (p.scale_b && col < p.N)
                 sb *= __ldg(p.scale_b + t.z * p.sb_stride + col);
@@ -869,40 +863,44 @@ __device__ __forceinline__ void few_rows_finish(const S8Params &p, const FewPlac
             if (!ok)
                 return;
         }
-        // Four columns of a row per thread.  Column 128 h + 32 t + 16 d + j is
-        // value (j, d) of lane 4 (row % 8) + t of half h.
-        const int quads = share / 4;
-        for (int i = ft; i < t.rows * quads; i += FT) {
-            const int row = i / quads, c = 4 * (i - row * quads);
-            const int32_t col = t.n0 + c0 + c;
-            if (col >= p.N)
+        // This CTA's share of the tile, in chunks of four columns 32 apart;
+        // rows past the last are left out in eights.
+        const int octets = (t.rows + 7) / 8, chunks = 2 * octets * 256;
+        const int last = (f.rank + 1) * chunks / f.ranks;
+        for (int i = f.rank * chunks / f.ranks + ft; i < last; i += FT) {
+            const int j = i & 15, r8 = (i >> 4) & 7, d1 = (i >> 7) & 1, ho = i >> 8;
+            const int h = ho >= octets, octet = ho - h * octets;
+            const int row = 8 * octet + r8;
+            if (row >= t.rows)
                 continue;
-            const int in = c0 + c, h = in >> 7, d = ((in >> 4) & 1) + 2 * ((row >> 3) & 1);
-            const uint32_t at = sums + 4u * uint32_t(h * Cfg::HALF_SUMS + few_rows_sum(row >> 4, in & 15, d,
-                                                                                       4 * (row & 7) + ((in >> 5) & 3)));
+            const uint32_t at = sums + 4u * uint32_t(h * Cfg::HALF_SUMS + few_rows_sum(octet, d1, r8, j, 0));
+            // Every CTA's chunk on its way at once.
+            uint4 x[8];
             int32_t v[4] = {};
-            if (f.ranks == 1) {
 #pragma unroll
-                for (int k = 0; k < 4; ++k)
-                    v[k] = int32_t(ptx::ld_shared_u32(at + 512u * k));
-            } else {
-#pragma unroll 2
-                for (int r = 0; r < f.ranks; ++r) {
-                    const uint32_t there = ptx::mapa_shared(at, uint32_t(r));
+            for (int r = 0; r < 8; ++r)
+                x[r] = r < f.ranks ? ptx::ld_cluster_v4(ptx::mapa_shared(at, uint32_t(r))) : make_uint4(0, 0, 0, 0);
 #pragma unroll
-                    for (int k = 0; k < 4; ++k)
-                        v[k] += int32_t(ptx::ld_cluster_u32(there + 512u * k));
-                }
+            for (int r = 0; r < 8; ++r) {
+                v[0] += int32_t(x[r].x);
+                v[1] += int32_t(x[r].y);
+                v[2] += int32_t(x[r].z);
+                v[3] += int32_t(x[r].w);
             }
             const float sa = __uint_as_float(ptx::ld_shared_u32(sa0 + 4u * row));
-            const uint4 s4 = ptx::ld_shared_v4(sb0 + 4u * c), b4 = ptx::ld_shared_v4(bias0 + 4u * c);
-            const float sb[4] = {__uint_as_float(s4.x), __uint_as_float(s4.y), __uint_as_float(s4.z), __uint_as_float(s4.w)};
-            const float bias[4] = {__uint_as_float(b4.x), __uint_as_float(b4.y), __uint_as_float(b4.z), __uint_as_float(b4.w)};
-            float o[4];
+            const int c = 128 * h + 16 * d1 + j;
+            const int64_t row_at = t.z * p.sC + row * p.ldc + t.n0;
+            const int32_t columns = p.N - t.n0;
+            with_activation<kActRuntime>(p.epi.act, [&](auto act) {
 #pragma unroll
-            for (int k = 0; k < 4; ++k)
-                o[k] = float(v[k]) * sa;
-            put4(p, t.z * p.sC + row * p.ldc + col, col, o, sb, bias);
+                for (int k = 0; k < 4; ++k) {
+                    const float sb = __uint_as_float(ptx::ld_shared_u32(sb0 + 4u * (c + 32 * k)));
+                    const float bias = __uint_as_float(ptx::ld_shared_u32(bias0 + 4u * (c + 32 * k)));
+                    const float o = epi_act(fmaf(sb, float(v[k]) * sa, bias), decltype(act)::value, p.epi.slope);
+                    if (c + 32 * k < columns)
+                        epi_store(p.C, row_at + c + 32 * k, o, p.epi.out_type);
+                }
+            });
         }
         ptx::named_bar_sync(1, FT);  // the sums and the terms have been read here
         if (f.ranks > 1) {
@@ -1000,7 +998,7 @@ __device__ __forceinline__ void few_rows_multiply(const CUtensorMap &map_a, cons
                 for (int j = 0; j < 16; ++j)
 #pragma unroll
                     for (int d = 0; d < 4; ++d) {
-                        atomicAdd(sums + few_rows_sum(m, j, d, lane), __float2int_rn(acc[m][j][d]));
+                        atomicAdd(sums + few_rows_sum(2 * m + (d >> 1), d & 1, g, j, t4), __float2int_rn(acc[m][j][d]));
                         acc[m][j][d] = 0.f;
                     }
         };
@@ -1267,7 +1265,7 @@ cudaError_t set_few(S8Capacity *cap)
                                          S8FewCfg<MT>::SMEM_BYTES);
     for (int i = 0; e == cudaSuccess && i < S8Capacity::KINDS; ++i) {
         cudaLaunchAttribute attr;
-        const cudaLaunchConfig_t cfg = few_config<MT>(1 << i, 1 << i, &attr, nullptr);
+        const cudaLaunchConfig_t cfg = few_config<MT>(i + 1, i + 1, &attr, nullptr);
         e = cudaOccupancyMaxActiveClusters(&cap->clusters[i], tsm_s8_few_kernel<MT>, &cfg);
     }
     return e;

@@ -116,11 +116,14 @@ __device__ __forceinline__ bool named_bar_and(uint32_t id, uint32_t count, bool 
     return all != 0;
 }
 
-// A word of shared memory of any CTA of the cluster.
-__device__ __forceinline__ uint32_t ld_cluster_u32(uint32_t cluster_addr)
+// 16 bytes of shared memory of any CTA of the cluster.
+__device__ __forceinline__ uint4 ld_cluster_v4(uint32_t cluster_addr)
 {
-    uint32_t v;
-    asm volatile("ld.shared::cluster.u32 %0, [%1];" : "=r"(v) : "r"(cluster_addr) : "memory");
+    uint4 v;
+    asm volatile("ld.shared::cluster.v4.u32 {%0, %1, %2, %3}, [%4];"
+                 : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+                 : "r"(cluster_addr)
+                 : "memory");
     return v;
 }
 
