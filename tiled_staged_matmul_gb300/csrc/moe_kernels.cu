@@ -16,6 +16,7 @@
 // HBM once and no inverse map of the slots is needed.  Sums run in f32 over j
 // in ascending order, rounded once to the rows' type; there are no atomics on
 // floating-point data, so a call is bitwise reproducible.
+#include "launch.cuh"
 #include "ops_internal.h"
 
 #include <cuda_bf16.h>
@@ -43,6 +44,8 @@ template <bool WIDE, int ROUNDS>
 __global__ void __launch_bounds__(32 * kRouteWarps) tsm_moe_count_kernel(RouteParams p)
 {
     extern __shared__ uint32_t count[];
+    chain_next();
+    chain_wait();
     for (int e = int(threadIdx.x); e < p.groups; e += int(blockDim.x))
         count[e] = 0;
     __syncthreads();
@@ -70,6 +73,8 @@ __global__ void __launch_bounds__(32 * kRouteWarps) tsm_moe_rank_kernel(RoutePar
     uint16_t *const seen = reinterpret_cast<uint16_t *>(smem + p.groups);  // [warps][groups]
     const int warp = int(threadIdx.x >> 5), lane = int(threadIdx.x & 31);
     const int G = p.groups;
+    chain_next();
+    chain_wait();
     const int64_t first = int64_t(blockIdx.x) * route_chunk(ROUNDS) + int64_t(warp) * 32 * ROUNDS;
     int32_t id[ROUNDS];
 #pragma unroll
@@ -211,6 +216,8 @@ constexpr int kCopyUnroll = 4;
 template <typename U>
 __global__ void __launch_bounds__(256) tsm_moe_dispatch_kernel(MoveParams p)
 {
+    chain_next();
+    chain_wait();
     const int lane = int(threadIdx.x & 31);
     const int64_t per = 32 * kCopyUnroll;
     const int64_t segs = (p.width + per - 1) / per;
@@ -248,6 +255,8 @@ template <int ET, bool VEC>
 __global__ void __launch_bounds__(256) tsm_moe_combine_kernel(MoveParams p)
 {
     using P = Piece<ET, VEC>;
+    chain_next();
+    chain_wait();
     const int64_t pieces = (p.width + P::V - 1) / P::V;
     const int64_t total = p.tokens * pieces;
     for (int64_t i = int64_t(blockIdx.x) * blockDim.x + threadIdx.x; i < total;
@@ -300,6 +309,8 @@ __global__ void __launch_bounds__(kGradThreads) tsm_moe_combine_grad_kernel(Move
 {
     using P = Piece<ET, VEC>;
     __shared__ float part[kGradThreads / 32][kGradUnroll];
+    chain_next();
+    chain_wait();
     const int64_t t = blockIdx.x;
     const int64_t pieces = (p.width + P::V - 1) / P::V;
     const char *dout = static_cast<const char *>(p.dout) + t * p.ld_dout * P::EB;
@@ -374,6 +385,8 @@ __global__ void __launch_bounds__(kQuantThreads) tsm_quantize_rows_kernel(QuantP
 {
     using P = Piece<ET, VEC>;
     __shared__ uint32_t part[kQuantThreads / 32];
+    chain_next();
+    chain_wait();
     const int64_t g = blockIdx.x / p.M;
     const int64_t r = blockIdx.x - g * p.M;
     if (p.group_rows && r >= int64_t(__ldg(p.group_rows + g)))
@@ -452,19 +465,22 @@ template <bool WIDE, int ROUNDS>
 cudaError_t route_as(const RouteParams &p, int64_t chunks, cudaStream_t stream)
 {
     constexpr int threads = 32 * kRouteWarps;
+    cudaError_t e = cudaSuccess;
     if (chunks > 1)
-        tsm_moe_count_kernel<WIDE, ROUNDS><<<unsigned(chunks), threads, size_t(p.groups) * 4, stream>>>(p);
-    tsm_moe_rank_kernel<WIDE, ROUNDS><<<unsigned(chunks), threads,
-                                        size_t(p.groups) * (4 + 2 * kRouteWarps), stream>>>(p);
-    return cudaGetLastError();
+        e = launch_chained(tsm_moe_count_kernel<WIDE, ROUNDS>, dim3(unsigned(chunks)), threads, size_t(p.groups) * 4, 0,
+                           stream, p);
+    if (e == cudaSuccess)
+        e = launch_chained(tsm_moe_rank_kernel<WIDE, ROUNDS>, dim3(unsigned(chunks)), threads,
+                           size_t(p.groups) * (4 + 2 * kRouteWarps), 0, stream, p);
+    return e;
 }
 
 template <typename U>
-void dispatch_as(const MoveParams &p, int sms, cudaStream_t stream)
+cudaError_t dispatch_as(const MoveParams &p, int sms, cudaStream_t stream)
 {
     const int64_t segs = (p.width + 32 * kCopyUnroll - 1) / (32 * kCopyUnroll);
     const int64_t blocks = (p.tokens * segs + 7) / 8;
-    tsm_moe_dispatch_kernel<U><<<unsigned(min(blocks, int64_t(sms) * 64)), 256, 0, stream>>>(p);
+    return launch_chained(tsm_moe_dispatch_kernel<U>, dim3(unsigned(min(blocks, int64_t(sms) * 64))), 256, 0, 0, stream, p);
 }
 
 }  // namespace
@@ -481,13 +497,12 @@ cudaError_t launch_route(const RouteParams &p, bool wide_ids, int rounds, int64_
 cudaError_t launch_dispatch(const MoveParams &p, int vec, int sms, cudaStream_t stream)
 {
     switch (vec) {
-    case 16: dispatch_as<uint4>(p, sms, stream); break;
-    case 8: dispatch_as<uint2>(p, sms, stream); break;
-    case 4: dispatch_as<uint32_t>(p, sms, stream); break;
-    case 2: dispatch_as<unsigned short>(p, sms, stream); break;
-    default: dispatch_as<unsigned char>(p, sms, stream); break;
+    case 16: return dispatch_as<uint4>(p, sms, stream);
+    case 8: return dispatch_as<uint2>(p, sms, stream);
+    case 4: return dispatch_as<uint32_t>(p, sms, stream);
+    case 2: return dispatch_as<unsigned short>(p, sms, stream);
+    default: return dispatch_as<unsigned char>(p, sms, stream);
     }
-    return cudaGetLastError();
 }
 
 cudaError_t launch_combine(const MoveParams &p, int elem, bool vec, int sms, cudaStream_t stream)
@@ -497,18 +512,18 @@ cudaError_t launch_combine(const MoveParams &p, int elem, bool vec, int sms, cud
     const unsigned grid = unsigned(min(blocks, int64_t(sms) * 64));
     if (vec) {
         if (elem == kOutF32)
-            tsm_moe_combine_kernel<kOutF32, true><<<grid, 256, 0, stream>>>(p);
+            return launch_chained(tsm_moe_combine_kernel<kOutF32, true>, dim3(grid), 256, 0, 0, stream, p);
         else if (elem == kOutF16)
-            tsm_moe_combine_kernel<kOutF16, true><<<grid, 256, 0, stream>>>(p);
+            return launch_chained(tsm_moe_combine_kernel<kOutF16, true>, dim3(grid), 256, 0, 0, stream, p);
         else
-            tsm_moe_combine_kernel<kOutBF16, true><<<grid, 256, 0, stream>>>(p);
+            return launch_chained(tsm_moe_combine_kernel<kOutBF16, true>, dim3(grid), 256, 0, 0, stream, p);
     } else {
         if (elem == kOutF32)
-            tsm_moe_combine_kernel<kOutF32, false><<<grid, 256, 0, stream>>>(p);
+            return launch_chained(tsm_moe_combine_kernel<kOutF32, false>, dim3(grid), 256, 0, 0, stream, p);
         else if (elem == kOutF16)
-            tsm_moe_combine_kernel<kOutF16, false><<<grid, 256, 0, stream>>>(p);
+            return launch_chained(tsm_moe_combine_kernel<kOutF16, false>, dim3(grid), 256, 0, 0, stream, p);
         else
-            tsm_moe_combine_kernel<kOutBF16, false><<<grid, 256, 0, stream>>>(p);
+            return launch_chained(tsm_moe_combine_kernel<kOutBF16, false>, dim3(grid), 256, 0, 0, stream, p);
     }
     return cudaGetLastError();
 }
@@ -518,18 +533,18 @@ cudaError_t launch_combine_grad(const MoveParams &p, int elem, bool vec, cudaStr
     const unsigned grid = unsigned(p.tokens);
     if (vec) {
         if (elem == kOutF32)
-            tsm_moe_combine_grad_kernel<kOutF32, true><<<grid, kGradThreads, 0, stream>>>(p);
+            return launch_chained(tsm_moe_combine_grad_kernel<kOutF32, true>, dim3(grid), kGradThreads, 0, 0, stream, p);
         else if (elem == kOutF16)
-            tsm_moe_combine_grad_kernel<kOutF16, true><<<grid, kGradThreads, 0, stream>>>(p);
+            return launch_chained(tsm_moe_combine_grad_kernel<kOutF16, true>, dim3(grid), kGradThreads, 0, 0, stream, p);
         else
-            tsm_moe_combine_grad_kernel<kOutBF16, true><<<grid, kGradThreads, 0, stream>>>(p);
+            return launch_chained(tsm_moe_combine_grad_kernel<kOutBF16, true>, dim3(grid), kGradThreads, 0, 0, stream, p);
     } else {
         if (elem == kOutF32)
-            tsm_moe_combine_grad_kernel<kOutF32, false><<<grid, kGradThreads, 0, stream>>>(p);
+            return launch_chained(tsm_moe_combine_grad_kernel<kOutF32, false>, dim3(grid), kGradThreads, 0, 0, stream, p);
         else if (elem == kOutF16)
-            tsm_moe_combine_grad_kernel<kOutF16, false><<<grid, kGradThreads, 0, stream>>>(p);
+            return launch_chained(tsm_moe_combine_grad_kernel<kOutF16, false>, dim3(grid), kGradThreads, 0, 0, stream, p);
         else
-            tsm_moe_combine_grad_kernel<kOutBF16, false><<<grid, kGradThreads, 0, stream>>>(p);
+            return launch_chained(tsm_moe_combine_grad_kernel<kOutBF16, false>, dim3(grid), kGradThreads, 0, 0, stream, p);
     }
     return cudaGetLastError();
 }
@@ -539,18 +554,18 @@ cudaError_t launch_quantize_rows(const QuantParams &p, int elem, bool vec, cudaS
     const unsigned grid = unsigned(p.M * p.batch);
     if (vec) {
         if (elem == kOutF32)
-            tsm_quantize_rows_kernel<kOutF32, true><<<grid, kQuantThreads, 0, stream>>>(p);
+            return launch_chained(tsm_quantize_rows_kernel<kOutF32, true>, dim3(grid), kQuantThreads, 0, 0, stream, p);
         else if (elem == kOutF16)
-            tsm_quantize_rows_kernel<kOutF16, true><<<grid, kQuantThreads, 0, stream>>>(p);
+            return launch_chained(tsm_quantize_rows_kernel<kOutF16, true>, dim3(grid), kQuantThreads, 0, 0, stream, p);
         else
-            tsm_quantize_rows_kernel<kOutBF16, true><<<grid, kQuantThreads, 0, stream>>>(p);
+            return launch_chained(tsm_quantize_rows_kernel<kOutBF16, true>, dim3(grid), kQuantThreads, 0, 0, stream, p);
     } else {
         if (elem == kOutF32)
-            tsm_quantize_rows_kernel<kOutF32, false><<<grid, kQuantThreads, 0, stream>>>(p);
+            return launch_chained(tsm_quantize_rows_kernel<kOutF32, false>, dim3(grid), kQuantThreads, 0, 0, stream, p);
         else if (elem == kOutF16)
-            tsm_quantize_rows_kernel<kOutF16, false><<<grid, kQuantThreads, 0, stream>>>(p);
+            return launch_chained(tsm_quantize_rows_kernel<kOutF16, false>, dim3(grid), kQuantThreads, 0, 0, stream, p);
         else
-            tsm_quantize_rows_kernel<kOutBF16, false><<<grid, kQuantThreads, 0, stream>>>(p);
+            return launch_chained(tsm_quantize_rows_kernel<kOutBF16, false>, dim3(grid), kQuantThreads, 0, 0, stream, p);
     }
     return cudaGetLastError();
 }

@@ -16,6 +16,7 @@
 // 1024 + (c + 128); subtracting 1152 leaves c, exactly.  Five instructions
 // turn four codes into two f16 pairs.
 #include "gemm_kernel.cuh"
+#include "launch.cuh"
 #include "ops_internal.h"
 #include "s8_ptx.cuh"
 
@@ -424,10 +425,13 @@ __global__ void __launch_bounds__(kS8Threads, 1)
     __syncwarp();
     if constexpr (PAIR)
         ptx::cluster_sync();
+    chain_next();
     if (warp == 1) {
         ptx::tmem_alloc<PAIR>(ptx::smem_addr(tmem_slot), 512);
         ptx::tmem_relinquish<PAIR>();
-    } else if (warp == 2 && p.group_rows) {
+    }
+    chain_wait();
+    if (warp == 2 && p.group_rows) {
         build_group_table(p.group_rows, p.batch, p.M, Cfg::TILE_M, p.tiles_n,
                           reinterpret_cast<uint32_t *>(ctrl_ptr + Cfg::GROUP_TABLE_OFF), p.status);
         __syncwarp();
@@ -1127,12 +1131,15 @@ __global__ void __launch_bounds__(S8FewCfg<MT>::THREADS, 1)
         }
         ptx::st_shared_u32(f.flag, 0u);
         ptx::fence_mbar_init();
-    } else if (warp == 1 && p.group_rows) {
-        build_group_table(p.group_rows, p.batch, p.M, Cfg::ROWS, p.tiles_n,
-                          reinterpret_cast<uint32_t *>(base_ptr + CTRL0 + Cfg::GROUP_TABLE_OFF), p.status);
     }
     for (int i = int(threadIdx.x); i < 2 * Cfg::SUMS / 4; i += Cfg::THREADS)
         ptx::st_shared_v4(f.sums0 + 16u * i, 0u, 0u, 0u, 0u);
+    chain_next();
+    chain_wait();
+    if (warp == 1 && p.group_rows) {
+        build_group_table(p.group_rows, p.batch, p.M, Cfg::ROWS, p.tiles_n,
+                          reinterpret_cast<uint32_t *>(base_ptr + CTRL0 + Cfg::GROUP_TABLE_OFF), p.status);
+    }
     __syncthreads();
     if (p.ranks > 1)
         ptx::cluster_sync();  // the other CTAs' barriers exist
@@ -1158,6 +1165,8 @@ __global__ void __launch_bounds__(256)
     tsm_pack_s8_kernel(const int8_t *src, int64_t s_ld, int64_t s_stride, int8_t *dst, int64_t d_ld, int64_t d_stride,
                        int64_t rows, int64_t cols, int64_t batch)
 {
+    chain_next();
+    chain_wait();
     const int64_t chunks = d_ld / 16;
     const int64_t total = batch * rows * chunks;
     for (int64_t i = int64_t(blockIdx.x) * blockDim.x + threadIdx.x; i < total; i += int64_t(gridDim.x) * blockDim.x) {
@@ -1205,19 +1214,8 @@ template <bool PAIR>
 cudaError_t launch_tiled(const CUtensorMap &map_a, const CUtensorMap &map_b, const S8Params &p, int grid,
                          cudaStream_t stream)
 {
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(unsigned(grid), 1, 1);
-    cfg.blockDim = dim3(kS8Threads, 1, 1);
-    cfg.dynamicSmemBytes = S8Cfg<PAIR>::SMEM_BYTES;
-    cfg.stream = stream;
-    cudaLaunchAttribute attr[1];
-    attr[0].id = cudaLaunchAttributeClusterDimension;
-    attr[0].val.clusterDim.x = 2;
-    attr[0].val.clusterDim.y = 1;
-    attr[0].val.clusterDim.z = 1;
-    cfg.attrs = PAIR ? attr : nullptr;
-    cfg.numAttrs = PAIR ? 1 : 0;
-    return cudaLaunchKernelEx(&cfg, tsm_s8_tiled_kernel<PAIR>, map_a, map_b, p);
+    return launch_chained(tsm_s8_tiled_kernel<PAIR>, dim3(unsigned(grid)), kS8Threads, S8Cfg<PAIR>::SMEM_BYTES,
+                          PAIR ? 2u : 0u, stream, map_a, map_b, p);
 }
 
 template <bool PAIR>
@@ -1242,30 +1240,22 @@ S8Shape s8_shape(S8Kind kind)
 namespace {
 
 template <int MT>
-cudaLaunchConfig_t few_config(int grid, int ranks, cudaLaunchAttribute *attr, cudaStream_t stream)
-{
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(unsigned(grid), 1, 1);
-    cfg.blockDim = dim3(S8FewCfg<MT>::THREADS, 1, 1);
-    cfg.dynamicSmemBytes = S8FewCfg<MT>::SMEM_BYTES;
-    cfg.stream = stream;
-    attr->id = cudaLaunchAttributeClusterDimension;
-    attr->val.clusterDim.x = unsigned(ranks);
-    attr->val.clusterDim.y = 1;
-    attr->val.clusterDim.z = 1;
-    cfg.attrs = attr;
-    cfg.numAttrs = 1;
-    return cfg;
-}
-
-template <int MT>
 cudaError_t set_few(S8Capacity *cap)
 {
     cudaError_t e = cudaFuncSetAttribute(tsm_s8_few_kernel<MT>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                          S8FewCfg<MT>::SMEM_BYTES);
     for (int i = 0; e == cudaSuccess && i < S8Capacity::KINDS; ++i) {
+        cudaLaunchConfig_t cfg = {};
+        cfg.gridDim = dim3(unsigned(i + 1), 1, 1);
+        cfg.blockDim = dim3(S8FewCfg<MT>::THREADS, 1, 1);
+        cfg.dynamicSmemBytes = S8FewCfg<MT>::SMEM_BYTES;
         cudaLaunchAttribute attr;
-        const cudaLaunchConfig_t cfg = few_config<MT>(i + 1, i + 1, &attr, nullptr);
+        attr.id = cudaLaunchAttributeClusterDimension;
+        attr.val.clusterDim.x = unsigned(i + 1);
+        attr.val.clusterDim.y = 1;
+        attr.val.clusterDim.z = 1;
+        cfg.attrs = &attr;
+        cfg.numAttrs = 1;
         e = cudaOccupancyMaxActiveClusters(&cap->clusters[i], tsm_s8_few_kernel<MT>, &cfg);
     }
     return e;
@@ -1275,9 +1265,8 @@ template <int MT>
 cudaError_t launch_few(const CUtensorMap &map_a, const CUtensorMap &map_b, const S8Params &p, int grid,
                        cudaStream_t stream)
 {
-    cudaLaunchAttribute attr;
-    const cudaLaunchConfig_t cfg = few_config<MT>(grid * p.ranks, p.ranks, &attr, stream);
-    return cudaLaunchKernelEx(&cfg, tsm_s8_few_kernel<MT>, map_a, map_b, p);
+    return launch_chained(tsm_s8_few_kernel<MT>, dim3(unsigned(grid * p.ranks)), S8FewCfg<MT>::THREADS,
+                          S8FewCfg<MT>::SMEM_BYTES, unsigned(p.ranks), stream, map_a, map_b, p);
 }
 
 }  // namespace
@@ -1310,9 +1299,8 @@ cudaError_t launch_pack_s8(const int8_t *src, int64_t s_ld, int64_t s_stride, in
                            cudaStream_t stream)
 {
     const int64_t blocks = (batch * rows * (d_ld / 16) + 255) / 256;
-    tsm_pack_s8_kernel<<<unsigned(min(blocks, int64_t(sms) * 32)), 256, 0, stream>>>(src, s_ld, s_stride, dst, d_ld,
-                                                                                     d_stride, rows, cols, batch);
-    return cudaGetLastError();
+    return launch_chained(tsm_pack_s8_kernel, dim3(unsigned(min(blocks, int64_t(sms) * 32))), 256, 0, 0, stream, src, s_ld,
+                          s_stride, dst, d_ld, d_stride, rows, cols, batch);
 }
 
 }  // namespace tsm
