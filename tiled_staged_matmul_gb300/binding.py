@@ -308,9 +308,10 @@ def check(status: int) -> None:
 # ------------------------------------------------------------------ torch conveniences
 
 def _stream_handle(stream):
-    import torch
     if stream is None:
-        return torch.cuda.current_stream().cuda_stream
+        # (torch.cuda.current_stream() builds a Stream object, ten times as long)
+        import torch
+        return torch._C._cuda_getCurrentRawStream(torch._C._cuda_getDevice())
     if isinstance(stream, int):
         return stream
     return stream.cuda_stream
@@ -461,31 +462,48 @@ def gemv(A, x, out=None, *, stream=None):
 # Mixture-of-Experts: token rows to their experts and back.  The experts' side
 # is a groups x capacity x width tensor, the layout grouped_gemm takes.
 
+# (The checks below are ordered so that contiguous CUDA tensors, the usual
+# case, pass with few attribute reads: a decode step's calls take the GPU two
+# or three microseconds each.)
+
+_ELEM_TYPES = {}
+
+
 def _elem_type(dtype):
-    import torch
-    code = {torch.float32: 0, torch.float16: 1, torch.bfloat16: 2}.get(dtype)
+    if not _ELEM_TYPES:
+        import torch
+        _ELEM_TYPES.update({torch.float32: 0, torch.float16: 1, torch.bfloat16: 2})
+    code = _ELEM_TYPES.get(dtype)
     if code is None:
         raise TypeError(f"rows must be torch.float32, torch.float16 or torch.bfloat16, not {dtype}")
     return code
 
 
-def _check_slots(slots, tokens):
+def _slots_of(slots):
+    """(tokens, topk) of a slots tensor."""
     import torch
     if slots.dtype != torch.int32 or not slots.is_cuda or slots.dim() != 2 or not slots.is_contiguous():
         raise ValueError("slots must be a contiguous CUDA int32 tensor of tokens x topk values")
-    if slots.shape[0] != tokens:
-        raise ValueError(f"slots are of {slots.shape[0]} tokens, not {tokens}")
+    return slots.shape
 
 
-def _check_token_rows(x, name):
-    if x.dim() != 2 or not x.is_cuda or (x.shape[1] > 1 and x.numel() and x.stride(1) != 1):
-        raise ValueError(f"{name} must be a 2-D CUDA tensor with a unit last stride")
+def _token_pitch(x, tokens, width, dtype, name):
+    """The row pitch of a tokens x width tensor."""
+    if x.dim() != 2 or not x.is_cuda or x.dtype != dtype or x.shape != (tokens, width):
+        raise ValueError(f"{name} must be a {tokens} x {width} CUDA tensor of {dtype}")
+    if x.is_contiguous():
+        return width
+    if width > 1 and x.numel() and x.stride(1) != 1:
+        raise ValueError(f"{name} must have a unit last stride")
+    return x.stride(0) if tokens > 1 else width
 
 
-def _check_expert_rows(rows, width, dtype, name):
-    """The pitch of a groups x capacity x width tensor whose rows are evenly spaced."""
-    if rows.dim() != 3 or not rows.is_cuda or rows.shape[2] != width or rows.dtype != dtype:
+def _expert_pitch(rows, width, dtype, name):
+    """The row pitch of a groups x capacity x width tensor of evenly spaced rows."""
+    if rows.dim() != 3 or not rows.is_cuda or rows.dtype != dtype or rows.shape[2] != width:
         raise ValueError(f"{name} must be a groups x capacity x {width} CUDA tensor of {dtype}")
+    if rows.is_contiguous():
+        return width
     G, cap, _ = rows.shape
     ld = rows.stride(1) if cap > 1 else rows.stride(0) if G > 1 else width
     if rows.numel() and ((width > 1 and rows.stride(2) != 1) or (G > 1 and rows.stride(0) != cap * ld)
@@ -495,11 +513,14 @@ def _check_expert_rows(rows, width, dtype, name):
     return max(ld, width)
 
 
-def _check_weights(weights, slots):
+def _weights_ptr(weights, slots):
     import torch
+    if weights is None:
+        return 0
     if weights.dtype != torch.float32 or not weights.is_cuda or weights.shape != slots.shape \
             or not weights.is_contiguous():
         raise ValueError("weights must be a contiguous CUDA float32 tensor of tokens x topk values")
+    return weights.data_ptr()
 
 
 def moe_route(expert_ids, groups, capacity, *, stream=None):
@@ -512,12 +533,12 @@ def moe_route(expert_ids, groups, capacity, *, stream=None):
     import torch
     if expert_ids.dtype not in (torch.int32, torch.int64) or not expert_ids.is_cuda or expert_ids.dim() != 2:
         raise ValueError("expert_ids must be a 2-D CUDA tensor of int32 or int64")
-    ids = expert_ids.contiguous()
+    ids = expert_ids if expert_ids.is_contiguous() else expert_ids.contiguous()
     T, k = ids.shape
     slots = torch.empty((T, k), dtype=torch.int32, device=ids.device)
     counts = torch.empty((groups,), dtype=torch.int32, device=ids.device)
-    check(moe_route_slots(ids.data_ptr(), ids.element_size(), slots.data_ptr(), counts.data_ptr(), T, k, groups,
-                        capacity, _stream_handle(stream)))
+    check(_lib.moe_route_slots(ids.data_ptr(), ids.element_size(), slots.data_ptr(), counts.data_ptr(), T, k, groups,
+                               capacity, _stream_handle(stream)))
     return slots, counts
 
 
@@ -528,17 +549,16 @@ def moe_dispatch(x, slots, groups, capacity, out=None, *, stream=None):
     ``x`` is tokens x width (f32, f16, bf16 or int8).  Returns ``out`` (groups
     x capacity x width); rows no slot names keep their contents (zeros when
     ``out`` is not given)."""
-    import torch
-    _check_token_rows(x, "x")
-    T, H = x.shape
-    _check_slots(slots, T)
+    T, k = _slots_of(slots)
+    H = x.shape[-1]
+    ldx = _token_pitch(x, T, H, x.dtype, "x")
     if out is None:
-        out = torch.zeros((groups, capacity, H), dtype=x.dtype, device=x.device)
-    if tuple(out.shape) != (groups, capacity, H):
+        out = x.new_zeros((groups, capacity, H))
+    if out.shape != (groups, capacity, H):
         raise ValueError(f"out must be a {groups} x {capacity} x {H} tensor")
-    ld = _check_expert_rows(out, H, x.dtype, "out")
-    check(moe_dispatch_rows(x.data_ptr(), x.element_size(), slots.data_ptr(), out.data_ptr(), T, slots.shape[1],
-                           groups * capacity, H, x.stride(0) if T > 1 else H, ld, _stream_handle(stream)))
+    ld = _expert_pitch(out, H, x.dtype, "out")
+    check(_lib.moe_dispatch_rows(x.data_ptr(), x.element_size(), slots.data_ptr(), out.data_ptr(), T, k,
+                                 groups * capacity, H, ldx, ld, _stream_handle(stream)))
     return out
 
 
@@ -546,18 +566,17 @@ def moe_dispatch_grad(drows, slots, out=None, *, stream=None):
     """The gradient of ``moe_dispatch``: ``dx[t] = sum_j drows[slots[t, j]]``
     for groups x capacity x width ``drows`` (f32, f16 or bf16); summed in f32,
     returned in the rows' type."""
-    import torch
+    code = _elem_type(drows.dtype)
+    T, k = _slots_of(slots)
     G, cap, H = drows.shape
-    ld = _check_expert_rows(drows, H, drows.dtype, "drows")
-    T, k = slots.shape
-    _check_slots(slots, T)
+    ld = _expert_pitch(drows, H, drows.dtype, "drows")
     if out is None:
-        out = torch.empty((T, H), dtype=drows.dtype, device=drows.device)
-    _check_token_rows(out, "out")
-    if tuple(out.shape) != (T, H) or out.dtype != drows.dtype:
-        raise ValueError(f"out must be a {T} x {H} tensor of {drows.dtype}")
-    check(moe_dispatch_rows_grad(drows.data_ptr(), _elem_type(drows.dtype), slots.data_ptr(), out.data_ptr(), T, k,
-                                G * cap, H, ld, out.stride(0) if T > 1 else H, _stream_handle(stream)))
+        out = drows.new_empty((T, H))
+        ldo = H
+    else:
+        ldo = _token_pitch(out, T, H, drows.dtype, "out")
+    check(_lib.moe_dispatch_rows_grad(drows.data_ptr(), code, slots.data_ptr(), out.data_ptr(), T, k, G * cap, H, ld,
+                                      ldo, _stream_handle(stream)))
     return out
 
 
@@ -566,21 +585,18 @@ def moe_combine(rows, slots, weights=None, out=None, *, stream=None):
     ``out[t] = sum_j weights[t, j] * rows[slots[t, j]]`` for groups x capacity
     x width ``rows`` (f32, f16 or bf16), f32 ``weights`` (tokens x topk; none:
     ones); summed in f32, returned in the rows' type."""
-    import torch
+    code = _elem_type(rows.dtype)
+    T, k = _slots_of(slots)
     G, cap, H = rows.shape
-    ld = _check_expert_rows(rows, H, rows.dtype, "rows")
-    T, k = slots.shape
-    _check_slots(slots, T)
-    if weights is not None:
-        _check_weights(weights, slots)
+    ld = _expert_pitch(rows, H, rows.dtype, "rows")
+    w = _weights_ptr(weights, slots)
     if out is None:
-        out = torch.empty((T, H), dtype=rows.dtype, device=rows.device)
-    _check_token_rows(out, "out")
-    if tuple(out.shape) != (T, H) or out.dtype != rows.dtype:
-        raise ValueError(f"out must be a {T} x {H} tensor of {rows.dtype}")
-    check(moe_combine_rows(rows.data_ptr(), _elem_type(rows.dtype), slots.data_ptr(),
-                          weights.data_ptr() if weights is not None else 0, out.data_ptr(), T, k, G * cap, H, ld,
-                          out.stride(0) if T > 1 else H, _stream_handle(stream)))
+        out = rows.new_empty((T, H))
+        ldo = H
+    else:
+        ldo = _token_pitch(out, T, H, rows.dtype, "out")
+    check(_lib.moe_combine_rows(rows.data_ptr(), code, slots.data_ptr(), w, out.data_ptr(), T, k, G * cap, H, ld, ldo,
+                                _stream_handle(stream)))
     return out
 
 
@@ -590,22 +606,20 @@ def moe_combine_grad(dout, rows, slots, weights=None, drows=None, *, stream=None
     their contents, zeros when ``drows`` is not given) and ``dweights[t, j] =
     <dout[t], rows[slots[t, j]]>`` (f32, 0 for a dropped choice)."""
     import torch
-    _check_token_rows(dout, "dout")
-    T, H = dout.shape
-    _check_slots(slots, T)
-    ld = _check_expert_rows(rows, H, dout.dtype, "rows")
-    if weights is not None:
-        _check_weights(weights, slots)
+    code = _elem_type(dout.dtype)
+    T, k = _slots_of(slots)
+    G, cap, H = rows.shape
+    ldd = _token_pitch(dout, T, H, dout.dtype, "dout")
+    ld = _expert_pitch(rows, H, dout.dtype, "rows")
+    w = _weights_ptr(weights, slots)
     if drows is None:
         drows = torch.zeros(rows.shape, dtype=rows.dtype, device=rows.device)
     if drows.shape != rows.shape:
         raise ValueError("drows must have the rows' shape")
-    ldd = _check_expert_rows(drows, H, dout.dtype, "drows")
-    dweights = torch.empty(slots.shape, dtype=torch.float32, device=dout.device)
-    check(moe_combine_rows_grad(dout.data_ptr(), rows.data_ptr(), _elem_type(dout.dtype), slots.data_ptr(),
-                               weights.data_ptr() if weights is not None else 0, drows.data_ptr(),
-                               dweights.data_ptr(), T, slots.shape[1], rows.shape[0] * rows.shape[1], H,
-                               dout.stride(0) if T > 1 else H, ld, ldd, _stream_handle(stream)))
+    ldr = _expert_pitch(drows, H, dout.dtype, "drows")
+    dweights = torch.empty((T, k), dtype=torch.float32, device=dout.device)
+    check(_lib.moe_combine_rows_grad(dout.data_ptr(), rows.data_ptr(), code, slots.data_ptr(), w, drows.data_ptr(),
+                                     dweights.data_ptr(), T, k, G * cap, H, ldd, ld, ldr, _stream_handle(stream)))
     return drows, dweights
 
 
@@ -621,77 +635,94 @@ def quantize_rows(X, group_rows=None, q=None, scales=None, *, stream=None):
     rows that are read and written."""
     import torch
     code = _elem_type(X.dtype)
+    three = X.dim() == 3
     if X.dim() not in (2, 3) or not X.is_cuda or (X.shape[-1] > 1 and X.numel() and X.stride(-1) != 1):
         raise ValueError("X must be a 2-D or 3-D CUDA tensor with a unit last stride")
-    batch = X.shape[0] if X.dim() == 3 else 1
-    M, K = X.shape[-2], X.shape[-1]
+    batch = X.shape[0] if three else 1
+    M, K = X.shape[-2:]
     if q is None:
-        q = torch.empty((*X.shape[:-1], -(-K // 16) * 16), dtype=torch.int8, device=X.device)[..., :K]
+        pitch = -(-K // 16) * 16
+        q = torch.empty((*X.shape[:-1], pitch), dtype=torch.int8, device=X.device)
+        if pitch != K:
+            q = q[..., :K]
+    elif q.shape != X.shape or q.dtype != torch.int8 or (K > 1 and q.numel() and q.stride(-1) != 1):
+        raise ValueError("q must be an int8 tensor of X's shape with a unit last stride")
     if scales is None:
         scales = torch.empty(X.shape[:-1], dtype=torch.float32, device=X.device)
-    if q.shape != X.shape or q.dtype != torch.int8 or (K > 1 and q.numel() and q.stride(-1) != 1):
-        raise ValueError("q must be an int8 tensor of X's shape with a unit last stride")
-    if scales.shape != X.shape[:-1] or scales.dtype != torch.float32 or (M > 1 and scales.stride(-1) != 1):
+    elif scales.shape != X.shape[:-1] or scales.dtype != torch.float32 or (M > 1 and scales.stride(-1) != 1):
         raise ValueError("scales must be a float32 tensor of one value per row")
-    if group_rows is not None and (group_rows.dtype != torch.int32 or not group_rows.is_cuda
-                                   or group_rows.numel() != batch or not group_rows.is_contiguous()):
-        raise ValueError("group_rows must be a contiguous CUDA int32 tensor of one count per matrix")
-    three = X.dim() == 3
-    check(quantize_rows_s8(X.data_ptr(), code, q.data_ptr(), scales.data_ptr(),
-                           group_rows.data_ptr() if group_rows is not None else 0, M, K,
-                           X.stride(-2) if M > 1 else K, q.stride(-2) if M > 1 else K,
-                           X.stride(0) if three else 0, q.stride(0) if three else 0,
-                           scales.stride(0) if three else 0, batch, _stream_handle(stream)))
+    counts = 0
+    if group_rows is not None:
+        if group_rows.dtype != torch.int32 or not group_rows.is_cuda or group_rows.numel() != batch \
+                or not group_rows.is_contiguous():
+            raise ValueError("group_rows must be a contiguous CUDA int32 tensor of one count per matrix")
+        counts = group_rows.data_ptr()
+    check(_lib.quantize_rows_s8(X.data_ptr(), code, q.data_ptr(), scales.data_ptr(), counts, M, K,
+                                X.stride(-2) if M > 1 else K, q.stride(-2) if M > 1 else K,
+                                X.stride(0) if three else 0, q.stride(0) if three else 0,
+                                scales.stride(0) if three else 0, batch, _stream_handle(stream)))
     return q, scales
+
+
+def _s8_vector(t, n, batch, three, name):
+    """(pointer, stride) of a vector of n values, or one per matrix."""
+    import torch
+    if t is None:
+        return 0, 0
+    dim = t.dim()
+    if t.dtype != torch.float32 or not t.is_cuda or t.shape[-1] != n or dim > (2 if three else 1) \
+            or (n > 1 and t.stride(-1) != 1) or (dim == 2 and t.shape[0] != batch):
+        raise ValueError(f"{name} must be a CUDA float32 tensor of {n} values" + (f" (or {batch} x {n})" if three else ""))
+    return t.data_ptr(), t.stride(0) if dim == 2 and batch > 1 else 0
 
 
 def _s8_call(A, B, scale_a, scale_b, group_rows, out, alpha, bias, activation, slope, out_dtype, stream):
     import torch
     if A.dtype != torch.int8 or B.dtype != torch.int8:
         raise TypeError("A and B must be torch.int8")
-    if A.dim() != B.dim() or A.dim() not in (2, 3):
+    dim = A.dim()
+    if dim != B.dim() or dim not in (2, 3):
         raise ValueError("A and B must both be 2-D or both 3-D")
-    three = A.dim() == 3
-    M, K = A.shape[-2], A.shape[-1]
-    N = B.shape[-1]
-    if B.shape[-2] != K:
-        raise ValueError(f"inner sizes differ: {K} vs {B.shape[-2]}")
-    batch = A.shape[0] if three else 1
-    if three and B.shape[0] != batch:
-        raise ValueError("batch sizes differ")
-    dtype = out.dtype if out is not None else (out_dtype or torch.float32)
-    shape = (batch, M, N) if three else (M, N)
+    three = dim == 3
+    if three:
+        batch, M, K = A.shape
+        batch_b, K2, N = B.shape
+        sA, lda, uA = A.stride()
+        sB, ldb, uB = B.stride()
+        if batch_b != batch:
+            raise ValueError("batch sizes differ")
+        shape = (batch, M, N)
+    else:
+        batch, sA, sB = 1, 0, 0
+        M, K = A.shape
+        K2, N = B.shape
+        lda, uA = A.stride()
+        ldb, uB = B.stride()
+        shape = (M, N)
+    if K2 != K:
+        raise ValueError(f"inner sizes differ: {K} vs {K2}")
     if out is None:
         make = torch.empty if group_rows is None else torch.zeros
-        out = make(shape, dtype=dtype, device=A.device)
-    if tuple(out.shape) != shape:
+        out = make(shape, dtype=out_dtype or torch.float32, device=A.device)
+    if out.shape != shape:
         raise ValueError(f"out must be a {' x '.join(map(str, shape))} tensor")
-    for t, name in ((A, "A"), (B, "B"), (out, "out")):
-        if not t.is_cuda or (t.shape[-1] > 1 and t.numel() and t.stride(-1) != 1):
+    sC, ldc, uC = out.stride() if three else (0, *out.stride())
+    for t, unit, n, name in ((A, uA, K, "A"), (B, uB, N, "B"), (out, uC, N, "out")):
+        if not t.is_cuda or (unit != 1 and n > 1 and t.numel()):
             raise ValueError(f"{name} must be a CUDA tensor with a unit last stride")
-
-    def vector(t, n, name):
-        if t is None:
-            return 0, 0
-        if t.dtype != torch.float32 or not t.is_cuda or t.shape[-1] != n or (n > 1 and t.stride(-1) != 1) \
-                or t.dim() > (2 if three else 1) or (t.dim() == 2 and t.shape[0] != batch):
-            raise ValueError(f"{name} must be a CUDA float32 tensor of {n} values"
-                             + (f" (or {batch} x {n})" if three else ""))
-        return t.data_ptr(), t.stride(0) if t.dim() == 2 and batch > 1 else 0
-
-    pa, sa = vector(scale_a, M, "scale_a")
-    pb, sb = vector(scale_b, N, "scale_b")
-    pbias, sbias = vector(bias, N, "bias")
-    epi = epilogue(alpha, pbias, sbias, activation, slope, _elem_type(dtype))
-    args = (M, N, K, A.stride(-2) if M > 1 else max(K, 1), B.stride(-2) if K > 1 else max(N, 1),
-            out.stride(-2) if M > 1 else max(N, 1), A.stride(0) if three else 0, B.stride(0) if three else 0,
-            out.stride(0) if three else 0, sa, sb)
+    pa, sa = _s8_vector(scale_a, M, batch, three, "scale_a")
+    pb, sb = _s8_vector(scale_b, N, batch, three, "scale_b")
+    pbias, sbias = _s8_vector(bias, N, batch, three, "bias")
+    epi = ctypes.byref(GemmEpilogue(alpha, pbias or None, sbias, ACTIVATIONS.get(activation, activation), slope,
+                                    _elem_type(out.dtype)))
+    args = (M, N, K, lda if M > 1 else max(K, 1), ldb if K > 1 else max(N, 1), ldc if M > 1 else max(N, 1), sA, sB,
+            sC, sa, sb)
     if group_rows is None:
-        check(gemm_s8_scaled(A.data_ptr(), B.data_ptr(), out.data_ptr(), pa, pb, *args, batch, epi,
-                             _stream_handle(stream)))
+        check(_lib.gemm_s8_scaled(A.data_ptr(), B.data_ptr(), out.data_ptr(), pa, pb, *args, batch, epi,
+                                  _stream_handle(stream)))
     else:
-        check(gemm_s8_grouped_scaled(A.data_ptr(), B.data_ptr(), out.data_ptr(), pa, pb, group_rows.data_ptr(),
-                                     batch, *args, epi, _stream_handle(stream)))
+        check(_lib.gemm_s8_grouped_scaled(A.data_ptr(), B.data_ptr(), out.data_ptr(), pa, pb, group_rows.data_ptr(),
+                                          batch, *args, epi, _stream_handle(stream)))
     return out
 
 
