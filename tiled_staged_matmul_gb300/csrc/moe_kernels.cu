@@ -141,19 +141,44 @@ struct Piece {
     static constexpr int EB = ET == kOutF32 ? 4 : 2;
     static constexpr int V = VEC ? 16 / EB : 1;
 
-    static __device__ __forceinline__ void load(const void *row, int64_t i, float (&v)[V])
+    // A piece as it lies in memory (kept so while it waits: half the registers).
+    struct Raw {
+        uint32_t w[VEC ? 4 : 1];
+    };
+    static __device__ __forceinline__ Raw get(const void *row, int64_t i)
     {
+        Raw r;
         if constexpr (!VEC) {
-            v[0] = one(static_cast<const char *>(row) + i * EB);
+            if constexpr (ET == kOutF32)
+                r.w[0] = __ldg(static_cast<const uint32_t *>(row) + i);
+            else
+                r.w[0] = __ldg(static_cast<const unsigned short *>(row) + i);
         } else {
             const uint4 u = __ldg(static_cast<const uint4 *>(row) + i);
-            const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+            r.w[0] = u.x;
+            r.w[1] = u.y;
+            r.w[2] = u.z;
+            r.w[3] = u.w;
+        }
+        return r;
+    }
+    static __device__ __forceinline__ void widen(const Raw &raw, float (&v)[V])
+    {
+        if constexpr (!VEC) {
+            if constexpr (ET == kOutF32)
+                v[0] = __uint_as_float(raw.w[0]);
+            else if constexpr (ET == kOutF16)
+                v[0] = __half2float(__ushort_as_half(uint16_t(raw.w[0])));
+            else
+                v[0] = __uint_as_float(raw.w[0] << 16);
+        } else {
+            const uint32_t *w = raw.w;
 #pragma unroll
             for (int k = 0; k < 4; ++k) {
                 if constexpr (ET == kOutF32) {
                     v[k] = __uint_as_float(w[k]);
                 } else if constexpr (ET == kOutF16) {
-                    const float2 f = __half22float2(*reinterpret_cast<const __half2 *>(&w[k]));
+                    const float2 f = __half22float2(*reinterpret_cast<const __half2 *>(w + k));
                     v[2 * k] = f.x;
                     v[2 * k + 1] = f.y;
                 } else {
@@ -188,17 +213,6 @@ struct Piece {
             }
             static_cast<uint4 *>(row)[i] = make_uint4(w[0], w[1], w[2], w[3]);
         }
-    }
-
-private:
-    static __device__ __forceinline__ float one(const char *p)
-    {
-        if constexpr (ET == kOutF32)
-            return __ldg(reinterpret_cast<const float *>(p));
-        else if constexpr (ET == kOutF16)
-            return __half2float(__ushort_as_half(__ldg(reinterpret_cast<const unsigned short *>(p))));
-        else
-            return __uint_as_float(uint32_t(__ldg(reinterpret_cast<const unsigned short *>(p))) << 16);
     }
 };
 
@@ -247,124 +261,120 @@ __global__ void __launch_bounds__(256) tsm_moe_dispatch_kernel(MoveParams p)
 
 // ------------------------------------------------------------- combine
 
-// A thread sums one piece of a token's row over its choices, kSumUnroll rows
-// loaded at a time.
-constexpr int kSumUnroll = 4;
-
-template <int ET, bool VEC>
+// A warp sums U x 32 pieces of a token's row over its choices, K rows at a
+// time: U x K loads of a lane in flight.  Many tokens: U = 4, K = 2, a row's
+// slots read by few warps; few tokens (a decode step): U = 1, K = 8, every
+// warp there is at work and a token's rows loaded in one go.
+template <int ET, bool VEC, int U, int K>
 __global__ void __launch_bounds__(256) tsm_moe_combine_kernel(MoveParams p)
 {
     using P = Piece<ET, VEC>;
     chain_next();
     chain_wait();
+    const int lane = int(threadIdx.x & 31);
     const int64_t pieces = (p.width + P::V - 1) / P::V;
-    const int64_t total = p.tokens * pieces;
-    for (int64_t i = int64_t(blockIdx.x) * blockDim.x + threadIdx.x; i < total;
-         i += int64_t(gridDim.x) * blockDim.x) {
-        const int64_t t = i / pieces;
-        const int64_t c = i - t * pieces;
-        float acc[P::V];
+    const int64_t segs = (pieces + 32 * U - 1) / (32 * U);
+    const int64_t warps = int64_t(gridDim.x) * (blockDim.x / 32);
+    for (int64_t i = int64_t(blockIdx.x) * (blockDim.x / 32) + (threadIdx.x >> 5); i < p.tokens * segs; i += warps) {
+        const int64_t t = i / segs;
+        const int64_t c0 = (i - t * segs) * (32 * U) + lane;
+        float acc[U][P::V];
 #pragma unroll
-        for (int k = 0; k < P::V; ++k)
-            acc[k] = 0.f;
-        for (int64_t j0 = 0; j0 < p.topk; j0 += kSumUnroll) {
-            float v[kSumUnroll][P::V];
-            float w[kSumUnroll];
-            bool on[kSumUnroll];
+        for (int u = 0; u < U; ++u)
 #pragma unroll
-            for (int u = 0; u < kSumUnroll; ++u) {
-                on[u] = false;
-                if (j0 + u < p.topk) {
-                    const int32_t slot = __ldg(p.slots + t * p.topk + j0 + u);
-                    on[u] = has_row(p, slot);
-                    if (on[u]) {
-                        w[u] = p.weights ? __ldg(p.weights + t * p.topk + j0 + u) : 1.f;
-                        P::load(static_cast<const char *>(p.src) + int64_t(slot) * p.ld_src * P::EB, c, v[u]);
-                    }
-                }
+            for (int k = 0; k < P::V; ++k)
+                acc[u][k] = 0.f;
+        for (int64_t j0 = 0; j0 < p.topk; j0 += K) {
+            typename P::Raw raw[K][U];
+            float w[K];
+            bool on[K];
+#pragma unroll
+            for (int j = 0; j < K; ++j) {
+                const bool in = j0 + j < p.topk;
+                const int32_t slot = in ? __ldg(p.slots + t * p.topk + j0 + j) : -1;
+                w[j] = in && p.weights ? __ldg(p.weights + t * p.topk + j0 + j) : 1.f;
+                on[j] = has_row(p, slot);
+                const char *row = static_cast<const char *>(p.src) + int64_t(slot) * p.ld_src * P::EB;
+#pragma unroll
+                for (int u = 0; u < U; ++u)
+                    if (on[j] && c0 + 32 * u < pieces)
+                        raw[j][u] = P::get(row, c0 + 32 * u);
             }
 #pragma unroll
-            for (int u = 0; u < kSumUnroll; ++u)
-                if (on[u]) {
+            for (int j = 0; j < K; ++j)
 #pragma unroll
-                    for (int k = 0; k < P::V; ++k)
-                        acc[k] = fmaf(w[u], v[u][k], acc[k]);
-                }
+                for (int u = 0; u < U; ++u)
+                    if (on[j] && c0 + 32 * u < pieces) {
+                        float v[P::V];
+                        P::widen(raw[j][u], v);
+#pragma unroll
+                        for (int k = 0; k < P::V; ++k)
+                            acc[u][k] = fmaf(w[j], v[k], acc[u][k]);
+                    }
         }
-        P::store(static_cast<char *>(p.dst) + t * p.ld_dst * P::EB, c, acc);
+        char *out = static_cast<char *>(p.dst) + t * p.ld_dst * P::EB;
+#pragma unroll
+        for (int u = 0; u < U; ++u)
+            if (c0 + 32 * u < pieces)
+                P::store(out, c0 + 32 * u, acc[u]);
     }
 }
 
 // ------------------------------------------------------------- combine's gradient
 
-// One CTA per token.  Choices are taken kGradUnroll at a time: each thread
-// walks its pieces of dout once for them, writes w dout and keeps one partial
-// dot product per choice; the partials meet in a fixed order (a butterfly in
-// the warp, then the warps in turn).
-constexpr int kGradUnroll = 6;
-constexpr int kGradThreads = 256;
+// A warp per choice: it walks the token's dout and the choice's row together,
+// kGradUnroll pieces of each in flight per lane, writes w dout and keeps the
+// dot product, which a butterfly adds up in a fixed order.  The warps of a
+// token's choices are neighbours, so dout comes from HBM once and from the L1
+// or L2 for the others; nothing waits for another warp.
+constexpr int kGradUnroll = 4;
 
 template <int ET, bool VEC>
-__global__ void __launch_bounds__(kGradThreads) tsm_moe_combine_grad_kernel(MoveParams p)
+__global__ void __launch_bounds__(256) tsm_moe_combine_grad_kernel(MoveParams p)
 {
     using P = Piece<ET, VEC>;
-    __shared__ float part[kGradThreads / 32][kGradUnroll];
     chain_next();
     chain_wait();
-    const int64_t t = blockIdx.x;
+    const int lane = int(threadIdx.x & 31);
     const int64_t pieces = (p.width + P::V - 1) / P::V;
-    const char *dout = static_cast<const char *>(p.dout) + t * p.ld_dout * P::EB;
-    const int warp = int(threadIdx.x >> 5), lane = int(threadIdx.x & 31);
-    for (int64_t j0 = 0; j0 < p.topk; j0 += kGradUnroll) {
-        float dot[kGradUnroll], w[kGradUnroll];
-        int32_t slot[kGradUnroll];
+    const int64_t warps = int64_t(gridDim.x) * (blockDim.x / 32);
+    for (int64_t i = int64_t(blockIdx.x) * (blockDim.x / 32) + (threadIdx.x >> 5); i < p.tokens * p.topk; i += warps) {
+        const int32_t slot = __ldg(p.slots + i);
+        float dot = 0.f;
+        if (has_row(p, slot)) {
+            const float w = p.weights ? __ldg(p.weights + i) : 1.f;
+            const char *dout = static_cast<const char *>(p.dout) + i / p.topk * p.ld_dout * P::EB;
+            const char *row = static_cast<const char *>(p.src) + int64_t(slot) * p.ld_src * P::EB;
+            char *drow = static_cast<char *>(p.dst) + int64_t(slot) * p.ld_dst * P::EB;
+            for (int64_t c0 = lane; c0 < pieces; c0 += 32 * kGradUnroll) {
+                typename P::Raw d[kGradUnroll], y[kGradUnroll];
 #pragma unroll
-        for (int u = 0; u < kGradUnroll; ++u) {
-            dot[u] = 0.f;
-            w[u] = 0.f;
-            slot[u] = -1;
-            if (j0 + u < p.topk) {
-                slot[u] = __ldg(p.slots + t * p.topk + j0 + u);
-                w[u] = p.weights ? __ldg(p.weights + t * p.topk + j0 + u) : 1.f;
-                if (!has_row(p, slot[u]))
-                    slot[u] = -1;
+                for (int u = 0; u < kGradUnroll; ++u)
+                    if (c0 + 32 * u < pieces) {
+                        d[u] = P::get(dout, c0 + 32 * u);
+                        y[u] = P::get(row, c0 + 32 * u);
+                    }
+#pragma unroll
+                for (int u = 0; u < kGradUnroll; ++u)
+                    if (c0 + 32 * u < pieces) {
+                        float dv[P::V], yv[P::V], s = 0.f;
+                        P::widen(d[u], dv);
+                        P::widen(y[u], yv);
+#pragma unroll
+                        for (int k = 0; k < P::V; ++k) {
+                            s = fmaf(dv[k], yv[k], s);
+                            dv[k] *= w;
+                        }
+                        dot += s;
+                        P::store(drow, c0 + 32 * u, dv);
+                    }
             }
-        }
-        for (int64_t c = threadIdx.x; c < pieces; c += kGradThreads) {
-            float d[P::V];
-            P::load(dout, c, d);
-#pragma unroll
-            for (int u = 0; u < kGradUnroll; ++u) {
-                if (slot[u] < 0)
-                    continue;
-                float y[P::V], g[P::V];
-                P::load(static_cast<const char *>(p.src) + int64_t(slot[u]) * p.ld_src * P::EB, c, y);
-                float s = 0.f;
-#pragma unroll
-                for (int k = 0; k < P::V; ++k) {
-                    s = fmaf(d[k], y[k], s);
-                    g[k] = w[u] * d[k];
-                }
-                dot[u] += s;
-                P::store(static_cast<char *>(p.dst) + int64_t(slot[u]) * p.ld_dst * P::EB, c, g);
-            }
-        }
-#pragma unroll
-        for (int u = 0; u < kGradUnroll; ++u) {
 #pragma unroll
             for (int m = 16; m; m >>= 1)
-                dot[u] += __shfl_xor_sync(0xffffffffu, dot[u], m);
-            if (lane == 0)
-                part[warp][u] = dot[u];
+                dot += __shfl_xor_sync(0xffffffffu, dot, m);
         }
-        __syncthreads();
-        if (threadIdx.x < kGradUnroll && j0 + threadIdx.x < p.topk && p.dweights) {
-            float s = 0.f;
-            for (int k = 0; k < kGradThreads / 32; ++k)
-                s += part[k][threadIdx.x];
-            p.dweights[t * p.topk + j0 + threadIdx.x] = s;
-        }
-        __syncthreads();
+        if (lane == 0 && p.dweights)
+            p.dweights[i] = dot;
     }
 }
 
@@ -394,25 +404,27 @@ __global__ void __launch_bounds__(kQuantThreads) tsm_quantize_rows_kernel(QuantP
     const char *x = static_cast<const char *>(p.X) + (g * p.sX + r * p.ldx) * P::EB;
     int8_t *q = p.q + g * p.sQ + r * p.ldq;
     const int64_t pieces = p.K / P::V;  // whole pieces; the host takes VEC only then
-    float keep[kQuantKeep][P::V];
+    typename P::Raw keep[kQuantKeep];
     uint32_t top = 0;
-#pragma unroll
-    for (int i = 0; i < kQuantKeep; ++i) {
-        const int64_t c = threadIdx.x + int64_t(i) * kQuantThreads;
-        if (c < pieces) {
-            P::load(x, c, keep[i]);
-#pragma unroll
-            for (int k = 0; k < P::V; ++k)
-                top = max(top, __float_as_uint(keep[i][k]) & 0x7fffffffu);
-        }
-    }
-    for (int64_t c = threadIdx.x + int64_t(kQuantKeep) * kQuantThreads; c < pieces; c += kQuantThreads) {
+    auto see = [&](const typename P::Raw &raw) {
         float v[P::V];
-        P::load(x, c, v);
+        P::widen(raw, v);
 #pragma unroll
         for (int k = 0; k < P::V; ++k)
             top = max(top, __float_as_uint(v[k]) & 0x7fffffffu);
+    };
+#pragma unroll
+    for (int i = 0; i < kQuantKeep; ++i) {
+        const int64_t c = threadIdx.x + int64_t(i) * kQuantThreads;
+        if (c < pieces)
+            keep[i] = P::get(x, c);
     }
+#pragma unroll
+    for (int i = 0; i < kQuantKeep; ++i)
+        if (threadIdx.x + int64_t(i) * kQuantThreads < pieces)
+            see(keep[i]);
+    for (int64_t c = threadIdx.x + int64_t(kQuantKeep) * kQuantThreads; c < pieces; c += kQuantThreads)
+        see(P::get(x, c));
     top = __reduce_max_sync(0xffffffffu, top);
     if ((threadIdx.x & 31) == 0)
         part[threadIdx.x >> 5] = top;
@@ -433,7 +445,9 @@ __global__ void __launch_bounds__(kQuantThreads) tsm_quantize_rows_kernel(QuantP
         const float c = fminf(fmaxf(rintf(__fdiv_rn(v, scale)), -127.f), 127.f);
         return uint32_t(int32_t(c)) & 0xffu;
     };
-    auto put = [&](int64_t c, const float (&v)[P::V]) {
+    auto put = [&](int64_t c, const typename P::Raw &raw) {
+        float v[P::V];
+        P::widen(raw, v);
         if constexpr (!VEC) {
             q[c] = int8_t(code(v[0]));
         } else {
@@ -454,11 +468,8 @@ __global__ void __launch_bounds__(kQuantThreads) tsm_quantize_rows_kernel(QuantP
         if (c < pieces)
             put(c, keep[i]);
     }
-    for (int64_t c = threadIdx.x + int64_t(kQuantKeep) * kQuantThreads; c < pieces; c += kQuantThreads) {
-        float v[P::V];
-        P::load(x, c, v);
-        put(c, v);
-    }
+    for (int64_t c = threadIdx.x + int64_t(kQuantKeep) * kQuantThreads; c < pieces; c += kQuantThreads)
+        put(c, P::get(x, c));
 }
 
 template <bool WIDE, int ROUNDS>
@@ -505,69 +516,63 @@ cudaError_t launch_dispatch(const MoveParams &p, int vec, int sms, cudaStream_t 
     }
 }
 
-cudaError_t launch_combine(const MoveParams &p, int elem, bool vec, int sms, cudaStream_t stream)
+namespace {
+
+template <int ET, bool VEC>
+cudaError_t combine_as(const MoveParams &p, int sms, cudaStream_t stream)
 {
-    const int64_t v = vec ? (elem == kOutF32 ? 4 : 8) : 1;
-    const int64_t blocks = (p.tokens * ((p.width + v - 1) / v) + 255) / 256;
-    const unsigned grid = unsigned(min(blocks, int64_t(sms) * 64));
-    if (vec) {
-        if (elem == kOutF32)
-            return launch_chained(tsm_moe_combine_kernel<kOutF32, true>, dim3(grid), 256, 0, 0, stream, p);
-        else if (elem == kOutF16)
-            return launch_chained(tsm_moe_combine_kernel<kOutF16, true>, dim3(grid), 256, 0, 0, stream, p);
-        else
-            return launch_chained(tsm_moe_combine_kernel<kOutBF16, true>, dim3(grid), 256, 0, 0, stream, p);
-    } else {
-        if (elem == kOutF32)
-            return launch_chained(tsm_moe_combine_kernel<kOutF32, false>, dim3(grid), 256, 0, 0, stream, p);
-        else if (elem == kOutF16)
-            return launch_chained(tsm_moe_combine_kernel<kOutF16, false>, dim3(grid), 256, 0, 0, stream, p);
-        else
-            return launch_chained(tsm_moe_combine_kernel<kOutBF16, false>, dim3(grid), 256, 0, 0, stream, p);
-    }
-    return cudaGetLastError();
+    const int64_t pieces = (p.width + Piece<ET, VEC>::V - 1) / Piece<ET, VEC>::V;
+    const auto grid = [&](int u) {
+        const int64_t blocks = (p.tokens * ((pieces + 32 * u - 1) / (32 * u)) + 7) / 8;
+        return dim3(unsigned(min(blocks, int64_t(sms) * 64)));
+    };
+    if (p.tokens * pieces < int64_t(sms) * 1024)
+        return launch_chained(tsm_moe_combine_kernel<ET, VEC, 1, 8>, grid(1), 256, 0, 0, stream, p);
+    return launch_chained(tsm_moe_combine_kernel<ET, VEC, 4, 2>, grid(4), 256, 0, 0, stream, p);
 }
 
-cudaError_t launch_combine_grad(const MoveParams &p, int elem, bool vec, cudaStream_t stream)
+template <int ET, bool VEC>
+cudaError_t combine_grad_as(const MoveParams &p, int sms, cudaStream_t stream)
 {
-    const unsigned grid = unsigned(p.tokens);
-    if (vec) {
-        if (elem == kOutF32)
-            return launch_chained(tsm_moe_combine_grad_kernel<kOutF32, true>, dim3(grid), kGradThreads, 0, 0, stream, p);
-        else if (elem == kOutF16)
-            return launch_chained(tsm_moe_combine_grad_kernel<kOutF16, true>, dim3(grid), kGradThreads, 0, 0, stream, p);
-        else
-            return launch_chained(tsm_moe_combine_grad_kernel<kOutBF16, true>, dim3(grid), kGradThreads, 0, 0, stream, p);
-    } else {
-        if (elem == kOutF32)
-            return launch_chained(tsm_moe_combine_grad_kernel<kOutF32, false>, dim3(grid), kGradThreads, 0, 0, stream, p);
-        else if (elem == kOutF16)
-            return launch_chained(tsm_moe_combine_grad_kernel<kOutF16, false>, dim3(grid), kGradThreads, 0, 0, stream, p);
-        else
-            return launch_chained(tsm_moe_combine_grad_kernel<kOutBF16, false>, dim3(grid), kGradThreads, 0, 0, stream, p);
+    const int64_t blocks = (p.tokens * p.topk + 7) / 8;
+    return launch_chained(tsm_moe_combine_grad_kernel<ET, VEC>, dim3(unsigned(min(blocks, int64_t(sms) * 64))), 256, 0,
+                          0, stream, p);
+}
+
+}  // namespace
+
+cudaError_t launch_combine(const MoveParams &p, int elem, bool vec, int sms, cudaStream_t stream)
+{
+    switch (elem) {
+    case kOutF32: return vec ? combine_as<kOutF32, true>(p, sms, stream) : combine_as<kOutF32, false>(p, sms, stream);
+    case kOutF16: return vec ? combine_as<kOutF16, true>(p, sms, stream) : combine_as<kOutF16, false>(p, sms, stream);
+    default: return vec ? combine_as<kOutBF16, true>(p, sms, stream) : combine_as<kOutBF16, false>(p, sms, stream);
     }
-    return cudaGetLastError();
+}
+
+cudaError_t launch_combine_grad(const MoveParams &p, int elem, bool vec, int sms, cudaStream_t stream)
+{
+    switch (elem) {
+    case kOutF32: return vec ? combine_grad_as<kOutF32, true>(p, sms, stream) : combine_grad_as<kOutF32, false>(p, sms, stream);
+    case kOutF16: return vec ? combine_grad_as<kOutF16, true>(p, sms, stream) : combine_grad_as<kOutF16, false>(p, sms, stream);
+    default: return vec ? combine_grad_as<kOutBF16, true>(p, sms, stream) : combine_grad_as<kOutBF16, false>(p, sms, stream);
+    }
+}
+
+template <bool VEC>
+static cudaError_t quantize_as(const QuantParams &p, int elem, cudaStream_t stream)
+{
+    const dim3 grid(unsigned(p.M * p.batch));
+    switch (elem) {
+    case kOutF32: return launch_chained(tsm_quantize_rows_kernel<kOutF32, VEC>, grid, kQuantThreads, 0, 0, stream, p);
+    case kOutF16: return launch_chained(tsm_quantize_rows_kernel<kOutF16, VEC>, grid, kQuantThreads, 0, 0, stream, p);
+    default: return launch_chained(tsm_quantize_rows_kernel<kOutBF16, VEC>, grid, kQuantThreads, 0, 0, stream, p);
+    }
 }
 
 cudaError_t launch_quantize_rows(const QuantParams &p, int elem, bool vec, cudaStream_t stream)
 {
-    const unsigned grid = unsigned(p.M * p.batch);
-    if (vec) {
-        if (elem == kOutF32)
-            return launch_chained(tsm_quantize_rows_kernel<kOutF32, true>, dim3(grid), kQuantThreads, 0, 0, stream, p);
-        else if (elem == kOutF16)
-            return launch_chained(tsm_quantize_rows_kernel<kOutF16, true>, dim3(grid), kQuantThreads, 0, 0, stream, p);
-        else
-            return launch_chained(tsm_quantize_rows_kernel<kOutBF16, true>, dim3(grid), kQuantThreads, 0, 0, stream, p);
-    } else {
-        if (elem == kOutF32)
-            return launch_chained(tsm_quantize_rows_kernel<kOutF32, false>, dim3(grid), kQuantThreads, 0, 0, stream, p);
-        else if (elem == kOutF16)
-            return launch_chained(tsm_quantize_rows_kernel<kOutF16, false>, dim3(grid), kQuantThreads, 0, 0, stream, p);
-        else
-            return launch_chained(tsm_quantize_rows_kernel<kOutBF16, false>, dim3(grid), kQuantThreads, 0, 0, stream, p);
-    }
-    return cudaGetLastError();
+    return vec ? quantize_as<true>(p, elem, stream) : quantize_as<false>(p, elem, stream);
 }
 
 }  // namespace tsm

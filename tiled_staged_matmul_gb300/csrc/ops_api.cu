@@ -304,7 +304,7 @@ gemm_status_t moe_combine_rows_grad(const void *dout, const void *rows_in, int32
     p.ld_src = ld_rows;
     p.ld_dst = ld_drows;
     p.ld_dout = ld_dout;
-    const cudaError_t e = launch_combine_grad(p, elem_type, (all & 15u) == 0, reinterpret_cast<cudaStream_t>(stream));
+    const cudaError_t e = launch_combine_grad(p, elem_type, (all & 15u) == 0, ds->sms, reinterpret_cast<cudaStream_t>(stream));
     return e == cudaSuccess ? GEMM_OK : fail_cuda(e, "combine gradient launch");
 }
 

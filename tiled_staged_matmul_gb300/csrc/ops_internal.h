@@ -45,7 +45,7 @@ struct MoveParams {
 cudaError_t launch_dispatch(const MoveParams &p, int vec, int sms, cudaStream_t stream);
 // `vec`: 16-byte accesses (every row 16-byte aligned), else element by element.
 cudaError_t launch_combine(const MoveParams &p, int elem, bool vec, int sms, cudaStream_t stream);
-cudaError_t launch_combine_grad(const MoveParams &p, int elem, bool vec, cudaStream_t stream);
+cudaError_t launch_combine_grad(const MoveParams &p, int elem, bool vec, int sms, cudaStream_t stream);
 
 // ------------------------------------------------------------- row quantisation
 
