@@ -135,62 +135,58 @@ __global__ void __launch_bounds__(32 * kRouteWarps) tsm_moe_rank_kernel(RoutePar
 
 // ------------------------------------------------------------- row types
 
-// One access of V elements of type ET (V x element size = 16 bytes, or V = 1).
-template <int ET, bool VEC>
+// One access of BYTES bytes (16, 4 or one element) of type ET.
+template <int ET, int BYTES>
 struct Piece {
     static constexpr int EB = ET == kOutF32 ? 4 : 2;
-    static constexpr int V = VEC ? 16 / EB : 1;
+    static constexpr int V = BYTES / EB;
+    static_assert(BYTES == 16 || BYTES == 4 || BYTES == EB, "piece");
 
     // A piece as it lies in memory (kept so while it waits: half the registers).
     struct Raw {
-        uint32_t w[VEC ? 4 : 1];
+        uint32_t w[BYTES == 16 ? 4 : 1];
     };
     static __device__ __forceinline__ Raw get(const void *row, int64_t i)
     {
         Raw r;
-        if constexpr (!VEC) {
-            if constexpr (ET == kOutF32)
-                r.w[0] = __ldg(static_cast<const uint32_t *>(row) + i);
-            else
-                r.w[0] = __ldg(static_cast<const unsigned short *>(row) + i);
-        } else {
+        if constexpr (BYTES == 16) {
             const uint4 u = __ldg(static_cast<const uint4 *>(row) + i);
             r.w[0] = u.x;
             r.w[1] = u.y;
             r.w[2] = u.z;
             r.w[3] = u.w;
+        } else if constexpr (BYTES == 4) {
+            r.w[0] = __ldg(static_cast<const uint32_t *>(row) + i);
+        } else {
+            r.w[0] = __ldg(static_cast<const unsigned short *>(row) + i);
         }
         return r;
     }
     static __device__ __forceinline__ void widen(const Raw &raw, float (&v)[V])
     {
-        if constexpr (!VEC) {
-            if constexpr (ET == kOutF32)
-                v[0] = __uint_as_float(raw.w[0]);
-            else if constexpr (ET == kOutF16)
-                v[0] = __half2float(__ushort_as_half(uint16_t(raw.w[0])));
-            else
-                v[0] = __uint_as_float(raw.w[0] << 16);
-        } else {
-            const uint32_t *w = raw.w;
+        if constexpr (ET == kOutF32) {
 #pragma unroll
-            for (int k = 0; k < 4; ++k) {
-                if constexpr (ET == kOutF32) {
-                    v[k] = __uint_as_float(w[k]);
-                } else if constexpr (ET == kOutF16) {
-                    const float2 f = __half22float2(*reinterpret_cast<const __half2 *>(w + k));
+            for (int k = 0; k < V; ++k)
+                v[k] = __uint_as_float(raw.w[k]);
+        } else if constexpr (V == 1) {
+            v[0] = ET == kOutF16 ? __half2float(__ushort_as_half(uint16_t(raw.w[0]))) : __uint_as_float(raw.w[0] << 16);
+        } else {
+#pragma unroll
+            for (int k = 0; k < V / 2; ++k) {
+                if constexpr (ET == kOutF16) {
+                    const float2 f = __half22float2(*reinterpret_cast<const __half2 *>(raw.w + k));
                     v[2 * k] = f.x;
                     v[2 * k + 1] = f.y;
                 } else {
-                    v[2 * k] = __uint_as_float(w[k] << 16);
-                    v[2 * k + 1] = __uint_as_float(w[k] & 0xffff0000u);
+                    v[2 * k] = __uint_as_float(raw.w[k] << 16);
+                    v[2 * k + 1] = __uint_as_float(raw.w[k] & 0xffff0000u);
                 }
             }
         }
     }
     static __device__ __forceinline__ void store(void *row, int64_t i, const float (&v)[V])
     {
-        if constexpr (!VEC) {
+        if constexpr (V == 1) {
             if constexpr (ET == kOutF32)
                 static_cast<float *>(row)[i] = v[0];
             else if constexpr (ET == kOutF16)
@@ -198,9 +194,9 @@ struct Piece {
             else
                 static_cast<__nv_bfloat16 *>(row)[i] = __float2bfloat16_rn(v[0]);
         } else {
-            uint32_t w[4];
+            uint32_t w[BYTES / 4];
 #pragma unroll
-            for (int k = 0; k < 4; ++k) {
+            for (int k = 0; k < BYTES / 4; ++k) {
                 if constexpr (ET == kOutF32) {
                     w[k] = __float_as_uint(v[k]);
                 } else if constexpr (ET == kOutF16) {
@@ -211,7 +207,10 @@ struct Piece {
                     w[k] = *reinterpret_cast<const uint32_t *>(&h);
                 }
             }
-            static_cast<uint4 *>(row)[i] = make_uint4(w[0], w[1], w[2], w[3]);
+            if constexpr (BYTES == 16)
+                static_cast<uint4 *>(row)[i] = make_uint4(w[0], w[1], w[2], w[3]);
+            else
+                static_cast<uint32_t *>(row)[i] = w[0];
         }
     }
 };
@@ -262,17 +261,19 @@ __global__ void __launch_bounds__(256) tsm_moe_dispatch_kernel(MoveParams p)
 // ------------------------------------------------------------- combine
 
 // A warp sums U x 32 pieces of a token's row over its choices, K rows at a
-// time: U x K loads of a lane in flight.  Many tokens: U = 4, K = 2, a row's
-// slots read by few warps; few tokens (a decode step): U = 1, K = 8, every
-// warp there is at work and a token's rows loaded in one go.
-template <int ET, bool VEC, int U, int K>
+// time: U x K loads of a lane in flight.  Many tokens: U = 2, K = 2 (8192
+// tokens, 2 choices, 4096 bf16: 36 us, 0.83 of the copy rate; U = 4 41 us, with
+// fewer warps on an SM; K = 4 59 us, half its loads without a row); few tokens (a
+// decode step): U = 1, K = 8, every warp there is at work and a token's rows
+// loaded in one go.
+template <int ET, int BYTES, int U, int K>
 __global__ void __launch_bounds__(256) tsm_moe_combine_kernel(MoveParams p)
 {
-    using P = Piece<ET, VEC>;
+    using P = Piece<ET, BYTES>;
     chain_next();
     chain_wait();
     const int lane = int(threadIdx.x & 31);
-    const int64_t pieces = (p.width + P::V - 1) / P::V;
+    const int64_t pieces = p.width / P::V;
     const int64_t segs = (pieces + 32 * U - 1) / (32 * U);
     const int64_t warps = int64_t(gridDim.x) * (blockDim.x / 32);
     for (int64_t i = int64_t(blockIdx.x) * (blockDim.x / 32) + (threadIdx.x >> 5); i < p.tokens * segs; i += warps) {
@@ -329,14 +330,14 @@ __global__ void __launch_bounds__(256) tsm_moe_combine_kernel(MoveParams p)
 // or L2 for the others; nothing waits for another warp.
 constexpr int kGradUnroll = 4;
 
-template <int ET, bool VEC>
+template <int ET, int BYTES>
 __global__ void __launch_bounds__(256) tsm_moe_combine_grad_kernel(MoveParams p)
 {
-    using P = Piece<ET, VEC>;
+    using P = Piece<ET, BYTES>;
     chain_next();
     chain_wait();
     const int lane = int(threadIdx.x & 31);
-    const int64_t pieces = (p.width + P::V - 1) / P::V;
+    const int64_t pieces = p.width / P::V;
     const int64_t warps = int64_t(gridDim.x) * (blockDim.x / 32);
     for (int64_t i = int64_t(blockIdx.x) * (blockDim.x / 32) + (threadIdx.x >> 5); i < p.tokens * p.topk; i += warps) {
         const int32_t slot = __ldg(p.slots + i);
@@ -384,26 +385,40 @@ __global__ void __launch_bounds__(256) tsm_moe_combine_grad_kernel(MoveParams p)
 //   a row with an infinity or a NaN: scale NaN, q 0, so that its products are NaN)
 //
 // One CTA per row; a row of up to kQuantKeep pieces per thread stays in
-// registers between the maximum and the rounding, so it is read once.  The
-// quotient is the IEEE division, so the codes are those of the formula in f32
-// whatever the launch shape.
-constexpr int kQuantThreads = 256;
-constexpr int kQuantKeep = 4;
+// registers between the maximum and the rounding, so it is read once.
+//
+// The codes are those of the IEEE quotient in f32, but few divisions are made:
+// x times the rounded reciprocal of the scale is within 127 x 2^-22 of it, and
+// where that is further than 1e-4 from the middle between two integers both
+// round alike; only the others (one in 5000) are divided.  Adding 1.5 x 2^23
+// rounds to the nearest integer, ties to even, and leaves it in the low bits:
+// no conversion either.  (8191 x 8192 bf16: 66 us with a division and a
+// conversion for each code, 3x us so; the copy floor is 30.)
+//
+// TPR threads take a row: a warp (eight rows a block, nothing to wait for)
+// where that gives a lane no more than kQuantKeep pieces, else 128; 256 where
+// there are too few rows to fill the GPU.
+constexpr int kQuantKeep = 8;
 
-template <int ET, bool VEC>
-__global__ void __launch_bounds__(kQuantThreads) tsm_quantize_rows_kernel(QuantParams p)
+template <int ET, int BYTES, int TPR>
+__global__ void __launch_bounds__(TPR < 256 && TPR > 32 ? TPR : 256) tsm_quantize_rows_kernel(QuantParams p)
 {
-    using P = Piece<ET, VEC>;
-    __shared__ uint32_t part[kQuantThreads / 32];
+    using P = Piece<ET, BYTES>;
+    constexpr int ROWS = TPR == 32 ? 8 : 1;  // per block
+    __shared__ uint32_t part[TPR / 32];
     chain_next();
     chain_wait();
-    const int64_t g = blockIdx.x / p.M;
-    const int64_t r = blockIdx.x - g * p.M;
+    const int64_t at = int64_t(blockIdx.x) * ROWS + (ROWS > 1 ? threadIdx.x >> 5 : 0);
+    if (at >= p.M * p.batch)
+        return;
+    const int tid = int(threadIdx.x) % TPR;
+    const int64_t g = at / p.M;
+    const int64_t r = at - g * p.M;
     if (p.group_rows && r >= int64_t(__ldg(p.group_rows + g)))
         return;
     const char *x = static_cast<const char *>(p.X) + (g * p.sX + r * p.ldx) * P::EB;
     int8_t *q = p.q + g * p.sQ + r * p.ldq;
-    const int64_t pieces = p.K / P::V;  // whole pieces; the host takes VEC only then
+    const int64_t pieces = p.K / P::V;
     typename P::Raw keep[kQuantKeep];
     uint32_t top = 0;
     auto see = [&](const typename P::Raw &raw) {
@@ -415,47 +430,74 @@ __global__ void __launch_bounds__(kQuantThreads) tsm_quantize_rows_kernel(QuantP
     };
 #pragma unroll
     for (int i = 0; i < kQuantKeep; ++i) {
-        const int64_t c = threadIdx.x + int64_t(i) * kQuantThreads;
+        const int64_t c = tid + int64_t(i) * TPR;
         if (c < pieces)
             keep[i] = P::get(x, c);
     }
 #pragma unroll
     for (int i = 0; i < kQuantKeep; ++i)
-        if (threadIdx.x + int64_t(i) * kQuantThreads < pieces)
+        if (tid + int64_t(i) * TPR < pieces)
             see(keep[i]);
-    for (int64_t c = threadIdx.x + int64_t(kQuantKeep) * kQuantThreads; c < pieces; c += kQuantThreads)
+    for (int64_t c = tid + int64_t(kQuantKeep) * TPR; c < pieces; c += TPR)
         see(P::get(x, c));
     top = __reduce_max_sync(0xffffffffu, top);
-    if ((threadIdx.x & 31) == 0)
-        part[threadIdx.x >> 5] = top;
-    __syncthreads();
+    if constexpr (TPR > 32) {
+        if ((tid & 31) == 0)
+            part[tid >> 5] = top;
+        __syncthreads();
 #pragma unroll
-    for (int k = 0; k < kQuantThreads / 32; ++k)
-        top = max(top, part[k]);
+        for (int k = 0; k < TPR / 32; ++k)
+            top = max(top, part[k]);
+    }
     // As bits of non-negative floats the maximum orders infinities and NaNs last.
     const bool finite = top < 0x7f800000u;
     const float scale = finite ? __fdiv_rn(__uint_as_float(top), 127.f) : __uint_as_float(0x7fffffffu);
     const bool zero = !finite || scale == 0.f;
-    if (threadIdx.x == 0)
+    if (tid == 0)
         p.scales[g * p.sS + r] = scale;
-    auto code = [&](float v) -> uint32_t {
-        if (zero)
-            return 0u;
-        // |v / scale| can pass 127 by a rounding (or, where the scale is subnormal, by more).
-        const float c = fminf(fmaxf(rintf(__fdiv_rn(v, scale)), -127.f), 127.f);
-        return uint32_t(int32_t(c)) & 0xffu;
+    const float inverse = __frcp_rn(scale);
+    const bool divide = !(inverse < __uint_as_float(0x7f800000u));  // (a subnormal scale)
+    auto exactly = [&](float v) {
+        // |v / scale| can pass 127 by more than a rounding where the scale is subnormal.
+        return fminf(fmaxf(rintf(__fdiv_rn(v, scale)), -127.f), 127.f);
+    };
+    constexpr float kMagic = 12582912.f;  // 1.5 x 2^23
+    // Codes of a piece's values, in the low bytes of the results.
+    auto codes = [&](const float (&v)[P::V], uint32_t (&out)[P::V]) {
+        float near = 0.f;
+#pragma unroll
+        for (int k = 0; k < P::V; ++k) {
+            const float y = v[k] * inverse;
+            const float t = y + kMagic;
+            near = fmaxf(near, fabsf(y - (t - kMagic)));
+            out[k] = __float_as_uint(t);
+        }
+        if (near > 0.4999f || divide) {
+#pragma unroll
+            for (int k = 0; k < P::V; ++k)
+                out[k] = __float_as_uint(exactly(v[k]) + kMagic);
+        }
+        if (zero) {
+#pragma unroll
+            for (int k = 0; k < P::V; ++k)
+                out[k] = 0u;
+        }
     };
     auto put = [&](int64_t c, const typename P::Raw &raw) {
         float v[P::V];
+        uint32_t o[P::V];
         P::widen(raw, v);
-        if constexpr (!VEC) {
-            q[c] = int8_t(code(v[0]));
+        codes(v, o);
+        if constexpr (P::V == 1) {
+            q[c] = int8_t(o[0]);
+        } else if constexpr (P::V == 2) {
+            reinterpret_cast<unsigned short *>(q)[c] = uint16_t(__byte_perm(o[0], o[1], 0x0040));
         } else {
             uint32_t w[P::V / 4];
 #pragma unroll
             for (int k = 0; k < P::V / 4; ++k)
-                w[k] = code(v[4 * k]) | code(v[4 * k + 1]) << 8 | code(v[4 * k + 2]) << 16 |
-                       code(v[4 * k + 3]) << 24;
+                w[k] = __byte_perm(__byte_perm(o[4 * k], o[4 * k + 1], 0x0040),
+                                   __byte_perm(o[4 * k + 2], o[4 * k + 3], 0x0040), 0x5410);
             if constexpr (P::V == 8)
                 reinterpret_cast<uint2 *>(q)[c] = make_uint2(w[0], w[1]);
             else
@@ -464,11 +506,11 @@ __global__ void __launch_bounds__(kQuantThreads) tsm_quantize_rows_kernel(QuantP
     };
 #pragma unroll
     for (int i = 0; i < kQuantKeep; ++i) {
-        const int64_t c = threadIdx.x + int64_t(i) * kQuantThreads;
+        const int64_t c = tid + int64_t(i) * TPR;
         if (c < pieces)
             put(c, keep[i]);
     }
-    for (int64_t c = threadIdx.x + int64_t(kQuantKeep) * kQuantThreads; c < pieces; c += kQuantThreads)
+    for (int64_t c = tid + int64_t(kQuantKeep) * TPR; c < pieces; c += TPR)
         put(c, P::get(x, c));
 }
 
@@ -518,61 +560,76 @@ cudaError_t launch_dispatch(const MoveParams &p, int vec, int sms, cudaStream_t 
 
 namespace {
 
-template <int ET, bool VEC>
+template <int ET, int BYTES>
 cudaError_t combine_as(const MoveParams &p, int sms, cudaStream_t stream)
 {
-    const int64_t pieces = (p.width + Piece<ET, VEC>::V - 1) / Piece<ET, VEC>::V;
+    const int64_t pieces = p.width / Piece<ET, BYTES>::V;
     const auto grid = [&](int u) {
         const int64_t blocks = (p.tokens * ((pieces + 32 * u - 1) / (32 * u)) + 7) / 8;
         return dim3(unsigned(min(blocks, int64_t(sms) * 64)));
     };
     if (p.tokens * pieces < int64_t(sms) * 1024)
-        return launch_chained(tsm_moe_combine_kernel<ET, VEC, 1, 8>, grid(1), 256, 0, 0, stream, p);
-    return launch_chained(tsm_moe_combine_kernel<ET, VEC, 4, 2>, grid(4), 256, 0, 0, stream, p);
+        return launch_chained(tsm_moe_combine_kernel<ET, BYTES, 1, 8>, grid(1), 256, 0, 0, stream, p);
+    return launch_chained(tsm_moe_combine_kernel<ET, BYTES, 2, 2>, grid(2), 256, 0, 0, stream, p);
 }
 
-template <int ET, bool VEC>
+template <int ET, int BYTES>
 cudaError_t combine_grad_as(const MoveParams &p, int sms, cudaStream_t stream)
 {
     const int64_t blocks = (p.tokens * p.topk + 7) / 8;
-    return launch_chained(tsm_moe_combine_grad_kernel<ET, VEC>, dim3(unsigned(min(blocks, int64_t(sms) * 64))), 256, 0,
+    return launch_chained(tsm_moe_combine_grad_kernel<ET, BYTES>, dim3(unsigned(min(blocks, int64_t(sms) * 64))), 256, 0,
                           0, stream, p);
 }
 
 }  // namespace
 
-cudaError_t launch_combine(const MoveParams &p, int elem, bool vec, int sms, cudaStream_t stream)
+namespace {
+
+// fn with a type and a piece size fixed at compile time.
+template <typename F>
+cudaError_t with_piece(int elem, int bytes, F &&fn)
 {
     switch (elem) {
-    case kOutF32: return vec ? combine_as<kOutF32, true>(p, sms, stream) : combine_as<kOutF32, false>(p, sms, stream);
-    case kOutF16: return vec ? combine_as<kOutF16, true>(p, sms, stream) : combine_as<kOutF16, false>(p, sms, stream);
-    default: return vec ? combine_as<kOutBF16, true>(p, sms, stream) : combine_as<kOutBF16, false>(p, sms, stream);
+    case kOutF32: return bytes == 16 ? fn(Piece<kOutF32, 16>{}) : fn(Piece<kOutF32, 4>{});
+    case kOutF16:
+        return bytes == 16 ? fn(Piece<kOutF16, 16>{}) : bytes == 4 ? fn(Piece<kOutF16, 4>{}) : fn(Piece<kOutF16, 2>{});
+    default:
+        return bytes == 16 ? fn(Piece<kOutBF16, 16>{}) : bytes == 4 ? fn(Piece<kOutBF16, 4>{}) : fn(Piece<kOutBF16, 2>{});
     }
 }
 
-cudaError_t launch_combine_grad(const MoveParams &p, int elem, bool vec, int sms, cudaStream_t stream)
+template <int ET, int BYTES>
+cudaError_t quantize_as(const QuantParams &p, int sms, cudaStream_t stream)
 {
-    switch (elem) {
-    case kOutF32: return vec ? combine_grad_as<kOutF32, true>(p, sms, stream) : combine_grad_as<kOutF32, false>(p, sms, stream);
-    case kOutF16: return vec ? combine_grad_as<kOutF16, true>(p, sms, stream) : combine_grad_as<kOutF16, false>(p, sms, stream);
-    default: return vec ? combine_grad_as<kOutBF16, true>(p, sms, stream) : combine_grad_as<kOutBF16, false>(p, sms, stream);
-    }
+    const int64_t rows = p.M * p.batch, pieces = p.K / Piece<ET, BYTES>::V;
+    if (rows < int64_t(sms) * 4)
+        return launch_chained(tsm_quantize_rows_kernel<ET, BYTES, 256>, dim3(unsigned(rows)), 256, 0, 0, stream, p);
+    if (pieces <= 32 * kQuantKeep)
+        return launch_chained(tsm_quantize_rows_kernel<ET, BYTES, 32>, dim3(unsigned((rows + 7) / 8)), 256, 0, 0, stream, p);
+    return launch_chained(tsm_quantize_rows_kernel<ET, BYTES, 128>, dim3(unsigned(rows)), 128, 0, 0, stream, p);
 }
 
-template <bool VEC>
-static cudaError_t quantize_as(const QuantParams &p, int elem, cudaStream_t stream)
+// The type and piece size of a Piece as template arguments of fn.
+template <int ET, int BYTES>
+constexpr int type_of(Piece<ET, BYTES>) { return ET; }
+template <int ET, int BYTES>
+constexpr int bytes_of(Piece<ET, BYTES>) { return BYTES; }
+
+}  // namespace
+
+cudaError_t launch_combine(const MoveParams &p, int elem, int bytes, int sms, cudaStream_t stream)
 {
-    const dim3 grid(unsigned(p.M * p.batch));
-    switch (elem) {
-    case kOutF32: return launch_chained(tsm_quantize_rows_kernel<kOutF32, VEC>, grid, kQuantThreads, 0, 0, stream, p);
-    case kOutF16: return launch_chained(tsm_quantize_rows_kernel<kOutF16, VEC>, grid, kQuantThreads, 0, 0, stream, p);
-    default: return launch_chained(tsm_quantize_rows_kernel<kOutBF16, VEC>, grid, kQuantThreads, 0, 0, stream, p);
-    }
+    return with_piece(elem, bytes, [&](auto x) { return combine_as<type_of(decltype(x){}), bytes_of(decltype(x){})>(p, sms, stream); });
 }
 
-cudaError_t launch_quantize_rows(const QuantParams &p, int elem, bool vec, cudaStream_t stream)
+cudaError_t launch_combine_grad(const MoveParams &p, int elem, int bytes, int sms, cudaStream_t stream)
 {
-    return vec ? quantize_as<true>(p, elem, stream) : quantize_as<false>(p, elem, stream);
+    return with_piece(elem, bytes, [&](auto x) { return combine_grad_as<type_of(decltype(x){}), bytes_of(decltype(x){})>(p, sms, stream); });
+}
+
+cudaError_t launch_quantize_rows(const QuantParams &p, int elem, int bytes, int sms, cudaStream_t stream)
+{
+    return with_piece(elem, bytes, [&](auto x) { return quantize_as<type_of(decltype(x){}), bytes_of(decltype(x){})>(p, sms, stream); });
 }
 
 }  // namespace tsm

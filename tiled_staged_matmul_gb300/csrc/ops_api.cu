@@ -71,6 +71,13 @@ int64_t span(int64_t rows, int64_t width, int64_t ld, int64_t elem)
     return span_bytes(1, 0, rows, ld, width, elem);
 }
 
+// Bytes of one access: 16 or 4 where every address, pitch and width in `all`
+// (or-ed together, in bytes) is a multiple, else one element.
+int access_bytes(uint64_t all, int64_t elem)
+{
+    return (all & 15u) == 0 ? 16 : (all & 3u) == 0 ? 4 : int(elem);
+}
+
 // What the four movement calls share: sizes of both sides and the slots.
 gemm_status_t check_move(int64_t tokens, int64_t topk, int64_t rows, int64_t width, int64_t ld_tokens,
                          int64_t ld_rows)
@@ -232,7 +239,7 @@ gemm_status_t combine(const void *rows_in, int32_t elem_type, const int32_t *slo
     p.width = width;
     p.ld_src = ld_rows;
     p.ld_dst = ld_out;
-    const cudaError_t e = launch_combine(p, elem_type, (all & 15u) == 0, ds->sms, stream);
+    const cudaError_t e = launch_combine(p, elem_type, access_bytes(all, eb), ds->sms, stream);
     return e == cudaSuccess ? GEMM_OK : fail_cuda(e, "combine launch");
 }
 
@@ -304,7 +311,7 @@ gemm_status_t moe_combine_rows_grad(const void *dout, const void *rows_in, int32
     p.ld_src = ld_rows;
     p.ld_dst = ld_drows;
     p.ld_dout = ld_dout;
-    const cudaError_t e = launch_combine_grad(p, elem_type, (all & 15u) == 0, ds->sms, reinterpret_cast<cudaStream_t>(stream));
+    const cudaError_t e = launch_combine_grad(p, elem_type, access_bytes(all, eb), ds->sms, reinterpret_cast<cudaStream_t>(stream));
     return e == cudaSuccess ? GEMM_OK : fail_cuda(e, "combine gradient launch");
 }
 
@@ -338,10 +345,12 @@ gemm_status_t quantize_rows_s8(const void *X, int32_t elem_type, int8_t *q, floa
     if ((st = current(&dev, &ds)) != GEMM_OK || (st = check_on_device(buf, 4, dev)) != GEMM_OK)
         return st;
     QuantParams p = {X, q, scales, group_rows, M, K, ldx, ldq, strideX, strideQ, scale_stride, batch};
-    const int64_t v = 16 / eb;  // elements per 16 bytes: as many bytes of q
-    const bool vec = K % v == 0 && !misaligned(X, 16) && !misaligned(q, v) && (M == 1 || (ldx % v == 0 && ldq % v == 0)) &&
-                     (batch == 1 || (strideX % v == 0 && strideQ % v == 0));
-    const cudaError_t e = launch_quantize_rows(p, elem_type, vec, reinterpret_cast<cudaStream_t>(stream));
+    // (A piece's codes are as many bytes as it has elements.)
+    const uint64_t x_all = reinterpret_cast<uintptr_t>(X) | uint64_t(K * eb) | uint64_t(M > 1 ? ldx * eb : 0) |
+                           uint64_t(batch > 1 ? strideX * eb : 0);
+    const uint64_t q_all = reinterpret_cast<uintptr_t>(q) | uint64_t(M > 1 ? ldq : 0) | uint64_t(batch > 1 ? strideQ : 0);
+    const int bytes = access_bytes(x_all | q_all * uint64_t(eb), eb);
+    const cudaError_t e = launch_quantize_rows(p, elem_type, bytes, ds->sms, reinterpret_cast<cudaStream_t>(stream));
     return e == cudaSuccess ? GEMM_OK : fail_cuda(e, "row quantisation launch");
 }
 

@@ -43,9 +43,10 @@ struct MoveParams {
 };
 // dispatch moves whole rows as units of `vec` bytes (16, 8, 4, 2 or 1).
 cudaError_t launch_dispatch(const MoveParams &p, int vec, int sms, cudaStream_t stream);
-// `vec`: 16-byte accesses (every row 16-byte aligned), else element by element.
-cudaError_t launch_combine(const MoveParams &p, int elem, bool vec, int sms, cudaStream_t stream);
-cudaError_t launch_combine_grad(const MoveParams &p, int elem, bool vec, int sms, cudaStream_t stream);
+// `bytes` of one access: 16, 4 or an element's; every row is aligned to it and a
+// multiple of it long.
+cudaError_t launch_combine(const MoveParams &p, int elem, int bytes, int sms, cudaStream_t stream);
+cudaError_t launch_combine_grad(const MoveParams &p, int elem, int bytes, int sms, cudaStream_t stream);
 
 // ------------------------------------------------------------- row quantisation
 
@@ -56,7 +57,7 @@ struct QuantParams {
     const int32_t *group_rows;  // null, or the rows of each batch that are computed
     int64_t M, K, ldx, ldq, sX, sQ, sS, batch;
 };
-cudaError_t launch_quantize_rows(const QuantParams &p, int elem, bool vec, cudaStream_t stream);
+cudaError_t launch_quantize_rows(const QuantParams &p, int elem, int bytes, int sms, cudaStream_t stream);
 
 // ------------------------------------------------------------- int8 products
 
