@@ -29,11 +29,13 @@ ACTIVATIONS = ["none", "relu", "leaky_relu", "gelu", "gelu_tanh", "silu"]
 UNITS = ([("gemm_kernels.cu", "gemm_kernels", [])] +
          [("gemm_epi.cu", f"gemm_epi_{a}", [f"-DTSM_EPI_ACT={i}"]) for i, a in enumerate(ACTIVATIONS)] +
          [("rowsum_kernels.cu", "rowsum_kernels", []), ("moe_kernels.cu", "moe_kernels", []),
-          ("s8_kernels.cu", "s8_kernels", []), ("gemm_api.cu", "gemm_api", []),
-          ("ops_api.cu", "ops_api", [])])
+          ("s8_kernels.cu", "s8_kernels", [])] +
+         [("s8_tiled.cu", f"s8_tiled_{a}", [f"-DTSM_S8_ACT={i}"]) for i, a in enumerate(ACTIVATIONS)] +
+         [("gemm_api.cu", "gemm_api", []), ("ops_api.cu", "ops_api", [])])
 HOST_SOURCES = ("gemm_api.cu", "ops_api.cu")
 SOURCES = sorted({u[0] for u in UNITS})
-HEADERS = ["api_internal.h", "gemm_internal.h", "gemm_kernel.cuh", "launch.cuh", "ops_internal.h", "ptx.cuh", "s8_ptx.cuh"]
+HEADERS = ["api_internal.h", "gemm_internal.h", "gemm_kernel.cuh", "launch.cuh", "ops_internal.h", "ptx.cuh", "s8_common.cuh",
+           "s8_ptx.cuh"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 
 

@@ -445,8 +445,10 @@ gemm_status_t launch_product(S8Params p, DeviceState *ds, cudaStream_t stream)
     if (g_s8_error[dev] != cudaSuccess)
         return fail_cuda(g_s8_error[dev], "setting up the int8 product kernels");
 
-    const S8Kind kind = p.M <= 16 ? S8Kind::kFew16 : p.M <= 32 ? S8Kind::kFew32
-                        : p.M <= 128 ? S8Kind::kOne : S8Kind::kPair;
+    // Few rows by M; in groups of up to 32 rows most have far fewer, so those
+    // are cut into sixteens and only the rows there are cost anything.
+    const S8Kind kind = p.M <= 16 || (p.group_rows && p.M <= 32) ? S8Kind::kFew16
+                        : p.M <= 32 ? S8Kind::kFew32 : p.M <= 128 ? S8Kind::kOne : S8Kind::kPair;
     const bool few = p.M <= 32;
     const S8Shape shape = s8_shape(kind);
     p.tiles_m = int32_t((int64_t(p.M) + shape.tile_m - 1) / shape.tile_m);
@@ -456,8 +458,8 @@ gemm_status_t launch_product(S8Params p, DeviceState *ds, cudaStream_t stream)
     p.workers = kind == S8Kind::kPair ? ds->sms / 2 : ds->sms;
     p.timeout_ns = 2000000000ull + uint64_t(p.kb) * 20000ull;
     p.tag = next_launch_epoch() >> 16;
-    const int64_t per4 = p.epi.out_type == kOutF32 ? 16 : 8;
-    p.vec_c = !misaligned(p.C, per4) && p.ldc % 4 == 0 && (p.batch == 1 || p.sC % 4 == 0);
+    const int64_t per16 = 16 / p.epi.out_bytes();
+    p.vec_c = !misaligned(p.C, 16) && p.ldc % per16 == 0 && (p.batch == 1 || p.sC % per16 == 0);
 
     // Workspace: packed copies of operands that cannot be addressed, then the
     // pieces' sums and arrival words.
@@ -472,8 +474,9 @@ gemm_status_t launch_product(S8Params p, DeviceState *ds, cudaStream_t stream)
     S8Schedule sched = {};
     int grid = 0;
     if (few) {
-        // (A grouped launch's tiles are counted on the device: at most these.)
-        p.ranks = few_rows_ranks(tiles, p.kb, g_s8_capacity[dev], kind == S8Kind::kFew32, &grid);
+        // (A grouped launch's tiles are counted on the device; the estimate is
+        // for one block of rows in every group.)
+        p.ranks = few_rows_ranks(p.group_rows ? int64_t(p.tiles_n) * p.batch : tiles, p.kb, g_s8_capacity[dev], kind == S8Kind::kFew32, &grid);
     } else {
         sched.plan(int32_t(tiles), p.kb, p.workers);
         grid = p.group_rows ? p.workers

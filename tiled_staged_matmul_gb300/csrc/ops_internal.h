@@ -115,7 +115,7 @@ struct S8Params {
     int32_t group_m;            // raster: tiles of M walked together
     int32_t workers;
     int32_t ranks;              // few rows: CTAs (a cluster) that cut a tile's K
-    int32_t vec_c;              // C's rows take stores of four elements
+    int32_t vec_c;              // C's rows are 16-byte aligned
     int32_t *partial;           // sums of pieces: two slots per worker
     unsigned long long *arrivals;  // one word per part of a shared tile: launch tag, count
     unsigned long long tag;     // 48 bits, unique to the launch
@@ -136,6 +136,12 @@ struct S8Capacity {
     int clusters[KINDS];
 };
 cudaError_t set_s8_attributes(S8Capacity *cap);
+// The tiled kernels for activation ACT (s8_tiled.cu, one unit per activation).
+template <int ACT>
+cudaError_t set_s8_tiled();
+template <int ACT>
+cudaError_t launch_s8_tiled(const CUtensorMap &map_a, const CUtensorMap &map_b, const S8Params &p, bool pair, int grid,
+                            cudaStream_t stream);
 cudaError_t launch_s8(const CUtensorMap &map_a, const CUtensorMap &map_b, const S8Params &p, S8Kind kind, int grid,
                       cudaStream_t stream);
 // Rows of `cols` bytes into rows 16-byte aligned and `d_ld` apart.

@@ -1,0 +1,191 @@
+// s8_common.cuh -- products of 8-bit integers with a scale per row and per
+// column:
+//
+//   C[i][j] = act(alpha * scale_a[i] * scale_b[j] * S[i][j] + bias[j]),
+//   S[i][j] = sum_k A[i][k] B[k][j]   (the exact 32-bit integer)
+//
+// The tensor cores' rate for 8-bit integers on this part is a small fraction
+// of their f16 rate, but f16 holds every integer up to 2048 exactly, so the
+// f16 pipe can do the work: a product of two codes is at most 2^14, exact in
+// the f32 accumulator, and so is the sum of 1024 of them (2^24).  The kernels
+// therefore feed the codes as f16 and take the accumulator out into 32-bit
+// integers every 1024 of K: S is exact, whatever the order of the pieces.
+//
+// A code becomes f16 without a conversion instruction: byte c of a word, sign
+// bit flipped (c + 128), placed below the byte 0x64 is the f16 number
+// 1024 + (c + 128); subtracting 1152 leaves c, exactly.  Five instructions
+// turn four codes into two f16 pairs.
+#pragma once
+
+#include "gemm_kernel.cuh"
+#include "launch.cuh"
+#include "ops_internal.h"
+#include "s8_ptx.cuh"
+
+namespace tsm {
+
+// Four codes (k, k+1, k+2, k+3 of a word) as two f16 pairs.
+__device__ __forceinline__ void codes_to_f16(uint32_t w, uint32_t &lo, uint32_t &hi)
+{
+    const uint32_t u = w ^ 0x80808080u;
+    const uint32_t l = __byte_perm(u, 0x64646464u, 0x4140);
+    const uint32_t h = __byte_perm(u, 0x64646464u, 0x4342);
+    const __half2 off = __half2half2(__ushort_as_half(0x6480));  // 1152
+    const __half2 a = __hsub2(*reinterpret_cast<const __half2 *>(&l), off);
+    const __half2 b = __hsub2(*reinterpret_cast<const __half2 *>(&h), off);
+    lo = *reinterpret_cast<const uint32_t *>(&a);
+    hi = *reinterpret_cast<const uint32_t *>(&b);
+}
+
+// The tiled kernel's shape (s8_tiled.cu).  PAIR: a CTA pair per 256 x 256 tile,
+// else one CTA per 128 x 128.
+template <bool PAIR>
+struct S8Cfg {
+    static constexpr int ROWS = 128;
+    static constexpr int CTAS = PAIR ? 2 : 1;
+    static constexpr int TILE_M = ROWS * CTAS;
+    static constexpr int B_COLS = 128;          // columns of B staged by one CTA
+    static constexpr int TILE_N = B_COLS * CTAS;  // the MMA's width
+    static constexpr int HC = TILE_N / 2;       // columns of one epilogue half
+    static constexpr int BK = 128;
+    static constexpr int A_CODES = ROWS * BK;   // bytes
+    static constexpr int B_CODES = B_COLS * BK;
+    static constexpr int CODE_STAGE = A_CODES + B_CODES;
+    static constexpr int F_BOX = 64 * BK * 2;   // 64 columns of f16
+    static constexpr int F_STAGE = 2 * F_BOX;
+    static constexpr int S1 = 3, S2 = 3;        // ring depths
+    static constexpr int STAGING = 8 * 32 * 64;   // per epilogue warp: 32 rows of 64 bytes
+    static constexpr int CTRL = 4096, GROUP_TABLE_OFF = 1024, TERMS_OFF = 2048;
+    static constexpr int SMEM_BYTES = 1024 + S1 * CODE_STAGE + S2 * F_STAGE + STAGING + CTRL;
+    static_assert(SMEM_BYTES <= 232448, "227 KiB per block");
+    static constexpr uint32_t A_COL = 256;      // TMEM: the accumulator, then the f16 A ring
+    static_assert(A_COL + S2 * (BK / 2) <= 512 && TILE_N <= 256, "TMEM columns");
+    static constexpr int PARTS = 2 * CTAS;      // (CTA, half) parts of a tile
+    static constexpr int32_t SLOT_INTS = PARTS * ROWS * HC;
+};
+
+// Where a tile lies.
+struct S8Tile {
+    int32_t m0, n0, z, rows;
+};
+
+__device__ __forceinline__ S8Tile tile_at(int32_t t, const S8Params &p, uint32_t gtab, int tile_m, int tile_n)
+{
+    S8Tile w;
+    int32_t tiles_m = p.tiles_m;
+    if (p.group_rows) {
+        int32_t lo = 0, hi = p.batch - 1;
+        while (lo < hi) {
+            const int32_t mid = (lo + hi) >> 1;
+            if (int32_t(ptx::ld_shared_u32(gtab + 4u * mid)) > t)
+                hi = mid;
+            else
+                lo = mid + 1;
+        }
+        const int32_t first = lo ? int32_t(ptx::ld_shared_u32(gtab + 4u * (lo - 1))) : 0;
+        tiles_m = (int32_t(ptx::ld_shared_u32(gtab + 4u * lo)) - first) / p.tiles_n;
+        t -= first;
+        w.z = lo;
+        w.rows = min(max(p.group_rows[lo], 0), p.M);
+    } else {
+        const int32_t per = p.tiles_m * p.tiles_n;
+        w.z = t / per;
+        t -= w.z * per;
+        w.rows = p.M;
+    }
+    const int32_t group = p.group_m * p.tiles_n;
+    const int32_t g = t / group;
+    const int32_t first_m = g * p.group_m;
+    const int32_t in_group = min(tiles_m - first_m, p.group_m);
+    const int32_t r = t - g * group;
+    w.m0 = (first_m + r % in_group) * tile_m;
+    w.n0 = r / in_group * tile_n;
+    return w;
+}
+
+// Bounded mbarrier wait, as wait_bounded, with nothing kept in registers
+// between waits: the CTA's abort flag is the word at `flag` in shared memory
+// (in a pair, at the same place in the peer), the limit and the status word
+// are the launch's.  ACQ_CLUSTER: the phase counts another CTA's arrivals.
+template <bool PAIR, bool ACQ_CLUSTER = false>
+__device__ __forceinline__ bool s8_wait(uint32_t bar, uint32_t parity, uint32_t flag, const S8Params &p, uint32_t who,
+                                        bool honor_abort = true)
+{
+    auto try_wait = [&]() {
+        return ACQ_CLUSTER ? ptx::mbar_try_wait_cluster(bar, parity) : ptx::mbar_try_wait(bar, parity);
+    };
+    if (try_wait())
+        return true;
+    const uint64_t t0 = ptx::globaltimer_ns();
+    for (uint32_t it = 1;; ++it) {
+        if (try_wait())
+            return true;
+        if ((it & 31u) == 0) {
+            if (honor_abort && ptx::ld_shared_u32(flag))
+                return false;
+            if (ptx::globaltimer_ns() - t0 > p.timeout_ns) {
+                ptx::st_shared_u32(flag, 1u);
+                if (PAIR)
+                    ptx::st_cluster_u32(ptx::mapa_shared(flag, ptx::cluster_ctarank() ^ 1u), 1u);
+                atomicOr(p.status, who);
+                return false;
+            }
+        }
+    }
+}
+
+// Add a chunk's f32 sums (HC columns of a TMEM lane) to the lane's integers.
+// 1.5 * 2^23 + f has f + kMagicBits as its bits while |f| < 2^22, so an
+// addition and an integer addition do what a conversion does at an eighth of
+// their rate (8192^3: 744 -> 7xx us).  A sum can reach 2^24, though it takes
+// codes near the limits with one sign to do so: where one of a warp's passes
+// 2^22, the warp converts those eight columns.  Eight columns are on their way
+// while eight are added.
+constexpr uint32_t kMagicBits = 0x4b400000u;  // of 1.5 * 2^23
+
+template <int HC>
+__device__ __forceinline__ void add_chunk(uint32_t acc, int32_t (&sum)[HC])
+{
+    const float magic = __uint_as_float(kMagicBits);
+    uint32_t r[2][8];
+    ptx::tmem_ld_32x32b_x8(acc, r[0]);
+#pragma unroll
+    for (int c = 0; c < HC / 8; ++c) {
+        ptx::tmem_wait_ld(r[c & 1]);
+        if (c + 1 < HC / 8)
+            ptx::tmem_ld_32x32b_x8(acc + 8u * (c + 1), r[(c + 1) & 1]);
+        float f[8];
+#pragma unroll
+        for (int j = 0; j < 8; ++j)
+            f[j] = __uint_as_float(r[c & 1][j]);
+        const float top = ptx::max_abs3(ptx::max_abs3(ptx::max_abs3(f[0], f[1], f[2]), f[3], f[4]), f[5],
+                                        ptx::max_abs3(f[6], f[7], 0.f));
+        if (__any_sync(0xffffffffu, top >= 4194304.f)) {
+#pragma unroll
+            for (int j = 0; j < 8; ++j)
+                sum[8 * c + j] += __float2int_rn(f[j]) + int32_t(kMagicBits);
+        } else {
+#pragma unroll
+            for (int j = 0; j < 8; ++j)
+                sum[8 * c + j] += __float_as_int(f[j] + magic);
+        }
+    }
+}
+
+// Arrive on a barrier of the pair's leader.  Released to the CTA only: what the
+// arrival stands for is complete in this SM before it is sent -- f16 in its own
+// shared memory (the proxy fence) or TMEM (the store wait), or TMEM read out
+// (the load wait) -- and is next touched by this SM's own tensor core.
+// Released to the cluster, every arrival would first wait for the warp's other
+// stores, global ones included: measured 1.34 times the whole kernel's time at
+// 8192^3 (1028 against 770 us).
+template <bool PAIR>
+__device__ __forceinline__ void arrive_leader(uint32_t bar)
+{
+    if constexpr (PAIR)
+        ptx::mbar_arrive_remote(bar);
+    else
+        ptx::mbar_arrive(bar);
+}
+
+}  // namespace tsm

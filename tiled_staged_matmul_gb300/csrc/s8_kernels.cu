@@ -1,758 +1,11 @@
-// s8_kernels.cu -- products of 8-bit integers with a scale per row and per
-// column:
-//
-//   C[i][j] = act(alpha * scale_a[i] * scale_b[j] * S[i][j] + bias[j]),
-//   S[i][j] = sum_k A[i][k] B[k][j]   (the exact 32-bit integer)
-//
-// The tensor cores' rate for 8-bit integers on this part is a small fraction
-// of their f16 rate, but f16 holds every integer up to 2048 exactly, so the
-// f16 pipe can do the work: a product of two codes is at most 2^14, exact in
-// the f32 accumulator, and so is the sum of 1024 of them (2^24).  The kernels
-// therefore feed the codes as f16 and take the accumulator out into 32-bit
-// integers every 1024 of K: S is exact, whatever the order of the pieces.
-//
-// A code becomes f16 without a conversion instruction: byte c of a word, sign
-// bit flipped (c + 128), placed below the byte 0x64 is the f16 number
-// 1024 + (c + 128); subtracting 1152 leaves c, exactly.  Five instructions
-// turn four codes into two f16 pairs.
-#include "gemm_kernel.cuh"
-#include "launch.cuh"
-#include "ops_internal.h"
-#include "s8_ptx.cuh"
+// s8_kernels.cu -- the 8-bit products' kernel for few rows, the repacking of
+// operands that TMA cannot address, and the launches (s8_common.cuh says what
+// is computed; s8_tiled.cu holds the tiled kernels).
+#include "s8_common.cuh"
 
 namespace tsm {
 
 namespace {
-
-constexpr int kChunkBlocks = 8;  // k-blocks of 128 whose sums the f32 accumulator holds exactly
-
-// Four codes (k, k+1, k+2, k+3 of a word) as two f16 pairs.
-__device__ __forceinline__ void codes_to_f16(uint32_t w, uint32_t &lo, uint32_t &hi)
-{
-    const uint32_t u = w ^ 0x80808080u;
-    const uint32_t l = __byte_perm(u, 0x64646464u, 0x4140);
-    const uint32_t h = __byte_perm(u, 0x64646464u, 0x4342);
-    const __half2 off = __half2half2(__ushort_as_half(0x6480));  // 1152
-    const __half2 a = __hsub2(*reinterpret_cast<const __half2 *>(&l), off);
-    const __half2 b = __hsub2(*reinterpret_cast<const __half2 *>(&h), off);
-    lo = *reinterpret_cast<const uint32_t *>(&a);
-    hi = *reinterpret_cast<const uint32_t *>(&b);
-}
-
-// ------------------------------------------------------------- tiled kernel
-//
-// One persistent CTA (or CTA pair) per SM (pair of SMs), warp-specialised:
-//   warp 0       TMA producer: codes of A (128 rows x 128 k) and B (128 k x 128
-//                columns) into the code ring
-//   warp 1       MMA issuer (the pair's leader): A from TMEM, B from shared memory
-//   warps 4-7    A's codes -> f16 -> TMEM, one row per lane (they never pass
-//                through shared memory as f16)
-//   warps 8-11   B's codes -> f16 -> the 128-byte swizzled layout of the MMA
-//   warps 12-19  two per TMEM lane quarter, one per column half of the tile:
-//                accumulator -> 32-bit sums, then the epilogue
-// The bound is shared-memory bandwidth: a 256 x 256 x 128 block costs an SM
-// 32 KB of codes in, 32 KB out to the converters, 32 KB of f16 B written and
-// 32 KB read by the MMAs = 1024 cycles at 128 bytes, just the time its MMAs
-// take; with A's f16 in shared memory too it would be 1.5 times that.  A's f16
-// ring takes the TMEM columns a second accumulator would need, so the MMAs
-// pause while a chunk of 1024 k is read out.  (Two accumulators of half the
-// width would not: but the MMA runs at full rate only at its full width, 256
-// columns for a pair.)
-template <bool PAIR>
-struct S8Cfg {
-    static constexpr int ROWS = 128;
-    static constexpr int CTAS = PAIR ? 2 : 1;
-    static constexpr int TILE_M = ROWS * CTAS;
-    static constexpr int B_COLS = 128;          // columns of B staged by one CTA
-    static constexpr int TILE_N = B_COLS * CTAS;  // the MMA's width
-    static constexpr int HC = TILE_N / 2;       // columns of one epilogue half
-    static constexpr int BK = 128;
-    static constexpr int A_CODES = ROWS * BK;   // bytes
-    static constexpr int B_CODES = B_COLS * BK;
-    static constexpr int CODE_STAGE = A_CODES + B_CODES;
-    static constexpr int F_BOX = 64 * BK * 2;   // 64 columns of f16
-    static constexpr int F_STAGE = 2 * F_BOX;
-    static constexpr int S1 = 3, S2 = 3;        // ring depths
-    static constexpr int STAGING = 8 * 32 * 32 * 4;
-    static constexpr int CTRL = 2048, GROUP_TABLE_OFF = 1024;
-    static constexpr int SMEM_BYTES = 1024 + S1 * CODE_STAGE + S2 * F_STAGE + STAGING + CTRL;
-    static_assert(SMEM_BYTES <= 232448, "227 KiB per block");
-    static constexpr uint32_t A_COL = 256;      // TMEM: the accumulator, then the f16 A ring
-    static_assert(A_COL + S2 * (BK / 2) <= 512 && TILE_N <= 256, "TMEM columns");
-    static constexpr int PARTS = 2 * CTAS;      // (CTA, half) parts of a tile
-    static constexpr int32_t SLOT_INTS = PARTS * ROWS * HC;
-};
-
-constexpr int kWarpA = 4, kWarpB = 8, kWarpDrain = 12, kS8Warps = 20;  // first warps of the roles
-constexpr int kS8Threads = 32 * kS8Warps;
-// Registers per thread by warpgroup (five of 128 threads): together exactly
-// what the block was launched with (640 x 96).
-constexpr int kS8RegsIssue = 48, kS8RegsConvert = 56, kS8RegsDrain = 160;
-static_assert(128 * kS8RegsIssue + 2 * 128 * kS8RegsConvert + 2 * 128 * kS8RegsDrain <= kS8Threads * 96,
-              "register split");
-
-// B's shared-memory descriptor: MN-major, 64-column boxes of BK rows of 128 bytes.
-template <bool PAIR>
-__device__ __forceinline__ uint64_t desc_b_s8(uint32_t saddr)
-{
-    return desc_common() | (uint64_t(S8Cfg<PAIR>::F_BOX >> 4) << 16) | uint64_t((saddr & 0x3FFFFu) >> 4);
-}
-
-// The schedule in shared memory, read field by field: the registers are for
-// the sums.  WARP: a whole warp reads it together, and the compiler is told
-// that the values are the warp's (they then need no register per lane).
-template <bool WARP>
-struct SharedSchedule {
-    uint32_t at;
-    __device__ __forceinline__ int32_t field(int i) const
-    {
-        const int32_t v = int32_t(ptx::ld_shared_u32(at + 4u * i));
-        return WARP ? __shfl_sync(0xffffffffu, v, 0) : v;
-    }
-    __device__ __forceinline__ void put(const S8Schedule &s) const
-    {
-        ptx::st_shared_u32(at, uint32_t(s.tiles));
-        ptx::st_shared_u32(at + 4, uint32_t(s.shared));
-        ptx::st_shared_u32(at + 8, uint32_t(s.kb));
-        ptx::st_shared_u32(at + 12, uint32_t(s.workers));
-        ptx::st_shared_u32(at + 16, uint32_t(s.cutters));
-    }
-    __device__ __forceinline__ int32_t tiles() const { return field(0); }
-    __device__ __forceinline__ int32_t kb() const { return field(2); }
-    __device__ __forceinline__ int32_t workers() const { return field(3); }
-    __device__ __forceinline__ S8Schedule all() const
-    {
-        S8Schedule s;
-        s.tiles = tiles();
-        s.shared = field(1);
-        s.kb = kb();
-        s.workers = workers();
-        s.cutters = field(4);
-        return s;
-    }
-};
-
-// One worker's pieces in order: its share of the cut tiles, then whole tiles.
-template <bool WARP>
-struct PieceWalk {
-    int32_t cur, end, next;  // blocks of the cut tiles; next whole tile
-    int32_t tile, kb0, kb1;
-    __device__ __forceinline__ PieceWalk(const SharedSchedule<WARP> &shared, int32_t w)
-    {
-        const S8Schedule s = shared.all();
-        const bool cuts = s.shared > 0 && w < s.cutters;
-        cur = cuts ? s.piece_begin(w) : 0;
-        end = cuts ? s.piece_begin(w + 1) : 0;
-        next = s.shared + w;
-        tile = kb0 = kb1 = 0;
-    }
-    __device__ __forceinline__ bool advance(const SharedSchedule<WARP> &s)
-    {
-        kb0 = 0;
-        kb1 = s.kb();
-        if (cur < end) {
-            tile = cur / kb1;
-            kb0 = cur - tile * kb1;
-            kb1 = min(kb1, kb0 + (end - cur));
-            cur += kb1 - kb0;
-            return true;
-        }
-        tile = next;
-        next += s.workers();
-        return tile < s.tiles();
-    }
-};
-
-// Where a tile lies.
-struct S8Tile {
-    int32_t m0, n0, z, rows;
-};
-
-__device__ __forceinline__ S8Tile tile_at(int32_t t, const S8Params &p, uint32_t gtab, int tile_m, int tile_n)
-{
-    S8Tile w;
-    int32_t tiles_m = p.tiles_m;
-    if (p.group_rows) {
-        int32_t lo = 0, hi = p.batch - 1;
-        while (lo < hi) {
-            const int32_t mid = (lo + hi) >> 1;
-            if (int32_t(ptx::ld_shared_u32(gtab + 4u * mid)) > t)
-                hi = mid;
-            else
-                lo = mid + 1;
-        }
-        const int32_t first = lo ? int32_t(ptx::ld_shared_u32(gtab + 4u * (lo - 1))) : 0;
-        tiles_m = (int32_t(ptx::ld_shared_u32(gtab + 4u * lo)) - first) / p.tiles_n;
-        t -= first;
-        w.z = lo;
-        w.rows = min(max(p.group_rows[lo], 0), p.M);
-    } else {
-        const int32_t per = p.tiles_m * p.tiles_n;
-        w.z = t / per;
-        t -= w.z * per;
-        w.rows = p.M;
-    }
-    const int32_t group = p.group_m * p.tiles_n;
-    const int32_t g = t / group;
-    const int32_t first_m = g * p.group_m;
-    const int32_t in_group = min(tiles_m - first_m, p.group_m);
-    const int32_t r = t - g * group;
-    w.m0 = (first_m + r % in_group) * tile_m;
-    w.n0 = r / in_group * tile_n;
-    return w;
-}
-
-// Count one arrival on `word` (a whole warp calls it): true for the last of
-// `total`.  The word holds the launch's tag and the count; under another tag
-// (whatever the workspace's last user left there) the count is none.  The
-// first exchange expects everyone else to have arrived, so that the last one,
-// whom the result waits for, is done after one trip to L2.  Any other failed
-// exchange means that another of the at most `total` contributors has arrived,
-// so the loop ends.  The loop is the warp's, not one lane's, so that the
-// compiler need not plan for a warp that has come apart.
-__device__ __forceinline__ bool arrive_last(unsigned long long *word, unsigned long long tag, uint32_t total, int lane)
-{
-    unsigned long long old = (tag << 16) | (total - 1u);
-    for (;;) {
-        const uint32_t seen = (old >> 16) == tag ? uint32_t(old & 0xffffu) : 0u;
-        unsigned long long prev = 0;
-        if (lane == 0)
-            prev = atomicCAS(word, old, (tag << 16) | (seen + 1u));
-        prev = __shfl_sync(0xffffffffu, prev, 0);
-        if (prev == old)
-            return seen + 1u == total;
-        old = prev;
-    }
-}
-
-// Bounded mbarrier wait, as wait_bounded, with nothing kept in registers
-// between waits: the CTA's abort flag is the word at `flag` in shared memory
-// (in a pair, at the same place in the peer), the limit and the status word
-// are the launch's.  ACQ_CLUSTER: the phase counts another CTA's arrivals.
-template <bool PAIR, bool ACQ_CLUSTER = false>
-__device__ __forceinline__ bool s8_wait(uint32_t bar, uint32_t parity, uint32_t flag, const S8Params &p, uint32_t who,
-                                        bool honor_abort = true)
-{
-    auto try_wait = [&]() {
-        return ACQ_CLUSTER ? ptx::mbar_try_wait_cluster(bar, parity) : ptx::mbar_try_wait(bar, parity);
-    };
-    if (try_wait())
-        return true;
-    const uint64_t t0 = ptx::globaltimer_ns();
-    for (uint32_t it = 1;; ++it) {
-        if (try_wait())
-            return true;
-        if ((it & 31u) == 0) {
-            if (honor_abort && ptx::ld_shared_u32(flag))
-                return false;
-            if (ptx::globaltimer_ns() - t0 > p.timeout_ns) {
-                ptx::st_shared_u32(flag, 1u);
-                if (PAIR)
-                    ptx::st_cluster_u32(ptx::mapa_shared(flag, ptx::cluster_ctarank() ^ 1u), 1u);
-                atomicOr(p.status, who);
-                return false;
-            }
-        }
-    }
-}
-
-// Add a chunk's f32 sums (HC columns of a TMEM lane) to the lane's integers.
-// 1.5 * 2^23 + f has f + kMagicBits as its bits while |f| < 2^22, so an
-// addition and an integer addition do what a conversion does at an eighth of
-// their rate (8192^3: 744 -> 7xx us).  A sum can reach 2^24, though it takes
-// codes near the limits with one sign to do so: where one of a warp's passes
-// 2^22, the warp converts those eight columns.  Eight columns are on their way
-// while eight are added.
-constexpr uint32_t kMagicBits = 0x4b400000u;  // of 1.5 * 2^23
-
-template <int HC>
-__device__ __forceinline__ void add_chunk(uint32_t acc, int32_t (&sum)[HC])
-{
-    const float magic = __uint_as_float(kMagicBits);
-    uint32_t r[2][8];
-    ptx::tmem_ld_32x32b_x8(acc, r[0]);
-#pragma unroll
-    for (int c = 0; c < HC / 8; ++c) {
-        ptx::tmem_wait_ld(r[c & 1]);
-        if (c + 1 < HC / 8)
-            ptx::tmem_ld_32x32b_x8(acc + 8u * (c + 1), r[(c + 1) & 1]);
-        float f[8];
-#pragma unroll
-        for (int j = 0; j < 8; ++j)
-            f[j] = __uint_as_float(r[c & 1][j]);
-        const float top = ptx::max_abs3(ptx::max_abs3(ptx::max_abs3(f[0], f[1], f[2]), f[3], f[4]), f[5],
-                                        ptx::max_abs3(f[6], f[7], 0.f));
-        if (__any_sync(0xffffffffu, top >= 4194304.f)) {
-#pragma unroll
-            for (int j = 0; j < 8; ++j)
-                sum[8 * c + j] += __float2int_rn(f[j]) + int32_t(kMagicBits);
-        } else {
-#pragma unroll
-            for (int j = 0; j < 8; ++j)
-                sum[8 * c + j] += __float_as_int(f[j] + magic);
-        }
-    }
-}
-
-// Arrive on a barrier of the pair's leader.  Released to the CTA only: what the
-// arrival stands for is complete in this SM before it is sent -- f16 in its own
-// shared memory (the proxy fence) or TMEM (the store wait), or TMEM read out
-// (the load wait) -- and is next touched by this SM's own tensor core.
-// Released to the cluster, every arrival would first wait for the warp's other
-// stores, global ones included: measured 1.34 times the whole kernel's time at
-// 8192^3 (1028 against 770 us).
-template <bool PAIR>
-__device__ __forceinline__ void arrive_leader(uint32_t bar)
-{
-    if constexpr (PAIR)
-        ptx::mbar_arrive_remote(bar);
-    else
-        ptx::mbar_arrive(bar);
-}
-
-// Column scales (times alpha) and biases of four columns.
-__device__ __forceinline__ void column_terms(const S8Params &p, int32_t z, int32_t col, float (&sb)[4],
-                                             float (&bias)[4])
-{
-#pragma unroll
-    for (int k = 0; k < 4; ++k) {
-        const bool in = col + k < p.N;
-        sb[k] = p.epi.alpha;
-        if (p.scale_b && in)
-            sb[k] *= __ldg(p.scale_b + z * p.sb_stride + col + k);
-        bias[k] = p.epi.bias && in ? __ldg(p.epi.bias + z * p.epi.bias_stride + col + k) : 0.f;
-    }
-}
-
-// Four values of a row (scaled by the row) through the epilogue into C.
-template <int ACT>
-__device__ __forceinline__ void put4_as(const S8Params &p, int64_t at, int32_t col, float (&o)[4],
-                                        const float (&sb)[4], const float (&bias)[4])
-{
-#pragma unroll
-    for (int k = 0; k < 4; ++k)
-        o[k] = epi_act(fmaf(sb[k], o[k], bias[k]), ACT, p.epi.slope);
-    if (p.vec_c && col + 3 < p.N) {
-        if (p.epi.out_type == kOutF32)
-            *reinterpret_cast<float4 *>(static_cast<float *>(p.C) + at) = make_float4(o[0], o[1], o[2], o[3]);
-        else
-            *reinterpret_cast<uint2 *>(static_cast<uint16_t *>(p.C) + at) =
-                make_uint2(epi_out16(o[0], p.epi.out_type) | (epi_out16(o[1], p.epi.out_type) << 16),
-                           epi_out16(o[2], p.epi.out_type) | (epi_out16(o[3], p.epi.out_type) << 16));
-        return;
-    }
-#pragma unroll
-    for (int k = 0; k < 4; ++k)
-        if (col + k < p.N)
-            epi_store(p.C, at + k, o[k], p.epi.out_type);
-}
-// A staged box (32 rows of 32 f32 values, 16-byte chunks swizzled by the row)
-// through the epilogue into C: eight lanes take a row's chunks, four rows at a
-// time.
-__device__ __forceinline__ void store_box(const S8Params &p, const S8Tile &t, uint32_t buf, int32_t row0, int32_t col0,
-                                          int lane)
-{
-    const int32_t col = col0 + 4 * (lane & 7);
-    if (col >= p.N)
-        return;
-    float sb[4], bias[4];
-    column_terms(p, t.z, col, sb, bias);
-    const int32_t rows = min(32, t.rows - row0);
-    with_activation<kActRuntime>(p.epi.act, [&](auto act) {
-#pragma unroll 1
-        for (int r = lane >> 3; r < rows; r += 4) {
-            const uint4 u = ptx::ld_shared_v4(buf + uint32_t(r) * 128u + (uint32_t((lane & 7) ^ (r & 7)) << 4));
-            float o[4] = {__uint_as_float(u.x), __uint_as_float(u.y), __uint_as_float(u.z), __uint_as_float(u.w)};
-            put4_as<decltype(act)::value>(p, t.z * p.sC + int64_t(row0 + r) * p.ldc + col, col, o, sb, bias);
-        }
-    });
-}
-
-template <bool PAIR>
-__global__ void __launch_bounds__(kS8Threads, 1)
-    tsm_s8_tiled_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ CUtensorMap map_b,
-                        const S8Params p)
-{
-    using Cfg = S8Cfg<PAIR>;
-    constexpr int S1 = Cfg::S1, S2 = Cfg::S2;
-    extern __shared__ uint8_t smem_raw[];
-    const uint32_t raw = ptx::smem_addr(smem_raw);
-    const uint32_t base = (raw + 1023u) & ~1023u;
-    uint8_t *const base_ptr = smem_raw + (base - raw);
-    const uint32_t codes0 = base;
-    const uint32_t f16_0 = codes0 + S1 * Cfg::CODE_STAGE;
-    const uint32_t staging = f16_0 + S2 * Cfg::F_STAGE;
-    const uint32_t ctrl = staging + Cfg::STAGING;
-    uint8_t *const ctrl_ptr = base_ptr + (ctrl - base);
-
-    // Barriers.  `ready` and `tempty` are used in the pair's leader only.
-    const uint32_t full0 = ctrl;               // [S1] codes landed
-    const uint32_t empty0 = ctrl + 32u;        // [S1] codes read by the converters
-    const uint32_t ready0 = ctrl + 64u;        // [S2] f16 written (both CTAs)
-    const uint32_t free0 = ctrl + 96u;         // [S2] MMAs that read the f16 are done
-    const uint32_t tfull = ctrl + 128u;        // accumulator complete
-    const uint32_t tempty = ctrl + 136u;       // accumulator read out (the leader's: by both CTAs)
-    const uint32_t done_bar = ctrl + 160u;     // all MMAs completed
-    uint32_t *const tmem_slot = reinterpret_cast<uint32_t *>(ctrl_ptr + 176);
-    const uint32_t flag = ctrl + 180u;         // this CTA gives up
-    const SharedSchedule<false> sched{ctrl + 256u};
-    const SharedSchedule<true> wsched{ctrl + 256u};
-    const uint32_t last_flag = ctrl + 184u;    // [2] one per column half
-    const uint32_t gtab = ctrl + Cfg::GROUP_TABLE_OFF;
-
-    const int warp = __shfl_sync(0xffffffffu, int(threadIdx.x >> 5), 0);  // (uniform to the compiler)
-    const int lane = int(threadIdx.x & 31);
-    const uint32_t rank = PAIR ? ptx::cluster_ctarank() : 0u;
-    const int32_t worker = int32_t(PAIR ? (blockIdx.x >> 1) : blockIdx.x);
-
-    if (threadIdx.x == 0) {
-        for (int s = 0; s < S1; ++s) {
-            ptx::mbar_init(full0 + 8u * s, 1);
-            ptx::mbar_init(empty0 + 8u * s, 8);
-        }
-        for (int s = 0; s < S2; ++s) {
-            ptx::mbar_init(ready0 + 8u * s, 8 * Cfg::CTAS);
-            ptx::mbar_init(free0 + 8u * s, 1);
-        }
-        ptx::mbar_init(tfull, 1);
-        ptx::mbar_init(tempty, 8 * Cfg::CTAS);
-        ptx::mbar_init(done_bar, 1);
-        ptx::st_shared_u32(flag, 0u);
-        ptx::fence_mbar_init();
-        ptx::prefetch_tensormap(&map_a);
-        ptx::prefetch_tensormap(&map_b);
-    }
-    __syncwarp();
-    if constexpr (PAIR)
-        ptx::cluster_sync();
-    chain_next();
-    if (warp == 1) {
-        ptx::tmem_alloc<PAIR>(ptx::smem_addr(tmem_slot), 512);
-        ptx::tmem_relinquish<PAIR>();
-    }
-    chain_wait();
-    if (warp == 2 && p.group_rows) {
-        build_group_table(p.group_rows, p.batch, p.M, Cfg::TILE_M, p.tiles_n,
-                          reinterpret_cast<uint32_t *>(ctrl_ptr + Cfg::GROUP_TABLE_OFF), p.status);
-        __syncwarp();
-    }
-    if (warp == 2 && lane == 0) {
-        S8Schedule s;
-        s.plan(p.group_rows ? int32_t(ptx::ld_shared_u32(gtab + 4u * (p.batch - 1))) : p.tiles_m * p.tiles_n * p.batch, p.kb, p.workers);
-        sched.put(s);
-    }
-    ptx::tc_fence_before_sync();
-    ptx::cta_sync();
-    ptx::tc_fence_after_sync();
-    const uint32_t tmem = *tmem_slot;
-
-    const uint32_t ready_lead0 = PAIR ? ptx::mapa_shared(ready0, 0) : ready0;
-    const uint32_t tempty_lead = PAIR ? ptx::mapa_shared(tempty, 0) : tempty;
-    const int32_t row_off = int32_t(rank) * Cfg::ROWS;
-
-    if (warp < 4) {
-        ptx::regs_dec<kS8RegsIssue>();
-        if (warp == 0 && lane == 0) {
-            // ---------------- TMA producer
-            uint32_t stage = 0, phase = 0;
-            uint32_t issued = 0;
-            bool ok = true;
-            for (PieceWalk<false> w(sched, worker); ok && w.advance(sched);) {
-                const S8Tile t = tile_at(w.tile, p, gtab, Cfg::TILE_M, Cfg::TILE_N);
-                const int32_t col = t.n0 + int32_t(rank) * 128;
-                for (int32_t kb = w.kb0; kb < w.kb1; ++kb) {
-                    if (!s8_wait<PAIR>(empty0 + 8u * stage, phase ^ 1u, flag, p, kStatusProducer)) {
-                        ok = false;
-                        break;
-                    }
-                    const uint32_t sa = codes0 + stage * Cfg::CODE_STAGE;
-                    const uint32_t fb = full0 + 8u * stage;
-                    ptx::mbar_arrive_expect_tx(fb, Cfg::CODE_STAGE);
-                    ptx::tma_load_3d(sa, &map_a, fb, kb * Cfg::BK, t.m0 + row_off, t.z);
-                    ptx::tma_load_3d(sa + Cfg::A_CODES, &map_b, fb, col, kb * Cfg::BK, t.z);
-                    ++issued;
-                    if (++stage == S1) {
-                        stage = 0;
-                        phase ^= 1u;
-                    }
-                }
-            }
-            // No TMA write into shared memory outlives the CTA.
-            // (The last S1 loads: the slots from `stage` on, oldest first.)
-            for (int i = 0; i < S1; ++i) {
-                if (issued + i >= uint32_t(S1))
-                    s8_wait<PAIR>(full0 + 8u * stage, phase ^ 1u, flag, p, kStatusDrain, false);
-                if (++stage == S1) {
-                    stage = 0;
-                    phase ^= 1u;
-                }
-            }
-        } else if (warp == 1 && lane == 0 && rank == 0) {
-            // ---------------- MMA issuer
-            constexpr uint32_t idesc = mma_idesc<Cfg::TILE_N, PAIR>();
-            constexpr uint16_t both = PAIR ? 3 : 1;
-            uint32_t stage = 0, phase = 0, aphase = 0;
-            bool ok = true;
-            for (PieceWalk<false> w(sched, worker); ok && w.advance(sched);) {
-                int c = 0;  // blocks in the accumulator
-                for (int32_t kb = w.kb0; ok && kb < w.kb1; ++kb) {
-                    if (!s8_wait<PAIR, PAIR>(ready0 + 8u * stage, phase, flag, p, kStatusMma)) {
-                        ok = false;
-                        break;
-                    }
-                    ptx::tc_fence_after_sync();
-                    const bool last = c == kChunkBlocks - 1 || kb == w.kb1 - 1;
-                    const uint32_t a = tmem + Cfg::A_COL + stage * uint32_t(Cfg::BK / 2);
-                    if (c == 0) {
-                        if (!s8_wait<PAIR, PAIR>(tempty, aphase ^ 1u, flag, p, kStatusMma)) {
-                            ok = false;
-                            break;
-                        }
-                        ptx::tc_fence_after_sync();
-                    }
-                    const uint32_t sb = f16_0 + stage * Cfg::F_STAGE;
-#pragma unroll
-                    for (int kk = 0; kk < Cfg::BK / 16; ++kk)
-                        ptx::mma_f16_ts<PAIR>(tmem, a + 8u * kk, desc_b_s8<PAIR>(sb + 2048u * kk), idesc,
-                                              (c > 0 || kk > 0) ? 1u : 0u);
-                    if (last)
-                        ptx::mma_commit<PAIR>(tfull, both);
-                    ptx::mma_commit<PAIR>(free0 + 8u * stage, both);
-                    if (++stage == S2) {
-                        stage = 0;
-                        phase ^= 1u;
-                    }
-                    c = last ? 0 : c + 1;
-                    if (last)
-                        aphase ^= 1u;
-                }
-            }
-            // Every MMA must finish before TMEM is freed.
-            ptx::mma_commit<PAIR>(done_bar, 1);
-            s8_wait<PAIR>(done_bar, 0, flag, p, kStatusDrain, false);
-        }
-        __syncwarp();
-    } else if (warp < kWarpDrain) {
-        // ---------------- converters
-        ptx::regs_dec<kS8RegsConvert>();
-        const bool is_a = warp < kWarpB;
-        const int q = is_a ? warp - kWarpA : warp - kWarpB;
-        uint32_t s1 = 0, p1 = 0, s2 = 0, p2 = 0;
-        bool ok = true;
-        for (PieceWalk<true> w(wsched, worker); ok && w.advance(wsched);) {
-            for (int32_t kb = w.kb0; kb < w.kb1; ++kb) {
-                ok = s8_wait<PAIR>(full0 + 8u * s1, p1, flag, p, kStatusProducer) &&
-                     s8_wait<PAIR>(free0 + 8u * s2, p2 ^ 1u, flag, p, kStatusProducer);
-                ok = __all_sync(0xffffffffu, ok);
-                if (!ok)
-                    break;
-                const uint32_t codes = codes0 + s1 * Cfg::CODE_STAGE;
-                if (is_a) {
-                    // Row 32q + lane: eight 16-byte chunks, swizzled by the row.
-                    ptx::tc_fence_after_sync();
-                    const uint32_t row = codes + uint32_t(32 * q + lane) * 128u;
-                    const uint32_t to = tmem + (uint32_t(32 * q) << 16) + Cfg::A_COL + s2 * uint32_t(Cfg::BK / 2);
-#pragma unroll
-                    for (int g = 0; g < 4; ++g) {
-                        const uint4 u = ptx::ld_shared_v4(row + (uint32_t((2 * g) ^ (lane & 7)) << 4));
-                        const uint4 v = ptx::ld_shared_v4(row + (uint32_t((2 * g + 1) ^ (lane & 7)) << 4));
-                        uint32_t r[16];
-                        codes_to_f16(u.x, r[0], r[1]);
-                        codes_to_f16(u.y, r[2], r[3]);
-                        codes_to_f16(u.z, r[4], r[5]);
-                        codes_to_f16(u.w, r[6], r[7]);
-                        codes_to_f16(v.x, r[8], r[9]);
-                        codes_to_f16(v.y, r[10], r[11]);
-                        codes_to_f16(v.z, r[12], r[13]);
-                        codes_to_f16(v.w, r[14], r[15]);
-                        ptx::tmem_st_32x32b_x16(to + 16u * g, r);
-                    }
-                    __syncwarp();
-                    if (lane == 0)
-                        ptx::mbar_arrive(empty0 + 8u * s1);
-                    ptx::tmem_wait_st();
-                    ptx::tc_fence_before_sync();
-                } else {
-                    // 128 rows (k) of 128 codes, swizzled by the row.  A warp
-                    // takes eight rows of one 64-column half at a time: a lane
-                    // 16 codes of a row, written as two 16-byte chunks of f16.
-                    // Rows k and k ^ 5 share eight lanes: bit 2 keeps their
-                    // loads, bit 0 their stores in different banks.
-                    const int c = lane & 3, i = lane >> 2;
-                    const uint32_t r0 = uint32_t((i >> 1) ^ ((i & 1) * 5));  // row of the eight
-#pragma unroll
-                    for (int j = 0; j < 8; ++j) {
-                        const int h = j & 1;
-                        const uint32_t k = uint32_t(8 * (4 * q + (j >> 1))) + r0;
-                        const uint4 u = ptx::ld_shared_v4(codes + uint32_t(Cfg::A_CODES) + k * 128u +
-                                                          (uint32_t(4 * h + c) ^ r0) * 16u);
-                        uint32_t r[8];
-                        codes_to_f16(u.x, r[0], r[1]);
-                        codes_to_f16(u.y, r[2], r[3]);
-                        codes_to_f16(u.z, r[4], r[5]);
-                        codes_to_f16(u.w, r[6], r[7]);
-                        const uint32_t to = f16_0 + s2 * Cfg::F_STAGE + uint32_t(h * Cfg::F_BOX) + k * 128u;
-                        const uint32_t first = (uint32_t(2 * c) ^ r0) << 4;
-                        ptx::st_shared_v4(to + first, r[0], r[1], r[2], r[3]);
-                        ptx::st_shared_v4(to + (first ^ 16u), r[4], r[5], r[6], r[7]);
-                    }
-                    ptx::fence_proxy_async_smem();
-                    __syncwarp();
-                    if (lane == 0)
-                        ptx::mbar_arrive(empty0 + 8u * s1);
-                }
-                __syncwarp();
-                if (lane == 0)
-                    arrive_leader<PAIR>(ready_lead0 + 8u * s2);
-                if (++s1 == S1) {
-                    s1 = 0;
-                    p1 ^= 1u;
-                }
-                if (++s2 == S2) {
-                    s2 = 0;
-                    p2 ^= 1u;
-                }
-            }
-        }
-    } else {
-        // ---------------- accumulator -> integers -> C
-        ptx::regs_inc<kS8RegsDrain>();
-        const int e = warp - kWarpDrain;
-        const int h = e >> 2;
-        const int q = warp & 3;
-        const uint32_t acc = tmem + (uint32_t(32 * q) << 16) + uint32_t(h * Cfg::HC);
-        const uint32_t buf = staging + uint32_t(e) * 4096u;
-        uint32_t aphase = 0;
-        bool ok = true;
-        for (PieceWalk<true> w(wsched, worker); ok && w.advance(wsched);) {
-            // The row's sums.  A chunk adds integer + kMagicBits to each (see
-            // add_chunk), so they start that much lower for every chunk.
-            int32_t sum[Cfg::HC];
-            const uint32_t chunks = uint32_t(w.kb1 - w.kb0 + kChunkBlocks - 1) / kChunkBlocks;
-#pragma unroll
-            for (int j = 0; j < Cfg::HC; ++j)
-                sum[j] = int32_t(0u - chunks * kMagicBits);
-            for (int32_t kb = w.kb0; kb < w.kb1; kb += kChunkBlocks) {
-                ok = s8_wait<PAIR>(tfull, aphase, flag, p, kStatusEpilogue);
-                ok = __all_sync(0xffffffffu, ok);
-                if (!ok)
-                    break;
-                ptx::tc_fence_after_sync();
-                add_chunk<Cfg::HC>(acc, sum);
-                ptx::tc_fence_before_sync();
-                __syncwarp();
-                if (lane == 0)
-                    arrive_leader<PAIR>(tempty_lead);
-                aphase ^= 1u;
-            }
-            // The four warps go on or give up together (they meet below).
-            ok = __all_sync(0xffffffffu, ptx::named_bar_and(1 + h, 128, ok));
-            if (!ok)
-                break;
-            // (Read again rather than kept through the loop above, where
-            // registers are short.)
-            const uint32_t rank_now = PAIR ? ptx::cluster_ctarank() : 0u;
-            const int32_t tid = 32 * q + lane;
-            const int32_t me = int32_t(PAIR ? ptx::cta_id() >> 1 : ptx::cta_id());
-            S8Tile t = tile_at(w.tile, p, gtab, Cfg::TILE_M, Cfg::TILE_N);
-            t.m0 = __shfl_sync(0xffffffffu, t.m0, 0);  // (uniform to the compiler)
-            t.n0 = __shfl_sync(0xffffffffu, t.n0, 0);
-            t.z = __shfl_sync(0xffffffffu, t.z, 0);
-            t.rows = __shfl_sync(0xffffffffu, t.rows, 0);
-            const int32_t row0 = t.m0 + int32_t(rank_now) * Cfg::ROWS + 32 * q;  // the warp's first row
-            int32_t cut_first = 0, cut_last = -1;  // contributors of a cut tile
-            if (w.kb1 - w.kb0 < wsched.kb()) {
-                // A piece: its sums go to this worker's slot, and whoever
-                // arrives last adds up the others'.  [4-column group][row].
-                // A tile's first contributor holds its first block and uses
-                // its second slot; the others start in the tile: their first.
-                const S8Schedule cut = wsched.all();
-                const int32_t first = cut.owner(w.tile * cut.kb);
-                const int32_t last = cut.owner((w.tile + 1) * cut.kb - 1);
-                const int32_t part = int32_t(rank_now) * 2 + h;
-                const int32_t lane_at = part * (Cfg::ROWS * Cfg::HC) + 4 * tid;
-                int32_t *const mine = p.partial + (2 * me + (me == first)) * Cfg::SLOT_INTS + lane_at;
-                if (row0 < t.rows) {
-#pragma unroll
-                    for (int j = 0; j < Cfg::HC; j += 4)
-                        __stcg(reinterpret_cast<int4 *>(mine + j * Cfg::ROWS),
-                               make_int4(sum[j], sum[j + 1], sum[j + 2], sum[j + 3]));
-                }
-                __threadfence();
-                ptx::named_bar_sync(1 + h, 128);
-                if (q == 0)
-                    ptx::st_shared_u32(last_flag + 4u * h, arrive_last(p.arrivals + w.tile * Cfg::PARTS + part, p.tag,
-                                                                      uint32_t(last - first + 1), lane));
-                ptx::named_bar_sync(1 + h, 128);
-                const bool mine_to_sum = __any_sync(0xffffffffu, ptx::ld_shared_u32(last_flag + 4u * h) != 0);
-                __threadfence();
-                if (!mine_to_sum)
-                    continue;
-                cut_first = first;
-                cut_last = last;
-            }
-            // Through the warp's staging box: lane = row in, lane = column group out.
-            const float sa = p.scale_a && row0 + lane < t.rows ? __ldg(p.scale_a + t.z * p.sa_stride + row0 + lane) : 1.f;
-            auto stage = [&](int j, int32_t a, int32_t b, int32_t c, int32_t d) {
-                ptx::st_shared_v4(buf + uint32_t(lane) * 128u + (uint32_t((j >> 2) ^ (lane & 7)) << 4),
-                                  __float_as_uint(float(a) * sa), __float_as_uint(float(b) * sa),
-                                  __float_as_uint(float(c) * sa), __float_as_uint(float(d) * sa));
-            };
-            const int32_t boxes = row0 < t.rows ? min(Cfg::HC / 32, (p.N - t.n0 - h * Cfg::HC + 31) / 32) : 0;
-            if (cut_first <= cut_last) {
-                // All contributors' sums, this one's too, a box at a time.
-                const int32_t *from = p.partial + (int32_t(rank_now) * 2 + h) * (Cfg::ROWS * Cfg::HC) + 4 * tid;
-#pragma unroll 1
-                for (int b = 0; b < boxes; ++b, from += 32 * Cfg::ROWS) {
-                    int4 x[8] = {};
-                    // Two contributors' loads in flight together.
-#pragma unroll 2
-                    for (int32_t v = cut_first; v <= cut_last; ++v) {
-                        const int32_t *theirs = from + (2 * v + (v == cut_first)) * Cfg::SLOT_INTS;
-#pragma unroll
-                        for (int i = 0; i < 8; ++i) {
-                            const int4 y = __ldcg(reinterpret_cast<const int4 *>(theirs + 4 * i * Cfg::ROWS));
-                            x[i].x += y.x;
-                            x[i].y += y.y;
-                            x[i].z += y.z;
-                            x[i].w += y.w;
-                        }
-                    }
-#pragma unroll
-                    for (int i = 0; i < 8; ++i)
-                        stage(4 * i, x[i].x, x[i].y, x[i].z, x[i].w);
-                    __syncwarp();
-                    store_box(p, t, buf, row0, t.n0 + h * Cfg::HC + 32 * b, lane);
-                    __syncwarp();
-                }
-                continue;
-            }
-#pragma unroll 1
-            for (int b = 0; b < boxes; ++b) {
-#pragma unroll
-                for (int bb = 0; bb < Cfg::HC / 32; ++bb)
-                    if (b == bb) {
-#pragma unroll
-                        for (int j = 0; j < 32; j += 4)
-                            stage(j, sum[32 * bb + j], sum[32 * bb + j + 1], sum[32 * bb + j + 2], sum[32 * bb + j + 3]);
-                    }
-                __syncwarp();
-                store_box(p, t, buf, row0, t.n0 + h * Cfg::HC + 32 * b, lane);
-                __syncwarp();
-            }
-        }
-    }
-
-    ptx::tc_fence_before_sync();
-    ptx::cta_sync();
-    if constexpr (PAIR)
-        ptx::cluster_sync();
-    if (warp == 1) {
-        __syncwarp();
-        ptx::tc_fence_after_sync();
-        ptx::tmem_dealloc<PAIR>(ptx::ld_shared_u32(ctrl + 176u), 512);
-    }
-}
 
 // ------------------------------------------------------------- few rows
 //
@@ -838,7 +91,8 @@ __device__ __forceinline__ void few_rows_finish(const S8Params &p, const FewPlac
     const uint32_t sb0 = f.terms0, bias0 = f.terms0 + 4u * Cfg::COLS, sa0 = f.terms0 + 8u * Cfg::COLS;
     uint32_t set = 0, phase = 0;
     for (int32_t tile = f.cluster; tile < f.tiles; tile += f.clusters) {
-        const S8Tile t = tile_at(tile, p, f.gtab, Cfg::ROWS, Cfg::COLS);
+        S8Tile t = tile_at(tile, p, f.gtab, Cfg::ROWS, Cfg::COLS);
+        t.rows = min(t.rows - t.m0, Cfg::ROWS);  // (from here on: the tile's)
         // The terms of the epilogue while the sums are on their way.
         for (int c = ft; c < Cfg::COLS; c += FT) {
             const int32_t col = t.n0 + c;
@@ -852,7 +106,7 @@ __device__ __forceinline__ void few_rows_finish(const S8Params &p, const FewPlac
         }
         if (ft < Cfg::ROWS)
             ptx::st_shared_u32(sa0 + 4u * ft, __float_as_uint(p.scale_a && ft < t.rows
-                                                                  ? __ldg(p.scale_a + t.z * p.sa_stride + ft) : 1.f));
+                                                                  ? __ldg(p.scale_a + t.z * p.sa_stride + t.m0 + ft) : 1.f));
         const uint32_t sums = f.sums0 + set * uint32_t(Cfg::SUMS * 4);
         bool ok = s8_wait<false>(f.sums_full0 + 8u * set, phase, f.flag, p, kStatusEpilogue);
         ok = __all_sync(0xffffffffu, ptx::named_bar_and(1, FT, ok));
@@ -893,7 +147,7 @@ __device__ __forceinline__ void few_rows_finish(const S8Params &p, const FewPlac
             }
             const float sa = __uint_as_float(ptx::ld_shared_u32(sa0 + 4u * row));
             const int c = 128 * h + 16 * d1 + j;
-            const int64_t row_at = t.z * p.sC + row * p.ldc + t.n0;
+            const int64_t row_at = t.z * p.sC + int64_t(t.m0 + row) * p.ldc + t.n0;
             const int32_t columns = p.N - t.n0;
             with_activation<kActRuntime>(p.epi.act, [&](auto act) {
 #pragma unroll
@@ -964,7 +218,7 @@ __device__ __forceinline__ void few_rows_multiply(const CUtensorMap &map_a, cons
             const uint32_t fb = full0 + 8u * stage;
             ptx::mbar_arrive_expect_tx(fb, Cfg::B_BYTES + Cfg::A_BYTES);
             ptx::tma_load_3d(ring_b + stage * Cfg::B_BYTES, &map_b, fb, pt.n0 + 128 * half, next_k * Cfg::BK, pt.z);
-            ptx::tma_load_3d(ring_a + stage * Cfg::A_BYTES, &map_a, fb, next_k * Cfg::BK, 0, pt.z);
+            ptx::tma_load_3d(ring_a + stage * Cfg::A_BYTES, &map_a, fb, next_k * Cfg::BK, pt.m0, pt.z);
         }
         __syncwarp();
         next_k += Cfg::KWARPS;
@@ -1143,7 +397,8 @@ __global__ void __launch_bounds__(S8FewCfg<MT>::THREADS, 1)
     __syncthreads();
     if (p.ranks > 1)
         ptx::cluster_sync();  // the other CTAs' barriers exist
-    f.tiles = p.group_rows ? int32_t(ptx::ld_shared_u32(f.gtab + 4u * (p.batch - 1))) : p.tiles_n * p.batch;
+    f.tiles = p.group_rows ? int32_t(ptx::ld_shared_u32(f.gtab + 4u * (p.batch - 1)))
+                           : p.tiles_m * p.tiles_n * p.batch;
     if (warp < Cfg::WARPS) {
         ptx::regs_inc<Cfg::MMA_REGS>();
         few_rows_multiply<MT>(map_a, map_b, p, f, ctrl + uint32_t(warp * S) * 8u,
@@ -1204,21 +459,6 @@ __global__ void __launch_bounds__(256)
 }
 
 template <bool PAIR>
-cudaError_t set_tiled()
-{
-    return cudaFuncSetAttribute(tsm_s8_tiled_kernel<PAIR>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                S8Cfg<PAIR>::SMEM_BYTES);
-}
-
-template <bool PAIR>
-cudaError_t launch_tiled(const CUtensorMap &map_a, const CUtensorMap &map_b, const S8Params &p, int grid,
-                         cudaStream_t stream)
-{
-    return launch_chained(tsm_s8_tiled_kernel<PAIR>, dim3(unsigned(grid)), kS8Threads, S8Cfg<PAIR>::SMEM_BYTES,
-                          PAIR ? 2u : 0u, stream, map_a, map_b, p);
-}
-
-template <bool PAIR>
 S8Shape shape_of()
 {
     using Cfg = S8Cfg<PAIR>;
@@ -1273,9 +513,17 @@ cudaError_t launch_few(const CUtensorMap &map_a, const CUtensorMap &map_b, const
 
 cudaError_t set_s8_attributes(S8Capacity *cap)
 {
-    cudaError_t e = set_tiled<true>();
+    cudaError_t e = set_s8_tiled<kActNone>();
     if (e == cudaSuccess)
-        e = set_tiled<false>();
+        e = set_s8_tiled<kActRelu>();
+    if (e == cudaSuccess)
+        e = set_s8_tiled<kActLeakyRelu>();
+    if (e == cudaSuccess)
+        e = set_s8_tiled<kActGelu>();
+    if (e == cudaSuccess)
+        e = set_s8_tiled<kActGeluTanh>();
+    if (e == cudaSuccess)
+        e = set_s8_tiled<kActSilu>();
     if (e == cudaSuccess)
         e = set_few<1>(cap);
     if (e == cudaSuccess)
@@ -1289,8 +537,16 @@ cudaError_t launch_s8(const CUtensorMap &map_a, const CUtensorMap &map_b, const 
     switch (kind) {
     case S8Kind::kFew16: return launch_few<1>(map_a, map_b, p, grid, stream);
     case S8Kind::kFew32: return launch_few<2>(map_a, map_b, p, grid, stream);
-    case S8Kind::kOne: return launch_tiled<false>(map_a, map_b, p, grid, stream);
-    default: return launch_tiled<true>(map_a, map_b, p, 2 * grid, stream);
+    default: break;
+    }
+    const bool pair = kind == S8Kind::kPair;
+    switch (p.epi.act) {
+    case kActRelu: return launch_s8_tiled<kActRelu>(map_a, map_b, p, pair, grid, stream);
+    case kActLeakyRelu: return launch_s8_tiled<kActLeakyRelu>(map_a, map_b, p, pair, grid, stream);
+    case kActGelu: return launch_s8_tiled<kActGelu>(map_a, map_b, p, pair, grid, stream);
+    case kActGeluTanh: return launch_s8_tiled<kActGeluTanh>(map_a, map_b, p, pair, grid, stream);
+    case kActSilu: return launch_s8_tiled<kActSilu>(map_a, map_b, p, pair, grid, stream);
+    default: return launch_s8_tiled<kActNone>(map_a, map_b, p, pair, grid, stream);
     }
 }
 
