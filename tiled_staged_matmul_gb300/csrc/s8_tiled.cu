@@ -300,7 +300,7 @@ __global__ void __launch_bounds__(kS8Threads, 1)
     const SharedSchedule<true> wsched{ctrl + 256u};
     const uint32_t last_flag = ctrl + 184u;    // [2] one per column half
     const uint32_t gtab = ctrl + Cfg::GROUP_TABLE_OFF;
-    const uint32_t terms0 = ctrl + Cfg::TERMS_OFF;  // [columns' scales, biases][256]
+    const uint32_t terms0 = ctrl + Cfg::TERMS_OFF;  // [2][columns' scales, biases][256]
 
     const int warp = __shfl_sync(0xffffffffu, int(threadIdx.x >> 5), 0);  // (uniform to the compiler)
     const int lane = int(threadIdx.x & 31);
@@ -524,9 +524,28 @@ __global__ void __launch_bounds__(kS8Threads, 1)
         const int q = warp & 3;
         const uint32_t acc = tmem + (uint32_t(32 * q) << 16) + uint32_t(h * Cfg::HC);
         const uint32_t buf = staging + uint32_t(e) * 2048u;
-        uint32_t aphase = 0;
+        uint32_t aphase = 0, turn = 0;
         bool ok = true;
         for (PieceWalk<true> w(wsched, worker); ok && w.advance(wsched);) {
+            // The columns' scales (times alpha) and biases of this half, while
+            // the first chunk is multiplied; two sets in turn, since the half's
+            // other warps may still be at the last tile's.  (They meet at the
+            // end of the chunks.)
+            {
+                const S8Tile t = tile_at(w.tile, p, gtab, Cfg::TILE_M, Cfg::TILE_N);
+                const int32_t c = 32 * q + lane, col = t.n0 + h * Cfg::HC + c;
+                const uint32_t at = terms0 + turn * 2048u + uint32_t(h) * 512u + 4u * c;
+                if (c < Cfg::HC) {
+                    const bool in = col < p.N;
+                    float sb = p.epi.alpha, bias = 0.f;
+                    if (p.scale_b && in)
+                        sb *= __ldg(p.scale_b + t.z * p.sb_stride + col);
+                    if (p.epi.bias && in)
+                        bias = __ldg(p.epi.bias + t.z * p.epi.bias_stride + col);
+                    ptx::st_shared_u32(at, __float_as_uint(sb));
+                    ptx::st_shared_u32(at + 1024u, __float_as_uint(bias));
+                }
+            }
             // The row's sums.  A chunk adds integer + kMagicBits to each (see
             // add_chunk), so they start that much lower for every chunk.
             int32_t sum[Cfg::HC];
@@ -588,26 +607,17 @@ __global__ void __launch_bounds__(kS8Threads, 1)
                 ptx::named_bar_sync(1 + h, 128);
                 const bool mine_to_sum = __any_sync(0xffffffffu, ptx::ld_shared_u32(last_flag + 4u * h) != 0);
                 __threadfence();
-                if (!mine_to_sum)
+                if (!mine_to_sum) {
+                    turn ^= 1u;
                     continue;
+                }
                 cut_first = first;
                 cut_last = last;
             }
-            // The columns' scales (times alpha) and biases of this half.
             const int32_t half0 = t.n0 + h * Cfg::HC;
-            const uint32_t sb0 = terms0 + uint32_t(h) * 512u, bias0 = sb0 + 1024u;
-            if (tid < Cfg::HC) {
-                const bool in = half0 + tid < p.N;
-                float sb = p.epi.alpha, bias = 0.f;
-                if (p.scale_b && in)
-                    sb *= __ldg(p.scale_b + t.z * p.sb_stride + half0 + tid);
-                if (p.epi.bias && in)
-                    bias = __ldg(p.epi.bias + t.z * p.epi.bias_stride + half0 + tid);
-                ptx::st_shared_u32(sb0 + 4u * tid, __float_as_uint(sb));
-                ptx::st_shared_u32(bias0 + 4u * tid, __float_as_uint(bias));
-            }
+            const uint32_t sb0 = terms0 + turn * 2048u + uint32_t(h) * 512u, bias0 = sb0 + 1024u;
+            turn ^= 1u;
             const float sa = p.scale_a && row0 + lane < t.rows ? __ldg(p.scale_a + t.z * p.sa_stride + row0 + lane) : 1.f;
-            ptx::named_bar_sync(1 + h, 128);
             const int32_t boxes = row0 < t.rows ? min(Cfg::HC / 32, (p.N - half0 + 31) / 32) : 0;
             if (cut_first <= cut_last) {
                 // All contributors' sums, this one's too, a box at a time.
