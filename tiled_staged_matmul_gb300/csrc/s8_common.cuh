@@ -55,7 +55,8 @@ struct S8Cfg {
     static constexpr int F_STAGE = 2 * F_BOX;
     static constexpr int S1 = 3, S2 = 3;        // ring depths
     static constexpr int STAGING = 8 * 32 * 64;   // per epilogue warp: 32 rows of 64 bytes
-    static constexpr int CTRL = 6144, GROUP_TABLE_OFF = 1024, TERMS_OFF = 2048;
+    static constexpr int TERMS = 3 * 256 * 4;     // the epilogue's column and row terms
+    static constexpr int CTRL = 2048 + 2 * TERMS, GROUP_TABLE_OFF = 1024, TERMS_OFF = 2048;
     static constexpr int SMEM_BYTES = 1024 + S1 * CODE_STAGE + S2 * F_STAGE + STAGING + CTRL;
     static_assert(SMEM_BYTES <= 232448, "227 KiB per block");
     static constexpr uint32_t A_COL = 256;      // TMEM: the accumulator, then the f16 A ring

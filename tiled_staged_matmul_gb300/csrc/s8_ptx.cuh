@@ -135,6 +135,20 @@ __device__ __forceinline__ uint32_t cta_id()
     return r;
 }
 
+// Put *src (or `otherwise` where src is null) at a shared-memory word without
+// waiting for it; fetch_wait waits for this thread's fetches.
+__device__ __forceinline__ void fetch_f32(uint32_t dst, const float *src, float otherwise)
+{
+    if (src)
+        asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(dst), "l"(src) : "memory");
+    else
+        asm volatile("st.shared.f32 [%0], %1;" ::"r"(dst), "f"(otherwise) : "memory");
+}
+__device__ __forceinline__ void fetch_wait()
+{
+    asm volatile("cp.async.wait_all;" ::: "memory");
+}
+
 // The largest of |a|, |b| and |c|.
 __device__ __forceinline__ float max_abs3(float a, float b, float c)
 {

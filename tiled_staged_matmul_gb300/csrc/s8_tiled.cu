@@ -145,9 +145,11 @@ __device__ __forceinline__ bool arrive_last(unsigned long long *word, unsigned l
 // while eight are added.
 constexpr uint32_t kMagicBits = 0x4b400000u;  // of 1.5 * 2^23
 
+// Returns no less than the largest magnitude added.
 template <int HC>
-__device__ __forceinline__ void add_chunk(uint32_t acc, int32_t (&sum)[HC])
+__device__ __forceinline__ float add_chunk(uint32_t acc, int32_t (&sum)[HC])
 {
+    float largest = 0.f;
     const float magic = __uint_as_float(kMagicBits);
     uint32_t r[2][8];
     ptx::tmem_ld_32x32b_x8(acc, r[0]);
@@ -162,6 +164,7 @@ __device__ __forceinline__ void add_chunk(uint32_t acc, int32_t (&sum)[HC])
             f[j] = __uint_as_float(r[c & 1][j]);
         const float top = ptx::max_abs3(ptx::max_abs3(ptx::max_abs3(f[0], f[1], f[2]), f[3], f[4]), f[5],
                                         ptx::max_abs3(f[6], f[7], 0.f));
+        largest = fmaxf(largest, top);
         if (__any_sync(0xffffffffu, top >= 4194304.f)) {
 #pragma unroll
             for (int j = 0; j < 8; ++j)
@@ -172,6 +175,18 @@ __device__ __forceinline__ void add_chunk(uint32_t acc, int32_t (&sum)[HC])
                 sum[8 * c + j] += __float_as_int(f[j] + magic);
         }
     }
+    return largest;
+}
+
+// Two values as the 16-bit output type stores them, in one conversion.
+__device__ __forceinline__ uint32_t out16_pair(float a, float b, int32_t out_type)
+{
+    if (out_type == kOutBF16) {
+        const __nv_bfloat162 x = __floats2bfloat162_rn(a, b);
+        return *reinterpret_cast<const uint32_t *>(&x);
+    }
+    const __half2 x = __floats2half2_rn(a, b);
+    return *reinterpret_cast<const uint32_t *>(&x);
 }
 
 // The epilogue of a box: 32 rows (a lane each) of 32 columns' sums.  Scaled,
@@ -180,7 +195,7 @@ __device__ __forceinline__ void add_chunk(uint32_t acc, int32_t (&sum)[HC])
 // another, 4096 x 14336 x 4096 took 358 us, not 321), then through the warp's
 // staging space (64 bytes a row, 16-byte chunks swizzled by the row) so that
 // the stores cover whole row segments.
-__device__ __forceinline__ void finish_box(const S8Params &p, const S8Tile &t, const int32_t (&s32)[32], float sa,
+__device__ __forceinline__ void finish_box(const S8Params &p, const S8Tile &t, const int32_t (&s32)[32], bool small, float sa,
                                            uint32_t sb_at, uint32_t bias_at, uint32_t buf, int32_t row0, int32_t col0,
                                            int lane)
 {
@@ -189,9 +204,12 @@ __device__ __forceinline__ void finish_box(const S8Params &p, const S8Tile &t, c
         const uint4 s = ptx::ld_shared_v4(sb_at + 4u * j), b = ptx::ld_shared_v4(bias_at + 4u * j);
         const uint32_t sw[4] = {s.x, s.y, s.z, s.w}, bw[4] = {b.x, b.y, b.z, b.w};
 #pragma unroll
-        for (int i = 0; i < 4; ++i)
-            v[i] = epi_act(fmaf(__uint_as_float(sw[i]), float(s32[j + i]) * sa, __uint_as_float(bw[i])), kAct,
-                           p.epi.slope);
+        for (int i = 0; i < 4; ++i) {
+            // (Sums below 2^22 become f32 by add_chunk's way, in reverse.)
+            const float s1 = small ? __int_as_float(s32[j + i] + int32_t(kMagicBits)) - __uint_as_float(kMagicBits)
+                                   : float(s32[j + i]);
+            v[i] = epi_act(fmaf(__uint_as_float(sw[i]), s1 * sa, __uint_as_float(bw[i])), kAct, p.epi.slope);
+        }
     };
     const int32_t rows = t.rows - row0;
     const uint32_t mine = buf + uint32_t(lane) * 64u, swizzle = uint32_t(lane >> 1) & 3u;
@@ -216,8 +234,8 @@ __device__ __forceinline__ void finish_box(const S8Params &p, const S8Tile &t, c
 #pragma unroll
                 for (int i = 0; i < 4; i += 2) {
                     four(8 * c + 2 * i, v);
-                    w[i] = epi_out16(v[0], p.epi.out_type) | epi_out16(v[1], p.epi.out_type) << 16;
-                    w[i + 1] = epi_out16(v[2], p.epi.out_type) | epi_out16(v[3], p.epi.out_type) << 16;
+                    w[i] = out16_pair(v[0], v[1], p.epi.out_type);
+                    w[i + 1] = out16_pair(v[2], v[3], p.epi.out_type);
                 }
             }
             ptx::st_shared_v4(mine + ((uint32_t(c) ^ swizzle) << 4), w[0], w[1], w[2], w[3]);
@@ -300,7 +318,8 @@ __global__ void __launch_bounds__(kS8Threads, 1)
     const SharedSchedule<true> wsched{ctrl + 256u};
     const uint32_t last_flag = ctrl + 184u;    // [2] one per column half
     const uint32_t gtab = ctrl + Cfg::GROUP_TABLE_OFF;
-    const uint32_t terms0 = ctrl + Cfg::TERMS_OFF;  // [2][columns' scales, biases][256]
+    const uint32_t tiles0 = ctrl + 512u;  // [8] an epilogue warp's tile
+    const uint32_t terms0 = ctrl + Cfg::TERMS_OFF;  // [2][columns' scales, biases, rows' scales][256]
 
     const int warp = __shfl_sync(0xffffffffu, int(threadIdx.x >> 5), 0);  // (uniform to the compiler)
     const int lane = int(threadIdx.x & 31);
@@ -527,28 +546,10 @@ __global__ void __launch_bounds__(kS8Threads, 1)
         uint32_t aphase = 0, turn = 0;
         bool ok = true;
         for (PieceWalk<true> w(wsched, worker); ok && w.advance(wsched);) {
-            // The columns' scales (times alpha) and biases of this half, while
-            // the first chunk is multiplied; two sets in turn, since the half's
-            // other warps may still be at the last tile's.  (They meet at the
-            // end of the chunks.)
-            {
-                const S8Tile t = tile_at(w.tile, p, gtab, Cfg::TILE_M, Cfg::TILE_N);
-                const int32_t c = 32 * q + lane, col = t.n0 + h * Cfg::HC + c;
-                const uint32_t at = terms0 + turn * 2048u + uint32_t(h) * 512u + 4u * c;
-                if (c < Cfg::HC) {
-                    const bool in = col < p.N;
-                    float sb = p.epi.alpha, bias = 0.f;
-                    if (p.scale_b && in)
-                        sb *= __ldg(p.scale_b + t.z * p.sb_stride + col);
-                    if (p.epi.bias && in)
-                        bias = __ldg(p.epi.bias + t.z * p.epi.bias_stride + col);
-                    ptx::st_shared_u32(at, __float_as_uint(sb));
-                    ptx::st_shared_u32(at + 1024u, __float_as_uint(bias));
-                }
-            }
             // The row's sums.  A chunk adds integer + kMagicBits to each (see
             // add_chunk), so they start that much lower for every chunk.
             int32_t sum[Cfg::HC];
+            float bound = 0.f;  // no sum is larger
             const uint32_t chunks = uint32_t(w.kb1 - w.kb0 + kChunkBlocks - 1) / kChunkBlocks;
 #pragma unroll
             for (int j = 0; j < Cfg::HC; ++j)
@@ -559,14 +560,34 @@ __global__ void __launch_bounds__(kS8Threads, 1)
                 if (!ok)
                     break;
                 ptx::tc_fence_after_sync();
-                add_chunk<Cfg::HC>(acc, sum);
+                bound += add_chunk<Cfg::HC>(acc, sum);
                 ptx::tc_fence_before_sync();
                 __syncwarp();
                 if (lane == 0)
                     arrive_leader<PAIR>(tempty_lead);
                 aphase ^= 1u;
+                if (kb != w.kb0)
+                    continue;
+                // With the first chunk out of the way (it was complete long
+                // before the last tile's epilogue was): where the tile is, for
+                // later, and its columns' scales and biases and rows' scales on
+                // their way.  Two sets in turn, since the half's other warps
+                // may still be at the last tile's; they meet below.
+                const S8Tile t = tile_at(w.tile, p, gtab, Cfg::TILE_M, Cfg::TILE_N);
+                const int32_t i = 32 * q + lane, col = t.n0 + h * Cfg::HC + i;
+                const int32_t row = t.m0 + int32_t(PAIR ? ptx::cluster_ctarank() : 0u) * Cfg::ROWS + i;
+                const uint32_t at = terms0 + turn * Cfg::TERMS + uint32_t(h) * 512u + 4u * i;
+                ptx::fetch_f32(at, p.scale_b && i < Cfg::HC && col < p.N ? p.scale_b + t.z * p.sb_stride + col : nullptr, 1.f);
+                ptx::fetch_f32(at + 1024u,
+                               p.epi.bias && i < Cfg::HC && col < p.N ? p.epi.bias + t.z * p.epi.bias_stride + col : nullptr, 0.f);
+                ptx::fetch_f32(at + 2048u, p.scale_a && row < t.rows ? p.scale_a + t.z * p.sa_stride + row : nullptr, 1.f);
+                if (lane == 0)
+                    ptx::st_shared_v4(tiles0 + 16u * uint32_t(e), uint32_t(t.m0), uint32_t(t.n0), uint32_t(t.z),
+                                      uint32_t(t.rows));
+                __syncwarp();
             }
             // The four warps go on or give up together (they meet below).
+            ptx::fetch_wait();
             ok = __all_sync(0xffffffffu, ptx::named_bar_and(1 + h, 128, ok));
             if (!ok)
                 break;
@@ -575,11 +596,12 @@ __global__ void __launch_bounds__(kS8Threads, 1)
             const uint32_t rank_now = PAIR ? ptx::cluster_ctarank() : 0u;
             const int32_t tid = 32 * q + lane;
             const int32_t me = int32_t(PAIR ? ptx::cta_id() >> 1 : ptx::cta_id());
-            S8Tile t = tile_at(w.tile, p, gtab, Cfg::TILE_M, Cfg::TILE_N);
-            t.m0 = __shfl_sync(0xffffffffu, t.m0, 0);  // (uniform to the compiler)
-            t.n0 = __shfl_sync(0xffffffffu, t.n0, 0);
-            t.z = __shfl_sync(0xffffffffu, t.z, 0);
-            t.rows = __shfl_sync(0xffffffffu, t.rows, 0);
+            const uint4 place = ptx::ld_shared_v4(tiles0 + 16u * uint32_t(e));
+            S8Tile t;
+            t.m0 = __shfl_sync(0xffffffffu, int32_t(place.x), 0);  // (uniform to the compiler)
+            t.n0 = __shfl_sync(0xffffffffu, int32_t(place.y), 0);
+            t.z = __shfl_sync(0xffffffffu, int32_t(place.z), 0);
+            t.rows = __shfl_sync(0xffffffffu, int32_t(place.w), 0);
             const int32_t row0 = t.m0 + int32_t(rank_now) * Cfg::ROWS + 32 * q;  // the warp's first row
             int32_t cut_first = 0, cut_last = -1;  // contributors of a cut tile
             if (w.kb1 - w.kb0 < wsched.kb()) {
@@ -615,9 +637,10 @@ __global__ void __launch_bounds__(kS8Threads, 1)
                 cut_last = last;
             }
             const int32_t half0 = t.n0 + h * Cfg::HC;
-            const uint32_t sb0 = terms0 + turn * 2048u + uint32_t(h) * 512u, bias0 = sb0 + 1024u;
+            const uint32_t sb0 = terms0 + turn * Cfg::TERMS + uint32_t(h) * 512u, bias0 = sb0 + 1024u;
             turn ^= 1u;
-            const float sa = p.scale_a && row0 + lane < t.rows ? __ldg(p.scale_a + t.z * p.sa_stride + row0 + lane) : 1.f;
+            const float sa = p.epi.alpha * __uint_as_float(ptx::ld_shared_u32(sb0 + 2048u + 4u * (32 * q + lane)));
+            const bool small = __all_sync(0xffffffffu, bound < 4194304.f);
             const int32_t boxes = row0 < t.rows ? min(Cfg::HC / 32, (p.N - half0 + 31) / 32) : 0;
             if (cut_first <= cut_last) {
                 // All contributors' sums, this one's too, a box at a time.
@@ -646,7 +669,7 @@ __global__ void __launch_bounds__(kS8Threads, 1)
                         s32[4 * i + 2] = x[i].z;
                         s32[4 * i + 3] = x[i].w;
                     }
-                    finish_box(p, t, s32, sa, sb0 + 128u * b, bias0 + 128u * b, buf, row0, half0 + 32 * b, lane);
+                    finish_box(p, t, s32, false, sa, sb0 + 128u * b, bias0 + 128u * b, buf, row0, half0 + 32 * b, lane);
                 }
                 continue;
             }
@@ -657,7 +680,7 @@ __global__ void __launch_bounds__(kS8Threads, 1)
 #pragma unroll
                     for (int j = 0; j < 32; ++j)
                         s32[j] = sum[32 * b + j];
-                    finish_box(p, t, s32, sa, sb0 + 128u * b, bias0 + 128u * b, buf, row0, half0 + 32 * b, lane);
+                    finish_box(p, t, s32, small, sa, sb0 + 128u * b, bias0 + 128u * b, buf, row0, half0 + 32 * b, lane);
                 }
         }
     }
