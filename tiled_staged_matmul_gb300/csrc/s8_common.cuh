@@ -46,7 +46,8 @@ struct S8Cfg {
     static constexpr int TILE_M = ROWS * CTAS;
     static constexpr int B_COLS = 128;          // columns of B staged by one CTA
     static constexpr int TILE_N = B_COLS * CTAS;  // the MMA's width
-    static constexpr int HC = TILE_N / 2;       // columns of one epilogue half
+    static constexpr int GROUPS = 4;            // groups of four epilogue warps, one per warp of TMEM lanes
+    static constexpr int HC = TILE_N / GROUPS;  // columns of one group
     static constexpr int BK = 128;
     static constexpr int A_CODES = ROWS * BK;   // bytes
     static constexpr int B_CODES = B_COLS * BK;
@@ -54,14 +55,15 @@ struct S8Cfg {
     static constexpr int F_BOX = 64 * BK * 2;   // 64 columns of f16
     static constexpr int F_STAGE = 2 * F_BOX;
     static constexpr int S1 = 3, S2 = 3;        // ring depths
-    static constexpr int STAGING = 8 * 32 * 64;   // per epilogue warp: 32 rows of 64 bytes
-    static constexpr int TERMS = 3 * 256 * 4;     // the epilogue's column and row terms
+    static constexpr int STAGING = 4 * GROUPS * 32 * 32;  // per epilogue warp: 32 rows of 32 bytes
+    static constexpr uint32_t GROUP_TERMS = (2 * HC + ROWS) * 4;  // a group's columns' scales and biases, rows' scales
+    static constexpr uint32_t TERMS = GROUPS * GROUP_TERMS;
     static constexpr int CTRL = 2048 + 2 * TERMS, GROUP_TABLE_OFF = 1024, TERMS_OFF = 2048;
     static constexpr int SMEM_BYTES = 1024 + S1 * CODE_STAGE + S2 * F_STAGE + STAGING + CTRL;
     static_assert(SMEM_BYTES <= 232448, "227 KiB per block");
     static constexpr uint32_t A_COL = 256;      // TMEM: the accumulator, then the f16 A ring
     static_assert(A_COL + S2 * (BK / 2) <= 512 && TILE_N <= 256, "TMEM columns");
-    static constexpr int PARTS = 2 * CTAS;      // (CTA, half) parts of a tile
+    static constexpr int PARTS = GROUPS * CTAS; // (CTA, group) parts of a tile
     static constexpr int32_t SLOT_INTS = PARTS * ROWS * HC;
 };
 

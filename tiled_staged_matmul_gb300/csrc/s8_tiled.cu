@@ -33,12 +33,13 @@ constexpr int kChunkBlocks = 8;  // k-blocks of 128 whose sums the f32 accumulat
 // pause while a chunk of 1024 k is read out.  (Two accumulators of half the
 // width would not: but the MMA runs at full rate only at its full width, 256
 // columns for a pair.)
-constexpr int kWarpA = 4, kWarpB = 8, kWarpDrain = 12, kS8Warps = 20;  // first warps of the roles
+constexpr int kWarpA = 4, kWarpB = 8, kWarpDrain = 12;  // first warps of the roles
+constexpr int kDrainWarps = 16, kS8Warps = kWarpDrain + kDrainWarps;
 constexpr int kS8Threads = 32 * kS8Warps;
-// Registers per thread by warpgroup (five of 128 threads): together exactly
-// what the block was launched with (640 x 96).
-constexpr int kS8RegsIssue = 48, kS8RegsConvert = 56, kS8RegsDrain = 160;
-static_assert(128 * kS8RegsIssue + 2 * 128 * kS8RegsConvert + 2 * 128 * kS8RegsDrain <= kS8Threads * 96,
+// Registers per thread by warpgroup (seven of 128 threads): together exactly
+// what the block was launched with (896 x 72).
+constexpr int kS8RegsIssue = 40, kS8RegsConvert = 56, kS8RegsDrain = 88;
+static_assert(128 * kS8RegsIssue + 2 * 128 * kS8RegsConvert + 32 * kDrainWarps * kS8RegsDrain <= kS8Threads * 72,
               "register split");
 
 // B's shared-memory descriptor: MN-major, 64-column boxes of BK rows of 128 bytes.
@@ -151,17 +152,15 @@ __device__ __forceinline__ float add_chunk(uint32_t acc, int32_t (&sum)[HC])
 {
     float largest = 0.f;
     const float magic = __uint_as_float(kMagicBits);
-    uint32_t r[2][8];
-    ptx::tmem_ld_32x32b_x8(acc, r[0]);
 #pragma unroll
     for (int c = 0; c < HC / 8; ++c) {
-        ptx::tmem_wait_ld(r[c & 1]);
-        if (c + 1 < HC / 8)
-            ptx::tmem_ld_32x32b_x8(acc + 8u * (c + 1), r[(c + 1) & 1]);
+        uint32_t r[8];
+        ptx::tmem_ld_32x32b_x8(acc + 8u * c, r);
+        ptx::tmem_wait_ld(r);
         float f[8];
 #pragma unroll
         for (int j = 0; j < 8; ++j)
-            f[j] = __uint_as_float(r[c & 1][j]);
+            f[j] = __uint_as_float(r[j]);
         const float top = ptx::max_abs3(ptx::max_abs3(ptx::max_abs3(f[0], f[1], f[2]), f[3], f[4]), f[5],
                                         ptx::max_abs3(f[6], f[7], 0.f));
         largest = fmaxf(largest, top);
@@ -212,28 +211,28 @@ __device__ __forceinline__ void finish_box(const S8Params &p, const S8Tile &t, c
         }
     };
     const int32_t rows = t.rows - row0;
-    const uint32_t mine = buf + uint32_t(lane) * 64u, swizzle = uint32_t(lane >> 1) & 3u;
+    const uint32_t mine = buf + uint32_t(lane) * 32u, swizzle = uint32_t(lane >> 2) & 1u;
     const bool f32 = p.epi.out_type == kOutF32;
     const int elem = f32 ? 4 : 2;
-    const int per_row = 64 / elem;  // columns staged at a time: 16 f32 or 32 16-bit ones
+    const int per_row = 32 / elem;  // columns staged at a time: 8 f32 or 16 16-bit ones
 #pragma unroll
-    for (int half = 0; half < 2; ++half) {
-        if (half && !f32)
+    for (int part = 0; part < 4; ++part) {
+        if (part >= 2 && !f32)
             break;
         __syncwarp();
 #pragma unroll
-        for (int c = 0; c < 4; ++c) {
+        for (int c = 0; c < 2; ++c) {
             uint32_t w[4];
             float v[4];
             if (f32) {
-                four(16 * half + 4 * c, v);
+                four(8 * part + 4 * c, v);
 #pragma unroll
                 for (int i = 0; i < 4; ++i)
                     w[i] = __float_as_uint(v[i]);
             } else {
 #pragma unroll
                 for (int i = 0; i < 4; i += 2) {
-                    four(8 * c + 2 * i, v);
+                    four((16 * part + 8 * c + 2 * i) & 31, v);
                     w[i] = out16_pair(v[0], v[1], p.epi.out_type);
                     w[i + 1] = out16_pair(v[2], v[3], p.epi.out_type);
                 }
@@ -241,14 +240,14 @@ __device__ __forceinline__ void finish_box(const S8Params &p, const S8Tile &t, c
             ptx::st_shared_v4(mine + ((uint32_t(c) ^ swizzle) << 4), w[0], w[1], w[2], w[3]);
         }
         __syncwarp();
-        const int32_t col = col0 + 16 * half;
+        const int32_t col = col0 + part * per_row;
         char *const c_at = static_cast<char *>(p.C) + (t.z * p.sC + int64_t(row0) * p.ldc + col) * elem;
         if (p.vec_c && col + per_row <= p.N) {
-            // Four lanes a row, eight rows at a time.
+            // Two lanes a row, sixteen rows at a time.
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                const int r = 8 * i + (lane >> 2), ch = lane & 3;
-                const uint4 u = ptx::ld_shared_v4(buf + uint32_t(r) * 64u + ((uint32_t(ch) ^ (uint32_t(r >> 1) & 3u)) << 4));
+            for (int i = 0; i < 2; ++i) {
+                const int r = 16 * i + (lane >> 1), ch = lane & 1;
+                const uint4 u = ptx::ld_shared_v4(buf + uint32_t(r) * 32u + ((uint32_t(ch) ^ (uint32_t(r >> 2) & 1u)) << 4));
                 if (r < rows)
                     *reinterpret_cast<uint4 *>(c_at + r * p.ldc * elem + 16 * ch) = u;
             }
@@ -257,7 +256,7 @@ __device__ __forceinline__ void finish_box(const S8Params &p, const S8Tile &t, c
 #pragma unroll 1
             for (int i = lane; i < 32 * per_row; i += 32) {
                 const int r = i / per_row, j = i % per_row;
-                const uint32_t at = buf + uint32_t(r) * 64u + ((uint32_t(j * elem >> 4) ^ (uint32_t(r >> 1) & 3u)) << 4) +
+                const uint32_t at = buf + uint32_t(r) * 32u + ((uint32_t(j * elem >> 4) ^ (uint32_t(r >> 2) & 1u)) << 4) +
                                     uint32_t(j * elem & 15);
                 if (r < rows && col + j < p.N) {
                     if (f32)
@@ -336,7 +335,7 @@ __global__ void __launch_bounds__(kS8Threads, 1)
             ptx::mbar_init(free0 + 8u * s, 1);
         }
         ptx::mbar_init(tfull, 1);
-        ptx::mbar_init(tempty, 8 * Cfg::CTAS);
+        ptx::mbar_init(tempty, kDrainWarps * Cfg::CTAS);
         ptx::mbar_init(done_bar, 1);
         ptx::st_shared_u32(flag, 0u);
         ptx::fence_mbar_init();
@@ -542,7 +541,7 @@ __global__ void __launch_bounds__(kS8Threads, 1)
         const int h = e >> 2;
         const int q = warp & 3;
         const uint32_t acc = tmem + (uint32_t(32 * q) << 16) + uint32_t(h * Cfg::HC);
-        const uint32_t buf = staging + uint32_t(e) * 2048u;
+        const uint32_t buf = staging + uint32_t(e) * 1024u;
         uint32_t aphase = 0, turn = 0;
         bool ok = true;
         for (PieceWalk<true> w(wsched, worker); ok && w.advance(wsched);) {
@@ -576,11 +575,13 @@ __global__ void __launch_bounds__(kS8Threads, 1)
                 const S8Tile t = tile_at(w.tile, p, gtab, Cfg::TILE_M, Cfg::TILE_N);
                 const int32_t i = 32 * q + lane, col = t.n0 + h * Cfg::HC + i;
                 const int32_t row = t.m0 + int32_t(PAIR ? ptx::cluster_ctarank() : 0u) * Cfg::ROWS + i;
-                const uint32_t at = terms0 + turn * Cfg::TERMS + uint32_t(h) * 512u + 4u * i;
-                ptx::fetch_f32(at, p.scale_b && i < Cfg::HC && col < p.N ? p.scale_b + t.z * p.sb_stride + col : nullptr, 1.f);
-                ptx::fetch_f32(at + 1024u,
-                               p.epi.bias && i < Cfg::HC && col < p.N ? p.epi.bias + t.z * p.epi.bias_stride + col : nullptr, 0.f);
-                ptx::fetch_f32(at + 2048u, p.scale_a && row < t.rows ? p.scale_a + t.z * p.sa_stride + row : nullptr, 1.f);
+                const uint32_t at = terms0 + turn * Cfg::TERMS + uint32_t(h) * Cfg::GROUP_TERMS + 4u * i;
+                if (i < Cfg::HC)
+                    ptx::fetch_f32(at, p.scale_b && col < p.N ? p.scale_b + t.z * p.sb_stride + col : nullptr, 1.f);
+                if (i < Cfg::HC)
+                    ptx::fetch_f32(at + 4u * Cfg::HC,
+                               p.epi.bias && col < p.N ? p.epi.bias + t.z * p.epi.bias_stride + col : nullptr, 0.f);
+                ptx::fetch_f32(at + 8u * Cfg::HC, p.scale_a && row < t.rows ? p.scale_a + t.z * p.sa_stride + row : nullptr, 1.f);
                 if (lane == 0)
                     ptx::st_shared_v4(tiles0 + 16u * uint32_t(e), uint32_t(t.m0), uint32_t(t.n0), uint32_t(t.z),
                                       uint32_t(t.rows));
@@ -612,7 +613,7 @@ __global__ void __launch_bounds__(kS8Threads, 1)
                 const S8Schedule cut = wsched.all();
                 const int32_t first = cut.owner(w.tile * cut.kb);
                 const int32_t last = cut.owner((w.tile + 1) * cut.kb - 1);
-                const int32_t part = int32_t(rank_now) * 2 + h;
+                const int32_t part = int32_t(rank_now) * Cfg::GROUPS + h;
                 const int32_t lane_at = part * (Cfg::ROWS * Cfg::HC) + 4 * tid;
                 int32_t *const mine = p.partial + (2 * me + (me == first)) * Cfg::SLOT_INTS + lane_at;
                 if (row0 < t.rows) {
@@ -637,14 +638,14 @@ __global__ void __launch_bounds__(kS8Threads, 1)
                 cut_last = last;
             }
             const int32_t half0 = t.n0 + h * Cfg::HC;
-            const uint32_t sb0 = terms0 + turn * Cfg::TERMS + uint32_t(h) * 512u, bias0 = sb0 + 1024u;
+            const uint32_t sb0 = terms0 + turn * Cfg::TERMS + uint32_t(h) * Cfg::GROUP_TERMS, bias0 = sb0 + 4u * Cfg::HC;
             turn ^= 1u;
-            const float sa = p.epi.alpha * __uint_as_float(ptx::ld_shared_u32(sb0 + 2048u + 4u * (32 * q + lane)));
+            const float sa = p.epi.alpha * __uint_as_float(ptx::ld_shared_u32(sb0 + 8u * Cfg::HC + 4u * (32 * q + lane)));
             const bool small = __all_sync(0xffffffffu, bound < 4194304.f);
             const int32_t boxes = row0 < t.rows ? min(Cfg::HC / 32, (p.N - half0 + 31) / 32) : 0;
             if (cut_first <= cut_last) {
                 // All contributors' sums, this one's too, a box at a time.
-                const int32_t *from = p.partial + (int32_t(rank_now) * 2 + h) * (Cfg::ROWS * Cfg::HC) + 4 * tid;
+                const int32_t *from = p.partial + (int32_t(rank_now) * Cfg::GROUPS + h) * (Cfg::ROWS * Cfg::HC) + 4 * tid;
 #pragma unroll 1
                 for (int b = 0; b < boxes; ++b, from += 32 * Cfg::ROWS) {
                     int4 x[8] = {};
