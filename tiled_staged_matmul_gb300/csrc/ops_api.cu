@@ -476,7 +476,10 @@ gemm_status_t launch_product(S8Params p, DeviceState *ds, cudaStream_t stream)
     if (few) {
         // (A grouped launch's tiles are counted on the device; the estimate is
         // for one block of rows in every group.)
-        p.ranks = few_rows_ranks(p.group_rows ? int64_t(p.tiles_n) * p.batch : tiles, p.kb, g_s8_capacity[dev], kind == S8Kind::kFew32, &grid);
+        p.ranks = few_rows_ranks(p.group_rows ? int64_t(p.tiles_n) * p.batch : tiles, p.kb, g_s8_capacity[dev],
+                                 kind == S8Kind::kFew32, &grid);
+        p.kb_each = p.kb / p.ranks;
+        p.kb_more = p.kb % p.ranks;
     } else {
         sched.plan(int32_t(tiles), p.kb, p.workers);
         grid = p.group_rows ? p.workers

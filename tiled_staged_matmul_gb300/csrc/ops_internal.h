@@ -125,7 +125,8 @@ struct S8Params {
     int32_t tiles_m, tiles_n, kb;
     int32_t group_m;            // raster: tiles of M walked together
     int32_t workers;
-    int32_t ranks;              // few rows: CTAs (a cluster) that cut a tile's K
+    int32_t ranks;              // few rows: CTAs (a cluster) that cut a tile's K,
+    int32_t kb_each, kb_more;   // blocks for each, and how many take one more
     int32_t vec_c;              // C's rows are 16-byte aligned
     int32_t *partial;           // sums of pieces: two slots per worker
     unsigned long long *arrivals;  // one word per part of a shared tile: launch tag, count

@@ -17,15 +17,20 @@ namespace {
 // bytes of it ran at 4.6 TB/s, 256 at 6.0, 512 no faster).  Each warp has a TMA
 // ring of its own and never waits for another.
 //
-// Warp-wide f16 MMAs (16 rows x 8 columns x 16 k) run far below the tcgen05
-// rate, but 16 or 32 rows need no more: one SM's share of the memory rate is 23
-// codes a cycle, 16 x 23 multiply-adds.  B's codes go from shared memory to the
-// MMA's operand layout in registers: lane 4g + t takes 16 columns (chunk g) of
-// rows 4t ... 4t + 3, and a byte of two rows each makes the f16 pair that it
-// has to hold for one column.  Which columns and which k a lane's registers
-// stand for is free as long as A's lanes agree, so no transpose is needed: MMA
-// j of 16 gets column 16 g + j, and k index 2t, 2t + 1, 2t + 8, 2t + 9 is row
-// 4t, 4t + 1, 4t + 2, 4t + 3.
+// Warp-wide f16 MMAs (16 x 8 x 16 k) run far below the tcgen05 rate, but so few
+// rows need no more: one SM's share of the memory rate is 23 codes a cycle, 23
+// multiply-adds a row, and the warps' MMAs do about 500.  C^T = B^T A^T is what
+// they compute: the wide side of an MMA is 16 of B's columns, the narrow one 8
+// rows, so that 8 rows or fewer (one token, most experts of a decode step) take
+// half the MMAs that 16 take (64 experts of 1 to 16 rows: 49 -> 44 us).
+//
+// B's codes go from shared memory to the MMA's operand layout in registers:
+// lane 4g + t takes 16 columns (chunk g) of rows 4t ... 4t + 3, and a byte of
+// two rows each makes the f16 pair that it has to hold for one column.  Which
+// columns and which k a lane's registers stand for is free as long as A's lanes
+// agree, so no transpose is needed: rows g and g + 8 of MMA j of 8 are columns
+// 16 g + 2j and 16 g + 2j + 1, and k index 2t, 2t + 1, 2t + 8, 2t + 9 is row 4t,
+// 4t + 1, 4t + 2, 4t + 3.
 //
 // A warp's f32 sums go into the CTA's 32-bit ones in shared memory (integer
 // atomics: any order gives the same sum) after at most 1024 k.  There are two
@@ -43,7 +48,8 @@ struct S8FewCfg {
     static constexpr int B_BYTES = BK * 128, A_BYTES = ROWS * BK;
     static constexpr int HALF_SUMS = ROWS * 128;  // of 128 columns (few_rows_sum)
     static constexpr int SUMS = 2 * HALF_SUMS;
-    static constexpr int CTRL = 6144, GROUP_TABLE_OFF = 1024, TERMS_OFF = 2048;
+    static constexpr int CTRL = 6144, GROUP_TABLE_OFF = 1024, TERMS_OFF = 2048, GROUP_ROWS_OFF = 4608;
+    static_assert(TERMS_OFF + 4 * (2 * COLS + ROWS) <= GROUP_ROWS_OFF && kMaxGroupsPerLaunch <= 256, "control block");
     static constexpr int SMEM_BYTES = 1024 + WARPS * STAGES * (B_BYTES + A_BYTES) + 2 * SUMS * 4 + CTRL;
     static_assert(SMEM_BYTES <= 232448 && SMEM_BYTES > 232448 / 2, "227 KiB per block, one block per SM");
     static constexpr int FLUSH = 1024 / BK;   // blocks whose sums f32 holds exactly
@@ -63,55 +69,158 @@ __device__ __forceinline__ uint32_t code_pair(uint32_t lo, uint32_t hi)
 }
 
 // Where a half's sums are kept: rows in groups of eight, then column bit 4, the
-// row, and chunks of the four columns 32 apart, column j's chunk at j ^ row --
-// so that the lanes of an accumulator value (eight rows of four columns 32
-// apart) add to different banks, and sixteen threads read sixteen neighbouring
-// columns' chunks.
+// row, and chunks of the four columns 32 apart, column j's chunk at j ^ row ^
+// bit 4 -- so that the lanes of an accumulator value (four rows of eight
+// columns 16 apart) add to different banks, and sixteen threads read sixteen
+// neighbouring columns' chunks.
 __device__ __forceinline__ constexpr int few_rows_sum(int octet, int d1, int row, int j, int t)
 {
-    return ((octet * 2 + d1) * 8 + row) * 64 + 4 * (j ^ row) + t;
+    return ((octet * 2 + d1) * 8 + row) * 64 + 4 * (j ^ row ^ d1) + t;
 }
 
 // A CTA's addresses and place in the launch.
 struct FewPlace {
     uint32_t sums0, terms0;                       // shared memory: [2][SUMS] ints; scales and biases
     uint32_t sums_full0, sums_free0, ready0, taken0;  // barriers, [2] each
-    uint32_t flag, gtab;
+    uint32_t flag, gtab, grows;                   // ...; the groups' tiles, summed, and their rows
     int32_t tiles, cluster, clusters, rank, ranks;
+    int32_t last, last_set;                       // the CTA's last tile, and the sums it is in
 };
 
-// The finishing warps: tile by tile, the cluster's sums of this CTA's share of
-// the tile through the epilogue into C.
+// Where a tile lies; `rows` is its own number of them.  (Short of divisions:
+// the first block waits for this.  A matrix has one tile along M, a group at
+// most two.)
 template <int MT>
-__device__ __forceinline__ void few_rows_finish(const S8Params &p, const FewPlace &f, int lane)
+__device__ __forceinline__ S8Tile few_rows_tile(const S8Params &p, const FewPlace &f, int32_t tile)
+{
+    using Cfg = S8FewCfg<MT>;
+    S8Tile t = {0, tile, 0, p.M};
+    if (p.group_rows) {
+        int32_t lo = 0, hi = p.batch - 1;
+        while (lo < hi) {
+            const int32_t mid = (lo + hi) >> 1;
+            if (int32_t(ptx::ld_shared_u32(f.gtab + 4u * mid)) > tile)
+                hi = mid;
+            else
+                lo = mid + 1;
+        }
+        t.z = lo;
+        t.rows = int32_t(ptx::ld_shared_u32(f.grows + 4u * lo));
+        const int32_t i = tile - (lo ? int32_t(ptx::ld_shared_u32(f.gtab + 4u * (lo - 1))) : 0);
+        const int two = t.rows > Cfg::ROWS;
+        t.m0 = (i & two) * Cfg::ROWS;
+        t.n0 = i >> two;
+    } else if (p.batch > 1) {
+        t.z = tile / p.tiles_n;
+        t.n0 = tile - t.z * p.tiles_n;
+    }
+    t.n0 *= Cfg::COLS;
+    t.rows = min(t.rows - t.m0, Cfg::ROWS);
+    return t;
+}
+
+// Before the first tile: the sums are clear, and the CTA's barriers exist.
+template <int MT>
+__device__ __forceinline__ void few_rows_start(const FewPlace &f)
+{
+    using Cfg = S8FewCfg<MT>;
+    for (int i = int(threadIdx.x); i < 2 * Cfg::SUMS / 4; i += Cfg::THREADS)
+        ptx::st_shared_v4(f.sums0 + 16u * i, 0u, 0u, 0u, 0u);
+    ptx::cta_sync();
+}
+
+// The first thing of a tile's end: the terms of its epilogue, while the sums
+// are on their way (the finishing warps').
+template <int MT>
+__device__ __forceinline__ S8Tile few_rows_terms(const S8Params &p, const FewPlace &f, int32_t tile, int ft)
+{
+    using Cfg = S8FewCfg<MT>;
+    constexpr int FT = 32 * Cfg::FINISHERS;
+    const S8Tile t = few_rows_tile<MT>(p, f, tile);
+    for (int c = ft; c < Cfg::COLS; c += FT) {
+        const int32_t col = t.n0 + c;
+        float sb = p.epi.alpha, bias = 0.f;
+        if (p.scale_b && col < p.N)
+            sb *= __ldg(p.scale_b + t.z * p.sb_stride + col);
+        if (p.epi.bias && col < p.N)
+            bias = __ldg(p.epi.bias + t.z * p.epi.bias_stride + col);
+        ptx::st_shared_u32(f.terms0 + 4u * c, __float_as_uint(sb));
+        ptx::st_shared_u32(f.terms0 + 4u * (Cfg::COLS + c), __float_as_uint(bias));
+    }
+    if (ft < Cfg::ROWS)
+        ptx::st_shared_u32(f.terms0 + 4u * (2 * Cfg::COLS + ft),
+                           __float_as_uint(p.scale_a && ft < t.rows
+                                               ? __ldg(p.scale_a + t.z * p.sa_stride + t.m0 + ft) : 1.f));
+    return t;
+}
+
+// This CTA's share of a tile: the cluster's sums through the epilogue into C,
+// by `threads` threads.  In chunks of four columns 32 apart, two rows' sixteen
+// a warp; rows past the last are left out in eights.
+template <int MT>
+__device__ __forceinline__ void few_rows_share(const S8Params &p, const FewPlace &f, const S8Tile &t, uint32_t sums,
+                                               int thread, int threads)
+{
+    using Cfg = S8FewCfg<MT>;
+    const uint32_t sb0 = f.terms0, bias0 = f.terms0 + 4u * Cfg::COLS, sa0 = f.terms0 + 8u * Cfg::COLS;
+    const int octets = (t.rows + 7) / 8, lane = thread & 31;
+    for (int u = f.rank + f.ranks * (thread >> 5); u < 16 * octets; u += f.ranks * (threads >> 5)) {
+        const int i = 32 * u + lane;
+        const int j = i & 15, r8 = (i >> 4) & 7, d1 = (i >> 7) & 1, ho = i >> 8;
+        const int h = ho >= octets, octet = ho - h * octets;
+        const int row = 8 * octet + r8;
+        if (row >= t.rows)
+            continue;
+        const uint32_t at = sums + 4u * uint32_t(h * Cfg::HALF_SUMS + few_rows_sum(octet, d1, r8, j, 0));
+        // Every CTA's chunk on its way at once.
+        uint4 x[8];
+        int32_t v[4] = {};
+#pragma unroll
+        for (int r = 0; r < 8; ++r)
+            x[r] = r < f.ranks ? ptx::ld_cluster_v4(ptx::mapa_shared(at, uint32_t(r))) : make_uint4(0, 0, 0, 0);
+#pragma unroll
+        for (int r = 0; r < 8; ++r) {
+            v[0] += int32_t(x[r].x);
+            v[1] += int32_t(x[r].y);
+            v[2] += int32_t(x[r].z);
+            v[3] += int32_t(x[r].w);
+        }
+        const float sa = __uint_as_float(ptx::ld_shared_u32(sa0 + 4u * row));
+        const int c = 128 * h + 16 * d1 + j;
+        const int64_t row_at = t.z * p.sC + int64_t(t.m0 + row) * p.ldc + t.n0;
+        const int32_t columns = p.N - t.n0;
+        with_activation<kActRuntime>(p.epi.act, [&](auto act) {
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+                const float sb = __uint_as_float(ptx::ld_shared_u32(sb0 + 4u * (c + 32 * k)));
+                const float bias = __uint_as_float(ptx::ld_shared_u32(bias0 + 4u * (c + 32 * k)));
+                const float o = epi_act(fmaf(sb, float(v[k]) * sa, bias), decltype(act)::value, p.epi.slope);
+                if (c + 32 * k < columns)
+                    epi_store(p.C, row_at + c + 32 * k, o, p.epi.out_type);
+            }
+        });
+    }
+}
+
+// The finishing warps: every tile but the CTA's last, whose terms they fetch.
+template <int MT>
+__device__ __forceinline__ bool few_rows_finish(const S8Params &p, FewPlace &f)
 {
     using Cfg = S8FewCfg<MT>;
     constexpr int FT = 32 * Cfg::FINISHERS;
     const int ft = int(threadIdx.x) - 32 * Cfg::WARPS;
-    const uint32_t sb0 = f.terms0, bias0 = f.terms0 + 4u * Cfg::COLS, sa0 = f.terms0 + 8u * Cfg::COLS;
     uint32_t set = 0, phase = 0;
     for (int32_t tile = f.cluster; tile < f.tiles; tile += f.clusters) {
-        S8Tile t = tile_at(tile, p, f.gtab, Cfg::ROWS, Cfg::COLS);
-        t.rows = min(t.rows - t.m0, Cfg::ROWS);  // (from here on: the tile's)
-        // The terms of the epilogue while the sums are on their way.
-        for (int c = ft; c < Cfg::COLS; c += FT) {
-            const int32_t col = t.n0 + c;
-            float sb = p.epi.alpha, bias = 0.f;
-            if (p.scale_b && col < p.N)
-                sb *= __ldg(p.scale_b + t.z * p.sb_stride + col);
-            if (p.epi.bias && col < p.N)
-                bias = __ldg(p.epi.bias + t.z * p.epi.bias_stride + col);
-            ptx::st_shared_u32(sb0 + 4u * c, __float_as_uint(sb));
-            ptx::st_shared_u32(bias0 + 4u * c, __float_as_uint(bias));
-        }
-        if (ft < Cfg::ROWS)
-            ptx::st_shared_u32(sa0 + 4u * ft, __float_as_uint(p.scale_a && ft < t.rows
-                                                                  ? __ldg(p.scale_a + t.z * p.sa_stride + t.m0 + ft) : 1.f));
+        const S8Tile t = few_rows_terms<MT>(p, f, tile, ft);
+        f.last = tile;
+        f.last_set = int32_t(set);
+        if (f.tiles - tile <= f.clusters)
+            break;
         const uint32_t sums = f.sums0 + set * uint32_t(Cfg::SUMS * 4);
         bool ok = s8_wait<false>(f.sums_full0 + 8u * set, phase, f.flag, p, kStatusEpilogue);
         ok = __all_sync(0xffffffffu, ptx::named_bar_and(1, FT, ok));
         if (!ok)
-            return;
+            return false;
         if (f.ranks > 1) {
             // This CTA's sums are complete: so says one thread to every CTA.
             if (ft < f.ranks)
@@ -119,87 +228,54 @@ __device__ __forceinline__ void few_rows_finish(const S8Params &p, const FewPlac
             ok = s8_wait<false, true>(f.ready0 + 8u * set, phase, f.flag, p, kStatusReduce);
             ok = __all_sync(0xffffffffu, ptx::named_bar_and(1, FT, ok));
             if (!ok)
-                return;
+                return false;
         }
-        // This CTA's share of the tile, in chunks of four columns 32 apart;
-        // rows past the last are left out in eights.
-        const int octets = (t.rows + 7) / 8, chunks = 2 * octets * 256;
-        const int last = (f.rank + 1) * chunks / f.ranks;
-        for (int i = f.rank * chunks / f.ranks + ft; i < last; i += FT) {
-            const int j = i & 15, r8 = (i >> 4) & 7, d1 = (i >> 7) & 1, ho = i >> 8;
-            const int h = ho >= octets, octet = ho - h * octets;
-            const int row = 8 * octet + r8;
-            if (row >= t.rows)
-                continue;
-            const uint32_t at = sums + 4u * uint32_t(h * Cfg::HALF_SUMS + few_rows_sum(octet, d1, r8, j, 0));
-            // Every CTA's chunk on its way at once.
-            uint4 x[8];
-            int32_t v[4] = {};
-#pragma unroll
-            for (int r = 0; r < 8; ++r)
-                x[r] = r < f.ranks ? ptx::ld_cluster_v4(ptx::mapa_shared(at, uint32_t(r))) : make_uint4(0, 0, 0, 0);
-#pragma unroll
-            for (int r = 0; r < 8; ++r) {
-                v[0] += int32_t(x[r].x);
-                v[1] += int32_t(x[r].y);
-                v[2] += int32_t(x[r].z);
-                v[3] += int32_t(x[r].w);
-            }
-            const float sa = __uint_as_float(ptx::ld_shared_u32(sa0 + 4u * row));
-            const int c = 128 * h + 16 * d1 + j;
-            const int64_t row_at = t.z * p.sC + int64_t(t.m0 + row) * p.ldc + t.n0;
-            const int32_t columns = p.N - t.n0;
-            with_activation<kActRuntime>(p.epi.act, [&](auto act) {
-#pragma unroll
-                for (int k = 0; k < 4; ++k) {
-                    const float sb = __uint_as_float(ptx::ld_shared_u32(sb0 + 4u * (c + 32 * k)));
-                    const float bias = __uint_as_float(ptx::ld_shared_u32(bias0 + 4u * (c + 32 * k)));
-                    const float o = epi_act(fmaf(sb, float(v[k]) * sa, bias), decltype(act)::value, p.epi.slope);
-                    if (c + 32 * k < columns)
-                        epi_store(p.C, row_at + c + 32 * k, o, p.epi.out_type);
-                }
-            });
-        }
+        few_rows_share<MT>(p, f, t, sums, ft, FT);
         ptx::named_bar_sync(1, FT);  // the sums and the terms have been read here
-        if (f.ranks > 1) {
-            // ... and in every CTA of the cluster, before they are cleared.
-            if (ft < f.ranks)
-                ptx::mbar_arrive_cluster(ptx::mapa_shared(f.taken0 + 8u * set, uint32_t(ft)));
-            ok = s8_wait<false, true>(f.taken0 + 8u * set, phase, f.flag, p, kStatusReduce);
-            ok = __all_sync(0xffffffffu, ptx::named_bar_and(1, FT, ok));
-            if (!ok)
-                return;
+        if (f.tiles - tile > 2 * f.clusters) {  // (else the set is not used again)
+            if (f.ranks > 1) {
+                // ... and in every CTA of the cluster, before they are cleared.
+                if (ft < f.ranks)
+                    ptx::mbar_arrive_cluster(ptx::mapa_shared(f.taken0 + 8u * set, uint32_t(ft)));
+                ok = s8_wait<false, true>(f.taken0 + 8u * set, phase, f.flag, p, kStatusReduce);
+                ok = __all_sync(0xffffffffu, ptx::named_bar_and(1, FT, ok));
+                if (!ok)
+                    return false;
+            }
+            for (int i = ft; i < Cfg::SUMS / 4; i += FT)
+                ptx::st_shared_v4(sums + 16u * i, 0u, 0u, 0u, 0u);
+            ptx::named_bar_sync(1, FT);
+            if (ft == 0)
+                ptx::mbar_arrive(f.sums_free0 + 8u * set);
         }
-        for (int i = ft; i < Cfg::SUMS / 4; i += FT)
-            ptx::st_shared_v4(sums + 16u * i, 0u, 0u, 0u, 0u);
-        ptx::named_bar_sync(1, FT);
-        if (ft == 0)
-            ptx::mbar_arrive(f.sums_free0 + 8u * set);
         set ^= 1u;
         if (set == 0)
             phase ^= 1u;
     }
+    return true;
 }
 
 // The multiplying warps.
 template <int MT>
-__device__ __forceinline__ void few_rows_multiply(const CUtensorMap &map_a, const CUtensorMap &map_b,
-                                                  const S8Params &p, const FewPlace &f, uint32_t full0,
+__device__ __forceinline__ bool few_rows_multiply(const CUtensorMap &map_a, const CUtensorMap &map_b,
+                                                  const S8Params &p, FewPlace &f, uint32_t full0,
                                                   uint32_t ring_b, uint32_t ring_a, int32_t *sums0, int warp, int lane)
 {
     using Cfg = S8FewCfg<MT>;
     constexpr uint32_t S = Cfg::STAGES;
+    constexpr int NB = 2 * MT;  // blocks of eight rows
     const int g = lane >> 2, t4 = lane & 3;
     const int half = warp & 1;
     // This CTA's k-blocks, and the warp's first of them.
-    const int32_t end = int32_t(int64_t(f.rank + 1) * p.kb / f.ranks);
-    const int32_t begin = int32_t(int64_t(f.rank) * p.kb / f.ranks) + (warp >> 1);
+    const int32_t first = f.rank * p.kb_each + min(f.rank, p.kb_more);
+    const int32_t end = first + p.kb_each + (f.rank < p.kb_more);
+    const int32_t begin = first + (warp >> 1);
 
     // The warp's loads run S blocks ahead of its MMAs.
     int32_t next_tile = f.cluster, next_k = begin;
     S8Tile pt = {};
     if (next_tile < f.tiles)
-        pt = tile_at(next_tile, p, f.gtab, Cfg::ROWS, Cfg::COLS);
+        pt = few_rows_tile<MT>(p, f, next_tile);
     uint32_t issued = 0;  // stages that hold or await a block
     auto issue = [&](uint32_t stage) {
         if (next_k >= end) {
@@ -208,7 +284,7 @@ __device__ __forceinline__ void few_rows_multiply(const CUtensorMap &map_a, cons
             next_k = begin;
             next_tile += f.clusters;
             if (next_tile < f.tiles)
-                pt = tile_at(next_tile, p, f.gtab, Cfg::ROWS, Cfg::COLS);
+                pt = few_rows_tile<MT>(p, f, next_tile);
         }
         if (next_tile >= f.tiles) {
             next_k = end;  // (comes back here; the tile only grows)
@@ -227,20 +303,24 @@ __device__ __forceinline__ void few_rows_multiply(const CUtensorMap &map_a, cons
 #pragma unroll 1
     for (uint32_t s = 0; s < S; ++s)
         issue(s);
+    few_rows_start<MT>(f);  // (while those are on their way: 1 us)
 
     uint32_t stage = 0, phase = 0, set = 0, set_phase = 0;
     bool ok = true;
     for (int32_t tile = f.cluster; ok && tile < f.tiles; tile += f.clusters) {
         int32_t *const sums = sums0 + set * Cfg::SUMS + half * Cfg::HALF_SUMS;
+        f.last = tile;
+        f.last_set = int32_t(set);
         bool mine = false;  // the set is this tile's
-        float acc[MT][16][4];
+        const int octets = (few_rows_tile<MT>(p, f, tile).rows + 7) / 8;
+        float acc[NB][8][4];
 #pragma unroll
-        for (int m = 0; m < MT; ++m)
+        for (int n = 0; n < NB; ++n)
 #pragma unroll
-            for (int j = 0; j < 16; ++j)
+            for (int j = 0; j < 8; ++j)
 #pragma unroll
                 for (int d = 0; d < 4; ++d)
-                    acc[m][j][d] = 0.f;
+                    acc[n][j][d] = 0.f;
         auto take = [&]() {  // the set's last tile has left it
             if (!mine)
                 ok = __all_sync(0xffffffffu, s8_wait<false>(f.sums_free0 + 8u * set, set_phase ^ 1u, f.flag, p, kStatusReduce));
@@ -251,14 +331,18 @@ __device__ __forceinline__ void few_rows_multiply(const CUtensorMap &map_a, cons
             if (!take())
                 return;
 #pragma unroll
-            for (int m = 0; m < MT; ++m)
+            for (int n = 0; n < NB; ++n) {
+                if (n >= octets)
+                    break;
 #pragma unroll
-                for (int j = 0; j < 16; ++j)
+                for (int j = 0; j < 8; ++j)
 #pragma unroll
                     for (int d = 0; d < 4; ++d) {
-                        atomicAdd(sums + few_rows_sum(2 * m + (d >> 1), d & 1, g, j, t4), __float2int_rn(acc[m][j][d]));
-                        acc[m][j][d] = 0.f;
+                        atomicAdd(sums + few_rows_sum(n, g & 1, 2 * t4 + (d & 1), 2 * j + (d >> 1), g >> 1),
+                                  __float2int_rn(acc[n][j][d]));
+                        acc[n][j][d] = 0.f;
                     }
+            }
         };
         int held = 0;
         for (int32_t kb = begin; kb < end; kb += Cfg::KWARPS) {
@@ -269,14 +353,11 @@ __device__ __forceinline__ void few_rows_multiply(const CUtensorMap &map_a, cons
             const uint32_t sb = ring_b + stage * Cfg::B_BYTES, sa = ring_a + stage * Cfg::A_BYTES;
 #pragma unroll 1
             for (int kk = 0; kk < 2; ++kk) {
-                uint32_t a[MT][4];
+                uint32_t a[NB][2];
 #pragma unroll
-                for (int m = 0; m < MT; ++m) {
-                    codes_to_f16(ptx::ld_shared_u32(sa + uint32_t((16 * m + g) * Cfg::BK + 16 * kk + 4 * t4)),
-                                 a[m][0], a[m][2]);
-                    codes_to_f16(ptx::ld_shared_u32(sa + uint32_t((16 * m + g + 8) * Cfg::BK + 16 * kk + 4 * t4)),
-                                 a[m][1], a[m][3]);
-                }
+                for (int n = 0; n < NB; ++n)
+                    codes_to_f16(ptx::ld_shared_u32(sa + uint32_t((8 * n + g) * Cfg::BK + 16 * kk + 4 * t4)), a[n][0],
+                                 a[n][1]);
                 uint32_t r[4][4];
 #pragma unroll
                 for (int i = 0; i < 4; ++i) {
@@ -289,18 +370,17 @@ __device__ __forceinline__ void few_rows_multiply(const CUtensorMap &map_a, cons
                 }
 #pragma unroll
                 for (int x = 0; x < 4; ++x) {
-                    auto column = [&](auto b) {
-                        constexpr int B = decltype(b)::value;
-                        const uint32_t b0 = code_pair<B>(r[0][x], r[1][x]);
-                        const uint32_t b1 = code_pair<B>(r[2][x], r[3][x]);
+                    auto columns = [&](auto half_word) {
+                        constexpr int B = decltype(half_word)::value;
+                        const uint32_t b[4] = {code_pair<B>(r[0][x], r[1][x]), code_pair<B + 1>(r[0][x], r[1][x]),
+                                               code_pair<B>(r[2][x], r[3][x]), code_pair<B + 1>(r[2][x], r[3][x])};
+                        ptx::mma_16816(acc[0][2 * x + B / 2], b, a[0][0], a[0][1]);
 #pragma unroll
-                        for (int m = 0; m < MT; ++m)
-                            ptx::mma_16816(acc[m][4 * x + B], a[m], b0, b1);
+                        for (int n = 1; n < NB; ++n)
+                            ptx::mma_16816_if(n < octets, acc[n][2 * x + B / 2], b, a[n][0], a[n][1]);
                     };
-                    column(ActTag<0>{});
-                    column(ActTag<1>{});
-                    column(ActTag<2>{});
-                    column(ActTag<3>{});
+                    columns(ActTag<0>{});
+                    columns(ActTag<2>{});
                 }
             }
             __syncwarp();  // every lane has read the stage
@@ -337,6 +417,7 @@ __device__ __forceinline__ void few_rows_multiply(const CUtensorMap &map_a, cons
             phase ^= 1u;
         }
     }
+    return ok;
 }
 
 template <int MT>
@@ -367,16 +448,23 @@ __global__ void __launch_bounds__(S8FewCfg<MT>::THREADS, 1)
     f.taken0 = ctrl + 432u;
     f.flag = ctrl + 448u;
     f.gtab = ctrl + Cfg::GROUP_TABLE_OFF;
+    f.grows = ctrl + Cfg::GROUP_ROWS_OFF;
     f.ranks = p.ranks;
     f.rank = int32_t(ptx::cluster_ctarank());
-    f.cluster = int32_t(blockIdx.x) / p.ranks;
-    f.clusters = int32_t(gridDim.x) / p.ranks;
+    f.cluster = int32_t(ptx::cluster_id());
+    f.clusters = int32_t(ptx::n_clusters());
+    f.last = -1;
+    f.last_set = 0;
 
-    if (threadIdx.x == 0) {
+    // A multiplying warp's own barriers are all that its first loads need.
+    if (warp < Cfg::WARPS && lane == 0) {
+        for (int s = 0; s < S; ++s)
+            ptx::mbar_init(ctrl + 8u * uint32_t(warp * S + s), 1);
+        ptx::fence_mbar_init();
+    }
+    if (int(threadIdx.x) == 32 * Cfg::WARPS) {
         ptx::prefetch_tensormap(&map_a);
         ptx::prefetch_tensormap(&map_b);
-        for (int i = 0; i < Cfg::WARPS * S; ++i)
-            ptx::mbar_init(ctrl + 8u * i, 1);
         for (uint32_t i = 0; i < 2; ++i) {
             ptx::mbar_init(f.sums_full0 + 8u * i, Cfg::WARPS);
             ptx::mbar_init(f.sums_free0 + 8u * i, 1);
@@ -386,31 +474,55 @@ __global__ void __launch_bounds__(S8FewCfg<MT>::THREADS, 1)
         ptx::st_shared_u32(f.flag, 0u);
         ptx::fence_mbar_init();
     }
-    for (int i = int(threadIdx.x); i < 2 * Cfg::SUMS / 4; i += Cfg::THREADS)
-        ptx::st_shared_v4(f.sums0 + 16u * i, 0u, 0u, 0u, 0u);
+    __syncwarp();
+    // (Relaxed, and before the first loads: a release would wait for those, 2.8
+    // us.  The barriers' fence has published all that the others need.)
+    if (p.ranks > 1)
+        ptx::cluster_arrive_relaxed();
     chain_next();
     chain_wait();
-    if (warp == 1 && p.group_rows) {
-        build_group_table(p.group_rows, p.batch, p.M, Cfg::ROWS, p.tiles_n,
-                          reinterpret_cast<uint32_t *>(base_ptr + CTRL0 + Cfg::GROUP_TABLE_OFF), p.status);
+    if (p.group_rows) {
+        if (warp == 1)
+            build_group_table(p.group_rows, p.batch, p.M, Cfg::ROWS, p.tiles_n,
+                              reinterpret_cast<uint32_t *>(base_ptr + CTRL0 + Cfg::GROUP_TABLE_OFF), p.status);
+        for (int i = int(threadIdx.x); i < p.batch; i += Cfg::THREADS)
+            ptx::st_shared_u32(f.grows + 4u * i, uint32_t(min(max(p.group_rows[i], 0), p.M)));
+        __syncthreads();
     }
-    __syncthreads();
-    if (p.ranks > 1)
-        ptx::cluster_sync();  // the other CTAs' barriers exist
     f.tiles = p.group_rows ? int32_t(ptx::ld_shared_u32(f.gtab + 4u * (p.batch - 1)))
                            : p.tiles_m * p.tiles_n * p.batch;
+    bool ok = true;
     if (warp < Cfg::WARPS) {
         ptx::regs_inc<Cfg::MMA_REGS>();
-        few_rows_multiply<MT>(map_a, map_b, p, f, ctrl + uint32_t(warp * S) * 8u,
-                              base + uint32_t(warp * S) * Cfg::B_BYTES, base + A0 + uint32_t(warp * S) * Cfg::A_BYTES,
-                              reinterpret_cast<int32_t *>(base_ptr + SUMS0), warp, lane);
+        ok = few_rows_multiply<MT>(map_a, map_b, p, f, ctrl + uint32_t(warp * S) * 8u,
+                                   base + uint32_t(warp * S) * Cfg::B_BYTES,
+                                   base + A0 + uint32_t(warp * S) * Cfg::A_BYTES,
+                                   reinterpret_cast<int32_t *>(base_ptr + SUMS0), warp, lane);
+        ptx::regs_dec<Cfg::LAUNCH_REGS>();
+        if (p.ranks > 1)
+            ptx::cluster_wait();
     } else {
         ptx::regs_dec<Cfg::FINISH_REGS>();
-        few_rows_finish<MT>(p, f, lane);
+        few_rows_start<MT>(f);
+        if (p.ranks > 1)
+            ptx::cluster_wait();  // the other CTAs' barriers exist
+        ok = few_rows_finish<MT>(p, f);
+        ptx::regs_inc<Cfg::LAUNCH_REGS>();
     }
+    // The CTA's last tile has nothing to hide behind, and every warp takes part
+    // in finishing it (four warps alone took 2 us for 16 rows, these 0.6).
     __syncwarp();
+    ok = __syncthreads_and(ok);
     if (p.ranks > 1)
-        ptx::cluster_sync();  // no CTA leaves while another may still reach into it
+        ptx::cluster_sync();  // the cluster's sums are complete
+    if (ok && f.last >= 0)
+        few_rows_share<MT>(p, f, few_rows_tile<MT>(p, f, f.last), f.sums0 + uint32_t(f.last_set) * uint32_t(Cfg::SUMS * 4),
+                           int(threadIdx.x), Cfg::THREADS);
+    __syncwarp();
+    if (p.ranks > 1) {  // no CTA leaves while another may still reach into it
+        ptx::cluster_arrive_relaxed();
+        ptx::cluster_wait();
+    }
 }
 
 // ------------------------------------------------------------- repacking
