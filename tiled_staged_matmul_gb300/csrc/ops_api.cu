@@ -454,7 +454,6 @@ gemm_status_t launch_product(S8Params p, DeviceState *ds, cudaStream_t stream)
     p.tiles_m = int32_t((int64_t(p.M) + shape.tile_m - 1) / shape.tile_m);
     p.tiles_n = int32_t((int64_t(p.N) + shape.tile_n - 1) / shape.tile_n);
     p.kb = int32_t((int64_t(p.K) + shape.block_k - 1) / shape.block_k);
-    p.group_m = 8;
     p.workers = kind == S8Kind::kPair ? ds->sms / 2 : ds->sms;
     p.timeout_ns = 2000000000ull + uint64_t(p.kb) * 20000ull;
     p.tag = next_launch_epoch() >> 16;
@@ -482,6 +481,7 @@ gemm_status_t launch_product(S8Params p, DeviceState *ds, cudaStream_t stream)
         p.kb_more = p.kb % p.ranks;
     } else {
         sched.plan(int32_t(tiles), p.kb, p.workers);
+        p.sched = sched;
         grid = p.group_rows ? p.workers
                             : int(std::max<int64_t>(sched.shared ? sched.cutters : 0,
                                                     std::min<int64_t>(sched.tiles, p.workers)));

@@ -123,7 +123,7 @@ struct S8Params {
     uint32_t *status;
     uint64_t timeout_ns;
     int32_t tiles_m, tiles_n, kb;
-    int32_t group_m;            // raster: tiles of M walked together
+    S8Schedule sched;           // tiled kernels, unless grouped (then it is made on the device)
     int32_t workers;
     int32_t ranks;              // few rows: CTAs (a cluster) that cut a tile's K,
     int32_t kb_each, kb_more;   // blocks for each, and how many take one more

@@ -96,17 +96,9 @@ __device__ __forceinline__ S8Tile few_rows_tile(const S8Params &p, const FewPlac
     using Cfg = S8FewCfg<MT>;
     S8Tile t = {0, tile, 0, p.M};
     if (p.group_rows) {
-        int32_t lo = 0, hi = p.batch - 1;
-        while (lo < hi) {
-            const int32_t mid = (lo + hi) >> 1;
-            if (int32_t(ptx::ld_shared_u32(f.gtab + 4u * mid)) > tile)
-                hi = mid;
-            else
-                lo = mid + 1;
-        }
-        t.z = lo;
-        t.rows = int32_t(ptx::ld_shared_u32(f.grows + 4u * lo));
-        const int32_t i = tile - (lo ? int32_t(ptx::ld_shared_u32(f.gtab + 4u * (lo - 1))) : 0);
+        int32_t i = tile;
+        t.z = group_of(i, p.batch, f.gtab);
+        t.rows = int32_t(ptx::ld_shared_u32(f.grows + 4u * t.z));
         const int two = t.rows > Cfg::ROWS;
         t.m0 = (i & two) * Cfg::ROWS;
         t.n0 = i >> two;
@@ -483,10 +475,7 @@ __global__ void __launch_bounds__(S8FewCfg<MT>::THREADS, 1)
     chain_wait();
     if (p.group_rows) {
         if (warp == 1)
-            build_group_table(p.group_rows, p.batch, p.M, Cfg::ROWS, p.tiles_n,
-                              reinterpret_cast<uint32_t *>(base_ptr + CTRL0 + Cfg::GROUP_TABLE_OFF), p.status);
-        for (int i = int(threadIdx.x); i < p.batch; i += Cfg::THREADS)
-            ptx::st_shared_u32(f.grows + 4u * i, uint32_t(min(max(p.group_rows[i], 0), p.M)));
+            build_s8_groups<Cfg::ROWS>(p, f.gtab, f.grows);
         __syncthreads();
     }
     f.tiles = p.group_rows ? int32_t(ptx::ld_shared_u32(f.gtab + 4u * (p.batch - 1)))

@@ -183,17 +183,6 @@ __device__ __forceinline__ float max_abs3(float a, float b, float c)
     return d;
 }
 
-// 16 bytes through L2 (not L1), in program order with the other accesses.
-__device__ __forceinline__ int4 ld_cg_v4(const int4 *p)
-{
-    int4 v;
-    asm volatile("ld.global.cg.v4.s32 {%0, %1, %2, %3}, [%4];"
-                 : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
-                 : "l"(p)
-                 : "memory");
-    return v;
-}
-
 __device__ __forceinline__ void st_shared_u32(uint32_t addr, uint32_t v)
 {
     asm volatile("st.shared.b32 [%0], %1;" ::"r"(addr), "r"(v) : "memory");

@@ -36,6 +36,7 @@ constexpr int kChunkBlocks = 8;  // k-blocks of 128 whose sums the f32 accumulat
 constexpr int kWarpA = 4, kWarpB = 8, kWarpDrain = 12;  // first warps of the roles
 constexpr int kDrainWarps = 16, kS8Warps = kWarpDrain + kDrainWarps;
 constexpr int kS8Threads = 32 * kS8Warps;
+constexpr int kBarGroup = 1, kBarSetup = 5;  // named barriers: four epilogue groups' (1 ... 4), the setup's
 // Registers per thread by warpgroup (seven of 128 threads): together exactly
 // what the block was launched with (896 x 72).
 constexpr int kS8RegsIssue = 40, kS8RegsConvert = 56, kS8RegsDrain = 88;
@@ -316,7 +317,7 @@ __global__ void __launch_bounds__(kS8Threads, 1)
     const SharedSchedule<false> sched{ctrl + 256u};
     const SharedSchedule<true> wsched{ctrl + 256u};
     const uint32_t last_flag = ctrl + 184u;    // [2] one per column half
-    const uint32_t gtab = ctrl + Cfg::GROUP_TABLE_OFF;
+    const uint32_t gtab = ctrl + Cfg::GROUP_TABLE_OFF, grows = ctrl + Cfg::GROUP_ROWS_OFF;
     const uint32_t tiles0 = ctrl + 512u;  // [8] an epilogue warp's tile
     const uint32_t terms0 = ctrl + Cfg::TERMS_OFF;  // [2][columns' scales, biases, rows' scales][256]
 
@@ -338,33 +339,45 @@ __global__ void __launch_bounds__(kS8Threads, 1)
         ptx::mbar_init(tempty, kDrainWarps * Cfg::CTAS);
         ptx::mbar_init(done_bar, 1);
         ptx::st_shared_u32(flag, 0u);
+        if (!p.group_rows)
+            sched.put(p.sched);
         ptx::fence_mbar_init();
         ptx::prefetch_tensormap(&map_a);
         ptx::prefetch_tensormap(&map_b);
     }
     __syncwarp();
+    ptx::cta_sync();  // the barriers are there
     if constexpr (PAIR)
-        ptx::cluster_sync();
+        ptx::cluster_arrive_relaxed();
     chain_next();
-    if (warp == 1) {
-        ptx::tmem_alloc<PAIR>(ptx::smem_addr(tmem_slot), 512);
-        ptx::tmem_relinquish<PAIR>();
+    // Unless the tiles are counted on the device, the producer has all it needs
+    // by now, and its first loads do not wait for the rest (0.6 us, 1.5 in a
+    // pair).
+    const bool early = warp == 0 && !p.group_rows;
+    if (!early) {
+        if constexpr (PAIR)
+            ptx::cluster_wait();  // the peer is there, and its barriers
+        if (warp == 1) {
+            ptx::tmem_alloc<PAIR>(ptx::smem_addr(tmem_slot), 512);
+            ptx::tmem_relinquish<PAIR>();
+        }
     }
     chain_wait();
-    if (warp == 2 && p.group_rows) {
-        build_group_table(p.group_rows, p.batch, p.M, Cfg::TILE_M, p.tiles_n,
-                          reinterpret_cast<uint32_t *>(ctrl_ptr + Cfg::GROUP_TABLE_OFF), p.status);
-        __syncwarp();
+    if (!early) {
+        if (warp == 2 && p.group_rows) {
+            build_s8_groups<Cfg::TILE_M>(p, gtab, grows);
+            if (lane == 0) {
+                S8Schedule s;
+                s.plan(int32_t(ptx::ld_shared_u32(gtab + 4u * (p.batch - 1))), p.kb, p.workers);
+                sched.put(s);
+            }
+        }
+        // (All warps that came here: all, or all but the first.)
+        ptx::tc_fence_before_sync();
+        ptx::named_bar_sync(kBarSetup, p.group_rows ? kS8Threads : kS8Threads - 32);
+        ptx::tc_fence_after_sync();
     }
-    if (warp == 2 && lane == 0) {
-        S8Schedule s;
-        s.plan(p.group_rows ? int32_t(ptx::ld_shared_u32(gtab + 4u * (p.batch - 1))) : p.tiles_m * p.tiles_n * p.batch, p.kb, p.workers);
-        sched.put(s);
-    }
-    ptx::tc_fence_before_sync();
-    ptx::cta_sync();
-    ptx::tc_fence_after_sync();
-    const uint32_t tmem = *tmem_slot;
+    const uint32_t tmem = early ? 0u : *tmem_slot;
 
     const uint32_t ready_lead0 = PAIR ? ptx::mapa_shared(ready0, 0) : ready0;
     const uint32_t tempty_lead = PAIR ? ptx::mapa_shared(tempty, 0) : tempty;
@@ -378,7 +391,7 @@ __global__ void __launch_bounds__(kS8Threads, 1)
             uint32_t issued = 0;
             bool ok = true;
             for (PieceWalk<false> w(sched, worker); ok && w.advance(sched);) {
-                const S8Tile t = tile_at(w.tile, p, gtab, Cfg::TILE_M, Cfg::TILE_N);
+                const S8Tile t = tile_at(w.tile, p, gtab, grows, Cfg::TILE_M, Cfg::TILE_N);
                 const int32_t col = t.n0 + int32_t(rank) * 128;
                 for (int32_t kb = w.kb0; kb < w.kb1; ++kb) {
                     if (!s8_wait<PAIR>(empty0 + 8u * stage, phase ^ 1u, flag, p, kStatusProducer)) {
@@ -452,6 +465,10 @@ __global__ void __launch_bounds__(kS8Threads, 1)
             s8_wait<PAIR>(done_bar, 0, flag, p, kStatusDrain, false);
         }
         __syncwarp();
+        if constexpr (PAIR) {
+            if (early)
+                ptx::cluster_wait();
+        }
     } else if (warp < kWarpDrain) {
         // ---------------- converters
         ptx::regs_dec<kS8RegsConvert>();
@@ -572,7 +589,7 @@ __global__ void __launch_bounds__(kS8Threads, 1)
                 // later, and its columns' scales and biases and rows' scales on
                 // their way.  Two sets in turn, since the half's other warps
                 // may still be at the last tile's; they meet below.
-                const S8Tile t = tile_at(w.tile, p, gtab, Cfg::TILE_M, Cfg::TILE_N);
+                const S8Tile t = tile_at(w.tile, p, gtab, grows, Cfg::TILE_M, Cfg::TILE_N);
                 const int32_t i = 32 * q + lane, col = t.n0 + h * Cfg::HC + i;
                 const int32_t row = t.m0 + int32_t(PAIR ? ptx::cluster_ctarank() : 0u) * Cfg::ROWS + i;
                 const uint32_t at = terms0 + turn * Cfg::TERMS + uint32_t(h) * Cfg::GROUP_TERMS + 4u * i;
@@ -589,7 +606,7 @@ __global__ void __launch_bounds__(kS8Threads, 1)
             }
             // The four warps go on or give up together (they meet below).
             ptx::fetch_wait();
-            ok = __all_sync(0xffffffffu, ptx::named_bar_and(1 + h, 128, ok));
+            ok = __all_sync(0xffffffffu, ptx::named_bar_and(kBarGroup + h, 128, ok));
             if (!ok)
                 break;
             // (Read again rather than kept through the loop above, where
@@ -623,11 +640,11 @@ __global__ void __launch_bounds__(kS8Threads, 1)
                                make_int4(sum[j], sum[j + 1], sum[j + 2], sum[j + 3]));
                 }
                 __threadfence();
-                ptx::named_bar_sync(1 + h, 128);
+                ptx::named_bar_sync(kBarGroup + h, 128);
                 if (q == 0)
                     ptx::st_shared_u32(last_flag + 4u * h, arrive_last(p.arrivals + w.tile * Cfg::PARTS + part, p.tag,
                                                                       uint32_t(last - first + 1), lane));
-                ptx::named_bar_sync(1 + h, 128);
+                ptx::named_bar_sync(kBarGroup + h, 128);
                 const bool mine_to_sum = __any_sync(0xffffffffu, ptx::ld_shared_u32(last_flag + 4u * h) != 0);
                 __threadfence();
                 if (!mine_to_sum) {
