@@ -635,32 +635,44 @@ def quantize_rows(X, group_rows=None, q=None, scales=None, *, stream=None):
     rows that are read and written."""
     import torch
     code = _elem_type(X.dtype)
-    three = X.dim() == 3
-    if X.dim() not in (2, 3) or not X.is_cuda or (X.shape[-1] > 1 and X.numel() and X.stride(-1) != 1):
+    shape = X.shape
+    three = len(shape) == 3
+    if three:
+        batch, M, K = shape
+        sX, ldx, unit = X.stride()
+    elif len(shape) == 2:
+        batch, (M, K), sX = 1, shape, 0
+        ldx, unit = X.stride()
+    if len(shape) not in (2, 3) or not X.is_cuda or (unit != 1 and K > 1 and X.numel()):
         raise ValueError("X must be a 2-D or 3-D CUDA tensor with a unit last stride")
-    batch = X.shape[0] if three else 1
-    M, K = X.shape[-2:]
     if q is None:
-        pitch = -(-K // 16) * 16
-        q = torch.empty((*X.shape[:-1], pitch), dtype=torch.int8, device=X.device)
-        if pitch != K:
+        ldq = K + -K % 16
+        sQ = M * ldq if three else 0
+        q = torch.empty((batch, M, ldq) if three else (M, ldq), dtype=torch.int8, device=X.device)
+        if ldq != K:
             q = q[..., :K]
-    elif q.shape != X.shape or q.dtype != torch.int8 or (K > 1 and q.numel() and q.stride(-1) != 1):
-        raise ValueError("q must be an int8 tensor of X's shape with a unit last stride")
+    else:
+        if q.shape != shape or q.dtype != torch.int8 or (K > 1 and q.numel() and q.stride(-1) != 1):
+            raise ValueError("q must be an int8 tensor of X's shape with a unit last stride")
+        ldq = q.stride(-2)
+        sQ = q.stride(0) if three else 0
     if scales is None:
-        scales = torch.empty(X.shape[:-1], dtype=torch.float32, device=X.device)
-    elif scales.shape != X.shape[:-1] or scales.dtype != torch.float32 or (M > 1 and scales.stride(-1) != 1):
-        raise ValueError("scales must be a float32 tensor of one value per row")
+        sS = M if three else 0
+        scales = torch.empty((batch, M) if three else M, dtype=torch.float32, device=X.device)
+    else:
+        if scales.shape != shape[:-1] or scales.dtype != torch.float32 or (M > 1 and scales.stride(-1) != 1):
+            raise ValueError("scales must be a float32 tensor of one value per row")
+        sS = scales.stride(0) if three else 0
     counts = 0
     if group_rows is not None:
         if group_rows.dtype != torch.int32 or not group_rows.is_cuda or group_rows.numel() != batch \
                 or not group_rows.is_contiguous():
             raise ValueError("group_rows must be a contiguous CUDA int32 tensor of one count per matrix")
         counts = group_rows.data_ptr()
-    check(_lib.quantize_rows_s8(X.data_ptr(), code, q.data_ptr(), scales.data_ptr(), counts, M, K,
-                                X.stride(-2) if M > 1 else K, q.stride(-2) if M > 1 else K,
-                                X.stride(0) if three else 0, q.stride(0) if three else 0,
-                                scales.stride(0) if three else 0, batch, _stream_handle(stream)))
+    if M <= 1:
+        ldx = ldq = K
+    check(_lib.quantize_rows_s8(X.data_ptr(), code, q.data_ptr(), scales.data_ptr(), counts, M, K, ldx, ldq, sX, sQ,
+                                sS, batch, _stream_handle(stream)))
     return q, scales
 
 
@@ -669,9 +681,10 @@ def _s8_vector(t, n, batch, three, name):
     import torch
     if t is None:
         return 0, 0
-    dim = t.dim()
-    if t.dtype != torch.float32 or not t.is_cuda or t.shape[-1] != n or dim > (2 if three else 1) \
-            or (n > 1 and t.stride(-1) != 1) or (dim == 2 and t.shape[0] != batch):
+    shape = t.shape
+    dim = len(shape)
+    if t.dtype != torch.float32 or not t.is_cuda or dim < 1 or shape[-1] != n or dim > (2 if three else 1) \
+            or (n > 1 and t.stride(-1) != 1) or (dim == 2 and shape[0] != batch):
         raise ValueError(f"{name} must be a CUDA float32 tensor of {n} values" + (f" (or {batch} x {n})" if three else ""))
     return t.data_ptr(), t.stride(0) if dim == 2 and batch > 1 else 0
 
@@ -713,8 +726,11 @@ def _s8_call(A, B, scale_a, scale_b, group_rows, out, alpha, bias, activation, s
     pa, sa = _s8_vector(scale_a, M, batch, three, "scale_a")
     pb, sb = _s8_vector(scale_b, N, batch, three, "scale_b")
     pbias, sbias = _s8_vector(bias, N, batch, three, "bias")
-    epi = ctypes.byref(GemmEpilogue(alpha, pbias or None, sbias, ACTIVATIONS.get(activation, activation), slope,
-                                    _elem_type(out.dtype)))
+    code = _elem_type(out.dtype)
+    epi = None  # (none: alpha 1, no bias or activation, f32)
+    if code or pbias or alpha != 1 or activation != "none":
+        epi = ctypes.byref(GemmEpilogue(alpha, pbias or None, sbias, ACTIVATIONS.get(activation, activation), slope,
+                                        code))
     args = (M, N, K, lda if M > 1 else max(K, 1), ldb if K > 1 else max(N, 1), ldc if M > 1 else max(N, 1), sA, sB,
             sC, sa, sb)
     if group_rows is None:
