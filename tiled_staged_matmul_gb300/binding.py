@@ -464,7 +464,8 @@ def gemv(A, x, out=None, *, stream=None):
 
 # (The checks below are ordered so that contiguous CUDA tensors, the usual
 # case, pass with few attribute reads: a decode step's calls take the GPU two
-# or three microseconds each.)
+# or three microseconds each.  torch.empty between two launches costs half of
+# what Tensor.new_empty does.)
 
 _ELEM_TYPES = {}
 
@@ -566,12 +567,13 @@ def moe_dispatch_grad(drows, slots, out=None, *, stream=None):
     """The gradient of ``moe_dispatch``: ``dx[t] = sum_j drows[slots[t, j]]``
     for groups x capacity x width ``drows`` (f32, f16 or bf16); summed in f32,
     returned in the rows' type."""
+    import torch
     code = _elem_type(drows.dtype)
     T, k = _slots_of(slots)
     G, cap, H = drows.shape
     ld = _expert_pitch(drows, H, drows.dtype, "drows")
     if out is None:
-        out = drows.new_empty((T, H))
+        out = torch.empty((T, H), dtype=drows.dtype, device=drows.device)
         ldo = H
     else:
         ldo = _token_pitch(out, T, H, drows.dtype, "out")
@@ -585,13 +587,14 @@ def moe_combine(rows, slots, weights=None, out=None, *, stream=None):
     ``out[t] = sum_j weights[t, j] * rows[slots[t, j]]`` for groups x capacity
     x width ``rows`` (f32, f16 or bf16), f32 ``weights`` (tokens x topk; none:
     ones); summed in f32, returned in the rows' type."""
+    import torch
     code = _elem_type(rows.dtype)
     T, k = _slots_of(slots)
     G, cap, H = rows.shape
     ld = _expert_pitch(rows, H, rows.dtype, "rows")
     w = _weights_ptr(weights, slots)
     if out is None:
-        out = rows.new_empty((T, H))
+        out = torch.empty((T, H), dtype=rows.dtype, device=rows.device)
         ldo = H
     else:
         ldo = _token_pitch(out, T, H, rows.dtype, "out")

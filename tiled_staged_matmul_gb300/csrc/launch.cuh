@@ -6,8 +6,10 @@
 // complete and visible.  Every block of such a kernel passes chain_wait before
 // it touches anything that another kernel reads or writes, on every path: what
 // follows in the stream relies on this kernel's end coming after the end of
-// what it waited for.  chain_next lets the next kernel's blocks come as soon
-// as this one's leave room.  Back to back, short kernels start 2 us earlier so.
+// what it waited for.  What it reads may still be written while it starts, so
+// that is read by ordinary loads, none of the read-only path's.  chain_next lets
+// the next kernel's blocks come as soon as this one's leave room.  Back to back,
+// short kernels start 2 us earlier so.
 #pragma once
 
 #include <cuda_runtime.h>

@@ -400,7 +400,9 @@ S8Capacity g_s8_capacity[64];
 // that is less; its pairs of warps (8, or 4 for two blocks of rows) take whole
 // blocks; adding up their sums takes 1 us.  The launch waits for the cluster
 // with the most tiles.  Finishing a tile takes 2 us, 3 where its sums pass
-// between CTAs; it hides behind the next tile if that takes longer.
+// between CTAs; it hides behind the next tile if that takes longer.  (Within 6 %
+// of the best of the eight on nine shapes, 1 x 4096 x 4096 to 16 x 57344 x 8192;
+// the worst of them took up to four times as long.)
 int few_rows_ranks(int64_t tiles, int32_t kb, const S8Capacity &cap, bool two, int *clusters)
 {
     const double block = 8192.0;                   // bytes of 32 k x 256 columns

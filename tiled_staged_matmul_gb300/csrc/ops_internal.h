@@ -75,9 +75,10 @@ struct S8Schedule {
     int32_t workers;        // of the whole tiles
     int32_t cutters;        // workers that get a piece
     static constexpr int32_t kMaxTiles = 1 << 30;
-    // What a cut costs, in blocks' time: 12 to 19 measured (1024 x 14336 x 4096, 2.95
-    // waves: 98 us cut, 86 whole; 512 x 14336 x 4096, 1.47 waves: 61 and 60;
-    // 64 x 14336 x 4096, 0.74: 31 and 29).
+    // What a cut costs, in blocks' time.  Whole against cut, us: 300 x 5000 x 8192
+    // 74.6 and 65.6, 128 x 4096 x 4096 26.6 and 19.8, 4096^3 106.1 and 104.3; 512 x
+    // 14336 x 4096 56.9 and 58.7, 64 x 14336 x 4096 27.0 and 29.4.  16 decides all
+    // of these right (6 and 24 do not).
     static constexpr int32_t kCutBlocks = 16;
 
     __host__ __device__ void plan(int32_t tiles_, int32_t kb_, int32_t workers_)

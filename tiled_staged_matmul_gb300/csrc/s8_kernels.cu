@@ -15,7 +15,10 @@ namespace {
 // independent warps in pairs take 32 k of the tile at a time, one warp for each
 // 128 columns, so that a row of B is read 256 bytes at a time (reading 128
 // bytes of it ran at 4.6 TB/s, 256 at 6.0, 512 no faster).  Each warp has a TMA
-// ring of its own and never waits for another.
+// ring of its own and never waits for another.  Measured: 16 x 57344 x 8192
+// 80.5 us, 5.9 TB/s (0.88 of the copy rate); 16 x 14336 x 4096 18.4 us and 1 x
+// 4096 x 4096 9.3, where a kernel that does nothing but read B takes 13.0 and
+// 6.4.
 //
 // Warp-wide f16 MMAs (16 x 8 x 16 k) run far below the tcgen05 rate, but so few
 // rows need no more: one SM's share of the memory rate is 23 codes a cycle, 23
@@ -133,16 +136,16 @@ __device__ __forceinline__ S8Tile few_rows_terms(const S8Params &p, const FewPla
         const int32_t col = t.n0 + c;
         float sb = p.epi.alpha, bias = 0.f;
         if (p.scale_b && col < p.N)
-            sb *= __ldg(p.scale_b + t.z * p.sb_stride + col);
+            sb *= p.scale_b[t.z * p.sb_stride + col];
         if (p.epi.bias && col < p.N)
-            bias = __ldg(p.epi.bias + t.z * p.epi.bias_stride + col);
+            bias = p.epi.bias[t.z * p.epi.bias_stride + col];
         ptx::st_shared_u32(f.terms0 + 4u * c, __float_as_uint(sb));
         ptx::st_shared_u32(f.terms0 + 4u * (Cfg::COLS + c), __float_as_uint(bias));
     }
     if (ft < Cfg::ROWS)
         ptx::st_shared_u32(f.terms0 + 4u * (2 * Cfg::COLS + ft),
                            __float_as_uint(p.scale_a && ft < t.rows
-                                               ? __ldg(p.scale_a + t.z * p.sa_stride + t.m0 + ft) : 1.f));
+                                               ? p.scale_a[t.z * p.sa_stride + t.m0 + ft] : 1.f));
     return t;
 }
 
@@ -295,7 +298,7 @@ __device__ __forceinline__ bool few_rows_multiply(const CUtensorMap &map_a, cons
 #pragma unroll 1
     for (uint32_t s = 0; s < S; ++s)
         issue(s);
-    few_rows_start<MT>(f);  // (while those are on their way: 1 us)
+    few_rows_start<MT>(f);  // (while those are on their way)
 
     uint32_t stage = 0, phase = 0, set = 0, set_phase = 0;
     bool ok = true;
@@ -499,7 +502,7 @@ __global__ void __launch_bounds__(S8FewCfg<MT>::THREADS, 1)
         ptx::regs_inc<Cfg::LAUNCH_REGS>();
     }
     // The CTA's last tile has nothing to hide behind, and every warp takes part
-    // in finishing it (four warps alone took 2 us for 16 rows, these 0.6).
+    // in finishing it (four warps alone took 2.1 us for 16 rows, these 1.0).
     __syncwarp();
     ok = __syncthreads_and(ok);
     if (p.ranks > 1)
@@ -538,22 +541,22 @@ __global__ void __launch_bounds__(256)
             if (off == 0) {
 #pragma unroll
                 for (int k = 0; k < 4; ++k)
-                    w[k] = __ldg(reinterpret_cast<const uint32_t *>(s) + k);
+                    w[k] = reinterpret_cast<const uint32_t *>(s)[k];
             } else {
                 const uint32_t *a = reinterpret_cast<const uint32_t *>(s - off) + 1;
                 uint32_t prev = 0;
                 for (int b = off; b < 4; ++b)
-                    prev |= uint32_t(__ldg(s - off + b)) << (8 * b);
+                    prev |= uint32_t(s[b - off]) << (8 * b);
 #pragma unroll
                 for (int k = 0; k < 4; ++k) {
-                    const uint32_t next = __ldg(a + k);
+                    const uint32_t next = a[k];
                     w[k] = __funnelshift_r(prev, next, 8 * off);
                     prev = next;
                 }
             }
         } else {
             for (int k = 0; k < 16 && c + k < cols; ++k)
-                w[k >> 2] |= uint32_t(__ldg(s + k)) << (8 * (k & 3));
+                w[k >> 2] |= uint32_t(s[k]) << (8 * (k & 3));
         }
         *reinterpret_cast<uint4 *>(dst + z * d_stride + r * d_ld + c) = make_uint4(w[0], w[1], w[2], w[3]);
     }

@@ -23,8 +23,14 @@ constexpr int kChunkBlocks = 8;  // k-blocks of 128 whose sums the f32 accumulat
 //   warps 4-7    A's codes -> f16 -> TMEM, one row per lane (they never pass
 //                through shared memory as f16)
 //   warps 8-11   B's codes -> f16 -> the 128-byte swizzled layout of the MMA
-//   warps 12-19  two per TMEM lane quarter, one per column half of the tile:
-//                accumulator -> 32-bit sums, then the epilogue
+//   warps 12-27  four per TMEM lane quarter, one per quarter of the tile's
+//                columns: accumulator -> 32-bit sums, then the epilogue (with
+//                two per lane quarter, half the columns each, a chunk took 1.05
+//                us to add up and 8192^3 665 us, not 647)
+// Measured: 8192^3 647 us (1.70 PFLOP/s, 0.89 of the f16 rate measured with
+// cuBLAS), 4096 x 14336 x 4096 304 us (0.83), 97 x 14333 x 4095 with one CTA a
+// tile 28 us.
+//
 // The bound is shared-memory bandwidth: a 256 x 256 x 128 block costs an SM
 // 32 KB of codes in, 32 KB out to the converters, 32 KB of f16 B written and
 // 32 KB read by the MMAs = 1024 cycles at 128 bytes, just the time its MMAs
@@ -32,7 +38,7 @@ constexpr int kChunkBlocks = 8;  // k-blocks of 128 whose sums the f32 accumulat
 // ring takes the TMEM columns a second accumulator would need, so the MMAs
 // pause while a chunk of 1024 k is read out.  (Two accumulators of half the
 // width would not: but the MMA runs at full rate only at its full width, 256
-// columns for a pair.)
+// columns for a pair.  One CTA's 128 x 128 tiles run at half of it.)
 constexpr int kWarpA = 4, kWarpB = 8, kWarpDrain = 12;  // first warps of the roles
 constexpr int kDrainWarps = 16, kS8Warps = kWarpDrain + kDrainWarps;
 constexpr int kS8Threads = 32 * kS8Warps;
@@ -192,9 +198,9 @@ __device__ __forceinline__ uint32_t out16_pair(float a, float b, int32_t out_typ
 // The epilogue of a box: 32 rows (a lane each) of 32 columns' sums.  Scaled,
 // biased and activated in registers, where a lane's columns are independent
 // work (done a row at a time after the exchange, where one value waited for
-// another, 4096 x 14336 x 4096 took 358 us, not 321), then through the warp's
-// staging space (64 bytes a row, 16-byte chunks swizzled by the row) so that
-// the stores cover whole row segments.
+// another, 4096 x 14336 x 4096 took 1.12 times as long), then through the
+// warp's staging space (32 bytes a row, 16-byte chunks swizzled by the row) so
+// that the stores cover whole sectors.
 __device__ __forceinline__ void finish_box(const S8Params &p, const S8Tile &t, const int32_t (&s32)[32], bool small, float sa,
                                            uint32_t sb_at, uint32_t bias_at, uint32_t buf, int32_t row0, int32_t col0,
                                            int lane)
@@ -316,10 +322,10 @@ __global__ void __launch_bounds__(kS8Threads, 1)
     const uint32_t flag = ctrl + 180u;         // this CTA gives up
     const SharedSchedule<false> sched{ctrl + 256u};
     const SharedSchedule<true> wsched{ctrl + 256u};
-    const uint32_t last_flag = ctrl + 184u;    // [2] one per column half
+    const uint32_t last_flag = ctrl + 184u;    // [4] one per epilogue group
     const uint32_t gtab = ctrl + Cfg::GROUP_TABLE_OFF, grows = ctrl + Cfg::GROUP_ROWS_OFF;
-    const uint32_t tiles0 = ctrl + 512u;  // [8] an epilogue warp's tile
-    const uint32_t terms0 = ctrl + Cfg::TERMS_OFF;  // [2][columns' scales, biases, rows' scales][256]
+    const uint32_t tiles0 = ctrl + 512u;  // [16] an epilogue warp's tile
+    const uint32_t terms0 = ctrl + Cfg::TERMS_OFF;  // [2][group][columns' scales, biases; rows' scales]
 
     const int warp = __shfl_sync(0xffffffffu, int(threadIdx.x >> 5), 0);  // (uniform to the compiler)
     const int lane = int(threadIdx.x & 31);
@@ -587,7 +593,7 @@ __global__ void __launch_bounds__(kS8Threads, 1)
                 // With the first chunk out of the way (it was complete long
                 // before the last tile's epilogue was): where the tile is, for
                 // later, and its columns' scales and biases and rows' scales on
-                // their way.  Two sets in turn, since the half's other warps
+                // their way.  Two sets in turn, since the group's other warps
                 // may still be at the last tile's; they meet below.
                 const S8Tile t = tile_at(w.tile, p, gtab, grows, Cfg::TILE_M, Cfg::TILE_N);
                 const int32_t i = 32 * q + lane, col = t.n0 + h * Cfg::HC + i;
