@@ -268,10 +268,10 @@ __global__ void __launch_bounds__(256) tsm_moe_dispatch_kernel(MoveParams p)
 
 // A warp sums U x 32 pieces of a token's row over its choices, K rows at a
 // time: U x K loads of a lane in flight.  Many tokens: U = 2, K = 2 (8192
-// tokens, 2 choices, 4096 bf16: 36 us, 0.83 of the copy rate; U = 4 41 us, with
-// fewer warps on an SM; K = 4 59 us, half its loads without a row); few tokens (a
-// decode step): U = 1, K = 8, every warp there is at work and a token's rows
-// loaded in one go.
+// tokens, 2 choices, 4096 bf16: 33 us, 0.92 of the copy rate; U = 3 39 us, with
+// fewer warps on an SM; K = 4 47 us, half its loads without a row.  4096 tokens, 6
+// choices, 2048 bf16: 21, 22 and 25); few tokens (a decode step): U = 1, K = 8,
+// every warp there is at work and a token's rows loaded in one go.
 template <int ET, int BYTES, int U, int K>
 __global__ void __launch_bounds__(256) tsm_moe_combine_kernel(MoveParams p)
 {
