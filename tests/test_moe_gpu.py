@@ -317,3 +317,36 @@ def test_refusals(b):
     # an allocation that ends before the last row
     assert b.moe_dispatch_rows(x.data_ptr(), 4, slots.data_ptr(), rows.data_ptr(), 4, 2, 1 << 28, 16, 16, 16) \
         == b.GEMM_ERR_INVALID_VALUE
+
+
+@pytest.mark.parametrize("topk", [31, 32, 33, 70])
+def test_more_choices_than_a_warp_has_lanes(b, topk):
+    groups, capacity, width = 80, 4, 40
+    g = torch.Generator().manual_seed(topk)
+    ids = torch.stack([torch.randperm(groups, generator=g)[:topk] for _ in range(6)]).int()
+    x = torch.randn((6, width), generator=g)
+    w = torch.rand((6, topk), generator=g)
+    slots, counts = b.moe_route(ids.cuda(), groups, capacity)
+    want, kept = route_reference(ids.numpy(), groups, capacity)
+    assert np.array_equal(slots.cpu().numpy(), want) and np.array_equal(counts.cpu().numpy(), kept)
+    rows = b.moe_dispatch(x.cuda(), slots, groups, capacity)
+    plain = torch.zeros((groups * capacity, width))
+    for t in range(6):
+        for j in range(topk):
+            if want[t, j] >= 0:
+                plain[want[t, j]] = x[t]
+    assert torch.equal(rows.cpu().view(-1, width), plain)
+    out = b.moe_combine(rows, slots, w.cuda()).cpu().double()
+    keep = torch.from_numpy(want >= 0).double() * w.double()
+    total = keep.sum(1, keepdim=True) * x.double()
+    assert ((out - total).abs() <= (topk + 2) * 2.0 ** -24 * total.abs()).all()
+
+
+def test_a_dropped_choice_adds_nothing_whatever_its_weight(b):
+    slots = torch.tensor([[0, -1], [-1, -1], [1, 5]], dtype=torch.int32, device="cuda")  # (4 rows)
+    rows = torch.randn((1, 4, 24), generator=torch.Generator().manual_seed(3)).cuda()
+    nan, inf = float("nan"), float("inf")
+    w = torch.tensor([[2.0, nan], [inf, nan], [0.5, -inf]], device="cuda")
+    out = b.moe_combine(rows, slots, w)
+    assert torch.equal(out[0], 2 * rows[0, 0]) and torch.equal(out[2], 0.5 * rows[0, 1])
+    assert (out[1] == 0).all()

@@ -325,3 +325,33 @@ def test_refusals(b):
     assert b.gemm_s8_scaled(A.data_ptr(), B.data_ptr(), A.data_ptr(), 0, 0, 4, 8, 32, 32, 8, 8) == b.GEMM_ERR_ALIAS
     with pytest.raises(TypeError):
         b.quantize_rows(A)
+
+
+@pytest.mark.parametrize("groups,M,N,K", [(33, 32, 200, 70), (17, 16, 300, 1030), (300, 9, 40, 33), (70, 300, 130, 130)])
+def test_every_count_of_rows(b, groups, M, N, K):
+    """Counts 0, 1, 2 ... M in turn, in more groups than one launch takes, too."""
+    rows = [(i * (1 if M < groups else 7)) % (M + 1) for i in range(groups)]
+    A, B = codes((groups, M, K), groups), codes((groups, K, N), groups + 1)
+    C = torch.full((groups, M, N), PRIOR, device="cuda")
+    b.grouped_gemm_s8(A.cuda(), B.cuda(), None, None, torch.tensor(rows, dtype=torch.int32, device="cuda"), C)
+    b.check(b.gemm_get_device_status(0))
+    got = C.cpu().numpy()
+    for g, r in enumerate(rows):
+        assert np.array_equal(got[g, :r], sums(A[g, :r], B[g]).astype(np.float32)), g
+        assert (got[g, r:] == PRIOR).all(), g
+
+
+@pytest.mark.parametrize("M", [5, 20, 100, 300])
+def test_small_and_large_sums_together(b, M):
+    """Sums on both sides of 2^22 and 2^24, where the ways to f32 differ."""
+    K, N = 3000, 70
+    A, B = codes((M, K), M), codes((K, N), M + 1)
+    for i, edge in enumerate((255, 256, 257, 1023, 1024, 1025)):
+        if 2 * i + 1 < M:
+            A[2 * i + 1] = 0
+            A[2 * i + 1, :edge] = -128
+        B[:, 2 * i] = -128
+        B[:, 2 * i + 1] = 127
+    C = b.gemm_s8(A.cuda(), B.cuda())
+    b.check(b.gemm_get_device_status(0))
+    assert np.array_equal(C.cpu().numpy(), sums(A, B).astype(np.float32))
