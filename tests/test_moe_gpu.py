@@ -350,3 +350,16 @@ def test_a_dropped_choice_adds_nothing_whatever_its_weight(b):
     out = b.moe_combine(rows, slots, w)
     assert torch.equal(out[0], 2 * rows[0, 0]) and torch.equal(out[2], 0.5 * rows[0, 1])
     assert (out[1] == 0).all()
+
+
+@pytest.mark.parametrize("n", [1023, 1024, 1025, 8191, 8192, 8193, 16384, 16385, 24576, 32768, 32769, 40001])
+@pytest.mark.parametrize("groups,wide", [(1, False), (8, True), (1000, False)])
+def test_route_over_chunks(b, n, groups, wide):
+    """Numbers of choices around those where the work is cut differently."""
+    g = torch.Generator().manual_seed(n + groups)
+    ids = torch.randint(-1, groups + 1, (n, 1), generator=g, dtype=torch.int64 if wide else torch.int32)
+    capacity = n // groups + 3
+    slots, counts = b.moe_route(ids.cuda(), groups, capacity)
+    want, kept = route_reference(ids.numpy(), groups, capacity)
+    assert np.array_equal(slots.cpu().numpy(), want)
+    assert np.array_equal(counts.cpu().numpy(), kept)

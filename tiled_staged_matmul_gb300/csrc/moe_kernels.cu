@@ -18,9 +18,12 @@
 // floating-point data, so a call is bitwise reproducible.
 #include "launch.cuh"
 #include "ops_internal.h"
+#include "s8_ptx.cuh"
 
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
+
+#include <type_traits>
 
 namespace tsm {
 
@@ -64,13 +67,17 @@ __global__ void __launch_bounds__(32 * kRouteWarps) tsm_moe_count_kernel(RoutePa
 // Ranks of one chunk.  Warp w holds ROUNDS x 32 consecutive assignments; a
 // lane's rank is what the warp counted in earlier rounds, plus the lower lanes
 // of the same expert (a warp match), plus the earlier warps' counts, plus the
-// earlier chunks' (summed here from the count kernel's table).
-template <bool WIDE, int ROUNDS>
+// earlier chunks'.  Those come from the count kernel's table or, where one
+// cluster holds all chunks (CLUSTER), from the other CTAs' shared memory, with
+// one launch and no table: 16384 choices of 8 experts 4.3 us, not 6.0; 32768 of
+// 64 7.9 and 8.0; a decode step's 32, one chunk, 2.3.
+template <bool WIDE, int ROUNDS, bool CLUSTER>
 __global__ void __launch_bounds__(32 * kRouteWarps) tsm_moe_rank_kernel(RouteParams p)
 {
     extern __shared__ uint32_t smem[];
     uint32_t *const base = smem;                                        // [groups]
-    uint16_t *const seen = reinterpret_cast<uint16_t *>(smem + p.groups);  // [warps][groups]
+    uint32_t *const total = smem + p.groups;                            // [groups], of this chunk (CLUSTER)
+    uint16_t *const seen = reinterpret_cast<uint16_t *>(smem + (CLUSTER ? 2 : 1) * p.groups);  // [warps][groups]
     const int warp = int(threadIdx.x >> 5), lane = int(threadIdx.x & 31);
     const int G = p.groups;
     chain_next();
@@ -83,7 +90,7 @@ __global__ void __launch_bounds__(32 * kRouteWarps) tsm_moe_rank_kernel(RoutePar
     for (int i = lane; i < G; i += 32)
         seen[warp * G + i] = 0;
     // The earlier chunks' counts, while the ids are on their way.
-    for (int e = int(threadIdx.x); e < G; e += int(blockDim.x)) {
+    for (int e = int(threadIdx.x); !CLUSTER && e < G; e += int(blockDim.x)) {
         uint32_t before = 0;
         for (int64_t c = 0; c < int64_t(blockIdx.x); ++c)
             before += uint32_t(p.hist[c * G + e]);
@@ -105,7 +112,7 @@ __global__ void __launch_bounds__(32 * kRouteWarps) tsm_moe_rank_kernel(RoutePar
         at[r] = earlier + lower;
     }
     __syncthreads();
-    // Exclusive sums over the warps, in place; the chunk's total on top of base.
+    // Exclusive sums over the warps, in place; the chunk's total.
     const bool last = blockIdx.x == gridDim.x - 1;
     for (int e = int(threadIdx.x); e < G; e += int(blockDim.x)) {
         uint32_t sum = 0;
@@ -114,8 +121,26 @@ __global__ void __launch_bounds__(32 * kRouteWarps) tsm_moe_rank_kernel(RoutePar
             seen[w * G + e] = uint16_t(sum);
             sum += c;
         }
-        if (last)
+        if (CLUSTER)
+            total[e] = sum;
+        else if (last)
             p.counts[e] = int32_t(min(base[e] + sum, uint32_t(p.capacity)));
+    }
+    if (CLUSTER) {
+        ptx::cluster_sync();
+        for (int e = int(threadIdx.x); e < G; e += int(blockDim.x)) {
+            uint32_t x[kRouteCluster - 1], before = 0;
+#pragma unroll
+            for (uint32_t c = 0; c < kRouteCluster - 1; ++c)
+                x[c] = c < blockIdx.x ? ptx::ld_cluster_u32(ptx::mapa_shared(ptx::smem_addr(total + e), c)) : 0u;
+#pragma unroll
+            for (uint32_t c = 0; c < kRouteCluster - 1; ++c)
+                before += x[c];
+            base[e] = before;
+            if (last)
+                p.counts[e] = int32_t(min(before + total[e], uint32_t(p.capacity)));
+        }
+        ptx::cluster_arrive_relaxed();
     }
     __syncthreads();
 #pragma unroll
@@ -131,6 +156,8 @@ __global__ void __launch_bounds__(32 * kRouteWarps) tsm_moe_rank_kernel(RoutePar
             p.slots[i] = slot;
         }
     }
+    if (CLUSTER)
+        ptx::cluster_wait();  // no CTA leaves while another may still read its totals
 }
 
 // ------------------------------------------------------------- row types
@@ -524,6 +551,13 @@ __global__ void __launch_bounds__(TPR < 256 && TPR > 32 ? TPR : 256) tsm_quantiz
 }
 
 template <bool WIDE, int ROUNDS>
+cudaError_t route_in_cluster(const RouteParams &p, int64_t chunks, cudaStream_t stream)
+{
+    return launch_chained(tsm_moe_rank_kernel<WIDE, ROUNDS, true>, dim3(unsigned(chunks)), 32 * kRouteWarps,
+                          size_t(p.groups) * (8 + 2 * kRouteWarps), unsigned(chunks), stream, p);
+}
+
+template <bool WIDE, int ROUNDS>
 cudaError_t route_as(const RouteParams &p, int64_t chunks, cudaStream_t stream)
 {
     constexpr int threads = 32 * kRouteWarps;
@@ -532,7 +566,7 @@ cudaError_t route_as(const RouteParams &p, int64_t chunks, cudaStream_t stream)
         e = launch_chained(tsm_moe_count_kernel<WIDE, ROUNDS>, dim3(unsigned(chunks)), threads, size_t(p.groups) * 4, 0,
                            stream, p);
     if (e == cudaSuccess)
-        e = launch_chained(tsm_moe_rank_kernel<WIDE, ROUNDS>, dim3(unsigned(chunks)), threads,
+        e = launch_chained(tsm_moe_rank_kernel<WIDE, ROUNDS, false>, dim3(unsigned(chunks)), threads,
                            size_t(p.groups) * (4 + 2 * kRouteWarps), 0, stream, p);
     return e;
 }
@@ -549,11 +583,18 @@ cudaError_t dispatch_as(const MoveParams &p, int sms, cudaStream_t stream)
 
 cudaError_t launch_route(const RouteParams &p, bool wide_ids, int rounds, int64_t chunks, cudaStream_t stream)
 {
-    if (rounds == kRouteRoundsSmall)
-        return wide_ids ? route_as<true, kRouteRoundsSmall>(p, chunks, stream)
-                        : route_as<false, kRouteRoundsSmall>(p, chunks, stream);
-    return wide_ids ? route_as<true, kRouteRoundsLarge>(p, chunks, stream)
-                    : route_as<false, kRouteRoundsLarge>(p, chunks, stream);
+    const auto run = [&](auto wide) {
+        constexpr bool W = decltype(wide)::value;
+        if (chunks > 1 && !p.hist)
+            switch (rounds) {
+            case kRouteRoundsSmall: return route_in_cluster<W, kRouteRoundsSmall>(p, chunks, stream);
+            case 2 * kRouteRoundsSmall: return route_in_cluster<W, 2 * kRouteRoundsSmall>(p, chunks, stream);
+            default: return route_in_cluster<W, kRouteRoundsCluster>(p, chunks, stream);
+            }
+        return rounds == kRouteRoundsSmall ? route_as<W, kRouteRoundsSmall>(p, chunks, stream)
+                                           : route_as<W, kRouteRoundsLarge>(p, chunks, stream);
+    };
+    return wide_ids ? run(std::true_type{}) : run(std::false_type{});
 }
 
 cudaError_t launch_dispatch(const MoveParams &p, int vec, int sms, cudaStream_t stream)

@@ -129,11 +129,14 @@ gemm_status_t moe_route_slots(const void *expert_ids, int32_t id_bytes, int32_t 
     if ((st = current(&dev, &ds)) != GEMM_OK || (st = check_on_device(buf, 3, dev)) != GEMM_OK)
         return st;
     cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
-    // Small chunks until they would be many: each rank block adds up the
-    // counts of the chunks before its own.
+    // One cluster while it holds the chunks.  Else small chunks until they would
+    // be many: each rank block adds up the counts of the chunks before its own.
     int rounds = kRouteRoundsSmall;
-    if (n > route_chunk(kRouteRoundsSmall) * ds->sms)
-        rounds = kRouteRoundsLarge;
+    while (rounds < kRouteRoundsCluster && n > route_chunk(rounds) * kRouteCluster)
+        rounds *= 2;
+    const bool cluster = n <= route_chunk(rounds) * kRouteCluster;
+    if (!cluster)
+        rounds = n > route_chunk(kRouteRoundsSmall) * ds->sms ? kRouteRoundsLarge : kRouteRoundsSmall;
     const int64_t chunks = std::max<int64_t>(1, (n + route_chunk(rounds) - 1) / route_chunk(rounds));
     RouteParams p = {};
     p.ids = expert_ids;
@@ -144,7 +147,7 @@ gemm_status_t moe_route_slots(const void *expert_ids, int32_t id_bytes, int32_t 
     p.capacity = int32_t(capacity);
     void *ws = nullptr;
     cudaError_t e;
-    if (chunks > 1) {
+    if (!cluster) {
         if ((e = cudaMallocFromPoolAsync(&ws, size_t(chunks * std::max<int64_t>(groups, 1) * 4), ds->pool, s)) !=
             cudaSuccess)
             return fail_cuda(e, "routing workspace");

@@ -15,14 +15,15 @@ struct RouteParams {
     const void *ids;      // n expert numbers, int32 or int64
     int32_t *slots;       // n
     int32_t *counts;      // groups
-    int32_t *hist;        // chunks x groups counts per chunk (more than one chunk), else null
+    int32_t *hist;        // chunks x groups counts per chunk; null: one chunk, or one cluster of them
     int64_t n;            // tokens x choices
     int32_t groups;
     int32_t capacity;
 };
 // One CTA ranks kRouteChunk(rounds) assignments.
 constexpr int kRouteWarps = 16;
-constexpr int kRouteRoundsSmall = 2, kRouteRoundsLarge = 16;
+constexpr int kRouteRoundsSmall = 2, kRouteRoundsCluster = 8, kRouteRoundsLarge = 16;
+constexpr int kRouteCluster = 8;  // chunks that one cluster holds
 __host__ __device__ constexpr int64_t route_chunk(int rounds) { return int64_t(kRouteWarps) * 32 * rounds; }
 cudaError_t launch_route(const RouteParams &p, bool wide_ids, int rounds, int64_t chunks, cudaStream_t stream);
 

@@ -58,7 +58,8 @@ struct S8Cfg {
     static constexpr int STAGING = 4 * GROUPS * 32 * 32;  // per epilogue warp: 32 rows of 32 bytes
     static constexpr uint32_t GROUP_TERMS = (2 * HC + ROWS) * 4;  // a group's columns' scales and biases, rows' scales
     static constexpr uint32_t TERMS = GROUPS * GROUP_TERMS;
-    static constexpr int CTRL = 3072 + 2 * TERMS, GROUP_TABLE_OFF = 1024, GROUP_ROWS_OFF = 2048, TERMS_OFF = 3072;
+    static constexpr int GROUP_TABLE_OFF = 1024, GROUP_ROWS_OFF = 2048, TERMS_OFF = GROUP_ROWS_OFF + 1024;
+    static constexpr int CTRL = TERMS_OFF + 2 * TERMS;
     static constexpr int SMEM_BYTES = 1024 + S1 * CODE_STAGE + S2 * F_STAGE + STAGING + CTRL;
     static_assert(SMEM_BYTES <= 232448, "227 KiB per block");
     static constexpr uint32_t A_COL = 256;      // TMEM: the accumulator, then the f16 A ring

@@ -1,6 +1,7 @@
 // s8_ptx.cuh -- inline-PTX wrappers that only the 8-bit products use: TMEM
 // stores, the MMA with A in TMEM, register reallocation between warpgroups,
-// and the warp-wide f16 MMA of the few-rows kernel.
+// and the warp-wide f16 MMA of the few-rows kernel; and reads of another CTA's
+// shared memory, which the routing needs too.
 #pragma once
 
 #include "ptx.cuh"
@@ -140,6 +141,14 @@ __device__ __forceinline__ bool named_bar_and(uint32_t id, uint32_t count, bool 
         : "r"(id), "r"(count), "r"(uint32_t(v))
         : "memory");
     return all != 0;
+}
+
+// 4 bytes of another CTA's shared memory.
+__device__ __forceinline__ uint32_t ld_cluster_u32(uint32_t cluster_addr)
+{
+    uint32_t v;
+    asm volatile("ld.shared::cluster.u32 %0, [%1];" : "=r"(v) : "r"(cluster_addr) : "memory");
+    return v;
 }
 
 // 16 bytes of shared memory of any CTA of the cluster.
