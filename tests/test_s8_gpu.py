@@ -355,3 +355,65 @@ def test_small_and_large_sums_together(b, M):
     C = b.gemm_s8(A.cuda(), B.cuda())
     b.check(b.gemm_get_device_status(0))
     assert np.array_equal(C.cpu().numpy(), sums(A, B).astype(np.float32))
+
+
+# Sizes that pairs of CTAs multiply (the smaller ones above go to single CTAs).
+@pytest.mark.parametrize("M,N,K", [(1500, 2100, 1200), (1537, 2049, 1025), (900, 3000, 2000), (4000, 4100, 130)])
+def test_large_sums_are_exact(b, M, N, K):
+    A, B = codes((M, K), M + K), codes((K, N), N + K)
+    want = sums(A, B).astype(np.float32)
+    for pitch in (16, 1):
+        dA, _ = padded(A, up(K, 16))
+        dB, _ = padded(B, up(N, 16))
+        C, buf = padded(torch.full((M, N), PRIOR), up(N, pitch) + (pitch == 16) * 16, 4, fill=PRIOR)
+        b.gemm_s8(dA, dB, out=C)
+        b.check(b.gemm_get_device_status(0))
+        assert np.array_equal(C.cpu().numpy(), want)
+        C.fill_(PRIOR)
+        assert (buf == PRIOR).all()
+
+
+@pytest.mark.parametrize("act", ["none", "relu", "leaky_relu", "gelu", "gelu_tanh", "silu"])
+@pytest.mark.parametrize("out_type", ["f32", "f16", "bf16"])
+def test_large_with_scales_bias_and_activation(b, out_type, act):
+    M, N, K = 1300, 2500, 700
+    g = torch.Generator().manual_seed(5)
+    A, B = codes((M, K), 1), codes((K, N), 2)
+    sa = torch.rand((M,), generator=g) * 0.03 + 1e-3
+    sb = (torch.rand((N,), generator=g) - 0.3) * 0.02
+    bias = torch.randn((N,), generator=g)
+    want, tol = value_reference(sums(A, B), sa.double().numpy(), sb.double().numpy(), 0.75, bias.double().numpy(), act)
+    for pitch in (16, 1):
+        C, _ = padded(torch.full((M, N), PRIOR, dtype=TORCH[out_type]), up(N + pitch, pitch), fill=PRIOR)
+        b.gemm_s8(A.cuda(), B.cuda(), sa.cuda(), sb.cuda(), C, alpha=0.75, bias=bias.cuda(), activation=act)
+        b.check(b.gemm_get_device_status(0))
+        check_values(C.double().cpu().numpy(), want, tol, out_type)
+
+
+def test_large_groups(b):
+    groups, M, N, K = 40, 300, 1024, 520
+    rows = [0, 300, 1, 255, 256, 257, 128, 129, 299, 64] * 4
+    A, B = codes((groups, M, K), 3), codes((groups, K, N), 4)
+    C = torch.full((groups, M, N), PRIOR, device="cuda")
+    b.grouped_gemm_s8(A.cuda(), B.cuda(), None, None, torch.tensor(rows, dtype=torch.int32, device="cuda"), C)
+    b.check(b.gemm_get_device_status(0))
+    got = C.cpu().numpy()
+    for g, r in enumerate(rows):
+        assert np.array_equal(got[g, :r], sums(A[g, :r], B[g]).astype(np.float32)), g
+        assert (got[g, r:] == PRIOR).all(), g
+
+
+def test_capture_of_a_pair_that_cuts_its_tiles(b):
+    M, N, K = 300, 5008, 8192
+    A, B = codes((M, K), 8).cuda(), codes((K, N), 9).cuda()
+    C = torch.zeros((M, N), device="cuda")
+    want = b.gemm_s8(A, B).clone()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        b.gemm_s8(A, B, out=C)
+    for _ in range(3):
+        C.zero_()
+        graph.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(C, want)
+    b.check(b.gemm_get_device_status(0))

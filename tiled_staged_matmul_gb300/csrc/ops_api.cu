@@ -433,6 +433,36 @@ int few_rows_ranks(int64_t tiles, int32_t kb, const S8Capacity &cap, bool two, i
     return best;
 }
 
+// The tiled kernel: a CTA per 128 x 128 tile, or a pair per 256 x 256, which does
+// twice the work at one SM's time for a block and a pair's longer start.  By the
+// time of the busiest worker: 5 us and 0.66 a block of 128 k, or 6.5 and 0.75
+// (the nearer of two on 20 shapes from 140 x 1072 x 272 to 512 x 14336 x 4096, us
+// as single CTAs and pairs: 140 x 1072 x 272 8.1 and 10.4, 512 x 4096 x 4096 26.8
+// and 33.8, 256 x 256 x 65536 42 and 52, 300 x 5008 x 8192 46.9 and 42.7, 2048^3
+// 28.8 and 20.7).  A grouped launch's tiles are counted on the device; all of
+// the groups' rows are taken to be there.
+S8Kind tiled_kind(const S8Params &p, int sms)
+{
+    S8Kind best = S8Kind::kPair;
+    double best_us = 0.0;
+    for (const S8Kind kind : {S8Kind::kPair, S8Kind::kOne}) {
+        const bool pair = kind == S8Kind::kPair;
+        const S8Shape shape = s8_shape(kind);
+        const int64_t tiles = (int64_t(p.M) + shape.tile_m - 1) / shape.tile_m *
+                              ((int64_t(p.N) + shape.tile_n - 1) / shape.tile_n) * p.batch;
+        if (tiles > S8Schedule::kMaxTiles)
+            continue;
+        S8Schedule s = {};
+        s.plan(int32_t(tiles), int32_t((int64_t(p.K) + shape.block_k - 1) / shape.block_k), pair ? sms / 2 : sms);
+        const double us = pair ? 6.5 + 0.75 * double(s.blocks()) : 5.0 + 0.66 * double(s.blocks());
+        if (best_us == 0.0 || us < best_us) {
+            best = kind;
+            best_us = us;
+        }
+    }
+    return best;
+}
+
 // All checks are done and every size is positive (K may be 0).
 gemm_status_t launch_product(S8Params p, DeviceState *ds, cudaStream_t stream)
 {
@@ -452,9 +482,9 @@ gemm_status_t launch_product(S8Params p, DeviceState *ds, cudaStream_t stream)
 
     // Few rows by M; in groups of up to 32 rows most have far fewer, so those
     // are cut into sixteens and only the rows there are cost anything.
-    const S8Kind kind = p.M <= 16 || (p.group_rows && p.M <= 32) ? S8Kind::kFew16
-                        : p.M <= 32 ? S8Kind::kFew32 : p.M <= 128 ? S8Kind::kOne : S8Kind::kPair;
     const bool few = p.M <= 32;
+    const S8Kind kind = p.M <= 16 || (p.group_rows && p.M <= 32) ? S8Kind::kFew16
+                        : few ? S8Kind::kFew32 : tiled_kind(p, ds->sms);
     const S8Shape shape = s8_shape(kind);
     p.tiles_m = int32_t((int64_t(p.M) + shape.tile_m - 1) / shape.tile_m);
     p.tiles_n = int32_t((int64_t(p.N) + shape.tile_n - 1) / shape.tile_n);

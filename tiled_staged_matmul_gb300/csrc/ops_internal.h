@@ -98,11 +98,16 @@ struct S8Schedule {
         cutters = pieces < 1 ? 1 : pieces < workers ? pieces : workers;
         // Cutting has its price: pieces' sums written, arrivals, sums read
         // back.  Whole tiles all the way where the last wave costs no more.
-        const int64_t cut = int64_t((tiles - shared) / workers) * kb + (shared * kb + cutters - 1) / cutters + kCutBlocks;
-        if (int64_t((tiles + workers - 1) / workers) * kb <= cut) {
+        if (shared && int64_t((tiles + workers - 1) / workers) * kb <= blocks()) {
             shared = 0;
             cutters = 1;
         }
+    }
+    // The time of the busiest worker, in blocks.
+    __host__ __device__ int64_t blocks() const
+    {
+        return shared ? int64_t((tiles - shared) / workers) * kb + (shared * kb + cutters - 1) / cutters + kCutBlocks
+                      : int64_t((tiles + workers - 1) / workers) * kb;
     }
     // First block of worker w's piece (w <= cutters).
     __host__ __device__ int32_t piece_begin(int32_t w) const { return shared * kb * w / cutters; }
