@@ -651,9 +651,7 @@ def quantize_rows(X, group_rows=None, q=None, scales=None, *, stream=None):
     if q is None:
         ldq = K + -K % 16
         sQ = M * ldq if three else 0
-        q = torch.empty((batch, M, ldq) if three else (M, ldq), dtype=torch.int8, device=X.device)
-        if ldq != K:
-            q = q[..., :K]
+        q = torch.empty_strided(shape, (sQ, ldq, 1) if three else (ldq, 1), dtype=torch.int8, device=X.device)
     else:
         if q.shape != shape or q.dtype != torch.int8 or (K > 1 and q.numel() and q.stride(-1) != 1):
             raise ValueError("q must be an int8 tensor of X's shape with a unit last stride")
