@@ -35,7 +35,7 @@ UNITS = ([("gemm_kernels.cu", "gemm_kernels", [])] +
 HOST_SOURCES = ("gemm_api.cu", "ops_api.cu")
 SOURCES = sorted({u[0] for u in UNITS})
 HEADERS = ["api_internal.h", "gemm_internal.h", "gemm_kernel.cuh", "launch.cuh", "ops_internal.h", "ptx.cuh", "s8_common.cuh",
-           "s8_ptx.cuh"]
+           "s8_plan.h", "s8_ptx.cuh"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 
 

@@ -3,6 +3,7 @@
 // launches.
 #include "api_internal.h"
 #include "ops_internal.h"
+#include "s8_plan.h"
 
 #include <algorithm>
 #include <mutex>
@@ -388,80 +389,9 @@ gemm_status_t check_s8(const S8Params &p, bool *trivial)
     return GEMM_OK;
 }
 
-// An operand the tensor-memory accelerator can address (no copy needed).
-bool addressable(const int8_t *x, int64_t ld, int64_t stride, int64_t rows, int64_t batch)
-{
-    return !misaligned(x, 16) && (rows == 1 || ld % 16 == 0) && (batch == 1 || stride % 16 == 0);
-}
-
 std::once_flag g_s8_once[64];
 cudaError_t g_s8_error[64];
 S8Capacity g_s8_capacity[64];
-
-// CTAs per cluster of a few-rows launch: the least estimated time over 1 to 8.
-// A CTA's rate is its share of the memory's, or what its warps can multiply if
-// that is less; its pairs of warps (8, or 4 for two blocks of rows) take whole
-// blocks; adding up their sums takes 1 us.  The launch waits for the cluster
-// with the most tiles.  Finishing a tile takes 2 us, 3 where its sums pass
-// between CTAs; it hides behind the next tile if that takes longer.  (Within 6 %
-// of the best of the eight on nine shapes, 1 x 4096 x 4096 to 16 x 57344 x 8192;
-// the worst of them took up to four times as long.)
-int few_rows_ranks(int64_t tiles, int32_t kb, const S8Capacity &cap, bool two, int *clusters)
-{
-    const double block = 8192.0;                   // bytes of 32 k x 256 columns
-    const double memory = 6.0e6;                   // bytes per us, all CTAs
-    const double most = two ? 38.0e3 : 45.0e3;     // bytes per us, one CTA
-    const int pairs = two ? 4 : 8;
-    int best = 1;
-    double best_us = 0.0;
-    for (int i = 0; i < S8Capacity::KINDS; ++i) {
-        const int ranks = i + 1;
-        if (cap.clusters[i] <= 0 || (i > 0 && ranks > kb))
-            continue;
-        const int64_t n = std::min<int64_t>(tiles, cap.clusters[i]);
-        const double rate = std::min(most, memory / double(n * ranks));
-        const double finish = ranks > 1 ? 3.0 : 2.0;
-        const int64_t steps = ((kb + ranks - 1) / ranks + pairs - 1) / pairs;
-        const double each = std::max(finish, double(steps * pairs) * block / rate + 1.0);
-        const double us = double((tiles + n - 1) / n) * each + finish;
-        if (i == 0 || us < best_us) {
-            best = ranks;
-            best_us = us;
-            *clusters = int(n);
-        }
-    }
-    return best;
-}
-
-// The tiled kernel: a CTA per 128 x 128 tile, or a pair per 256 x 256, which does
-// twice the work at one SM's time for a block and a pair's longer start.  By the
-// time of the busiest worker: 5 us and 0.66 a block of 128 k, or 6.5 and 0.75
-// (the nearer of two on 20 shapes from 140 x 1072 x 272 to 512 x 14336 x 4096, us
-// as single CTAs and pairs: 140 x 1072 x 272 8.1 and 10.4, 512 x 4096 x 4096 26.8
-// and 33.8, 256 x 256 x 65536 42 and 52, 300 x 5008 x 8192 46.9 and 42.7, 2048^3
-// 28.8 and 20.7).  A grouped launch's tiles are counted on the device; all of
-// the groups' rows are taken to be there.
-S8Kind tiled_kind(const S8Params &p, int sms)
-{
-    S8Kind best = S8Kind::kPair;
-    double best_us = 0.0;
-    for (const S8Kind kind : {S8Kind::kPair, S8Kind::kOne}) {
-        const bool pair = kind == S8Kind::kPair;
-        const S8Shape shape = s8_shape(kind);
-        const int64_t tiles = (int64_t(p.M) + shape.tile_m - 1) / shape.tile_m *
-                              ((int64_t(p.N) + shape.tile_n - 1) / shape.tile_n) * p.batch;
-        if (tiles > S8Schedule::kMaxTiles)
-            continue;
-        S8Schedule s = {};
-        s.plan(int32_t(tiles), int32_t((int64_t(p.K) + shape.block_k - 1) / shape.block_k), pair ? sms / 2 : sms);
-        const double us = pair ? 6.5 + 0.75 * double(s.blocks()) : 5.0 + 0.66 * double(s.blocks());
-        if (best_us == 0.0 || us < best_us) {
-            best = kind;
-            best_us = us;
-        }
-    }
-    return best;
-}
 
 // All checks are done and every size is positive (K may be 0).
 gemm_status_t launch_product(S8Params p, DeviceState *ds, cudaStream_t stream)
@@ -480,16 +410,19 @@ gemm_status_t launch_product(S8Params p, DeviceState *ds, cudaStream_t stream)
     if (g_s8_error[dev] != cudaSuccess)
         return fail_cuda(g_s8_error[dev], "setting up the int8 product kernels");
 
-    // Few rows by M; in groups of up to 32 rows most have far fewer, so those
-    // are cut into sixteens and only the rows there are cost anything.
-    const bool few = p.M <= 32;
-    const S8Kind kind = p.M <= 16 || (p.group_rows && p.M <= 32) ? S8Kind::kFew16
-                        : few ? S8Kind::kFew32 : tiled_kind(p, ds->sms);
-    const S8Shape shape = s8_shape(kind);
-    p.tiles_m = int32_t((int64_t(p.M) + shape.tile_m - 1) / shape.tile_m);
-    p.tiles_n = int32_t((int64_t(p.N) + shape.tile_n - 1) / shape.tile_n);
-    p.kb = int32_t((int64_t(p.K) + shape.block_k - 1) / shape.block_k);
-    p.workers = kind == S8Kind::kPair ? ds->sms / 2 : ds->sms;
+    S8Plan plan;
+    if (!plan.make(p, ds->sms, g_s8_capacity[dev]))
+        return fail(GEMM_ERR_INVALID_VALUE, "more than 2^30 output tiles in one call");
+    const S8Shape shape = plan.shape;
+    const bool few = plan.few();
+    p.tiles_m = plan.tiles_m;
+    p.tiles_n = plan.tiles_n;
+    p.kb = plan.kb;
+    p.workers = plan.workers;
+    p.ranks = plan.ranks;
+    p.kb_each = plan.kb / plan.ranks;
+    p.kb_more = plan.kb % plan.ranks;
+    p.sched = plan.sched;
     p.timeout_ns = 2000000000ull + uint64_t(p.kb) * 20000ull;
     p.tag = next_launch_epoch() >> 16;
     const int64_t per16 = 16 / p.epi.out_bytes();
@@ -497,41 +430,15 @@ gemm_status_t launch_product(S8Params p, DeviceState *ds, cudaStream_t stream)
 
     // Workspace: packed copies of operands that cannot be addressed, then the
     // pieces' sums and arrival words.
-    const bool pack_a = !addressable(p.A, p.lda, p.sA, p.M, p.batch);
-    const bool pack_b = !addressable(p.B, p.ldb, p.sB, p.K, p.batch);
-    const int64_t lda2 = round_up(p.K, 16), ldb2 = round_up(p.N, 16);
-    const int64_t bytes_a = pack_a ? round_up(p.batch * p.M * lda2, 256) : 0;
-    const int64_t bytes_b = pack_b ? round_up(p.batch * int64_t(p.K) * ldb2, 256) : 0;
-    const int64_t tiles = int64_t(p.tiles_m) * p.tiles_n * p.batch;
-    if (tiles > S8Schedule::kMaxTiles)
-        return fail(GEMM_ERR_INVALID_VALUE, "more than 2^30 output tiles in one call");
-    S8Schedule sched = {};
-    int grid = 0;
-    if (few) {
-        // (A grouped launch's tiles are counted on the device; the estimate is
-        // for one block of rows in every group.)
-        p.ranks = few_rows_ranks(p.group_rows ? int64_t(p.tiles_n) * p.batch : tiles, p.kb, g_s8_capacity[dev],
-                                 kind == S8Kind::kFew32, &grid);
-        p.kb_each = p.kb / p.ranks;
-        p.kb_more = p.kb % p.ranks;
-    } else {
-        sched.plan(int32_t(tiles), p.kb, p.workers);
-        p.sched = sched;
-        grid = p.group_rows ? p.workers
-                            : int(std::max<int64_t>(sched.shared ? sched.cutters : 0,
-                                                    std::min<int64_t>(sched.tiles, p.workers)));
-    }
-    // (A grouped launch's tiles are counted on the device: any number up to these.)
-    const int64_t cut = few ? 0 : p.group_rows ? 2 * int64_t(p.workers) : sched.shared;
-    const int64_t bytes_p = cut ? 2 * int64_t(p.workers) * shape.slot_bytes : 0;
-    const int64_t bytes_w = cut * shape.parts * 8;
+    const int64_t bytes_a = plan.bytes_a, bytes_b = plan.bytes_b, bytes_p = plan.bytes_p, bytes_w = plan.bytes_w;
+    const int64_t lda2 = plan.lda2, ldb2 = plan.ldb2;
     char *ws = nullptr;
     if (bytes_a + bytes_b + bytes_p + bytes_w > 0 &&
         (e = cudaMallocFromPoolAsync(reinterpret_cast<void **>(&ws), size_t(bytes_a + bytes_b + bytes_p + bytes_w),
                                      ds->pool, stream)) != cudaSuccess)
         return fail_cuda(e, "int8 product workspace");
     gemm_status_t st = GEMM_OK;
-    if (pack_a) {
+    if (plan.pack_a) {
         int8_t *to = reinterpret_cast<int8_t *>(ws);
         if ((e = launch_pack_s8(p.A, p.lda, p.sA, to, lda2, p.M * lda2, p.M, p.K, p.batch, ds->sms, stream)) !=
             cudaSuccess)
@@ -540,7 +447,7 @@ gemm_status_t launch_product(S8Params p, DeviceState *ds, cudaStream_t stream)
         p.lda = lda2;
         p.sA = p.M * lda2;
     }
-    if (pack_b && st == GEMM_OK) {
+    if (plan.pack_b && st == GEMM_OK) {
         int8_t *to = reinterpret_cast<int8_t *>(ws + bytes_a);
         if ((e = launch_pack_s8(p.B, p.ldb, p.sB, to, ldb2, p.K * ldb2, p.K, p.N, p.batch, ds->sms, stream)) !=
             cudaSuccess)
@@ -574,7 +481,7 @@ gemm_status_t launch_product(S8Params p, DeviceState *ds, cudaStream_t stream)
         st = encode_3d(&map_b, CU_TENSOR_MAP_DATA_TYPE_UINT8, 1, p.B, p.N, p.K, p.batch, ldb, sB, 128, uint32_t(shape.block_k),
                        CU_TENSOR_MAP_L2_PROMOTION_L2_256B, "B");
     if (st == GEMM_OK) {
-        e = launch_s8(map_a, map_b, p, kind, grid, stream);
+        e = launch_s8(map_a, map_b, p, plan.kind, plan.grid, stream);
         if (e != cudaSuccess)
             st = fail_cuda(e, "int8 product launch");
     }

@@ -148,7 +148,9 @@ struct S8Shape {
     int64_t slot_bytes;         // of one worker's partial sums of one tile
     int parts;                  // arrival words per tile
 };
-S8Shape s8_shape(S8Kind kind);
+constexpr S8Shape kS8Shapes[] = {
+    {16, 256, 32, 0, 0}, {32, 256, 32, 0, 0}, {128, 128, 128, 65536, 4}, {256, 256, 128, 262144, 8}};
+constexpr S8Shape s8_shape(S8Kind kind) { return kS8Shapes[int(kind)]; }
 // Clusters of 1 to 8 CTAs of the few-rows kernels that fit on the device at once.
 struct S8Capacity {
     static constexpr int KINDS = 8;

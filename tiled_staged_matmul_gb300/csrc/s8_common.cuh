@@ -66,6 +66,9 @@ struct S8Cfg {
     static_assert(A_COL + S2 * (BK / 2) <= 512 && TILE_N <= 256, "TMEM columns");
     static constexpr int PARTS = GROUPS * CTAS; // (CTA, group) parts of a tile
     static constexpr int32_t SLOT_INTS = PARTS * ROWS * HC;
+    static constexpr S8Shape SHAPE = s8_shape(PAIR ? S8Kind::kPair : S8Kind::kOne);
+    static_assert(SHAPE.tile_m == TILE_M && SHAPE.tile_n == TILE_N && SHAPE.block_k == BK &&
+                  SHAPE.slot_bytes == 4 * SLOT_INTS && SHAPE.parts == PARTS, "the host's idea of a tile");
 };
 
 // Where a tile lies.

@@ -55,6 +55,8 @@ struct S8FewCfg {
     static_assert(TERMS_OFF + 4 * (2 * COLS + ROWS) <= GROUP_ROWS_OFF && kMaxGroupsPerLaunch <= 256, "control block");
     static constexpr int SMEM_BYTES = 1024 + WARPS * STAGES * (B_BYTES + A_BYTES) + 2 * SUMS * 4 + CTRL;
     static_assert(SMEM_BYTES <= 232448 && SMEM_BYTES > 232448 / 2, "227 KiB per block, one block per SM");
+    static constexpr S8Shape SHAPE = s8_shape(MT == 1 ? S8Kind::kFew16 : S8Kind::kFew32);
+    static_assert(SHAPE.tile_m == ROWS && SHAPE.tile_n == COLS && SHAPE.block_k == BK, "the host's idea of a tile");
     static constexpr int FLUSH = 1024 / BK;   // blocks whose sums f32 holds exactly
     // Registers by role: the MMA warps' accumulators need more than an even share.
     static constexpr int LAUNCH_REGS = MT == 1 ? 96 : 168;
@@ -561,27 +563,6 @@ __global__ void __launch_bounds__(256)
         *reinterpret_cast<uint4 *>(dst + z * d_stride + r * d_ld + c) = make_uint4(w[0], w[1], w[2], w[3]);
     }
 }
-
-template <bool PAIR>
-S8Shape shape_of()
-{
-    using Cfg = S8Cfg<PAIR>;
-    return S8Shape{Cfg::TILE_M, Cfg::TILE_N, Cfg::BK, int64_t(Cfg::SLOT_INTS) * 4, Cfg::PARTS};
-}
-
-}  // namespace
-
-S8Shape s8_shape(S8Kind kind)
-{
-    switch (kind) {
-    case S8Kind::kFew16: return S8Shape{16, 256, 32, 0, 0};
-    case S8Kind::kFew32: return S8Shape{32, 256, 32, 0, 0};
-    case S8Kind::kOne: return shape_of<false>();
-    default: return shape_of<true>();
-    }
-}
-
-namespace {
 
 template <int MT>
 cudaError_t set_few(S8Capacity *cap)
