@@ -459,6 +459,23 @@ def gemv(A, x, out=None, *, stream=None):
     return out
 
 
+def _on_stream(stream, call, *args, **kwargs):
+    """``call`` with ``stream`` (a torch stream or a handle) as torch's current
+    one.  What a call allocates, fills or copies in torch goes to the current
+    stream, with nothing that orders it with kernels on another: results could
+    be filled over, or lie in memory that the current stream still works on.
+    The tensors it returns belong to ``stream``."""
+    import torch
+    handle = _stream_handle(stream)
+    if handle == _stream_handle(None):
+        return call(*args, **kwargs)
+    if isinstance(stream, int):
+        # (0 and 1 both name the default stream.)
+        stream = torch.cuda.ExternalStream(handle) if handle > 1 else torch.cuda.default_stream()
+    with torch.cuda.stream(stream):
+        return call(*args, **kwargs)
+
+
 # Mixture-of-Experts: token rows to their experts and back.  The experts' side
 # is a groups x capacity x width tensor, the layout grouped_gemm takes.
 
@@ -532,6 +549,8 @@ def moe_route(expert_ids, groups, capacity, *, stream=None):
     choice past the capacity or an id outside [0, groups); ``counts`` is what
     ``grouped_gemm`` takes as ``group_rows``.  Both are int32."""
     import torch
+    if stream is not None:
+        return _on_stream(stream, moe_route, expert_ids, groups, capacity)
     if expert_ids.dtype not in (torch.int32, torch.int64) or not expert_ids.is_cuda or expert_ids.dim() != 2:
         raise ValueError("expert_ids must be a 2-D CUDA tensor of int32 or int64")
     ids = expert_ids if expert_ids.is_contiguous() else expert_ids.contiguous()
@@ -550,6 +569,8 @@ def moe_dispatch(x, slots, groups, capacity, out=None, *, stream=None):
     ``x`` is tokens x width (f32, f16, bf16 or int8).  Returns ``out`` (groups
     x capacity x width); rows no slot names keep their contents (zeros when
     ``out`` is not given)."""
+    if out is None and stream is not None:
+        return _on_stream(stream, moe_dispatch, x, slots, groups, capacity)
     T, k = _slots_of(slots)
     H = x.shape[-1]
     ldx = _token_pitch(x, T, H, x.dtype, "x")
@@ -568,6 +589,8 @@ def moe_dispatch_grad(drows, slots, out=None, *, stream=None):
     for groups x capacity x width ``drows`` (f32, f16 or bf16); summed in f32,
     returned in the rows' type."""
     import torch
+    if out is None and stream is not None:
+        return _on_stream(stream, moe_dispatch_grad, drows, slots)
     code = _elem_type(drows.dtype)
     T, k = _slots_of(slots)
     G, cap, H = drows.shape
@@ -588,6 +611,8 @@ def moe_combine(rows, slots, weights=None, out=None, *, stream=None):
     x width ``rows`` (f32, f16 or bf16), f32 ``weights`` (tokens x topk; none:
     ones); summed in f32, returned in the rows' type."""
     import torch
+    if out is None and stream is not None:
+        return _on_stream(stream, moe_combine, rows, slots, weights)
     code = _elem_type(rows.dtype)
     T, k = _slots_of(slots)
     G, cap, H = rows.shape
@@ -609,6 +634,8 @@ def moe_combine_grad(dout, rows, slots, weights=None, drows=None, *, stream=None
     their contents, zeros when ``drows`` is not given) and ``dweights[t, j] =
     <dout[t], rows[slots[t, j]]>`` (f32, 0 for a dropped choice)."""
     import torch
+    if stream is not None:
+        return _on_stream(stream, moe_combine_grad, dout, rows, slots, weights, drows)
     code = _elem_type(dout.dtype)
     T, k = _slots_of(slots)
     G, cap, H = rows.shape
@@ -637,6 +664,8 @@ def quantize_rows(X, group_rows=None, q=None, scales=None, *, stream=None):
     products want.  ``group_rows`` (int32, one count per matrix) limits the
     rows that are read and written."""
     import torch
+    if stream is not None and (q is None or scales is None):
+        return _on_stream(stream, quantize_rows, X, group_rows, q, scales)
     code = _elem_type(X.dtype)
     shape = X.shape
     three = len(shape) == 3
@@ -692,6 +721,9 @@ def _s8_vector(t, n, batch, three, name):
 
 def _s8_call(A, B, scale_a, scale_b, group_rows, out, alpha, bias, activation, slope, out_dtype, stream):
     import torch
+    if out is None and stream is not None:
+        return _on_stream(stream, _s8_call, A, B, scale_a, scale_b, group_rows, None, alpha, bias, activation, slope,
+                          out_dtype, None)
     if A.dtype != torch.int8 or B.dtype != torch.int8:
         raise TypeError("A and B must be torch.int8")
     dim = A.dim()
