@@ -81,3 +81,21 @@ def test_the_default_stream_by_its_handle(b, data):
     torch.cuda.default_stream().synchronize()
     side.synchronize()
     assert torch.equal(got, want)
+
+
+OLDER = {
+    "gemm": lambda b, d, s: [b.gemm(d["x"], d["W"][0], stream=s)],
+    "grouped_gemm": lambda b, d, s: [b.grouped_gemm(d["rows"], d["W"], d["counts"], stream=s)],
+    "grouped_gemm, strided counts": lambda b, d, s: [b.grouped_gemm(d["rows"], d["W"], d["wide_counts"][::2], stream=s)],
+    "rowsum": lambda b, d, s: [b.rowsum(d["x"], stream=s)],
+    "gemv": lambda b, d, s: [b.gemv(d["x"], d["rows"][0, 0], stream=s)],
+}
+
+
+@pytest.mark.parametrize("name", list(OLDER))
+def test_so_do_the_matrix_calls(b, data, name):
+    data["W"] = torch.randn((GROUPS, WIDTH, COLS), generator=torch.Generator(device="cuda").manual_seed(5),
+                            device="cuda").half()
+    data["wide_counts"] = data["counts"].repeat_interleave(2)
+    torch.cuda.synchronize()
+    check(lambda s: OLDER[name](b, data, s), False)

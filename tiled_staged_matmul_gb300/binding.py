@@ -317,6 +317,23 @@ def _stream_handle(stream):
     return stream.cuda_stream
 
 
+def _on_stream(stream, call, *args, **kwargs):
+    """``call`` with ``stream`` (a torch stream or a handle) as torch's current
+    one.  What a call allocates, fills or copies in torch goes to the current
+    stream, with nothing that orders it with kernels on another: results could
+    be filled over, or lie in memory that the current stream still works on.
+    The tensors it returns belong to ``stream``."""
+    import torch
+    handle = _stream_handle(stream)
+    if handle == _stream_handle(None):
+        return call(*args, **kwargs)
+    if isinstance(stream, int):
+        # (0 and 1 both name the default stream.)
+        stream = torch.cuda.ExternalStream(handle) if handle > 1 else torch.cuda.default_stream()
+    with torch.cuda.stream(stream):
+        return call(*args, **kwargs)
+
+
 def gemm(A, B, out=None, *, alpha=1.0, bias=None, activation="none", slope=0.01, out_dtype=None,
          split_k=0, tile_n=0, tile_m=0, timeout_ms=0, inject_stall=0, stream=None):
     """``out = activation(alpha * (A @ B) + bias)`` for f16 CUDA tensors A
@@ -328,6 +345,10 @@ def gemm(A, B, out=None, *, alpha=1.0, bias=None, activation="none", slope=0.01,
     padded (``stride(-2) >= size(-1)``) but the last stride must be 1.
     Returns ``out`` (allocated with ``torch.empty`` when not given)."""
     import torch
+    if out is None and stream is not None:
+        return _on_stream(stream, gemm, A, B, alpha=alpha, bias=bias, activation=activation, slope=slope,
+                          out_dtype=out_dtype, split_k=split_k, tile_n=tile_n, tile_m=tile_m,
+                          timeout_ms=timeout_ms, inject_stall=inject_stall)
     if A.dtype != torch.float16 or B.dtype != torch.float16:
         raise TypeError("A and B must be torch.float16")
     batched = A.dim() == 3
@@ -386,6 +407,10 @@ def grouped_gemm(A, B, group_rows, out=None, *, alpha=1.0, bias=None, activation
     group's count keep the contents of ``out`` (zeros when ``out`` is not
     given).  Returns ``out`` (groups x M x N, f32)."""
     import torch
+    if stream is not None and (out is None or not group_rows.is_contiguous()):
+        return _on_stream(stream, grouped_gemm, A, B, group_rows, out, alpha=alpha, bias=bias,
+                          activation=activation, slope=slope, out_dtype=out_dtype, tile_n=tile_n,
+                          tile_m=tile_m)
     if A.dtype != torch.float16 or B.dtype != torch.float16:
         raise TypeError("A and B must be torch.float16")
     if A.dim() != 3 or B.dim() != 3 or A.shape[0] != B.shape[0] or A.shape[2] != B.shape[1]:
@@ -427,6 +452,8 @@ def rowsum(X, out=None, *, stream=None):
     """Row sums of a 2-D CUDA tensor (f32, f16 or bf16; any strides): an f32
     tensor of X.shape[0] values, summed in f32 in a fixed order."""
     import torch
+    if out is None and stream is not None:
+        return _on_stream(stream, rowsum, X)
     names = {torch.float32: "f32", torch.float16: "f16", torch.bfloat16: "bf16"}
     if X.dtype not in names or X.dim() != 2 or not X.is_cuda:
         raise ValueError("X must be a 2-D CUDA tensor of float32, float16 or bfloat16")
@@ -444,6 +471,8 @@ def gemv(A, x, out=None, *, stream=None):
     """``A @ x`` for an f16 CUDA matrix A (unit last stride) and f16 vector x
     (any stride): an f32 vector."""
     import torch
+    if out is None and stream is not None:
+        return _on_stream(stream, gemv, A, x)
     if A.dtype != torch.float16 or x.dtype != torch.float16 or A.dim() != 2 or x.dim() != 1:
         raise ValueError("A must be a 2-D and x a 1-D torch.float16 CUDA tensor")
     M, K = A.shape
@@ -457,23 +486,6 @@ def gemv(A, x, out=None, *, stream=None):
                           A.stride(0) if M > 1 else max(K, 1), x.stride(0) if K > 1 else 1,
                           _stream_handle(stream)))
     return out
-
-
-def _on_stream(stream, call, *args, **kwargs):
-    """``call`` with ``stream`` (a torch stream or a handle) as torch's current
-    one.  What a call allocates, fills or copies in torch goes to the current
-    stream, with nothing that orders it with kernels on another: results could
-    be filled over, or lie in memory that the current stream still works on.
-    The tensors it returns belong to ``stream``."""
-    import torch
-    handle = _stream_handle(stream)
-    if handle == _stream_handle(None):
-        return call(*args, **kwargs)
-    if isinstance(stream, int):
-        # (0 and 1 both name the default stream.)
-        stream = torch.cuda.ExternalStream(handle) if handle > 1 else torch.cuda.default_stream()
-    with torch.cuda.stream(stream):
-        return call(*args, **kwargs)
 
 
 # Mixture-of-Experts: token rows to their experts and back.  The experts' side
