@@ -136,3 +136,32 @@ def test_product_epilogue_and_groups(b):
     assert status(b, b.gemm_s8_grouped_scaled(A0, B0, C0, 0, 0, 0, 2, *tail)) == "GEMM_ERR_INVALID_VALUE"
     assert status(b, b.gemm_s8_grouped_scaled(A0, B0, C0, 0, 0, D0 + 1, 2, *tail)) == "GEMM_ERR_MISALIGNED"
     assert status(b, b.gemm_s8_grouped_scaled(A0, B0, C0, 0, 0, 0, 0, *tail)) == "GEMM_OK"
+
+
+# Pitches and strides whose spans pass 64 bits: what wraps there would look like
+# a small buffer.  The written buffer lies above, so that the true span meets it.
+FAR = 1 << 62
+
+
+@pytest.mark.parametrize("call,args", [
+    ("moe_dispatch_rows", (A0, 2, B0, C0, 5, 2, 8, 16, FAR, 16)),
+    ("moe_dispatch_rows", (B0, 2, C0, A0, 5, 2, 5, 16, 16, FAR)),
+    ("moe_dispatch_rows_grad", (A0, 1, B0, C0, 5, 2, 5, 16, FAR, 16)),
+    ("moe_combine_rows", (A0, 0, B0, D0, C0, 5, 2, 5, 16, FAR, 16)),
+    ("moe_combine_rows", (B0, 1, C0, D0, A0, 5, 2, 8, 16, 16, FAR)),
+    ("moe_combine_rows_grad", (A0, B0, 1, C0, D0, E0, 0, 5, 2, 8, 16, FAR, 16, 16)),
+    ("moe_combine_rows_grad", (B0, A0, 1, C0, D0, E0, 0, 5, 2, 5, 16, 16, FAR, 16)),
+    ("moe_combine_rows_grad", (B0, C0, 1, D0, E0, A0, 0, 5, 2, 5, 16, 16, 16, FAR)),
+    ("quantize_rows_s8", (A0, 1, B0, C0, 0, 5, 16, FAR, 16)),
+    ("quantize_rows_s8", (B0, 1, A0, C0, 0, 5, 16, 16, FAR)),
+    ("quantize_rows_s8", (A0, 1, B0, C0, 0, 4, 16, 16, 16, FAR, 64, 4, 5)),
+    ("quantize_rows_s8", (B0, 1, C0, A0, 0, 4, 16, 16, 16, 64, 64, FAR, 5)),
+    ("gemm_s8_scaled", (A0, B0, C0, 0, 0, 5, 8, 4, FAR, 8, 8)),
+    ("gemm_s8_scaled", (B0, A0, C0, 0, 0, 5, 8, 5, 5, FAR, 8)),
+    ("gemm_s8_scaled", (B0, C0, A0, 0, 0, 5, 8, 4, 4, 8, FAR)),
+    ("gemm_s8_scaled", (A0, B0, C0, 0, 0, 4, 8, 4, 4, 8, 8, FAR, 32, 32, 0, 0, 5)),
+    ("gemm_s8_scaled", (B0, C0, D0, A0, 0, 4, 8, 4, 4, 8, 8, 16, 32, 32, FAR, 0, 5)),
+    ("gemm_s8_scaled", (B0, C0, A0, 0, 0, 5, 8, 4, 4, 8, FAR, 20, 32, 32, 0, 0, 2)),
+])
+def test_spans_past_64_bits(b, call, args):
+    assert status(b, getattr(b, call)(*args)) == "GEMM_ERR_ALIAS"

@@ -66,11 +66,19 @@ gemm_status_t check_on_device(const Buffer *b, int n, int dev)
     return GEMM_OK;
 }
 
-// Bytes of `rows` rows of `width` elements `ld` apart.
-int64_t span(int64_t rows, int64_t width, int64_t ld, int64_t elem)
+// Bytes spanned by `batch` matrices `stride` elements apart of `rows` rows `ld`
+// apart.  More than 64 bits hold come out as the most that they hold, which
+// lies in no allocation.
+int64_t reach(int64_t batch, int64_t stride, int64_t rows, int64_t ld, int64_t cols, int64_t elem)
 {
-    return span_bytes(1, 0, rows, ld, width, elem);
+    if (batch <= 0 || rows <= 0 || cols <= 0)
+        return 0;
+    const __int128 bytes = (__int128(batch - 1) * stride + __int128(rows - 1) * ld + cols) * elem;
+    return bytes > INT64_MAX ? INT64_MAX : int64_t(bytes);
 }
+
+// Bytes of `rows` rows of `width` elements `ld` apart.
+int64_t span(int64_t rows, int64_t width, int64_t ld, int64_t elem) { return reach(1, 0, rows, ld, width, elem); }
 
 // Bytes of one access: 16 or 4 where every address, pitch and width in `all`
 // (or-ed together, in bytes) is a multiple, else one element.
@@ -332,15 +340,15 @@ gemm_status_t quantize_rows_s8(const void *X, int32_t elem_type, int8_t *q, floa
         return fail(GEMM_ERR_INVALID_VALUE, "M x batch must be below 2^31");
     if (ldx < K || ldq < K)
         return fail(GEMM_ERR_INVALID_VALUE, "a row pitch is below K (%lld)", (long long)K);
-    if (batch > 1 && M > 0 && (strideX < 0 || strideQ < (M - 1) * ldq + K || scale_stride < M))
+    if (batch > 1 && M > 0 && (strideX < 0 || strideQ < span(M, K, ldq, 1) || scale_stride < M))
         return fail(GEMM_ERR_INVALID_VALUE, "batch strides let matrices of q or of the scales overlap");
     const int64_t eb = elem_bytes(elem_type);
     if (misaligned(X, eb) || misaligned(scales, 4) || misaligned(group_rows, 4))
         return fail(GEMM_ERR_MISALIGNED, "X, scales and group_rows must sit at their natural alignment");
-    const Buffer buf[] = {{X, span_bytes(batch, strideX, M, ldx, K, eb), "X", false},
+    const Buffer buf[] = {{X, reach(batch, strideX, M, ldx, K, eb), "X", false},
                           {group_rows, group_rows ? batch * 4 : 0, "group_rows", false},
-                          {q, span_bytes(batch, strideQ, M, ldq, K, 1), "q", true},
-                          {scales, span_bytes(batch, scale_stride, 1, M, M, 4), "scales", true}};
+                          {q, reach(batch, strideQ, M, ldq, K, 1), "q", true},
+                          {scales, reach(batch, scale_stride, 1, M, M, 4), "scales", true}};
     gemm_status_t st = check_buffers(buf, 4);
     if (st != GEMM_OK || M == 0 || batch == 0)
         return st;
@@ -384,7 +392,7 @@ gemm_status_t check_s8(const S8Params &p, bool *trivial)
     if (misaligned(p.scale_a, 4) || misaligned(p.scale_b, 4) || misaligned(p.epi.bias, 4) ||
         misaligned(p.group_rows, 4))
         return fail(GEMM_ERR_MISALIGNED, "scales, bias and group_rows must be 4-byte aligned");
-    if (p.batch > 1 && p.sC < int64_t(p.M - 1) * p.ldc + p.N)
+    if (p.batch > 1 && p.sC < span(p.M, p.N, p.ldc, 1))
         return fail(GEMM_ERR_ALIAS, "batches of C overlap (strideC too small)");
     return GEMM_OK;
 }
@@ -497,13 +505,13 @@ gemm_status_t run_s8(S8Params p, cudaStream_t stream)
     if (st != GEMM_OK || trivial)
         return st;
     const Buffer buf[] = {
-        {p.A, p.K ? span_bytes(p.batch, p.sA, p.M, p.lda, p.K, 1) : 0, "A", false},
-        {p.B, p.K ? span_bytes(p.batch, p.sB, p.K, p.ldb, p.N, 1) : 0, "B", false},
-        {p.scale_a, p.scale_a ? span_bytes(p.batch, p.sa_stride, 1, p.M, p.M, 4) : 0, "scale_a", false},
-        {p.scale_b, p.scale_b ? span_bytes(p.batch, p.sb_stride, 1, p.N, p.N, 4) : 0, "scale_b", false},
-        {p.epi.bias, p.epi.bias ? span_bytes(p.batch, p.epi.bias_stride, 1, p.N, p.N, 4) : 0, "bias", false},
+        {p.A, p.K ? reach(p.batch, p.sA, p.M, p.lda, p.K, 1) : 0, "A", false},
+        {p.B, p.K ? reach(p.batch, p.sB, p.K, p.ldb, p.N, 1) : 0, "B", false},
+        {p.scale_a, p.scale_a ? reach(p.batch, p.sa_stride, 1, p.M, p.M, 4) : 0, "scale_a", false},
+        {p.scale_b, p.scale_b ? reach(p.batch, p.sb_stride, 1, p.N, p.N, 4) : 0, "scale_b", false},
+        {p.epi.bias, p.epi.bias ? reach(p.batch, p.epi.bias_stride, 1, p.N, p.N, 4) : 0, "bias", false},
         {p.group_rows, p.group_rows ? int64_t(p.batch) * 4 : 0, "group_rows", false},
-        {p.C, span_bytes(p.batch, p.sC, p.M, p.ldc, p.N, p.epi.out_bytes()), "C", true}};
+        {p.C, reach(p.batch, p.sC, p.M, p.ldc, p.N, p.epi.out_bytes()), "C", true}};
     if ((st = check_buffers(buf, 7)) != GEMM_OK)
         return st;
     int dev = 0;
