@@ -411,9 +411,10 @@ gemm_status_t quantize_rows_s8(const void *X, int32_t elem_type, int8_t *q, floa
 
 /* C[i][j] = act(alpha * scale_a[i] * scale_b[j] * S[i][j] + bias[j]),
  * S[i][j] = sum over k of A[i][k] * B[k][j], for 8-bit integers A and B.
- * The sum is the exact integer (32 bits: K below 131072), so a call is
- * bitwise reproducible whatever the launch shape; it is converted to f32,
- * scaled, and rounded once to the output type.
+ * The sum is the exact integer (32 bits: K below 131072).  It is converted to
+ * f32, multiplied by alpha * scale_a[i], then by scale_b[j] with bias[j] added
+ * in one rounding, and rounded once to the output type, in every kernel alike:
+ * a row's result is bitwise the same whatever the call's other rows are.
  *   A        device, M rows of K int8 values (-128 included), row stride lda
  *   B        device, K rows of N int8 values, row stride ldb
  *   C        device, M rows of N values of epi->out_type (f32 without epi), row stride ldc;

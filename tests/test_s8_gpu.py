@@ -435,3 +435,28 @@ def test_scales_are_quotients_for_every_mantissa(b, dtype):
         m = rows.shape[0]
         assert np.array_equal(s.cpu().numpy(), want_s[:m])
         assert np.array_equal(q.cpu().numpy(), np.tile(want_q[:m], rows.shape[1] // 6))
+
+
+@pytest.mark.parametrize("act", ["none", "relu", "leaky_relu", "gelu", "gelu_tanh", "silu"])
+@pytest.mark.parametrize("out_type", ["f32", "f16", "bf16"])
+def test_a_row_does_not_depend_on_the_rows_beside_it(b, out_type, act):
+    """The same rows in calls of 1 to 1400: every kernel, the same bits."""
+    N, K = 2600, 700
+    g = torch.Generator().manual_seed(21)
+    A, B = codes((1400, K), 21).cuda(), codes((K, up(N, 16)), 22).cuda()[:, :N]
+    sa = (torch.rand((1400,), generator=g) * 0.03 + 1e-3).cuda()
+    sb = ((torch.rand((N,), generator=g) - 0.3) * 0.02).cuda()
+    bias = torch.randn((N,), generator=g).cuda()
+    for kw in ({"bias": bias, "alpha": 0.7}, {"alpha": 0.7}, {"bias": bias}):
+        for scales in ((sa, sb), (None, sb), (sa, None)):
+            def call(m):
+                return b.gemm_s8(A[:m], B, *(v[:m] if v is sa else v for v in scales), activation=act,
+                                 out_dtype=TORCH[out_type], **kw)
+            all_rows = call(1400)
+            for m in (1, 16, 17, 32, 33, 128, 300):
+                assert torch.equal(call(m), all_rows[:m]), m
+    groups = b.grouped_gemm_s8(A[:60].view(2, 30, K), torch.stack([B, B]), sa[:60].view(2, 30), sb,
+                               torch.tensor([30, 7], dtype=torch.int32, device="cuda"), alpha=0.7, bias=bias,
+                               activation=act, out_dtype=TORCH[out_type])
+    rows = b.gemm_s8(A, B, sa, sb, alpha=0.7, bias=bias, activation=act, out_dtype=TORCH[out_type])
+    assert torch.equal(groups[0], rows[:30]) and torch.equal(groups[1, :7], rows[30:37])

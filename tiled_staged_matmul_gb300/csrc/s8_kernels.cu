@@ -136,18 +136,20 @@ __device__ __forceinline__ S8Tile few_rows_terms(const S8Params &p, const FewPla
     const S8Tile t = few_rows_tile<MT>(p, f, tile);
     for (int c = ft; c < Cfg::COLS; c += FT) {
         const int32_t col = t.n0 + c;
-        float sb = p.epi.alpha, bias = 0.f;
+        float sb = 1.f, bias = 0.f;
         if (p.scale_b && col < p.N)
-            sb *= p.scale_b[t.z * p.sb_stride + col];
+            sb = p.scale_b[t.z * p.sb_stride + col];
         if (p.epi.bias && col < p.N)
             bias = p.epi.bias[t.z * p.epi.bias_stride + col];
         ptx::st_shared_u32(f.terms0 + 4u * c, __float_as_uint(sb));
         ptx::st_shared_u32(f.terms0 + 4u * (Cfg::COLS + c), __float_as_uint(bias));
     }
+    // (alpha goes into the row's factor, as in the tiled kernels: a row's bits are
+    // the same whichever kernel its call takes.)
     if (ft < Cfg::ROWS)
         ptx::st_shared_u32(f.terms0 + 4u * (2 * Cfg::COLS + ft),
-                           __float_as_uint(p.scale_a && ft < t.rows
-                                               ? p.scale_a[t.z * p.sa_stride + t.m0 + ft] : 1.f));
+                           __float_as_uint(p.epi.alpha * (p.scale_a && ft < t.rows
+                                                              ? p.scale_a[t.z * p.sa_stride + t.m0 + ft] : 1.f)));
     return t;
 }
 
