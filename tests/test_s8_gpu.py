@@ -460,3 +460,27 @@ def test_a_row_does_not_depend_on_the_rows_beside_it(b, out_type, act):
                                activation=act, out_dtype=TORCH[out_type])
     rows = b.gemm_s8(A, B, sa, sb, alpha=0.7, bias=bias, activation=act, out_dtype=TORCH[out_type])
     assert torch.equal(groups[0], rows[:30]) and torch.equal(groups[1, :7], rows[30:37])
+
+
+@pytest.mark.parametrize("K", [0, 48])
+def test_counts_out_of_range_are_reported_without_a_sum_too(b, K):
+    groups, M, N = 300, 6, 16  # (more groups than one launch takes)
+    A, B = codes((groups, M, K), 23).cuda(), codes((groups, K, N), 24).cuda()
+    bias = torch.arange(N, device="cuda", dtype=torch.float32)
+    rows = torch.full((groups,), M, dtype=torch.int32)
+    want = None
+    for at, bad in ((None, None), (0, M + 1), (5, -1), (299, 2 ** 31 - 1)):
+        counts = rows.clone()
+        if at is not None:
+            counts[at] = bad
+        out = b.grouped_gemm_s8(A, B, None, None, counts.cuda(), torch.full((groups, M, N), PRIOR, device="cuda"),
+                                bias=bias)
+        assert b.gemm_get_device_status(0) == (b.GEMM_OK if at is None else b.GEMM_ERR_INVALID_VALUE)
+        assert b.gemm_get_device_status(0) == b.GEMM_OK
+        if at is None:
+            want = out
+        else:
+            expect = want.clone()
+            if bad < 0:
+                expect[at] = PRIOR
+            assert torch.equal(out, expect)

@@ -409,6 +409,8 @@ gemm_status_t launch_product(S8Params p, DeviceState *ds, cudaStream_t stream)
         const int64_t total = int64_t(p.M) * p.N * p.batch;
         const int grid = int(std::min<int64_t>((total + 255) / 256, int64_t(ds->sms) * 8));
         e = launch_zero_fill(p.C, p.M, p.N, p.batch, p.ldc, p.sC, p.group_rows, p.epi, grid, stream);
+        if (e == cudaSuccess && p.group_rows)
+            e = launch_s8_counts(p, stream);
         return e == cudaSuccess ? GEMM_OK : fail_cuda(e, "int8 product of the empty sum");
     }
     int dev = 0;

@@ -165,6 +165,8 @@ cudaError_t launch_s8_tiled(const CUtensorMap &map_a, const CUtensorMap &map_b, 
                             cudaStream_t stream);
 cudaError_t launch_s8(const CUtensorMap &map_a, const CUtensorMap &map_b, const S8Params &p, S8Kind kind, int grid,
                       cudaStream_t stream);
+// Raises kStatusGroupRows where a count is outside [0, M] (the products above do so themselves).
+cudaError_t launch_s8_counts(const S8Params &p, cudaStream_t stream);
 // Rows of `cols` bytes into rows 16-byte aligned and `d_ld` apart.
 cudaError_t launch_pack_s8(const int8_t *src, int64_t s_ld, int64_t s_stride, int8_t *dst, int64_t d_ld,
                            int64_t d_stride, int64_t rows, int64_t cols, int64_t batch, int sms,

@@ -521,6 +521,21 @@ __global__ void __launch_bounds__(S8FewCfg<MT>::THREADS, 1)
     }
 }
 
+// ------------------------------------------------------------- counts alone
+
+// Report counts outside [0, M], for a grouped launch whose sums are empty: the
+// fill that does its work only clamps them.
+__global__ void __launch_bounds__(kMaxGroupsPerLaunch)
+    tsm_s8_counts_kernel(const int32_t *group_rows, int32_t groups, int32_t M, uint32_t *status)
+{
+    chain_next();
+    chain_wait();
+    const int32_t g = int32_t(threadIdx.x);
+    const int32_t rows = g < groups ? __ldcg(group_rows + g) : 0;
+    if (rows < 0 || rows > M)
+        atomicOr(status, kStatusGroupRows);
+}
+
 // ------------------------------------------------------------- repacking
 
 // One thread per 16 bytes of the packed rows (zeros past a row's end).
@@ -635,6 +650,12 @@ cudaError_t launch_s8(const CUtensorMap &map_a, const CUtensorMap &map_b, const 
     case kActSilu: return launch_s8_tiled<kActSilu>(map_a, map_b, p, pair, grid, stream);
     default: return launch_s8_tiled<kActNone>(map_a, map_b, p, pair, grid, stream);
     }
+}
+
+cudaError_t launch_s8_counts(const S8Params &p, cudaStream_t stream)
+{
+    return launch_chained(tsm_s8_counts_kernel, dim3(1), kMaxGroupsPerLaunch, 0, 0, stream, p.group_rows, p.batch, p.M,
+                          p.status);
 }
 
 cudaError_t launch_pack_s8(const int8_t *src, int64_t s_ld, int64_t s_stride, int8_t *dst, int64_t d_ld,
