@@ -363,3 +363,71 @@ def test_route_over_chunks(b, n, groups, wide):
     want, kept = route_reference(ids.numpy(), groups, capacity)
     assert np.array_equal(slots.cpu().numpy(), want)
     assert np.array_equal(counts.cpu().numpy(), kept)
+
+
+def many_slots(tokens, topk, groups, capacity, seed):
+    """Slots of random choices with room for about two thirds of them."""
+    ids = draw_ids(tokens, topk, groups, seed)
+    slots = np.full(ids.size, -1, dtype=np.int64)
+    for e in range(groups):
+        at = np.flatnonzero(ids.reshape(-1) == e)[:capacity]
+        slots[at] = e * capacity + np.arange(at.size)
+    return torch.from_numpy(slots.reshape(ids.shape))
+
+
+# As many tokens as make one warp take two rows of two pieces at a time (155648
+# pieces in all on 152 SMs), and more warps' work than one grid has warps (77824).
+MANY = [(700, 5, 9, 300, 2048), (2500, 3, 4, 1300, 1001), (1300, 7, 16, 400, 1032), (90001, 2, 5, 30000, 40),
+        (40003, 3, 7, 12000, 24)]
+
+
+@pytest.mark.parametrize("dtype", ["f32", "f16", "bf16"])
+@pytest.mark.parametrize("tokens,topk,groups,capacity,width", MANY)
+def test_many_tokens(b, tokens, topk, groups, capacity, width, dtype):
+    """Every call on one set of slots, against sums in 64 bits on the GPU."""
+    dt = TYPES[dtype]
+    slots = many_slots(tokens, topk, groups, capacity, 11).cuda()
+    dslots = slots.int()
+    g = torch.Generator(device="cuda").manual_seed(tokens)
+    rnd = lambda *s: torch.randn(s, generator=g, device="cuda")
+    R = groups * capacity
+    at, on = slots.clamp(min=0), slots >= 0
+    named = torch.zeros(R, dtype=torch.bool, device="cuda")
+    named[slots[on]] = True
+    x, dout, w = rnd(tokens, width).to(dt), rnd(tokens, width).to(dt), rnd(tokens, topk)
+    rows = rnd(R, width).to(dt)
+    rows[~named] = float("nan")
+    w[~on] = float("nan")
+    token = torch.arange(tokens, device="cuda")[:, None].expand(-1, topk)
+
+    out = torch.full((groups, capacity, width), 99.0, dtype=dt, device="cuda")
+    b.moe_dispatch(x, dslots, groups, capacity, out)
+    want = torch.full((R, width), 99.0, dtype=dt, device="cuda")
+    want[slots[on]] = x[token[on]]
+    assert torch.equal(out.view(R, width), want)
+
+    view = rows.view(groups, capacity, width)
+    for weights in (w, None):
+        total, mag = (torch.zeros((tokens, width), dtype=torch.float64, device="cuda") for _ in range(2))
+        for j in range(topk):
+            c = torch.where(on[:, j], w[:, j].double() if weights is not None else 1.0, 0.0)[:, None]
+            v = torch.where(on[:, j, None], rows[at[:, j]].double(), 0.0) * c
+            total += v
+            mag += v.abs()
+        got = b.moe_combine(view, dslots, weights) if weights is not None else b.moe_dispatch_grad(view, dslots)
+        bound = (topk + 1) * 2.0 ** -24 * mag + ROUNDOFF[dt] * (total.abs() + 2.0 ** -20 * mag) + TINY[dt]
+        assert bool(((got.double() - total).abs() <= bound).all())
+
+    drows, dw = b.moe_combine_grad(dout, view, dslots, w,
+                                   torch.full((groups, capacity, width), 55.0, dtype=dt, device="cuda"))
+    want = torch.full((R, width), 55.0, dtype=torch.float64, device="cuda")
+    exact = w[on].double()[:, None] * dout[token[on]].double()
+    want[slots[on]] = exact
+    tol = torch.zeros_like(want)
+    tol[slots[on]] = (2.0 ** -23 + ROUNDOFF[dt]) * exact.abs() + TINY[dt]
+    assert bool(((drows.view(R, width).double() - want).abs() <= tol).all())
+    for j in range(topk):
+        r = torch.where(on[:, j, None], rows[at[:, j]].double(), 0.0)
+        d = dout.double()
+        assert bool(((dw[:, j].double() - (d * r).sum(1)).abs()
+                     <= (width + 2) * 2.0 ** -24 * (d.abs() * r.abs()).sum(1)).all())

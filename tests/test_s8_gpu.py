@@ -484,3 +484,52 @@ def test_counts_out_of_range_are_reported_without_a_sum_too(b, K):
             if bad < 0:
                 expect[at] = PRIOR
             assert torch.equal(out, expect)
+
+
+# From 608 rows on 152 SMs a warp takes a row of at most 256 pieces (of 16 or 4
+# bytes, or one element), and 128 threads a longer one, past 1024 pieces in a loop.
+@pytest.mark.parametrize("dtype", ["f32", "f16", "bf16"])
+@pytest.mark.parametrize("M,K", [(611, 100), (1003, 1023), (1001, 1), (2000, 64), (700, 8200), (650, 40000), (613, 257)])
+def test_quantize_many_rows(b, M, K, dtype):
+    g = torch.Generator().manual_seed(M + K)
+    x = (torch.randn((M, K), generator=g) * torch.exp(3 * torch.randn((M, 1), generator=g))).to(TORCH[dtype])
+    x[7] = 0.0
+    x[8, K // 2] = float("inf")
+    x[M - 1, K // 3] = float("nan")
+    x[M - 2] = torch.sign(x[M - 2].float()).to(x.dtype) * 5e-8
+    x[M - 3, 0] = torch.finfo(x.dtype).max
+    want_q, want_s = quantize_reference(x)
+    for pitch, out_pitch in ((K, K), (up(K, 16), up(K, 16)), (K + 2, K + 5), (K + 1, up(K, 4))):
+        dx, _ = padded(x, pitch, fill=float("nan"))
+        buf = torch.full((M, out_pitch), 33, dtype=torch.int8, device="cuda")
+        q, s = b.quantize_rows(dx, q=buf[:, :K])
+        assert np.array_equal(q.cpu().numpy(), want_q)
+        assert np.array_equal(s.cpu().numpy(), want_s, equal_nan=True)
+        assert bool((buf[:, K:] == 33).all())
+
+
+@pytest.mark.parametrize("M,K", [(9, 64), (70, 1408), (90, 5000)])
+def test_quantize_experts_rows_with_counts(b, M, K):
+    """Kernels of each size, with counts of every kind."""
+    groups = 70
+    g = torch.Generator().manual_seed(M)
+    x = torch.randn((groups, M, K), generator=g).half()
+    rows = torch.randint(-2, M + 3, (groups,), generator=g, dtype=torch.int32)
+    q = torch.full((groups, M, K), 55, dtype=torch.int8, device="cuda")
+    s = torch.full((groups, M), -1.0, device="cuda")
+    b.quantize_rows(x.cuda(), rows.cuda(), q, s)
+    want_q, want_s = quantize_reference(x)
+    q, s = q.cpu().numpy(), s.cpu().numpy()
+    for e, r in enumerate(rows.clamp(0, M).tolist()):
+        assert np.array_equal(q[e, :r], want_q[e, :r]) and np.array_equal(s[e, :r], want_s[e, :r])
+        assert (q[e, r:] == 55).all() and (s[e, r:] == -1).all()
+
+
+def test_large_operands_of_any_pitch(b):
+    """Packed copies of more than one grid's bytes, at every byte offset."""
+    M, N, K = 1030, 4099, 5003
+    A, B = codes((M, K), 25), codes((K, N), 26)
+    want = b.gemm_s8(padded(A, up(K, 16))[0], padded(B, up(N, 16))[0])
+    for oa, ob in ((0, 0), (1, 2), (2, 3), (3, 1)):
+        assert torch.equal(b.gemm_s8(padded(A, K, oa)[0], padded(B, N, ob)[0]), want)
+    assert np.array_equal(want[::97].cpu().numpy(), sums(A[::97], B).astype(np.float32))
