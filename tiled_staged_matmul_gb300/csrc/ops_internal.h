@@ -137,7 +137,8 @@ struct S8Params {
     int32_t vec_c;              // C's rows are 16-byte aligned
     int32_t *partial;           // sums of pieces: two slots per worker
     unsigned long long *arrivals;  // one word per part of a shared tile: launch tag, count
-    unsigned long long tag;     // 48 bits, unique to the launch
+    unsigned long long tag;     // 48 bits of a hash of the launch's number (a word's old contents have them by
+                                // chance once in 2^48)
 };
 
 // The kernels: few rows (up to 16 or 32, 256 columns a tile); tiled, one CTA per

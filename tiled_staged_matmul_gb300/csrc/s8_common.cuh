@@ -206,58 +206,4 @@ __device__ __forceinline__ bool s8_wait(uint32_t bar, uint32_t parity, uint32_t 
     }
 }
 
-// Add a chunk's f32 sums (HC columns of a TMEM lane) to the lane's integers.
-// 1.5 * 2^23 + f has f + kMagicBits as its bits while |f| < 2^22, so an
-// addition and an integer addition do what a conversion does at an eighth of
-// their rate (8192^3: 744 -> 7xx us).  A sum can reach 2^24, though it takes
-// codes near the limits with one sign to do so: where one of a warp's passes
-// 2^22, the warp converts those eight columns.  Eight columns are on their way
-// while eight are added.
-constexpr uint32_t kMagicBits = 0x4b400000u;  // of 1.5 * 2^23
-
-template <int HC>
-__device__ __forceinline__ void add_chunk(uint32_t acc, int32_t (&sum)[HC])
-{
-    const float magic = __uint_as_float(kMagicBits);
-    uint32_t r[2][8];
-    ptx::tmem_ld_32x32b_x8(acc, r[0]);
-#pragma unroll
-    for (int c = 0; c < HC / 8; ++c) {
-        ptx::tmem_wait_ld(r[c & 1]);
-        if (c + 1 < HC / 8)
-            ptx::tmem_ld_32x32b_x8(acc + 8u * (c + 1), r[(c + 1) & 1]);
-        float f[8];
-#pragma unroll
-        for (int j = 0; j < 8; ++j)
-            f[j] = __uint_as_float(r[c & 1][j]);
-        const float top = ptx::max_abs3(ptx::max_abs3(ptx::max_abs3(f[0], f[1], f[2]), f[3], f[4]), f[5],
-                                        ptx::max_abs3(f[6], f[7], 0.f));
-        if (__any_sync(0xffffffffu, top >= 4194304.f)) {
-#pragma unroll
-            for (int j = 0; j < 8; ++j)
-                sum[8 * c + j] += __float2int_rn(f[j]) + int32_t(kMagicBits);
-        } else {
-#pragma unroll
-            for (int j = 0; j < 8; ++j)
-                sum[8 * c + j] += __float_as_int(f[j] + magic);
-        }
-    }
-}
-
-// Arrive on a barrier of the pair's leader.  Released to the CTA only: what the
-// arrival stands for is complete in this SM before it is sent -- f16 in its own
-// shared memory (the proxy fence) or TMEM (the store wait), or TMEM read out
-// (the load wait) -- and is next touched by this SM's own tensor core.
-// Released to the cluster, every arrival would first wait for the warp's other
-// stores, global ones included: measured 1.34 times the whole kernel's time at
-// 8192^3 (1028 against 770 us).
-template <bool PAIR>
-__device__ __forceinline__ void arrive_leader(uint32_t bar)
-{
-    if constexpr (PAIR)
-        ptx::mbar_arrive_remote(bar);
-    else
-        ptx::mbar_arrive(bar);
-}
-
 }  // namespace tsm

@@ -99,8 +99,17 @@ struct S8Plan {
     bool make(const S8Params &p, int sms, const S8Capacity &cap)
     {
         *this = {};
-        // Few rows by M; in groups of up to 32 rows most have far fewer, so those
-        // are cut into sixteens and only the rows there are cost anything.
+        // Few rows by M.  As few rows and as tiles, us: 16 x 4096 x 4096 10.5 and
+        // 16.2, 16 x 14336 x 4096 18.1 and 26.1, 32 x 1024 x 1024 8.8 and 9.9, 32 x
+        // 4096 x 4096 13.0 and 16.2, 32 x 57344 x 8192 121 and 130, 32 x 14336 x 4096
+        // 26.4 and 25.9, 32 x 4096 x 14336 28.3 and 27.2; the few-rows kernel holds
+        // no more than 32.
+        // In groups of up to 32 rows most have far fewer, so those are cut into
+        // sixteens and only the rows there are cost anything.  64 groups by 1408
+        // columns and 2048 k, as sixteens and as tiles: 192 rows in all 43.8 and
+        // 64.2, 16 each 49.9 and 64.9; but 32 each, which only the device knows, 89
+        // and 65.  Groups with room for more go to the tiles whatever their counts:
+        // 192 rows in all take 65 us where there is room for 33 to 128, 77 for 512.
         kind = p.M <= 16 || (p.group_rows && p.M <= 32) ? S8Kind::kFew16
                : p.M <= 32                              ? S8Kind::kFew32
                                                         : tiled_kind(p, sms);
