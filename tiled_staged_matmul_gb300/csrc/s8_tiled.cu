@@ -27,8 +27,8 @@ constexpr int kChunkBlocks = 8;  // k-blocks of 128 whose sums the f32 accumulat
 //                columns: accumulator -> 32-bit sums, then the epilogue (with
 //                two per lane quarter, half the columns each, a chunk took 1.05
 //                us to add up and 8192^3 665 us, not 647)
-// Measured: 8192^3 647 us (1.70 PFLOP/s, 0.89 of the f16 rate measured with
-// cuBLAS), 4096 x 14336 x 4096 304 us (0.83), 97 x 14333 x 4095 with one CTA a
+// Measured: 8192^3 651 us (1.69 PFLOP/s, 0.89 of the f16 rate measured with
+// cuBLAS), 4096 x 14336 x 4096 305 us (0.83), 97 x 14333 x 4095 with one CTA a
 // tile 28 us.
 //
 // The bound is shared-memory bandwidth: a 256 x 256 x 128 block costs an SM
