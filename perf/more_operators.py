@@ -399,7 +399,7 @@ def _run_own(s):
     b = lib.Fp4Rows(*s["B"], block)
     if op == "experts":
         return lib.grouped_gemm_fp4(lib.Fp4Rows(*s["A"], block), b, s["counts"], s["out"], activation=s["act"])
-    a = lib.Fp4Rows(*s["A"], block) if op == "product" else lib.quantize_rows_fp4(s["x"], block=block)
+    a = lib.Fp4Rows(*s["A"], block) if op == "product" else lib.quantize_fp4(s["x"], block=block)
     return lib.gemm_fp4(a, b, s["out"], bias=s["bias_v"], activation=s["act"])
 
 
