@@ -390,6 +390,43 @@ gemm_status_t moe_combine_rows_grad(const void *dout, const void *rows_in, int32
                                int64_t ld_dout, int64_t ld_rows, int64_t ld_drows,
                                gemm_stream_t stream);
 
+/* Which experts each token takes, and with what weight: what moe_route_slots
+ * takes as expert_ids and moe_combine_rows as weights.  For token t with logits
+ * x[0 ... experts):
+ *     s = softmax(x), or sigmoid(x) of each;   c = s + bias   (bias NULL: c = s)
+ *     of `groups` groups of experts / groups consecutive experts, the keep_groups with the
+ *     largest sums of their group_best (1 or 2) largest c are kept;
+ *     ids[t * topk + j] = the expert with the j-th largest c in the kept groups
+ *     weights[t * topk + j] = scale * s[id], or renormalised scale * s[id] / sum over the topk of s
+ * Equal values go to the lower number.  The bias takes part in the choice only.
+ * The choice is that of exact arithmetic (f64 where f32 cannot tell two values
+ * apart); the weights are formed in f32.
+ * An expert whose logit or bias is -infinity is not there: it is never chosen and
+ * adds nothing to its group's sum.  Where fewer than topk are there to choose
+ * from, the remaining ids are -1 (which moe_route_slots drops) and their weights
+ * 0.  A token with a NaN (in a logit or the bias), or with a logit of +infinity under
+ * softmax, gets the ids 0 ... topk - 1 and NaN weights, so that what it becomes is NaN.
+ *   logits   device, tokens rows of `experts` values of elem_type, ld apart
+ *   bias     NULL, or device, experts f32
+ *   ids      device, tokens x topk int32, written
+ *   weights  device, tokens x topk f32, written
+ * experts <= 1024 (512 where groups is no power of two), topk <= 32 and at most
+ * experts, groups <= 32 and a divisor of experts. */
+typedef enum moe_score { MOE_SCORE_SOFTMAX = 0, MOE_SCORE_SIGMOID = 1 } moe_score_t;
+gemm_status_t choose_experts(const void *logits, int32_t elem_type, const float *bias, int32_t *ids, float *weights,
+                                 int64_t tokens, int64_t experts, int64_t topk, int64_t ld, int32_t score, int64_t groups,
+                                 int64_t keep_groups, int32_t group_best, int32_t renormalize, float scale,
+                                 gemm_stream_t stream);
+
+/* The gradient of choose_experts' weights, for the ids it chose (an id
+ * outside [0, experts) takes no part; an id that comes twice counts twice):
+ *     dlogits[t][e] = sum over j of dweights[t * topk + j] * d weights[t * topk + j] / d x[e]
+ * formed in f32 and rounded once to elem_type.  The choice itself has no
+ * gradient, nor has the bias.  dlogits (tokens rows, ld_d apart) is written whole. */
+gemm_status_t choose_experts_grad(const float *dweights, const void *logits, int32_t elem_type, const int32_t *ids,
+                                      void *dlogits, int64_t tokens, int64_t experts, int64_t topk, int64_t ld, int64_t ld_d,
+                                      int32_t score, int32_t renormalize, float scale, gemm_stream_t stream);
+
 /* ---------------------------------------------------------------- 8-bit integers */
 
 /* Quantise rows to 8-bit integers, symmetrically:
@@ -444,6 +481,73 @@ gemm_status_t gemm_s8_grouped_scaled(const int8_t *A, const int8_t *B, void *C, 
                                      int64_t strideA, int64_t strideB, int64_t strideC,
                                      int64_t scale_a_stride, int64_t scale_b_stride,
                                      const gemm_epilogue_t *epi, gemm_stream_t stream);
+
+/* ---------------------------------------------------------------- 4-bit floating point
+ *
+ * Microscaled rows: e2m1 codes (sign, 0, 1/2, 1, 3/2, 2, 3, 4, 6) along k, two to a
+ * byte (the even k in the low half), and a scale for every block of 16 or 32 of a row:
+ *   block 16  e4m3 scales, and an f32 scale per row
+ *   block 32  powers of two (e8m0), nothing else
+ * Both operands of a product are such rows: A has M of them, B has N (a weight
+ * matrix as [outputs][inputs], the transpose of the other calls' B).
+ * A row takes ceil(K / 2) bytes; with an odd K the last byte's high half is 0.
+ * Block scales lie in tiles of 512 bytes, 128 rows by 4 blocks: the scale of row i and
+ * block b at byte  16 * (i % 32) + 4 * (i % 128 / 32) + b % 4  of tile
+ * [i / 128][b / 4];  ceil(rows / 128) x ceil(ceil(K / block) / 4) tiles a matrix, row by row,
+ * the matrices of a batch one after another.  Scales of rows that are not there
+ * are not read into any result; those of blocks past the row's last must not be
+ * NaN (fp4_quantize_rows writes 0). */
+
+/* Quantise rows to 4-bit floating point.  Roundings are to nearest, ties to even,
+ * each of the exact quotient.
+ *   block 16:  scales[i] = 2^e, the smallest (e >= -126) with max over k of |X[i][k]| <= 2688 * 2^e
+ *              (2688 = 6 * 448, the largest code and scale); 0 for a row of zeros
+ *              block scale = max of the block / (6 * scales[i]), rounded to e4m3
+ *              code = X / (block scale * scales[i]), rounded to e2m1, at most 6 (0 where the scale is)
+ *   block 32:  block scale = 2^e, e = max(floor(log2(max of the block)) - 2, -127)
+ *              code = X / 2^e, rounded to e2m1, at most 6
+ * A NaN or an infinity: the row's scale (block 16) is NaN and its codes 0, or the
+ * block's scale (block 32) is, so that its products come out NaN.
+ *   X             device, batch matrices of M rows of K values of elem_type, ldx / strideX apart
+ *   q             device, written, ldq / strideQ bytes apart (ldq a multiple of 16 suits the products)
+ *   block_scales  device, written as described above (16-byte aligned)
+ *   scales        block 16: device, batch x M f32, scale_stride apart, written; block 32: not used
+ *   group_rows    NULL, or device, batch int32: only the first group_rows[b] rows of matrix b are
+ *                 read and written (the grouped calls' counts) */
+gemm_status_t fp4_quantize_rows(const void *X, int32_t elem_type, int32_t block, uint8_t *q, uint8_t *block_scales,
+                                float *scales, const int32_t *group_rows, int64_t M, int64_t K, int64_t ldx, int64_t ldq,
+                                int64_t strideX, int64_t strideQ, int64_t scale_stride, int64_t batch,
+                                gemm_stream_t stream);
+
+/* C[i][j] = act(alpha * scale_a[i] * scale_b[j] * S[i][j] + bias[j]),
+ * S[i][j] = sum over k of A[i][k] * sa[i][k / block] * B[j][k] * sb[j][k / block], accumulated in f32
+ * by the tensor cores.  S is multiplied by alpha * scale_a[i], then by scale_b[j] with
+ * bias[j] added in one rounding, and rounded once to the output type.
+ *   A, B            device, M and N rows of codes, lda / strideA and ldb / strideB bytes apart
+ *   block_scales_a, block_scales_b  device, 16-byte aligned, as described above
+ *   C               device, M rows of N values of epi->out_type (f32 without epi), row stride ldc;
+ *                   written, never read; elements of a row past N are left untouched
+ *   scale_a         device, M f32 values per matrix, scale_a_stride apart (NULL: ones)
+ *   scale_b         device, N f32 values per matrix, scale_b_stride apart (NULL: ones)
+ *   epi             as for gemm_f16_fused; NULL: f32, no bias, no activation
+ * Any pitch and base of A, B and C is accepted; A and B with 16-byte aligned bases,
+ * pitches and batch strides are read in place, others are first copied to such a
+ * layout.  K <= 2^23; K == 0 gives act(bias[j]) in every cell.  A call is bitwise
+ * reproducible; the order of its sums depends on its sizes.  Other errors as for
+ * gemm_f16_f32acc_batched. */
+gemm_status_t gemm_fp4_scaled(const uint8_t *A, const uint8_t *B, void *C, const uint8_t *block_scales_a,
+                              const uint8_t *block_scales_b, const float *scale_a, const float *scale_b, int32_t block,
+                              int64_t M, int64_t N, int64_t K, int64_t lda, int64_t ldb, int64_t ldc, int64_t strideA,
+                              int64_t strideB, int64_t strideC, int64_t scale_a_stride, int64_t scale_b_stride,
+                              int64_t batch, const gemm_epilogue_t *epi, gemm_stream_t stream);
+
+/* The grouped (Mixture-of-Experts) form, as gemm_s8_grouped_scaled. */
+gemm_status_t gemm_fp4_grouped_scaled(const uint8_t *A, const uint8_t *B, void *C, const uint8_t *block_scales_a,
+                                      const uint8_t *block_scales_b, const float *scale_a, const float *scale_b,
+                                      int32_t block, const int32_t *group_rows, int64_t groups, int64_t M, int64_t N,
+                                      int64_t K, int64_t lda, int64_t ldb, int64_t ldc, int64_t strideA, int64_t strideB,
+                                      int64_t strideC, int64_t scale_a_stride, int64_t scale_b_stride,
+                                      const gemm_epilogue_t *epi, gemm_stream_t stream);
 
 /* The plan the library would use, computed on the host only (no GPU is
  * touched).  num_sms is the SM count to plan for (0 = the current device's).

@@ -12,6 +12,7 @@ from __future__ import annotations
 
 import ctypes
 import os
+import typing
 
 from .csrc import build as _build
 
@@ -36,6 +37,7 @@ class GemmOptions(ctypes.Structure):
 
 ACTIVATIONS = {"none": 0, "relu": 1, "leaky_relu": 2, "gelu": 3, "gelu_tanh": 4, "silu": 5}
 OUT_TYPES = {"f32": 0, "f16": 1, "bf16": 2}
+MOE_SCORES = {"softmax": 0, "sigmoid": 1}
 
 
 class GemmEpilogue(ctypes.Structure):
@@ -140,6 +142,19 @@ def _load() -> ctypes.CDLL:
     lib.gemm_s8_grouped_scaled.restype = ctypes.c_int
     lib.gemm_s8_grouped_scaled.argtypes = [vp, vp, vp, vp, vp, vp, i64, i64, i64, i64, i64, i64, i64, i64,
                                            i64, i64, i64, i64, ctypes.POINTER(GemmEpilogue), vp]
+    f32 = ctypes.c_float
+    lib.choose_experts.restype = ctypes.c_int
+    lib.choose_experts.argtypes = [vp, i32, vp, vp, vp, i64, i64, i64, i64, i32, i64, i64, i32, i32, f32, vp]
+    lib.choose_experts_grad.restype = ctypes.c_int
+    lib.choose_experts_grad.argtypes = [vp, vp, i32, vp, vp, i64, i64, i64, i64, i64, i32, i32, f32, vp]
+    lib.fp4_quantize_rows.restype = ctypes.c_int
+    lib.fp4_quantize_rows.argtypes = [vp, i32, i32, vp, vp, vp, vp, i64, i64, i64, i64, i64, i64, i64, i64, vp]
+    lib.gemm_fp4_scaled.restype = ctypes.c_int
+    lib.gemm_fp4_scaled.argtypes = [vp, vp, vp, vp, vp, vp, vp, i32, i64, i64, i64, i64, i64, i64, i64, i64, i64, i64,
+                                    i64, i64, ctypes.POINTER(GemmEpilogue), vp]
+    lib.gemm_fp4_grouped_scaled.restype = ctypes.c_int
+    lib.gemm_fp4_grouped_scaled.argtypes = [vp, vp, vp, vp, vp, vp, vp, i32, vp, i64, i64, i64, i64, i64, i64, i64, i64,
+                                            i64, i64, i64, i64, ctypes.POINTER(GemmEpilogue), vp]
     lib.gemm_f16_f32acc_splitk_noalloc.restype = ctypes.c_int
     lib.gemm_f16_f32acc_splitk_noalloc.argtypes = [vp, vp, vp, i64, i64, i64, i64, i64, i64,
                                                    i32, vp]
@@ -264,6 +279,42 @@ def gemm_s8_grouped_scaled(A, B, C, scale_a, scale_b, group_rows, groups, M, N, 
     e = ctypes.byref(epi) if epi is not None else None
     return _lib.gemm_s8_grouped_scaled(A, B, C, scale_a, scale_b, group_rows, groups, M, N, K, lda, ldb, ldc,
                                        strideA, strideB, strideC, scale_a_stride, scale_b_stride, e, stream)
+
+
+def choose_experts(logits, elem_type, bias, ids, weights, tokens, experts, topk, ld, score=0, groups=1,
+                       keep_groups=1, group_best=2, renormalize=False, scale=1.0, stream=0) -> int:
+    return _lib.choose_experts(logits, OUT_TYPES.get(elem_type, elem_type), bias, ids, weights, tokens, experts, topk,
+                                   ld, MOE_SCORES.get(score, score), groups, keep_groups, group_best, renormalize, scale,
+                                   stream)
+
+
+def choose_experts_grad(dweights, logits, elem_type, ids, dlogits, tokens, experts, topk, ld, ld_d, score=0,
+                            renormalize=False, scale=1.0, stream=0) -> int:
+    return _lib.choose_experts_grad(dweights, logits, OUT_TYPES.get(elem_type, elem_type), ids, dlogits, tokens,
+                                        experts, topk, ld, ld_d, MOE_SCORES.get(score, score), renormalize, scale, stream)
+
+
+def fp4_quantize_rows(X, elem_type, block, q, block_scales, scales, group_rows, M, K, ldx, ldq, strideX=0, strideQ=0,
+                          scale_stride=0, batch=1, stream=0) -> int:
+    return _lib.fp4_quantize_rows(X, OUT_TYPES.get(elem_type, elem_type), block, q, block_scales, scales, group_rows, M,
+                                  K, ldx, ldq, strideX, strideQ, scale_stride, batch, stream)
+
+
+def gemm_fp4_scaled(A, B, C, block_scales_a, block_scales_b, scale_a, scale_b, block, M, N, K, lda, ldb, ldc, strideA=0,
+                    strideB=0, strideC=0, scale_a_stride=0, scale_b_stride=0, batch=1, epi: GemmEpilogue | None = None,
+                    stream=0) -> int:
+    e = ctypes.byref(epi) if epi is not None else None
+    return _lib.gemm_fp4_scaled(A, B, C, block_scales_a, block_scales_b, scale_a, scale_b, block, M, N, K, lda, ldb, ldc,
+                                strideA, strideB, strideC, scale_a_stride, scale_b_stride, batch, e, stream)
+
+
+def gemm_fp4_grouped_scaled(A, B, C, block_scales_a, block_scales_b, scale_a, scale_b, block, group_rows, groups, M, N, K,
+                            lda, ldb, ldc, strideA, strideB, strideC, scale_a_stride=0, scale_b_stride=0,
+                            epi: GemmEpilogue | None = None, stream=0) -> int:
+    e = ctypes.byref(epi) if epi is not None else None
+    return _lib.gemm_fp4_grouped_scaled(A, B, C, block_scales_a, block_scales_b, scale_a, scale_b, block, group_rows,
+                                        groups, M, N, K, lda, ldb, ldc, strideA, strideB, strideC, scale_a_stride,
+                                        scale_b_stride, e, stream)
 
 
 def gemm_plan(M, N, K, batch=1, opts: GemmOptions | None = None, num_sms=0) -> dict:
@@ -574,6 +625,70 @@ def moe_route(expert_ids, groups, capacity, *, stream=None):
     return slots, counts
 
 
+def moe_choose(logits, topk, *, score="softmax", bias=None, groups=1, keep_groups=1, group_best=2, renormalize=False,
+               scale=1.0, stream=None):
+    """The experts that a router's logits choose for each token: ``(ids,
+    weights)``, tokens x topk, int32 and f32.
+
+    ``logits`` is tokens x experts (f32, f16 or bf16; rows may be padded).  The
+    scores are their softmax or sigmoid; ``bias`` (f32, one per expert) is added
+    for the choice only.  With ``groups`` the experts are chosen from the
+    ``keep_groups`` groups with the largest sums of their ``group_best`` (1 or 2)
+    best.  Weights are the chosen scores, divided by their sum with
+    ``renormalize``, times ``scale``.  Equal values go to the lower number; a
+    logit of -infinity hides an expert, and a choice that finds none has the id
+    -1 and the weight 0."""
+    import torch
+    if stream is not None:
+        return _on_stream(stream, moe_choose, logits, topk, score=score, bias=bias, groups=groups, keep_groups=keep_groups,
+                          group_best=group_best, renormalize=renormalize, scale=scale)
+    code = _elem_type(logits.dtype)
+    if logits.dim() != 2:
+        raise ValueError("logits must be a tokens x experts tensor")
+    T, E = logits.shape
+    ld = _token_pitch(logits, T, E, logits.dtype, "logits")
+    if bias is not None and (bias.dtype != torch.float32 or not bias.is_cuda or bias.shape != (E,)
+                             or not bias.is_contiguous()):
+        raise ValueError("bias must be a contiguous CUDA float32 tensor of one value per expert")
+    if score not in MOE_SCORES:
+        raise ValueError(f"score must be one of {', '.join(MOE_SCORES)}")
+    ids = torch.empty((T, topk), dtype=torch.int32, device=logits.device)
+    weights = torch.empty((T, topk), dtype=torch.float32, device=logits.device)
+    check(_lib.choose_experts(logits.data_ptr(), code, 0 if bias is None else bias.data_ptr(), ids.data_ptr(),
+                                  weights.data_ptr(), T, E, topk, ld, MOE_SCORES[score], groups, keep_groups, group_best,
+                                  renormalize, scale, _stream_handle(stream)))
+    return ids, weights
+
+
+def moe_choose_grad(dweights, logits, ids, out=None, *, score="softmax", renormalize=False, scale=1.0, stream=None):
+    """The gradient of ``moe_choose``'s weights towards the logits (tokens x
+    experts, in their type), for the ``ids`` it chose."""
+    import torch
+    if out is None and stream is not None:
+        return _on_stream(stream, moe_choose_grad, dweights, logits, ids, score=score, renormalize=renormalize, scale=scale)
+    code = _elem_type(logits.dtype)
+    if logits.dim() != 2:
+        raise ValueError("logits must be a tokens x experts tensor")
+    T, E = logits.shape
+    ld = _token_pitch(logits, T, E, logits.dtype, "logits")
+    if ids.dtype != torch.int32 or not ids.is_cuda or ids.dim() != 2 or ids.shape[0] != T or not ids.is_contiguous():
+        raise ValueError("ids must be a contiguous CUDA int32 tensor of tokens x topk values")
+    if dweights.dtype != torch.float32 or not dweights.is_cuda or dweights.shape != ids.shape \
+            or not dweights.is_contiguous():
+        raise ValueError("dweights must be a contiguous CUDA float32 tensor of tokens x topk values")
+    if score not in MOE_SCORES:
+        raise ValueError(f"score must be one of {', '.join(MOE_SCORES)}")
+    if out is None:
+        out = torch.empty((T, E), dtype=logits.dtype, device=logits.device)
+        ldo = E
+    else:
+        ldo = _token_pitch(out, T, E, logits.dtype, "out")
+    check(_lib.choose_experts_grad(dweights.data_ptr(), logits.data_ptr(), code, ids.data_ptr(), out.data_ptr(), T, E,
+                                       ids.shape[1], ld, ldo, MOE_SCORES[score], renormalize, scale,
+                                       _stream_handle(stream)))
+    return out
+
+
 def moe_dispatch(x, slots, groups, capacity, out=None, *, stream=None):
     """Copy token rows to their experts: ``out[e, r] = x[t]`` where
     ``slots[t, j] == e * capacity + r``.
@@ -809,6 +924,150 @@ def grouped_gemm_s8(A, B, scale_a, scale_b, group_rows, out=None, *, alpha=1.0, 
             or group_rows.numel() != A.shape[0] or not group_rows.is_contiguous():
         raise ValueError("A must be 3-D and group_rows a contiguous CUDA int32 tensor of one count per group")
     return _s8_call(A, B, scale_a, scale_b, group_rows, out, alpha, bias, activation, slope, out_dtype, stream)
+
+
+# 4-bit floating point.
+
+class Fp4Rows(typing.NamedTuple):
+    """Microscaled 4-bit rows, as ``quantize_fp4`` returns them: ``codes`` (M
+    x K / 2 uint8, or batch x M x K / 2), ``block_scales`` (uint8 tiles, ...
+    x ceil(M / 128) x ceil(blocks / 4) x 512), ``scales`` (f32, one per row, or
+    None) and ``block``, 16 or 32."""
+    codes: object
+    block_scales: object
+    scales: object
+    block: int
+
+
+def quantize_fp4(X, group_rows=None, *, block=16, stream=None):
+    """Quantise the rows of an M x K (or batch x M x K) CUDA tensor (f32, f16 or
+    bf16) to 4-bit floating point with a scale per block of 16 (e4m3, and an f32
+    scale per row) or 32 (powers of two): an ``Fp4Rows``.
+
+    The codes' rows have a pitch of a multiple of 16 bytes, as the products want.
+    ``group_rows`` (int32, one count per matrix) limits the rows that are read
+    and written."""
+    import torch
+    if stream is not None:
+        return _on_stream(stream, quantize_fp4, X, group_rows, block=block)
+    code = _elem_type(X.dtype)
+    if block not in (16, 32):
+        raise ValueError("block must be 16 or 32")
+    shape = X.shape
+    three = len(shape) == 3
+    if three:
+        batch, M, K = shape
+        sX, ldx, unit = X.stride()
+    elif len(shape) == 2:
+        batch, (M, K), sX = 1, shape, 0
+        ldx, unit = X.stride()
+    if len(shape) not in (2, 3) or not X.is_cuda or (unit != 1 and K > 1 and X.numel()):
+        raise ValueError("X must be a 2-D or 3-D CUDA tensor with a unit last stride")
+    counts = 0
+    if group_rows is not None:
+        if group_rows.dtype != torch.int32 or not group_rows.is_cuda or group_rows.numel() != batch \
+                or not group_rows.is_contiguous():
+            raise ValueError("group_rows must be a contiguous CUDA int32 tensor of one count per matrix")
+        counts = group_rows.data_ptr()
+    width = (K + 1) // 2
+    ldq = width + -width % 16
+    sQ = M * ldq
+    tiles = (-(-M // 128), -(-K // (4 * block)), 512)
+    q = torch.empty_strided((batch, M, width) if three else (M, width), (sQ, ldq, 1) if three else (ldq, 1),
+                            dtype=torch.uint8, device=X.device)
+    s = torch.empty((batch, *tiles) if three else tiles, dtype=torch.uint8, device=X.device)
+    r = torch.empty((batch, M) if three else (M,), dtype=torch.float32, device=X.device) if block == 16 else None
+    check(_lib.fp4_quantize_rows(X.data_ptr(), code, block, q.data_ptr(), s.data_ptr(), 0 if r is None else r.data_ptr(),
+                                 counts, M, K, ldx if M > 1 else K, ldq, sX, sQ, M, batch, _stream_handle(stream)))
+    return Fp4Rows(q, s, r, block)
+
+
+def _fp4_operand(x, name):
+    """(batch or None, rows, bytes of a row, pitch, stride) of an Fp4Rows."""
+    import torch
+    codes, tiles = x.codes, x.block_scales
+    if codes.dtype != torch.uint8 or tiles.dtype != torch.uint8:
+        raise TypeError(f"{name}'s codes and block scales must be torch.uint8")
+    if x.block not in (16, 32):
+        raise ValueError(f"{name}'s block must be 16 or 32")
+    shape = codes.shape
+    if len(shape) == 3:
+        batch, rows, width = shape
+        stride, ld, unit = codes.stride()
+        want = (batch, -(-rows // 128), -(-width // (2 * x.block)), 512)
+    elif len(shape) == 2:
+        batch, stride = None, 0
+        rows, width = shape
+        ld, unit = codes.stride()
+        want = (-(-rows // 128), -(-width // (2 * x.block)), 512)
+    else:
+        raise ValueError(f"{name}'s codes must be 2-D or 3-D")
+    if not codes.is_cuda or (unit != 1 and width > 1 and codes.numel()):
+        raise ValueError(f"{name}'s codes must be a CUDA tensor with a unit last stride")
+    if tiles.shape != want or not tiles.is_cuda or not tiles.is_contiguous():
+        raise ValueError(f"{name}'s block scales must be a contiguous {' x '.join(map(str, want))} CUDA tensor")
+    return batch, rows, width, ld if rows > 1 else max(width, 1), stride
+
+
+def _fp4_call(a, b, group_rows, out, alpha, bias, activation, slope, out_dtype, stream):
+    import torch
+    if out is None and stream is not None:
+        return _on_stream(stream, _fp4_call, a, b, group_rows, None, alpha, bias, activation, slope, out_dtype, None)
+    batch, M, width, lda, sA = _fp4_operand(a, "a")
+    batch_b, N, width_b, ldb, sB = _fp4_operand(b, "b")
+    if a.block != b.block:
+        raise ValueError(f"blocks of {a.block} and of {b.block}")
+    if batch != batch_b:
+        raise ValueError("batch sizes differ")
+    if width != width_b:
+        raise ValueError(f"inner sizes differ: {2 * width} vs {2 * width_b}")
+    three = batch is not None
+    n = batch if three else 1
+    shape = (batch, M, N) if three else (M, N)
+    if out is None:
+        make = torch.empty if group_rows is None else torch.zeros
+        out = make(shape, dtype=out_dtype or torch.float32, device=a.codes.device)
+    if out.shape != shape:
+        raise ValueError(f"out must be a {' x '.join(map(str, shape))} tensor")
+    sC, ldc, uC = out.stride() if three else (0, *out.stride())
+    if not out.is_cuda or (uC != 1 and N > 1 and out.numel()):
+        raise ValueError("out must be a CUDA tensor with a unit last stride")
+    pa, sa = _s8_vector(a.scales, M, n, three, "a.scales")
+    pb, sb = _s8_vector(b.scales, N, n, three, "b.scales")
+    pbias, sbias = _s8_vector(bias, N, n, three, "bias")
+    code = _elem_type(out.dtype)
+    epi = None  # (none: alpha 1, no bias or activation, f32)
+    if code or pbias or alpha != 1 or activation != "none":
+        epi = ctypes.byref(GemmEpilogue(alpha, pbias or None, sbias, ACTIVATIONS.get(activation, activation), slope,
+                                        code))
+    args = (M, N, 2 * width, lda, ldb, ldc if M > 1 else max(N, 1), sA, sB, sC, sa, sb)
+    head = (a.codes.data_ptr(), b.codes.data_ptr(), out.data_ptr(), a.block_scales.data_ptr(), b.block_scales.data_ptr(),
+            pa, pb, a.block)
+    if group_rows is None:
+        check(_lib.gemm_fp4_scaled(*head, *args, n, epi, _stream_handle(stream)))
+    else:
+        check(_lib.gemm_fp4_grouped_scaled(*head, group_rows.data_ptr(), n, *args, epi, _stream_handle(stream)))
+    return out
+
+
+def gemm_fp4(a, b, out=None, *, alpha=1.0, bias=None, activation="none", slope=0.01, out_dtype=None, stream=None):
+    """``out = activation(alpha * (A @ B.T) + bias)`` for ``Fp4Rows`` a (M rows) and
+    b (N rows, a weight as [outputs, inputs]) of one block size, or a batch of
+    them; f32 accumulation.  ``out`` (M x N) is f32 unless ``out_dtype`` (or the
+    given ``out``) says torch.float16 / torch.bfloat16.  Returns ``out``."""
+    return _fp4_call(a, b, None, out, alpha, bias, activation, slope, out_dtype, stream)
+
+
+def grouped_gemm_fp4(a, b, group_rows, out=None, *, alpha=1.0, bias=None, activation="none", slope=0.01, out_dtype=None,
+                     stream=None):
+    """The grouped (Mixture-of-Experts) form of ``gemm_fp4``: a holds groups x M
+    rows, b groups x N; of group g the first ``group_rows[g]`` rows are computed,
+    the others keep the contents of ``out`` (zeros when not given)."""
+    import torch
+    if a.codes.dim() != 3 or group_rows.dtype != torch.int32 or not group_rows.is_cuda \
+            or group_rows.numel() != a.codes.shape[0] or not group_rows.is_contiguous():
+        raise ValueError("a must be 3-D and group_rows a contiguous CUDA int32 tensor of one count per group")
+    return _fp4_call(a, b, group_rows, out, alpha, bias, activation, slope, out_dtype, stream)
 
 
 def gemm_host(A_host, B_host, C_host, dA, dB, dC, stream=None):

@@ -3,7 +3,8 @@
 The translation units compile in parallel: the plain GEMM kernels and the
 cluster split-K sums, the fused-epilogue GEMM kernels once per activation
 (``gemm_epi.cu`` with ``-DTSM_EPI_ACT``), the row-reduction kernels, the
-expert token movement, the 8-bit integer products and the host API.  The kernel units are compiled with ``-Xptxas -v`` and the build
+expert token movement, the choice of experts once per type of the logits, the
+8-bit integer and the 4-bit products and the host API.  The kernel units are compiled with ``-Xptxas -v`` and the build
 fails if ptxas reports any spill stores or loads (only ptxas's printed
 summary is read).
 """
@@ -31,11 +32,13 @@ UNITS = ([("gemm_kernels.cu", "gemm_kernels", [])] +
          [("rowsum_kernels.cu", "rowsum_kernels", []), ("moe_kernels.cu", "moe_kernels", []),
           ("s8_kernels.cu", "s8_kernels", [])] +
          [("s8_tiled.cu", f"s8_tiled_{a}", [f"-DTSM_S8_ACT={i}"]) for i, a in enumerate(ACTIVATIONS)] +
-         [("gemm_api.cu", "gemm_api", []), ("ops_api.cu", "ops_api", [])])
-HOST_SOURCES = ("gemm_api.cu", "ops_api.cu")
+         [("choose_kernels.cu", f"choose_{t}", [f"-DTSM_CHOOSE_ELEM={i}"]) for i, t in enumerate(("f32", "f16", "bf16"))] +
+         [("fp4_quantize.cu", "fp4_quantize", []), ("fp4_product.cu", "fp4_product", [])] +
+         [("gemm_api.cu", "gemm_api", []), ("ops_api.cu", "ops_api", []), ("fp4_api.cu", "fp4_api", [])])
+HOST_SOURCES = ("gemm_api.cu", "ops_api.cu", "fp4_api.cu")
 SOURCES = sorted({u[0] for u in UNITS})
-HEADERS = ["api_internal.h", "gemm_internal.h", "gemm_kernel.cuh", "launch.cuh", "ops_internal.h", "ptx.cuh", "s8_common.cuh",
-           "s8_plan.h", "s8_ptx.cuh"]
+HEADERS = ["api_checks.h", "api_internal.h", "fp4_internal.h", "fp4_plan.h", "fp4_ptx.cuh", "gemm_internal.h",
+           "gemm_kernel.cuh", "launch.cuh", "ops_internal.h", "piece.cuh", "ptx.cuh", "s8_common.cuh", "s8_plan.h", "s8_ptx.cuh"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 
 

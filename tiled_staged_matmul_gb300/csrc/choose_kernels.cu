@@ -1,0 +1,529 @@
+// choose_kernels.cu -- the choice of experts and its gradient.
+//
+//   s = softmax(x) or sigmoid(x) over a token's logits x;  c = s + bias
+//   groups of experts are kept by the sum of their one or two largest c, then
+//   the topk largest c of the kept groups are chosen;  ties go to the lower number
+//   w_j = s[id_j] (/ sum_j s[id_j]) * scale
+//
+//   g_j = scale dw_j, or scale / S (dw_j - sum_i dw_i s_i / S) with S = sum_i s_i
+//   dx = s (ds - sum ds s) for the softmax, ds s (1 - s) for the sigmoid, ds_e = sum of
+//   the g_j with id_j = e
+//
+// A warp takes a token.  Scores are formed in f32, but which expert is chosen is
+// what it is in exact arithmetic: where two scores that decide something lie
+// within the bound of their f32 errors, the warp forms the token's scores again
+// in f64 and decides by those.  (Without a bias the logits themselves give the
+// order, exactly.)  With random logits one token in a thousand needs it.
+//
+// Bound by launch and instruction latency rather than by its bytes: some 300
+// instructions of a warp for a kilobyte.  Compiled once per type of the logits
+// (-DTSM_CHOOSE_ELEM, gemm_internal.h's kOut* values).
+#include "fp4_internal.h"
+#include "launch.cuh"
+#include "piece.cuh"
+
+#ifndef TSM_CHOOSE_ELEM
+#error "compile with -DTSM_CHOOSE_ELEM=<element type>"
+#endif
+
+namespace tsm {
+
+namespace {
+
+constexpr uint32_t kAll = 0xffffffffu;
+constexpr int kChooseWarps = 4;  // tokens of a block
+
+__device__ __forceinline__ bool is_nan(float v) { return v != v; }
+
+// A float's place in the order of floats, above 0 (which stands for none);
+// -0 as +0.
+__device__ __forceinline__ uint32_t order_of(float v)
+{
+    const uint32_t b = __float_as_uint(v + 0.f);
+    return b ^ (uint32_t(int32_t(b) >> 31) | 0x80000000u);
+}
+__device__ __forceinline__ uint64_t order_of(double v)
+{
+    const uint64_t b = uint64_t(__double_as_longlong(v + 0.0));
+    return b ^ (uint64_t(int64_t(b) >> 63) | (uint64_t(1) << 63));
+}
+
+__device__ __forceinline__ uint32_t warp_max(uint32_t v) { return __reduce_max_sync(kAll, v); }
+__device__ __forceinline__ uint64_t warp_max(uint64_t v)
+{
+    const uint32_t hi = __reduce_max_sync(kAll, uint32_t(v >> 32));
+    const uint32_t lo = __reduce_max_sync(kAll, uint32_t(v >> 32) == hi ? uint32_t(v) : 0u);
+    return (uint64_t(hi) << 32) | lo;
+}
+
+template <typename F>
+__device__ __forceinline__ F warp_sum(F v)
+{
+#pragma unroll
+    for (int d = 16; d; d >>= 1)
+        v += __shfl_xor_sync(kAll, v, d);
+    return v;
+}
+
+__device__ __forceinline__ float exp_of(float v) { return expf(v); }
+__device__ __forceinline__ double exp_of(double v) { return exp(v); }
+
+// An order's type.
+template <typename F>
+struct OrderOf {
+    using type = uint32_t;
+};
+template <>
+struct OrderOf<double> {
+    using type = uint64_t;
+};
+
+// Where a token's experts lie in its warp: L lanes to a group, VM experts to a
+// lane, so that lanes and a lane's experts are in ascending order.
+struct Layout {
+    int per;    // experts of a group
+    int L;      // lanes of a group (a power of two)
+    int group;  // this lane's
+    int first;  // this lane's first expert
+    int count;  // how many it has
+    __device__ __forceinline__ Layout(int experts, int groups, int vm, int lane)
+    {
+        per = experts / groups;
+        L = 32;
+        while (L * groups > 32)
+            L >>= 1;
+        group = lane / L;
+        const int at = lane % L * vm;
+        first = group * per + at;
+        count = group < groups ? max(0, min(vm, per - at)) : 0;
+    }
+};
+
+// A lane's logits; -infinity for what it has no expert for.
+template <int ET, int VM, bool WIDE>
+__device__ __forceinline__ void read_logits(const ChooseParams &p, int64_t token, const Layout &at, float (&x)[VM])
+{
+    constexpr int EB = ET == kOutF32 ? 4 : 2;
+    using E = Piece<ET, EB>;
+    const char *row = static_cast<const char *>(p.logits) + (token * p.ld + at.first) * EB;
+    if constexpr (WIDE && VM * EB >= 4) {
+        // (All of a lane's experts or none are there.)
+        using P = Piece<ET, VM * EB >= 16 ? 16 : 4>;
+#pragma unroll
+        for (int i = 0; i < VM / P::V; ++i) {
+            float v[P::V];
+#pragma unroll
+            for (int j = 0; j < P::V; ++j)
+                v[j] = __uint_as_float(0xff800000u);
+            if (at.count)
+                P::widen(P::get(row, i), v);
+#pragma unroll
+            for (int j = 0; j < P::V; ++j)
+                x[P::V * i + j] = v[j];
+        }
+    } else {
+#pragma unroll
+        for (int i = 0; i < VM; ++i) {
+            float v[1] = {__uint_as_float(0xff800000u)};
+            if (i < at.count)
+                E::widen(E::get(row, i), v);
+            x[i] = v[0];
+        }
+    }
+}
+
+template <int ET>
+__device__ __forceinline__ float logit_at(const ChooseParams &p, int64_t token, int e)
+{
+    constexpr int EB = ET == kOutF32 ? 4 : 2;
+    using E = Piece<ET, EB>;
+    float v[1];
+    E::widen(E::get(static_cast<const char *>(p.logits) + token * p.ld * EB, e), v);
+    return v[0];
+}
+
+// The warp's choice, formed in F.  Lane j ends with the j-th chosen expert, -1 where
+// there is none.  False: two f32 values that decide something are too close.
+template <typename F, int ET, int VM>
+__device__ __forceinline__ bool choose(const ChooseParams &p, int64_t token, const Layout &at, const float (&x)[VM], float top,
+                                       float total, int lane, int &id)
+{
+    using O = typename OrderOf<F>::type;
+    constexpr bool CHECK = sizeof(F) == 4;
+    const float none = __uint_as_float(0xff800000u);
+    const bool limited = p.keep < p.groups;
+    const bool by_score = p.bias || (limited && p.best > 1);
+    F sum = F(total);
+    if (!CHECK && by_score && !p.sigmoid) {
+        F mine = F(0);
+#pragma unroll
+        for (int i = 0; i < VM; ++i)
+            if (x[i] != none)
+                mine += exp_of(F(x[i]) - F(top));
+        sum = warp_sum(mine);
+    }
+    auto score = [&](float v) {
+        if (p.sigmoid)
+            return F(1) / (F(1) + exp_of(-F(v)));
+        return exp_of(F(v) - F(top)) / sum;
+    };
+    // Places in order, 0 where there is no expert to choose.
+    O c[VM];
+    float bias[VM];
+#pragma unroll
+    for (int i = 0; i < VM; ++i) {
+        bias[i] = p.bias && i < at.count ? p.bias[at.first + i] : 0.f;
+        c[i] = 0;
+        if (i < at.count && x[i] != none && bias[i] != none)
+            c[i] = order_of(p.bias ? score(x[i]) + F(bias[i]) : F(x[i]));
+    }
+    auto value_of = [](O o) {  // the number with this place
+        if constexpr (sizeof(O) == 4) {
+            const uint32_t b = o & 0x80000000u ? o ^ 0x80000000u : ~o;
+            return __uint_as_float(b);
+        } else {
+            const uint64_t b = o >> 63 ? o ^ (uint64_t(1) << 63) : ~o;
+            return __longlong_as_double(int64_t(b));
+        }
+    };
+    // The f32 error of a score, or of a sum with one of its magnitude: for the
+    // sigmoid 2^-22 s of the exponential, rounding twice, and the sum's; for the
+    // softmax the exponent's rounding (at most 2^-24 |d| e^-d <= 2^-25 of the largest
+    // score, which is at most 1) and the total's 40 roundings at most, too.
+    const float eps = p.sigmoid ? 9.6e-7f : 6e-6f;  // 2^-20, 100 x 2^-24
+    bool sure = true;
+    if (limited) {
+        // The group's one or two best: a lane's, then its lanes'.
+        O a = 0, b = 0;
+        auto take = [&](O v) {
+            b = max(b, min(a, v));
+            a = max(a, v);
+        };
+#pragma unroll
+        for (int i = 0; i < VM; ++i)
+            take(c[i]);
+        for (int d = 1; d < at.L; d <<= 1) {
+            const O a2 = __shfl_xor_sync(kAll, a, d), b2 = __shfl_xor_sync(kAll, b, d);
+            b = max(min(a, a2), max(b, b2));
+            a = max(a, a2);
+        }
+        F v = F(0);
+        if (a != 0) {
+            // (Without a bias the places are the logits'.)
+            v = p.bias ? F(value_of(a)) : p.best > 1 ? score(float(value_of(a))) : F(value_of(a));
+            if (p.best > 1 && b != 0)
+                v += p.bias ? F(value_of(b)) : score(float(value_of(b)));
+        }
+        O g = a == 0 ? O(0) : order_of(v);
+        // Lane l < groups holds group l's.
+        g = __shfl_sync(kAll, g, min(lane, p.groups - 1) * at.L);
+        // Its rank among the groups.
+        int before = 0;
+        for (int j = 0; j < p.groups; ++j) {
+            const O other = __shfl_sync(kAll, g, j);
+            before += other > g || (other == g && j < lane);
+        }
+        const bool kept = lane < p.groups && before < p.keep && g != 0;
+        if (CHECK && by_score) {
+            // The last one kept against the first one not.
+            const uint32_t in = __ballot_sync(kAll, lane < p.groups && before == p.keep - 1);
+            const uint32_t out = __ballot_sync(kAll, lane < p.groups && before == p.keep);
+            const O gi = __shfl_sync(kAll, g, __ffs(in) - 1), go = __shfl_sync(kAll, g, __ffs(out) - 1);
+            if (go != 0) {
+                const float vi = float(value_of(gi)), vo = float(value_of(go));
+                sure = !(vi - vo <= eps * (4.f + fabsf(vi) + fabsf(vo)));
+            }
+        }
+        const uint32_t mask = __ballot_sync(kAll, kept);
+        if (!(mask >> (at.group & 31) & 1u)) {
+#pragma unroll
+            for (int i = 0; i < VM; ++i)
+                c[i] = 0;
+        }
+    }
+    // One after another.  With the check one more than are wanted: the one that
+    // comes next.
+    O mine = 0, best = 0;
+#pragma unroll
+    for (int i = 0; i < VM; ++i)
+        best = max(best, c[i]);
+    id = -1;
+    const bool check = CHECK && p.bias;
+    const int rounds = min(p.topk + (check ? 1 : 0), 32);
+    for (int j = 0; j < rounds; ++j) {
+        const O m = warp_max(best);
+        if (m == 0)
+            break;
+        const int winner = __ffs(__ballot_sync(kAll, best == m)) - 1;
+        int which = 0;
+        if (lane == winner) {
+            bool found = false;
+            best = 0;
+#pragma unroll
+            for (int i = 0; i < VM; ++i) {
+                if (!found && c[i] == m) {
+                    found = true;
+                    which = at.first + i;
+                    c[i] = 0;
+                }
+                best = max(best, c[i]);
+            }
+        }
+        which = __shfl_sync(kAll, which, winner);
+        if (lane == j) {
+            id = which;
+            mine = m;
+        }
+    }
+    if (check) {
+        const O next = __shfl_down_sync(kAll, mine, 1);
+        const float a = float(value_of(mine)), b = float(value_of(next));
+        bool close = lane < p.topk && mine != 0 && next != 0 && a - b <= eps * (1.f + fabsf(a) + fabsf(b));
+        // Experts alike in logit and bias tie in any arithmetic (but the last one
+        // may have more of them after it).
+        const float xi = id >= 0 ? logit_at<ET>(p, token, id) : 0.f, bi = id >= 0 ? p.bias[id] : 0.f;
+        const float xn = __shfl_down_sync(kAll, xi, 1), bn = __shfl_down_sync(kAll, bi, 1);
+        const bool alike = xi == xn && bi == bn;
+        close &= !(alike && lane < p.topk - 1);
+        // With 32 choices there is no lane for the one that comes next.
+        const bool more = warp_max(best) != 0;
+        if (lane == 31)
+            close = p.topk == 32 && more;
+        sure &= __all_sync(kAll, !close) != 0;
+    }
+    if (lane >= p.topk)
+        id = -1;
+    return sure;
+}
+
+// The same in f64, out of the way of the usual one's registers.
+template <int ET, int VM, bool WIDE>
+__device__ __noinline__ int choose_exactly(const ChooseParams &p, int64_t token, float top, float total)
+{
+    const int lane = int(threadIdx.x & 31);
+    const Layout at(p.experts, p.groups, VM, lane);
+    float x[VM];
+    read_logits<ET, VM, WIDE>(p, token, at, x);
+    int id;
+    choose<double, ET, VM>(p, token, at, x, top, total, lane, id);
+    return id;
+}
+
+template <int ET, int VM, bool WIDE>
+__global__ void __launch_bounds__(32 * kChooseWarps, VM == 32 ? 2 : 4) tsm_choose_kernel(const __grid_constant__ ChooseParams p)
+{
+    chain_next();
+    chain_wait();
+    const int lane = int(threadIdx.x & 31);
+    const Layout at(p.experts, p.groups, VM, lane);
+    const float none = __uint_as_float(0xff800000u);
+    const int64_t warps = int64_t(gridDim.x) * kChooseWarps;
+    for (int64_t t = int64_t(blockIdx.x) * kChooseWarps + (threadIdx.x >> 5); t < p.tokens; t += warps) {
+        float x[VM];
+        read_logits<ET, VM, WIDE>(p, t, at, x);
+        bool bad = false;
+        uint32_t high = 0;
+#pragma unroll
+        for (int i = 0; i < VM; ++i) {
+            bad |= is_nan(x[i]) || (i < at.count && p.bias && is_nan(p.bias[at.first + i]));
+            high = max(high, x[i] != none ? order_of(x[i]) : 0u);
+        }
+        float top = 0.f, total = 0.f;
+        if (!p.sigmoid) {
+            high = warp_max(high);
+            const uint32_t b = high & 0x80000000u ? high ^ 0x80000000u : ~high;
+            top = high ? __uint_as_float(b) : 0.f;
+            bad |= top == __uint_as_float(0x7f800000u);
+#pragma unroll
+            for (int i = 0; i < VM; ++i)
+                total += expf(x[i] - top);
+            total = warp_sum(total);
+        }
+        bad = __any_sync(kAll, bad);
+        int id;
+        if (bad) {
+            id = lane;
+        } else if (!choose<float, ET, VM>(p, t, at, x, top, total, lane, id)) {
+            id = choose_exactly<ET, VM, WIDE>(p, t, top, total);
+        }
+        if (lane >= p.topk)
+            id = -1;
+        float w = 0.f;
+        const float mine = id >= 0 ? logit_at<ET>(p, t, id) : 0.f;
+        if (p.renormalize) {
+            // s_j / sum s, with the largest exponential taken out of both.
+            const float e = p.sigmoid ? fminf(mine, 0.f) : mine;
+            const uint32_t m = warp_max(id >= 0 ? order_of(e) : 0u);
+            const float most = m ? __uint_as_float(m & 0x80000000u ? m ^ 0x80000000u : ~m) : 0.f;
+            if (id >= 0)
+                w = expf(e - most) / (p.sigmoid ? 1.f + expf(-fabsf(mine)) : 1.f);
+            const float all = warp_sum(w);
+            w = id >= 0 ? w / all * p.scale : 0.f;
+        } else if (id >= 0) {
+            w = (p.sigmoid ? 1.f / (1.f + expf(-mine)) : expf(mine - top) / total) * p.scale;
+        }
+        if (bad)
+            w = __uint_as_float(0x7fffffffu);
+        if (lane < p.topk) {
+            p.ids[t * p.topk + lane] = id;
+            p.weights[t * p.topk + lane] = w;
+        }
+    }
+}
+
+template <int ET, int VM, bool WIDE>
+__global__ void __launch_bounds__(32 * kChooseWarps) tsm_choose_grad_kernel(const __grid_constant__ ChooseParams p)
+{
+    constexpr int EB = ET == kOutF32 ? 4 : 2;
+    using E = Piece<ET, EB>;
+    chain_next();
+    chain_wait();
+    const int lane = int(threadIdx.x & 31);
+    const Layout at(p.experts, 1, VM, lane);
+    const bool whole = !p.sigmoid && !p.renormalize;
+    const int64_t warps = int64_t(gridDim.x) * kChooseWarps;
+    for (int64_t t = int64_t(blockIdx.x) * kChooseWarps + (threadIdx.x >> 5); t < p.tokens; t += warps) {
+        int id = lane < p.topk ? p.ids[t * p.topk + lane] : -1;
+        if (id >= p.experts || id < 0)
+            id = -1;
+        const float dw = id >= 0 ? p.dweights[t * p.topk + lane] * p.scale : 0.f;
+        const float mine = id >= 0 ? logit_at<ET>(p, t, id) : 0.f;
+        float x[VM];
+        float top = 0.f, total = 1.f;
+        if (whole) {
+            read_logits<ET, VM, WIDE>(p, t, at, x);
+            float high = __uint_as_float(0xff800000u);
+#pragma unroll
+            for (int i = 0; i < VM; ++i)
+                high = fmaxf(high, x[i]);
+            top = high;
+#pragma unroll
+            for (int d = 16; d; d >>= 1)
+                top = fmaxf(top, __shfl_xor_sync(kAll, top, d));
+            if (top == __uint_as_float(0xff800000u))
+                top = 0.f;  // (no expert is there: zeros below)
+            total = 0.f;
+#pragma unroll
+            for (int i = 0; i < VM; ++i) {
+                x[i] = expf(x[i] - top);
+                total += x[i];
+            }
+            total = warp_sum(total);
+        }
+        // The lane's choice: g_j ds_j/dx_j but for the softmax's sum.
+        float g = 0.f, sum = 0.f;
+        if (p.renormalize) {
+            const float e = p.sigmoid ? fminf(mine, 0.f) : mine;
+            const uint32_t m = warp_max(id >= 0 ? order_of(e) : 0u);
+            const float most = m ? __uint_as_float(m & 0x80000000u ? m ^ 0x80000000u : ~m) : 0.f;
+            float w = 0.f;
+            if (id >= 0)
+                w = expf(e - most) / (p.sigmoid ? 1.f + expf(-fabsf(mine)) : 1.f);
+            const float all = warp_sum(w);
+            w = all > 0.f || is_nan(all) ? w / all : 0.f;
+            const float mean = warp_sum(dw * w);
+            g = w * (dw - mean) * (p.sigmoid ? 1.f / (1.f + expf(mine)) : 1.f);
+        } else if (p.sigmoid) {
+            const float s = 1.f / (1.f + expf(-mine));
+            g = dw * s * (1.f / (1.f + expf(mine)));
+        } else {
+            g = dw * (id >= 0 ? expf(mine - top) / total : 0.f);
+            sum = warp_sum(g);
+        }
+        if (id < 0)
+            g = 0.f;
+        float d[VM];
+        const float per = whole && total > 0.f ? sum / total : whole && is_nan(total) ? total : 0.f;
+#pragma unroll
+        for (int i = 0; i < VM; ++i)
+            d[i] = whole ? -x[i] * per : 0.f;
+        for (int j = 0; j < p.topk; ++j) {
+            const int e = __shfl_sync(kAll, id, j) - at.first;
+            const float v = __shfl_sync(kAll, g, j);
+#pragma unroll
+            for (int i = 0; i < VM; ++i)
+                d[i] += e == i ? v : 0.f;
+        }
+        char *row = static_cast<char *>(p.dlogits) + (t * p.ld_d + at.first) * EB;
+        if constexpr (WIDE && VM * EB >= 4) {
+            using P = Piece<ET, VM * EB >= 16 ? 16 : 4>;
+            if (at.count) {
+#pragma unroll
+                for (int i = 0; i < VM / P::V; ++i) {
+                    float v[P::V];
+#pragma unroll
+                    for (int j = 0; j < P::V; ++j)
+                        v[j] = d[P::V * i + j];
+                    P::store(row, i, v);
+                }
+            }
+        } else {
+#pragma unroll
+            for (int i = 0; i < VM; ++i)
+                if (i < at.count) {
+                    const float v[1] = {d[i]};
+                    E::store(row, i, v);
+                }
+        }
+    }
+}
+
+template <int ET, int VM, bool GRAD>
+cudaError_t choose_as(const ChooseParams &p, bool wide, int sms, cudaStream_t stream)
+{
+    const int64_t blocks = (p.tokens + kChooseWarps - 1) / kChooseWarps;
+    const dim3 grid(unsigned(min(blocks, int64_t(sms) * 64)));
+    if constexpr (GRAD)
+        return wide ? launch_chained(tsm_choose_grad_kernel<ET, VM, true>, grid, 32 * kChooseWarps, 0, 0, stream, p)
+                    : launch_chained(tsm_choose_grad_kernel<ET, VM, false>, grid, 32 * kChooseWarps, 0, 0, stream, p);
+    else
+        return wide ? launch_chained(tsm_choose_kernel<ET, VM, true>, grid, 32 * kChooseWarps, 0, 0, stream, p)
+                    : launch_chained(tsm_choose_kernel<ET, VM, false>, grid, 32 * kChooseWarps, 0, 0, stream, p);
+}
+
+// Experts of a lane: a power of two that lets a group's lanes hold its experts.
+int lane_experts(int experts, int groups)
+{
+    int lanes = 32;
+    while (lanes * groups > 32)
+        lanes /= 2;
+    const int per = experts / groups;
+    int vm = 2;
+    while (vm * lanes < per)
+        vm *= 2;
+    return vm;
+}
+
+template <int ET, bool GRAD>
+cudaError_t choose_type(const ChooseParams &p, bool aligned, int sms, cudaStream_t stream)
+{
+    const int groups = GRAD ? 1 : p.groups;
+    const int vm = lane_experts(p.experts, groups);
+    // Wide accesses where every lane's experts are all there or all not, and start
+    // at a multiple of them.
+    const bool wide = aligned && p.experts / groups % vm == 0;
+    switch (vm) {
+    case 2: return choose_as<ET, 2, GRAD>(p, wide, sms, stream);
+    case 4: return choose_as<ET, 4, GRAD>(p, wide, sms, stream);
+    case 8: return choose_as<ET, 8, GRAD>(p, wide, sms, stream);
+    case 16: return choose_as<ET, 16, GRAD>(p, wide, sms, stream);
+    case 32: return choose_as<ET, 32, GRAD>(p, wide, sms, stream);
+    default: return cudaErrorInvalidValue;  // (more than the caller lets through)
+    }
+}
+
+}  // namespace
+
+template <>
+cudaError_t launch_choose<TSM_CHOOSE_ELEM>(const ChooseParams &p, bool aligned, int sms, cudaStream_t stream)
+{
+    return choose_type<TSM_CHOOSE_ELEM, false>(p, aligned, sms, stream);
+}
+
+template <>
+cudaError_t launch_choose_grad<TSM_CHOOSE_ELEM>(const ChooseParams &p, bool aligned, int sms, cudaStream_t stream)
+{
+    return choose_type<TSM_CHOOSE_ELEM, true>(p, aligned, sms, stream);
+}
+
+}  // namespace tsm

@@ -1,0 +1,58 @@
+// fp4_plan.h -- how a product of 4-bit rows is launched: the kernel, its tiles
+// and their schedule, and the workspace.  Host arithmetic only: no CUDA call is
+// made.
+#pragma once
+
+#include "fp4_internal.h"
+#include "s8_plan.h"
+
+#include <algorithm>
+
+namespace tsm {
+
+// A launch of a product whose sizes are all positive.
+struct Fp4Plan {
+    Fp4Kind kind;
+    Fp4Shape shape;
+    int32_t tiles_m, tiles_n, kb;
+    int32_t workers;            // CTAs, or pairs, that share a launch
+    int grid;
+    S8Schedule sched;           // not grouped
+    bool pack_a, pack_b;        // copied to rows lda2 / ldb2 bytes apart first
+    int64_t lda2, ldb2;
+    // Workspace: the copies, the pieces' sums, the arrival words.
+    int64_t bytes_a, bytes_b, bytes_p, bytes_w;
+
+    // False: more tiles than a launch can count.
+    bool make(const Fp4Params &p, const uint8_t *A, int64_t lda, int64_t sA, const uint8_t *B, int64_t ldb, int64_t sB, int sms)
+    {
+        *this = {};
+        kind = p.M <= 32 ? Fp4Kind::kRows32 : p.M <= 64 ? Fp4Kind::kRows64 : p.M <= 128 ? Fp4Kind::kRows128 : Fp4Kind::kPair;
+        shape = fp4_shape(kind);
+        const auto up = [](int64_t x, int64_t m) { return (x + m - 1) / m * m; };
+        tiles_m = int32_t((int64_t(p.M) + shape.tile_m - 1) / shape.tile_m);
+        tiles_n = int32_t((int64_t(p.N) + shape.tile_n - 1) / shape.tile_n);
+        kb = int32_t((int64_t(p.K) + kFp4BlockK - 1) / kFp4BlockK);
+        workers = kind == Fp4Kind::kPair ? sms / 2 : sms;
+        const int64_t tiles = int64_t(tiles_m) * tiles_n * p.batch;
+        if (tiles > S8Schedule::kMaxTiles)
+            return false;
+        sched.plan(int32_t(tiles), kb, workers, shape.price, shape.part);
+        grid = p.group_rows
+                   ? workers
+                   : int(std::max<int64_t>(sched.shared ? sched.cutters : 0, std::min<int64_t>(sched.tiles, workers)));
+        const int64_t width = (int64_t(p.K) + 1) / 2;
+        pack_a = !addressable(reinterpret_cast<const int8_t *>(A), lda, sA, p.M, p.batch);
+        pack_b = !addressable(reinterpret_cast<const int8_t *>(B), ldb, sB, p.N, p.batch);
+        lda2 = ldb2 = up(width, 16);
+        bytes_a = pack_a ? up(int64_t(p.batch) * p.M * lda2, 256) : 0;
+        bytes_b = pack_b ? up(int64_t(p.batch) * p.N * ldb2, 256) : 0;
+        // (A grouped launch's tiles are counted on the device: any number up to these.)
+        const int64_t cut = p.group_rows ? 2 * int64_t(workers) : sched.shared;
+        bytes_p = cut ? 2 * int64_t(workers) * shape.slot_bytes : 0;
+        bytes_w = cut * shape.parts * 8;
+        return true;
+    }
+};
+
+}  // namespace tsm

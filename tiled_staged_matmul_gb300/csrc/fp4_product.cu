@@ -1,0 +1,526 @@
+// fp4_product.cu -- products of microscaled 4-bit floating-point rows:
+//
+//   C[i][j] = act(alpha * scale_a[i] * scale_b[j] * S[i][j] + bias[j]),
+//   S[i][j] = sum over blocks b of  sa[i][b] sb[j][b] * sum over k in b of A[i][k] B[j][k]
+//
+// A and B are rows of e2m1 codes along k, with a scale per block of 16 (e4m3)
+// or 32 (a power of two).  tcgen05.mma takes codes and block scales as they
+// are: the codes from shared memory, the scales from TMEM, where tcgen05.cp
+// puts a 512-byte scale tile in the order in which it lies in memory.
+//
+// The product is computed transposed, columns of C (rows of B, the weights) on
+// the MMA's 128 TMEM lanes and rows of C (tokens) on its N side, so that one
+// kernel serves one token and thousands: a tile is 128 columns by 32, 64 or 128
+// rows, or a CTA pair's 256 by 256.  A lane's scale and bias of its column are
+// then registers, and a warp's 32 lanes store consecutive elements of a row.
+//
+// One persistent CTA (or pair) per SM (pair of SMs), warp-specialised:
+//   warp 0      TMA producer: codes of both operands and their scale tiles
+//   warp 1      MMA issuer (the pair's leader): scales to TMEM, four MMAs of 64 k
+//               a stage
+//   warps 2-9   epilogue, two per TMEM lane quarter (half of the rows each)
+// Few rows are bound by reading B once; their tiles are cut along K so that
+// every SM reads its share, the f32 sums joined in a fixed order by whoever
+// arrives last.
+#include "fp4_internal.h"
+#include "fp4_ptx.cuh"
+#include "s8_common.cuh"
+
+namespace tsm {
+
+namespace {
+
+constexpr int kFp4Threads = 320;
+constexpr int kEpiWarps = 8;
+constexpr int kFp4BarGroup = 1, kFp4BarSetup = 3;  // named barriers: two epilogue halves' (1, 2), the setup's
+
+template <int NT, bool PAIR, int BLK>
+struct Fp4Cfg {
+    static constexpr int CTAS = PAIR ? 2 : 1;
+    static constexpr int COLS = 128;                     // columns of C per CTA
+    static constexpr int ROWS = NT / CTAS;               // rows of C staged by one CTA
+    static constexpr int TILE_M = NT, TILE_N = COLS * CTAS;
+    static constexpr int B_BYTES = COLS * 128;
+    static constexpr int A_BYTES = ROWS * 128;
+    static constexpr int KT = kFp4BlockK / (4 * BLK);    // scale tiles along a stage's k
+    static constexpr int MT = PAIR ? 2 : 1;              // scale tiles along the tile's rows
+    static constexpr int SB_BYTES = KT * kScaleTile;
+    static constexpr int SA_BYTES = MT * KT * kScaleTile;
+    static constexpr int STAGE = B_BYTES + A_BYTES + SB_BYTES + SA_BYTES;
+    static constexpr int HC = NT / 2;                    // rows of one epilogue half
+    static constexpr int TERMS_OFF = 3072;
+    static constexpr int CTRL = TERMS_OFF + 2 * 2 * HC * 4;
+    static constexpr int FIT = (232448 - 1024 - CTRL) / STAGE;
+    static constexpr int S = FIT > 8 ? 8 : FIT;
+    static constexpr int SMEM_BYTES = 1024 + S * STAGE + CTRL;
+    static_assert(STAGE % 1024 == 0 && S >= 4, "stages");
+    static_assert(SMEM_BYTES > 232448 / 2, "one CTA per SM keeps TMEM allocation uncontended");
+    // TMEM: two accumulators, then the scales at the end.  A pair's accumulators
+    // of 256 columns leave no room for them, so the second one starts OVER
+    // columns before the first one's end; the epilogue reads those first.
+    static constexpr int SB_COLS = 4 * KT, SA_COLS = 4 * MT * KT;
+    static constexpr int SCALE_COLS = SB_COLS + SA_COLS;
+    static constexpr int RING = PAIR ? 1 : S;            // sets of scales
+    static constexpr int OVER = PAIR ? 48 : 0;
+    static constexpr int ACC1 = NT - OVER;
+    static constexpr int SCALE_AT = 512 - RING * SCALE_COLS;
+    static_assert(ACC1 + NT <= SCALE_AT, "TMEM columns");
+    static constexpr int PARTS = 2 * CTAS;
+    static constexpr int32_t SLOT = CTAS * NT * COLS;    // floats
+    static constexpr Fp4Kind KIND = PAIR       ? Fp4Kind::kPair
+                                    : NT == 32 ? Fp4Kind::kRows32
+                                    : NT == 64 ? Fp4Kind::kRows64
+                                               : Fp4Kind::kRows128;
+    static constexpr Fp4Shape SHAPE = fp4_shape(KIND);
+    static_assert(SHAPE.tile_m == TILE_M && SHAPE.tile_n == TILE_N && SHAPE.slot_bytes == 4 * SLOT && SHAPE.parts == PARTS,
+                  "the host's idea of a tile");
+    // The MMA's descriptor: e2m1 x e2m1 (bits 7-9 and 10-12 = 1), both K-major, N
+    // / 8 from bit 17, scales e4m3 or e8m0 (bit 23), M / 16 from bit 24.  With two
+    // scales a row for 64 k, the upper two of a tile's four are chosen by 2 at bits
+    // 4-5 (N side) and 29-30 (M side).
+    static constexpr uint32_t IDESC = (1u << 7) | (1u << 10) | (uint32_t(NT >> 3) << 17) | (uint32_t(BLK == 32) << 23) |
+                                      (uint32_t(COLS * CTAS >> 4) << 24);
+    static constexpr uint32_t UPPER = (2u << 4) | (2u << 29);
+};
+
+// Shared-memory descriptor of a scale tile: 32 rows of 16 bytes, no swizzle,
+// groups of eight rows 128 bytes apart.
+__device__ __forceinline__ uint64_t desc_scales(uint32_t saddr)
+{
+    return (uint64_t(128 >> 4) << 32) | (uint64_t(1) << 46) | uint64_t((saddr & 0x3FFFFu) >> 4);
+}
+
+// Sixteen rows of the lane's column of C: scaled, biased, activated, stored.
+// `row` the first, `rows` how many there are; sa_at: the rows' scales (alpha in
+// them).  16-bit types go in pairs of columns where they are aligned: neighbour
+// lanes exchange values, so that even lanes store two columns of one row, odd
+// lanes of the next.
+__device__ __forceinline__ void finish_rows(const Fp4Params &p, const float (&acc)[16], uint32_t sa_at, float sb, float bias,
+                                            int32_t z, int32_t row, int32_t rows, int32_t col, int lane)
+{
+    float v[16];
+#pragma unroll
+    for (int j = 0; j < 16; j += 4) {
+        const uint4 s = ptx::ld_shared_v4(sa_at + 4u * j);
+        const uint32_t w[4] = {s.x, s.y, s.z, s.w};
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+            v[j + i] = fmaf(sb, acc[j + i] * __uint_as_float(w[i]), bias);
+    }
+    with_activation<kActRuntime>(p.epi.act, [&](auto act) {
+#pragma unroll
+        for (int j = 0; j < 16; ++j)
+            v[j] = epi_act(v[j], decltype(act)::value, p.epi.slope);
+    });
+    const int64_t at = int64_t(z) * p.sC + int64_t(row) * p.ldc + col;
+    if (p.epi.out_type == kOutF32) {
+        float *c = static_cast<float *>(p.C) + at;
+        if (col < p.N) {
+#pragma unroll
+            for (int j = 0; j < 16; ++j, c += p.ldc)
+                if (j < rows)
+                    *c = v[j];
+        }
+    } else if (p.vec_c) {
+        const int odd = lane & 1;
+        uint16_t *c = static_cast<uint16_t *>(p.C) + at - odd + odd * p.ldc;
+#pragma unroll
+        for (int j = 0; j < 16; j += 2, c += 2 * p.ldc) {
+            const float other = __shfl_xor_sync(0xffffffffu, odd ? v[j] : v[j + 1], 1);
+            const uint32_t two = odd ? out16_pair(other, v[j + 1], p.epi.out_type) : out16_pair(v[j], other, p.epi.out_type);
+            if (j + odd < rows) {
+                if ((col | 1) < p.N)
+                    *reinterpret_cast<uint32_t *>(c) = two;
+                else if (col - odd < p.N)
+                    *c = uint16_t(two);
+            }
+        }
+    } else if (col < p.N) {
+        uint16_t *c = static_cast<uint16_t *>(p.C) + at;
+#pragma unroll
+        for (int j = 0; j < 16; ++j, c += p.ldc)
+            if (j < rows)
+                *c = uint16_t(epi_out16(v[j], p.epi.out_type));
+    }
+}
+
+template <int NT, bool PAIR, int BLK>
+__global__ void __launch_bounds__(kFp4Threads, 1)
+    tsm_fp4_kernel(const __grid_constant__ Fp4Maps maps, const Fp4Params p)
+{
+    using Cfg = Fp4Cfg<NT, PAIR, BLK>;
+    constexpr int S = Cfg::S;
+    extern __shared__ uint8_t smem_raw[];
+    const uint32_t raw = ptx::smem_addr(smem_raw);
+    const uint32_t base = (raw + 1023u) & ~1023u;
+    const uint32_t ctrl = base + S * Cfg::STAGE;
+    // Barriers.  `full`, `tempty` and `over` are used in the pair's leader only.
+    const uint32_t full0 = ctrl;               // [S] a stage has landed (both CTAs')
+    const uint32_t empty0 = ctrl + 64u;        // [S] the MMAs that read it are done
+    const uint32_t tfull0 = ctrl + 128u;       // [2] accumulator complete
+    const uint32_t tempty0 = ctrl + 144u;      // [2] accumulator read out
+    const uint32_t over = ctrl + 160u;         // the columns that both accumulators share are read out
+    const uint32_t done_bar = ctrl + 168u;     // all MMAs completed
+    const uint32_t tmem_slot = ctrl + 176u;
+    const uint32_t flag = ctrl + 180u;         // this CTA gives up
+    const uint32_t last_flag = ctrl + 184u;    // [2] one per epilogue half
+    const SharedSchedule<false> sched{ctrl + 256u};
+    const SharedSchedule<true> wsched{ctrl + 256u};
+    const uint32_t gtab = ctrl + 1024u, grows = ctrl + 2048u;
+    const uint32_t terms0 = ctrl + Cfg::TERMS_OFF;  // [2][half][rows' scales]
+
+    const int warp = __shfl_sync(0xffffffffu, int(threadIdx.x >> 5), 0);  // (uniform to the compiler)
+    const int lane = int(threadIdx.x & 31);
+    const uint32_t rank = PAIR ? ptx::cluster_ctarank() : 0u;
+    const int32_t worker = int32_t(PAIR ? (blockIdx.x >> 1) : blockIdx.x);
+
+    if (threadIdx.x == 0) {
+        for (int s = 0; s < S; ++s) {
+            ptx::mbar_init(full0 + 8u * s, 1);
+            ptx::mbar_init(empty0 + 8u * s, 1);
+        }
+        for (int b = 0; b < 2; ++b) {
+            ptx::mbar_init(tfull0 + 8u * b, 1);
+            ptx::mbar_init(tempty0 + 8u * b, kEpiWarps * Cfg::CTAS);
+        }
+        ptx::mbar_init(over, kEpiWarps / 2 * Cfg::CTAS);
+        ptx::mbar_init(done_bar, 1);
+        ptx::st_shared_u32(flag, 0u);
+        if (!p.group_rows)
+            sched.put(p.sched);
+        ptx::fence_mbar_init();
+        ptx::prefetch_tensormap(&maps.a);
+        ptx::prefetch_tensormap(&maps.b);
+        ptx::prefetch_tensormap(&maps.scales_a);
+        ptx::prefetch_tensormap(&maps.scales_b);
+    }
+    __syncwarp();
+    ptx::cta_sync();  // the barriers are there
+    if constexpr (PAIR)
+        ptx::cluster_arrive_relaxed();
+    chain_next();
+    if constexpr (PAIR)
+        ptx::cluster_wait();  // the peer is there, and its barriers
+    // Unless the tiles are counted on the device, the producer has all it needs
+    // by now, and its first loads do not wait for the rest.
+    const bool early = warp == 0 && !p.group_rows;
+    if (!early && warp == 1) {
+        ptx::tmem_alloc<PAIR>(tmem_slot, 512);
+        ptx::tmem_relinquish<PAIR>();
+    }
+    chain_wait();
+    if (!early) {
+        if (warp == 2 && p.group_rows) {
+            build_s8_groups<Cfg::TILE_M>(p, gtab, grows);
+            if (lane == 0) {
+                S8Schedule s;
+                s.plan(int32_t(ptx::ld_shared_u32(gtab + 4u * (p.batch - 1))), p.kb, p.workers, p.sched_price, p.sched_part);
+                sched.put(s);
+            }
+        }
+        // (All warps that came here: all, or all but the first.)
+        ptx::tc_fence_before_sync();
+        ptx::named_bar_sync(kFp4BarSetup, p.group_rows ? kFp4Threads : kFp4Threads - 32);
+        ptx::tc_fence_after_sync();
+    }
+    const uint32_t tmem = early ? 0u : ptx::ld_shared_u32(tmem_slot);
+
+    if (warp == 0) {
+        if (lane == 0) {
+            // ---------------- TMA producer (each CTA fills its own stages)
+            const uint32_t full_lead0 = PAIR ? ptx::mapa_shared(full0, 0) : full0;
+            uint32_t stage = 0, phase = 0, issued = 0;
+            bool ok = true;
+            auto load = [&](uint32_t to, const CUtensorMap &map, uint32_t bar, int32_t c0, int32_t c1, int32_t c2) {
+                if constexpr (PAIR)
+                    ptx::tma_load_3d_pair(to, &map, bar, c0, c1, c2);
+                else
+                    ptx::tma_load_3d(to, &map, bar, c0, c1, c2);
+            };
+            for (PieceWalk<false> w(sched, worker); ok && w.advance(sched);) {
+                const S8Tile t = tile_at(w.tile, p, gtab, grows, Cfg::TILE_M, Cfg::TILE_N);
+                const int32_t col = t.n0 + int32_t(rank) * Cfg::COLS, row = t.m0 + int32_t(rank) * Cfg::ROWS;
+                const int32_t sb_row = t.z * p.scale_rows_b + col / 128, sa_row = t.z * p.scale_rows_a + t.m0 / 128;
+                for (int32_t kb = w.kb0; kb < w.kb1; ++kb) {
+                    if (!s8_wait<PAIR>(empty0 + 8u * stage, phase ^ 1u, flag, p, kStatusProducer)) {
+                        ok = false;
+                        break;
+                    }
+                    const uint32_t to = base + stage * Cfg::STAGE;
+                    const uint32_t fb = full_lead0 + 8u * stage;
+                    // Both CTAs' bytes are counted on the leader's barrier.
+                    if (rank == 0)
+                        ptx::mbar_arrive_expect_tx(full0 + 8u * stage, Cfg::CTAS * Cfg::STAGE);
+                    load(to, maps.b, fb, kb * 128, col, t.z);
+                    load(to + Cfg::B_BYTES, maps.a, fb, kb * 128, row, t.z);
+                    load(to + Cfg::B_BYTES + Cfg::A_BYTES, maps.scales_b, fb, 0, kb * Cfg::KT, sb_row);
+                    load(to + Cfg::B_BYTES + Cfg::A_BYTES + Cfg::SB_BYTES, maps.scales_a, fb, 0, kb * Cfg::KT, sa_row);
+                    ++issued;
+                    if (++stage == S) {
+                        stage = 0;
+                        phase ^= 1u;
+                    }
+                }
+            }
+            if (rank == 0) {
+                // No TMA write into shared memory outlives the CTA (the pair):
+                // the last S loads, the stages from `stage` on, oldest first.
+                for (int i = 0; i < S; ++i) {
+                    if (issued + i >= uint32_t(S))
+                        s8_wait<PAIR>(full0 + 8u * stage, phase ^ 1u, flag, p, kStatusDrain, false);
+                    if (++stage == S) {
+                        stage = 0;
+                        phase ^= 1u;
+                    }
+                }
+            } else if (ptx::ld_shared_u32(flag)) {
+                // The peer's loads are counted in the leader only: after giving
+                // up, a fixed time for them to land.
+                const uint64_t t0 = ptx::globaltimer_ns();
+                while (ptx::globaltimer_ns() - t0 < 200000ull) {
+                }
+            }
+        }
+        __syncwarp();
+    } else if (warp == 1) {
+        if (lane == 0 && rank == 0) {
+            // ---------------- MMA issuer
+            constexpr uint16_t both = PAIR ? 3 : 1;
+            uint32_t stage = 0, phase = 0, acc = 0, aphase = 0, turn = 0;
+            bool ok = true;
+            for (PieceWalk<false> w(sched, worker); ok && w.advance(sched);) {
+                ok = s8_wait<PAIR, PAIR>(tempty0 + 8u * acc, aphase ^ 1u, flag, p, kStatusMma);
+                if (PAIR && ok)
+                    ok = s8_wait<PAIR, PAIR>(over, turn ^ 1u, flag, p, kStatusMma);
+                if (!ok)
+                    break;
+                ptx::tc_fence_after_sync();
+                const uint32_t d = tmem + acc * uint32_t(Cfg::ACC1);
+                for (int32_t kb = w.kb0; kb < w.kb1; ++kb) {
+                    if (!s8_wait<PAIR>(full0 + 8u * stage, phase, flag, p, kStatusMma)) {
+                        ok = false;
+                        break;
+                    }
+                    ptx::tc_fence_after_sync();
+                    const uint32_t sb = base + stage * Cfg::STAGE, sa = sb + Cfg::B_BYTES;
+                    const uint32_t ssb = sa + Cfg::A_BYTES, ssa = ssb + Cfg::SB_BYTES;
+                    const uint32_t tsb = tmem + Cfg::SCALE_AT + (stage % Cfg::RING) * uint32_t(Cfg::SCALE_COLS);
+                    const uint32_t tsa = tsb + Cfg::SB_COLS;
+#pragma unroll
+                    for (int i = 0; i < Cfg::KT; ++i) {
+                        ptx::tmem_cp_scales<PAIR>(tsb + 4u * i, desc_scales(ssb + uint32_t(i * kScaleTile)));
+#pragma unroll
+                        for (int m = 0; m < Cfg::MT; ++m)
+                            ptx::tmem_cp_scales<PAIR>(tsa + uint32_t(4 * (i * Cfg::MT + m)),
+                                                      desc_scales(ssa + uint32_t((m * Cfg::KT + i) * kScaleTile)));
+                    }
+                    // (What lies past K is zeros.)
+                    const int32_t left = p.K - kb * kFp4BlockK;
+#pragma unroll
+                    for (int kk = 0; kk < 4; ++kk) {
+                        if (64 * kk >= left)
+                            break;
+                        const int i = BLK == 16 ? kk : kk / 2;
+                        const uint32_t id = Cfg::IDESC | (BLK == 32 && (kk & 1) ? Cfg::UPPER : 0u);
+                        ptx::mma_fp4<PAIR, BLK>(d, desc_a(sb + 32u * kk), desc_a(sa + 32u * kk), id, tsb + 4u * i,
+                                                tsa + uint32_t(4 * Cfg::MT * i), (kb > w.kb0 || kk > 0) ? 1u : 0u);
+                    }
+                    ptx::mma_commit<PAIR>(empty0 + 8u * stage, both);
+                    if (++stage == S) {
+                        stage = 0;
+                        phase ^= 1u;
+                    }
+                }
+                if (!ok)
+                    break;
+                ptx::mma_commit<PAIR>(tfull0 + 8u * acc, both);
+                turn ^= 1u;
+                acc ^= 1u;
+                if (acc == 0)
+                    aphase ^= 1u;
+            }
+            // Every MMA must finish before TMEM is freed.
+            ptx::mma_commit<PAIR>(done_bar, 1);
+            s8_wait<PAIR>(done_bar, 0, flag, p, kStatusDrain, false);
+        }
+        __syncwarp();
+    } else {
+        // ---------------- epilogue
+        constexpr int HC = Cfg::HC, CH = HC / 16;
+        const int h = (warp - 2) >> 2, q = warp & 3;
+        const int tid = 32 * q + lane;
+        const uint32_t tempty_lead0 = PAIR ? ptx::mapa_shared(tempty0, 0) : tempty0;
+        const uint32_t over_lead = PAIR ? ptx::mapa_shared(over, 0) : over;
+        uint32_t acc = 0, aphase = 0, turn = 0;
+        for (PieceWalk<true> w(wsched, worker); w.advance(wsched);) {
+            const S8Tile t = tile_at(w.tile, p, gtab, grows, Cfg::TILE_M, Cfg::TILE_N);
+            const int32_t col = t.n0 + int32_t(rank) * Cfg::COLS + tid;
+            const int32_t row0 = t.m0 + h * HC, rows = t.rows - row0;
+            const uint32_t sa_at = terms0 + (turn * 2u + uint32_t(h)) * uint32_t(4 * HC);
+            // The tile's scales and bias, before its sums are there.  (Two sets of
+            // the rows' in turn: the half's other warps may still be at the last
+            // tile's.)
+            if (tid < HC)
+                ptx::st_shared_u32(sa_at + 4u * uint32_t(tid),
+                                   __float_as_uint(p.epi.alpha * (p.scale_a && tid < rows ? p.scale_a[t.z * p.sa_stride + row0 + tid] : 1.f)));
+            const float sb = p.scale_b && col < p.N ? p.scale_b[t.z * p.sb_stride + col] : 1.f;
+            const float bias = p.epi.bias && col < p.N ? p.epi.bias[t.z * p.epi.bias_stride + col] : 0.f;
+            const bool whole = w.kb1 - w.kb0 == wsched.kb();
+            bool ok = s8_wait<PAIR>(tfull0 + 8u * acc, aphase, flag, p, kStatusEpilogue);
+            // The four warps go on or give up together (they meet below).
+            ok = __all_sync(0xffffffffu, ptx::named_bar_and(kFp4BarGroup + h, 128, ok));
+            if (!ok)
+                break;
+            ptx::tc_fence_after_sync();
+            const uint32_t from = tmem + (uint32_t(32 * q) << 16) + acc * uint32_t(Cfg::ACC1) + uint32_t(h * HC);
+            // The half that holds the shared columns starts with them: the last
+            // ones of the first accumulator, the first ones of the second.
+            const bool shares = PAIR && h == (acc ? 0 : 1);
+            const bool backwards = PAIR && acc == 0;
+            const uint32_t tempty = tempty_lead0 + 8u * acc;
+            // After chunk i has left TMEM:
+            auto released = [&](int i) {
+                if (PAIR && i == Cfg::OVER / 16 - 1 && shares) {
+                    ptx::tc_fence_before_sync();
+                    __syncwarp();
+                    if (lane == 0)
+                        arrive_leader<PAIR>(over_lead);
+                }
+                if (i == CH - 1) {
+                    ptx::tc_fence_before_sync();
+                    __syncwarp();
+                    if (lane == 0)
+                        arrive_leader<PAIR>(tempty);
+                }
+            };
+            const float *parts = nullptr;
+            int32_t first = 0, last = -1;
+            const int32_t part_at = (int32_t(rank) * NT + h * HC) * Cfg::COLS + tid;
+            bool mine = true;
+            if (!whole) {
+                // A piece: its sums go to this worker's slot ([row][column]), and
+                // whoever arrives last adds up the contributors', in their order.
+                // A tile's first contributor holds its first block and uses its
+                // second slot; the others start in the tile: their first.
+                const S8Schedule cut = wsched.all();
+                first = cut.owner(w.tile * cut.kb);
+                last = cut.owner((w.tile + 1) * cut.kb - 1);
+                float *const to = p.partial + int64_t(2 * worker + (worker == first)) * Cfg::SLOT + part_at;
+#pragma unroll 1
+                for (int i = 0; i < CH; ++i) {
+                    const int c = backwards ? CH - 1 - i : i;
+                    if (16 * c < rows) {
+                        uint32_t r[16];
+                        ptx::tmem_ld_32x32b_x16(from + 16u * c, r);
+                        ptx::tmem_wait_ld(r);
+#pragma unroll
+                        for (int j = 0; j < 16; ++j)
+                            __stcg(to + (16 * c + j) * Cfg::COLS, __uint_as_float(r[j]));
+                    }
+                    released(i);
+                }
+                __threadfence();
+                ptx::named_bar_sync(kFp4BarGroup + h, 128);
+                if (q == 0)
+                    ptx::st_shared_u32(last_flag + 4u * h, arrive_last(p.arrivals + w.tile * Cfg::PARTS + int32_t(rank) * 2 + h, p.tag,
+                                                                      uint32_t(last - first + 1), lane));
+                ptx::named_bar_sync(kFp4BarGroup + h, 128);
+                mine = __any_sync(0xffffffffu, ptx::ld_shared_u32(last_flag + 4u * h) != 0);
+                __threadfence();
+                parts = p.partial + part_at;
+            }
+            if (mine) {
+#pragma unroll 1
+                for (int i = 0; i < CH; ++i) {
+                    const int c = backwards ? CH - 1 - i : i;
+                    float v[16];
+                    if (whole) {
+                        uint32_t r[16];
+                        if (16 * c < rows) {
+                            ptx::tmem_ld_32x32b_x16(from + 16u * c, r);
+                            ptx::tmem_wait_ld(r);
+                        }
+                        released(i);
+#pragma unroll
+                        for (int j = 0; j < 16; ++j)
+                            v[j] = __uint_as_float(r[j]);
+                    } else if (16 * c < rows) {
+#pragma unroll
+                        for (int j = 0; j < 16; ++j)
+                            v[j] = 0.f;
+                        for (int32_t k = first; k <= last; ++k) {
+                            const float *theirs = parts + int64_t(2 * k + (k == first)) * Cfg::SLOT + 16 * c * Cfg::COLS;
+#pragma unroll
+                            for (int j = 0; j < 16; ++j)
+                                v[j] += __ldcg(theirs + j * Cfg::COLS);
+                        }
+                    }
+                    if (16 * c < rows)
+                        finish_rows(p, v, sa_at + 64u * c, sb, bias, t.z, row0 + 16 * c, rows - 16 * c, col, lane);
+                }
+            }
+            turn ^= 1u;
+            acc ^= 1u;
+            if (acc == 0)
+                aphase ^= 1u;
+        }
+    }
+
+    ptx::tc_fence_before_sync();
+    ptx::cta_sync();
+    if constexpr (PAIR)
+        ptx::cluster_sync();
+    if (warp == 1) {
+        __syncwarp();
+        ptx::tc_fence_after_sync();
+        ptx::tmem_dealloc<PAIR>(ptx::ld_shared_u32(tmem_slot), 512);
+    }
+}
+
+// fn with the tile and block of a kernel fixed at compile time.
+template <int NT, bool PAIR, int BLK>
+struct Fp4Tag {
+    static constexpr int rows = NT, block = BLK;
+    static constexpr bool pair = PAIR;
+};
+template <int BLK, typename F>
+cudaError_t with_kind(Fp4Kind kind, F &&fn)
+{
+    switch (kind) {
+    case Fp4Kind::kRows32: return fn(Fp4Tag<32, false, BLK>{});
+    case Fp4Kind::kRows64: return fn(Fp4Tag<64, false, BLK>{});
+    case Fp4Kind::kRows128: return fn(Fp4Tag<128, false, BLK>{});
+    default: return fn(Fp4Tag<256, true, BLK>{});
+    }
+}
+
+}  // namespace
+
+cudaError_t set_fp4_attributes()
+{
+    const auto set = [](auto tag) {
+        using T = decltype(tag);
+        return cudaFuncSetAttribute(tsm_fp4_kernel<T::rows, T::pair, T::block>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                    Fp4Cfg<T::rows, T::pair, T::block>::SMEM_BYTES);
+    };
+    for (const Fp4Kind kind : {Fp4Kind::kRows32, Fp4Kind::kRows64, Fp4Kind::kRows128, Fp4Kind::kPair}) {
+        cudaError_t e = with_kind<16>(kind, set);
+        if (e == cudaSuccess)
+            e = with_kind<32>(kind, set);
+        if (e != cudaSuccess)
+            return e;
+    }
+    return cudaSuccess;
+}
+
+cudaError_t launch_fp4(const Fp4Maps &maps, const Fp4Params &p, Fp4Kind kind, int block, int grid, cudaStream_t stream)
+{
+    const auto run = [&](auto tag) {
+        using T = decltype(tag);
+        return launch_chained(tsm_fp4_kernel<T::rows, T::pair, T::block>, dim3(unsigned(T::pair ? 2 * grid : grid)), kFp4Threads,
+                              Fp4Cfg<T::rows, T::pair, T::block>::SMEM_BYTES, T::pair ? 2u : 0u, stream, maps, p);
+    };
+    return block == 16 ? with_kind<16>(kind, run) : with_kind<32>(kind, run);
+}
+
+}  // namespace tsm

@@ -1,7 +1,7 @@
 // ops_api.cu -- host side of the expert token movement and of the 8-bit
 // integer products (include/tsm_gemm.h): argument checks, launch shapes and
 // launches.
-#include "api_internal.h"
+#include "api_checks.h"
 #include "ops_internal.h"
 #include "s8_plan.h"
 
@@ -10,82 +10,6 @@
 
 namespace tsm {
 namespace {
-
-constexpr int64_t kInt32Max = 2147483647;
-constexpr int64_t kMaxSize = int64_t(1) << 40;
-
-bool misaligned(const void *p, int64_t bytes)
-{
-    return (reinterpret_cast<uintptr_t>(p) & uintptr_t(bytes - 1)) != 0;
-}
-
-int elem_bytes(int32_t t) { return t == GEMM_OUT_F32 ? 4 : 2; }
-
-bool known_elem(int32_t t) { return t == GEMM_OUT_F32 || t == GEMM_OUT_F16 || t == GEMM_OUT_BF16; }
-
-// The current device and its state.
-gemm_status_t current(int *dev, DeviceState **ds)
-{
-    const cudaError_t e = cudaGetDevice(dev);
-    if (e != cudaSuccess)
-        return fail_cuda(e, "cudaGetDevice");
-    return device_state(*dev, ds);
-}
-
-// One buffer of a call: checked for its address and, once all are known, on
-// the device.
-struct Buffer {
-    const void *p;
-    int64_t bytes;
-    const char *name;
-    bool written;
-};
-
-// Every buffer non-null where it holds something, no written one overlapping
-// another.
-gemm_status_t check_buffers(const Buffer *b, int n)
-{
-    for (int i = 0; i < n; ++i)
-        if (b[i].bytes > 0 && !b[i].p)
-            return fail(GEMM_ERR_INVALID_VALUE, "%s is NULL", b[i].name);
-    for (int i = 0; i < n; ++i)
-        for (int j = i + 1; j < n; ++j)
-            if ((b[i].written || b[j].written) && overlaps(b[i].p, b[i].bytes, b[j].p, b[j].bytes))
-                return fail(GEMM_ERR_ALIAS, "%s overlaps %s", b[i].name, b[j].name);
-    return GEMM_OK;
-}
-
-gemm_status_t check_on_device(const Buffer *b, int n, int dev)
-{
-    for (int i = 0; i < n; ++i)
-        if (b[i].bytes > 0) {
-            const gemm_status_t st = check_device_pointer(b[i].p, b[i].bytes, dev, b[i].name);
-            if (st != GEMM_OK)
-                return st;
-        }
-    return GEMM_OK;
-}
-
-// Bytes spanned by `batch` matrices `stride` elements apart of `rows` rows `ld`
-// apart.  More than 64 bits hold come out as the most that they hold, which
-// lies in no allocation.
-int64_t reach(int64_t batch, int64_t stride, int64_t rows, int64_t ld, int64_t cols, int64_t elem)
-{
-    if (batch <= 0 || rows <= 0 || cols <= 0)
-        return 0;
-    const __int128 bytes = (__int128(batch - 1) * stride + __int128(rows - 1) * ld + cols) * elem;
-    return bytes > INT64_MAX ? INT64_MAX : int64_t(bytes);
-}
-
-// Bytes of `rows` rows of `width` elements `ld` apart.
-int64_t span(int64_t rows, int64_t width, int64_t ld, int64_t elem) { return reach(1, 0, rows, ld, width, elem); }
-
-// Bytes of one access: 16 or 4 where every address, pitch and width in `all`
-// (or-ed together, in bytes) is a multiple, else one element.
-int access_bytes(uint64_t all, int64_t elem)
-{
-    return (all & 15u) == 0 ? 16 : (all & 3u) == 0 ? 4 : int(elem);
-}
 
 // What the four movement calls share: sizes of both sides and the slots.
 gemm_status_t check_move(int64_t tokens, int64_t topk, int64_t rows, int64_t width, int64_t ld_tokens,

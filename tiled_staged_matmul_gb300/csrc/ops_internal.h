@@ -82,17 +82,22 @@ struct S8Schedule {
     // of these right (6 and 24 do not).
     static constexpr int32_t kCutBlocks = 16;
 
-    __host__ __device__ void plan(int32_t tiles_, int32_t kb_, int32_t workers_)
+    int32_t price;          // of a cut
+
+    // `part`: the last contributor's time for one of the others' sums, in quarters
+    // of a block's time.
+    __host__ __device__ void plan(int32_t tiles_, int32_t kb_, int32_t workers_, int32_t price_ = kCutBlocks, int32_t part = 8)
     {
         tiles = tiles_;
         kb = kb_;
         workers = workers_;
+        price = price_;
         const int32_t over = tiles % workers;
         shared = over == 0 ? 0 : tiles < workers ? tiles : over + workers;
         // A tile's contributors: as many as balance the blocks each multiplies
-        // with the sums the last one adds up, about two blocks' time apiece.
+        // with the sums the last one adds up.
         int32_t each = 1;
-        while (2 * each * each < kb)
+        while (part * each * each < 4 * kb)
             ++each;
         const int32_t pieces = shared * each;
         cutters = pieces < 1 ? 1 : pieces < workers ? pieces : workers;
@@ -106,7 +111,7 @@ struct S8Schedule {
     // The time of the busiest worker, in blocks.
     __host__ __device__ int64_t blocks() const
     {
-        return shared ? int64_t((tiles - shared) / workers) * kb + (shared * kb + cutters - 1) / cutters + kCutBlocks
+        return shared ? int64_t((tiles - shared) / workers) * kb + (shared * kb + cutters - 1) / cutters + price
                       : int64_t((tiles + workers - 1) / workers) * kb;
     }
     // First block of worker w's piece (w <= cutters).

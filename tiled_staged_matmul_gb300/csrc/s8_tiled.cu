@@ -56,94 +56,6 @@ __device__ __forceinline__ uint64_t desc_b_s8(uint32_t saddr)
     return desc_common() | (uint64_t(S8Cfg<PAIR>::F_BOX >> 4) << 16) | uint64_t((saddr & 0x3FFFFu) >> 4);
 }
 
-// The schedule in shared memory, read field by field: the registers are for
-// the sums.  WARP: a whole warp reads it together, and the compiler is told
-// that the values are the warp's (they then need no register per lane).
-template <bool WARP>
-struct SharedSchedule {
-    uint32_t at;
-    __device__ __forceinline__ int32_t field(int i) const
-    {
-        const int32_t v = int32_t(ptx::ld_shared_u32(at + 4u * i));
-        return WARP ? __shfl_sync(0xffffffffu, v, 0) : v;
-    }
-    __device__ __forceinline__ void put(const S8Schedule &s) const
-    {
-        ptx::st_shared_u32(at, uint32_t(s.tiles));
-        ptx::st_shared_u32(at + 4, uint32_t(s.shared));
-        ptx::st_shared_u32(at + 8, uint32_t(s.kb));
-        ptx::st_shared_u32(at + 12, uint32_t(s.workers));
-        ptx::st_shared_u32(at + 16, uint32_t(s.cutters));
-    }
-    __device__ __forceinline__ int32_t tiles() const { return field(0); }
-    __device__ __forceinline__ int32_t kb() const { return field(2); }
-    __device__ __forceinline__ int32_t workers() const { return field(3); }
-    __device__ __forceinline__ S8Schedule all() const
-    {
-        S8Schedule s;
-        s.tiles = tiles();
-        s.shared = field(1);
-        s.kb = kb();
-        s.workers = workers();
-        s.cutters = field(4);
-        return s;
-    }
-};
-
-// One worker's pieces in order: its share of the cut tiles, then whole tiles.
-template <bool WARP>
-struct PieceWalk {
-    int32_t cur, end, next;  // blocks of the cut tiles; next whole tile
-    int32_t tile, kb0, kb1;
-    __device__ __forceinline__ PieceWalk(const SharedSchedule<WARP> &shared, int32_t w)
-    {
-        const S8Schedule s = shared.all();
-        const bool cuts = s.shared > 0 && w < s.cutters;
-        cur = cuts ? s.piece_begin(w) : 0;
-        end = cuts ? s.piece_begin(w + 1) : 0;
-        next = s.shared + w;
-        tile = kb0 = kb1 = 0;
-    }
-    __device__ __forceinline__ bool advance(const SharedSchedule<WARP> &s)
-    {
-        kb0 = 0;
-        kb1 = s.kb();
-        if (cur < end) {
-            tile = cur / kb1;
-            kb0 = cur - tile * kb1;
-            kb1 = min(kb1, kb0 + (end - cur));
-            cur += kb1 - kb0;
-            return true;
-        }
-        tile = next;
-        next += s.workers();
-        return tile < s.tiles();
-    }
-};
-
-// Count one arrival on `word` (a whole warp calls it): true for the last of
-// `total`.  The word holds the launch's tag and the count; under another tag
-// (whatever the workspace's last user left there) the count is none.  The
-// first exchange expects everyone else to have arrived, so that the last one,
-// whom the result waits for, is done after one trip to L2.  Any other failed
-// exchange means that another of the at most `total` contributors has arrived,
-// so the loop ends.  The loop is the warp's, not one lane's, so that the
-// compiler need not plan for a warp that has come apart.
-__device__ __forceinline__ bool arrive_last(unsigned long long *word, unsigned long long tag, uint32_t total, int lane)
-{
-    unsigned long long old = (tag << 16) | (total - 1u);
-    for (;;) {
-        const uint32_t seen = (old >> 16) == tag ? uint32_t(old & 0xffffu) : 0u;
-        unsigned long long prev = 0;
-        if (lane == 0)
-            prev = atomicCAS(word, old, (tag << 16) | (seen + 1u));
-        prev = __shfl_sync(0xffffffffu, prev, 0);
-        if (prev == old)
-            return seen + 1u == total;
-        old = prev;
-    }
-}
-
 // Add a chunk's f32 sums (HC columns of a TMEM lane) to the lane's integers.
 // 1.5 * 2^23 + f has f + kMagicBits as its bits while |f| < 2^22, so an
 // addition and an integer addition do what a conversion does at an eighth of
@@ -182,17 +94,6 @@ __device__ __forceinline__ float add_chunk(uint32_t acc, int32_t (&sum)[HC])
         }
     }
     return largest;
-}
-
-// Two values as the 16-bit output type stores them, in one conversion.
-__device__ __forceinline__ uint32_t out16_pair(float a, float b, int32_t out_type)
-{
-    if (out_type == kOutBF16) {
-        const __nv_bfloat162 x = __floats2bfloat162_rn(a, b);
-        return *reinterpret_cast<const uint32_t *>(&x);
-    }
-    const __half2 x = __floats2half2_rn(a, b);
-    return *reinterpret_cast<const uint32_t *>(&x);
 }
 
 // The epilogue of a box: 32 rows (a lane each) of 32 columns' sums.  Scaled,
@@ -277,22 +178,6 @@ __device__ __forceinline__ void finish_box(const S8Params &p, const S8Tile &t, c
         }
     }
     __syncwarp();
-}
-
-// Arrive on a barrier of the pair's leader.  Released to the CTA only: what the
-// arrival stands for is complete in this SM before it is sent -- f16 in its own
-// shared memory (the proxy fence) or TMEM (the store wait), or TMEM read out
-// (the load wait) -- and is next touched by this SM's own tensor core.
-// Released to the cluster, every arrival would first wait for the warp's other
-// stores, global ones included: measured 1.34 times the whole kernel's time at
-// 8192^3 (1028 against 770 us).
-template <bool PAIR>
-__device__ __forceinline__ void arrive_leader(uint32_t bar)
-{
-    if constexpr (PAIR)
-        ptx::mbar_arrive_remote(bar);
-    else
-        ptx::mbar_arrive(bar);
 }
 
 template <bool PAIR>
