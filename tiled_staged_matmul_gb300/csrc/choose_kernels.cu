@@ -11,14 +11,17 @@
 //
 // A warp takes a token.  Scores are formed in f32, but which expert is chosen is
 // what it is in exact arithmetic: where two scores that decide something lie
-// within the bound of their f32 errors, the warp forms the token's scores again
-// in f64 and decides by those.  (Without a bias the logits themselves give the
-// order, exactly.)  With random logits one token in a thousand needs it.
+// within the bound of their f32 errors, the warp forms them again in f64 and
+// decides by those.  (Without a bias the logits themselves give the order,
+// exactly.)  With random logits one token in a thousand needs it.
 //
-// Bound by launch and instruction latency rather than by its bytes: some 300
-// instructions of a warp for a kilobyte.  Compiled once per type of the logits
+// Bound by instructions rather than by its bytes.  So the choice is not made one
+// expert after another (370 instructions for 8 of 256) but among few: the topk-th
+// largest of the lanes' maxima bounds the topk-th largest of all from below, a
+// dozen experts reach it, and those move to a lane each and are ranked there.  Compiled once per type of the logits
 // (-DTSM_CHOOSE_ELEM, gemm_internal.h's kOut* values).
 #include "fp4_internal.h"
+#include "fp4_ptx.cuh"
 #include "launch.cuh"
 #include "piece.cuh"
 
@@ -48,6 +51,12 @@ __device__ __forceinline__ uint64_t order_of(double v)
     return b ^ (uint64_t(int64_t(b) >> 63) | (uint64_t(1) << 63));
 }
 
+// The float with this place in order.
+__device__ __forceinline__ float value_of(uint32_t o)
+{
+    return __uint_as_float(o & 0x80000000u ? o ^ 0x80000000u : ~o);
+}
+
 __device__ __forceinline__ uint32_t warp_max(uint32_t v) { return __reduce_max_sync(kAll, v); }
 __device__ __forceinline__ uint64_t warp_max(uint64_t v)
 {
@@ -64,9 +73,6 @@ __device__ __forceinline__ F warp_sum(F v)
         v += __shfl_xor_sync(kAll, v, d);
     return v;
 }
-
-__device__ __forceinline__ float exp_of(float v) { return expf(v); }
-__device__ __forceinline__ double exp_of(double v) { return exp(v); }
 
 // An order's type.
 template <typename F>
@@ -142,10 +148,28 @@ __device__ __forceinline__ float logit_at(const ChooseParams &p, int64_t token, 
     return v[0];
 }
 
-// The warp's choice, formed in F.  Lane j ends with the j-th chosen expert, -1 where
-// there is none.  False: two f32 values that decide something are too close.
+// Bounds of the f32 error of a score s <= 1.  exp(v) by ex2.approx is off by 2 +
+// 1.173 |v| units in the last place at most, which s (1 - s) weighs: (0.5 + 0.27) 2^-23;
+// the sum rounds by 2^-24, the division by 2 x 2^-23.  For the softmax the
+// exponentials' errors (e^-d (2 + 1.173 d) 2^-23 with d = max - x: 2 x 2^-23), the
+// total's (as large, and 40 roundings of 2^-24) and the quotient's: 25 x 2^-23.
+constexpr float kSigmoidError = 4.f / 8388608.f, kSoftmaxError = 25.f / 8388608.f;
+
+// A score in F; `top` and `sum` are the softmax's.
+template <typename F>
+__device__ __forceinline__ F score_of(bool sigmoid, float x, float top, F sum)
+{
+    if constexpr (sizeof(F) == 4)
+        return sigmoid ? __fdividef(1.f, 1.f + __expf(-x)) : __fdividef(__expf(x - top), sum);
+    else
+        return sigmoid ? F(1) / (F(1) + exp(-F(x))) : exp(F(x) - F(top)) / sum;
+}
+
+// The warp's choice, one expert after another, formed in F.  Lane j ends with the
+// j-th chosen expert, -1 where there is none.  False: two f32 values that decide
+// something are too close.
 template <typename F, int ET, int VM>
-__device__ __forceinline__ bool choose(const ChooseParams &p, int64_t token, const Layout &at, const float (&x)[VM], float top,
+__device__ __forceinline__ bool choose_in_turn(const ChooseParams &p, int64_t token, const Layout &at, const float (&x)[VM], float top,
                                        float total, int lane, int &id)
 {
     using O = typename OrderOf<F>::type;
@@ -159,14 +183,10 @@ __device__ __forceinline__ bool choose(const ChooseParams &p, int64_t token, con
 #pragma unroll
         for (int i = 0; i < VM; ++i)
             if (x[i] != none)
-                mine += exp_of(F(x[i]) - F(top));
+                mine += exp(F(x[i]) - F(top));
         sum = warp_sum(mine);
     }
-    auto score = [&](float v) {
-        if (p.sigmoid)
-            return F(1) / (F(1) + exp_of(-F(v)));
-        return exp_of(F(v) - F(top)) / sum;
-    };
+    auto score = [&](float v) { return score_of<F>(p.sigmoid, v, top, sum); };
     // Places in order, 0 where there is no expert to choose.
     O c[VM];
     float bias[VM];
@@ -186,11 +206,7 @@ __device__ __forceinline__ bool choose(const ChooseParams &p, int64_t token, con
             return __longlong_as_double(int64_t(b));
         }
     };
-    // The f32 error of a score, or of a sum with one of its magnitude: for the
-    // sigmoid 2^-22 s of the exponential, rounding twice, and the sum's; for the
-    // softmax the exponent's rounding (at most 2^-24 |d| e^-d <= 2^-25 of the largest
-    // score, which is at most 1) and the total's 40 roundings at most, too.
-    const float eps = p.sigmoid ? 9.6e-7f : 6e-6f;  // 2^-20, 100 x 2^-24
+    const float eps = p.sigmoid ? kSigmoidError : kSoftmaxError;
     bool sure = true;
     if (limited) {
         // The group's one or two best: a lane's, then its lanes'.
@@ -278,7 +294,7 @@ __device__ __forceinline__ bool choose(const ChooseParams &p, int64_t token, con
     if (check) {
         const O next = __shfl_down_sync(kAll, mine, 1);
         const float a = float(value_of(mine)), b = float(value_of(next));
-        bool close = lane < p.topk && mine != 0 && next != 0 && a - b <= eps * (1.f + fabsf(a) + fabsf(b));
+        bool close = lane < p.topk && mine != 0 && next != 0 && a - b <= eps * (2.f + fabsf(a) + fabsf(b));
         // Experts alike in logit and bias tie in any arithmetic (but the last one
         // may have more of them after it).
         const float xi = id >= 0 ? logit_at<ET>(p, token, id) : 0.f, bi = id >= 0 ? p.bias[id] : 0.f;
@@ -296,16 +312,215 @@ __device__ __forceinline__ bool choose(const ChooseParams &p, int64_t token, con
     return sure;
 }
 
-// The same in f64, out of the way of the usual one's registers.
+// The one or two largest of a group's lanes' values, in every lane of the group.
+template <typename T>
+__device__ __forceinline__ void best_of_lanes(T &a, T &b, int lanes)
+{
+    for (int d = 1; d < lanes; d <<= 1) {
+        const T a2 = __shfl_xor_sync(kAll, a, d), b2 = __shfl_xor_sync(kAll, b, d);
+        b = max(min(a, a2), max(b, b2));
+        a = max(a, a2);
+    }
+}
+
+// The sum of a group's `best` largest scores (with the bias) in f64, a whole warp
+// for one group.  Sigmoids only.
+template <int ET>
+__device__ __forceinline__ double group_exactly(const ChooseParams &p, int64_t token, int group, int per, int lane)
+{
+    const double none = __longlong_as_double(0xfff0000000000000ll);
+    double a = none, b = none;
+    for (int i = lane; i < per; i += 32) {
+        const int e = group * per + i;
+        const float x = logit_at<ET>(p, token, e), add = p.bias ? p.bias[e] : 0.f;
+        if (x == __uint_as_float(0xff800000u) || add == __uint_as_float(0xff800000u))
+            continue;
+        const double v = score_of<double>(true, x, 0.f, 1.0) + double(add);
+        b = fmax(b, fmin(a, v));
+        a = fmax(a, v);
+    }
+    __syncwarp();
+    best_of_lanes(a, b, 32);
+    return p.best > 1 && b != none ? a + b : a;
+}
+
+// The warp's choice: as choose_in_turn, for what a warp of candidates holds.  `keys`
+// and `names` are the warp's, 32 each.
+enum class Chosen { kYes, kInTurn, kExactly };  // done, too many candidates, f64 is needed for all
+template <int ET, int VM>
+__device__ __forceinline__ Chosen choose(const ChooseParams &p, int64_t token, const Layout &at, const float (&x)[VM],
+                                         const float (&bias)[VM], float top, float total, int lane, uint32_t *keys, int *names,
+                                         int &id)
+{
+    const float none = __uint_as_float(0xff800000u);
+    const bool limited = p.keep < p.groups;
+    const float eps = p.sigmoid ? kSigmoidError : kSoftmaxError;
+    uint32_t c[VM];  // places in order, 0 where there is no expert to choose
+#pragma unroll
+    for (int i = 0; i < VM; ++i) {
+        const bool there = i < at.count && x[i] != none && bias[i] != none;
+        c[i] = !there ? 0u : order_of(p.bias ? score_of<float>(p.sigmoid, x[i], top, total) + bias[i] : x[i]);
+    }
+    if (limited) {
+        uint32_t a = 0, b = 0;
+#pragma unroll
+        for (int i = 0; i < VM; ++i) {
+            b = max(b, min(a, c[i]));
+            a = max(a, c[i]);
+        }
+        best_of_lanes(a, b, at.L);
+        const bool by_score = p.bias || p.best > 1;
+        float v = value_of(a);  // (Without a bias the places are the logits'.)
+        if (by_score && !p.bias)
+            v = score_of<float>(p.sigmoid, v, top, total);
+        if (p.best > 1 && b != 0)
+            v += p.bias ? value_of(b) : score_of<float>(p.sigmoid, value_of(b), top, total);
+        uint32_t g = a == 0 ? 0u : order_of(v);
+        // Lane l < groups holds group l's; its rank.
+        g = __shfl_sync(kAll, g, min(lane, p.groups - 1) * at.L);
+        int before = 0;
+        for (int j = 0; j < p.groups; ++j) {
+            const uint32_t other = __shfl_sync(kAll, g, j);
+            before += other > g || (other == g && j < lane);
+        }
+        const bool mine = lane < p.groups && g != 0;
+        uint32_t mask = __ballot_sync(kAll, mine && before < p.keep);
+        if (by_score) {
+            // The last group kept and the first one not: those within reach of
+            // both are ranked again in f64.
+            const uint32_t in = __ballot_sync(kAll, mine && before == p.keep - 1);
+            const uint32_t out = __ballot_sync(kAll, mine && before == p.keep);
+            if (out != 0) {
+                const float vi = value_of(__shfl_sync(kAll, g, __ffs(in) - 1));
+                const float vo = value_of(__shfl_sync(kAll, g, __ffs(out) - 1));
+                // (Two scores on either side, and their sums' roundings.)
+                const float reach = 4.f * eps + 0.25f * eps * (fabsf(vi) + fabsf(vo));
+                if (!(vi - vo > reach)) {
+                    if (!p.sigmoid)
+                        return Chosen::kExactly;
+                    const float v = value_of(g);
+                    const uint32_t sure = __ballot_sync(kAll, mine && v > vo + reach);
+                    uint32_t open = __ballot_sync(kAll, mine && v <= vo + reach && v >= vi - reach);
+                    double exact = 0.0;
+                    for (uint32_t left = open; left; left &= left - 1) {
+                        const int group = __ffs(left) - 1;
+                        const double d = group_exactly<ET>(p, token, group, at.per, lane);
+                        if (lane == group)
+                            exact = d;
+                    }
+                    int rank = 0;
+                    for (uint32_t left = open; left; left &= left - 1) {
+                        const int j = __ffs(left) - 1;
+                        const double other = __shfl_sync(kAll, exact, j);
+                        rank += other > exact || (other == exact && j < lane);
+                    }
+                    mask = sure | __ballot_sync(kAll, (open >> lane & 1u) && rank < p.keep - __popc(sure));
+                }
+            }
+        }
+        if (!(mask >> (at.group & 31) & 1u)) {
+#pragma unroll
+            for (int i = 0; i < VM; ++i)
+                c[i] = 0;
+        }
+    }
+    // At least `want` experts lie at or above the want-th largest of the lanes'
+    // maxima (equal ones are taken together).  With a bias one more than are
+    // chosen, and what may be as large.
+    const bool check = p.bias != nullptr;
+    const int want = p.topk + (check ? 1 : 0);
+    uint32_t best = 0;
+#pragma unroll
+    for (int i = 0; i < VM; ++i)
+        best = max(best, c[i]);
+    uint32_t low = 1;
+    for (int n = 0; n < want;) {
+        const uint32_t m = warp_max(best);
+        if (m == 0) {
+            low = 1;
+            break;
+        }
+        low = m;
+        n += __popc(__ballot_sync(kAll, best == m));
+        if (best == m)
+            best = 0;
+    }
+    if (check && low > 1) {
+        const float v = value_of(low);
+        low = order_of(v - 3.f * eps - 0.25f * eps * fabsf(v));
+    }
+    int mine = 0;
+#pragma unroll
+    for (int i = 0; i < VM; ++i)
+        mine += c[i] >= low;
+    int before = mine;
+#pragma unroll
+    for (int d = 1; d < 32; d <<= 1) {
+        const int v = __shfl_up_sync(kAll, before, d);
+        if (lane >= d)
+            before += v;
+    }
+    const int n = __shfl_sync(kAll, before, 31);
+    if (n > 32)
+        return Chosen::kInTurn;
+    before -= mine;
+    __syncwarp();
+#pragma unroll
+    for (int i = 0; i < VM; ++i)
+        if (c[i] >= low) {
+            keys[before] = c[i];
+            names[before++] = at.first + i;
+        }
+    __syncwarp();
+    uint32_t key = lane < n ? keys[lane] : 0u;
+    int name = lane < n ? names[lane] : 1 << 30;
+    int rank = 0;
+    for (int j = 0; j < n; ++j) {
+        const uint32_t other = __shfl_sync(kAll, key, j);
+        rank += other > key || (other == key && j < lane);  // (candidates are in order of their numbers)
+    }
+    if (check) {
+        // Sorted, is anyone that is chosen too close to the next?
+        __syncwarp();
+        if (lane < n)
+            keys[rank] = key;
+        __syncwarp();
+        const float a = value_of(key), b = rank + 1 < n ? value_of(keys[rank + 1]) : none;
+        const bool close = lane < n && rank < p.topk && rank + 1 < n && !(a - b > 2.f * eps + 0.25f * eps * (fabsf(a) + fabsf(b)));
+        if (__any_sync(kAll, close)) {
+            if (!p.sigmoid)
+                return Chosen::kExactly;
+            double exact = 0.0;
+            if (lane < n)
+                exact = score_of<double>(true, logit_at<ET>(p, token, name), 0.f, 1.0) + double(p.bias[name]);
+            __syncwarp();
+            rank = 0;
+            for (int j = 0; j < n; ++j) {
+                const double other = __shfl_sync(kAll, exact, j);
+                rank += other > exact || (other == exact && j < lane);
+            }
+        }
+    }
+    __syncwarp();
+    if (lane < n)
+        names[rank] = name;
+    __syncwarp();
+    id = lane < min(n, p.topk) ? names[lane] : -1;
+    return Chosen::kYes;
+}
+
+// One after another, in f32 or (as few tokens need) f64; out of the way of the usual
+// path's registers.
 template <int ET, int VM, bool WIDE>
-__device__ __noinline__ int choose_exactly(const ChooseParams &p, int64_t token, float top, float total)
+__device__ __noinline__ int choose_slowly(const ChooseParams &p, int64_t token, float top, float total, bool exactly)
 {
     const int lane = int(threadIdx.x & 31);
     const Layout at(p.experts, p.groups, VM, lane);
     float x[VM];
     read_logits<ET, VM, WIDE>(p, token, at, x);
     int id;
-    choose<double, ET, VM>(p, token, at, x, top, total, lane, id);
+    if (exactly || !choose_in_turn<float, ET, VM>(p, token, at, x, top, total, lane, id))
+        choose_in_turn<double, ET, VM>(p, token, at, x, top, total, lane, id);
     return id;
 }
 
@@ -314,37 +529,46 @@ __global__ void __launch_bounds__(32 * kChooseWarps, VM == 32 ? 2 : 4) tsm_choos
 {
     chain_next();
     chain_wait();
+    __shared__ uint32_t keys[kChooseWarps][32];
+    __shared__ int names[kChooseWarps][32];
     const int lane = int(threadIdx.x & 31);
     const Layout at(p.experts, p.groups, VM, lane);
     const float none = __uint_as_float(0xff800000u);
+    float bias[VM];
+#pragma unroll
+    for (int i = 0; i < VM; ++i)
+        bias[i] = p.bias && i < at.count ? p.bias[at.first + i] : 0.f;
     const int64_t warps = int64_t(gridDim.x) * kChooseWarps;
     for (int64_t t = int64_t(blockIdx.x) * kChooseWarps + (threadIdx.x >> 5); t < p.tokens; t += warps) {
         float x[VM];
         read_logits<ET, VM, WIDE>(p, t, at, x);
-        bool bad = false;
-        uint32_t high = 0;
+        // (NaN where there is one; absent experts' values are set below.)
+        float seen = 0.f;
 #pragma unroll
-        for (int i = 0; i < VM; ++i) {
-            bad |= is_nan(x[i]) || (i < at.count && p.bias && is_nan(p.bias[at.first + i]));
-            high = max(high, x[i] != none ? order_of(x[i]) : 0u);
-        }
-        float top = 0.f, total = 0.f;
+        for (int i = 0; i < VM; ++i)
+            seen = ptx::max_abs3_nan(seen, i < at.count ? x[i] : 0.f, bias[i]);
+        bool bad = is_nan(seen);
+        float top = 0.f, total = 1.f;
         if (!p.sigmoid) {
-            high = warp_max(high);
-            const uint32_t b = high & 0x80000000u ? high ^ 0x80000000u : ~high;
-            top = high ? __uint_as_float(b) : 0.f;
-            bad |= top == __uint_as_float(0x7f800000u);
+            uint32_t high = 0;
 #pragma unroll
             for (int i = 0; i < VM; ++i)
-                total += expf(x[i] - top);
+                high = max(high, x[i] != none ? order_of(x[i]) : 0u);
+            high = warp_max(high);
+            top = high ? value_of(high) : 0.f;
+            bad |= top == __uint_as_float(0x7f800000u);
+            total = 0.f;
+#pragma unroll
+            for (int i = 0; i < VM; ++i)
+                total += __expf(x[i] - top);
             total = warp_sum(total);
         }
         bad = __any_sync(kAll, bad);
-        int id;
-        if (bad) {
-            id = lane;
-        } else if (!choose<float, ET, VM>(p, t, at, x, top, total, lane, id)) {
-            id = choose_exactly<ET, VM, WIDE>(p, t, top, total);
+        int id = lane;
+        if (!bad) {
+            const Chosen how = choose<ET, VM>(p, t, at, x, bias, top, total, lane, keys[threadIdx.x >> 5], names[threadIdx.x >> 5], id);
+            if (how != Chosen::kYes)
+                id = choose_slowly<ET, VM, WIDE>(p, t, top, total, how == Chosen::kExactly);
         }
         if (lane >= p.topk)
             id = -1;
@@ -354,7 +578,7 @@ __global__ void __launch_bounds__(32 * kChooseWarps, VM == 32 ? 2 : 4) tsm_choos
             // s_j / sum s, with the largest exponential taken out of both.
             const float e = p.sigmoid ? fminf(mine, 0.f) : mine;
             const uint32_t m = warp_max(id >= 0 ? order_of(e) : 0u);
-            const float most = m ? __uint_as_float(m & 0x80000000u ? m ^ 0x80000000u : ~m) : 0.f;
+            const float most = m ? value_of(m) : 0.f;
             if (id >= 0)
                 w = expf(e - most) / (p.sigmoid ? 1.f + expf(-fabsf(mine)) : 1.f);
             const float all = warp_sum(w);
@@ -415,7 +639,7 @@ __global__ void __launch_bounds__(32 * kChooseWarps) tsm_choose_grad_kernel(cons
         if (p.renormalize) {
             const float e = p.sigmoid ? fminf(mine, 0.f) : mine;
             const uint32_t m = warp_max(id >= 0 ? order_of(e) : 0u);
-            const float most = m ? __uint_as_float(m & 0x80000000u ? m ^ 0x80000000u : ~m) : 0.f;
+            const float most = m ? value_of(m) : 0.f;
             float w = 0.f;
             if (id >= 0)
                 w = expf(e - most) / (p.sigmoid ? 1.f + expf(-fabsf(mine)) : 1.f);

@@ -58,12 +58,12 @@ struct Fp4Cfg {
     // TMEM: two accumulators, then the scales at the end.  A pair's accumulators
     // of 256 columns leave no room for them, so the second one starts OVER
     // columns before the first one's end; the epilogue reads those first.
-    static constexpr int SB_COLS = 4 * KT, SA_COLS = 4 * MT * KT;
-    static constexpr int SCALE_COLS = SB_COLS + SA_COLS;
-    static constexpr int RING = PAIR ? 1 : S;            // sets of scales
+    static constexpr int PER = 4 / KT;                   // MMAs that take their scales from one set of tiles
+    static constexpr int SET_COLS = 4 + 4 * MT;          // B's tile, then A's
+    static constexpr int SETS = PAIR ? 4 : S * KT;
     static constexpr int OVER = PAIR ? 48 : 0;
     static constexpr int ACC1 = NT - OVER;
-    static constexpr int SCALE_AT = 512 - RING * SCALE_COLS;
+    static constexpr int SCALE_AT = 512 - SETS * SET_COLS;
     static_assert(ACC1 + NT <= SCALE_AT, "TMEM columns");
     static constexpr int PARTS = 2 * CTAS;
     static constexpr int32_t SLOT = CTAS * NT * COLS;    // floats
@@ -223,7 +223,7 @@ __global__ void __launch_bounds__(kFp4Threads, 1)
         ptx::named_bar_sync(kFp4BarSetup, p.group_rows ? kFp4Threads : kFp4Threads - 32);
         ptx::tc_fence_after_sync();
     }
-    const uint32_t tmem = early ? 0u : ptx::ld_shared_u32(tmem_slot);
+    const uint32_t tmem = early ? 0u : __shfl_sync(0xffffffffu, ptx::ld_shared_u32(tmem_slot), 0);
 
     if (warp == 0) {
         if (lane == 0) {
@@ -283,64 +283,85 @@ __global__ void __launch_bounds__(kFp4Threads, 1)
         }
         __syncwarp();
     } else if (warp == 1) {
-        if (lane == 0 && rank == 0) {
-            // ---------------- MMA issuer
+        if (rank == 0) {
+            // ---------------- MMA issuer: the warp in step, its first lane issues
+            const bool on = lane == 0;
+            const auto wait = [&](bool good) { return __all_sync(0xffffffffu, good) != 0; };
             constexpr uint16_t both = PAIR ? 3 : 1;
-            uint32_t stage = 0, phase = 0, acc = 0, aphase = 0, turn = 0;
+            uint32_t stage = 0, phase = 0, acc = 0, aphase = 0, turn = 0, set = 0;
             bool ok = true;
-            for (PieceWalk<false> w(sched, worker); ok && w.advance(sched);) {
-                ok = s8_wait<PAIR, PAIR>(tempty0 + 8u * acc, aphase ^ 1u, flag, p, kStatusMma);
+            for (PieceWalk<true> w(wsched, worker); ok && w.advance(wsched);) {
+                // Set i of a stage's scales to TMEM (the next set there).
+                auto copy = [&](uint32_t of, int i) {
+                    const uint32_t ssb = base + of * Cfg::STAGE + Cfg::B_BYTES + Cfg::A_BYTES, ssa = ssb + Cfg::SB_BYTES;
+                    const uint32_t to = tmem + Cfg::SCALE_AT + set * uint32_t(Cfg::SET_COLS);
+                    ptx::tmem_cp_scales<PAIR>(on, to, desc_scales(ssb + uint32_t(i * kScaleTile)));
+#pragma unroll
+                    for (int m = 0; m < Cfg::MT; ++m)
+                        ptx::tmem_cp_scales<PAIR>(on, to + uint32_t(4 + 4 * m), desc_scales(ssa + uint32_t((m * Cfg::KT + i) * kScaleTile)));
+                };
+                // The first stage of a piece, and its first scales, before the
+                // accumulator is free.
+                ok = wait(s8_wait<PAIR>(full0 + 8u * stage, phase, flag, p, kStatusMma));
+                if (!ok)
+                    break;
+                ptx::tc_fence_after_sync();
+                copy(stage, 0);
+                ok = wait(s8_wait<PAIR, PAIR>(tempty0 + 8u * acc, aphase ^ 1u, flag, p, kStatusMma));
                 if (PAIR && ok)
-                    ok = s8_wait<PAIR, PAIR>(over, turn ^ 1u, flag, p, kStatusMma);
+                    ok = wait(s8_wait<PAIR, PAIR>(over, turn ^ 1u, flag, p, kStatusMma));
                 if (!ok)
                     break;
                 ptx::tc_fence_after_sync();
                 const uint32_t d = tmem + acc * uint32_t(Cfg::ACC1);
                 for (int32_t kb = w.kb0; kb < w.kb1; ++kb) {
-                    if (!s8_wait<PAIR>(full0 + 8u * stage, phase, flag, p, kStatusMma)) {
-                        ok = false;
-                        break;
-                    }
-                    ptx::tc_fence_after_sync();
                     const uint32_t sb = base + stage * Cfg::STAGE, sa = sb + Cfg::B_BYTES;
-                    const uint32_t ssb = sa + Cfg::A_BYTES, ssa = ssb + Cfg::SB_BYTES;
-                    const uint32_t tsb = tmem + Cfg::SCALE_AT + (stage % Cfg::RING) * uint32_t(Cfg::SCALE_COLS);
-                    const uint32_t tsa = tsb + Cfg::SB_COLS;
-#pragma unroll
-                    for (int i = 0; i < Cfg::KT; ++i) {
-                        ptx::tmem_cp_scales<PAIR>(tsb + 4u * i, desc_scales(ssb + uint32_t(i * kScaleTile)));
-#pragma unroll
-                        for (int m = 0; m < Cfg::MT; ++m)
-                            ptx::tmem_cp_scales<PAIR>(tsa + uint32_t(4 * (i * Cfg::MT + m)),
-                                                      desc_scales(ssa + uint32_t((m * Cfg::KT + i) * kScaleTile)));
-                    }
+                    const uint32_t here = stage, next = stage + 1 == S ? 0u : stage + 1, next_phase = next ? phase : phase ^ 1u;
+                    const bool more = kb + 1 < w.kb1;
                     // (What lies past K is zeros.)
                     const int32_t left = p.K - kb * kFp4BlockK;
 #pragma unroll
-                    for (int kk = 0; kk < 4; ++kk) {
-                        if (64 * kk >= left)
-                            break;
-                        const int i = BLK == 16 ? kk : kk / 2;
-                        const uint32_t id = Cfg::IDESC | (BLK == 32 && (kk & 1) ? Cfg::UPPER : 0u);
-                        ptx::mma_fp4<PAIR, BLK>(d, desc_a(sb + 32u * kk), desc_a(sa + 32u * kk), id, tsb + 4u * i,
-                                                tsa + uint32_t(4 * Cfg::MT * i), (kb > w.kb0 || kk > 0) ? 1u : 0u);
+                    for (int i = 0; i < Cfg::KT; ++i) {
+                        // The next set's copies go before this one's MMAs: the
+                        // tensor pipe takes them in order, and copies that an MMA
+                        // does not wait for run beside it.
+                        const uint32_t tsb = tmem + Cfg::SCALE_AT + set * uint32_t(Cfg::SET_COLS);
+                        if (++set == uint32_t(Cfg::SETS))
+                            set = 0;
+                        if (i + 1 < Cfg::KT) {
+                            copy(here, i + 1);
+                        } else if (more) {
+                            ok = wait(s8_wait<PAIR>(full0 + 8u * next, next_phase, flag, p, kStatusMma));
+                            if (!ok)
+                                break;
+                            ptx::tc_fence_after_sync();
+                            copy(next, 0);
+                        }
+#pragma unroll
+                        for (int m = 0; m < Cfg::PER; ++m) {
+                            const int kk = i * Cfg::PER + m;
+                            if (64 * kk < left)
+                                ptx::mma_fp4<PAIR, BLK>(on, d, desc_a(sb + 32u * kk), desc_a(sa + 32u * kk),
+                                                        Cfg::IDESC | (m ? Cfg::UPPER : 0u), tsb, tsb + 4u,
+                                                        (kb > w.kb0 || kk > 0) ? 1u : 0u);
+                        }
                     }
-                    ptx::mma_commit<PAIR>(empty0 + 8u * stage, both);
-                    if (++stage == S) {
-                        stage = 0;
-                        phase ^= 1u;
-                    }
+                    if (!ok)
+                        break;
+                    ptx::mma_commit_if<PAIR>(on, empty0 + 8u * stage, both);
+                    stage = next;
+                    phase = next_phase;
                 }
                 if (!ok)
                     break;
-                ptx::mma_commit<PAIR>(tfull0 + 8u * acc, both);
+                ptx::mma_commit_if<PAIR>(on, tfull0 + 8u * acc, both);
                 turn ^= 1u;
                 acc ^= 1u;
                 if (acc == 0)
                     aphase ^= 1u;
             }
             // Every MMA must finish before TMEM is freed.
-            ptx::mma_commit<PAIR>(done_bar, 1);
+            ptx::mma_commit_if<PAIR>(on, done_bar, 1);
             s8_wait<PAIR>(done_bar, 0, flag, p, kStatusDrain, false);
         }
         __syncwarp();

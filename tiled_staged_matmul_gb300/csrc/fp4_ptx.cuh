@@ -8,20 +8,26 @@
 namespace tsm {
 namespace ptx {
 
+// The three below are for code that a whole warp runs in step, of which one lane
+// (`on`) issues: their operands are then the warp's, in the registers that the
+// tensor core's instructions take.  (From a branch of one lane each operand is
+// moved there first: three copies and an MMA took 270 cycles to issue.)
+
 // D[tmem] (+)= A[smem desc] x B[smem desc] of e2m1 codes, 64 k, each block of BLK
 // scaled by its rows' scales in TMEM (16: e4m3, four a row; 32: e8m0, two a
 // row); f32 accumulator.  With PAIR each CTA supplies half of A's rows with their
 // scales and half of B's rows; the scales of all of B's rows lie in both.
 template <bool PAIR, int BLK>
-__device__ __forceinline__ void mma_fp4(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc, uint32_t idesc, uint32_t a_scales,
+__device__ __forceinline__ void mma_fp4(bool on, uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc, uint32_t idesc, uint32_t a_scales,
                                         uint32_t b_scales, uint32_t accumulate)
 {
 #define TSM_MMA_FP4(GROUP, VEC)                                                                                            \
-    asm volatile("{\n\t.reg .pred p;\n\t"                                                                                  \
+    asm volatile("{\n\t.reg .pred p, q;\n\t"                                                                               \
                  "setp.ne.b32 p, %4, 0;\n\t"                                                                               \
-                 "tcgen05.mma.cta_group::" GROUP ".kind::mxf4nvf4.block_scale.scale_vec::" VEC " [%0], %1, %2, %3, [%5], [%6], p;\n\t}" ::"r"( \
+                 "setp.ne.b32 q, %7, 0;\n\t"                                                                               \
+                 "@q tcgen05.mma.cta_group::" GROUP ".kind::mxf4nvf4.block_scale.scale_vec::" VEC " [%0], %1, %2, %3, [%5], [%6], p;\n\t}" ::"r"( \
                      d_tmem),                                                                                              \
-                 "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(accumulate), "r"(a_scales), "r"(b_scales)                        \
+                 "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(accumulate), "r"(a_scales), "r"(b_scales), "r"(uint32_t(on))      \
                  : "memory")
     if constexpr (PAIR && BLK == 16)
         TSM_MMA_FP4("2", "4X");
@@ -38,12 +44,34 @@ __device__ __forceinline__ void mma_fp4(uint32_t d_tmem, uint64_t a_desc, uint64
 // the same in each of the four lane quarters.  With PAIR in both CTAs, each from
 // its own shared memory.  Ordered before this thread's later MMAs.
 template <bool PAIR>
-__device__ __forceinline__ void tmem_cp_scales(uint32_t taddr, uint64_t desc)
+__device__ __forceinline__ void tmem_cp_scales(bool on, uint32_t taddr, uint64_t desc)
+{
+#define TSM_CP(GROUP)                                                                                                      \
+    asm volatile("{\n\t.reg .pred q;\n\tsetp.ne.b32 q, %2, 0;\n\t"                                                        \
+                 "@q tcgen05.cp.cta_group::" GROUP ".32x128b.warpx4 [%0], %1;\n\t}" ::"r"(taddr), "l"(desc), "r"(uint32_t(on)) \
+                 : "memory")
+    if constexpr (PAIR)
+        TSM_CP("2");
+    else
+        TSM_CP("1");
+#undef TSM_CP
+}
+
+// As mma_commit.
+template <bool PAIR>
+__device__ __forceinline__ void mma_commit_if(bool on, uint32_t bar, uint16_t cta_mask = 1)
 {
     if constexpr (PAIR)
-        asm volatile("tcgen05.cp.cta_group::2.32x128b.warpx4 [%0], %1;" ::"r"(taddr), "l"(desc) : "memory");
+        asm volatile(
+            "{\n\t.reg .pred q;\n\tsetp.ne.b32 q, %2, 0;\n\t"
+            "@q tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;\n\t}" ::"r"(bar),
+            "h"(cta_mask), "r"(uint32_t(on))
+            : "memory");
     else
-        asm volatile("tcgen05.cp.cta_group::1.32x128b.warpx4 [%0], %1;" ::"r"(taddr), "l"(desc) : "memory");
+        asm volatile("{\n\t.reg .pred q;\n\tsetp.ne.b32 q, %1, 0;\n\t"
+                     "@q tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n\t}" ::"r"(bar),
+                     "r"(uint32_t(on))
+                     : "memory");
 }
 
 // Warp-wide: lane l reads 16 consecutive 32-bit columns of TMEM lane
