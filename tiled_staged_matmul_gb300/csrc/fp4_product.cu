@@ -16,9 +16,15 @@
 //
 // One persistent CTA (or pair) per SM (pair of SMs), warp-specialised:
 //   warp 0      TMA producer: codes of both operands and their scale tiles
-//   warp 1      MMA issuer (the pair's leader): scales to TMEM, four MMAs of 64 k
-//               a stage
-//   warps 2-9   epilogue, two per TMEM lane quarter (half of the rows each)
+//   warp 1      MMA issuer (the pair's leader): four MMAs of 64 k a stage
+//   warp 2      scales to TMEM (the pair's leader)
+//   warps 3-18  epilogue, four per TMEM lane quarter, a quarter of the rows each:
+//               a warp takes all its sums out of TMEM before it works on them, so
+//               that the accumulator is free at once
+// A copy of a scale tile to TMEM takes the tensor core 40 cycles, and a 256 x 256
+// stage with blocks of 16 has twelve, as long as its MMAs.  Copies that the MMAs'
+// own thread issues run one after another with them; those of another thread run
+// beside them (8192^3 296 us so, TODO otherwise), with barriers between the two.
 // Few rows are bound by reading B once; their tiles are cut along K so that
 // every SM reads its share, the f32 sums joined in a fixed order by whoever
 // arrives last.
@@ -30,9 +36,9 @@ namespace tsm {
 
 namespace {
 
-constexpr int kFp4Threads = 320;
-constexpr int kEpiWarps = 8;
-constexpr int kFp4BarGroup = 1, kFp4BarSetup = 3;  // named barriers: two epilogue halves' (1, 2), the setup's
+constexpr int kFirstEpi = 3, kEpiWarps = 16, kEpiGroups = 4;
+constexpr int kFp4Threads = 32 * (kFirstEpi + kEpiWarps);
+constexpr int kFp4BarGroup = 1, kFp4BarSetup = 5;  // named barriers: four epilogue groups' (1 ... 4), the setup's
 
 template <int NT, bool PAIR, int BLK>
 struct Fp4Cfg {
@@ -47,25 +53,26 @@ struct Fp4Cfg {
     static constexpr int SB_BYTES = KT * kScaleTile;
     static constexpr int SA_BYTES = MT * KT * kScaleTile;
     static constexpr int STAGE = B_BYTES + A_BYTES + SB_BYTES + SA_BYTES;
-    static constexpr int HC = NT / 2;                    // rows of one epilogue half
+    static constexpr int HC = NT / kEpiGroups;           // rows of one epilogue group
     static constexpr int TERMS_OFF = 3072;
-    static constexpr int CTRL = TERMS_OFF + 2 * 2 * HC * 4;
+    static constexpr int CTRL = TERMS_OFF + 2 * NT * 4;
     static constexpr int FIT = (232448 - 1024 - CTRL) / STAGE;
     static constexpr int S = FIT > 8 ? 8 : FIT;
     static constexpr int SMEM_BYTES = 1024 + S * STAGE + CTRL;
     static_assert(STAGE % 1024 == 0 && S >= 4, "stages");
     static_assert(SMEM_BYTES > 232448 / 2, "one CTA per SM keeps TMEM allocation uncontended");
-    // TMEM: two accumulators, then the scales at the end.  A pair's accumulators
-    // of 256 columns leave no room for them, so the second one starts OVER
-    // columns before the first one's end; the epilogue reads those first.
-    static constexpr int PER = 4 / KT;                   // MMAs that take their scales from one set of tiles
+    // TMEM: two accumulators, then the scales of two stages.  A pair's accumulators
+    // of 256 columns leave no room for those, so the second one starts OVER
+    // columns before the first one's end.
     static constexpr int SET_COLS = 4 + 4 * MT;          // B's tile, then A's
-    static constexpr int SETS = PAIR ? 4 : S * KT;
-    static constexpr int OVER = PAIR ? 48 : 0;
+    static constexpr int SCALE_COLS = KT * SET_COLS;     // of a stage
+    static constexpr int PER = 4 / KT;                   // MMAs that take their scales from one set of tiles
+    static constexpr int SLOTS = 2;
+    static constexpr int OVER = PAIR ? 96 : 0;
     static constexpr int ACC1 = NT - OVER;
-    static constexpr int SCALE_AT = 512 - SETS * SET_COLS;
+    static constexpr int SCALE_AT = 512 - SLOTS * SCALE_COLS;
     static_assert(ACC1 + NT <= SCALE_AT, "TMEM columns");
-    static constexpr int PARTS = 2 * CTAS;
+    static constexpr int PARTS = kEpiGroups * CTAS;
     static constexpr int32_t SLOT = CTAS * NT * COLS;    // floats
     static constexpr Fp4Kind KIND = PAIR       ? Fp4Kind::kPair
                                     : NT == 32 ? Fp4Kind::kRows32
@@ -90,57 +97,78 @@ __device__ __forceinline__ uint64_t desc_scales(uint32_t saddr)
     return (uint64_t(128 >> 4) << 32) | (uint64_t(1) << 46) | uint64_t((saddr & 0x3FFFFu) >> 4);
 }
 
-// Sixteen rows of the lane's column of C: scaled, biased, activated, stored.
-// `row` the first, `rows` how many there are; sa_at: the rows' scales (alpha in
-// them).  16-bit types go in pairs of columns where they are aligned: neighbour
-// lanes exchange values, so that even lanes store two columns of one row, odd
-// lanes of the next.
-__device__ __forceinline__ void finish_rows(const Fp4Params &p, const float (&acc)[16], uint32_t sa_at, float sb, float bias,
-                                            int32_t z, int32_t row, int32_t rows, int32_t col, int lane)
+// CW rows of a lane's column of C: scaled, biased, activated.  sa_at: the rows' scales
+// (alpha in them).
+template <int CW>
+__device__ __forceinline__ void scale_and_activate(const Fp4Params &p, float (&v)[CW], uint32_t sa_at, float sb, float bias)
 {
-    float v[16];
 #pragma unroll
-    for (int j = 0; j < 16; j += 4) {
+    for (int j = 0; j < CW; j += 4) {
         const uint4 s = ptx::ld_shared_v4(sa_at + 4u * j);
         const uint32_t w[4] = {s.x, s.y, s.z, s.w};
 #pragma unroll
         for (int i = 0; i < 4; ++i)
-            v[j + i] = fmaf(sb, acc[j + i] * __uint_as_float(w[i]), bias);
+            v[j + i] = fmaf(sb, v[j + i] * __uint_as_float(w[i]), bias);
     }
     with_activation<kActRuntime>(p.epi.act, [&](auto act) {
 #pragma unroll
-        for (int j = 0; j < 16; ++j)
+        for (int j = 0; j < CW; ++j)
             v[j] = epi_act(v[j], decltype(act)::value, p.epi.slope);
     });
-    const int64_t at = int64_t(z) * p.sC + int64_t(row) * p.ldc + col;
-    if (p.epi.out_type == kOutF32) {
-        float *c = static_cast<float *>(p.C) + at;
-        if (col < p.N) {
+}
+
+// Stores of a lane's rows of C, `rows` of them from `at` on.
+template <int CW>
+__device__ __forceinline__ void store_f32(const Fp4Params &p, const float (&v)[CW], int64_t at, int32_t rows, int32_t col)
+{
+    float *c = static_cast<float *>(p.C) + at;
+    if (col < p.N) {
 #pragma unroll
-            for (int j = 0; j < 16; ++j, c += p.ldc)
-                if (j < rows)
-                    *c = v[j];
+        for (int j = 0; j < CW; ++j, c += p.ldc)
+            if (j < rows)
+                *c = v[j];
+    }
+}
+
+// 16-bit values, two to a word.  Where C is aligned for it neighbour lanes have
+// exchanged theirs: even lanes hold two columns of one row, odd lanes of the next.
+// Else a word holds two rows of the lane's column.
+template <int CW>
+__device__ __forceinline__ void pack_16(const Fp4Params &p, const float (&v)[CW], uint32_t *two, int lane)
+{
+    const bool odd = lane & 1;
+#pragma unroll
+    for (int j = 0; j < CW; j += 2) {
+        float a = v[j], b = v[j + 1];
+        if (p.vec_c) {
+            const float other = __shfl_xor_sync(0xffffffffu, odd ? a : b, 1);
+            (odd ? a : b) = other;
         }
-    } else if (p.vec_c) {
+        two[j / 2] = out16_pair(a, b, p.epi.out_type);
+    }
+}
+
+template <int CW>
+__device__ __forceinline__ void store_16(const Fp4Params &p, const uint32_t *two, int64_t at, int32_t rows, int32_t col, int lane)
+{
+    uint16_t *c = static_cast<uint16_t *>(p.C) + at;
+    if (p.vec_c) {
         const int odd = lane & 1;
-        uint16_t *c = static_cast<uint16_t *>(p.C) + at - odd + odd * p.ldc;
+        c += odd * (p.ldc - 1);
 #pragma unroll
-        for (int j = 0; j < 16; j += 2, c += 2 * p.ldc) {
-            const float other = __shfl_xor_sync(0xffffffffu, odd ? v[j] : v[j + 1], 1);
-            const uint32_t two = odd ? out16_pair(other, v[j + 1], p.epi.out_type) : out16_pair(v[j], other, p.epi.out_type);
+        for (int j = 0; j < CW; j += 2, c += 2 * p.ldc) {
             if (j + odd < rows) {
                 if ((col | 1) < p.N)
-                    *reinterpret_cast<uint32_t *>(c) = two;
+                    *reinterpret_cast<uint32_t *>(c) = two[j / 2];
                 else if (col - odd < p.N)
-                    *c = uint16_t(two);
+                    *c = uint16_t(two[j / 2]);
             }
         }
     } else if (col < p.N) {
-        uint16_t *c = static_cast<uint16_t *>(p.C) + at;
 #pragma unroll
-        for (int j = 0; j < 16; ++j, c += p.ldc)
+        for (int j = 0; j < CW; ++j, c += p.ldc)
             if (j < rows)
-                *c = uint16_t(epi_out16(v[j], p.epi.out_type));
+                *c = uint16_t(two[j / 2] >> (16 * (j & 1)));
     }
 }
 
@@ -163,11 +191,13 @@ __global__ void __launch_bounds__(kFp4Threads, 1)
     const uint32_t done_bar = ctrl + 168u;     // all MMAs completed
     const uint32_t tmem_slot = ctrl + 176u;
     const uint32_t flag = ctrl + 180u;         // this CTA gives up
-    const uint32_t last_flag = ctrl + 184u;    // [2] one per epilogue half
+    const uint32_t last_flag = ctrl + 184u;    // [4] one per epilogue group
+    const uint32_t sfull0 = ctrl + 200u;       // [2] a stage's scales are in TMEM
+    const uint32_t sdone_bar = ctrl + 216u;    // all copies of scales completed
     const SharedSchedule<false> sched{ctrl + 256u};
     const SharedSchedule<true> wsched{ctrl + 256u};
     const uint32_t gtab = ctrl + 1024u, grows = ctrl + 2048u;
-    const uint32_t terms0 = ctrl + Cfg::TERMS_OFF;  // [2][half][rows' scales]
+    const uint32_t terms0 = ctrl + Cfg::TERMS_OFF;  // [2][group][rows' scales]
 
     const int warp = __shfl_sync(0xffffffffu, int(threadIdx.x >> 5), 0);  // (uniform to the compiler)
     const int lane = int(threadIdx.x & 31);
@@ -182,9 +212,11 @@ __global__ void __launch_bounds__(kFp4Threads, 1)
         for (int b = 0; b < 2; ++b) {
             ptx::mbar_init(tfull0 + 8u * b, 1);
             ptx::mbar_init(tempty0 + 8u * b, kEpiWarps * Cfg::CTAS);
+            ptx::mbar_init(sfull0 + 8u * b, 1);
         }
         ptx::mbar_init(over, kEpiWarps / 2 * Cfg::CTAS);
         ptx::mbar_init(done_bar, 1);
+        ptx::mbar_init(sdone_bar, 1);
         ptx::st_shared_u32(flag, 0u);
         if (!p.group_rows)
             sched.put(p.sched);
@@ -288,25 +320,9 @@ __global__ void __launch_bounds__(kFp4Threads, 1)
             const bool on = lane == 0;
             const auto wait = [&](bool good) { return __all_sync(0xffffffffu, good) != 0; };
             constexpr uint16_t both = PAIR ? 3 : 1;
-            uint32_t stage = 0, phase = 0, acc = 0, aphase = 0, turn = 0, set = 0;
+            uint32_t stage = 0, phase = 0, acc = 0, aphase = 0, turn = 0, slot = 0, sphase = 0;
             bool ok = true;
             for (PieceWalk<true> w(wsched, worker); ok && w.advance(wsched);) {
-                // Set i of a stage's scales to TMEM (the next set there).
-                auto copy = [&](uint32_t of, int i) {
-                    const uint32_t ssb = base + of * Cfg::STAGE + Cfg::B_BYTES + Cfg::A_BYTES, ssa = ssb + Cfg::SB_BYTES;
-                    const uint32_t to = tmem + Cfg::SCALE_AT + set * uint32_t(Cfg::SET_COLS);
-                    ptx::tmem_cp_scales<PAIR>(on, to, desc_scales(ssb + uint32_t(i * kScaleTile)));
-#pragma unroll
-                    for (int m = 0; m < Cfg::MT; ++m)
-                        ptx::tmem_cp_scales<PAIR>(on, to + uint32_t(4 + 4 * m), desc_scales(ssa + uint32_t((m * Cfg::KT + i) * kScaleTile)));
-                };
-                // The first stage of a piece, and its first scales, before the
-                // accumulator is free.
-                ok = wait(s8_wait<PAIR>(full0 + 8u * stage, phase, flag, p, kStatusMma));
-                if (!ok)
-                    break;
-                ptx::tc_fence_after_sync();
-                copy(stage, 0);
                 ok = wait(s8_wait<PAIR, PAIR>(tempty0 + 8u * acc, aphase ^ 1u, flag, p, kStatusMma));
                 if (PAIR && ok)
                     ok = wait(s8_wait<PAIR, PAIR>(over, turn ^ 1u, flag, p, kStatusMma));
@@ -315,42 +331,31 @@ __global__ void __launch_bounds__(kFp4Threads, 1)
                 ptx::tc_fence_after_sync();
                 const uint32_t d = tmem + acc * uint32_t(Cfg::ACC1);
                 for (int32_t kb = w.kb0; kb < w.kb1; ++kb) {
+                    ok = wait(s8_wait<PAIR>(full0 + 8u * stage, phase, flag, p, kStatusMma) &&
+                              s8_wait<PAIR>(sfull0 + 8u * slot, sphase, flag, p, kStatusMma));
+                    if (!ok)
+                        break;
+                    ptx::tc_fence_after_sync();
                     const uint32_t sb = base + stage * Cfg::STAGE, sa = sb + Cfg::B_BYTES;
-                    const uint32_t here = stage, next = stage + 1 == S ? 0u : stage + 1, next_phase = next ? phase : phase ^ 1u;
-                    const bool more = kb + 1 < w.kb1;
+                    const uint32_t scales = tmem + Cfg::SCALE_AT + slot * uint32_t(Cfg::SCALE_COLS);
                     // (What lies past K is zeros.)
                     const int32_t left = p.K - kb * kFp4BlockK;
 #pragma unroll
-                    for (int i = 0; i < Cfg::KT; ++i) {
-                        // The next set's copies go before this one's MMAs: the
-                        // tensor pipe takes them in order, and copies that an MMA
-                        // does not wait for run beside it.
-                        const uint32_t tsb = tmem + Cfg::SCALE_AT + set * uint32_t(Cfg::SET_COLS);
-                        if (++set == uint32_t(Cfg::SETS))
-                            set = 0;
-                        if (i + 1 < Cfg::KT) {
-                            copy(here, i + 1);
-                        } else if (more) {
-                            ok = wait(s8_wait<PAIR>(full0 + 8u * next, next_phase, flag, p, kStatusMma));
-                            if (!ok)
-                                break;
-                            ptx::tc_fence_after_sync();
-                            copy(next, 0);
-                        }
-#pragma unroll
-                        for (int m = 0; m < Cfg::PER; ++m) {
-                            const int kk = i * Cfg::PER + m;
-                            if (64 * kk < left)
-                                ptx::mma_fp4<PAIR, BLK>(on, d, desc_a(sb + 32u * kk), desc_a(sa + 32u * kk),
-                                                        Cfg::IDESC | (m ? Cfg::UPPER : 0u), tsb, tsb + 4u,
-                                                        (kb > w.kb0 || kk > 0) ? 1u : 0u);
-                        }
+                    for (int kk = 0; kk < 4; ++kk) {
+                        const uint32_t tsb = scales + uint32_t(kk / Cfg::PER * Cfg::SET_COLS);
+                        if (64 * kk < left)
+                            ptx::mma_fp4<PAIR, BLK>(on, d, desc_a(sb + 32u * kk), desc_a(sa + 32u * kk),
+                                                    Cfg::IDESC | (kk % Cfg::PER ? Cfg::UPPER : 0u), tsb, tsb + 4u,
+                                                    (kb > w.kb0 || kk > 0) ? 1u : 0u);
                     }
-                    if (!ok)
-                        break;
                     ptx::mma_commit_if<PAIR>(on, empty0 + 8u * stage, both);
-                    stage = next;
-                    phase = next_phase;
+                    if (++stage == S) {
+                        stage = 0;
+                        phase ^= 1u;
+                    }
+                    slot ^= 1u;
+                    if (slot == 0)
+                        sphase ^= 1u;
                 }
                 if (!ok)
                     break;
@@ -365,21 +370,63 @@ __global__ void __launch_bounds__(kFp4Threads, 1)
             s8_wait<PAIR>(done_bar, 0, flag, p, kStatusDrain, false);
         }
         __syncwarp();
+    } else if (warp == 2) {
+        if (rank == 0) {
+            // ---------------- scales to TMEM: the warp in step, as above
+            const bool on = lane == 0;
+            const auto wait = [&](bool good) { return __all_sync(0xffffffffu, good) != 0; };
+            uint32_t stage = 0, phase = 0, slot = 0, count = 0;
+            // The stage before the last one, whose MMAs read the slot that comes
+            // next: its end is that of the slot's use.
+            uint32_t old_stage = 0, old_phase = 0;
+            bool ok = true;
+            for (PieceWalk<true> w(wsched, worker); ok && w.advance(wsched);) {
+                for (int32_t kb = w.kb0; kb < w.kb1; ++kb) {
+                    ok = wait(s8_wait<PAIR>(full0 + 8u * stage, phase, flag, p, kStatusMma) &&
+                              (count < 2 || s8_wait<PAIR>(empty0 + 8u * old_stage, old_phase, flag, p, kStatusMma)));
+                    if (!ok)
+                        break;
+                    ptx::tc_fence_after_sync();
+                    const uint32_t ssb = base + stage * Cfg::STAGE + Cfg::B_BYTES + Cfg::A_BYTES, ssa = ssb + Cfg::SB_BYTES;
+                    const uint32_t to = tmem + Cfg::SCALE_AT + slot * uint32_t(Cfg::SCALE_COLS);
+#pragma unroll
+                    for (int i = 0; i < Cfg::KT; ++i) {
+                        ptx::tmem_cp_scales<PAIR>(on, to + uint32_t(i * Cfg::SET_COLS), desc_scales(ssb + uint32_t(i * kScaleTile)));
+#pragma unroll
+                        for (int m = 0; m < Cfg::MT; ++m)
+                            ptx::tmem_cp_scales<PAIR>(on, to + uint32_t(i * Cfg::SET_COLS + 4 + 4 * m),
+                                                      desc_scales(ssa + uint32_t((m * Cfg::KT + i) * kScaleTile)));
+                    }
+                    ptx::mma_commit_if<PAIR>(on, sfull0 + 8u * slot, 1);
+                    if (++stage == S) {
+                        stage = 0;
+                        phase ^= 1u;
+                    }
+                    slot ^= 1u;
+                    if (++count > 2 && ++old_stage == S) {
+                        old_stage = 0;
+                        old_phase ^= 1u;
+                    }
+                }
+            }
+            // So must every copy.
+            ptx::mma_commit_if<PAIR>(on, sdone_bar, 1);
+            s8_wait<PAIR>(sdone_bar, 0, flag, p, kStatusDrain, false);
+        }
+        __syncwarp();
     } else {
         // ---------------- epilogue
-        constexpr int HC = Cfg::HC, CH = HC / 16;
-        const int h = (warp - 2) >> 2, q = warp & 3;
+        constexpr int HC = Cfg::HC, CW = HC < 16 ? HC : 16;  // (rows worked on at a time)
+        const int h = (warp - kFirstEpi) >> 2, q = warp & 3;
         const int tid = 32 * q + lane;
-        const uint32_t tempty_lead0 = PAIR ? ptx::mapa_shared(tempty0, 0) : tempty0;
-        const uint32_t over_lead = PAIR ? ptx::mapa_shared(over, 0) : over;
-        uint32_t acc = 0, aphase = 0, turn = 0;
+        uint32_t acc = 0, aphase = 0;
         for (PieceWalk<true> w(wsched, worker); w.advance(wsched);) {
             const S8Tile t = tile_at(w.tile, p, gtab, grows, Cfg::TILE_M, Cfg::TILE_N);
             const int32_t col = t.n0 + int32_t(rank) * Cfg::COLS + tid;
             const int32_t row0 = t.m0 + h * HC, rows = t.rows - row0;
-            const uint32_t sa_at = terms0 + (turn * 2u + uint32_t(h)) * uint32_t(4 * HC);
+            const uint32_t sa_at = terms0 + (acc * uint32_t(kEpiGroups) + uint32_t(h)) * uint32_t(4 * HC);
             // The tile's scales and bias, before its sums are there.  (Two sets of
-            // the rows' in turn: the half's other warps may still be at the last
+            // the rows' in turn: the group's other warps may still be at the last
             // tile's.)
             if (tid < HC)
                 ptx::st_shared_u32(sa_at + 4u * uint32_t(tid),
@@ -394,93 +441,93 @@ __global__ void __launch_bounds__(kFp4Threads, 1)
                 break;
             ptx::tc_fence_after_sync();
             const uint32_t from = tmem + (uint32_t(32 * q) << 16) + acc * uint32_t(Cfg::ACC1) + uint32_t(h * HC);
-            // The half that holds the shared columns starts with them: the last
-            // ones of the first accumulator, the first ones of the second.
-            const bool shares = PAIR && h == (acc ? 0 : 1);
-            const bool backwards = PAIR && acc == 0;
-            const uint32_t tempty = tempty_lead0 + 8u * acc;
-            // After chunk i has left TMEM:
-            auto released = [&](int i) {
-                if (PAIR && i == Cfg::OVER / 16 - 1 && shares) {
-                    ptx::tc_fence_before_sync();
-                    __syncwarp();
-                    if (lane == 0)
-                        arrive_leader<PAIR>(over_lead);
-                }
-                if (i == CH - 1) {
-                    ptx::tc_fence_before_sync();
-                    __syncwarp();
-                    if (lane == 0)
-                        arrive_leader<PAIR>(tempty);
+            const int64_t at = int64_t(t.z) * p.sC + int64_t(row0) * p.ldc + col;
+            const bool f32 = p.epi.out_type == kOutF32;
+            // The accumulator has been read.
+            const auto release = [&]() {
+                ptx::tc_fence_before_sync();
+                __syncwarp();
+                if (lane == 0) {
+                    // The columns that both accumulators use are the last ones of
+                    // the first, the first ones of the second.
+                    if (PAIR && (acc ? h * HC < Cfg::OVER : (h + 1) * HC > Cfg::ACC1))
+                        arrive_leader<PAIR>(PAIR ? ptx::mapa_shared(over, 0) : over);
+                    arrive_leader<PAIR>(PAIR ? ptx::mapa_shared(tempty0 + 8u * acc, 0) : tempty0 + 8u * acc);
                 }
             };
-            const float *parts = nullptr;
-            int32_t first = 0, last = -1;
-            const int32_t part_at = (int32_t(rank) * NT + h * HC) * Cfg::COLS + tid;
-            bool mine = true;
-            if (!whole) {
+            if (whole) {
+                // 16-bit results wait in registers until the accumulator is free.
+                uint32_t two[HC / 2];
+#pragma unroll
+                for (int i = 0; i < HC; i += CW)
+                    if (i < rows) {
+                        float v[CW];
+                        ptx::tmem_ld_cols(from + uint32_t(i), v);
+                        scale_and_activate(p, v, sa_at + 4u * uint32_t(i), sb, bias);
+                        if (f32)
+                            store_f32(p, v, at + i * p.ldc, rows - i, col);
+                        else
+                            pack_16(p, v, two + i / 2, lane);
+                    }
+                release();
+                if (!f32)
+                    store_16<HC>(p, two, at, rows, col, lane);
+            } else {
                 // A piece: its sums go to this worker's slot ([row][column]), and
                 // whoever arrives last adds up the contributors', in their order.
                 // A tile's first contributor holds its first block and uses its
                 // second slot; the others start in the tile: their first.
                 const S8Schedule cut = wsched.all();
-                first = cut.owner(w.tile * cut.kb);
-                last = cut.owner((w.tile + 1) * cut.kb - 1);
-                float *const to = p.partial + int64_t(2 * worker + (worker == first)) * Cfg::SLOT + part_at;
+                const int32_t first = cut.owner(w.tile * cut.kb), last = cut.owner((w.tile + 1) * cut.kb - 1);
+                float *const parts = p.partial + (int32_t(rank) * NT + h * HC) * Cfg::COLS + tid;
+                float *const to = parts + int64_t(2 * worker + (worker == first)) * Cfg::SLOT;
 #pragma unroll 1
-                for (int i = 0; i < CH; ++i) {
-                    const int c = backwards ? CH - 1 - i : i;
-                    if (16 * c < rows) {
-                        uint32_t r[16];
-                        ptx::tmem_ld_32x32b_x16(from + 16u * c, r);
-                        ptx::tmem_wait_ld(r);
+                for (int i = 0; i < HC; i += CW)
+                    if (i < rows) {
+                        float v[CW];
+                        ptx::tmem_ld_cols(from + uint32_t(i), v);
 #pragma unroll
-                        for (int j = 0; j < 16; ++j)
-                            __stcg(to + (16 * c + j) * Cfg::COLS, __uint_as_float(r[j]));
+                        for (int j = 0; j < CW; ++j)
+                            if (i + j < rows)
+                                __stcg(to + (i + j) * Cfg::COLS, v[j]);
                     }
-                    released(i);
-                }
+                release();
                 __threadfence();
                 ptx::named_bar_sync(kFp4BarGroup + h, 128);
                 if (q == 0)
-                    ptx::st_shared_u32(last_flag + 4u * h, arrive_last(p.arrivals + w.tile * Cfg::PARTS + int32_t(rank) * 2 + h, p.tag,
-                                                                      uint32_t(last - first + 1), lane));
+                    ptx::st_shared_u32(last_flag + 4u * h, arrive_last(p.arrivals + w.tile * Cfg::PARTS + int32_t(rank) * kEpiGroups + h,
+                                                                      p.tag, uint32_t(last - first + 1), lane));
                 ptx::named_bar_sync(kFp4BarGroup + h, 128);
-                mine = __any_sync(0xffffffffu, ptx::ld_shared_u32(last_flag + 4u * h) != 0);
+                const bool mine = __any_sync(0xffffffffu, ptx::ld_shared_u32(last_flag + 4u * h) != 0);
                 __threadfence();
-                parts = p.partial + part_at;
-            }
-            if (mine) {
+                if (mine) {
 #pragma unroll 1
-                for (int i = 0; i < CH; ++i) {
-                    const int c = backwards ? CH - 1 - i : i;
-                    float v[16];
-                    if (whole) {
-                        uint32_t r[16];
-                        if (16 * c < rows) {
-                            ptx::tmem_ld_32x32b_x16(from + 16u * c, r);
-                            ptx::tmem_wait_ld(r);
+                    for (int i = 0; i < HC; i += CW)
+                        if (i < rows) {
+                            float v[CW];
+#pragma unroll
+                            for (int j = 0; j < CW; ++j)
+                                v[j] = 0.f;
+                            // (Two contributors' loads in flight together.)
+#pragma unroll 2
+                            for (int32_t k = first; k <= last; ++k) {
+                                const float *theirs = parts + int64_t(2 * k + (k == first)) * Cfg::SLOT + i * Cfg::COLS;
+#pragma unroll
+                                for (int j = 0; j < CW; ++j)
+                                    if (i + j < rows)
+                                        v[j] += __ldcg(theirs + j * Cfg::COLS);
+                            }
+                            scale_and_activate(p, v, sa_at + 4u * uint32_t(i), sb, bias);
+                            if (f32) {
+                                store_f32(p, v, at + i * p.ldc, rows - i, col);
+                            } else {
+                                uint32_t two[CW / 2];
+                                pack_16(p, v, two, lane);
+                                store_16<CW>(p, two, at + i * p.ldc, rows - i, col, lane);
+                            }
                         }
-                        released(i);
-#pragma unroll
-                        for (int j = 0; j < 16; ++j)
-                            v[j] = __uint_as_float(r[j]);
-                    } else if (16 * c < rows) {
-#pragma unroll
-                        for (int j = 0; j < 16; ++j)
-                            v[j] = 0.f;
-                        for (int32_t k = first; k <= last; ++k) {
-                            const float *theirs = parts + int64_t(2 * k + (k == first)) * Cfg::SLOT + 16 * c * Cfg::COLS;
-#pragma unroll
-                            for (int j = 0; j < 16; ++j)
-                                v[j] += __ldcg(theirs + j * Cfg::COLS);
-                        }
-                    }
-                    if (16 * c < rows)
-                        finish_rows(p, v, sa_at + 64u * c, sb, bias, t.z, row0 + 16 * c, rows - 16 * c, col, lane);
                 }
             }
-            turn ^= 1u;
             acc ^= 1u;
             if (acc == 0)
                 aphase ^= 1u;

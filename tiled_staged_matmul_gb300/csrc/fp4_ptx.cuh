@@ -76,7 +76,7 @@ __device__ __forceinline__ void mma_commit_if(bool on, uint32_t bar, uint16_t ct
 
 // Warp-wide: lane l reads 16 consecutive 32-bit columns of TMEM lane
 // (taddr.lane + l).
-__device__ __forceinline__ void tmem_ld_32x32b_x16(uint32_t taddr, uint32_t (&r)[16])
+__device__ __forceinline__ void tmem_ld_32x32b_x16(uint32_t taddr, uint32_t *r)
 {
     asm volatile(
         "tcgen05.ld.sync.aligned.32x32b.x16.b32 "
@@ -87,14 +87,26 @@ __device__ __forceinline__ void tmem_ld_32x32b_x16(uint32_t taddr, uint32_t (&r)
         : "memory");
 }
 
-// tcgen05.wait::ld for a load into r: naming r keeps its uses after the wait.
-__device__ __forceinline__ void tmem_wait_ld(uint32_t (&r)[16])
+// N consecutive columns (8, or a multiple of 16) of the lane, complete on return.
+// (Naming the registers after the wait keeps their uses behind it.)
+template <int N>
+__device__ __forceinline__ void tmem_ld_cols(uint32_t taddr, float (&v)[N])
 {
-    asm volatile("tcgen05.wait::ld.sync.aligned;"
-                 : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]), "+r"(r[6]), "+r"(r[7]), "+r"(r[8]),
-                   "+r"(r[9]), "+r"(r[10]), "+r"(r[11]), "+r"(r[12]), "+r"(r[13]), "+r"(r[14]), "+r"(r[15])
-                 :
-                 : "memory");
+    static_assert(N == 8 || N % 16 == 0, "columns");
+    uint32_t r[N];
+    if constexpr (N == 8) {
+        tmem_ld_32x32b_x8(taddr, r);
+    } else {
+#pragma unroll
+        for (int i = 0; i < N; i += 16)
+            tmem_ld_32x32b_x16(taddr + uint32_t(i), r + i);
+    }
+    asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+        asm volatile("" : "+r"(r[i])::"memory");
+        v[i] = __uint_as_float(r[i]);
+    }
 }
 
 // The largest of |a|, |b| and |c|, NaN where one is.
