@@ -36,7 +36,7 @@ namespace tsm {
 
 namespace {
 
-constexpr int kFirstEpi = 3, kEpiWarps = 16, kEpiGroups = 4;
+constexpr int kFirstEpi = 4, kEpiWarps = 16, kEpiGroups = 4;
 constexpr int kFp4Threads = 32 * (kFirstEpi + kEpiWarps);
 constexpr int kFp4BarGroup = 1, kFp4BarSetup = 5;  // named barriers: four epilogue groups' (1 ... 4), the setup's
 
@@ -212,11 +212,11 @@ __global__ void __launch_bounds__(kFp4Threads, 1)
         for (int b = 0; b < 2; ++b) {
             ptx::mbar_init(tfull0 + 8u * b, 1);
             ptx::mbar_init(tempty0 + 8u * b, kEpiWarps * Cfg::CTAS);
-            ptx::mbar_init(sfull0 + 8u * b, 1);
+            ptx::mbar_init(sfull0 + 8u * b, 2);
         }
         ptx::mbar_init(over, kEpiWarps / 2 * Cfg::CTAS);
         ptx::mbar_init(done_bar, 1);
-        ptx::mbar_init(sdone_bar, 1);
+        ptx::mbar_init(sdone_bar, 2);
         ptx::st_shared_u32(flag, 0u);
         if (!p.group_rows)
             sched.put(p.sched);
@@ -370,7 +370,7 @@ __global__ void __launch_bounds__(kFp4Threads, 1)
             s8_wait<PAIR>(done_bar, 0, flag, p, kStatusDrain, false);
         }
         __syncwarp();
-    } else if (warp == 2) {
+    } else if (warp < kFirstEpi) {
         if (rank == 0) {
             // ---------------- scales to TMEM: the warp in step, as above
             const bool on = lane == 0;
@@ -390,7 +390,8 @@ __global__ void __launch_bounds__(kFp4Threads, 1)
                     const uint32_t ssb = base + stage * Cfg::STAGE + Cfg::B_BYTES + Cfg::A_BYTES, ssa = ssb + Cfg::SB_BYTES;
                     const uint32_t to = tmem + Cfg::SCALE_AT + slot * uint32_t(Cfg::SCALE_COLS);
 #pragma unroll
-                    for (int i = 0; i < Cfg::KT; ++i) {
+                    for (int i0 = 0; i0 < Cfg::KT; i0 += 2) {
+                        const int i = i0 + (warp & 1);
                         ptx::tmem_cp_scales<PAIR>(on, to + uint32_t(i * Cfg::SET_COLS), desc_scales(ssb + uint32_t(i * kScaleTile)));
 #pragma unroll
                         for (int m = 0; m < Cfg::MT; ++m)
