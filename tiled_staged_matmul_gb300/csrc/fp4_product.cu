@@ -61,16 +61,19 @@ struct Fp4Cfg {
     static constexpr int SMEM_BYTES = 1024 + S * STAGE + CTRL;
     static_assert(STAGE % 1024 == 0 && S >= 4, "stages");
     static_assert(SMEM_BYTES > 232448 / 2, "one CTA per SM keeps TMEM allocation uncontended");
-    // TMEM: two accumulators, then the scales of two stages.  A pair's accumulators
-    // of 256 columns leave no room for those, so the second one starts OVER
-    // columns before the first one's end.
+    // TMEM: two accumulators, then the scales of a few stages.  A pair's
+    // accumulators of 256 columns leave no room for those, so the second one starts
+    // OVER columns before the first one's end.
     static constexpr int SET_COLS = 4 + 4 * MT;          // B's tile, then A's
     static constexpr int SCALE_COLS = KT * SET_COLS;     // of a stage
     static constexpr int PER = 4 / KT;                   // MMAs that take their scales from one set of tiles
-    static constexpr int SLOTS = 2;
-    static constexpr int OVER = PAIR ? 96 : 0;
+    static constexpr int SLOTS = PAIR && BLK == 16 ? 3 : 4;
+    static constexpr int OVER = PAIR ? SLOTS * SCALE_COLS : 0;
+    // Epilogue groups whose rows' columns both accumulators use.
+    static constexpr int OVER_GROUPS = (OVER + HC - 1) / HC;
     static constexpr int ACC1 = NT - OVER;
     static constexpr int SCALE_AT = 512 - SLOTS * SCALE_COLS;
+    static_assert(SLOTS < S, "a slot's last use is known by its stage's");
     static_assert(ACC1 + NT <= SCALE_AT, "TMEM columns");
     static constexpr int PARTS = kEpiGroups * CTAS;
     static constexpr int32_t SLOT = CTAS * NT * COLS;    // floats
@@ -192,8 +195,8 @@ __global__ void __launch_bounds__(kFp4Threads, 1)
     const uint32_t tmem_slot = ctrl + 176u;
     const uint32_t flag = ctrl + 180u;         // this CTA gives up
     const uint32_t last_flag = ctrl + 184u;    // [4] one per epilogue group
-    const uint32_t sfull0 = ctrl + 200u;       // [2] a stage's scales are in TMEM
-    const uint32_t sdone_bar = ctrl + 216u;    // all copies of scales completed
+    const uint32_t sfull0 = ctrl + 200u;       // [SLOTS] a stage's scales are in TMEM
+    const uint32_t sdone_bar = ctrl + 232u;    // all copies of scales completed
     const SharedSchedule<false> sched{ctrl + 256u};
     const SharedSchedule<true> wsched{ctrl + 256u};
     const uint32_t gtab = ctrl + 1024u, grows = ctrl + 2048u;
@@ -212,9 +215,11 @@ __global__ void __launch_bounds__(kFp4Threads, 1)
         for (int b = 0; b < 2; ++b) {
             ptx::mbar_init(tfull0 + 8u * b, 1);
             ptx::mbar_init(tempty0 + 8u * b, kEpiWarps * Cfg::CTAS);
-            ptx::mbar_init(sfull0 + 8u * b, 2);
         }
-        ptx::mbar_init(over, kEpiWarps / 2 * Cfg::CTAS);
+        for (int i = 0; i < Cfg::SLOTS; ++i)
+            ptx::mbar_init(sfull0 + 8u * i, 2);
+        if (PAIR)
+            ptx::mbar_init(over, 4 * Cfg::OVER_GROUPS * Cfg::CTAS);
         ptx::mbar_init(done_bar, 1);
         ptx::mbar_init(sdone_bar, 2);
         ptx::st_shared_u32(flag, 0u);
@@ -353,9 +358,10 @@ __global__ void __launch_bounds__(kFp4Threads, 1)
                         stage = 0;
                         phase ^= 1u;
                     }
-                    slot ^= 1u;
-                    if (slot == 0)
+                    if (++slot == uint32_t(Cfg::SLOTS)) {
+                        slot = 0;
                         sphase ^= 1u;
+                    }
                 }
                 if (!ok)
                     break;
@@ -376,14 +382,14 @@ __global__ void __launch_bounds__(kFp4Threads, 1)
             const bool on = lane == 0;
             const auto wait = [&](bool good) { return __all_sync(0xffffffffu, good) != 0; };
             uint32_t stage = 0, phase = 0, slot = 0, count = 0;
-            // The stage before the last one, whose MMAs read the slot that comes
-            // next: its end is that of the slot's use.
+            // The stage SLOTS before, whose MMAs read the same slot: where they end
+            // it is free.
             uint32_t old_stage = 0, old_phase = 0;
             bool ok = true;
             for (PieceWalk<true> w(wsched, worker); ok && w.advance(wsched);) {
                 for (int32_t kb = w.kb0; kb < w.kb1; ++kb) {
                     ok = wait(s8_wait<PAIR>(full0 + 8u * stage, phase, flag, p, kStatusMma) &&
-                              (count < 2 || s8_wait<PAIR>(empty0 + 8u * old_stage, old_phase, flag, p, kStatusMma)));
+                              (count < uint32_t(Cfg::SLOTS) || s8_wait<PAIR>(empty0 + 8u * old_stage, old_phase, flag, p, kStatusMma)));
                     if (!ok)
                         break;
                     ptx::tc_fence_after_sync();
@@ -403,8 +409,9 @@ __global__ void __launch_bounds__(kFp4Threads, 1)
                         stage = 0;
                         phase ^= 1u;
                     }
-                    slot ^= 1u;
-                    if (++count > 2 && ++old_stage == S) {
+                    if (++slot == uint32_t(Cfg::SLOTS))
+                        slot = 0;
+                    if (++count > uint32_t(Cfg::SLOTS) && ++old_stage == S) {
                         old_stage = 0;
                         old_phase ^= 1u;
                     }
