@@ -17,10 +17,10 @@
 // One persistent CTA (or pair) per SM (pair of SMs), warp-specialised:
 //   warp 0      TMA producer: codes of both operands and their scale tiles
 //   warp 1      MMA issuer (the pair's leader): four MMAs of 64 k a stage
-//   warp 2      scales to TMEM (the pair's leader)
-//   warps 3-18  epilogue, four per TMEM lane quarter, a quarter of the rows each:
-//               a warp takes all its sums out of TMEM before it works on them, so
-//               that the accumulator is free at once
+//   warps 2, 3  scales to TMEM (the pair's leader)
+//   warps 4-19  epilogue, four per TMEM lane quarter, a quarter of the rows each:
+//               a pair's take the sums out of the columns that the next tile needs
+//               before they work on any
 // A copy of a scale tile to TMEM takes the tensor core 40 cycles, and a 256 x 256
 // stage with blocks of 16 has twelve, as long as its MMAs.  Copies that the MMAs'
 // own thread issues run one after another with them; those of another thread run
@@ -38,7 +38,7 @@ namespace {
 
 constexpr int kFirstEpi = 4, kEpiWarps = 16, kEpiGroups = 4;
 constexpr int kFp4Threads = 32 * (kFirstEpi + kEpiWarps);
-constexpr int kFp4BarGroup = 1, kFp4BarSetup = 5;  // named barriers: four epilogue groups' (1 ... 4), the setup's
+constexpr int kFp4BarGroup = 1, kFp4BarSetup = 5, kFp4BarEpi = 6;  // named barriers: four epilogue groups' (1 ... 4), the setup's, the epilogue's
 
 template <int NT, bool PAIR, int BLK>
 struct Fp4Cfg {
@@ -53,7 +53,11 @@ struct Fp4Cfg {
     static constexpr int SB_BYTES = KT * kScaleTile;
     static constexpr int SA_BYTES = MT * KT * kScaleTile;
     static constexpr int STAGE = B_BYTES + A_BYTES + SB_BYTES + SA_BYTES;
-    static constexpr int HC = NT / kEpiGroups;           // rows of one epilogue group
+    // The epilogue works on CW rows at a time; a group of four warps takes every
+    // fourth such chunk.
+    static constexpr int CW = NT < 64 ? 8 : 16;
+    static constexpr int CHUNKS = NT / CW / kEpiGroups;
+    static_assert(CHUNKS >= 1 && CHUNKS * CW * kEpiGroups == NT, "chunks");
     static constexpr int TERMS_OFF = 3072;
     static constexpr int CTRL = TERMS_OFF + 2 * NT * 4;
     static constexpr int FIT = (232448 - 1024 - CTRL) / STAGE;
@@ -69,8 +73,8 @@ struct Fp4Cfg {
     static constexpr int PER = 4 / KT;                   // MMAs that take their scales from one set of tiles
     static constexpr int SLOTS = PAIR && BLK == 16 ? 3 : 4;
     static constexpr int OVER = PAIR ? SLOTS * SCALE_COLS : 0;
-    // Epilogue groups whose rows' columns both accumulators use.
-    static constexpr int OVER_GROUPS = (OVER + HC - 1) / HC;
+    // A group's chunks in columns that both accumulators use.
+    static constexpr int EARLY = (OVER + CW * kEpiGroups - 1) / (CW * kEpiGroups);
     static constexpr int ACC1 = NT - OVER;
     static constexpr int SCALE_AT = 512 - SLOTS * SCALE_COLS;
     static_assert(SLOTS < S, "a slot's last use is known by its stage's");
@@ -200,7 +204,7 @@ __global__ void __launch_bounds__(kFp4Threads, 1)
     const SharedSchedule<false> sched{ctrl + 256u};
     const SharedSchedule<true> wsched{ctrl + 256u};
     const uint32_t gtab = ctrl + 1024u, grows = ctrl + 2048u;
-    const uint32_t terms0 = ctrl + Cfg::TERMS_OFF;  // [2][group][rows' scales]
+    const uint32_t terms0 = ctrl + Cfg::TERMS_OFF;  // [2][rows' scales]
 
     const int warp = __shfl_sync(0xffffffffu, int(threadIdx.x >> 5), 0);  // (uniform to the compiler)
     const int lane = int(threadIdx.x & 31);
@@ -219,7 +223,7 @@ __global__ void __launch_bounds__(kFp4Threads, 1)
         for (int i = 0; i < Cfg::SLOTS; ++i)
             ptx::mbar_init(sfull0 + 8u * i, 2);
         if (PAIR)
-            ptx::mbar_init(over, 4 * Cfg::OVER_GROUPS * Cfg::CTAS);
+            ptx::mbar_init(over, kEpiWarps * Cfg::CTAS);
         ptx::mbar_init(done_bar, 1);
         ptx::mbar_init(sdone_bar, 2);
         ptx::st_shared_u32(flag, 0u);
@@ -424,62 +428,75 @@ __global__ void __launch_bounds__(kFp4Threads, 1)
         __syncwarp();
     } else {
         // ---------------- epilogue
-        constexpr int HC = Cfg::HC, CW = HC < 16 ? HC : 16;  // (rows worked on at a time)
+        constexpr int CW = Cfg::CW, EARLY = Cfg::EARLY;
         const int h = (warp - kFirstEpi) >> 2, q = warp & 3;
-        const int tid = 32 * q + lane;
         uint32_t acc = 0, aphase = 0;
         for (PieceWalk<true> w(wsched, worker); w.advance(wsched);) {
             const S8Tile t = tile_at(w.tile, p, gtab, grows, Cfg::TILE_M, Cfg::TILE_N);
-            const int32_t col = t.n0 + int32_t(rank) * Cfg::COLS + tid;
-            const int32_t row0 = t.m0 + h * HC, rows = t.rows - row0;
-            const uint32_t sa_at = terms0 + (acc * uint32_t(kEpiGroups) + uint32_t(h)) * uint32_t(4 * HC);
+            const int32_t col = t.n0 + int32_t(rank) * Cfg::COLS + 32 * q + lane;
+            const int32_t rows = t.rows - t.m0;
+            const uint32_t sa0 = terms0 + acc * uint32_t(4 * NT);
             // The tile's scales and bias, before its sums are there.  (Two sets of
-            // the rows' in turn: the group's other warps may still be at the last
-            // tile's.)
-            if (tid < HC)
-                ptx::st_shared_u32(sa_at + 4u * uint32_t(tid),
-                                   __float_as_uint(p.epi.alpha * (p.scale_a && tid < rows ? p.scale_a[t.z * p.sa_stride + row0 + tid] : 1.f)));
+            // the rows' in turn: other warps may still be at the last tile's.)
+            const int32_t tid = int32_t(threadIdx.x) - 32 * kFirstEpi;
+            if (tid < NT)
+                ptx::st_shared_u32(sa0 + 4u * uint32_t(tid),
+                                   __float_as_uint(p.epi.alpha * (p.scale_a && tid < rows ? p.scale_a[t.z * p.sa_stride + t.m0 + tid] : 1.f)));
             const float sb = p.scale_b && col < p.N ? p.scale_b[t.z * p.sb_stride + col] : 1.f;
             const float bias = p.epi.bias && col < p.N ? p.epi.bias[t.z * p.epi.bias_stride + col] : 0.f;
             const bool whole = w.kb1 - w.kb0 == wsched.kb();
             bool ok = s8_wait<PAIR>(tfull0 + 8u * acc, aphase, flag, p, kStatusEpilogue);
-            // The four warps go on or give up together (they meet below).
-            ok = __all_sync(0xffffffffu, ptx::named_bar_and(kFp4BarGroup + h, 128, ok));
+            // The warps go on or give up together (they meet below).
+            ok = __all_sync(0xffffffffu, ptx::named_bar_and(kFp4BarEpi, 32 * kEpiWarps, ok));
             if (!ok)
                 break;
             ptx::tc_fence_after_sync();
-            const uint32_t from = tmem + (uint32_t(32 * q) << 16) + acc * uint32_t(Cfg::ACC1) + uint32_t(h * HC);
-            const int64_t at = int64_t(t.z) * p.sC + int64_t(row0) * p.ldc + col;
-            const bool f32 = p.epi.out_type == kOutF32;
-            // The accumulator has been read.
-            const auto release = [&]() {
+            const uint32_t from = tmem + (uint32_t(32 * q) << 16) + acc * uint32_t(Cfg::ACC1);
+            const int64_t at = int64_t(t.z) * p.sC + int64_t(t.m0) * p.ldc + col;
+            // The group's chunks, those in the columns that both accumulators use
+            // first: the last ones of the first, the first ones of the second.
+            const int set = PAIR && acc == 0 ? kEpiGroups - 1 - h : h;
+            const auto row_of = [&](int i) { return (set + kEpiGroups * (PAIR && acc == 0 ? Cfg::CHUNKS - 1 - i : i)) * CW; };
+            const auto release = [&](uint32_t bar) {
                 ptx::tc_fence_before_sync();
                 __syncwarp();
-                if (lane == 0) {
-                    // The columns that both accumulators use are the last ones of
-                    // the first, the first ones of the second.
-                    if (PAIR && (acc ? h * HC < Cfg::OVER : (h + 1) * HC > Cfg::ACC1))
-                        arrive_leader<PAIR>(PAIR ? ptx::mapa_shared(over, 0) : over);
-                    arrive_leader<PAIR>(PAIR ? ptx::mapa_shared(tempty0 + 8u * acc, 0) : tempty0 + 8u * acc);
+                if (lane == 0)
+                    arrive_leader<PAIR>(PAIR ? ptx::mapa_shared(bar, 0) : bar);
+            };
+            const auto finish = [&](float (&v)[CW], int32_t row) {
+                scale_and_activate(p, v, sa0 + 4u * uint32_t(row), sb, bias);
+                if (p.epi.out_type == kOutF32) {
+                    store_f32(p, v, at + row * p.ldc, rows - row, col);
+                } else {
+                    uint32_t two[CW / 2];
+                    pack_16(p, v, two, lane);
+                    store_16<CW>(p, two, at + row * p.ldc, rows - row, col, lane);
                 }
             };
             if (whole) {
-                // 16-bit results wait in registers until the accumulator is free.
-                uint32_t two[HC / 2];
+                float early[EARLY ? EARLY : 1][CW];
+                if constexpr (EARLY > 0) {
 #pragma unroll
-                for (int i = 0; i < HC; i += CW)
-                    if (i < rows) {
-                        float v[CW];
-                        ptx::tmem_ld_cols(from + uint32_t(i), v);
-                        scale_and_activate(p, v, sa_at + 4u * uint32_t(i), sb, bias);
-                        if (f32)
-                            store_f32(p, v, at + i * p.ldc, rows - i, col);
-                        else
-                            pack_16(p, v, two + i / 2, lane);
+                    for (int i = 0; i < EARLY; ++i)
+                        ptx::tmem_ld_cols(from + uint32_t(row_of(i)), early[i]);
+                    release(over);
+                }
+#pragma unroll
+                for (int i = 0; i < Cfg::CHUNKS; ++i) {
+                    const int32_t row = row_of(i);
+                    float v[CW];
+                    if (i >= EARLY && row < rows)
+                        ptx::tmem_ld_cols(from + uint32_t(row), v);
+                    if (i == Cfg::CHUNKS - 1)
+                        release(tempty0 + 8u * acc);
+                    if (i < EARLY) {
+#pragma unroll
+                        for (int j = 0; j < CW; ++j)
+                            v[j] = early[EARLY ? i : 0][j];
                     }
-                release();
-                if (!f32)
-                    store_16<HC>(p, two, at, rows, col, lane);
+                    if (row < rows)
+                        finish(v, row);
+                }
             } else {
                 // A piece: its sums go to this worker's slot ([row][column]), and
                 // whoever arrives last adds up the contributors', in their order.
@@ -487,31 +504,36 @@ __global__ void __launch_bounds__(kFp4Threads, 1)
                 // second slot; the others start in the tile: their first.
                 const S8Schedule cut = wsched.all();
                 const int32_t first = cut.owner(w.tile * cut.kb), last = cut.owner((w.tile + 1) * cut.kb - 1);
-                float *const parts = p.partial + (int32_t(rank) * NT + h * HC) * Cfg::COLS + tid;
+                float *const parts = p.partial + int32_t(rank) * NT * Cfg::COLS + 32 * q + lane;
                 float *const to = parts + int64_t(2 * worker + (worker == first)) * Cfg::SLOT;
 #pragma unroll 1
-                for (int i = 0; i < HC; i += CW)
-                    if (i < rows) {
+                for (int i = 0; i < Cfg::CHUNKS; ++i) {
+                    const int32_t row = row_of(i);
+                    if (row < rows) {
                         float v[CW];
-                        ptx::tmem_ld_cols(from + uint32_t(i), v);
+                        ptx::tmem_ld_cols(from + uint32_t(row), v);
 #pragma unroll
                         for (int j = 0; j < CW; ++j)
-                            if (i + j < rows)
-                                __stcg(to + (i + j) * Cfg::COLS, v[j]);
+                            if (row + j < rows)
+                                __stcg(to + (row + j) * Cfg::COLS, v[j]);
                     }
-                release();
+                }
+                if (PAIR)
+                    release(over);
+                release(tempty0 + 8u * acc);
                 __threadfence();
                 ptx::named_bar_sync(kFp4BarGroup + h, 128);
                 if (q == 0)
-                    ptx::st_shared_u32(last_flag + 4u * h, arrive_last(p.arrivals + w.tile * Cfg::PARTS + int32_t(rank) * kEpiGroups + h,
+                    ptx::st_shared_u32(last_flag + 4u * h, arrive_last(p.arrivals + w.tile * Cfg::PARTS + int32_t(rank) * kEpiGroups + set,
                                                                       p.tag, uint32_t(last - first + 1), lane));
                 ptx::named_bar_sync(kFp4BarGroup + h, 128);
                 const bool mine = __any_sync(0xffffffffu, ptx::ld_shared_u32(last_flag + 4u * h) != 0);
                 __threadfence();
                 if (mine) {
 #pragma unroll 1
-                    for (int i = 0; i < HC; i += CW)
-                        if (i < rows) {
+                    for (int i = 0; i < Cfg::CHUNKS; ++i) {
+                        const int32_t row = row_of(i);
+                        if (row < rows) {
                             float v[CW];
 #pragma unroll
                             for (int j = 0; j < CW; ++j)
@@ -519,21 +541,15 @@ __global__ void __launch_bounds__(kFp4Threads, 1)
                             // (Two contributors' loads in flight together.)
 #pragma unroll 2
                             for (int32_t k = first; k <= last; ++k) {
-                                const float *theirs = parts + int64_t(2 * k + (k == first)) * Cfg::SLOT + i * Cfg::COLS;
+                                const float *theirs = parts + int64_t(2 * k + (k == first)) * Cfg::SLOT + row * Cfg::COLS;
 #pragma unroll
                                 for (int j = 0; j < CW; ++j)
-                                    if (i + j < rows)
+                                    if (row + j < rows)
                                         v[j] += __ldcg(theirs + j * Cfg::COLS);
                             }
-                            scale_and_activate(p, v, sa_at + 4u * uint32_t(i), sb, bias);
-                            if (f32) {
-                                store_f32(p, v, at + i * p.ldc, rows - i, col);
-                            } else {
-                                uint32_t two[CW / 2];
-                                pack_16(p, v, two, lane);
-                                store_16<CW>(p, two, at + i * p.ldc, rows - i, col, lane);
-                            }
+                            finish(v, row);
                         }
+                    }
                 }
             }
             acc ^= 1u;
