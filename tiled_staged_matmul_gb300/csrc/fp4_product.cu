@@ -124,58 +124,47 @@ __device__ __forceinline__ void scale_and_activate(const Fp4Params &p, float (&v
     });
 }
 
-// Stores of a lane's rows of C, `rows` of them from `at` on.
-template <int CW>
-__device__ __forceinline__ void store_f32(const Fp4Params &p, const float (&v)[CW], int64_t at, int32_t rows, int32_t col)
+// CW values of a lane's column to `rows` rows of C from element `at` on (`left`: the
+// columns that are there from the lane's own on).  16-bit types go in pairs of
+// columns where they are aligned: neighbour lanes exchange values, so that even
+// lanes store two columns of one row, odd lanes of the next.  FULL: all rows and
+// columns are there.
+template <int CW, bool FULL>
+__device__ __forceinline__ void store_rows(const Fp4Params &p, const float (&v)[CW], int64_t at, int32_t rows, int32_t left, int lane)
 {
-    float *c = static_cast<float *>(p.C) + at;
-    if (col < p.N) {
+    if (p.epi.out_type == kOutF32) {
+        float *c = static_cast<float *>(p.C) + at;
+        if (FULL || left > 0) {
 #pragma unroll
-        for (int j = 0; j < CW; ++j, c += p.ldc)
-            if (j < rows)
-                *c = v[j];
-    }
-}
-
-// 16-bit values, two to a word.  Where C is aligned for it neighbour lanes have
-// exchanged theirs: even lanes hold two columns of one row, odd lanes of the next.
-// Else a word holds two rows of the lane's column.
-template <int CW>
-__device__ __forceinline__ void pack_16(const Fp4Params &p, const float (&v)[CW], uint32_t *two, int lane)
-{
-    const bool odd = lane & 1;
-#pragma unroll
-    for (int j = 0; j < CW; j += 2) {
-        float a = v[j], b = v[j + 1];
-        if (p.vec_c) {
-            const float other = __shfl_xor_sync(0xffffffffu, odd ? a : b, 1);
-            (odd ? a : b) = other;
+            for (int j = 0; j < CW; ++j, c += p.ldc)
+                if (FULL || j < rows)
+                    *c = v[j];
         }
-        two[j / 2] = out16_pair(a, b, p.epi.out_type);
+        return;
     }
-}
-
-template <int CW>
-__device__ __forceinline__ void store_16(const Fp4Params &p, const uint32_t *two, int64_t at, int32_t rows, int32_t col, int lane)
-{
     uint16_t *c = static_cast<uint16_t *>(p.C) + at;
     if (p.vec_c) {
         const int odd = lane & 1;
+        const uint32_t halves = odd ? 0x3276u : 0x5410u;
         c += odd * (p.ldc - 1);
 #pragma unroll
         for (int j = 0; j < CW; j += 2, c += 2 * p.ldc) {
-            if (j + odd < rows) {
-                if ((col | 1) < p.N)
-                    *reinterpret_cast<uint32_t *>(c) = two[j / 2];
-                else if (col - odd < p.N)
-                    *c = uint16_t(two[j / 2]);
+            const uint32_t mine = out16_pair(v[j], v[j + 1], p.epi.out_type);
+            const uint32_t two = __byte_perm(mine, __shfl_xor_sync(0xffffffffu, mine, 1), halves);
+            if (FULL) {
+                *reinterpret_cast<uint32_t *>(c) = two;
+            } else if (j + odd < rows) {
+                if (left + odd > 1)
+                    *reinterpret_cast<uint32_t *>(c) = two;
+                else if (left + odd == 1)
+                    *c = uint16_t(two);
             }
         }
-    } else if (col < p.N) {
+    } else if (FULL || left > 0) {
 #pragma unroll
         for (int j = 0; j < CW; ++j, c += p.ldc)
-            if (j < rows)
-                *c = uint16_t(two[j / 2] >> (16 * (j & 1)));
+            if (FULL || j < rows)
+                *c = uint16_t(epi_out16(v[j], p.epi.out_type));
     }
 }
 
@@ -463,15 +452,13 @@ __global__ void __launch_bounds__(kFp4Threads, 1)
                 if (lane == 0)
                     arrive_leader<PAIR>(PAIR ? ptx::mapa_shared(bar, 0) : bar);
             };
+            const bool full_columns = t.n0 + int32_t(rank) * Cfg::COLS + Cfg::COLS <= p.N;
             const auto finish = [&](float (&v)[CW], int32_t row) {
                 scale_and_activate(p, v, sa0 + 4u * uint32_t(row), sb, bias);
-                if (p.epi.out_type == kOutF32) {
-                    store_f32(p, v, at + row * p.ldc, rows - row, col);
-                } else {
-                    uint32_t two[CW / 2];
-                    pack_16(p, v, two, lane);
-                    store_16<CW>(p, two, at + row * p.ldc, rows - row, col, lane);
-                }
+                if (full_columns && row + CW <= rows)
+                    store_rows<CW, true>(p, v, at + row * p.ldc, CW, 0, lane);
+                else
+                    store_rows<CW, false>(p, v, at + row * p.ldc, rows - row, p.N - col, lane);
             };
             if (whole) {
                 float early[EARLY ? EARLY : 1][CW];
@@ -481,7 +468,9 @@ __global__ void __launch_bounds__(kFp4Threads, 1)
                         ptx::tmem_ld_cols(from + uint32_t(row_of(i)), early[i]);
                     release(over);
                 }
-#pragma unroll
+                // (Not unrolled: the warps are out of step, and their instructions
+                // have to stay in the cache.)
+#pragma unroll 1
                 for (int i = 0; i < Cfg::CHUNKS; ++i) {
                     const int32_t row = row_of(i);
                     float v[CW];
@@ -489,11 +478,13 @@ __global__ void __launch_bounds__(kFp4Threads, 1)
                         ptx::tmem_ld_cols(from + uint32_t(row), v);
                     if (i == Cfg::CHUNKS - 1)
                         release(tempty0 + 8u * acc);
-                    if (i < EARLY) {
 #pragma unroll
-                        for (int j = 0; j < CW; ++j)
-                            v[j] = early[EARLY ? i : 0][j];
-                    }
+                    for (int k = 0; k < EARLY; ++k)
+                        if (i == k) {
+#pragma unroll
+                            for (int j = 0; j < CW; ++j)
+                                v[j] = early[k][j];
+                        }
                     if (row < rows)
                         finish(v, row);
                 }
