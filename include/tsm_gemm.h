@@ -521,7 +521,7 @@ gemm_status_t fp4_quantize_rows(const void *X, int32_t elem_type, int32_t block,
 
 /* C[i][j] = act(alpha * scale_a[i] * scale_b[j] * S[i][j] + bias[j]),
  * S[i][j] = sum over k of A[i][k] * sa[i][k / block] * B[j][k] * sb[j][k / block], accumulated in f32
- * by the tensor cores.  S is multiplied by alpha * scale_a[i], then by scale_b[j] with
+ * by the tensor cores.  S is multiplied by scale_a[i], then by alpha * scale_b[j] with
  * bias[j] added in one rounding, and rounded once to the output type.
  *   A, B            device, M and N rows of codes, lda / strideA and ldb / strideB bytes apart
  *   block_scales_a, block_scales_b  device, 16-byte aligned, as described above

@@ -38,7 +38,15 @@ namespace {
 
 constexpr int kFirstEpi = 4, kEpiWarps = 16, kEpiGroups = 4;
 constexpr int kFp4Threads = 32 * (kFirstEpi + kEpiWarps);
-constexpr int kFp4BarGroup = 1, kFp4BarSetup = 5, kFp4BarEpi = 6;  // named barriers: four epilogue groups' (1 ... 4), the setup's, the epilogue's
+constexpr int kFp4BarGroup = 1, kFp4BarSetup = 5;  // named barriers: four epilogue groups' (1 ... 4), the setup's
+// The producer tells the epilogue where its pieces lie: it decodes each once, and
+// ahead of time.  It is at most the ring's stages, two accumulators and the piece in
+// hand ahead, less than this many.
+constexpr int kNotes = 16;
+struct Fp4Note {
+    S8Tile t;
+    int32_t tile, kb0, kb1;  // tile -1: no more
+};
 
 template <int NT, bool PAIR, int BLK>
 struct Fp4Cfg {
@@ -58,8 +66,10 @@ struct Fp4Cfg {
     static constexpr int CW = NT < 64 ? 8 : 16;
     static constexpr int CHUNKS = NT / CW / kEpiGroups;
     static_assert(CHUNKS >= 1 && CHUNKS * CW * kEpiGroups == NT, "chunks");
-    static constexpr int TERMS_OFF = 3072;
-    static constexpr int CTRL = TERMS_OFF + 2 * NT * 4;
+    static constexpr int EPI_ROWS = CHUNKS * CW;         // of one warp
+    static constexpr int NOTES_OFF = 3072, TERMS_OFF = NOTES_OFF + 32 * kNotes;
+    static constexpr int TERMS = EPI_ROWS + 64;          // words of a warp: its rows' scales, its columns' scales and biases
+    static constexpr int CTRL = TERMS_OFF + 2 * kEpiWarps * TERMS * 4;
     static constexpr int FIT = (232448 - 1024 - CTRL) / STAGE;
     static constexpr int S = FIT > 8 ? 8 : FIT;
     static constexpr int SMEM_BYTES = 1024 + S * STAGE + CTRL;
@@ -77,6 +87,7 @@ struct Fp4Cfg {
     static constexpr int EARLY = (OVER + CW * kEpiGroups - 1) / (CW * kEpiGroups);
     static constexpr int ACC1 = NT - OVER;
     static constexpr int SCALE_AT = 512 - SLOTS * SCALE_COLS;
+    static_assert(S + 3 < kNotes, "notes");
     static_assert(SLOTS < S, "a slot's last use is known by its stage's");
     static_assert(ACC1 + NT <= SCALE_AT, "TMEM columns");
     static constexpr int PARTS = kEpiGroups * CTAS;
@@ -104,8 +115,8 @@ __device__ __forceinline__ uint64_t desc_scales(uint32_t saddr)
     return (uint64_t(128 >> 4) << 32) | (uint64_t(1) << 46) | uint64_t((saddr & 0x3FFFFu) >> 4);
 }
 
-// CW rows of a lane's column of C: scaled, biased, activated.  sa_at: the rows' scales
-// (alpha in them).
+// CW rows of a lane's column of C: scaled, biased, activated.  sa_at: the rows'
+// scales; sb: the column's, with alpha in it.
 template <int CW>
 __device__ __forceinline__ void scale_and_activate(const Fp4Params &p, float (&v)[CW], uint32_t sa_at, float sb, float bias)
 {
@@ -193,7 +204,9 @@ __global__ void __launch_bounds__(kFp4Threads, 1)
     const SharedSchedule<false> sched{ctrl + 256u};
     const SharedSchedule<true> wsched{ctrl + 256u};
     const uint32_t gtab = ctrl + 1024u, grows = ctrl + 2048u;
-    const uint32_t terms0 = ctrl + Cfg::TERMS_OFF;  // [2][rows' scales]
+    const uint32_t note0 = ctrl + 320u;        // [kNotes] a note has been written
+    const uint32_t notes = ctrl + Cfg::NOTES_OFF;
+    const uint32_t terms0 = ctrl + Cfg::TERMS_OFF;  // [2][epilogue warp][terms]
 
     const int warp = __shfl_sync(0xffffffffu, int(threadIdx.x >> 5), 0);  // (uniform to the compiler)
     const int lane = int(threadIdx.x & 31);
@@ -211,6 +224,8 @@ __global__ void __launch_bounds__(kFp4Threads, 1)
         }
         for (int i = 0; i < Cfg::SLOTS; ++i)
             ptx::mbar_init(sfull0 + 8u * i, 2);
+        for (int i = 0; i < kNotes; ++i)
+            ptx::mbar_init(note0 + 8u * i, 1);
         if (PAIR)
             ptx::mbar_init(over, kEpiWarps * Cfg::CTAS);
         ptx::mbar_init(done_bar, 1);
@@ -267,8 +282,17 @@ __global__ void __launch_bounds__(kFp4Threads, 1)
                 else
                     ptx::tma_load_3d(to, &map, bar, c0, c1, c2);
             };
+            uint32_t note = 0;
+            const auto tell = [&](const S8Tile &t, int32_t tile, int32_t kb0, int32_t kb1) {
+                const uint32_t to = notes + 32u * (note % kNotes);
+                ptx::st_shared_v4(to, uint32_t(t.m0), uint32_t(t.n0), uint32_t(t.z), uint32_t(t.rows));
+                ptx::st_shared_v4(to + 16u, uint32_t(tile), uint32_t(kb0), uint32_t(kb1), 0u);
+                ptx::mbar_arrive(note0 + 8u * (note % kNotes));
+                ++note;
+            };
             for (PieceWalk<false> w(sched, worker); ok && w.advance(sched);) {
                 const S8Tile t = tile_at(w.tile, p, gtab, grows, Cfg::TILE_M, Cfg::TILE_N);
+                tell(t, w.tile, w.kb0, w.kb1);
                 const int32_t col = t.n0 + int32_t(rank) * Cfg::COLS, row = t.m0 + int32_t(rank) * Cfg::ROWS;
                 const int32_t sb_row = t.z * p.scale_rows_b + col / 128, sa_row = t.z * p.scale_rows_a + t.m0 / 128;
                 for (int32_t kb = w.kb0; kb < w.kb1; ++kb) {
@@ -292,6 +316,7 @@ __global__ void __launch_bounds__(kFp4Threads, 1)
                     }
                 }
             }
+            tell({}, -1, 0, 0);
             if (rank == 0) {
                 // No TMA write into shared memory outlives the CTA (the pair):
                 // the last S loads, the stages from `stage` on, oldest first.
@@ -417,35 +442,66 @@ __global__ void __launch_bounds__(kFp4Threads, 1)
         __syncwarp();
     } else {
         // ---------------- epilogue
-        constexpr int CW = Cfg::CW, EARLY = Cfg::EARLY;
+        constexpr int CW = Cfg::CW, EARLY = Cfg::EARLY, MINE = (Cfg::EPI_ROWS + 31) / 32;
         const int h = (warp - kFirstEpi) >> 2, q = warp & 3;
-        uint32_t acc = 0, aphase = 0;
-        for (PieceWalk<true> w(wsched, worker); w.advance(wsched);) {
-            const S8Tile t = tile_at(w.tile, p, gtab, grows, Cfg::TILE_M, Cfg::TILE_N);
+        uint32_t acc = 0, aphase = 0, note = 0;
+        // The group's chunks of a tile, those in the columns that both accumulators
+        // use first: the last ones of the first, the first ones of the second.
+        const auto row_of = [&](int i, uint32_t a) {
+            return PAIR && a == 0 ? (kEpiGroups * (Cfg::CHUNKS - i) - 1 - h) * CW : (kEpiGroups * i + h) * CW;
+        };
+        const auto terms_of = [&](uint32_t a) {
+            return terms0 + (a * uint32_t(kEpiWarps) + uint32_t(warp - kFirstEpi)) * uint32_t(4 * Cfg::TERMS);
+        };
+        const auto read = [&]() {
+            const uint32_t from = notes + 32u * (note % kNotes);
+            const uint4 x = ptx::ld_shared_v4(from), y = ptx::ld_shared_v4(from + 16u);
+            return Fp4Note{{int32_t(x.x), int32_t(x.y), int32_t(x.z), int32_t(x.w)}, int32_t(y.x), int32_t(y.y), int32_t(y.z)};
+        };
+        // The next piece's scales and bias, on their way while this one's sums are
+        // stored.
+        bool ok = true;
+        const auto look_ahead = [&](uint32_t a) {
+            ok = s8_wait<PAIR>(note0 + 8u * (note % kNotes), (note / kNotes) & 1u, flag, p, kStatusEpilogue);
+            if (!ok)
+                return;
+            const Fp4Note n = read();
+            if (n.tile < 0)
+                return;
+            const int32_t col = n.t.n0 + int32_t(rank) * Cfg::COLS + 32 * q + lane;
+            const uint32_t to = terms_of(a) + 4u * uint32_t(lane);
+#pragma unroll
+            for (int k = 0; k < MINE; ++k) {
+                const int at = 32 * k + lane;
+                const int32_t row = n.t.m0 + row_of(at / CW, a) + at % CW;
+                if (at < Cfg::EPI_ROWS)
+                    ptx::fetch_f32(to + 128u * k, p.scale_a && row < n.t.rows ? p.scale_a + n.t.z * p.sa_stride + row : nullptr, 1.f);
+            }
+            ptx::fetch_f32(to + 4u * Cfg::EPI_ROWS, p.scale_b && col < p.N ? p.scale_b + n.t.z * p.sb_stride + col : nullptr, 1.f);
+            ptx::fetch_f32(to + 4u * Cfg::EPI_ROWS + 128u, p.epi.bias && col < p.N ? p.epi.bias + n.t.z * p.epi.bias_stride + col : nullptr, 0.f);
+        };
+        look_ahead(acc);
+        for (;;) {
+            Fp4Note w = {{}, -1, 0, 0};
+            if (ok)
+                w = read();
+            ++note;
+            ok = w.tile >= 0 && s8_wait<PAIR>(tfull0 + 8u * acc, aphase, flag, p, kStatusEpilogue);
+            // The group's warps go on or stop together (they meet below).
+            if (!__all_sync(0xffffffffu, ptx::named_bar_and(kFp4BarGroup + h, 128, ok)))
+                break;
+            const S8Tile &t = w.t;
             const int32_t col = t.n0 + int32_t(rank) * Cfg::COLS + 32 * q + lane;
             const int32_t rows = t.rows - t.m0;
-            const uint32_t sa0 = terms0 + acc * uint32_t(4 * NT);
-            // The tile's scales and bias, before its sums are there.  (Two sets of
-            // the rows' in turn: other warps may still be at the last tile's.)
-            const int32_t tid = int32_t(threadIdx.x) - 32 * kFirstEpi;
-            if (tid < NT)
-                ptx::st_shared_u32(sa0 + 4u * uint32_t(tid),
-                                   __float_as_uint(p.epi.alpha * (p.scale_a && tid < rows ? p.scale_a[t.z * p.sa_stride + t.m0 + tid] : 1.f)));
-            const float sb = p.scale_b && col < p.N ? p.scale_b[t.z * p.sb_stride + col] : 1.f;
-            const float bias = p.epi.bias && col < p.N ? p.epi.bias[t.z * p.epi.bias_stride + col] : 0.f;
+            ptx::fetch_wait();
+            __syncwarp();
+            const uint32_t sa0 = terms_of(acc);
+            const float sb = p.epi.alpha * __uint_as_float(ptx::ld_shared_u32(sa0 + 4u * uint32_t(Cfg::EPI_ROWS + lane)));
+            const float bias = __uint_as_float(ptx::ld_shared_u32(sa0 + 4u * uint32_t(Cfg::EPI_ROWS + 32 + lane)));
             const bool whole = w.kb1 - w.kb0 == wsched.kb();
-            bool ok = s8_wait<PAIR>(tfull0 + 8u * acc, aphase, flag, p, kStatusEpilogue);
-            // The warps go on or give up together (they meet below).
-            ok = __all_sync(0xffffffffu, ptx::named_bar_and(kFp4BarEpi, 32 * kEpiWarps, ok));
-            if (!ok)
-                break;
             ptx::tc_fence_after_sync();
             const uint32_t from = tmem + (uint32_t(32 * q) << 16) + acc * uint32_t(Cfg::ACC1);
             const int64_t at = int64_t(t.z) * p.sC + int64_t(t.m0) * p.ldc + col;
-            // The group's chunks, those in the columns that both accumulators use
-            // first: the last ones of the first, the first ones of the second.
-            const int set = PAIR && acc == 0 ? kEpiGroups - 1 - h : h;
-            const auto row_of = [&](int i) { return (set + kEpiGroups * (PAIR && acc == 0 ? Cfg::CHUNKS - 1 - i : i)) * CW; };
             const auto release = [&](uint32_t bar) {
                 ptx::tc_fence_before_sync();
                 __syncwarp();
@@ -453,8 +509,8 @@ __global__ void __launch_bounds__(kFp4Threads, 1)
                     arrive_leader<PAIR>(PAIR ? ptx::mapa_shared(bar, 0) : bar);
             };
             const bool full_columns = t.n0 + int32_t(rank) * Cfg::COLS + Cfg::COLS <= p.N;
-            const auto finish = [&](float (&v)[CW], int32_t row) {
-                scale_and_activate(p, v, sa0 + 4u * uint32_t(row), sb, bias);
+            const auto finish = [&](float (&v)[CW], int i, int32_t row) {
+                scale_and_activate(p, v, sa0 + uint32_t(4 * CW * i), sb, bias);
                 if (full_columns && row + CW <= rows)
                     store_rows<CW, true>(p, v, at + row * p.ldc, CW, 0, lane);
                 else
@@ -465,14 +521,15 @@ __global__ void __launch_bounds__(kFp4Threads, 1)
                 if constexpr (EARLY > 0) {
 #pragma unroll
                     for (int i = 0; i < EARLY; ++i)
-                        ptx::tmem_ld_cols(from + uint32_t(row_of(i)), early[i]);
+                        ptx::tmem_ld_cols(from + uint32_t(row_of(i, acc)), early[i]);
                     release(over);
                 }
+                look_ahead(acc ^ 1u);
                 // (Not unrolled: the warps are out of step, and their instructions
                 // have to stay in the cache.)
 #pragma unroll 1
                 for (int i = 0; i < Cfg::CHUNKS; ++i) {
-                    const int32_t row = row_of(i);
+                    const int32_t row = row_of(i, acc);
                     float v[CW];
                     if (i >= EARLY && row < rows)
                         ptx::tmem_ld_cols(from + uint32_t(row), v);
@@ -486,7 +543,7 @@ __global__ void __launch_bounds__(kFp4Threads, 1)
                                 v[j] = early[k][j];
                         }
                     if (row < rows)
-                        finish(v, row);
+                        finish(v, i, row);
                 }
             } else {
                 // A piece: its sums go to this worker's slot ([row][column]), and
@@ -499,7 +556,7 @@ __global__ void __launch_bounds__(kFp4Threads, 1)
                 float *const to = parts + int64_t(2 * worker + (worker == first)) * Cfg::SLOT;
 #pragma unroll 1
                 for (int i = 0; i < Cfg::CHUNKS; ++i) {
-                    const int32_t row = row_of(i);
+                    const int32_t row = row_of(i, acc);
                     if (row < rows) {
                         float v[CW];
                         ptx::tmem_ld_cols(from + uint32_t(row), v);
@@ -512,10 +569,11 @@ __global__ void __launch_bounds__(kFp4Threads, 1)
                 if (PAIR)
                     release(over);
                 release(tempty0 + 8u * acc);
+                look_ahead(acc ^ 1u);
                 __threadfence();
                 ptx::named_bar_sync(kFp4BarGroup + h, 128);
                 if (q == 0)
-                    ptx::st_shared_u32(last_flag + 4u * h, arrive_last(p.arrivals + w.tile * Cfg::PARTS + int32_t(rank) * kEpiGroups + set,
+                    ptx::st_shared_u32(last_flag + 4u * h, arrive_last(p.arrivals + w.tile * Cfg::PARTS + int32_t(rank) * kEpiGroups + (PAIR && acc == 0 ? kEpiGroups - 1 - h : h),
                                                                       p.tag, uint32_t(last - first + 1), lane));
                 ptx::named_bar_sync(kFp4BarGroup + h, 128);
                 const bool mine = __any_sync(0xffffffffu, ptx::ld_shared_u32(last_flag + 4u * h) != 0);
@@ -523,7 +581,7 @@ __global__ void __launch_bounds__(kFp4Threads, 1)
                 if (mine) {
 #pragma unroll 1
                     for (int i = 0; i < Cfg::CHUNKS; ++i) {
-                        const int32_t row = row_of(i);
+                        const int32_t row = row_of(i, acc);
                         if (row < rows) {
                             float v[CW];
 #pragma unroll
@@ -538,7 +596,7 @@ __global__ void __launch_bounds__(kFp4Threads, 1)
                                     if (row + j < rows)
                                         v[j] += __ldcg(theirs + j * Cfg::COLS);
                             }
-                            finish(v, row);
+                            finish(v, i, row);
                         }
                     }
                 }
@@ -547,6 +605,7 @@ __global__ void __launch_bounds__(kFp4Threads, 1)
             if (acc == 0)
                 aphase ^= 1u;
         }
+        ptx::fetch_wait();
     }
 
     ptx::tc_fence_before_sync();
