@@ -203,6 +203,10 @@ using namespace tsm;
 
 int main()
 {
+    Fp4Capacity cap;
+    for (auto &kind : cap.clusters)
+        for (int i = 0; i < Fp4Capacity::RANKS; ++i)
+            kind[i] = 152 / (i + 1);
     long long M, N, K, batch, lda, ldb, a, b, grouped;
     while (std::scanf("%lld %lld %lld %lld %lld %lld %lld %lld %lld", &M, &N, &K, &batch, &lda, &ldb, &a, &b, &grouped) == 9) {
         static const int32_t counts[1] = {0};
@@ -214,7 +218,7 @@ int main()
         p.group_rows = grouped ? counts : nullptr;
         Fp4Plan s;
         const bool ok = s.make(p, reinterpret_cast<const uint8_t *>(a), lda, M * lda, reinterpret_cast<const uint8_t *>(b), ldb,
-                               N * ldb, 152);
+                               N * ldb, 152, cap);
         // Every worker's piece lies in at most two tiles of its own to sum, and
         // the pieces together are the cut tiles.
         bool sound = true;
@@ -226,14 +230,14 @@ int main()
                 sound = sound && begin < end && end - begin < 2 * s.kb && s.sched.owner(begin) == w && s.sched.owner(end - 1) == w;
             }
         }
-        std::printf("%d %d %d %d %d %d %d %d %lld %lld %lld %lld %d\n", int(ok), int(s.kind), s.tiles_m, s.tiles_n, s.kb, s.grid,
+        std::printf("%d %d %d %d %d %d %d %d %d %lld %lld %lld %lld %d\n", int(ok), int(s.kind), s.tiles_m, s.tiles_n, s.kb, s.ranks, s.grid,
                     int(s.sched.shared), int(s.sched.cutters), (long long)s.bytes_a, (long long)s.bytes_b, (long long)s.bytes_p,
                     (long long)s.bytes_w, int(sound));
     }
     return 0;
 }
 """
-FIELDS = ("ok", "kind", "tiles_m", "tiles_n", "kb", "grid", "shared", "cutters", "bytes_a", "bytes_b", "bytes_p", "bytes_w",
+FIELDS = ("ok", "kind", "tiles_m", "tiles_n", "kb", "ranks", "grid", "shared", "cutters", "bytes_a", "bytes_b", "bytes_p", "bytes_w",
           "sound")
 
 
@@ -258,7 +262,7 @@ def test_plans_are_sound(plans):
     """Over all kinds of sizes: the schedule covers the work, the workspace holds
     every worker's two slots, and copies are made where they are needed only."""
     slot = (16384, 32768, 65536, 262144)
-    parts = (2, 2, 2, 4)
+    parts = (4, 4, 4, 8)
     sizes = [(M, N, K) for M in (1, 16, 32, 33, 64, 65, 128, 129, 1000, 8191) for N in (1, 128, 1000, 14336)
              for K in (1, 256, 4010, 16384, 1 << 23)]
     for grouped in (0, 1):
@@ -268,7 +272,9 @@ def test_plans_are_sound(plans):
             assert s["bytes_a"] == 0 and s["bytes_b"] == 0
             k = s["kind"]
             workers = 76 if k == 3 else 152
-            assert s["grid"] <= workers
+            assert s["grid"] * s["ranks"] <= workers
+            assert s["ranks"] == 1 or (s["shared"] == 0 and s["grid"] == s["tiles_m"] * s["tiles_n"] * p[3]
+                                       and s["kb"] >= 2 * s["ranks"] and k < 3 and not grouped)
             if grouped:
                 assert s["grid"] == workers and s["bytes_p"] == 2 * workers * slot[k]
             if s["shared"] or grouped:

@@ -190,6 +190,7 @@ namespace {
 
 std::once_flag g_fp4_once[64];
 cudaError_t g_fp4_error[64];
+Fp4Capacity g_fp4_capacity[64];
 
 // The operands of a product, beside its Fp4Params.
 struct Fp4Operands {
@@ -246,17 +247,18 @@ gemm_status_t launch_product(Fp4Params p, Fp4Operands o, DeviceState *ds, cudaSt
     int dev = 0;
     if ((e = cudaGetDevice(&dev)) != cudaSuccess)
         return fail_cuda(e, "cudaGetDevice");
-    std::call_once(g_fp4_once[dev], [dev] { g_fp4_error[dev] = set_fp4_attributes(); });
+    std::call_once(g_fp4_once[dev], [dev] { g_fp4_error[dev] = set_fp4_attributes(&g_fp4_capacity[dev]); });
     if (g_fp4_error[dev] != cudaSuccess)
         return fail_cuda(g_fp4_error[dev], "setting up the 4-bit product kernels");
 
     Fp4Plan plan;
-    if (!plan.make(p, o.A, o.lda, o.sA, o.B, o.ldb, o.sB, ds->sms))
+    if (!plan.make(p, o.A, o.lda, o.sA, o.B, o.ldb, o.sB, ds->sms, g_fp4_capacity[dev]))
         return fail(GEMM_ERR_INVALID_VALUE, "more than 2^30 output tiles in one call");
     p.tiles_m = plan.tiles_m;
     p.tiles_n = plan.tiles_n;
     p.kb = plan.kb;
     p.workers = plan.workers;
+    p.ranks = plan.ranks;
     p.sched = plan.sched;
     p.sched_price = plan.shape.price;
     p.sched_part = plan.shape.part;

@@ -44,6 +44,7 @@ struct Fp4Params {
     int32_t tiles_m, tiles_n, kb;
     S8Schedule sched;           // unless grouped (then it is made on the device)
     int32_t workers;
+    int32_t ranks;              // CTAs (a cluster) that cut a tile's K; 1: the schedule's pieces
     int32_t sched_price, sched_part;
     int32_t scale_rows_a, scale_rows_b;  // rows of scale tiles in a matrix
     int32_t vec_c;              // C's rows are 4-byte aligned (16-bit types: stored in pairs)
@@ -71,7 +72,12 @@ constexpr int kFp4BlockK = 256;  // k of one stage: 128 bytes of a row
 struct Fp4Maps {
     CUtensorMap a, b, scales_a, scales_b;
 };
-cudaError_t set_fp4_attributes();
+// Clusters of 1 to 8 CTAs of the kernels of one CTA that fit on the device at once.
+struct Fp4Capacity {
+    static constexpr int RANKS = 8;
+    int clusters[3][RANKS];
+};
+cudaError_t set_fp4_attributes(Fp4Capacity *cap);
 cudaError_t launch_fp4(const Fp4Maps &maps, const Fp4Params &p, Fp4Kind kind, int block, int grid, cudaStream_t stream);
 
 // ------------------------------------------------------------- choice of experts

@@ -16,7 +16,8 @@ struct Fp4Plan {
     Fp4Shape shape;
     int32_t tiles_m, tiles_n, kb;
     int32_t workers;            // CTAs, or pairs, that share a launch
-    int grid;
+    int32_t ranks;              // CTAs of a cluster that cuts a tile's K
+    int grid;                   // workers, or clusters
     S8Schedule sched;           // not grouped
     bool pack_a, pack_b;        // copied to rows lda2 / ldb2 bytes apart first
     int64_t lda2, ldb2;
@@ -24,7 +25,8 @@ struct Fp4Plan {
     int64_t bytes_a, bytes_b, bytes_p, bytes_w;
 
     // False: more tiles than a launch can count.
-    bool make(const Fp4Params &p, const uint8_t *A, int64_t lda, int64_t sA, const uint8_t *B, int64_t ldb, int64_t sB, int sms)
+    bool make(const Fp4Params &p, const uint8_t *A, int64_t lda, int64_t sA, const uint8_t *B, int64_t ldb, int64_t sB, int sms,
+              const Fp4Capacity &cap)
     {
         *this = {};
         kind = p.M <= 32 ? Fp4Kind::kRows32 : p.M <= 64 ? Fp4Kind::kRows64 : p.M <= 128 ? Fp4Kind::kRows128 : Fp4Kind::kPair;
@@ -37,9 +39,17 @@ struct Fp4Plan {
         const int64_t tiles = int64_t(tiles_m) * tiles_n * p.batch;
         if (tiles > S8Schedule::kMaxTiles)
             return false;
+        // As many CTAs to a tile as leave all tiles in one round.
+        ranks = 1;
+        for (int r = 2; kind != Fp4Kind::kPair && !p.group_rows && r <= Fp4Capacity::RANKS && 2 * r <= kb; ++r)
+            if (tiles <= cap.clusters[int(kind)][r - 1])
+                ranks = r;
         sched.plan(int32_t(tiles), kb, workers, shape.price, shape.part);
+        if (ranks > 1)
+            sched.shared = 0;
         grid = p.group_rows
                    ? workers
+               : ranks > 1 ? int(tiles)
                    : int(std::max<int64_t>(sched.shared ? sched.cutters : 0, std::min<int64_t>(sched.tiles, workers)));
         const int64_t width = (int64_t(p.K) + 1) / 2;
         pack_a = !addressable(reinterpret_cast<const int8_t *>(A), lda, sA, p.M, p.batch);

@@ -25,9 +25,11 @@
 // stage with blocks of 16 has twelve, as long as its MMAs.  Copies that the MMAs'
 // own thread issues run one after another with them; those of another thread run
 // beside them (8192^3 296 us so, TODO otherwise), with barriers between the two.
-// Few rows are bound by reading B once; their tiles are cut along K so that
-// every SM reads its share, the f32 sums joined in a fixed order by whoever
-// arrives last.
+// Few rows are bound by reading B once.  Where their tiles are few, too, a tile's K
+// is cut over a cluster, whose CTAs add up each other's sums through distributed
+// shared memory (1 x 4096 x 4096: TODO); else tiles of a last wave that costs too
+// much are cut over the SMs, their sums joined through memory by whoever arrives
+// last.  Either way in a fixed order.
 #include "fp4_internal.h"
 #include "fp4_ptx.cuh"
 #include "s8_common.cuh"
@@ -106,6 +108,36 @@ struct Fp4Cfg {
     static constexpr uint32_t IDESC = (1u << 7) | (1u << 10) | (uint32_t(NT >> 3) << 17) | (uint32_t(BLK == 32) << 23) |
                                       (uint32_t(COLS * CTAS >> 4) << 24);
     static constexpr uint32_t UPPER = (2u << 4) | (2u << 29);
+};
+
+// A CTA's (or pair's) pieces: the schedule's or, in a cluster that cuts a tile's K,
+// the CTA's share of the cluster's one tile.
+template <bool WARP>
+struct Fp4Walk {
+    PieceWalk<WARP> w;
+    int32_t tile, kb0, kb1;
+    bool split;
+    __device__ __forceinline__ Fp4Walk(const SharedSchedule<WARP> &shared, const Fp4Params &p, int32_t worker)
+        : w(shared, worker), tile(-1), kb0(0), kb1(0), split(p.ranks > 1)
+    {
+    }
+    __device__ __forceinline__ bool advance(const SharedSchedule<WARP> &shared, const Fp4Params &p)
+    {
+        if (split) {
+            if (tile >= 0)
+                return false;
+            const int32_t rank = int32_t(ptx::cluster_ctarank());
+            tile = int32_t(ptx::cluster_id());
+            kb0 = rank * p.kb / p.ranks;
+            kb1 = (rank + 1) * p.kb / p.ranks;
+            return true;
+        }
+        const bool more = w.advance(shared);
+        tile = w.tile;
+        kb0 = w.kb0;
+        kb1 = w.kb1;
+        return more;
+    }
 };
 
 // Shared-memory descriptor of a scale tile: 32 rows of 16 bytes, no swizzle,
@@ -205,6 +237,7 @@ __global__ void __launch_bounds__(kFp4Threads, 1)
     const SharedSchedule<true> wsched{ctrl + 256u};
     const uint32_t gtab = ctrl + 1024u, grows = ctrl + 2048u;
     const uint32_t note0 = ctrl + 320u;        // [kNotes] a note has been written
+    const uint32_t sums0 = ctrl + 512u;        // [epilogue warp] a cluster's CTAs' sums are in shared memory
     const uint32_t notes = ctrl + Cfg::NOTES_OFF;
     const uint32_t terms0 = ctrl + Cfg::TERMS_OFF;  // [2][epilogue warp][terms]
 
@@ -226,6 +259,8 @@ __global__ void __launch_bounds__(kFp4Threads, 1)
             ptx::mbar_init(sfull0 + 8u * i, 2);
         for (int i = 0; i < kNotes; ++i)
             ptx::mbar_init(note0 + 8u * i, 1);
+        for (int i = 0; !PAIR && i < kEpiWarps; ++i)
+            ptx::mbar_init(sums0 + 8u * i, uint32_t(p.ranks));
         if (PAIR)
             ptx::mbar_init(over, kEpiWarps * Cfg::CTAS);
         ptx::mbar_init(done_bar, 1);
@@ -241,7 +276,8 @@ __global__ void __launch_bounds__(kFp4Threads, 1)
     }
     __syncwarp();
     ptx::cta_sync();  // the barriers are there
-    if constexpr (PAIR)
+    const bool split = !PAIR && p.ranks > 1;
+    if (PAIR || split)
         ptx::cluster_arrive_relaxed();
     chain_next();
     if constexpr (PAIR)
@@ -290,7 +326,7 @@ __global__ void __launch_bounds__(kFp4Threads, 1)
                 ptx::mbar_arrive(note0 + 8u * (note % kNotes));
                 ++note;
             };
-            for (PieceWalk<false> w(sched, worker); ok && w.advance(sched);) {
+            for (Fp4Walk<false> w(sched, p, worker); ok && w.advance(sched, p);) {
                 const S8Tile t = tile_at(w.tile, p, gtab, grows, Cfg::TILE_M, Cfg::TILE_N);
                 tell(t, w.tile, w.kb0, w.kb1);
                 const int32_t col = t.n0 + int32_t(rank) * Cfg::COLS, row = t.m0 + int32_t(rank) * Cfg::ROWS;
@@ -345,7 +381,7 @@ __global__ void __launch_bounds__(kFp4Threads, 1)
             constexpr uint16_t both = PAIR ? 3 : 1;
             uint32_t stage = 0, phase = 0, acc = 0, aphase = 0, turn = 0, slot = 0, sphase = 0;
             bool ok = true;
-            for (PieceWalk<true> w(wsched, worker); ok && w.advance(wsched);) {
+            for (Fp4Walk<true> w(wsched, p, worker); ok && w.advance(wsched, p);) {
                 ok = wait(s8_wait<PAIR, PAIR>(tempty0 + 8u * acc, aphase ^ 1u, flag, p, kStatusMma));
                 if (PAIR && ok)
                     ok = wait(s8_wait<PAIR, PAIR>(over, turn ^ 1u, flag, p, kStatusMma));
@@ -404,7 +440,7 @@ __global__ void __launch_bounds__(kFp4Threads, 1)
             // it is free.
             uint32_t old_stage = 0, old_phase = 0;
             bool ok = true;
-            for (PieceWalk<true> w(wsched, worker); ok && w.advance(wsched);) {
+            for (Fp4Walk<true> w(wsched, p, worker); ok && w.advance(wsched, p);) {
                 for (int32_t kb = w.kb0; kb < w.kb1; ++kb) {
                     ok = wait(s8_wait<PAIR>(full0 + 8u * stage, phase, flag, p, kStatusMma) &&
                               (count < uint32_t(Cfg::SLOTS) || s8_wait<PAIR>(empty0 + 8u * old_stage, old_phase, flag, p, kStatusMma)));
@@ -445,6 +481,7 @@ __global__ void __launch_bounds__(kFp4Threads, 1)
         constexpr int CW = Cfg::CW, EARLY = Cfg::EARLY, MINE = (Cfg::EPI_ROWS + 31) / 32;
         const int h = (warp - kFirstEpi) >> 2, q = warp & 3;
         uint32_t acc = 0, aphase = 0, note = 0;
+        bool met = !split;
         // The group's chunks of a tile, those in the columns that both accumulators
         // use first: the last ones of the first, the first ones of the second.
         const auto row_of = [&](int i, uint32_t a) {
@@ -498,7 +535,7 @@ __global__ void __launch_bounds__(kFp4Threads, 1)
             const uint32_t sa0 = terms_of(acc);
             const float sb = p.epi.alpha * __uint_as_float(ptx::ld_shared_u32(sa0 + 4u * uint32_t(Cfg::EPI_ROWS + lane)));
             const float bias = __uint_as_float(ptx::ld_shared_u32(sa0 + 4u * uint32_t(Cfg::EPI_ROWS + 32 + lane)));
-            const bool whole = w.kb1 - w.kb0 == wsched.kb();
+            const bool whole = w.kb1 - w.kb0 == p.kb;
             ptx::tc_fence_after_sync();
             const uint32_t from = tmem + (uint32_t(32 * q) << 16) + acc * uint32_t(Cfg::ACC1);
             const int64_t at = int64_t(t.z) * p.sC + int64_t(t.m0) * p.ldc + col;
@@ -545,6 +582,51 @@ __global__ void __launch_bounds__(kFp4Threads, 1)
                     if (row < rows)
                         finish(v, i, row);
                 }
+            } else if (split) {
+                // A share of the tile's K.  The sums go to the ring's place in shared
+                // memory ([row][column]; all of this CTA's MMAs are done with it), each
+                // chunk is added up by one CTA, in the order of K, by the warp that
+                // has the same columns and rows in each.
+                ptx::cluster_wait();  // the others are there, and their barriers
+                met = true;
+                const uint32_t mine = base + uint32_t(32 * q + lane) * 4u;
+#pragma unroll 1
+                for (int i = 0; i < Cfg::CHUNKS; ++i) {
+                    const int32_t row = row_of(i, acc);
+                    if (row < rows) {
+                        float v[CW];
+                        ptx::tmem_ld_cols(from + uint32_t(row), v);
+#pragma unroll
+                        for (int j = 0; j < CW; ++j)
+                            ptx::st_shared_u32(mine + uint32_t(row + j) * 512u, __float_as_uint(v[j]));
+                    }
+                }
+                __syncwarp();
+                const uint32_t bar = sums0 + 8u * uint32_t(warp - kFirstEpi);
+                if (lane < p.ranks)
+                    ptx::mbar_arrive_cluster(ptx::mapa_shared(bar, uint32_t(lane)));
+                ok = __all_sync(0xffffffffu, s8_wait<PAIR, true>(bar, 0, flag, p, kStatusReduce));
+#pragma unroll 1
+                for (int i = 0; ok && i < Cfg::CHUNKS; ++i) {
+                    const int32_t row = row_of(i, acc);
+                    if (row < rows && (row / CW) % p.ranks == int32_t(ptx::cluster_ctarank())) {
+                        float v[CW];
+#pragma unroll
+                        for (int j = 0; j < CW; ++j)
+                            v[j] = 0.f;
+                        // (Four CTAs' loads in flight together.)
+#pragma unroll 4
+                        for (int32_t r = 0; r < p.ranks; ++r) {
+                            const uint32_t theirs = ptx::mapa_shared(mine + uint32_t(row) * 512u, uint32_t(r));
+#pragma unroll
+                            for (int j = 0; j < CW; ++j)
+                                if (row + j < rows)
+                                    v[j] += __uint_as_float(ptx::ld_cluster_u32(theirs + 512u * uint32_t(j)));
+                        }
+                        finish(v, i, row);
+                    }
+                }
+                look_ahead(acc ^ 1u);
             } else {
                 // A piece: its sums go to this worker's slot ([row][column]), and
                 // whoever arrives last adds up the contributors', in their order.
@@ -606,12 +688,16 @@ __global__ void __launch_bounds__(kFp4Threads, 1)
                 aphase ^= 1u;
         }
         ptx::fetch_wait();
+        if (!met)
+            ptx::cluster_wait();
     }
 
     ptx::tc_fence_before_sync();
+    if (split && warp < kFirstEpi)
+        ptx::cluster_wait();  // (the meeting that began at the start; the epilogue's warps have been there)
     ptx::cta_sync();
-    if constexpr (PAIR)
-        ptx::cluster_sync();
+    if (PAIR || split)
+        ptx::cluster_sync();  // no CTA leaves while another may still read its sums or signal it
     if (warp == 1) {
         __syncwarp();
         ptx::tc_fence_after_sync();
@@ -638,14 +724,31 @@ cudaError_t with_kind(Fp4Kind kind, F &&fn)
 
 }  // namespace
 
-cudaError_t set_fp4_attributes()
+cudaError_t set_fp4_attributes(Fp4Capacity *cap)
 {
-    const auto set = [](auto tag) {
-        using T = decltype(tag);
-        return cudaFuncSetAttribute(tsm_fp4_kernel<T::rows, T::pair, T::block>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                    Fp4Cfg<T::rows, T::pair, T::block>::SMEM_BYTES);
-    };
     for (const Fp4Kind kind : {Fp4Kind::kRows32, Fp4Kind::kRows64, Fp4Kind::kRows128, Fp4Kind::kPair}) {
+        const auto set = [&](auto tag) {
+            using T = decltype(tag);
+            const auto kernel = tsm_fp4_kernel<T::rows, T::pair, T::block>;
+            constexpr int smem = Fp4Cfg<T::rows, T::pair, T::block>::SMEM_BYTES;
+            cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+            // (Both block sizes' kernels have one CTA on an SM, and alike clusters.)
+            for (int i = 0; e == cudaSuccess && !T::pair && T::block == 16 && i < Fp4Capacity::RANKS; ++i) {
+                cudaLaunchConfig_t cfg = {};
+                cfg.gridDim = dim3(unsigned(i + 1), 1, 1);
+                cfg.blockDim = dim3(kFp4Threads, 1, 1);
+                cfg.dynamicSmemBytes = smem;
+                cudaLaunchAttribute attr;
+                attr.id = cudaLaunchAttributeClusterDimension;
+                attr.val.clusterDim.x = unsigned(i + 1);
+                attr.val.clusterDim.y = 1;
+                attr.val.clusterDim.z = 1;
+                cfg.attrs = &attr;
+                cfg.numAttrs = 1;
+                e = cudaOccupancyMaxActiveClusters(&cap->clusters[int(kind)][i], kernel, &cfg);
+            }
+            return e;
+        };
         cudaError_t e = with_kind<16>(kind, set);
         if (e == cudaSuccess)
             e = with_kind<32>(kind, set);
@@ -659,8 +762,9 @@ cudaError_t launch_fp4(const Fp4Maps &maps, const Fp4Params &p, Fp4Kind kind, in
 {
     const auto run = [&](auto tag) {
         using T = decltype(tag);
-        return launch_chained(tsm_fp4_kernel<T::rows, T::pair, T::block>, dim3(unsigned(T::pair ? 2 * grid : grid)), kFp4Threads,
-                              Fp4Cfg<T::rows, T::pair, T::block>::SMEM_BYTES, T::pair ? 2u : 0u, stream, maps, p);
+        const unsigned cluster = T::pair ? 2u : unsigned(p.ranks);
+        return launch_chained(tsm_fp4_kernel<T::rows, T::pair, T::block>, dim3(unsigned(grid) * cluster), kFp4Threads,
+                              Fp4Cfg<T::rows, T::pair, T::block>::SMEM_BYTES, cluster > 1 ? cluster : 0u, stream, maps, p);
     };
     return block == 16 ? with_kind<16>(kind, run) : with_kind<32>(kind, run);
 }
