@@ -62,9 +62,9 @@ struct Fp4Shape {
     int parts;                  // arrival words per tile
     int32_t price, part;        // S8Schedule::plan's
 };
-constexpr Fp4Shape kFp4Shapes[] = {{32, 128, 16384, 4, 6, 1},
-                                   {64, 128, 32768, 4, 8, 2},
-                                   {128, 128, 65536, 4, 12, 4},
+constexpr Fp4Shape kFp4Shapes[] = {{32, 128, 16384, 4, 20, 1},
+                                   {64, 128, 32768, 4, 22, 2},
+                                   {128, 128, 65536, 4, 25, 4},
                                    {256, 256, 262144, 8, 30, 8}};
 constexpr Fp4Shape fp4_shape(Fp4Kind kind) { return kFp4Shapes[int(kind)]; }
 constexpr int kFp4BlockK = 256;  // k of one stage: 128 bytes of a row

@@ -24,14 +24,12 @@ struct Fp4Plan {
     // Workspace: the copies, the pieces' sums, the arrival words.
     int64_t bytes_a, bytes_b, bytes_p, bytes_w;
 
-    // False: more tiles than a launch can count.
-    bool make(const Fp4Params &p, const uint8_t *A, int64_t lda, int64_t sA, const uint8_t *B, int64_t ldb, int64_t sB, int sms,
-              const Fp4Capacity &cap)
+    // Tiles, schedule and grid for one kind of kernel.  False: more tiles than a
+    // launch can count.
+    bool lay_out(Fp4Kind kind_, const Fp4Params &p, int sms, const Fp4Capacity &cap)
     {
-        *this = {};
-        kind = p.M <= 32 ? Fp4Kind::kRows32 : p.M <= 64 ? Fp4Kind::kRows64 : p.M <= 128 ? Fp4Kind::kRows128 : Fp4Kind::kPair;
+        kind = kind_;
         shape = fp4_shape(kind);
-        const auto up = [](int64_t x, int64_t m) { return (x + m - 1) / m * m; };
         tiles_m = int32_t((int64_t(p.M) + shape.tile_m - 1) / shape.tile_m);
         tiles_n = int32_t((int64_t(p.N) + shape.tile_n - 1) / shape.tile_n);
         kb = int32_t((int64_t(p.K) + kFp4BlockK - 1) / kFp4BlockK);
@@ -47,10 +45,36 @@ struct Fp4Plan {
         sched.plan(int32_t(tiles), kb, workers, shape.price, shape.part);
         if (ranks > 1)
             sched.shared = 0;
-        grid = p.group_rows
-                   ? workers
-               : ranks > 1 ? int(tiles)
-                   : int(std::max<int64_t>(sched.shared ? sched.cutters : 0, std::min<int64_t>(sched.tiles, workers)));
+        grid = p.group_rows ? workers
+               : ranks > 1  ? int(tiles)
+                            : int(std::max<int64_t>(sched.shared ? sched.cutters : 0, std::min<int64_t>(sched.tiles, workers)));
+        return true;
+    }
+
+    // False: more tiles than a launch can count.
+    bool make(const Fp4Params &p, const uint8_t *A, int64_t lda, int64_t sA, const uint8_t *B, int64_t ldb, int64_t sB, int sms,
+              const Fp4Capacity &cap)
+    {
+        *this = {};
+        const Fp4Kind rows = p.M <= 32 ? Fp4Kind::kRows32 : p.M <= 64 ? Fp4Kind::kRows64 : Fp4Kind::kRows128;
+        // A CTA pair's tiles do four times the work of a CTA's of 128 rows at a
+        // block's time, but there are a quarter as many, and no cluster cuts them.  By
+        // the time of the busiest worker, us: 7.5 and 0.36 a block for pairs, 6.8 and
+        // 0.4 for one CTA, 0.5 more in a cluster (TODO both sides).  A grouped
+        // launch's rows are counted on the device: all are taken to be there.
+        if (p.M <= 128) {
+            if (!lay_out(rows, p, sms, cap))
+                return false;
+        } else if (p.group_rows || !lay_out(rows, p, sms, cap)) {
+            if (!lay_out(Fp4Kind::kPair, p, sms, cap))
+                return false;
+        } else {
+            const double one = 6.8 + (ranks > 1 ? 0.5 + 0.4 * ((kb + ranks - 1) / ranks) : 0.4 * double(sched.blocks()));
+            const Fp4Plan single = *this;
+            if (!lay_out(Fp4Kind::kPair, p, sms, cap) || one < 7.5 + 0.36 * double(sched.blocks()))
+                *this = single;
+        }
+        const auto up = [](int64_t x, int64_t m) { return (x + m - 1) / m * m; };
         const int64_t width = (int64_t(p.K) + 1) / 2;
         pack_a = !addressable(reinterpret_cast<const int8_t *>(A), lda, sA, p.M, p.batch);
         pack_b = !addressable(reinterpret_cast<const int8_t *>(B), ldb, sB, p.N, p.batch);
