@@ -983,46 +983,48 @@ def quantize_fp4(X, group_rows=None, *, block=16, stream=None):
 
 
 def _fp4_operand(x, name):
-    """(batch or None, rows, bytes of a row, pitch, stride) of an Fp4Rows."""
+    """(shape, pitch, stride) of an Fp4Rows' codes."""
     import torch
-    codes, tiles = x.codes, x.block_scales
+    codes, tiles, _, block = x
     if codes.dtype != torch.uint8 or tiles.dtype != torch.uint8:
         raise TypeError(f"{name}'s codes and block scales must be torch.uint8")
-    if x.block not in (16, 32):
+    if block != 16 and block != 32:
         raise ValueError(f"{name}'s block must be 16 or 32")
     shape = codes.shape
-    if len(shape) == 3:
+    if len(shape) == 2:
+        rows, width = shape
+        stride = 0
+        ld, unit = codes.stride()
+        want = (-(-rows // 128), -(-width // (2 * block)), 512)
+    elif len(shape) == 3:
         batch, rows, width = shape
         stride, ld, unit = codes.stride()
-        want = (batch, -(-rows // 128), -(-width // (2 * x.block)), 512)
-    elif len(shape) == 2:
-        batch, stride = None, 0
-        rows, width = shape
-        ld, unit = codes.stride()
-        want = (-(-rows // 128), -(-width // (2 * x.block)), 512)
+        want = (batch, -(-rows // 128), -(-width // (2 * block)), 512)
     else:
         raise ValueError(f"{name}'s codes must be 2-D or 3-D")
     if not codes.is_cuda or (unit != 1 and width > 1 and codes.numel()):
         raise ValueError(f"{name}'s codes must be a CUDA tensor with a unit last stride")
     if tiles.shape != want or not tiles.is_cuda or not tiles.is_contiguous():
         raise ValueError(f"{name}'s block scales must be a contiguous {' x '.join(map(str, want))} CUDA tensor")
-    return batch, rows, width, ld if rows > 1 else max(width, 1), stride
+    return shape, ld if rows > 1 else max(width, 1), stride
 
 
 def _fp4_call(a, b, group_rows, out, alpha, bias, activation, slope, out_dtype, stream):
     import torch
     if out is None and stream is not None:
         return _on_stream(stream, _fp4_call, a, b, group_rows, None, alpha, bias, activation, slope, out_dtype, None)
-    batch, M, width, lda, sA = _fp4_operand(a, "a")
-    batch_b, N, width_b, ldb, sB = _fp4_operand(b, "b")
+    sizes_a, lda, sA = _fp4_operand(a, "a")
+    sizes_b, ldb, sB = _fp4_operand(b, "b")
     if a.block != b.block:
         raise ValueError(f"blocks of {a.block} and of {b.block}")
-    if batch != batch_b:
+    if len(sizes_a) != len(sizes_b) or sizes_a[:-2] != sizes_b[:-2]:
         raise ValueError("batch sizes differ")
-    if width != width_b:
-        raise ValueError(f"inner sizes differ: {2 * width} vs {2 * width_b}")
-    three = batch is not None
-    n = batch if three else 1
+    M, width = sizes_a[-2:]
+    N = sizes_b[-2]
+    if width != sizes_b[-1]:
+        raise ValueError(f"inner sizes differ: {2 * width} vs {2 * sizes_b[-1]}")
+    three = len(sizes_a) == 3
+    batch = sizes_a[0] if three else 1
     shape = (batch, M, N) if three else (M, N)
     if out is None:
         make = torch.empty if group_rows is None else torch.zeros
@@ -1032,9 +1034,9 @@ def _fp4_call(a, b, group_rows, out, alpha, bias, activation, slope, out_dtype, 
     sC, ldc, uC = out.stride() if three else (0, *out.stride())
     if not out.is_cuda or (uC != 1 and N > 1 and out.numel()):
         raise ValueError("out must be a CUDA tensor with a unit last stride")
-    pa, sa = _s8_vector(a.scales, M, n, three, "a.scales")
-    pb, sb = _s8_vector(b.scales, N, n, three, "b.scales")
-    pbias, sbias = _s8_vector(bias, N, n, three, "bias")
+    pa, sa = _s8_vector(a.scales, M, batch, three, "a.scales")
+    pb, sb = _s8_vector(b.scales, N, batch, three, "b.scales")
+    pbias, sbias = _s8_vector(bias, N, batch, three, "bias")
     code = _elem_type(out.dtype)
     epi = None  # (none: alpha 1, no bias or activation, f32)
     if code or pbias or alpha != 1 or activation != "none":
@@ -1044,9 +1046,9 @@ def _fp4_call(a, b, group_rows, out, alpha, bias, activation, slope, out_dtype, 
     head = (a.codes.data_ptr(), b.codes.data_ptr(), out.data_ptr(), a.block_scales.data_ptr(), b.block_scales.data_ptr(),
             pa, pb, a.block)
     if group_rows is None:
-        check(_lib.gemm_fp4_scaled(*head, *args, n, epi, _stream_handle(stream)))
+        check(_lib.gemm_fp4_scaled(*head, *args, batch, epi, _stream_handle(stream)))
     else:
-        check(_lib.gemm_fp4_grouped_scaled(*head, group_rows.data_ptr(), n, *args, epi, _stream_handle(stream)))
+        check(_lib.gemm_fp4_grouped_scaled(*head, group_rows.data_ptr(), batch, *args, epi, _stream_handle(stream)))
     return out
 
 
