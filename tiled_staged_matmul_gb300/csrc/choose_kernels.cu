@@ -189,13 +189,12 @@ __device__ __forceinline__ bool choose_in_turn(const ChooseParams &p, int64_t to
     auto score = [&](float v) { return score_of<F>(p.sigmoid, v, top, sum); };
     // Places in order, 0 where there is no expert to choose.
     O c[VM];
-    float bias[VM];
 #pragma unroll
     for (int i = 0; i < VM; ++i) {
-        bias[i] = p.bias && i < at.count ? p.bias[at.first + i] : 0.f;
+        const float bias = p.bias && i < at.count ? p.bias[at.first + i] : 0.f;
         c[i] = 0;
-        if (i < at.count && x[i] != none && bias[i] != none)
-            c[i] = order_of(p.bias ? score(x[i]) + F(bias[i]) : F(x[i]));
+        if (i < at.count && x[i] != none && bias != none)
+            c[i] = order_of(p.bias ? score(x[i]) + F(bias) : F(x[i]));
     }
     auto value_of = [](O o) {  // the number with this place
         if constexpr (sizeof(O) == 4) {
@@ -326,7 +325,7 @@ __device__ __forceinline__ void best_of_lanes(T &a, T &b, int lanes)
 // The sum of a group's `best` largest scores (with the bias) in f64, a whole warp
 // for one group.  Sigmoids only.
 template <int ET>
-__device__ __forceinline__ double group_exactly(const ChooseParams &p, int64_t token, int group, int per, int lane)
+__device__ __noinline__ double group_exactly(const ChooseParams &p, int64_t token, int group, int per, int lane)
 {
     const double none = __longlong_as_double(0xfff0000000000000ll);
     double a = none, b = none;
@@ -344,12 +343,27 @@ __device__ __forceinline__ double group_exactly(const ChooseParams &p, int64_t t
     return p.best > 1 && b != none ? a + b : a;
 }
 
+// The rank of a lane's candidate among `n` by its score (a sigmoid) in f64.
+template <int ET>
+__device__ __noinline__ int rank_exactly(const ChooseParams &p, int64_t token, int name, int n, int lane)
+{
+    double exact = 0.0;
+    if (lane < n)
+        exact = score_of<double>(true, logit_at<ET>(p, token, name), 0.f, 1.0) + double(p.bias[name]);
+    __syncwarp();
+    int rank = 0;
+    for (int j = 0; j < n; ++j) {
+        const double other = __shfl_sync(kAll, exact, j);
+        rank += other > exact || (other == exact && j < lane);
+    }
+    return rank;
+}
+
 // The warp's choice: as choose_in_turn, for what a warp of candidates holds.  `keys`
 // and `names` are the warp's, 32 each.
 enum class Chosen { kYes, kInTurn, kExactly };  // done, too many candidates, f64 is needed for all
 template <int ET, int VM>
-__device__ __forceinline__ Chosen choose(const ChooseParams &p, int64_t token, const Layout &at, const float (&x)[VM],
-                                         const float (&bias)[VM], float top, float total, int lane, uint32_t *keys, int *names,
+__device__ __forceinline__ Chosen choose(const ChooseParams &p, int64_t token, const Layout &at, const float (&x)[VM], float top, float total, int lane, uint32_t *keys, int *names,
                                          int &id)
 {
     const float none = __uint_as_float(0xff800000u);
@@ -358,8 +372,9 @@ __device__ __forceinline__ Chosen choose(const ChooseParams &p, int64_t token, c
     uint32_t c[VM];  // places in order, 0 where there is no expert to choose
 #pragma unroll
     for (int i = 0; i < VM; ++i) {
-        const bool there = i < at.count && x[i] != none && bias[i] != none;
-        c[i] = !there ? 0u : order_of(p.bias ? score_of<float>(p.sigmoid, x[i], top, total) + bias[i] : x[i]);
+        const float bias = p.bias && i < at.count ? p.bias[at.first + i] : 0.f;
+        const bool there = i < at.count && x[i] != none && bias != none;
+        c[i] = !there ? 0u : order_of(p.bias ? score_of<float>(p.sigmoid, x[i], top, total) + bias : x[i]);
     }
     if (limited) {
         uint32_t a = 0, b = 0;
@@ -490,15 +505,7 @@ __device__ __forceinline__ Chosen choose(const ChooseParams &p, int64_t token, c
         if (__any_sync(kAll, close)) {
             if (!p.sigmoid)
                 return Chosen::kExactly;
-            double exact = 0.0;
-            if (lane < n)
-                exact = score_of<double>(true, logit_at<ET>(p, token, name), 0.f, 1.0) + double(p.bias[name]);
-            __syncwarp();
-            rank = 0;
-            for (int j = 0; j < n; ++j) {
-                const double other = __shfl_sync(kAll, exact, j);
-                rank += other > exact || (other == exact && j < lane);
-            }
+            rank = rank_exactly<ET>(p, token, name, n, lane);
         }
     }
     __syncwarp();
@@ -525,7 +532,7 @@ __device__ __noinline__ int choose_slowly(const ChooseParams &p, int64_t token, 
 }
 
 template <int ET, int VM, bool WIDE>
-__global__ void __launch_bounds__(32 * kChooseWarps, VM == 32 ? 2 : 4) tsm_choose_kernel(const __grid_constant__ ChooseParams p)
+__global__ void __launch_bounds__(32 * kChooseWarps, VM == 32 ? 2 : VM == 16 ? 4 : 6) tsm_choose_kernel(const __grid_constant__ ChooseParams p)
 {
     chain_next();
     chain_wait();
@@ -534,10 +541,9 @@ __global__ void __launch_bounds__(32 * kChooseWarps, VM == 32 ? 2 : 4) tsm_choos
     const int lane = int(threadIdx.x & 31);
     const Layout at(p.experts, p.groups, VM, lane);
     const float none = __uint_as_float(0xff800000u);
-    float bias[VM];
-#pragma unroll
-    for (int i = 0; i < VM; ++i)
-        bias[i] = p.bias && i < at.count ? p.bias[at.first + i] : 0.f;
+    bool bad_bias = false;
+    for (int e = lane; p.bias && e < p.experts; e += 32)
+        bad_bias |= is_nan(p.bias[e]);
     const int64_t warps = int64_t(gridDim.x) * kChooseWarps;
     for (int64_t t = int64_t(blockIdx.x) * kChooseWarps + (threadIdx.x >> 5); t < p.tokens; t += warps) {
         float x[VM];
@@ -546,8 +552,8 @@ __global__ void __launch_bounds__(32 * kChooseWarps, VM == 32 ? 2 : 4) tsm_choos
         float seen = 0.f;
 #pragma unroll
         for (int i = 0; i < VM; ++i)
-            seen = ptx::max_abs3_nan(seen, i < at.count ? x[i] : 0.f, bias[i]);
-        bool bad = is_nan(seen);
+            seen = ptx::max_abs3_nan(seen, i < at.count ? x[i] : 0.f, 0.f);
+        bool bad = bad_bias || is_nan(seen);
         float top = 0.f, total = 1.f;
         if (!p.sigmoid) {
             uint32_t high = 0;
@@ -566,7 +572,7 @@ __global__ void __launch_bounds__(32 * kChooseWarps, VM == 32 ? 2 : 4) tsm_choos
         bad = __any_sync(kAll, bad);
         int id = lane;
         if (!bad) {
-            const Chosen how = choose<ET, VM>(p, t, at, x, bias, top, total, lane, keys[threadIdx.x >> 5], names[threadIdx.x >> 5], id);
+            const Chosen how = choose<ET, VM>(p, t, at, x, top, total, lane, keys[threadIdx.x >> 5], names[threadIdx.x >> 5], id);
             if (how != Chosen::kYes)
                 id = choose_slowly<ET, VM, WIDE>(p, t, top, total, how == Chosen::kExactly);
         }
