@@ -27,9 +27,7 @@ namespace tsm {
 namespace {
 
 constexpr int kUnit = 16;    // elements a thread takes at a time
-// Units of a thread that stay in registers (32 elements of 16 bits are 16 registers).
-template <int ET, bool ALIGNED>
-constexpr int kUnitsKept = ALIGNED && ET != kOutF32 ? 4 : 2;
+constexpr int kUnitsKept = 2;  // units of a thread that stay in registers
 
 // A unit as it lies in memory; what lies past the row's end as zeros.
 template <int ET, bool WIDE>
@@ -51,6 +49,13 @@ struct Unit16 {
                     raw[i] = P::get(x, unit * PIECES + i);
                 return;
             }
+#pragma unroll
+            for (int i = 0; i < PIECES; ++i)
+#pragma unroll
+                for (int w = 0; w < 4; ++w)
+                    raw[i].w[w] = 0u;
+            if (k0 >= K)
+                return;
 #pragma unroll
             for (int i = 0; i < PIECES; ++i)
 #pragma unroll
@@ -102,6 +107,27 @@ struct Unit16 {
     }
 };
 
+// x / d as f32 rounds it: c is 1 / d rounded, and one correction by the exact
+// remainder makes up for what x c is off (P. Markstein, IA-64 and Elementary
+// Functions, 2000).
+__device__ __forceinline__ float divide(float x, float d, float c)
+{
+    const float q = x * c;
+    return fmaf(fmaf(-q, d, x), c, q);
+}
+// Two at a time.
+__device__ __forceinline__ void divide2(float &x, float &y, float d, float c)
+{
+    asm("{\n\t.reg .b64 v, q, r, dd, cc;\n\t"
+        "mov.b64 v, {%0, %1};\n\tmov.b64 dd, {%2, %2};\n\tmov.b64 cc, {%3, %3};\n\t"
+        "mul.rn.f32x2 q, v, cc;\n\t"
+        "fma.rn.f32x2 r, q, dd, v;\n\t"
+        "fma.rn.f32x2 q, r, cc, q;\n\t"
+        "mov.b64 {%0, %1}, q;\n\t}"
+        : "+f"(x), "+f"(y)
+        : "f"(-d), "f"(c));
+}
+
 // ALIGNED: rows of X are 16-byte and rows of q 8-byte aligned.
 template <int ET, int BLOCK, bool ALIGNED, int TPR>
 __global__ void __launch_bounds__(TPR < 256 && TPR > 32 ? TPR : 256) tsm_quantize_fp4_kernel(Fp4QuantParams p)
@@ -114,7 +140,8 @@ __global__ void __launch_bounds__(TPR < 256 && TPR > 32 ? TPR : 256) tsm_quantiz
     if (at >= p.M * p.batch)
         return;
     const int tid = int(threadIdx.x) % TPR;
-    const int64_t g = at / p.M, r = at - g * p.M;
+    // (Fewer than 2^31 rows.)
+    const int64_t g = p.batch == 1 ? 0 : uint32_t(at) / uint32_t(p.M), r = at - g * p.M;
     if (p.group_rows && r >= int64_t(p.group_rows[g]))
         return;
     const char *x = static_cast<const char *>(p.X) + (g * p.sX + r * p.ldx) * (ET == kOutF32 ? 4 : 2);
@@ -123,19 +150,25 @@ __global__ void __launch_bounds__(TPR < 256 && TPR > 32 ? TPR : 256) tsm_quantiz
     const int32_t K = int32_t(p.K);  // (below 2^31 - 2^16: the last units' ends are counted, too)
     const int32_t units = (K + kUnit - 1) / kUnit;
     const int32_t all = int32_t(p.tile_cols) * 4 * (BLOCK / kUnit);  // and those of zeros that fill the last scale tile
-    constexpr int KEEP = kUnitsKept<ET, ALIGNED>;
+    constexpr int KEEP = kUnitsKept;
     Unit16<ET, ALIGNED> keep[KEEP];
 #pragma unroll
     for (int i = 0; i < KEEP; ++i)
         keep[i].load(x, tid + i * TPR, K);
 
     float inverse = 1.f;  // 1 / r
+    float r_ = 1.f;       // r
     bool none = false;    // the row's codes are zeros
+    bool tiny = false;    // the row's values are worked on 2^60 times as large (r and 1 / r say so)
+    float tops[KEEP];
+#pragma unroll
+    for (int i = 0; i < KEEP; ++i)
+        tops[i] = keep[i].top();
     if constexpr (BLOCK == 16) {
         float top = 0.f;
 #pragma unroll
         for (int i = 0; i < KEEP; ++i)
-            top = ptx::max_abs3_nan(top, keep[i].top(), 0.f);
+            top = ptx::max_abs3_nan(top, tops[i], 0.f);
         for (int32_t u = tid + KEEP * TPR; u < units; u += TPR) {
             Unit16<ET, ALIGNED> one;
             one.load(x, u, K);
@@ -157,26 +190,33 @@ __global__ void __launch_bounds__(TPR < 256 && TPR > 32 ? TPR : 256) tsm_quantiz
         int e = int(bits >> 23) - 127 - 11 + ((bits & 0x7fffffu) > 0x280000u);
         e = max(e, -126);
         none = !finite || bits == 0;
-        inverse = __uint_as_float(uint32_t(127 - e) << 23);
         if (tid == 0)
             p.scales[g * p.sS + r] = !finite ? __uint_as_float(0x7fffffffu) : bits == 0 ? 0.f : __uint_as_float(uint32_t(127 + e) << 23);
+        // (1 / (s r) and the remainders below would leave f32's range.)
+        tiny = e < -60;
+        if (tiny)
+            e += 60;
+        inverse = __uint_as_float(uint32_t(127 - e) << 23);
+        r_ = __uint_as_float(uint32_t(127 + e) << 23);
     }
 
-    auto put = [&](int32_t u, const Unit16<ET, ALIGNED> &unit) {
+    auto put = [&](int32_t u, const Unit16<ET, ALIGNED> &unit, float top) {
         float v[kUnit];
         uint32_t scale;  // as stored
-        const float top = unit.top();
         unit.widen(v);
         if constexpr (BLOCK == 16) {
-            scale = none ? 0u : ptx::to_e4m3(__fdiv_rn(top * inverse, 6.f));
-            const float sf = ptx::from_e4m3(scale);
-            const float rs = __frcp_rn(sf);
+            if (tiny) {
+                top *= 0x1p60f;
 #pragma unroll
-            for (int j = 0; j < kUnit; ++j) {
-                const float y = v[j] * inverse;
-                const float q0 = y * rs;
-                v[j] = fmaf(fmaf(-q0, sf, y), rs, q0);
+                for (int j = 0; j < kUnit; ++j)
+                    v[j] *= 0x1p60f;
             }
+            scale = none ? 0u : ptx::to_e4m3(divide(top * inverse, 6.f, 1.f / 6.f));
+            const float sf = ptx::from_e4m3(scale);
+            const float d = sf * r_, c = __frcp_rn(sf) * inverse;  // (powers of two: both exact)
+#pragma unroll
+            for (int j = 0; j < kUnit; j += 2)
+                divide2(v[j], v[j + 1], d, c);
         } else {
             // The neighbour lane holds the block's other half.
             const float other = __shfl_xor_sync(0xffffffffu, top, 1);
@@ -211,11 +251,11 @@ __global__ void __launch_bounds__(TPR < 256 && TPR > 32 ? TPR : 256) tsm_quantiz
 #pragma unroll
     for (int i = 0; i < KEEP; ++i)
         if (i * TPR < all)
-            put(tid + i * TPR, keep[i]);
+            put(tid + i * TPR, keep[i], tops[i]);
     for (int32_t u = tid + KEEP * TPR; u - tid < all; u += TPR) {
         Unit16<ET, ALIGNED> one;
         one.load(x, u, K);
-        put(u, one);
+        put(u, one, one.top());
     }
 }
 
@@ -223,11 +263,17 @@ template <int ET, int BLOCK, bool ALIGNED>
 cudaError_t quantize_as(const Fp4QuantParams &p, int sms, cudaStream_t stream)
 {
     const int64_t rows = p.M * p.batch, units = (p.K + kUnit - 1) / kUnit;
-    if (rows < int64_t(sms) * 4)
-        return launch_chained(tsm_quantize_fp4_kernel<ET, BLOCK, ALIGNED, 256>, dim3(unsigned(rows)), 256, 0, 0, stream, p);
-    if (units <= 32 * kUnitsKept<ET, ALIGNED>)
-        return launch_chained(tsm_quantize_fp4_kernel<ET, BLOCK, ALIGNED, 32>, dim3(unsigned((rows + 7) / 8)), 256, 0, 0, stream, p);
-    return launch_chained(tsm_quantize_fp4_kernel<ET, BLOCK, ALIGNED, 128>, dim3(unsigned(rows)), 128, 0, 0, stream, p);
+    // As few threads to a row as keep it (a warp: eight rows a CTA, nothing to wait
+    // for), 256 where none do or where there are too few rows to fill the GPU.
+    if (rows >= int64_t(sms) * 4) {
+        if (units <= 32 * kUnitsKept)
+            return launch_chained(tsm_quantize_fp4_kernel<ET, BLOCK, ALIGNED, 32>, dim3(unsigned((rows + 7) / 8)), 256, 0, 0, stream, p);
+        if (units <= 64 * kUnitsKept)
+            return launch_chained(tsm_quantize_fp4_kernel<ET, BLOCK, ALIGNED, 64>, dim3(unsigned(rows)), 64, 0, 0, stream, p);
+        if (units <= 128 * kUnitsKept)
+            return launch_chained(tsm_quantize_fp4_kernel<ET, BLOCK, ALIGNED, 128>, dim3(unsigned(rows)), 128, 0, 0, stream, p);
+    }
+    return launch_chained(tsm_quantize_fp4_kernel<ET, BLOCK, ALIGNED, 256>, dim3(unsigned(rows)), 256, 0, 0, stream, p);
 }
 
 template <int ET>
