@@ -358,6 +358,37 @@ def check(status: int) -> None:
 
 # ------------------------------------------------------------------ torch conveniences
 
+# The choice of experts and the 4-bit operators read their tensors in an extension
+# module (csrc/tensor_calls.cpp), which calls the same C functions.
+
+_calls = None
+
+
+def _load_calls():
+    global _calls
+    import torch  # noqa: F401  (the module's libraries come with it)
+    import importlib.machinery
+    import importlib.util
+    loader = importlib.machinery.ExtensionFileLoader("tsm_tensor_calls", _build.CALLS_PATH)
+    module = importlib.util.module_from_spec(importlib.util.spec_from_loader("tsm_tensor_calls", loader))
+    loader.exec_module(module)
+    _calls = module
+    return module
+
+
+def _done(result):
+    """What the module returned, unless that is a status of the library."""
+    if result.__class__ is int:
+        check(result)
+    return result
+
+
+def _score(name):
+    if name not in MOE_SCORES:
+        raise ValueError(f"score must be one of {', '.join(MOE_SCORES)}")
+    return MOE_SCORES[name]
+
+
 def _stream_handle(stream):
     if stream is None:
         # (torch.cuda.current_stream() builds a Stream object, ten times as long)
@@ -638,55 +669,20 @@ def moe_choose(logits, topk, *, score="softmax", bias=None, groups=1, keep_group
     ``renormalize``, times ``scale``.  Equal values go to the lower number; a
     logit of -infinity hides an expert, and a choice that finds none has the id
     -1 and the weight 0."""
-    import torch
     if stream is not None:
         return _on_stream(stream, moe_choose, logits, topk, score=score, bias=bias, groups=groups, keep_groups=keep_groups,
                           group_best=group_best, renormalize=renormalize, scale=scale)
-    code = _elem_type(logits.dtype)
-    if logits.dim() != 2:
-        raise ValueError("logits must be a tokens x experts tensor")
-    T, E = logits.shape
-    ld = _token_pitch(logits, T, E, logits.dtype, "logits")
-    if bias is not None and (bias.dtype != torch.float32 or not bias.is_cuda or bias.shape != (E,)
-                             or not bias.is_contiguous()):
-        raise ValueError("bias must be a contiguous CUDA float32 tensor of one value per expert")
-    if score not in MOE_SCORES:
-        raise ValueError(f"score must be one of {', '.join(MOE_SCORES)}")
-    ids = torch.empty((T, topk), dtype=torch.int32, device=logits.device)
-    weights = torch.empty((T, topk), dtype=torch.float32, device=logits.device)
-    check(_lib.choose_experts(logits.data_ptr(), code, 0 if bias is None else bias.data_ptr(), ids.data_ptr(),
-                                  weights.data_ptr(), T, E, topk, ld, MOE_SCORES[score], groups, keep_groups, group_best,
-                                  renormalize, scale, _stream_handle(stream)))
-    return ids, weights
+    return _done((_calls or _load_calls()).moe_choose(logits, topk, _score(score), bias, groups, keep_groups, group_best,
+                                                      renormalize, scale))
 
 
 def moe_choose_grad(dweights, logits, ids, out=None, *, score="softmax", renormalize=False, scale=1.0, stream=None):
     """The gradient of ``moe_choose``'s weights towards the logits (tokens x
     experts, in their type), for the ``ids`` it chose."""
-    import torch
-    if out is None and stream is not None:
-        return _on_stream(stream, moe_choose_grad, dweights, logits, ids, score=score, renormalize=renormalize, scale=scale)
-    code = _elem_type(logits.dtype)
-    if logits.dim() != 2:
-        raise ValueError("logits must be a tokens x experts tensor")
-    T, E = logits.shape
-    ld = _token_pitch(logits, T, E, logits.dtype, "logits")
-    if ids.dtype != torch.int32 or not ids.is_cuda or ids.dim() != 2 or ids.shape[0] != T or not ids.is_contiguous():
-        raise ValueError("ids must be a contiguous CUDA int32 tensor of tokens x topk values")
-    if dweights.dtype != torch.float32 or not dweights.is_cuda or dweights.shape != ids.shape \
-            or not dweights.is_contiguous():
-        raise ValueError("dweights must be a contiguous CUDA float32 tensor of tokens x topk values")
-    if score not in MOE_SCORES:
-        raise ValueError(f"score must be one of {', '.join(MOE_SCORES)}")
-    if out is None:
-        out = torch.empty((T, E), dtype=logits.dtype, device=logits.device)
-        ldo = E
-    else:
-        ldo = _token_pitch(out, T, E, logits.dtype, "out")
-    check(_lib.choose_experts_grad(dweights.data_ptr(), logits.data_ptr(), code, ids.data_ptr(), out.data_ptr(), T, E,
-                                       ids.shape[1], ld, ldo, MOE_SCORES[score], renormalize, scale,
-                                       _stream_handle(stream)))
-    return out
+    if stream is not None:
+        return _on_stream(stream, moe_choose_grad, dweights, logits, ids, out, score=score, renormalize=renormalize,
+                          scale=scale)
+    return _done((_calls or _load_calls()).moe_choose_grad(dweights, logits, ids, out, _score(score), renormalize, scale))
 
 
 def moe_dispatch(x, slots, groups, capacity, out=None, *, stream=None):
@@ -947,109 +943,21 @@ def quantize_fp4(X, group_rows=None, *, block=16, stream=None):
     The codes' rows have a pitch of a multiple of 16 bytes, as the products want.
     ``group_rows`` (int32, one count per matrix) limits the rows that are read
     and written."""
-    import torch
     if stream is not None:
         return _on_stream(stream, quantize_fp4, X, group_rows, block=block)
-    code = _elem_type(X.dtype)
-    if block not in (16, 32):
-        raise ValueError("block must be 16 or 32")
-    shape = X.shape
-    three = len(shape) == 3
-    if three:
-        batch, M, K = shape
-        sX, ldx, unit = X.stride()
-    elif len(shape) == 2:
-        batch, (M, K), sX = 1, shape, 0
-        ldx, unit = X.stride()
-    if len(shape) not in (2, 3) or not X.is_cuda or (unit != 1 and K > 1 and X.numel()):
-        raise ValueError("X must be a 2-D or 3-D CUDA tensor with a unit last stride")
-    counts = 0
-    if group_rows is not None:
-        if group_rows.dtype != torch.int32 or not group_rows.is_cuda or group_rows.numel() != batch \
-                or not group_rows.is_contiguous():
-            raise ValueError("group_rows must be a contiguous CUDA int32 tensor of one count per matrix")
-        counts = group_rows.data_ptr()
-    width = (K + 1) // 2
-    ldq = width + -width % 16
-    sQ = M * ldq
-    tiles = (-(-M // 128), -(-K // (4 * block)), 512)
-    q = torch.empty_strided((batch, M, width) if three else (M, width), (sQ, ldq, 1) if three else (ldq, 1),
-                            dtype=torch.uint8, device=X.device)
-    s = torch.empty((batch, *tiles) if three else tiles, dtype=torch.uint8, device=X.device)
-    r = torch.empty((batch, M) if three else (M,), dtype=torch.float32, device=X.device) if block == 16 else None
-    check(_lib.fp4_quantize_rows(X.data_ptr(), code, block, q.data_ptr(), s.data_ptr(), 0 if r is None else r.data_ptr(),
-                                 counts, M, K, ldx if M > 1 else K, ldq, sX, sQ, M, batch, _stream_handle(stream)))
-    return Fp4Rows(q, s, r, block)
-
-
-def _fp4_operand(x, name):
-    """(shape, pitch, stride) of an Fp4Rows' codes."""
-    import torch
-    codes, tiles, _, block = x
-    if codes.dtype != torch.uint8 or tiles.dtype != torch.uint8:
-        raise TypeError(f"{name}'s codes and block scales must be torch.uint8")
-    if block != 16 and block != 32:
-        raise ValueError(f"{name}'s block must be 16 or 32")
-    shape = codes.shape
-    if len(shape) == 2:
-        rows, width = shape
-        stride = 0
-        ld, unit = codes.stride()
-        want = (-(-rows // 128), -(-width // (2 * block)), 512)
-    elif len(shape) == 3:
-        batch, rows, width = shape
-        stride, ld, unit = codes.stride()
-        want = (batch, -(-rows // 128), -(-width // (2 * block)), 512)
-    else:
-        raise ValueError(f"{name}'s codes must be 2-D or 3-D")
-    if not codes.is_cuda or (unit != 1 and width > 1 and codes.numel()):
-        raise ValueError(f"{name}'s codes must be a CUDA tensor with a unit last stride")
-    if tiles.shape != want or not tiles.is_cuda or not tiles.is_contiguous():
-        raise ValueError(f"{name}'s block scales must be a contiguous {' x '.join(map(str, want))} CUDA tensor")
-    return shape, ld if rows > 1 else max(width, 1), stride
+    return Fp4Rows(*_done((_calls or _load_calls()).quantize_fp4(X, group_rows, block)), block)
 
 
 def _fp4_call(a, b, group_rows, out, alpha, bias, activation, slope, out_dtype, stream):
-    import torch
-    if out is None and stream is not None:
-        return _on_stream(stream, _fp4_call, a, b, group_rows, None, alpha, bias, activation, slope, out_dtype, None)
-    sizes_a, lda, sA = _fp4_operand(a, "a")
-    sizes_b, ldb, sB = _fp4_operand(b, "b")
-    if a.block != b.block:
-        raise ValueError(f"blocks of {a.block} and of {b.block}")
-    if len(sizes_a) != len(sizes_b) or sizes_a[:-2] != sizes_b[:-2]:
-        raise ValueError("batch sizes differ")
-    M, width = sizes_a[-2:]
-    N = sizes_b[-2]
-    if width != sizes_b[-1]:
-        raise ValueError(f"inner sizes differ: {2 * width} vs {2 * sizes_b[-1]}")
-    three = len(sizes_a) == 3
-    batch = sizes_a[0] if three else 1
-    shape = (batch, M, N) if three else (M, N)
-    if out is None:
-        make = torch.empty if group_rows is None else torch.zeros
-        out = make(shape, dtype=out_dtype or torch.float32, device=a.codes.device)
-    if out.shape != shape:
-        raise ValueError(f"out must be a {' x '.join(map(str, shape))} tensor")
-    sC, ldc, uC = out.stride() if three else (0, *out.stride())
-    if not out.is_cuda or (uC != 1 and N > 1 and out.numel()):
-        raise ValueError("out must be a CUDA tensor with a unit last stride")
-    pa, sa = _s8_vector(a.scales, M, batch, three, "a.scales")
-    pb, sb = _s8_vector(b.scales, N, batch, three, "b.scales")
-    pbias, sbias = _s8_vector(bias, N, batch, three, "bias")
-    code = _elem_type(out.dtype)
-    epi = None  # (none: alpha 1, no bias or activation, f32)
-    if code or pbias or alpha != 1 or activation != "none":
-        epi = ctypes.byref(GemmEpilogue(alpha, pbias or None, sbias, ACTIVATIONS.get(activation, activation), slope,
-                                        code))
-    args = (M, N, 2 * width, lda, ldb, ldc if M > 1 else max(N, 1), sA, sB, sC, sa, sb)
-    head = (a.codes.data_ptr(), b.codes.data_ptr(), out.data_ptr(), a.block_scales.data_ptr(), b.block_scales.data_ptr(),
-            pa, pb, a.block)
-    if group_rows is None:
-        check(_lib.gemm_fp4_scaled(*head, *args, batch, epi, _stream_handle(stream)))
-    else:
-        check(_lib.gemm_fp4_grouped_scaled(*head, group_rows.data_ptr(), batch, *args, epi, _stream_handle(stream)))
-    return out
+    if stream is not None:
+        return _on_stream(stream, _fp4_call, a, b, group_rows, out, alpha, bias, activation, slope, out_dtype, None)
+    codes_a, tiles_a, scales_a, block = a
+    codes_b, tiles_b, scales_b, block_b = b
+    if block != block_b:
+        raise ValueError(f"blocks of {block} and of {block_b}")
+    return _done((_calls or _load_calls()).gemm_fp4(codes_a, tiles_a, scales_a, codes_b, tiles_b, scales_b, block, group_rows,
+                                                    out, alpha, bias, ACTIVATIONS.get(activation, activation), slope,
+                                                    out_dtype))
 
 
 def gemm_fp4(a, b, out=None, *, alpha=1.0, bias=None, activation="none", slope=0.01, out_dtype=None, stream=None):
@@ -1065,9 +973,7 @@ def grouped_gemm_fp4(a, b, group_rows, out=None, *, alpha=1.0, bias=None, activa
     """The grouped (Mixture-of-Experts) form of ``gemm_fp4``: a holds groups x M
     rows, b groups x N; of group g the first ``group_rows[g]`` rows are computed,
     the others keep the contents of ``out`` (zeros when not given)."""
-    import torch
-    if a.codes.dim() != 3 or group_rows.dtype != torch.int32 or not group_rows.is_cuda \
-            or group_rows.numel() != a.codes.shape[0] or not group_rows.is_contiguous():
+    if a.codes.dim() != 3 or group_rows is None:
         raise ValueError("a must be 3-D and group_rows a contiguous CUDA int32 tensor of one count per group")
     return _fp4_call(a, b, group_rows, out, alpha, bias, activation, slope, out_dtype, stream)
 

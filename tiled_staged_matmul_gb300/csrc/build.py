@@ -1,4 +1,5 @@
-"""Build ``libtsm_gemm.so`` in-tree with nvcc for sm_103a only.
+"""Build ``libtsm_gemm.so`` in-tree with nvcc for sm_103a only, and with the host
+compiler the extension module that passes torch tensors to some of its calls.
 
 The translation units compile in parallel: the plain GEMM kernels and the
 cluster split-K sums, the fused-epilogue GEMM kernels once per activation
@@ -15,6 +16,7 @@ import re
 import shutil
 import subprocess
 import sys
+import sysconfig
 from concurrent.futures import ThreadPoolExecutor
 
 HERE = os.path.dirname(os.path.abspath(__file__))
@@ -23,6 +25,8 @@ REPO = os.path.dirname(PKG)
 BUILD_DIR = os.path.join(PKG, "_build")
 LIB_NAME = "libtsm_gemm.so"
 LIB_PATH = os.path.join(BUILD_DIR, LIB_NAME)
+CALLS_PATH = os.path.join(BUILD_DIR, "tsm_tensor_calls.so")
+CALLS_SOURCE = "tensor_calls.cpp"
 PTXAS_LOG = os.path.join(BUILD_DIR, "ptxas.log")
 
 # (source, object name, extra nvcc flags); the activations are gemm_internal.h's kAct* values
@@ -50,16 +54,16 @@ def _nvcc() -> str:
 
 
 def _inputs() -> list[str]:
-    files = [os.path.join(HERE, f) for f in SOURCES + HEADERS]
+    files = [os.path.join(HERE, f) for f in SOURCES + HEADERS + [CALLS_SOURCE]]
     files.append(os.path.join(REPO, "include", "tsm_gemm.h"))
     files.append(os.path.abspath(__file__))
     return files
 
 
 def up_to_date() -> bool:
-    if not os.path.exists(LIB_PATH):
+    if not os.path.exists(LIB_PATH) or not os.path.exists(CALLS_PATH):
         return False
-    t = os.path.getmtime(LIB_PATH)
+    t = min(os.path.getmtime(LIB_PATH), os.path.getmtime(CALLS_PATH))
     return all(os.path.getmtime(f) <= t for f in _inputs())
 
 
@@ -72,6 +76,22 @@ def _compile(src: str, obj: str, verbose_ptxas: bool, flags: list[str]) -> str:
     if r.returncode != 0:
         raise RuntimeError(f"nvcc failed on {src}:\n{r.stdout}\n{r.stderr}")
     return r.stdout + r.stderr
+
+
+def _compile_calls(obj: str) -> list[str]:
+    """Compile the extension module's unit; the command that links it."""
+    import torch
+    torch_dir = os.path.dirname(torch.__file__)
+    cuda = os.path.dirname(os.path.dirname(_nvcc()))
+    inc = [os.path.join(torch_dir, "include"), os.path.join(torch_dir, "include", "torch", "csrc", "api", "include"),
+           sysconfig.get_paths()["include"], os.path.join(cuda, "include")]
+    cmd = ["g++", "-O2", "-std=c++17", "-fPIC", f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}",
+           *[x for i in inc for x in ("-isystem", i)], "-c", os.path.join(HERE, CALLS_SOURCE), "-o", obj]
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    if r.returncode != 0:
+        raise RuntimeError(f"g++ failed on {CALLS_SOURCE}:\n{r.stdout}\n{r.stderr}")
+    return ["g++", "-shared", obj, "-L" + os.path.join(torch_dir, "lib"), "-ltorch_python", "-ltorch_cpu", "-lc10",
+            "-lc10_cuda", "-L" + BUILD_DIR, "-l:" + LIB_NAME, "-Wl,-rpath,$ORIGIN"]
 
 
 def check_spills(log: str) -> None:
@@ -88,7 +108,8 @@ def build(force: bool = False, quiet: bool = True) -> str:
     os.makedirs(BUILD_DIR, exist_ok=True)
     objs = [os.path.join(BUILD_DIR, name + ".o") for _, name, _ in UNITS]
     kernel_unit = [src not in HOST_SOURCES for src, _, _ in UNITS]
-    with ThreadPoolExecutor(len(UNITS)) as ex:
+    with ThreadPoolExecutor(len(UNITS) + 1) as ex:
+        calls = ex.submit(_compile_calls, os.path.join(BUILD_DIR, "tensor_calls.o"))
         logs = list(ex.map(lambda a: _compile(*a),
                            [(src, o, k, fl) for (src, _, fl), o, k in zip(UNITS, objs, kernel_unit)]))
     ptxas = "".join(log for log, k in zip(logs, kernel_unit) if k)
@@ -101,6 +122,11 @@ def build(force: bool = False, quiet: bool = True) -> str:
     if r.returncode != 0:
         raise RuntimeError(f"link failed:\n{r.stdout}\n{r.stderr}")
     os.replace(tmp, LIB_PATH)
+    tmp = CALLS_PATH + f".tmp{os.getpid()}"
+    r = subprocess.run(calls.result() + ["-o", tmp], capture_output=True, text=True)
+    if r.returncode != 0:
+        raise RuntimeError(f"link failed:\n{r.stdout}\n{r.stderr}")
+    os.replace(tmp, CALLS_PATH)
     if not quiet:
         print(logs[0], file=sys.stderr)
     return LIB_PATH
