@@ -1,7 +1,10 @@
-"""A mixture-of-experts layer on the library's operators: training step and
-int8 serving.
+"""A mixture-of-experts layer on the library's operators: training step, and
+serving in int8 or in 4-bit floating point.
 
     out[t] = sum_j weights[t, j] * (silu(x[t] W1[e]) W2[e]),   e = ids[t, j]
+
+A router (a width x groups matrix) makes the ids and weights of the tokens:
+the topk largest softmax scores, renormalised.
 
 Run it for the time of each path at a prompt and at a decode step:
 
@@ -19,11 +22,28 @@ from tiled_staged_matmul_gb300 import binding as tsm
 
 class MoELayer:
     """Experts W1 (groups x width x hidden) and W2 (groups x hidden x width),
-    f16; ``capacity`` rows are kept for each expert, choices past it dropped."""
+    f16; ``capacity`` rows are kept for each expert, choices past it dropped.
+    ``router``, if there is one, is f16, too."""
 
-    def __init__(self, W1, W2, capacity):
+    def __init__(self, W1, W2, capacity, router=None):
         self.W1, self.W2, self.capacity = W1, W2, capacity
         self.groups = W1.shape[0]
+        self.router = router
+
+    # ------------------------------------------------------------- the router
+
+    def choose(self, x, topk):
+        """ids, weights, and what ``choose_backward`` needs."""
+        logits = tsm.gemm(x, self.router)
+        ids, weights = tsm.moe_choose(logits, topk, renormalize=True)
+        return ids, weights, (x, logits, ids)
+
+    def choose_backward(self, dweights, saved):
+        """Gradients of x (its part by way of the weights) and of the router."""
+        x, logits, ids = saved
+        dlogits = tsm.moe_choose_grad(dweights, logits, ids, renormalize=True).to(x.dtype)
+        return (tsm.gemm(dlogits, self.router.t().contiguous(), out_dtype=x.dtype),
+                tsm.gemm(x.t().contiguous(), dlogits))
 
     # ------------------------------------------------------------- training
 
@@ -77,6 +97,23 @@ class MoELayer:
         y = tsm.grouped_gemm_s8(qa, self.q2, ascales, self.s2, counts, out_dtype=x.dtype)
         return tsm.moe_combine(y, slots, weights)
 
+    def quantise_fp4(self, block=16):
+        """Both weights as 4-bit rows along the inner dimension, once."""
+        self.f1 = tsm.quantize_fp4(self.W1.transpose(1, 2).contiguous(), block=block)
+        self.f2 = tsm.quantize_fp4(self.W2.transpose(1, 2).contiguous(), block=block)
+
+    def serve_fp4(self, x, ids, weights):
+        """The layer on 4-bit products: the experts' rows are quantised where they
+        lie (their block scales are kept 128 rows at a time)."""
+        slots, counts = tsm.moe_route(ids, self.groups, self.capacity)
+        rows = tsm.moe_dispatch(x, slots, self.groups, self.capacity,
+                                torch.empty((self.groups, self.capacity, x.shape[1]), dtype=x.dtype, device=x.device))
+        q = tsm.quantize_fp4(rows, counts, block=self.f1.block)
+        a = tsm.grouped_gemm_fp4(q, self.f1, counts, activation="silu", out_dtype=x.dtype)
+        qa = tsm.quantize_fp4(a, counts, block=self.f2.block)
+        y = tsm.grouped_gemm_fp4(qa, self.f2, counts, out_dtype=x.dtype)
+        return tsm.moe_combine(y, slots, weights)
+
 
 def main():
     width, hidden, groups, topk = 2048, 1408, 64, 6
@@ -84,6 +121,7 @@ def main():
     rand = lambda *s: torch.randn(s, generator=g, device="cuda")
     W1 = (rand(groups, width, hidden) * width ** -0.5).half()
     W2 = (rand(groups, hidden, width) * hidden ** -0.5).half()
+    router = (rand(width, groups) * width ** -0.5).half()
 
     def microseconds(f):
         for _ in range(3):
@@ -99,19 +137,25 @@ def main():
         return sorted(times)[len(times) // 2]
 
     for tokens, capacity in ((4096, 512), (32, 32)):
-        layer = MoELayer(W1, W2, capacity)
+        layer = MoELayer(W1, W2, capacity, router)
         layer.quantise()
+        layer.quantise_fp4()
         x = rand(tokens, width).half()
-        weights, ids = torch.softmax(rand(tokens, groups), 1).topk(topk)
-        ids = ids.int()
-        weights = (weights / weights.sum(1, keepdim=True)).contiguous()
+        ids, weights, chosen = layer.choose(x, topk)
         out, saved = layer.forward(x, ids, weights)
-        served = layer.serve(x, ids, weights)
-        err = float((served.float() - out.float()).norm() / out.float().norm())
-        print(f"{tokens} tokens: forward {microseconds(lambda: layer.forward(x, ids, weights)):.0f} us, "
+        dweights = layer.backward(out, saved)[1]
+
+        def away(served):
+            return float((served.float() - out.float()).norm() / out.float().norm())
+
+        print(f"{tokens} tokens: router {microseconds(lambda: layer.choose(x, topk)):.0f} us and "
+              f"{microseconds(lambda: layer.choose_backward(dweights, chosen)):.0f} back, "
+              f"forward {microseconds(lambda: layer.forward(x, ids, weights)):.0f} us, "
               f"backward {microseconds(lambda: layer.backward(out, saved)):.0f} us, "
               f"int8 {microseconds(lambda: layer.serve(x, ids, weights)):.0f} us "
-              f"({err:.4f} of the f16 result's norm away)")
+              f"({away(layer.serve(x, ids, weights)):.4f} of the f16 result's norm away), "
+              f"4 bits {microseconds(lambda: layer.serve_fp4(x, ids, weights)):.0f} us "
+              f"({away(layer.serve_fp4(x, ids, weights)):.4f})")
 
 
 if __name__ == "__main__":

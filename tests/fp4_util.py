@@ -112,8 +112,8 @@ def unpacked(rows, K):
     """(codes, scale bytes) of a 2-D operand that the library wrote."""
     raw = rows.codes.cpu().numpy()
     M = raw.shape[0]
-    codes = np.stack([raw & 15, raw >> 4], axis=2).reshape(M, -1)
+    codes = np.stack([raw & 15, raw >> 4], axis=2).reshape(M, 2 * raw.shape[1])
     blocks = -(-K // rows.block)
     flat = rows.block_scales.cpu().numpy().reshape(-1)
     i, b = np.meshgrid(np.arange(M), np.arange(-(-blocks // 4) * 4), indexing="ij")
-    return codes, flat[scale_place(i, b, blocks)] if M and blocks else np.zeros((M, 0), dtype=np.uint8)
+    return codes, flat[scale_place(i, b, blocks)]
