@@ -190,17 +190,29 @@ __device__ __forceinline__ void store_rows(const Fp4Params &p, const float (&v)[
         const int odd = lane & 1;
         const uint32_t halves = odd ? 0x3276u : 0x5410u;
         c += odd * (p.ldc - 1);
+        uint32_t two[CW / 2];
+        if (p.epi.out_type == kOutBF16) {
 #pragma unroll
-        for (int j = 0; j < CW; j += 2, c += 2 * p.ldc) {
-            const uint32_t mine = out16_pair(v[j], v[j + 1], p.epi.out_type);
-            const uint32_t two = __byte_perm(mine, __shfl_xor_sync(0xffffffffu, mine, 1), halves);
+            for (int j = 0; j < CW; j += 2)
+                two[j / 2] = out16_pair(v[j], v[j + 1], kOutBF16);
+        } else {
+#pragma unroll
+            for (int j = 0; j < CW; j += 2)
+                two[j / 2] = out16_pair(v[j], v[j + 1], kOutF16);
+        }
+#pragma unroll
+        for (int j = 0; j < CW; j += 2)
+            two[j / 2] = __byte_perm(two[j / 2], __shfl_xor_sync(0xffffffffu, two[j / 2], 1), halves);
+        const int64_t step = 2 * p.ldc;
+#pragma unroll
+        for (int j = 0; j < CW; j += 2, c += step) {
             if (FULL) {
-                *reinterpret_cast<uint32_t *>(c) = two;
+                *reinterpret_cast<uint32_t *>(c) = two[j / 2];
             } else if (j + odd < rows) {
                 if (left + odd > 1)
-                    *reinterpret_cast<uint32_t *>(c) = two;
+                    *reinterpret_cast<uint32_t *>(c) = two[j / 2];
                 else if (left + odd == 1)
-                    *c = uint16_t(two);
+                    *c = uint16_t(two[j / 2]);
             }
         }
     } else if (FULL || left > 0) {
@@ -562,9 +574,9 @@ __global__ void __launch_bounds__(kFp4Threads, 1)
                     release(over);
                 }
                 look_ahead(acc ^ 1u);
-                // (Not unrolled: the warps are out of step, and their instructions
+                // (x are out of step, and their instructions
                 // have to stay in the cache.)
-#pragma unroll 1
+#pragma unroll
                 for (int i = 0; i < Cfg::CHUNKS; ++i) {
                     const int32_t row = row_of(i, acc);
                     float v[CW];
