@@ -18,7 +18,9 @@
 // Bound by instructions rather than by its bytes.  So the choice is not made one
 // expert after another (370 instructions for 8 of 256) but among few: the topk-th
 // largest of the lanes' maxima bounds the topk-th largest of all from below, a
-// dozen experts reach it, and those move to a lane each and are ranked there.  Compiled once per type of the logits
+// dozen experts reach it, and those move to a lane each and are ranked there
+// (8192 x 256, 8 of 4 of 8 groups, with a bias: 16.4 us, 28.8 one after another;
+// without groups or bias 9.6).  Compiled once per type of the logits
 // (-DTSM_CHOOSE_ELEM, gemm_internal.h's kOut* values).
 #include "fp4_internal.h"
 #include "fp4_ptx.cuh"

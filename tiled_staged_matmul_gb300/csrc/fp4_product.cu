@@ -24,12 +24,12 @@
 // A copy of a scale tile to TMEM takes the tensor core 40 cycles, and a 256 x 256
 // stage with blocks of 16 has twelve, as long as its MMAs.  Copies that the MMAs'
 // own thread issues run one after another with them; those of another thread run
-// beside them (8192^3 296 us so, TODO otherwise), with barriers between the two.
+// beside them (8192^3 296 us so, 233 otherwise), with barriers between the two.
 // Few rows are bound by reading B once.  Where their tiles are few, too, a tile's K
 // is cut over a cluster, whose CTAs add up each other's sums through distributed
-// shared memory (1 x 4096 x 4096: TODO); else tiles of a last wave that costs too
-// much are cut over the SMs, their sums joined through memory by whoever arrives
-// last.  Either way in a fixed order.
+// shared memory (1 x 4096 x 4096 7.4 us, 16.0 otherwise); else tiles of a last wave
+// that costs too much are cut over the SMs, their sums joined through memory by
+// whoever arrives last.  Either way in a fixed order.
 #include "fp4_internal.h"
 #include "fp4_ptx.cuh"
 #include "s8_common.cuh"
@@ -68,10 +68,10 @@ struct Fp4Cfg {
     static constexpr int CW = NT < 64 ? 8 : 16;
     static constexpr int CHUNKS = NT / CW / kEpiGroups;
     static_assert(CHUNKS >= 1 && CHUNKS * CW * kEpiGroups == NT, "chunks");
-    static constexpr int EPI_ROWS = CHUNKS * CW;         // of one warp
+    static constexpr int EPI_ROWS = CHUNKS * CW;         // of one epilogue group
     static constexpr int NOTES_OFF = 3072, TERMS_OFF = NOTES_OFF + 32 * kNotes;
-    static constexpr int TERMS = EPI_ROWS + 64;          // words of a warp: its rows' scales, its columns' scales and biases
-    static constexpr int CTRL = TERMS_OFF + 2 * kEpiWarps * TERMS * 4;
+    static constexpr int COLS_OFF = TERMS_OFF + 2 * NT * 4;
+    static constexpr int CTRL = COLS_OFF + 2 * kEpiWarps * 64 * 4;
     static constexpr int FIT = (232448 - 1024 - CTRL) / STAGE;
     static constexpr int S = FIT > 8 ? 8 : FIT;
     static constexpr int SMEM_BYTES = 1024 + S * STAGE + CTRL;
@@ -251,7 +251,8 @@ __global__ void __launch_bounds__(kFp4Threads, 1)
     const uint32_t note0 = ctrl + 320u;        // [kNotes] a note has been written
     const uint32_t sums0 = ctrl + 512u;        // [epilogue warp] a cluster's CTAs' sums are in shared memory
     const uint32_t notes = ctrl + Cfg::NOTES_OFF;
-    const uint32_t terms0 = ctrl + Cfg::TERMS_OFF;  // [2][epilogue warp][terms]
+    const uint32_t terms0 = ctrl + Cfg::TERMS_OFF;  // [2][group][its rows' scales]
+    const uint32_t cols0 = ctrl + Cfg::COLS_OFF;    // [2][epilogue warp][its columns' scales, biases]
 
     const int warp = __shfl_sync(0xffffffffu, int(threadIdx.x >> 5), 0);  // (uniform to the compiler)
     const int lane = int(threadIdx.x & 31);
@@ -490,7 +491,7 @@ __global__ void __launch_bounds__(kFp4Threads, 1)
         __syncwarp();
     } else {
         // ---------------- epilogue
-        constexpr int CW = Cfg::CW, EARLY = Cfg::EARLY, MINE = (Cfg::EPI_ROWS + 31) / 32;
+        constexpr int CW = Cfg::CW, EARLY = Cfg::EARLY;
         const int h = (warp - kFirstEpi) >> 2, q = warp & 3;
         uint32_t acc = 0, aphase = 0, note = 0;
         bool met = !split;
@@ -499,9 +500,8 @@ __global__ void __launch_bounds__(kFp4Threads, 1)
         const auto row_of = [&](int i, uint32_t a) {
             return PAIR && a == 0 ? (kEpiGroups * (Cfg::CHUNKS - i) - 1 - h) * CW : (kEpiGroups * i + h) * CW;
         };
-        const auto terms_of = [&](uint32_t a) {
-            return terms0 + (a * uint32_t(kEpiWarps) + uint32_t(warp - kFirstEpi)) * uint32_t(4 * Cfg::TERMS);
-        };
+        const auto rows_of = [&](uint32_t a) { return terms0 + (a * uint32_t(kEpiGroups) + uint32_t(h)) * uint32_t(4 * Cfg::EPI_ROWS); };
+        const auto cols_of = [&](uint32_t a) { return cols0 + (a * uint32_t(kEpiWarps) + uint32_t(warp - kFirstEpi)) * 256u + 4u * uint32_t(lane); };
         const auto read = [&]() {
             const uint32_t from = notes + 32u * (note % kNotes);
             const uint4 x = ptx::ld_shared_v4(from), y = ptx::ld_shared_v4(from + 16u);
@@ -518,16 +518,14 @@ __global__ void __launch_bounds__(kFp4Threads, 1)
             if (n.tile < 0)
                 return;
             const int32_t col = n.t.n0 + int32_t(rank) * Cfg::COLS + 32 * q + lane;
-            const uint32_t to = terms_of(a) + 4u * uint32_t(lane);
-#pragma unroll
-            for (int k = 0; k < MINE; ++k) {
-                const int at = 32 * k + lane;
-                const int32_t row = n.t.m0 + row_of(at / CW, a) + at % CW;
-                if (at < Cfg::EPI_ROWS)
-                    ptx::fetch_f32(to + 128u * k, p.scale_a && row < n.t.rows ? p.scale_a + n.t.z * p.sa_stride + row : nullptr, 1.f);
-            }
-            ptx::fetch_f32(to + 4u * Cfg::EPI_ROWS, p.scale_b && col < p.N ? p.scale_b + n.t.z * p.sb_stride + col : nullptr, 1.f);
-            ptx::fetch_f32(to + 4u * Cfg::EPI_ROWS + 128u, p.epi.bias && col < p.N ? p.epi.bias + n.t.z * p.epi.bias_stride + col : nullptr, 0.f);
+            // A quarter of the group's rows each.
+            const int at = q * (Cfg::EPI_ROWS / 4) + lane;
+            const int32_t row = n.t.m0 + row_of(at / CW, a) + at % CW;
+            if (lane < Cfg::EPI_ROWS / 4)
+                ptx::fetch_f32(rows_of(a) + 4u * uint32_t(at),
+                               p.scale_a && row < n.t.rows ? p.scale_a + n.t.z * p.sa_stride + row : nullptr, 1.f);
+            ptx::fetch_f32(cols_of(a), p.scale_b && col < p.N ? p.scale_b + n.t.z * p.sb_stride + col : nullptr, 1.f);
+            ptx::fetch_f32(cols_of(a) + 128u, p.epi.bias && col < p.N ? p.epi.bias + n.t.z * p.epi.bias_stride + col : nullptr, 0.f);
         };
         look_ahead(acc);
         for (;;) {
@@ -536,17 +534,17 @@ __global__ void __launch_bounds__(kFp4Threads, 1)
                 w = read();
             ++note;
             ok = w.tile >= 0 && s8_wait<PAIR>(tfull0 + 8u * acc, aphase, flag, p, kStatusEpilogue);
-            // The group's warps go on or stop together (they meet below).
+            // The group's warps go on or stop together (they meet below), and have
+            // each other's terms.
+            ptx::fetch_wait();
             if (!__all_sync(0xffffffffu, ptx::named_bar_and(kFp4BarGroup + h, 128, ok)))
                 break;
             const S8Tile &t = w.t;
             const int32_t col = t.n0 + int32_t(rank) * Cfg::COLS + 32 * q + lane;
             const int32_t rows = t.rows - t.m0;
-            ptx::fetch_wait();
-            __syncwarp();
-            const uint32_t sa0 = terms_of(acc);
-            const float sb = p.epi.alpha * __uint_as_float(ptx::ld_shared_u32(sa0 + 4u * uint32_t(Cfg::EPI_ROWS + lane)));
-            const float bias = __uint_as_float(ptx::ld_shared_u32(sa0 + 4u * uint32_t(Cfg::EPI_ROWS + 32 + lane)));
+            const uint32_t sa0 = rows_of(acc);
+            const float sb = p.epi.alpha * __uint_as_float(ptx::ld_shared_u32(cols_of(acc)));
+            const float bias = __uint_as_float(ptx::ld_shared_u32(cols_of(acc) + 128u));
             const bool whole = w.kb1 - w.kb0 == p.kb;
             ptx::tc_fence_after_sync();
             const uint32_t from = tmem + (uint32_t(32 * q) << 16) + acc * uint32_t(Cfg::ACC1);
@@ -574,8 +572,7 @@ __global__ void __launch_bounds__(kFp4Threads, 1)
                     release(over);
                 }
                 look_ahead(acc ^ 1u);
-                // (x are out of step, and their instructions
-                // have to stay in the cache.)
+                // (Unrolled: the chunks' buffers are registers.)
 #pragma unroll
                 for (int i = 0; i < Cfg::CHUNKS; ++i) {
                     const int32_t row = row_of(i, acc);
