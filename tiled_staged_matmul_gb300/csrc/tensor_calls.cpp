@@ -62,6 +62,14 @@ int64_t integer(PyObject *o)
     return v;
 }
 
+int32_t integer32(PyObject *o)
+{
+    const int64_t v = integer(o);
+    if (v != int32_t(v))
+        refuse(std::to_string(v) + " does not fit 32 bits");
+    return int32_t(v);
+}
+
 float real(PyObject *o)
 {
     const double v = PyFloat_AsDouble(o);
@@ -151,7 +159,8 @@ PyObject *moe_choose(PyObject *, PyObject *const *a, Py_ssize_t n)
         const float *bias = nullptr;
         if (a[3] != Py_None)
             bias = static_cast<const float *>(dense(tensor(a[3], "bias"), at::kFloat, {E}, "bias").data_ptr());
-        const int64_t score = integer(a[2]), groups = integer(a[4]), keep = integer(a[5]), best = integer(a[6]);
+        const int64_t groups = integer(a[4]), keep = integer(a[5]);
+        const int32_t score = integer32(a[2]), best = integer32(a[6]);
         const bool renormalize = PyObject_IsTrue(a[7]) == 1;
         const float scale = real(a[8]);
         if (topk < 0)
@@ -160,8 +169,8 @@ PyObject *moe_choose(PyObject *, PyObject *const *a, Py_ssize_t n)
         const at::Tensor ids = at::empty({T, topk}, like.dtype(at::kInt)), weights = at::empty({T, topk}, like.dtype(at::kFloat));
         const gemm_status_t st = call([&] {
             return choose_experts(x.data_ptr(), type, bias, static_cast<int32_t *>(ids.data_ptr()),
-                                  static_cast<float *>(weights.data_ptr()), T, E, topk, ld, int32_t(score), groups, keep,
-                                  int32_t(best), renormalize, scale, stream());
+                                  static_cast<float *>(weights.data_ptr()), T, E, topk, ld, score, groups, keep, best,
+                                  renormalize, scale, stream());
         });
         if (st != GEMM_OK)
             return PyLong_FromLong(st);
@@ -197,13 +206,13 @@ PyObject *moe_choose_grad(PyObject *, PyObject *const *a, Py_ssize_t n)
                 refuse("out must be a tensor of the logits' shape and type");
             ldo = pitch(out, "out");
         }
-        const int64_t score = integer(a[4]);
+        const int32_t score = integer32(a[4]);
         const bool renormalize = PyObject_IsTrue(a[5]) == 1;
         const float scale = real(a[6]);
         const gemm_status_t st = call([&] {
             return choose_experts_grad(static_cast<const float *>(dw.data_ptr()), x.data_ptr(), type,
                                        static_cast<const int32_t *>(ids.data_ptr()), out.data_ptr(), T, E, topk, ld, ldo,
-                                       int32_t(score), renormalize, scale, stream());
+                                       score, renormalize, scale, stream());
         });
         if (st != GEMM_OK)
             return PyLong_FromLong(st);
@@ -345,7 +354,7 @@ PyObject *gemm_fp4(PyObject *, PyObject *const *p, Py_ssize_t n)
         epi.alpha = real(p[9]);
         epi.bias = bias.at;
         epi.bias_stride = bias.stride;
-        epi.activation = int32_t(integer(p[11]));
+        epi.activation = integer32(p[11]);
         epi.slope = real(p[12]);
         epi.out_type = elem_type(out);
         const int64_t ldc = M > 1 ? out.stride(-2) : std::max<int64_t>(N, 1), sC = three ? out.stride(0) : 0;
