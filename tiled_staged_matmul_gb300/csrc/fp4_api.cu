@@ -178,7 +178,7 @@ gemm_status_t fp4_quantize_rows(const void *X, int32_t elem_type, int32_t block,
                               tile_rows, tile_cols};
     const uint64_t x_all = reinterpret_cast<uintptr_t>(X) | uint64_t(M > 1 ? ldx * eb : 0) | uint64_t(batch > 1 ? strideX * eb : 0);
     const uint64_t q_all = reinterpret_cast<uintptr_t>(q) | uint64_t(M > 1 ? ldq : 0) | uint64_t(batch > 1 ? strideQ : 0);
-    const cudaError_t e = launch_quantize_fp4(p, elem_type, (x_all & 15u) == 0 && (q_all & 7u) == 0, block, ds->sms,
+    const cudaError_t e = launch_quantize_fp4(p, elem_type, (x_all & 15u) == 0 && (q_all & 7u) == 0, block,
                                               reinterpret_cast<cudaStream_t>(stream));
     return e == cudaSuccess ? GEMM_OK : fail_cuda(e, "4-bit row quantisation launch");
 }

@@ -25,7 +25,7 @@ struct Fp4QuantParams {
     int64_t tile_rows, tile_cols;
 };
 // aligned: rows of X are 16-byte and rows of q 8-byte aligned.
-cudaError_t launch_quantize_fp4(const Fp4QuantParams &p, int elem, bool aligned, int block, int sms, cudaStream_t stream);
+cudaError_t launch_quantize_fp4(const Fp4QuantParams &p, int elem, bool aligned, int block, cudaStream_t stream);
 
 // Arguments of a product (device pointers).  What the kernels call rows are the
 // rows of C (tokens), columns are those of C (rows of B).
