@@ -17,13 +17,23 @@ inline int elem_bytes(int32_t t) { return t == GEMM_OUT_F32 ? 4 : 2; }
 
 inline bool known_elem(int32_t t) { return t == GEMM_OUT_F32 || t == GEMM_OUT_F16 || t == GEMM_OUT_BF16; }
 
-// The current device and its state.
+// The current device and its state.  (What makes the state, in the thread's first
+// call, goes to no stream, so that call may be a captured one.)
 inline gemm_status_t current(int *dev, DeviceState **ds)
 {
     const cudaError_t e = cudaGetDevice(dev);
     if (e != cudaSuccess)
         return fail_cuda(e, "cudaGetDevice");
-    return device_state(*dev, ds);
+    thread_local int made = -1;  // the device of the last call
+    if (made == *dev)
+        return device_state(*dev, ds);
+    cudaStreamCaptureMode mode = cudaStreamCaptureModeRelaxed;
+    cudaThreadExchangeStreamCaptureMode(&mode);
+    const gemm_status_t st = device_state(*dev, ds);
+    cudaThreadExchangeStreamCaptureMode(&mode);
+    if (st == GEMM_OK)
+        made = *dev;
+    return st;
 }
 
 // One buffer of a call: checked for its address and, once all are known, on

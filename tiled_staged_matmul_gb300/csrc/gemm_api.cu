@@ -120,12 +120,6 @@ gemm_status_t device_state(int dev, DeviceState **out)
     std::lock_guard<std::mutex> lock(g_device_mutex);
     DeviceState &s = g_devices[dev];
     if (!s.ready) {
-        // (Nothing here goes to a stream, so a process may capture its first call.)
-        struct Relaxed {
-            cudaStreamCaptureMode mode = cudaStreamCaptureModeRelaxed;
-            Relaxed() { cudaThreadExchangeStreamCaptureMode(&mode); }
-            ~Relaxed() { cudaThreadExchangeStreamCaptureMode(&mode); }
-        } relaxed;
         cudaError_t e;
         if ((e = cudaDeviceGetAttribute(&s.sms, cudaDevAttrMultiProcessorCount, dev)) != cudaSuccess)
             return fail_cuda(e, "cudaDeviceGetAttribute(SM count)");
