@@ -62,10 +62,17 @@ struct Fp4Shape {
     int parts;                  // arrival words per tile
     int32_t price, part;        // S8Schedule::plan's
 };
-constexpr Fp4Shape kFp4Shapes[] = {{32, 128, 16384, 4, 20, 1},
-                                   {64, 128, 32768, 4, 22, 2},
-                                   {128, 128, 65536, 4, 25, 4},
-                                   {256, 256, 262144, 8, 30, 8}};
+// The prices of a cut, in blocks of 256 k.  Cut where the schedule says so and never,
+// us: 16 x 20000 x 16384 37.3 and 47.0, 128 x 20000 x 16384 45.2 and 51.1, 1024 x 5000 x
+// 28672 67.0 and 86.1, 2048 x 2560 x 65536 138 and 183, one of 8 experts 3 x 4096 x
+// 14336 16.9 and 22.6.  Cut wherever it balances (prices of 0) and as the schedule
+// says: 16 x 14336 x 4096 18.6 and 9.7, 97 x 14333 x 4010 22.7 and 11.2, 4096^3 41.1 and
+// 31.0.  Parts of 1, 2, 4 and 8 cut a tile further, which few calls notice: one of 8
+// experts 512 x 512 x 16384 30.3 us, 27.1 with these.
+constexpr Fp4Shape kFp4Shapes[] = {{32, 128, 16384, 4, 20, 8},
+                                   {64, 128, 32768, 4, 22, 12},
+                                   {128, 128, 65536, 4, 25, 20},
+                                   {256, 256, 262144, 8, 30, 32}};
 constexpr Fp4Shape fp4_shape(Fp4Kind kind) { return kFp4Shapes[int(kind)]; }
 constexpr int kFp4BlockK = 256;  // k of one stage: 128 bytes of a row
 

@@ -59,11 +59,13 @@ struct Fp4Plan {
         const Fp4Kind rows = p.M <= 32 ? Fp4Kind::kRows32 : p.M <= 64 ? Fp4Kind::kRows64 : Fp4Kind::kRows128;
         // A CTA pair's tiles do four times the work of a CTA's of 128 rows, but there
         // are a quarter as many, and no cluster cuts them.  By the time of the busiest
-        // worker, us: 7.0 and 0.385 a block for pairs, 6.8 and 0.28 for one CTA, 7.3
-        // and 0.36 in a cluster (the nearer of both on 14 shapes; us as single CTAs and
-        // pairs: 150 x 1000 x 1000 7.7 and 7.8, 256 x 4096 x 4096 10.5 and 12.4, 300 x
-        // 5000 x 8192 14.6 and 19.4, 512 x 4096 x 4096 9.7 and 12.6, 1024 x 4096 x 4096
-        // 14.8 and 13.2, 1024 x 14336 x 4096 35.7 and 27.1, 4096^3 40.8 and 32.1).
+        // worker, us, a block of K at a time; cutting a pair's tile adds the reading of
+        // its contributors' sums.  As single CTAs and pairs, us: 150 x 1000 x 1000 7.7 and
+        // 7.8, 256 x 4096 x 4096 10.5 and 12.4, 300 x 5000 x 8192 14.8 and 18.5, 512 x 512 x
+        // 65536 21.2 and 49.1, 1024 x 1024 x 65536 43.6 and 53.4, 1500 x 1500 x 65536 76.2
+        // and 81.8, 256 x 28672 x 8192 37.2 and 35.7, 512 x 8192 x 8192 24.2 and 18.8,
+        // 2048 x 2048 x 16384 41.3 and 28.7, 4096^3 40.8 and 31.0.  The constants choose
+        // the shorter in each of these.
         // Groups with room for more than 128 rows take pairs, whatever their counts,
         // which only the device knows: 64 experts' prompt 63.7 and 62.0, 8 experts'
         // 550 and 375, but 16 small ones' 24 and 27.
@@ -74,9 +76,14 @@ struct Fp4Plan {
             if (!lay_out(Fp4Kind::kPair, p, sms, cap))
                 return false;
         } else {
-            const double one = ranks > 1 ? 7.3 + 0.36 * double((kb + ranks - 1) / ranks) : 6.8 + 0.28 * double(sched.blocks());
+            const double one = ranks > 1 ? 7.5 + 0.5 * ranks + 0.274 * double((kb + ranks - 1) / ranks)
+                                         : 6.8 + 0.27 * double(sched.blocks());
             const Fp4Plan single = *this;
-            if (!lay_out(Fp4Kind::kPair, p, sms, cap) || one < 7.0 + 0.385 * double(sched.blocks()))
+            const auto two = [this] {
+                return 7.0 + (sched.shared ? 0.42 * double(sched.blocks()) + 3.0 * sched.cutters / sched.shared
+                                           : 0.385 * double(sched.blocks()));
+            };
+            if (!lay_out(Fp4Kind::kPair, p, sms, cap) || one < two())
                 *this = single;
         }
         const auto up = [](int64_t x, int64_t m) { return (x + m - 1) / m * m; };
