@@ -155,15 +155,19 @@ __device__ __forceinline__ void scale_and_activate(const Fp4Params &p, float (&v
 #pragma unroll
     for (int j = 0; j < CW; j += 4) {
         const uint4 s = ptx::ld_shared_v4(sa_at + 4u * j);
-        const uint32_t w[4] = {s.x, s.y, s.z, s.w};
-#pragma unroll
-        for (int i = 0; i < 4; ++i)
-            v[j + i] = fmaf(sb, v[j + i] * __uint_as_float(w[i]), bias);
+        ptx::mul_fma2(v[j], v[j + 1], __uint_as_float(s.x), __uint_as_float(s.y), sb, bias);
+        ptx::mul_fma2(v[j + 2], v[j + 3], __uint_as_float(s.z), __uint_as_float(s.w), sb, bias);
     }
     with_activation<kActRuntime>(p.epi.act, [&](auto act) {
+        if constexpr (decltype(act)::value == kActSilu) {
 #pragma unroll
-        for (int j = 0; j < CW; ++j)
-            v[j] = epi_act(v[j], decltype(act)::value, p.epi.slope);
+            for (int j = 0; j < CW; j += 2)
+                ptx::silu2(v[j], v[j + 1]);
+        } else {
+#pragma unroll
+            for (int j = 0; j < CW; ++j)
+                v[j] = epi_act(v[j], decltype(act)::value, p.epi.slope);
+        }
     });
 }
 

@@ -147,5 +147,36 @@ __device__ __forceinline__ uint32_t to_e2m1x8(const float *v)
     return d;
 }
 
+// Two values at a time (each as the scalar instructions round it):  x = m (x sx) + b.
+__device__ __forceinline__ void mul_fma2(float &x, float &y, float sx, float sy, float m, float b)
+{
+    asm("{\n\t.reg .b64 v, s, mm, bb;\n\t"
+        "mov.b64 v, {%0, %1};\n\tmov.b64 s, {%2, %3};\n\tmov.b64 mm, {%4, %4};\n\tmov.b64 bb, {%5, %5};\n\t"
+        "mul.rn.f32x2 v, v, s;\n\t"
+        "fma.rn.f32x2 v, v, mm, bb;\n\t"
+        "mov.b64 {%0, %1}, v;\n\t}"
+        : "+f"(x), "+f"(y)
+        : "f"(sx), "f"(sy), "f"(m), "f"(b));
+}
+// x / (1 + 2^(-x log2 e)), to within a few units of f32 where 1 + ... is below 2^126,
+// else 0.
+__device__ __forceinline__ void silu2(float &x, float &y)
+{
+    asm("{\n\t.reg .b64 v, t, one;\n\t.reg .f32 a, b;\n\t"
+        "mov.b64 v, {%0, %1};\n\tmov.b64 t, {%2, %2};\n\tmov.b64 one, {%3, %3};\n\t"
+        "mul.rn.f32x2 t, v, t;\n\t"
+        "mov.b64 {a, b}, t;\n\t"
+        "ex2.approx.ftz.f32 a, a;\n\tex2.approx.ftz.f32 b, b;\n\t"
+        "mov.b64 t, {a, b};\n\t"
+        "add.rn.f32x2 t, t, one;\n\t"
+        "mov.b64 {a, b}, t;\n\t"
+        "rcp.approx.ftz.f32 a, a;\n\trcp.approx.ftz.f32 b, b;\n\t"
+        "mov.b64 t, {a, b};\n\t"
+        "mul.rn.f32x2 v, v, t;\n\t"
+        "mov.b64 {%0, %1}, v;\n\t}"
+        : "+f"(x), "+f"(y)
+        : "f"(-1.4426950408889634f), "f"(1.f));
+}
+
 }  // namespace ptx
 }  // namespace tsm
