@@ -19,8 +19,8 @@
 // expert after another (370 instructions for 8 of 256) but among few: the topk-th
 // largest of the lanes' maxima bounds the topk-th largest of all from below, a
 // dozen experts reach it, and those move to a lane each and are ranked there
-// (8192 x 256, 8 of 4 of 8 groups, with a bias: 16.4 us, 28.8 one after another;
-// without groups or bias 9.6).  Compiled once per type of the logits
+// (8192 x 256, 8 of 4 of 8 groups, with a bias: 14 us, 28.8 one after another;
+// without groups or bias 8.0, of 1024 in bf16 18.6).  Compiled once per type of the logits
 // (-DTSM_CHOOSE_ELEM, gemm_internal.h's kOut* values).
 #include "fp4_internal.h"
 #include "fp4_ptx.cuh"
@@ -365,19 +365,25 @@ __device__ __noinline__ int rank_exactly(const ChooseParams &p, int64_t token, i
 // and `names` are the warp's, 32 each.
 enum class Chosen { kYes, kInTurn, kExactly };  // done, too many candidates, f64 is needed for all
 template <int ET, int VM>
-__device__ __forceinline__ Chosen choose(const ChooseParams &p, int64_t token, const Layout &at, const float (&x)[VM], float top, float total, int lane, uint32_t *keys, int *names,
-                                         int &id)
+__device__ __forceinline__ Chosen choose(const ChooseParams &p, int64_t token, const Layout &at, const float (&x)[VM], const float (&add)[VM], float top,
+                                         float total, int lane, uint32_t *keys, int *names, int &id)
 {
     const float none = __uint_as_float(0xff800000u);
     const bool limited = p.keep < p.groups;
     const float eps = p.sigmoid ? kSigmoidError : kSoftmaxError;
     uint32_t c[VM];  // places in order, 0 where there is no expert to choose
+    // (What is no expert's has a logit of -infinity.)
+    const auto place = [&](auto &&value) {
 #pragma unroll
-    for (int i = 0; i < VM; ++i) {
-        const float bias = p.bias && i < at.count ? p.bias[at.first + i] : 0.f;
-        const bool there = i < at.count && x[i] != none && bias != none;
-        c[i] = !there ? 0u : order_of(p.bias ? score_of<float>(p.sigmoid, x[i], top, total) + bias : x[i]);
-    }
+        for (int i = 0; i < VM; ++i)
+            c[i] = x[i] == none || add[i] == none ? 0u : order_of(value(i));
+    };
+    if (!p.bias)
+        place([&](int i) { return x[i]; });
+    else if (p.sigmoid)
+        place([&](int i) { return score_of<float>(true, x[i], top, total) + add[i]; });
+    else
+        place([&](int i) { return score_of<float>(false, x[i], top, total) + add[i]; });
     if (limited) {
         uint32_t a = 0, b = 0;
 #pragma unroll
@@ -534,7 +540,7 @@ __device__ __noinline__ int choose_slowly(const ChooseParams &p, int64_t token, 
 }
 
 template <int ET, int VM, bool WIDE>
-__global__ void __launch_bounds__(32 * kChooseWarps, VM == 32 ? 2 : VM == 16 ? 4 : 6) tsm_choose_kernel(const __grid_constant__ ChooseParams p)
+__global__ void __launch_bounds__(32 * kChooseWarps, VM == 32 ? 2 : VM == 16 ? 4 : VM == 8 && !WIDE ? 5 : 6) tsm_choose_kernel(const __grid_constant__ ChooseParams p)
 {
     chain_next();
     chain_wait();
@@ -543,19 +549,18 @@ __global__ void __launch_bounds__(32 * kChooseWarps, VM == 32 ? 2 : VM == 16 ? 4
     const int lane = int(threadIdx.x & 31);
     const Layout at(p.experts, p.groups, VM, lane);
     const float none = __uint_as_float(0xff800000u);
-    bool bad_bias = false;
-    for (int e = lane; p.bias && e < p.experts; e += 32)
-        bad_bias |= is_nan(p.bias[e]);
     const int64_t warps = int64_t(gridDim.x) * kChooseWarps;
     for (int64_t t = int64_t(blockIdx.x) * kChooseWarps + (threadIdx.x >> 5); t < p.tokens; t += warps) {
         float x[VM];
         read_logits<ET, VM, WIDE>(p, t, at, x);
         // (NaN where there is one; absent experts' values are set below.)
-        float seen = 0.f;
+        float seen = 0.f, add[VM];  // (add: the bias)
 #pragma unroll
-        for (int i = 0; i < VM; ++i)
-            seen = ptx::max_abs3_nan(seen, i < at.count ? x[i] : 0.f, 0.f);
-        bool bad = bad_bias || is_nan(seen);
+        for (int i = 0; i < VM; ++i) {
+            add[i] = p.bias && i < at.count ? p.bias[at.first + i] : 0.f;
+            seen = ptx::max_abs3_nan(seen, i < at.count ? x[i] : 0.f, add[i]);
+        }
+        bool bad = is_nan(seen);
         float top = 0.f, total = 1.f;
         if (!p.sigmoid) {
             uint32_t high = 0;
@@ -574,7 +579,7 @@ __global__ void __launch_bounds__(32 * kChooseWarps, VM == 32 ? 2 : VM == 16 ? 4
         bad = __any_sync(kAll, bad);
         int id = lane;
         if (!bad) {
-            const Chosen how = choose<ET, VM>(p, t, at, x, top, total, lane, keys[threadIdx.x >> 5], names[threadIdx.x >> 5], id);
+            const Chosen how = choose<ET, VM>(p, t, at, x, add, top, total, lane, keys[threadIdx.x >> 5], names[threadIdx.x >> 5], id);
             if (how != Chosen::kYes)
                 id = choose_slowly<ET, VM, WIDE>(p, t, top, total, how == Chosen::kExactly);
         }
@@ -668,15 +673,9 @@ __global__ void __launch_bounds__(32 * kChooseWarps) tsm_choose_grad_kernel(cons
         const float per = whole && total > 0.f ? sum / total : whole && is_nan(total) ? total : 0.f;
 #pragma unroll
         for (int i = 0; i < VM; ++i)
-            d[i] = whole ? -x[i] * per : 0.f;
-        for (int j = 0; j < p.topk; ++j) {
-            const int e = __shfl_sync(kAll, id, j) - at.first;
-            const float v = __shfl_sync(kAll, g, j);
-#pragma unroll
-            for (int i = 0; i < VM; ++i)
-                d[i] += e == i ? v : 0.f;
-        }
-        char *row = static_cast<char *>(p.dlogits) + (t * p.ld_d + at.first) * EB;
+            d[i] = whole ? 0.f - x[i] * per : 0.f;
+        char *const first = static_cast<char *>(p.dlogits) + t * p.ld_d * EB;
+        char *row = first + at.first * EB;
         if constexpr (WIDE && VM * EB >= 4) {
             using P = Piece<ET, VM * EB >= 16 ? 16 : 4>;
             if (at.count) {
@@ -697,6 +696,22 @@ __global__ void __launch_bounds__(32 * kChooseWarps) tsm_choose_grad_kernel(cons
                     E::store(row, i, v);
                 }
         }
+        // Over these the choices' own, each by its lane; those of one expert by the first
+        // of them, in their order.  (8192 x 256 4.2 us, 6.0 with every choice compared with
+        // every lane's experts; 8192 x 1024 bf16 10.8 and 16.0.)
+        const uint32_t alike = __match_any_sync(kAll, id);
+        float v[1] = {whole ? 0.f - expf(mine - top) * per : 0.f};
+        if (__any_sync(kAll, id >= 0 && (alike & (alike - 1)) != 0)) {
+            for (int j = 0; j < p.topk; ++j) {
+                const float other = __shfl_sync(kAll, g, j);
+                v[0] += alike >> j & 1u ? other : 0.f;
+            }
+        } else {
+            v[0] += g;
+        }
+        __syncwarp();
+        if (id >= 0 && lane == __ffs(alike) - 1)
+            E::store(first, id, v);
     }
 }
 
