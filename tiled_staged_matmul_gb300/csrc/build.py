@@ -90,7 +90,7 @@ def _compile_calls(obj: str) -> list[str]:
     r = subprocess.run(cmd, capture_output=True, text=True)
     if r.returncode != 0:
         raise RuntimeError(f"g++ failed on {CALLS_SOURCE}:\n{r.stdout}\n{r.stderr}")
-    return ["g++", "-shared", obj, "-L" + os.path.join(torch_dir, "lib"), "-ltorch_python", "-ltorch_cpu", "-lc10",
+    return ["g++", "-shared", obj, "-L" + os.path.join(torch_dir, "lib"), "-ltorch_python", "-ltorch_cuda", "-ltorch_cpu", "-lc10",
             "-lc10_cuda", "-L" + BUILD_DIR, "-l:" + LIB_NAME, "-Wl,-rpath,$ORIGIN"]
 
 

@@ -6,15 +6,15 @@
 //
 // Checks of types and shapes, outputs and the stream, nothing else: what the
 // library checks itself (pointers, spans, alignment, sizes) is left to it.  (From
-// Python, through ctypes, a decode step's calls took two to four times as long: one
-// token's product 14.4 us of host time, quantising 18.2, the choice 15.2.)
+// Python, through ctypes, a decode step's calls took three to four times as long: one
+// token's product 14.4 us of host time, 3.4 so; quantising 18.2, 5.4; the choice 15.2,
+// 4.2; its gradient 13.6, 3.4.)
 //
 // A function returns its results, or the library's status where that is not
 // GEMM_OK, for the caller to raise.
 #include <Python.h>
 
-#include <ATen/ops/empty.h>
-#include <ATen/ops/empty_strided.h>
+#include <ATen/cuda/EmptyTensor.h>
 #include <ATen/ops/zeros.h>
 #include <c10/cuda/CUDAStream.h>
 #include <torch/csrc/Exceptions.h>
@@ -109,6 +109,18 @@ std::string sizes(at::IntArrayRef s)
     return text;
 }
 
+// A new tensor beside another (dense, or with these strides), without the way
+// through the dispatcher that at::empty takes (three of them: quantising 8.3 us of
+// host time so, 5.4 without).
+at::Tensor fresh(const at::Tensor &like, at::IntArrayRef shape, at::ScalarType type)
+{
+    return at::Tensor(at::detail::empty_cuda(shape, type, like.device(), std::nullopt));
+}
+at::Tensor fresh(const at::Tensor &like, at::IntArrayRef shape, at::IntArrayRef strides, at::ScalarType type)
+{
+    return at::Tensor(at::detail::empty_strided_cuda(shape, strides, type, like.device()));
+}
+
 // The row pitch of a matrix of rows with a unit last stride.
 int64_t pitch(const at::Tensor &t, const char *name)
 {
@@ -165,8 +177,7 @@ PyObject *moe_choose(PyObject *, PyObject *const *a, Py_ssize_t n)
         const float scale = real(a[8]);
         if (topk < 0)
             refuse("topk must not be negative");
-        const auto like = at::TensorOptions().device(x.device());
-        const at::Tensor ids = at::empty({T, topk}, like.dtype(at::kInt)), weights = at::empty({T, topk}, like.dtype(at::kFloat));
+        const at::Tensor ids = fresh(x, {T, topk}, at::kInt), weights = fresh(x, {T, topk}, at::kFloat);
         const gemm_status_t st = call([&] {
             return choose_experts(x.data_ptr(), type, bias, static_cast<int32_t *>(ids.data_ptr()),
                                   static_cast<float *>(weights.data_ptr()), T, E, topk, ld, score, groups, keep, best,
@@ -199,7 +210,7 @@ PyObject *moe_choose_grad(PyObject *, PyObject *const *a, Py_ssize_t n)
         at::Tensor out;
         int64_t ldo = E;
         if (a[3] == Py_None) {
-            out = at::empty({T, E}, x.options().memory_format(at::MemoryFormat::Contiguous));
+            out = fresh(x, {T, E}, x.scalar_type());
         } else {
             out = tensor(a[3], "out");
             if (out.dim() != 2 || out.sizes() != x.sizes() || out.scalar_type() != x.scalar_type())
@@ -241,14 +252,11 @@ PyObject *quantize_fp4(PyObject *, PyObject *const *a, Py_ssize_t n)
         const int32_t *counts = counts_of(a[1], batch);
         const int64_t width = (K + 1) / 2, ldq = (width + 15) / 16 * 16, sQ = M * ldq;
         const int64_t rows = (M + 127) / 128, cols = (K + 4 * block - 1) / (4 * block);
-        const auto like = at::TensorOptions().device(x.device());
-        const auto bytes = like.dtype(at::kByte);
-        const at::Tensor q = three ? at::empty_strided({batch, M, width}, {sQ, ldq, 1}, bytes)
-                                   : at::empty_strided({M, width}, {ldq, 1}, bytes);
-        const at::Tensor s = three ? at::empty({batch, rows, cols, 512}, bytes) : at::empty({rows, cols, 512}, bytes);
+        const at::Tensor q = three ? fresh(x, {batch, M, width}, {sQ, ldq, 1}, at::kByte) : fresh(x, {M, width}, {ldq, 1}, at::kByte);
+        const at::Tensor s = three ? fresh(x, {batch, rows, cols, 512}, at::kByte) : fresh(x, {rows, cols, 512}, at::kByte);
         at::Tensor r;
         if (block == 16)
-            r = three ? at::empty({batch, M}, like.dtype(at::kFloat)) : at::empty({M}, like.dtype(at::kFloat));
+            r = three ? fresh(x, {batch, M}, at::kFloat) : fresh(x, {M}, at::kFloat);
         const gemm_status_t st = call([&] {
             return fp4_quantize_rows(x.data_ptr(), type, int32_t(block), static_cast<uint8_t *>(q.data_ptr()),
                                      static_cast<uint8_t *>(s.data_ptr()), r.defined() ? static_cast<float *>(r.data_ptr()) : nullptr,
@@ -340,8 +348,7 @@ PyObject *gemm_fp4(PyObject *, PyObject *const *p, Py_ssize_t n)
                     refuse_type("out_dtype must be a torch dtype");
                 type = reinterpret_cast<THPDtype *>(p[13])->scalar_type;
             }
-            const auto like = at::TensorOptions().device(a.codes.device()).dtype(type);
-            out = counts ? at::zeros(wanted, like) : at::empty(wanted, like);
+            out = counts ? at::zeros(wanted, at::TensorOptions().device(a.codes.device()).dtype(type)) : fresh(a.codes, wanted, type);
         } else {
             out = tensor(p[8], "out");
         }
