@@ -20,7 +20,9 @@
 // largest of the lanes' maxima bounds the topk-th largest of all from below, a
 // dozen experts reach it, and those move to a lane each and are ranked there
 // (8192 x 256, 8 of 4 of 8 groups, with a bias: 14 us, 28.8 one after another;
-// without groups or bias 8.0, of 1024 in bf16 18.6).  Compiled once per type of the logits
+// without groups or bias 8.1, of 1024 in bf16 18.3).  Where the largest lie together in
+// few lanes there are too many candidates, and they are taken one after another after
+// all (all of a token's in order of their numbers: 30.6).  Compiled once per type of the logits
 // (-DTSM_CHOOSE_ELEM, gemm_internal.h's kOut* values).
 #include "fp4_internal.h"
 #include "fp4_ptx.cuh"
@@ -94,14 +96,12 @@ struct Layout {
     int group;  // this lane's
     int first;  // this lane's first expert
     int count;  // how many it has
-    __device__ __forceinline__ Layout(int experts, int groups, int vm, int lane)
+    __device__ __forceinline__ Layout(int per_, int groups, int lanes_log, int vm, int lane)
     {
-        per = experts / groups;
-        L = 32;
-        while (L * groups > 32)
-            L >>= 1;
-        group = lane / L;
-        const int at = lane % L * vm;
+        per = per_;
+        L = 1 << lanes_log;
+        group = lane >> lanes_log;
+        const int at = (lane & (L - 1)) * vm;
         first = group * per + at;
         count = group < groups ? max(0, min(vm, per - at)) : 0;
     }
@@ -530,7 +530,7 @@ template <int ET, int VM, bool WIDE>
 __device__ __noinline__ int choose_slowly(const ChooseParams &p, int64_t token, float top, float total, bool exactly)
 {
     const int lane = int(threadIdx.x & 31);
-    const Layout at(p.experts, p.groups, VM, lane);
+    const Layout at(p.per, p.groups, p.lanes_log, VM, lane);
     float x[VM];
     read_logits<ET, VM, WIDE>(p, token, at, x);
     int id;
@@ -540,14 +540,14 @@ __device__ __noinline__ int choose_slowly(const ChooseParams &p, int64_t token, 
 }
 
 template <int ET, int VM, bool WIDE>
-__global__ void __launch_bounds__(32 * kChooseWarps, VM == 32 ? 2 : VM == 16 ? 4 : VM == 8 && !WIDE ? 5 : 6) tsm_choose_kernel(const __grid_constant__ ChooseParams p)
+__global__ void __launch_bounds__(32 * kChooseWarps, VM == 32 ? 2 : VM == 16 ? 4 : VM == 8 ? 5 : 6) tsm_choose_kernel(const __grid_constant__ ChooseParams p)
 {
     chain_next();
     chain_wait();
     __shared__ uint32_t keys[kChooseWarps][32];
     __shared__ int names[kChooseWarps][32];
     const int lane = int(threadIdx.x & 31);
-    const Layout at(p.experts, p.groups, VM, lane);
+    const Layout at(p.per, p.groups, p.lanes_log, VM, lane);
     const float none = __uint_as_float(0xff800000u);
     const int64_t warps = int64_t(gridDim.x) * kChooseWarps;
     for (int64_t t = int64_t(blockIdx.x) * kChooseWarps + (threadIdx.x >> 5); t < p.tokens; t += warps) {
@@ -616,7 +616,7 @@ __global__ void __launch_bounds__(32 * kChooseWarps) tsm_choose_grad_kernel(cons
     chain_next();
     chain_wait();
     const int lane = int(threadIdx.x & 31);
-    const Layout at(p.experts, 1, VM, lane);
+    const Layout at(p.experts, 1, 5, VM, lane);
     const bool whole = !p.sigmoid && !p.renormalize;
     const int64_t warps = int64_t(gridDim.x) * kChooseWarps;
     for (int64_t t = int64_t(blockIdx.x) * kChooseWarps + (threadIdx.x >> 5); t < p.tokens; t += warps) {
@@ -728,27 +728,19 @@ cudaError_t choose_as(const ChooseParams &p, bool wide, int sms, cudaStream_t st
                     : launch_chained(tsm_choose_kernel<ET, VM, false>, grid, 32 * kChooseWarps, 0, 0, stream, p);
 }
 
-// Experts of a lane: a power of two that lets a group's lanes hold its experts.
-int lane_experts(int experts, int groups)
-{
-    int lanes = 32;
-    while (lanes * groups > 32)
-        lanes /= 2;
-    const int per = experts / groups;
-    int vm = 2;
-    while (vm * lanes < per)
-        vm *= 2;
-    return vm;
-}
-
 template <int ET, bool GRAD>
-cudaError_t choose_type(const ChooseParams &p, bool aligned, int sms, cudaStream_t stream)
+cudaError_t choose_type(ChooseParams p, bool aligned, int sms, cudaStream_t stream)
 {
-    const int groups = GRAD ? 1 : p.groups;
-    const int vm = lane_experts(p.experts, groups);
+    p.per = p.experts / p.groups;
+    for (p.lanes_log = 5; p.groups << p.lanes_log > 32; --p.lanes_log) {
+    }
+    // Experts of a lane: a power of two that lets a group's lanes hold its experts.
+    int vm = 2;
+    while (vm << p.lanes_log < p.per)
+        vm *= 2;
     // Wide accesses where every lane's experts are all there or all not, and start
     // at a multiple of them.
-    const bool wide = aligned && p.experts / groups % vm == 0;
+    const bool wide = aligned && p.per % vm == 0;
     switch (vm) {
     case 2: return choose_as<ET, 2, GRAD>(p, wide, sms, stream);
     case 4: return choose_as<ET, 4, GRAD>(p, wide, sms, stream);

@@ -100,6 +100,8 @@ struct ChooseParams {
     int32_t experts, topk, groups, keep, best;
     int32_t sigmoid, renormalize;
     float scale;
+    // What the launch adds: experts of a group, and its lanes' logarithm.
+    int32_t per, lanes_log;
 };
 constexpr int kMaxChooseExperts = 1024, kMaxChooseTopk = 32, kMaxChooseGroups = 32;
 // Experts where the groups are not a power of two: they leave lanes of the warp idle.
