@@ -201,6 +201,19 @@ def test_what_is_not_a_number(b):
     assert torch.isnan(w).all() and (ids.cpu() == torch.arange(5)).all()
 
 
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+@pytest.mark.parametrize("E,k,groups,keep", [(256, 8, 1, 1), (256, 8, 8, 2), (1000, 20, 1, 1), (300, 30, 3, 1)])
+def test_the_largest_lie_together(b, score, E, k, groups, keep):
+    """Experts in order of their scores, up and down, with and without a bias: what is
+    chosen is a few lanes'."""
+    g = torch.Generator().manual_seed(E)
+    x = 0.1 * torch.randn((40, E), generator=g)
+    slope = torch.linspace(-3, 3, E)
+    for by in (slope, slope.flip(0)):
+        check(b, x + by, k, score=score, groups=groups, keep=keep, renormalize=True)
+        check(b, x + by, k, score=score, bias=by.clone(), groups=groups, keep=keep, renormalize=True)
+
+
 @pytest.mark.parametrize("dtype", list(TYPES))
 def test_rows_of_any_pitch_and_base(b, dtype):
     for E, pitch, offset in ((64, 64, 0), (64, 72, 0), (64, 65, 0), (64, 64, 1), (60, 61, 3), (2, 3, 1), (128, 136, 4)):

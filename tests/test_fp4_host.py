@@ -294,3 +294,12 @@ def test_copies(plans):
 
 def test_too_many_tiles(plans):
     assert not plans([(2**31 - 600, 2**31 - 600, 64, 1, 32, 32, A0, B0, 0)])[0]["ok"]
+
+
+def test_tiles_are_cut_where_it_pays(plans):
+    """The sizes with which the GPU tests reach each way of cutting a tile's K: over
+    a cluster, or over the workers, for every kind of kernel."""
+    from test_fp4_cut_gpu import CUT
+    for (M, N, K), (kind, ranks, cut) in CUT.items():
+        s = plans([(M, N, K, 1, 1 << 23, 1 << 23, A0, B0, 0)])[0]
+        assert s["kind"] == kind and (s["ranks"] > 1) == (ranks > 1) and (s["shared"] > 0) == cut, (M, N, K, s)
