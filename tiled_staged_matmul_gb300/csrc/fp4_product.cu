@@ -69,7 +69,7 @@ struct Fp4Cfg {
     static constexpr int CHUNKS = NT / CW / kEpiGroups;
     static_assert(CHUNKS >= 1 && CHUNKS * CW * kEpiGroups == NT, "chunks");
     static constexpr int EPI_ROWS = CHUNKS * CW;         // of one epilogue group
-    static constexpr int NOTES_OFF = 3072, TERMS_OFF = NOTES_OFF + 32 * kNotes;
+    static constexpr int NOTES_OFF = 3 * 1024, TERMS_OFF = NOTES_OFF + 32 * kNotes;
     static constexpr int COLS_OFF = TERMS_OFF + 2 * NT * 4;
     static constexpr int CTRL = COLS_OFF + 2 * kEpiWarps * 64 * 4;
     static constexpr int FIT = (232448 - 1024 - CTRL) / STAGE;
