@@ -18,8 +18,8 @@
 // Bound by memory: one read of a row, its 16-element units (one block of 16, half
 // of one of 32) staying in registers between the maximum and the rounding.  What
 // is read and written over the time, of the copy rate of 6.8 TB/s: 8191 x 8192 bf16
-// blocks of 16 33.0 us, 0.77 (instructions come next: the corrected division),
-// blocks of 32 25.3 us, 1.0; f32 45.1 us, 1.0; 8191 x 2048 bf16 10.1 us, 0.62.
+// blocks of 16 28.8 us, 0.88 (instructions come next: the corrected division),
+// blocks of 32 25.1 us, 1.0; f32 45.1 us, 1.0; 8191 x 2048 bf16 9.1 us, 0.70.
 #include "fp4_internal.h"
 #include "fp4_ptx.cuh"
 #include "launch.cuh"
@@ -100,6 +100,17 @@ struct Unit16 {
     // The largest magnitude; NaN where there is one.
     __device__ __forceinline__ float top() const
     {
+        if constexpr (WIDE && ET != kOutF32) {
+            // (Magnitudes in order are their bits in order, NaNs last.  With maxima of
+            // widened values 8191 x 8192 took 33.0 us.)
+            static_assert(PIECES == 2, "two pieces");
+            uint32_t m = 0u;
+#pragma unroll
+            for (int w = 0; w < 4; ++w)
+                m = __vimax3_u16x2(m, raw[0].w[w] & 0x7fff7fffu, raw[1].w[w] & 0x7fff7fffu);
+            const uint32_t most = max(m & 0xffffu, m >> 16);
+            return ET == kOutBF16 ? __uint_as_float(most << 16) : __half2float(__ushort_as_half(uint16_t(most)));
+        }
         float v[kUnit];
         widen(v);
         float m = 0.f;
@@ -267,7 +278,8 @@ cudaError_t quantize_as(const Fp4QuantParams &p, cudaStream_t stream)
 {
     const int64_t rows = p.M * p.batch, units = (p.K + kUnit - 1) / kUnit;
     // As few threads to a row as keep it (a warp: eight rows a CTA, nothing to wait
-    // for), 256 where none do.  So and with 256 throughout, blocks of 16, bf16, us: 8191
+    // for), 256 where none do.  So and with 256 throughout, blocks of 16, bf16, us (both
+    // while maxima were taken of widened values: now 9.1 and 14.9 of 2048 and 4096): 8191
     // rows of 512 3.8 and 22.0, of 2048 10.1 and 23.6, of 4096 16.3 and 25.5; 512 of
     // 1024 2.0 and 2.5; 16 of 4096 1.7 and 1.6.
     if (units <= 32 * kUnitsKept)
