@@ -20,9 +20,9 @@
 // largest of the lanes' maxima bounds the topk-th largest of all from below, a
 // dozen experts reach it, and those move to a lane each and are ranked there
 // (8192 x 256, 8 of 4 of 8 groups, with a bias: 14 us, 28.8 one after another;
-// without groups or bias 8.1, of 1024 in bf16 18.3).  Where the largest lie together in
+// without groups or bias 7.7, of 1024 in bf16 17.7).  Where the largest lie together in
 // few lanes there are too many candidates, and they are taken one after another after
-// all (all of a token's in order of their numbers: 30.6).  Compiled once per type of the logits
+// all (scores in the order of the experts' numbers: 30).  Compiled once per type of the logits
 // (-DTSM_CHOOSE_ELEM, gemm_internal.h's kOut* values).
 #include "fp4_internal.h"
 #include "fp4_ptx.cuh"
@@ -91,17 +91,13 @@ struct OrderOf<double> {
 // Where a token's experts lie in its warp: L lanes to a group, VM experts to a
 // lane, so that lanes and a lane's experts are in ascending order.
 struct Layout {
-    int per;    // experts of a group
-    int L;      // lanes of a group (a power of two)
     int group;  // this lane's
     int first;  // this lane's first expert
     int count;  // how many it has
-    __device__ __forceinline__ Layout(int per_, int groups, int lanes_log, int vm, int lane)
+    __device__ __forceinline__ Layout(int per, int groups, int lanes_log, int vm, int lane)
     {
-        per = per_;
-        L = 1 << lanes_log;
         group = lane >> lanes_log;
-        const int at = (lane & (L - 1)) * vm;
+        const int at = (lane & ((1 << lanes_log) - 1)) * vm;
         first = group * per + at;
         count = group < groups ? max(0, min(vm, per - at)) : 0;
     }
@@ -219,7 +215,7 @@ __device__ __forceinline__ bool choose_in_turn(const ChooseParams &p, int64_t to
 #pragma unroll
         for (int i = 0; i < VM; ++i)
             take(c[i]);
-        for (int d = 1; d < at.L; d <<= 1) {
+        for (int d = 1; d < (1 << p.lanes_log); d <<= 1) {
             const O a2 = __shfl_xor_sync(kAll, a, d), b2 = __shfl_xor_sync(kAll, b, d);
             b = max(min(a, a2), max(b, b2));
             a = max(a, a2);
@@ -233,7 +229,7 @@ __device__ __forceinline__ bool choose_in_turn(const ChooseParams &p, int64_t to
         }
         O g = a == 0 ? O(0) : order_of(v);
         // Lane l < groups holds group l's.
-        g = __shfl_sync(kAll, g, min(lane, p.groups - 1) * at.L);
+        g = __shfl_sync(kAll, g, min(lane, p.groups - 1) * (1 << p.lanes_log));
         // Its rank among the groups.
         int before = 0;
         for (int j = 0; j < p.groups; ++j) {
@@ -391,7 +387,7 @@ __device__ __forceinline__ Chosen choose(const ChooseParams &p, int64_t token, c
             b = max(b, min(a, c[i]));
             a = max(a, c[i]);
         }
-        best_of_lanes(a, b, at.L);
+        best_of_lanes(a, b, (1 << p.lanes_log));
         const bool by_score = p.bias || p.best > 1;
         float v = value_of(a);  // (Without a bias the places are the logits'.)
         if (by_score && !p.bias)
@@ -400,7 +396,7 @@ __device__ __forceinline__ Chosen choose(const ChooseParams &p, int64_t token, c
             v += p.bias ? value_of(b) : score_of<float>(p.sigmoid, value_of(b), top, total);
         uint32_t g = a == 0 ? 0u : order_of(v);
         // Lane l < groups holds group l's; its rank.
-        g = __shfl_sync(kAll, g, min(lane, p.groups - 1) * at.L);
+        g = __shfl_sync(kAll, g, min(lane, p.groups - 1) * (1 << p.lanes_log));
         int before = 0;
         for (int j = 0; j < p.groups; ++j) {
             const uint32_t other = __shfl_sync(kAll, g, j);
@@ -427,7 +423,7 @@ __device__ __forceinline__ Chosen choose(const ChooseParams &p, int64_t token, c
                     double exact = 0.0;
                     for (uint32_t left = open; left; left &= left - 1) {
                         const int group = __ffs(left) - 1;
-                        const double d = group_exactly<ET>(p, token, group, at.per, lane);
+                        const double d = group_exactly<ET>(p, token, group, p.per, lane);
                         if (lane == group)
                             exact = d;
                     }
@@ -540,7 +536,7 @@ __device__ __noinline__ int choose_slowly(const ChooseParams &p, int64_t token, 
 }
 
 template <int ET, int VM, bool WIDE>
-__global__ void __launch_bounds__(32 * kChooseWarps, VM == 32 ? 2 : VM == 16 ? 4 : VM == 8 ? 5 : 6) tsm_choose_kernel(const __grid_constant__ ChooseParams p)
+__global__ void __launch_bounds__(32 * kChooseWarps, VM == 32 ? 2 : VM == 16 ? 4 : VM == 8 && !WIDE ? 5 : 6) tsm_choose_kernel(const __grid_constant__ ChooseParams p)
 {
     chain_next();
     chain_wait();
@@ -553,12 +549,12 @@ __global__ void __launch_bounds__(32 * kChooseWarps, VM == 32 ? 2 : VM == 16 ? 4
     for (int64_t t = int64_t(blockIdx.x) * kChooseWarps + (threadIdx.x >> 5); t < p.tokens; t += warps) {
         float x[VM];
         read_logits<ET, VM, WIDE>(p, t, at, x);
-        // (NaN where there is one; absent experts' values are set below.)
-        float seen = 0.f, add[VM];  // (add: the bias)
+        // (seen: NaN where there is one.  add: the bias.)
+        float seen = 0.f, add[VM];
 #pragma unroll
         for (int i = 0; i < VM; ++i) {
-            add[i] = p.bias && i < at.count ? p.bias[at.first + i] : 0.f;
-            seen = ptx::max_abs3_nan(seen, i < at.count ? x[i] : 0.f, add[i]);
+            add[i] = p.bias && (WIDE ? at.count > 0 : i < at.count) ? p.bias[at.first + i] : 0.f;
+            seen = ptx::max_abs3_nan(seen, x[i], add[i]);
         }
         bool bad = is_nan(seen);
         float top = 0.f, total = 1.f;
