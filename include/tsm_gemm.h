@@ -414,9 +414,9 @@ gemm_status_t moe_combine_rows_grad(const void *dout, const void *rows_in, int32
  * experts, groups <= 32 and a divisor of experts. */
 typedef enum moe_score { MOE_SCORE_SOFTMAX = 0, MOE_SCORE_SIGMOID = 1 } moe_score_t;
 gemm_status_t choose_experts(const void *logits, int32_t elem_type, const float *bias, int32_t *ids, float *weights,
-                                 int64_t tokens, int64_t experts, int64_t topk, int64_t ld, int32_t score, int64_t groups,
-                                 int64_t keep_groups, int32_t group_best, int32_t renormalize, float scale,
-                                 gemm_stream_t stream);
+                             int64_t tokens, int64_t experts, int64_t topk, int64_t ld, int32_t score, int64_t groups,
+                             int64_t keep_groups, int32_t group_best, int32_t renormalize, float scale,
+                             gemm_stream_t stream);
 
 /* The gradient of choose_experts' weights, for the ids it chose (an id
  * outside [0, experts) takes no part; an id that comes twice counts twice):
@@ -424,8 +424,8 @@ gemm_status_t choose_experts(const void *logits, int32_t elem_type, const float 
  * formed in f32 and rounded once to elem_type.  The choice itself has no
  * gradient, nor has the bias.  dlogits (tokens rows, ld_d apart) is written whole. */
 gemm_status_t choose_experts_grad(const float *dweights, const void *logits, int32_t elem_type, const int32_t *ids,
-                                      void *dlogits, int64_t tokens, int64_t experts, int64_t topk, int64_t ld, int64_t ld_d,
-                                      int32_t score, int32_t renormalize, float scale, gemm_stream_t stream);
+                                  void *dlogits, int64_t tokens, int64_t experts, int64_t topk, int64_t ld, int64_t ld_d,
+                                  int32_t score, int32_t renormalize, float scale, gemm_stream_t stream);
 
 /* ---------------------------------------------------------------- 8-bit integers */
 

@@ -282,20 +282,20 @@ def gemm_s8_grouped_scaled(A, B, C, scale_a, scale_b, group_rows, groups, M, N, 
 
 
 def choose_experts(logits, elem_type, bias, ids, weights, tokens, experts, topk, ld, score=0, groups=1,
-                       keep_groups=1, group_best=2, renormalize=False, scale=1.0, stream=0) -> int:
+                   keep_groups=1, group_best=2, renormalize=False, scale=1.0, stream=0) -> int:
     return _lib.choose_experts(logits, OUT_TYPES.get(elem_type, elem_type), bias, ids, weights, tokens, experts, topk,
-                                   ld, MOE_SCORES.get(score, score), groups, keep_groups, group_best, renormalize, scale,
-                                   stream)
+                               ld, MOE_SCORES.get(score, score), groups, keep_groups, group_best, renormalize, scale,
+                               stream)
 
 
 def choose_experts_grad(dweights, logits, elem_type, ids, dlogits, tokens, experts, topk, ld, ld_d, score=0,
-                            renormalize=False, scale=1.0, stream=0) -> int:
+                        renormalize=False, scale=1.0, stream=0) -> int:
     return _lib.choose_experts_grad(dweights, logits, OUT_TYPES.get(elem_type, elem_type), ids, dlogits, tokens,
-                                        experts, topk, ld, ld_d, MOE_SCORES.get(score, score), renormalize, scale, stream)
+                                    experts, topk, ld, ld_d, MOE_SCORES.get(score, score), renormalize, scale, stream)
 
 
 def fp4_quantize_rows(X, elem_type, block, q, block_scales, scales, group_rows, M, K, ldx, ldq, strideX=0, strideQ=0,
-                          scale_stride=0, batch=1, stream=0) -> int:
+                      scale_stride=0, batch=1, stream=0) -> int:
     return _lib.fp4_quantize_rows(X, OUT_TYPES.get(elem_type, elem_type), block, q, block_scales, scales, group_rows, M,
                                   K, ldx, ldq, strideX, strideQ, scale_stride, batch, stream)
 

@@ -36,9 +36,9 @@ using namespace tsm;
 extern "C" {
 
 gemm_status_t choose_experts(const void *logits, int32_t elem_type, const float *bias, int32_t *ids, float *weights,
-                                 int64_t tokens, int64_t experts, int64_t topk, int64_t ld, int32_t score, int64_t groups,
-                                 int64_t keep_groups, int32_t group_best, int32_t renormalize, float scale,
-                                 gemm_stream_t stream)
+                             int64_t tokens, int64_t experts, int64_t topk, int64_t ld, int32_t score, int64_t groups,
+                             int64_t keep_groups, int32_t group_best, int32_t renormalize, float scale,
+                             gemm_stream_t stream)
 {
     g_last_error.clear();
     gemm_status_t st = check_choose(elem_type, tokens, experts, topk, ld, score);
@@ -91,8 +91,8 @@ gemm_status_t choose_experts(const void *logits, int32_t elem_type, const float 
 }
 
 gemm_status_t choose_experts_grad(const float *dweights, const void *logits, int32_t elem_type, const int32_t *ids,
-                                      void *dlogits, int64_t tokens, int64_t experts, int64_t topk, int64_t ld, int64_t ld_d,
-                                      int32_t score, int32_t renormalize, float scale, gemm_stream_t stream)
+                                  void *dlogits, int64_t tokens, int64_t experts, int64_t topk, int64_t ld, int64_t ld_d,
+                                  int32_t score, int32_t renormalize, float scale, gemm_stream_t stream)
 {
     g_last_error.clear();
     gemm_status_t st = check_choose(elem_type, tokens, experts, topk, std::min(ld, ld_d), score);

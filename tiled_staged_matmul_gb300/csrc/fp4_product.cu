@@ -504,8 +504,12 @@ __global__ void __launch_bounds__(kFp4Threads, 1)
         const auto row_of = [&](int i, uint32_t a) {
             return PAIR && a == 0 ? (kEpiGroups * (Cfg::CHUNKS - i) - 1 - h) * CW : (kEpiGroups * i + h) * CW;
         };
-        const auto rows_of = [&](uint32_t a) { return terms0 + (a * uint32_t(kEpiGroups) + uint32_t(h)) * uint32_t(4 * Cfg::EPI_ROWS); };
-        const auto cols_of = [&](uint32_t a) { return cols0 + (a * uint32_t(kEpiWarps) + uint32_t(warp - kFirstEpi)) * 256u + 4u * uint32_t(lane); };
+        const auto rows_of = [&](uint32_t a) {
+            return terms0 + (a * uint32_t(kEpiGroups) + uint32_t(h)) * uint32_t(4 * Cfg::EPI_ROWS);
+        };
+        const auto cols_of = [&](uint32_t a) {
+            return cols0 + (a * uint32_t(kEpiWarps) + uint32_t(warp - kFirstEpi)) * 256u + 4u * uint32_t(lane);
+        };
         const auto read = [&]() {
             const uint32_t from = notes + 32u * (note % kNotes);
             const uint4 x = ptx::ld_shared_v4(from), y = ptx::ld_shared_v4(from + 16u);
@@ -667,9 +671,11 @@ __global__ void __launch_bounds__(kFp4Threads, 1)
                 look_ahead(acc ^ 1u);
                 __threadfence();
                 ptx::named_bar_sync(kFp4BarGroup + h, 128);
+                // (A pair's first accumulator is taken from its end: the groups the other way round.)
+                const int part = int(rank) * kEpiGroups + (PAIR && acc == 0 ? kEpiGroups - 1 - h : h);
                 if (q == 0)
-                    ptx::st_shared_u32(last_flag + 4u * h, arrive_last(p.arrivals + w.tile * Cfg::PARTS + int32_t(rank) * kEpiGroups + (PAIR && acc == 0 ? kEpiGroups - 1 - h : h),
-                                                                      p.tag, uint32_t(last - first + 1), lane));
+                    ptx::st_shared_u32(last_flag + 4u * h, arrive_last(p.arrivals + w.tile * Cfg::PARTS + part, p.tag,
+                                                                      uint32_t(last - first + 1), lane));
                 ptx::named_bar_sync(kFp4BarGroup + h, 128);
                 const bool mine = __any_sync(0xffffffffu, ptx::ld_shared_u32(last_flag + 4u * h) != 0);
                 __threadfence();
