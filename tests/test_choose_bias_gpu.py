@@ -1,0 +1,50 @@
+"""Biases of any size in the choice of experts.  Choices are compared for equality
+with those of 64 bits."""
+import pytest
+import torch
+
+from test_choose_gpu import INF, b, check  # noqa: F401  (b: a fixture)
+
+pytestmark = pytest.mark.gpu
+
+LOW, HIGH = torch.finfo(torch.float32).min, torch.finfo(torch.float32).max
+# The choices and groups of a call: among candidates in a lane each, and (few kept lanes that
+# hold more experts than a warp has lanes) one after another.
+FORMS = [(64, 6, 8, 4), (64, 6, 8, 1), (256, 8, 8, 2), (512, 9, 4, 1), (12, 3, 6, 2)]
+
+
+def group_biases(E, groups, keep, g):
+    """Biases that leave f32 in a group's sum, or begin outside it."""
+    per = E // groups
+    small = 0.1 * torch.randn(E, generator=g)
+    whole = small.view(groups, per)
+    for hidden in sorted({1, groups - keep, min(groups - keep + 1, groups), groups}):
+        for first in (0, groups - hidden):
+            bias = whole.clone()
+            bias[first:first + hidden] = LOW
+            yield bias.flatten()
+    for pinned in (1, keep, keep + 1, groups):
+        for at in (0, per - 1):
+            bias = whole.clone()
+            bias[groups - pinned:, at] = INF
+            yield bias.flatten()
+    bias = whole.clone()
+    bias[groups - 1] = INF
+    yield bias.flatten()
+    # Sums of 1.2 to 2 times the largest number, in another order than the groups'.
+    bias = whole.clone()
+    order = torch.randperm(groups, generator=g)
+    bias[:, 0] = HIGH
+    bias[:, 1 % per] = HIGH * (0.2 + 0.8 * order.float() / groups)
+    yield bias.flatten()
+    yield -bias.flatten()
+
+
+@pytest.mark.parametrize("E,k,groups,keep", FORMS)
+@pytest.mark.parametrize("best", [1, 2])
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+def test_group_sums_outside_f32(b, score, best, E, k, groups, keep):  # noqa: F811
+    g = torch.Generator().manual_seed(E + keep)
+    x = torch.randn((21, E), generator=g)
+    for bias in group_biases(E, groups, keep, g):
+        check(b, x, k, score=score, bias=bias, groups=groups, keep=keep, best=best, renormalize=True)

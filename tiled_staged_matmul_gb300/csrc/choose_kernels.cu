@@ -153,6 +153,16 @@ __device__ __forceinline__ float logit_at(const ChooseParams &p, int64_t token, 
 // total's (as large, and 40 roundings of 2^-24) and the quotient's: 25 x 2^-23.
 constexpr float kSigmoidError = 4.f / 8388608.f, kSoftmaxError = 25.f / 8388608.f;
 
+// The least (to = -1) or the most (1) that a group's sum may be in exact arithmetic, of one
+// or two values of this error that come to v in f32.  What has left f32's range is
+// as far as that goes: two biases' sum may be there, or one of +infinity.
+constexpr float kLargest = 3.402823466e38f;
+__device__ __forceinline__ float bound_of_sum(float v, float to, float eps)
+{
+    const float off = 2.f * eps + 0.25f * eps * fminf(fabsf(v), kLargest);  // (the scores, and all roundings)
+    return to * (fmaxf(to * v, -kLargest) + off);
+}
+
 // A score in F; `top` and `sum` are the softmax's.
 template <typename F>
 __device__ __forceinline__ F score_of(bool sigmoid, float x, float top, F sum)
@@ -238,14 +248,9 @@ __device__ __forceinline__ bool choose_in_turn(const ChooseParams &p, int64_t to
         }
         const bool kept = lane < p.groups && before < p.keep && g != 0;
         if (CHECK && by_score) {
-            // The last one kept against the first one not.
-            const uint32_t in = __ballot_sync(kAll, lane < p.groups && before == p.keep - 1);
-            const uint32_t out = __ballot_sync(kAll, lane < p.groups && before == p.keep);
-            const O gi = __shfl_sync(kAll, g, __ffs(in) - 1), go = __shfl_sync(kAll, g, __ffs(out) - 1);
-            if (go != 0) {
-                const float vi = float(value_of(gi)), vo = float(value_of(go));
-                sure = !(vi - vo <= eps * (4.f + fabsf(vi) + fabsf(vo)));
-            }
+            // No group that is kept may lie below one that is not.
+            const uint32_t edge = g != 0 ? order_of(bound_of_sum(float(value_of(g)), kept ? -1.f : 1.f, eps)) : 0u;
+            sure = __reduce_min_sync(kAll, kept ? edge : kAll) > warp_max(kept || lane >= p.groups ? 0u : edge);
         }
         const uint32_t mask = __ballot_sync(kAll, kept);
         if (!(mask >> (at.group & 31) & 1u)) {
@@ -323,7 +328,7 @@ __device__ __forceinline__ void best_of_lanes(T &a, T &b, int lanes)
 // The sum of a group's `best` largest scores (with the bias) in f64, a whole warp
 // for one group.  Sigmoids only.
 template <int ET>
-__device__ __noinline__ double group_exactly(const ChooseParams &p, int64_t token, int group, int per, int lane)
+__device__ __forceinline__ double group_exactly(const ChooseParams &p, int64_t token, int group, int per, int lane)
 {
     const double none = __longlong_as_double(0xfff0000000000000ll);
     double a = none, b = none;
@@ -341,10 +346,32 @@ __device__ __noinline__ double group_exactly(const ChooseParams &p, int64_t toke
     return p.best > 1 && b != none ? a + b : a;
 }
 
+// The groups that are kept, by it: the sure ones, and the largest of the open ones.
+template <int ET>
+__device__ __noinline__ uint32_t kept_exactly(const ChooseParams &p, int64_t token, uint32_t sure, uint32_t open)
+{
+    const int lane = int(threadIdx.x & 31);
+    double exact = 0.0;
+    for (uint32_t left = open; left; left &= left - 1) {
+        const int group = __ffs(left) - 1;
+        const double d = group_exactly<ET>(p, token, group, p.per, lane);
+        if (lane == group)
+            exact = d;
+    }
+    int rank = 0;
+    for (uint32_t left = open; left; left &= left - 1) {
+        const int j = __ffs(left) - 1;
+        const double other = __shfl_sync(kAll, exact, j);
+        rank += other > exact || (other == exact && j < lane);
+    }
+    return sure | __ballot_sync(kAll, (open >> lane & 1u) && rank < p.keep - __popc(sure));
+}
+
 // The rank of a lane's candidate among `n` by its score (a sigmoid) in f64.
 template <int ET>
-__device__ __noinline__ int rank_exactly(const ChooseParams &p, int64_t token, int name, int n, int lane)
+__device__ __noinline__ int rank_exactly(const ChooseParams &p, int64_t token, int name, int n)
 {
+    const int lane = int(threadIdx.x & 31);
     double exact = 0.0;
     if (lane < n)
         exact = score_of<double>(true, logit_at<ET>(p, token, name), 0.f, 1.0) + double(p.bias[name]);
@@ -405,36 +432,18 @@ __device__ __forceinline__ Chosen choose(const ChooseParams &p, int64_t token, c
         const bool mine = lane < p.groups && g != 0;
         uint32_t mask = __ballot_sync(kAll, mine && before < p.keep);
         if (by_score) {
-            // The last group kept and the first one not: those within reach of
-            // both are ranked again in f64.
-            const uint32_t in = __ballot_sync(kAll, mine && before == p.keep - 1);
-            const uint32_t out = __ballot_sync(kAll, mine && before == p.keep);
-            if (out != 0) {
-                const float vi = value_of(__shfl_sync(kAll, g, __ffs(in) - 1));
-                const float vo = value_of(__shfl_sync(kAll, g, __ffs(out) - 1));
-                // (Two scores on either side, and their sums' roundings.)
-                const float reach = 4.f * eps + 0.25f * eps * (fabsf(vi) + fabsf(vo));
-                if (!(vi - vo > reach)) {
-                    if (!p.sigmoid)
-                        return Chosen::kExactly;
-                    const float v = value_of(g);
-                    const uint32_t sure = __ballot_sync(kAll, mine && v > vo + reach);
-                    uint32_t open = __ballot_sync(kAll, mine && v <= vo + reach && v >= vi - reach);
-                    double exact = 0.0;
-                    for (uint32_t left = open; left; left &= left - 1) {
-                        const int group = __ffs(left) - 1;
-                        const double d = group_exactly<ET>(p, token, group, p.per, lane);
-                        if (lane == group)
-                            exact = d;
-                    }
-                    int rank = 0;
-                    for (uint32_t left = open; left; left &= left - 1) {
-                        const int j = __ffs(left) - 1;
-                        const double other = __shfl_sync(kAll, exact, j);
-                        rank += other > exact || (other == exact && j < lane);
-                    }
-                    mask = sure | __ballot_sync(kAll, (open >> lane & 1u) && rank < p.keep - __popc(sure));
-                }
+            // Those that may lie on the other side of the border between the groups that
+            // are kept and those that are not are ranked again in f64.
+            const bool kept = mask >> lane & 1u;
+            const uint32_t edge = mine ? order_of(bound_of_sum(value_of(g), kept ? -1.f : 1.f, eps)) : 0u;
+            const uint32_t least = __reduce_min_sync(kAll, kept ? edge : kAll);
+            const uint32_t most = warp_max(kept ? 0u : edge);
+            if (least <= most) {
+                if (!p.sigmoid)
+                    return Chosen::kExactly;
+                const uint32_t sure = __ballot_sync(kAll, kept && edge > most);
+                const uint32_t open = __ballot_sync(kAll, kept ? edge <= most : edge >= least);
+                mask = kept_exactly<ET>(p, token, sure, open);
             }
         }
         if (!(mask >> (at.group & 31) & 1u)) {
@@ -509,7 +518,7 @@ __device__ __forceinline__ Chosen choose(const ChooseParams &p, int64_t token, c
         if (__any_sync(kAll, close)) {
             if (!p.sigmoid)
                 return Chosen::kExactly;
-            rank = rank_exactly<ET>(p, token, name, n, lane);
+            rank = rank_exactly<ET>(p, token, name, n);
         }
     }
     __syncwarp();
@@ -545,8 +554,8 @@ __global__ void __launch_bounds__(32 * kChooseWarps, VM == 32 ? 2 : VM == 16 ? 4
     const int lane = int(threadIdx.x & 31);
     const Layout at(p.per, p.groups, p.lanes_log, VM, lane);
     const float none = __uint_as_float(0xff800000u);
-    const int64_t warps = int64_t(gridDim.x) * kChooseWarps;
-    for (int64_t t = int64_t(blockIdx.x) * kChooseWarps + (threadIdx.x >> 5); t < p.tokens; t += warps) {
+    // (Fewer than 2^31 tokens, and far fewer warps.)
+    for (uint32_t t = blockIdx.x * kChooseWarps + (threadIdx.x >> 5); t < uint32_t(p.tokens); t += gridDim.x * kChooseWarps) {
         float x[VM];
         read_logits<ET, VM, WIDE>(p, t, at, x);
         // (seen: NaN where there is one.  add: the bias.)
@@ -598,8 +607,8 @@ __global__ void __launch_bounds__(32 * kChooseWarps, VM == 32 ? 2 : VM == 16 ? 4
         if (bad)
             w = __uint_as_float(0x7fffffffu);
         if (lane < p.topk) {
-            p.ids[t * p.topk + lane] = id;
-            p.weights[t * p.topk + lane] = w;
+            p.ids[int64_t(t) * p.topk + lane] = id;
+            p.weights[int64_t(t) * p.topk + lane] = w;
         }
     }
 }
