@@ -48,3 +48,19 @@ def test_group_sums_outside_f32(b, score, best, E, k, groups, keep):  # noqa: F8
     x = torch.randn((21, E), generator=g)
     for bias in group_biases(E, groups, keep, g):
         check(b, x, k, score=score, bias=bias, groups=groups, keep=keep, best=best, renormalize=True)
+
+
+@pytest.mark.parametrize("E,k", [(64, 6), (256, 8), (1000, 31), (40, 32), (2, 1)])
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+def test_infinite_biases(b, score, E, k):  # noqa: F811
+    """From one to all experts, spread over the warp's lanes or together."""
+    g = torch.Generator().manual_seed(E)
+    x = torch.randn((21, E), generator=g)
+    for pinned in sorted({1, k - 1, k, min(k + 1, E), min(k + 5, E), E}):
+        for at in (torch.randperm(E, generator=g)[:pinned], torch.arange(E - pinned, E),
+                   (torch.arange(pinned) * E) // max(pinned, 1)):
+            bias = 0.1 * torch.randn(E, generator=g)
+            bias[at] = INF
+            check(b, x, k, score=score, bias=bias)
+            bias[at[::2]] = HIGH
+            check(b, x, k, score=score, bias=bias)

@@ -474,8 +474,8 @@ __device__ __forceinline__ Chosen choose(const ChooseParams &p, int64_t token, c
             best = 0;
     }
     if (check && low > 1) {
-        const float v = value_of(low);
-        low = order_of(v - 3.f * eps - 0.25f * eps * fabsf(v));
+        const float v = value_of(low);  // (+infinity with a bias of that: then those alone)
+        low = order_of(v - 3.f * eps - 0.25f * eps * fminf(fabsf(v), kLargest));
     }
     int mine = 0;
 #pragma unroll
