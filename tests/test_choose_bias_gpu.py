@@ -64,3 +64,39 @@ def test_infinite_biases(b, score, E, k):  # noqa: F811
             check(b, x, k, score=score, bias=bias)
             bias[at[::2]] = HIGH
             check(b, x, k, score=score, bias=bias)
+
+
+@pytest.mark.parametrize("size", [100.0, 1000.0, 1e5])
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+def test_biases_that_cancel_in_pairs(b, score, size):  # noqa: F811
+    """Groups of two with biases of +size and -size: their sums are those of two scores,
+    each added to a bias that rounds it."""
+    T = 1 << 20
+    x = torch.randn((T, 4), generator=torch.Generator().manual_seed(int(size)))
+    x[0] = torch.tensor([-0.35108897, 1.4023322, 0.89841217, 0.020195935])
+    for bias in (torch.tensor([size, -size, -size, size]), torch.tensor([-size, size, size, -size]),
+                 torch.tensor([size, -size, size, -size])):
+        d, c = x.double(), bias.double()
+        s = torch.softmax(d, 1) if score == "softmax" else 1 / (1 + torch.exp(-d))
+        c = s + c
+        v = c.view(T, 2, 2).sum(2)
+        first = torch.where(v[:, 1] > v[:, 0], 2, 0)
+        want = first + (c.gather(1, first[:, None] + 1) > c.gather(1, first[:, None]))[:, 0]
+        ids, _ = b.moe_choose(x.cuda(), 1, score=score, bias=bias.cuda(), groups=2, keep_groups=1)
+        assert torch.equal(ids.cpu()[:, 0].long(), want)
+
+
+@pytest.mark.parametrize("size", [1000.0, 1e5])
+@pytest.mark.parametrize("E,k,groups,keep", FORMS)
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+def test_biases_that_cancel_in_groups(b, score, E, k, groups, keep, size):  # noqa: F811
+    """A group's largest two cancel but for their scores; the other experts lie below."""
+    g = torch.Generator().manual_seed(E * 3 + keep)
+    x = torch.randn((600, E), generator=g)
+    bias = torch.full((groups, E // groups), -2 * size)
+    bias[:, 0], bias[:, -1] = -size, size
+    check(b, x, k, score=score, bias=bias.flatten(), groups=groups, keep=keep)
+    # Of one group only, which then decides about the others.
+    only = 0.1 * torch.randn((groups, E // groups), generator=g)
+    only[groups // 2] = bias[groups // 2]
+    check(b, x, k, score=score, bias=only.flatten(), groups=groups, keep=keep)

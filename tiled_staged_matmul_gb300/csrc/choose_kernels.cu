@@ -153,13 +153,24 @@ __device__ __forceinline__ float logit_at(const ChooseParams &p, int64_t token, 
 // total's (as large, and 40 roundings of 2^-24) and the quotient's: 25 x 2^-23.
 constexpr float kSigmoidError = 4.f / 8388608.f, kSoftmaxError = 25.f / 8388608.f;
 
-// The least (to = -1) or the most (1) that a group's sum may be in exact arithmetic, of one
-// or two values of this error that come to v in f32.  What has left f32's range is
-// as far as that goes: two biases' sum may be there, or one of +infinity.
+// A group's sum of one or two values: the sum in f32, and what it may be off by.  Each value
+// has its score's error and is rounded, with its bias in it, and so is the sum: by a
+// part of the values' sizes, not of the sum's, in which they may cancel.
 constexpr float kLargest = 3.402823466e38f;
-__device__ __forceinline__ float bound_of_sum(float v, float to, float eps)
+template <typename F>
+struct GroupSum {
+    F v = F(0);
+    float off = 0.f;
+    __device__ __forceinline__ void add(F c, float eps)
+    {
+        v += c;
+        off += eps + 0x1p-22f * fminf(fabsf(float(c)), kLargest);  // (2^-24 each: c, the sum, its bound)
+    }
+};
+// The least (to = -1) or the most (1) that it is in exact arithmetic.  What has left f32's
+// range is as far as that goes: two biases' sum may be there, or one of +infinity.
+__device__ __forceinline__ float bound_of(float v, float off, float to)
 {
-    const float off = 2.f * eps + 0.25f * eps * fminf(fabsf(v), kLargest);  // (the scores, and all roundings)
     return to * (fmaxf(to * v, -kLargest) + off);
 }
 
@@ -230,14 +241,14 @@ __device__ __forceinline__ bool choose_in_turn(const ChooseParams &p, int64_t to
             b = max(min(a, a2), max(b, b2));
             a = max(a, a2);
         }
-        F v = F(0);
-        if (a != 0) {
-            // (Without a bias the places are the logits'.)
-            v = p.bias ? F(value_of(a)) : p.best > 1 ? score(float(value_of(a))) : F(value_of(a));
-            if (p.best > 1 && b != 0)
-                v += p.bias ? F(value_of(b)) : score(float(value_of(b)));
-        }
-        O g = a == 0 ? O(0) : order_of(v);
+        // (Without a bias the places are the logits'.)
+        const auto value = [&](O o) { return p.bias || p.best == 1 ? F(value_of(o)) : score(float(value_of(o))); };
+        GroupSum<F> sum;
+        if (a != 0)
+            sum.add(value(a), eps);
+        if (p.best > 1 && b != 0)
+            sum.add(value(b), eps);
+        O g = a == 0 ? O(0) : order_of(sum.v);
         // Lane l < groups holds group l's.
         g = __shfl_sync(kAll, g, min(lane, p.groups - 1) * (1 << p.lanes_log));
         // Its rank among the groups.
@@ -249,7 +260,8 @@ __device__ __forceinline__ bool choose_in_turn(const ChooseParams &p, int64_t to
         const bool kept = lane < p.groups && before < p.keep && g != 0;
         if (CHECK && by_score) {
             // No group that is kept may lie below one that is not.
-            const uint32_t edge = g != 0 ? order_of(bound_of_sum(float(value_of(g)), kept ? -1.f : 1.f, eps)) : 0u;
+            const float off = __shfl_sync(kAll, sum.off, min(lane, p.groups - 1) * (1 << p.lanes_log));
+            const uint32_t edge = g != 0 ? order_of(bound_of(float(value_of(g)), off, kept ? -1.f : 1.f)) : 0u;
             sure = __reduce_min_sync(kAll, kept ? edge : kAll) > warp_max(kept || lane >= p.groups ? 0u : edge);
         }
         const uint32_t mask = __ballot_sync(kAll, kept);
@@ -416,12 +428,16 @@ __device__ __forceinline__ Chosen choose(const ChooseParams &p, int64_t token, c
         }
         best_of_lanes(a, b, (1 << p.lanes_log));
         const bool by_score = p.bias || p.best > 1;
-        float v = value_of(a);  // (Without a bias the places are the logits'.)
-        if (by_score && !p.bias)
-            v = score_of<float>(p.sigmoid, v, top, total);
+        // (Without a bias the places are the logits'.)
+        const auto value = [&](uint32_t o) {
+            return p.bias || !by_score ? value_of(o) : score_of<float>(p.sigmoid, value_of(o), top, total);
+        };
+        GroupSum<float> sum;
+        if (a != 0)
+            sum.add(value(a), eps);
         if (p.best > 1 && b != 0)
-            v += p.bias ? value_of(b) : score_of<float>(p.sigmoid, value_of(b), top, total);
-        uint32_t g = a == 0 ? 0u : order_of(v);
+            sum.add(value(b), eps);
+        uint32_t g = a == 0 ? 0u : order_of(sum.v);
         // Lane l < groups holds group l's; its rank.
         g = __shfl_sync(kAll, g, min(lane, p.groups - 1) * (1 << p.lanes_log));
         int before = 0;
@@ -435,7 +451,8 @@ __device__ __forceinline__ Chosen choose(const ChooseParams &p, int64_t token, c
             // Those that may lie on the other side of the border between the groups that
             // are kept and those that are not are ranked again in f64.
             const bool kept = mask >> lane & 1u;
-            const uint32_t edge = mine ? order_of(bound_of_sum(value_of(g), kept ? -1.f : 1.f, eps)) : 0u;
+            const float off = __shfl_sync(kAll, sum.off, min(lane, p.groups - 1) * (1 << p.lanes_log));
+            const uint32_t edge = mine ? order_of(bound_of(value_of(g), off, kept ? -1.f : 1.f)) : 0u;
             const uint32_t least = __reduce_min_sync(kAll, kept ? edge : kAll);
             const uint32_t most = warp_max(kept ? 0u : edge);
             if (least <= most) {
