@@ -399,8 +399,11 @@ gemm_status_t moe_combine_rows_grad(const void *dout, const void *rows_in, int32
  *     ids[t * topk + j] = the expert with the j-th largest c in the kept groups
  *     weights[t * topk + j] = scale * s[id], or renormalised scale * s[id] / sum over the topk of s
  * Equal values go to the lower number.  The bias takes part in the choice only.
- * The choice is that of exact arithmetic (f64 where f32 cannot tell two values
- * apart); the weights are formed in f32.
+ * Values are compared as f64 holds them, formed so wherever f32 cannot tell two apart;
+ * what f64 rounds alike is equal (beside a bias sigmoids of logits past 37 are all 1, and
+ * so are they in the sums of two).  Without a bias experts, and groups by their largest
+ * one, are compared by their logits, where different ones are never equal.  The
+ * weights are formed in f32.
  * An expert whose logit or bias is -infinity is not there: it is never chosen and
  * adds nothing to its group's sum.  Where fewer than topk are there to choose
  * from, the remaining ids are -1 (which moe_route_slots drops) and their weights

@@ -100,3 +100,20 @@ def test_biases_that_cancel_in_groups(b, score, E, k, groups, keep, size):  # no
     only = 0.1 * torch.randn((groups, E // groups), generator=g)
     only[groups // 2] = bias[groups // 2]
     check(b, x, k, score=score, bias=only.flatten(), groups=groups, keep=keep)
+
+
+def test_what_64_bits_cannot_tell_apart(b):  # noqa: F811
+    """Scores are compared as 64 bits hold them: with a bias sigmoids of logits past 37
+    are all 1 and go to the lower number; without one the logits decide."""
+    x = torch.zeros((3, 16))
+    x[:, 3], x[:, 9], x[:, 12] = 40.0, 45.0, 38.0
+    assert b.moe_choose(x.cuda(), 3, score="sigmoid")[0].tolist() == [[9, 3, 12]] * 3
+    assert b.moe_choose(x.cuda(), 3, score="sigmoid", bias=torch.zeros(16).cuda())[0].tolist() == [[3, 9, 12]] * 3
+    # (Sums of a group's two best are sums of scores, with a bias or without.)
+    y = torch.zeros((3, 8))
+    y[:, 2], y[:, 3], y[:, 4], y[:, 5] = 40.0, 41.0, 44.0, 45.0
+    for bias in (None, torch.zeros(8).cuda()):
+        ids, _ = b.moe_choose(y.cuda(), 2, score="sigmoid", bias=bias, groups=4, keep_groups=1)
+        assert sorted(ids[0].tolist()) == [2, 3]
+    ids, _ = b.moe_choose(y.cuda(), 2, score="sigmoid", groups=4, keep_groups=1, group_best=1)
+    assert ids.tolist() == [[5, 4]] * 3

@@ -666,7 +666,8 @@ def moe_choose(logits, topk, *, score="softmax", bias=None, groups=1, keep_group
     for the choice only.  With ``groups`` the experts are chosen from the
     ``keep_groups`` groups with the largest sums of their ``group_best`` (1 or 2)
     best.  Weights are the chosen scores, divided by their sum with
-    ``renormalize``, times ``scale``.  Equal values go to the lower number; a
+    ``renormalize``, times ``scale``.  Equal values (of f64: scores are compared as
+    it holds them, or without a bias by their logits) go to the lower number; a
     logit of -infinity hides an expert, and a choice that finds none has the id
     -1 and the weight 0."""
     if stream is not None:

@@ -10,10 +10,11 @@
 //   the g_j with id_j = e
 //
 // A warp takes a token.  Scores are formed in f32, but which expert is chosen is
-// what it is in exact arithmetic: where two scores that decide something lie
-// within the bound of their f32 errors, the warp forms them again in f64 and
-// decides by those.  (Without a bias the logits themselves give the order,
-// exactly.)  With random logits one token in a thousand needs it.
+// what it is in f64: where two scores that decide something lie within the bound
+// of their f32 errors, the warp forms them again in f64 and decides by those.  What
+// f64 rounds alike (with a bias the sigmoids of 40 and 45) goes to the lower number.
+// (Without a bias the logits themselves give the order, exactly.)  With random
+// logits one token in a thousand needs it.
 //
 // Bound by instructions rather than by its bytes.  So the choice is not made one
 // expert after another (370 instructions for 8 of 256) but among few: the topk-th
