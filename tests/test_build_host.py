@@ -1,0 +1,38 @@
+"""What the build takes for up to date, and for whom."""
+import importlib.machinery
+import importlib.util
+import sysconfig
+
+import pytest
+
+from tiled_staged_matmul_gb300.csrc import build as tsm_build
+
+
+@pytest.fixture(scope="module", autouse=True)
+def built():
+    tsm_build.build()
+
+
+def another_python(monkeypatch, tmp_path):
+    own = sysconfig.get_config_var
+    monkeypatch.setattr(sysconfig, "get_config_var", lambda name: ".cpython-399.so" if name == "EXT_SUFFIX" else own(name))
+
+
+def another_torch(monkeypatch, tmp_path):
+    (tmp_path / "__init__.py").write_text("")
+    (tmp_path / "version.py").write_text("__version__ = '99.0'\n")
+    spec = importlib.machinery.ModuleSpec("torch", None, origin=str(tmp_path / "__init__.py"))
+    own = importlib.util.find_spec
+    monkeypatch.setattr(importlib.util, "find_spec", lambda name, *a: spec if name == "torch" else own(name, *a))
+
+
+@pytest.mark.parametrize("change", [another_python, another_torch])
+def test_an_extension_module_for_another_torch_or_python(monkeypatch, tmp_path, change):
+    """It is built again, and until then refused instead of loaded."""
+    from tiled_staged_matmul_gb300 import binding
+    assert tsm_build.up_to_date()
+    change(monkeypatch, tmp_path)
+    assert not tsm_build.up_to_date()
+    monkeypatch.setattr(binding, "_calls", None)
+    with pytest.raises(ImportError, match="another torch or Python"):
+        binding._load_calls()

@@ -369,6 +369,10 @@ def _load_calls():
     import torch  # noqa: F401  (the module's libraries come with it)
     import importlib.machinery
     import importlib.util
+    if not _build.calls_match():
+        raise ImportError(
+            f"{_build.CALLS_PATH} is missing, or was built for another torch or Python: build it first "
+            "(python -c 'import __graft_entry__ as g; g.build()')")
     loader = importlib.machinery.ExtensionFileLoader("tsm_tensor_calls", _build.CALLS_PATH)
     module = importlib.util.module_from_spec(importlib.util.spec_from_loader("tsm_tensor_calls", loader))
     loader.exec_module(module)

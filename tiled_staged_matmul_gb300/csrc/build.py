@@ -11,6 +11,7 @@ summary is read).
 """
 from __future__ import annotations
 
+import importlib.util
 import os
 import re
 import shutil
@@ -27,6 +28,7 @@ LIB_NAME = "libtsm_gemm.so"
 LIB_PATH = os.path.join(BUILD_DIR, LIB_NAME)
 CALLS_PATH = os.path.join(BUILD_DIR, "tsm_tensor_calls.so")
 CALLS_SOURCE = "tensor_calls.cpp"
+CALLS_STAMP = os.path.join(BUILD_DIR, "tsm_tensor_calls.abi")
 PTXAS_LOG = os.path.join(BUILD_DIR, "ptxas.log")
 
 # (source, object name, extra nvcc flags); the activations are gemm_internal.h's kAct* values
@@ -60,8 +62,24 @@ def _inputs() -> list[str]:
     return files
 
 
+def calls_abi() -> str:
+    """What the extension module is compiled against and works with alone: this Python's
+    ABI and the installed torch (found, not imported)."""
+    torch_dir = os.path.dirname(importlib.util.find_spec("torch").origin)
+    with open(os.path.join(torch_dir, "version.py")) as f:
+        return "\n".join([str(sysconfig.get_config_var("EXT_SUFFIX")), torch_dir, f.read()])
+
+
+def calls_match() -> bool:
+    """Whether the extension module that is there was compiled against these."""
+    if not os.path.exists(CALLS_PATH) or not os.path.exists(CALLS_STAMP):
+        return False
+    with open(CALLS_STAMP) as f:
+        return f.read() == calls_abi()
+
+
 def up_to_date() -> bool:
-    if not os.path.exists(LIB_PATH) or not os.path.exists(CALLS_PATH):
+    if not os.path.exists(LIB_PATH) or not calls_match():
         return False
     t = min(os.path.getmtime(LIB_PATH), os.path.getmtime(CALLS_PATH))
     return all(os.path.getmtime(f) <= t for f in _inputs())
@@ -127,6 +145,8 @@ def build(force: bool = False, quiet: bool = True) -> str:
     if r.returncode != 0:
         raise RuntimeError(f"link failed:\n{r.stdout}\n{r.stderr}")
     os.replace(tmp, CALLS_PATH)
+    with open(CALLS_STAMP, "w") as f:
+        f.write(calls_abi())
     if not quiet:
         print(logs[0], file=sys.stderr)
     return LIB_PATH
