@@ -1,6 +1,9 @@
 """What the build takes for up to date, and for whom."""
 import importlib.machinery
 import importlib.util
+import os
+import subprocess
+import sys
 import sysconfig
 
 import pytest
@@ -36,3 +39,18 @@ def test_an_extension_module_for_another_torch_or_python(monkeypatch, tmp_path, 
     monkeypatch.setattr(binding, "_calls", None)
     with pytest.raises(ImportError, match="another torch or Python"):
         binding._load_calls()
+
+
+def test_the_library_where_there_is_no_torch(monkeypatch, tmp_path):
+    """The C ABI needs none; the extension module is left out."""
+    monkeypatch.setitem(sys.modules, "torch", None)
+    monkeypatch.setattr(tsm_build, "BUILD_DIR", str(tmp_path))
+    for name in ("LIB_PATH", "CALLS_PATH", "CALLS_STAMP", "PTXAS_LOG"):
+        if hasattr(tsm_build, name):
+            monkeypatch.setattr(tsm_build, name, str(tmp_path / os.path.basename(getattr(tsm_build, name))))
+    # (Empty units in place of the library's.)
+    monkeypatch.setattr(tsm_build, "_compile", lambda src, obj, verbose, flags: subprocess.run(
+        ["g++", "-x", "c++", "-c", os.devnull, "-fPIC", "-o", obj], check=True) and "")
+    tsm_build.build()
+    assert os.path.exists(tsm_build.LIB_PATH) and not os.path.exists(tsm_build.CALLS_PATH)
+    assert tsm_build.up_to_date()

@@ -1,5 +1,6 @@
 """Build ``libtsm_gemm.so`` in-tree with nvcc for sm_103a only, and with the host
-compiler the extension module that passes torch tensors to some of its calls.
+compiler, where torch is installed, the extension module that passes torch tensors to
+some of its calls.
 
 The translation units compile in parallel: the plain GEMM kernels and the
 cluster split-K sums, the fused-epilogue GEMM kernels once per activation
@@ -62,10 +63,13 @@ def _inputs() -> list[str]:
     return files
 
 
-def calls_abi() -> str:
+def calls_abi() -> str | None:
     """What the extension module is compiled against and works with alone: this Python's
-    ABI and the installed torch (found, not imported)."""
-    torch_dir = os.path.dirname(importlib.util.find_spec("torch").origin)
+    ABI and the installed torch (found, not imported); None where there is no torch."""
+    torch = importlib.util.find_spec("torch")
+    if torch is None:
+        return None
+    torch_dir = os.path.dirname(torch.origin)
     with open(os.path.join(torch_dir, "version.py")) as f:
         return "\n".join([str(sysconfig.get_config_var("EXT_SUFFIX")), torch_dir, f.read()])
 
@@ -79,9 +83,14 @@ def calls_match() -> bool:
 
 
 def up_to_date() -> bool:
-    if not os.path.exists(LIB_PATH) or not calls_match():
+    outputs = [LIB_PATH]
+    if calls_abi() is not None:
+        if not calls_match():
+            return False
+        outputs.append(CALLS_PATH)
+    if not os.path.exists(LIB_PATH):
         return False
-    t = min(os.path.getmtime(LIB_PATH), os.path.getmtime(CALLS_PATH))
+    t = min(os.path.getmtime(f) for f in outputs)
     return all(os.path.getmtime(f) <= t for f in _inputs())
 
 
@@ -127,7 +136,8 @@ def build(force: bool = False, quiet: bool = True) -> str:
     objs = [os.path.join(BUILD_DIR, name + ".o") for _, name, _ in UNITS]
     kernel_unit = [src not in HOST_SOURCES for src, _, _ in UNITS]
     with ThreadPoolExecutor(len(UNITS) + 1) as ex:
-        calls = ex.submit(_compile_calls, os.path.join(BUILD_DIR, "tensor_calls.o"))
+        abi = calls_abi()
+        calls = abi and ex.submit(_compile_calls, os.path.join(BUILD_DIR, "tensor_calls.o"))
         logs = list(ex.map(lambda a: _compile(*a),
                            [(src, o, k, fl) for (src, _, fl), o, k in zip(UNITS, objs, kernel_unit)]))
     ptxas = "".join(log for log, k in zip(logs, kernel_unit) if k)
@@ -140,13 +150,14 @@ def build(force: bool = False, quiet: bool = True) -> str:
     if r.returncode != 0:
         raise RuntimeError(f"link failed:\n{r.stdout}\n{r.stderr}")
     os.replace(tmp, LIB_PATH)
-    tmp = CALLS_PATH + f".tmp{os.getpid()}"
-    r = subprocess.run(calls.result() + ["-o", tmp], capture_output=True, text=True)
-    if r.returncode != 0:
-        raise RuntimeError(f"link failed:\n{r.stdout}\n{r.stderr}")
-    os.replace(tmp, CALLS_PATH)
-    with open(CALLS_STAMP, "w") as f:
-        f.write(calls_abi())
+    if calls:
+        tmp = CALLS_PATH + f".tmp{os.getpid()}"
+        r = subprocess.run(calls.result() + ["-o", tmp], capture_output=True, text=True)
+        if r.returncode != 0:
+            raise RuntimeError(f"link failed:\n{r.stdout}\n{r.stderr}")
+        os.replace(tmp, CALLS_PATH)
+        with open(CALLS_STAMP, "w") as f:
+            f.write(abi)
     if not quiet:
         print(logs[0], file=sys.stderr)
     return LIB_PATH
