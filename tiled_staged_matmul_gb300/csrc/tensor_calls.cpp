@@ -78,6 +78,14 @@ float real(PyObject *o)
     return float(v);
 }
 
+bool truth(PyObject *o)
+{
+    const int v = PyObject_IsTrue(o);
+    if (v < 0)
+        throw python_error();
+    return v != 0;
+}
+
 int32_t elem_type(const at::Tensor &t)
 {
     switch (t.scalar_type()) {
@@ -173,7 +181,7 @@ PyObject *moe_choose(PyObject *, PyObject *const *a, Py_ssize_t n)
             bias = static_cast<const float *>(dense(tensor(a[3], "bias"), at::kFloat, {E}, "bias").data_ptr());
         const int64_t groups = integer(a[4]), keep = integer(a[5]);
         const int32_t score = integer32(a[2]), best = integer32(a[6]);
-        const bool renormalize = PyObject_IsTrue(a[7]) == 1;
+        const bool renormalize = truth(a[7]);
         const float scale = real(a[8]);
         if (topk < 0)
             refuse("topk must not be negative");
@@ -218,7 +226,7 @@ PyObject *moe_choose_grad(PyObject *, PyObject *const *a, Py_ssize_t n)
             ldo = pitch(out, "out");
         }
         const int32_t score = integer32(a[4]);
-        const bool renormalize = PyObject_IsTrue(a[5]) == 1;
+        const bool renormalize = truth(a[5]);
         const float scale = real(a[6]);
         const gemm_status_t st = call([&] {
             return choose_experts_grad(static_cast<const float *>(dw.data_ptr()), x.data_ptr(), type,
