@@ -242,8 +242,8 @@ __global__ void __launch_bounds__(TPR < 256 && TPR > 32 ? TPR : 256) tsm_quantiz
                 v[j] *= m;
         }
         // (What a scale of 0 or NaN makes of the values is not kept.)
-        const bool zeros = BLOCK == 16 ? scale == 0 : scale == 255u;
-        const uint32_t lo = zeros ? 0u : ptx::to_e2m1x8(v), hi = zeros ? 0u : ptx::to_e2m1x8(v + 8);
+        const uint32_t kept = (BLOCK == 16 ? scale == 0 : scale == 255u) ? 0u : 0xffffffffu;
+        const uint32_t lo = ptx::to_e2m1x8(v) & kept, hi = ptx::to_e2m1x8(v + 8) & kept;
         if (u < units) {
             const int32_t bytes = (K + 1) / 2 - u * 8;  // left in the row
             uint8_t *const to = q + u * 8;
