@@ -26,3 +26,18 @@ def test_a_truth_value_that_raises(b):
         with pytest.raises((ValueError, RuntimeError), match=text):
             b.moe_choose_grad(w, x, ids, renormalize=flag)
     assert torch.equal(b.moe_choose(x, 2, renormalize=torch.ones(1))[1], w)
+
+
+def test_a_tensor_whose_address_may_not_be_taken(b):
+    """As tracers mark theirs: an error, raised under the interpreter's lock."""
+    x = torch.randn((4, 8), device="cuda")
+    ids, w = b.moe_choose(x, 2)
+    q = b.quantize_fp4(x)
+    marked, codes = x.clone(), q.codes.clone()
+    for t in (marked, codes):
+        torch._C._set_throw_on_mutable_data_ptr(t)
+    for call in (lambda: b.moe_choose(marked, 2), lambda: b.moe_choose_grad(w, marked, ids), lambda: b.quantize_fp4(marked),
+                 lambda: b.gemm_fp4(q._replace(codes=codes), q)):
+        with pytest.raises(RuntimeError):
+            call()
+    assert torch.equal(b.moe_choose(x, 2)[0], ids)

@@ -99,14 +99,16 @@ int32_t elem_type(const at::Tensor &t)
 gemm_stream_t stream() { return c10::cuda::getCurrentCUDAStream().stream(); }
 
 // The library's call without the interpreter's lock (a full launch queue can hold
-// it up), and its status.
+// it up), and its status.  The lock is back before an exception (of a tensor whose
+// address may not be taken, say) goes on.
 template <typename F>
 gemm_status_t call(F &&fn)
 {
-    PyThreadState *state = PyEval_SaveThread();
-    const gemm_status_t st = fn();
-    PyEval_RestoreThread(state);
-    return st;
+    struct Unlocked {
+        PyThreadState *state = PyEval_SaveThread();
+        ~Unlocked() { PyEval_RestoreThread(state); }
+    } unlocked;
+    return fn();
 }
 
 std::string sizes(at::IntArrayRef s)
