@@ -21,9 +21,13 @@
 // largest of the lanes' maxima bounds the topk-th largest of all from below, a
 // dozen experts reach it, and those move to a lane each and are ranked there
 // (8192 x 256, 8 of 4 of 8 groups, with a bias: 14 us, 28.8 one after another;
-// without groups or bias 7.7, of 1024 in bf16 17.7).  Where the largest lie together in
-// few lanes there are too many candidates, and they are taken one after another after
-// all (scores in the order of the experts' numbers: 30).  Compiled once per type of the logits
+// without groups 12, without a bias either 8 to 9, of 1024 in bf16 18 to 19).  Where the
+// largest lie together in few lanes there are too many candidates, and they are taken one
+// after another after all (scores in the order of the experts' numbers: 30).  So they
+// are for every token where the kept groups' lanes are no more than topk (with a bias)
+// and hold more than 32 experts: 8 of 2 of 8 groups 32 us, by the softmax 41; and with a
+// bias for choices near 32, a warp's lanes: 31 of 256 56, 32, which leaves none for the
+// one that comes next and so ends in f64, 159.  Compiled once per type of the logits
 // (-DTSM_CHOOSE_ELEM, gemm_internal.h's kOut* values).
 #include "fp4_internal.h"
 #include "fp4_ptx.cuh"
