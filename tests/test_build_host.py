@@ -41,9 +41,20 @@ def test_an_extension_module_for_another_torch_or_python(monkeypatch, tmp_path, 
         binding._load_calls()
 
 
-def test_the_library_where_there_is_no_torch(monkeypatch, tmp_path):
-    """The C ABI needs none; the extension module is left out."""
+def no_torch(monkeypatch, tmp_path):
     monkeypatch.setitem(sys.modules, "torch", None)
+
+
+def a_folder_of_its_name(monkeypatch, tmp_path):
+    spec = importlib.machinery.ModuleSpec("torch", None, origin=None, is_package=True)
+    own = importlib.util.find_spec
+    monkeypatch.setattr(importlib.util, "find_spec", lambda name, *a: spec if name == "torch" else own(name, *a))
+
+
+@pytest.mark.parametrize("missing", [no_torch, a_folder_of_its_name])
+def test_the_library_where_there_is_no_torch(monkeypatch, tmp_path, missing):
+    """The C ABI needs none; the extension module is left out."""
+    missing(monkeypatch, tmp_path)
     monkeypatch.setattr(tsm_build, "BUILD_DIR", str(tmp_path))
     for name in ("LIB_PATH", "CALLS_PATH", "CALLS_STAMP", "PTXAS_LOG"):
         if hasattr(tsm_build, name):

@@ -67,7 +67,7 @@ def calls_abi() -> str | None:
     """What the extension module is compiled against and works with alone: this Python's
     ABI and the installed torch (found, not imported); None where there is no torch."""
     torch = importlib.util.find_spec("torch")
-    if torch is None:
+    if torch is None or torch.origin is None:  # (a folder of that name is none)
         return None
     torch_dir = os.path.dirname(torch.origin)
     with open(os.path.join(torch_dir, "version.py")) as f:
